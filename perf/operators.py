@@ -217,7 +217,6 @@ def prepare(case, seed):
             st["workspace"] = _bytes(api.tree_attention_workspace(h, B, T, case["heads"], H, D))
         if op == "evict":
             st["dst"] = api.KVCache(st["dst_k"], st["dst_v"], st["dst_table"])
-            st["workspace"] = _bytes(api.cache_evict_workspace(h, B, H, capacity, case["keep"]))
     return st
 
 
@@ -365,7 +364,7 @@ def run(st):
                                            path=st["path"], scale=st["scale"])}
     kept, new_len, scores = api.cache_evict(h, st["scores"], cache, st["len"], st["dst"], st["case"]["keep"],
                                             st["case"]["recent"], kept=st["kept"], new_len=st["new_len"],
-                                            dst_scores=st["dst_scores"], workspace=st["workspace"])
+                                            dst_scores=st["dst_scores"])
     return {"kept": kept, "new_len": new_len, "k": st["dst_k"], "v": st["dst_v"], "scores": scores}
 
 
