@@ -45,8 +45,22 @@ SIGNATURES = {
     "dflash2_gemm_conv2tap": (I32, [P, P, P, P, P, P, P, P, P, I64, I64, I64, I64, P, SZ, P, I32, P]),
     "dflash2_pair_scores_proj": (I32, [P, P, P, P, P, P, P, P, I64, I64, I64, I64, P, SZ, P, P]),
     "dflash2_lmhead_topk_noalloc": (I32, [P, P, P, I64, I64, I64, P, P, P]),
+    "dflash2_tree_attention_workspace": (SZ, [P, I64, I64, I64, I64, I64]),
+    "dflash2_tree_attention": (I32, [P, P, I64, I64, I64, P, P, P, P, I64, I64, I64, P, I64, I64, I64, F32, P, P, P,
+                                     SZ, P]),
+    "dflash2_cache_commit": (I32, [P, P, P, I64, I64, I64, P, P, P, P, I64, I64, P, I64, P, P]),
+    "dflash2_cache_scores": (I32, [P, P, I64, I64, I64, P, P, P, P, P, I64, I64, I64, F32, P, I64, P]),
+    "dflash2_cache_evict": (I32, [P, P, I64, P, P, P, I64, I64, I64, P, P, P, I64, P]),
     "dflash2_selftest_wait_timeout": (I32, [P, U64, P, P]),
 }
+
+
+class KvCacheStruct(ctypes.Structure):
+    """dflash2_kv_cache."""
+    _fields_ = [("k", P), ("v", P), ("num_pages", I64), ("page_size", I64), ("heads", I64), ("head_dim", I64),
+                ("page_stride", I64), ("token_stride", I64), ("head_stride", I64), ("block_table", P),
+                ("max_pages", I64), ("table_ld", I64)]
+
 
 _lib = None
 

@@ -20,6 +20,9 @@ STATUS = {0: "OK", -1: "INVALID_ARG", -2: "UNSUPPORTED", -3: "MISALIGNED", -4: "
 DEVERR_BAD_TOKEN = 0x1
 DEVERR_TIMEOUT = 0x2
 DEVERR_BAD_SLOT = 0x4
+DEVERR_BAD_PAGE = 0x8
+DEVERR_BAD_LENGTH = 0x10
+DEVERR_BAD_NODE = 0x20
 
 
 class Dflash2Error(RuntimeError):
@@ -337,6 +340,180 @@ def lmhead_topk_noalloc(h: Handle, hidden, W, vals=None, idx=None, stream=None):
                                               _stream(stream)), "dflash2_lmhead_topk_noalloc")
     return vals, idx
 
+
+class KVCache:
+    """A cache of keys and values in pages (the C struct dflash2_kv_cache, built once and passed to many calls).
+
+    k, v: bf16 [num_pages, page_size, kv_heads, head_dim] with equal strides, head_dim (64 or 128)
+    contiguous; a head-major pool [num_pages, kv_heads, page_size, head_dim] is passed as
+    ``pool.transpose(1, 2)``.  block_table: int32 [B, max_pages], position j of sequence b is in page
+    ``block_table[b, j // page_size]``; None: page b is the whole of sequence b."""
+
+    def __init__(self, k, v, block_table=None):
+        _need(_is16(k) and _is16(v) and k.dim() == 4 and k.shape == v.shape and k.stride() == v.stride() and
+              (k.stride(3) == 1 or k.shape[3] == 1), "k, v: bf16 [pages, page_size, heads, dim], equal strides, "
+              "unit stride along dim")
+        self.k, self.v, self.block_table = k, v, block_table
+        pages, page, heads, dim = k.shape
+        s = self.struct = _lib.KvCacheStruct()
+        s.k, s.v = _ptr(k), _ptr(v)
+        s.num_pages, s.page_size, s.heads, s.head_dim = pages, page, heads, dim
+        s.page_stride, s.token_stride, s.head_stride = k.stride()[:3]
+        if block_table is not None:
+            _need(block_table.dtype == torch.int32 and block_table.dim() == 2 and
+                  (block_table.stride(1) == 1 or block_table.shape[1] <= 1), "block_table: int32 [B, max_pages]")
+            s.block_table = _ptr(block_table)
+            s.max_pages, s.table_ld = block_table.shape[1], block_table.stride(0)
+        else:
+            s.max_pages = 1
+        self.batch = pages if block_table is None else block_table.shape[0]
+        self.capacity = page * s.max_pages
+        self.heads, self.dim = heads, dim
+        self.ref = ctypes.byref(s)
+
+
+def _rows(name, t, heads, dim):
+    _need(_is16(t) and t.dim() == 4 and t.shape[3] == dim and (heads is None or t.shape[2] == heads) and
+          t.stride(3) == 1, f"{name}: bf16 [B, T, heads, {dim}], unit stride along the last dimension")
+    return t.shape
+
+
+def _vec(name, t, dtype, shape):
+    _need(t.dtype == dtype and tuple(t.shape) == shape and t.is_contiguous(), f"{name}: contiguous {dtype} {shape}")
+
+
+def _new_on(stream, shape, dtype, dev):
+    """A tensor of the allocator's pool for the call's stream (so that its memory, once freed, is not handed to
+    another stream while the call still runs)."""
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=dev)
+    with torch.cuda.stream(stream):
+        return torch.empty(shape, dtype=dtype, device=dev)
+
+
+def tree_attention_workspace(h: Handle, B: int, T: int, heads: int, kv_heads: int, head_dim: int) -> int:
+    return int(h._lib.dflash2_tree_attention_workspace(h.ptr, B, T, heads, kv_heads, head_dim))
+
+
+def tree_attention(h: Handle, q, cache: KVCache, cache_len, k_new=None, v_new=None, tree_mask=None,
+                   scale: float = None, out=None, lse=None, workspace=None, stream=None):
+    """Drafted tokens over a cache and over their own chain or tree -> (out bf16 [B, T, heads, dim], lse fp32 [B, T, heads]).
+
+    q [B, T, heads, dim]; k_new, v_new [B, T, kv_heads, dim] (equal strides; None: the cache alone); tree_mask
+    int64 [B, T, (T + 63) // 64], bit s % 64 of word s // 64 of node t set where t sees s (None: a chain).
+    scale: 1 / sqrt(dim) when None.  workspace: device bytes of at least tree_attention_workspace(...)."""
+    B, T, heads, dim = _rows("q", q, None, cache.dim)
+    _need(cache.batch >= B, "cache: fewer sequences than q")
+    _vec("cache_len", cache_len, torch.int32, (B,))
+    qs = q.stride()
+    ns = (0, 0, 0)
+    if k_new is not None or v_new is not None:
+        _need(k_new is not None and v_new is not None and k_new.stride() == v_new.stride(),
+              "k_new, v_new: both or neither, with equal strides")
+        for name, t in (("k_new", k_new), ("v_new", v_new)):
+            _need(_rows(name, t, cache.heads, dim)[:2] == (B, T), f"{name}: [B, T] of q")
+        ns = k_new.stride()
+    if tree_mask is not None:
+        _vec("tree_mask", tree_mask, torch.int64, (B, T, (T + 63) // 64))
+    if out is None:
+        out = _new_on(stream, (B, T, heads, dim), torch.bfloat16, q.device)
+    else:
+        _need(_is16(out) and out.shape == q.shape and out.is_contiguous(), "out: contiguous bf16 of q's shape")
+    if lse is None:
+        lse = _new_on(stream, (B, T, heads), torch.float32, q.device)
+    else:
+        _vec("lse", lse, torch.float32, (B, T, heads))
+    if workspace is None:
+        workspace = _new_on(stream, (max(tree_attention_workspace(h, B, T, heads, cache.heads, dim), 256),),
+                            torch.uint8, q.device)
+    _check(h._lib.dflash2_tree_attention(
+        h.ptr, _ptr(q), qs[0], qs[1], qs[2], cache.ref, _ptr(cache_len), _ptr(k_new), _ptr(v_new), ns[0], ns[1], ns[2],
+        _ptr(tree_mask), B, T, heads, dim ** -0.5 if scale is None else scale, _ptr(out), _ptr(lse), _ptr(workspace),
+        workspace.numel() * workspace.element_size(), _stream(stream)), "dflash2_tree_attention")
+    return out, lse
+
+
+def cache_commit(h: Handle, k_new, v_new, cache: KVCache, cache_len, count=None, path=None, scores=None,
+                 new_len=None, stream=None):
+    """Appends the accepted nodes' keys and values to the cache -> new_len int32 [B].
+
+    k_new, v_new [B, T, kv_heads, dim]; count int32 [B] accepted nodes (None: T); path int32 [B, T] their ids
+    (None: 0, 1, ...); scores fp32 [B, kv_heads, ld]: the appended positions' entries become 0."""
+    B, T = _rows("k_new", k_new, cache.heads, cache.dim)[:2]
+    _need(_rows("v_new", v_new, cache.heads, cache.dim)[:2] == (B, T) and k_new.stride() == v_new.stride(),
+          "v_new: shape and strides of k_new")
+    _need(cache.batch >= B, "cache: fewer sequences than k_new")
+    _vec("cache_len", cache_len, torch.int32, (B,))
+    if count is not None:
+        _vec("count", count, torch.int32, (B,))
+    if path is not None:
+        _vec("path", path, torch.int32, (B, T))
+    ld = 0
+    if scores is not None:
+        ld = scores.shape[-1]
+        _vec("scores", scores, torch.float32, (B, cache.heads, ld))
+    if new_len is None:
+        new_len = _new_on(stream, (B,), torch.int32, k_new.device)
+    else:
+        _vec("new_len", new_len, torch.int32, (B,))
+    s = k_new.stride()
+    _check(h._lib.dflash2_cache_commit(h.ptr, _ptr(k_new), _ptr(v_new), s[0], s[1], s[2], cache.ref, _ptr(cache_len),
+                                       _ptr(count), _ptr(path), B, T, _ptr(scores), ld, _ptr(new_len),
+                                       _stream(stream)), "dflash2_cache_commit")
+    return new_len
+
+
+def cache_scores(h: Handle, q, lse, cache: KVCache, cache_len, scores, count=None, path=None, scale: float = None,
+                 stream=None):
+    """Adds to scores fp32 [B, kv_heads, ld] the attention weight that each cached position received from the
+    accepted nodes (q and lse as in tree_attention, count and path as in cache_commit) -> scores."""
+    B, T, heads, dim = _rows("q", q, None, cache.dim)
+    _need(cache.batch >= B, "cache: fewer sequences than q")
+    _vec("lse", lse, torch.float32, (B, T, heads))
+    _vec("cache_len", cache_len, torch.int32, (B,))
+    ld = scores.shape[-1]
+    _vec("scores", scores, torch.float32, (B, cache.heads, ld))
+    if count is not None:
+        _vec("count", count, torch.int32, (B,))
+    if path is not None:
+        _vec("path", path, torch.int32, (B, T))
+    s = q.stride()
+    _check(h._lib.dflash2_cache_scores(h.ptr, _ptr(q), s[0], s[1], s[2], _ptr(lse), cache.ref, _ptr(cache_len),
+                                       _ptr(count), _ptr(path), B, T, heads, dim ** -0.5 if scale is None else scale,
+                                       _ptr(scores), ld, _stream(stream)), "dflash2_cache_scores")
+    return scores
+
+
+def cache_evict(h: Handle, scores, cache: KVCache, cache_len, dst: KVCache, keep: int, recent: int, kept=None,
+                new_len=None, dst_scores=None, want_scores: bool = True, stream=None):
+    """Keeps, per head, the last `recent` positions and the highest-scored others, `keep` in all, in dst ->
+    (kept int32 [B, kv_heads, keep], new_len int32 [B], dst_scores fp32 [B, kv_heads, keep] or None).
+
+    scores fp32 [B, kv_heads, ld]; dst's pages must be none of the source's."""
+    B, ld = scores.shape[0], scores.shape[-1]
+    _vec("scores", scores, torch.float32, (B, cache.heads, ld))
+    _need(cache.batch >= B and dst.batch >= B, "cache, dst: fewer sequences than scores")
+    _vec("cache_len", cache_len, torch.int32, (B,))
+    shape = (B, cache.heads, keep)
+    if kept is None:
+        kept = _new_on(stream, shape, torch.int32, scores.device)
+    else:
+        _vec("kept", kept, torch.int32, shape)
+    if new_len is None:
+        new_len = _new_on(stream, (B,), torch.int32, scores.device)
+    else:
+        _vec("new_len", new_len, torch.int32, (B,))
+    dst_ld = keep
+    if dst_scores is not None:
+        dst_ld = dst_scores.shape[-1]
+        _need(dst_ld >= keep, "dst_scores: [B, kv_heads, at least keep]")
+        _vec("dst_scores", dst_scores, torch.float32, (B, cache.heads, dst_ld))
+    elif want_scores:
+        dst_scores = _new_on(stream, shape, torch.float32, scores.device)
+    _check(h._lib.dflash2_cache_evict(h.ptr, _ptr(scores), ld, cache.ref, _ptr(cache_len), dst.ref, B, keep, recent,
+                                      _ptr(kept), _ptr(new_len), _ptr(dst_scores), dst_ld, _stream(stream)),
+           "dflash2_cache_evict")
+    return kept, new_len, dst_scores
 
 
 def selftest_wait_timeout(h: Handle, limit_ns: int, words=None, stream=None):

@@ -9,6 +9,7 @@
 #include <nvtx3/nvToolsExt.h>
 
 #include "dflash2.h"
+#include "attn.h"
 #include "common.cuh"
 #include "launch.h"
 
@@ -22,6 +23,8 @@ namespace {
 
 constexpr int kK = 16;
 constexpr int64_t kMaxL = 64;
+constexpr int64_t kMaxKvHeads = 4096;
+constexpr int64_t kMaxCapacity = (int64_t(1) << 31) - 256;
 
 bool aligned(const void* p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p) & (a - 1)) == 0; }
 
@@ -55,6 +58,74 @@ struct NvtxRange {
   NvtxRange(const NvtxRange&) = delete;
   NvtxRange& operator=(const NvtxRange&) = delete;
 };
+
+// A stride in elements between `extent` pieces of `least` elements each: of no
+// effect when there is one piece, else a multiple of 8 that keeps them apart.
+bool bad_stride(int64_t stride, int64_t extent, int64_t least) {
+  return extent > 1 && (stride < least || stride >= (int64_t(1) << 38));
+}
+bool odd_stride(int64_t stride, int64_t extent) { return extent > 1 && stride % 8 != 0; }
+
+// Checks a cache descriptor for B sequences and turns it into the device view.
+int view_cache(const dflash2_kv_cache* c, int64_t B, dflash2::KvView* out) {
+  if (c == nullptr || c->num_pages < 0 || c->page_size < 0 || c->heads <= 0 || c->max_pages < 0)
+    return DFLASH2_ERR_INVALID_ARG;
+  if ((c->head_dim != 64 && c->head_dim != 128) || c->heads > kMaxKvHeads || c->num_pages >= (int64_t(1) << 31))
+    return DFLASH2_ERR_UNSUPPORTED;
+  const bool paged = c->block_table != nullptr;
+  if (paged && (c->page_size < 16 || (c->page_size & (c->page_size - 1)) != 0)) return DFLASH2_ERR_UNSUPPORTED;
+  if (c->page_size > kMaxCapacity || (paged && c->max_pages > kMaxCapacity / c->page_size))
+    return DFLASH2_ERR_UNSUPPORTED;
+  if (paged ? (c->table_ld < c->max_pages && B > 1) : c->num_pages < B) return DFLASH2_ERR_INVALID_ARG;
+  const int64_t capacity = paged ? c->max_pages * c->page_size : c->page_size;
+  if (capacity > 0 && c->num_pages > 0 && (!c->k || !c->v)) return DFLASH2_ERR_INVALID_ARG;
+  if (capacity > 0 && c->num_pages == 0 && B > 0) return DFLASH2_ERR_INVALID_ARG;
+  if (bad_stride(c->page_stride, c->num_pages, c->head_dim) || bad_stride(c->token_stride, c->page_size, c->head_dim) ||
+      bad_stride(c->head_stride, c->heads, c->head_dim))
+    return DFLASH2_ERR_INVALID_ARG;
+  if (!aligned(c->k, 16) || !aligned(c->v, 16) || !aligned(c->block_table, 4) ||
+      odd_stride(c->page_stride, c->num_pages) || odd_stride(c->token_stride, c->page_size) ||
+      odd_stride(c->head_stride, c->heads))
+    return DFLASH2_ERR_MISALIGNED;
+  out->k = c->k;
+  out->v = c->v;
+  // strides of single pieces are never multiplied by more than 0: any valid one will do
+  out->page_stride = c->num_pages > 1 ? c->page_stride : c->head_dim;
+  out->token_stride = c->page_size > 1 ? c->token_stride : c->head_dim;
+  out->head_stride = c->heads > 1 ? c->head_stride : c->head_dim;
+  out->table = c->block_table;
+  out->table_ld = c->table_ld;
+  out->num_pages = static_cast<int32_t>(c->num_pages);
+  out->page_size = static_cast<int32_t>(c->page_size);
+  out->page_shift = 0;
+  while (paged && (int64_t(1) << out->page_shift) < c->page_size) ++out->page_shift;
+  out->capacity = static_cast<int32_t>(capacity);
+  out->heads = static_cast<int32_t>(c->heads);
+  return DFLASH2_OK;
+}
+
+// Strides of a [B, T, n, d] bf16 operand.
+struct RowStrides {
+  int64_t b, t, h;
+};
+
+int check_rows(RowStrides* s, int64_t B, int64_t T, int64_t n, int64_t d) {
+  if (bad_stride(s->b, B, d) || bad_stride(s->t, T, d) || bad_stride(s->h, n, d)) return DFLASH2_ERR_INVALID_ARG;
+  if (odd_stride(s->b, B) || odd_stride(s->t, T) || odd_stride(s->h, n)) return DFLASH2_ERR_MISALIGNED;
+  if (B <= 1) s->b = d;
+  if (T <= 1) s->t = d;
+  if (n <= 1) s->h = d;
+  return DFLASH2_OK;
+}
+
+// What the query side of attention and scores shares.
+int check_queries(int64_t B, int64_t T, int64_t heads, const dflash2_kv_cache* cache, float scale) {
+  if (B < 0 || T < 0 || heads <= 0 || cache == nullptr || cache->heads <= 0 || heads % cache->heads != 0 ||
+      !(scale > 0.0f) || scale > 3.0e38f)
+    return DFLASH2_ERR_INVALID_ARG;
+  if (T > dflash2::kMaxNodes || B > 65535 || heads / cache->heads > 128) return DFLASH2_ERR_UNSUPPORTED;
+  return DFLASH2_OK;
+}
 
 }  // namespace
 
@@ -389,6 +460,159 @@ int dflash2_lmhead_topk_noalloc(dflash2_handle* h, const uint16_t* hidden, const
   if (dflash2::lmhead_noalloc_scratch(h->device, &scratch) != cudaSuccess) return DFLASH2_ERR_CUDA;
   return launched(dflash2::launch_lmhead_topk(hidden, W, M, V, d, vals, idx, scratch, h->num_sms, h->err,
                                               as_stream(stream)));
+}
+
+size_t dflash2_tree_attention_workspace(const dflash2_handle* h, int64_t B, int64_t T, int64_t heads,
+                                        int64_t kv_heads, int64_t head_dim) {
+  if (bad_handle(h) || B <= 0 || T <= 0 || T > dflash2::kMaxNodes || kv_heads <= 0 || heads <= 0 ||
+      heads % kv_heads != 0 || (head_dim != 64 && head_dim != 128))
+    return 0;
+  return dflash2::tree_attn_workspace_bytes(B, T, heads, kv_heads, head_dim, h->num_sms);
+}
+
+int dflash2_tree_attention(dflash2_handle* h, const uint16_t* q, int64_t q_batch_stride, int64_t q_token_stride,
+                           int64_t q_head_stride, const dflash2_kv_cache* cache, const int32_t* cache_len,
+                           const uint16_t* k_new, const uint16_t* v_new, int64_t new_batch_stride,
+                           int64_t new_token_stride, int64_t new_head_stride, const uint64_t* tree_mask, int64_t B,
+                           int64_t T, int64_t heads, float scale, uint16_t* out, float* lse, void* workspace,
+                           size_t ws_bytes, void* stream) {
+  const NvtxRange range("dflash2_tree_attention");
+  if (bad_handle(h)) return DFLASH2_ERR_INVALID_ARG;
+  if (const int st = check_queries(B, T, heads, cache, scale)) return st;
+  dflash2::AttnArgs a;
+  if (const int st = view_cache(cache, B, &a.cache)) return st;
+  if (B == 0 || T == 0) return DFLASH2_OK;
+  if (!q || !cache_len || !out || (k_new == nullptr) != (v_new == nullptr) || (tree_mask && !k_new))
+    return DFLASH2_ERR_INVALID_ARG;
+  RowStrides qs = {q_batch_stride, q_token_stride, q_head_stride};
+  RowStrides ns = {new_batch_stride, new_token_stride, new_head_stride};
+  if (const int st = check_rows(&qs, B, T, heads, cache->head_dim)) return st;
+  if (k_new)
+    if (const int st = check_rows(&ns, B, T, cache->heads, cache->head_dim)) return st;
+  if (!aligned(q, 16) || !aligned(k_new, 16) || !aligned(v_new, 16) || !aligned(cache_len, 4) ||
+      !aligned(tree_mask, 8) || !aligned(out, 16) || !aligned(lse, 4) || !aligned(workspace, 256))
+    return DFLASH2_ERR_MISALIGNED;
+  if (ws_bytes < dflash2::tree_attn_workspace_bytes(B, T, heads, cache->heads, cache->head_dim, h->num_sms) ||
+      workspace == nullptr)
+    return DFLASH2_ERR_WORKSPACE;
+  if (const int st = wrong_device(h)) return st;
+  a.q = q;
+  a.q_b = qs.b, a.q_t = qs.t, a.q_h = qs.h;
+  a.cache_len = cache_len;
+  a.k_new = k_new;
+  a.v_new = v_new;
+  a.new_b = ns.b, a.new_t = ns.t, a.new_h = ns.h;
+  a.mask = tree_mask;
+  a.B = B;
+  a.T = static_cast<int32_t>(T);
+  a.heads = static_cast<int32_t>(heads);
+  a.group = static_cast<int32_t>(heads / cache->heads);
+  a.scale = scale;
+  a.out = out;
+  a.lse = lse;
+  a.err = h->err;
+  return launched(dflash2::launch_tree_attn(a, cache->head_dim, workspace, h->num_sms, as_stream(stream)));
+}
+
+int dflash2_cache_commit(dflash2_handle* h, const uint16_t* k_new, const uint16_t* v_new, int64_t new_batch_stride,
+                         int64_t new_token_stride, int64_t new_head_stride, const dflash2_kv_cache* cache,
+                         const int32_t* cache_len, const int32_t* count, const int32_t* path, int64_t B, int64_t T,
+                         float* scores, int64_t scores_ld, int32_t* new_len, void* stream) {
+  const NvtxRange range("dflash2_cache_commit");
+  if (bad_handle(h) || B < 0 || T < 0 || (scores && scores_ld < 0)) return DFLASH2_ERR_INVALID_ARG;
+  if (T > dflash2::kMaxNodes || B > 65535) return DFLASH2_ERR_UNSUPPORTED;
+  dflash2::CommitArgs a;
+  if (const int st = view_cache(cache, B, &a.cache)) return st;
+  if (B == 0) return DFLASH2_OK;
+  if (!cache_len || !new_len || cache_len == new_len || (T > 0 && (!k_new || !v_new))) return DFLASH2_ERR_INVALID_ARG;
+  RowStrides ns = {new_batch_stride, new_token_stride, new_head_stride};
+  if (const int st = check_rows(&ns, B, T, cache->heads, cache->head_dim)) return st;
+  if (!aligned(k_new, 16) || !aligned(v_new, 16) || !aligned(cache_len, 4) || !aligned(count, 4) ||
+      !aligned(path, 4) || !aligned(scores, 4) || !aligned(new_len, 4))
+    return DFLASH2_ERR_MISALIGNED;
+  if (const int st = wrong_device(h)) return st;
+  a.k_new = k_new;
+  a.v_new = v_new;
+  a.new_b = ns.b, a.new_t = ns.t, a.new_h = ns.h;
+  a.cache_len = cache_len;
+  a.count = count;
+  a.path = path;
+  a.B = B;
+  a.T = static_cast<int32_t>(T);
+  a.scores = scores;
+  a.scores_ld = scores_ld;
+  a.new_len = new_len;
+  a.err = h->err;
+  return launched(dflash2::launch_cache_commit(a, cache->head_dim, as_stream(stream)));
+}
+
+int dflash2_cache_scores(dflash2_handle* h, const uint16_t* q, int64_t q_batch_stride, int64_t q_token_stride,
+                         int64_t q_head_stride, const float* lse, const dflash2_kv_cache* cache,
+                         const int32_t* cache_len, const int32_t* count, const int32_t* path, int64_t B, int64_t T,
+                         int64_t heads, float scale, float* scores, int64_t scores_ld, void* stream) {
+  const NvtxRange range("dflash2_cache_scores");
+  if (bad_handle(h) || scores_ld < 0) return DFLASH2_ERR_INVALID_ARG;
+  if (const int st = check_queries(B, T, heads, cache, scale)) return st;
+  dflash2::ScoresArgs a;
+  if (const int st = view_cache(cache, B, &a.cache)) return st;
+  if (B == 0 || T == 0) return DFLASH2_OK;
+  if (!q || !lse || !cache_len || !scores) return DFLASH2_ERR_INVALID_ARG;
+  RowStrides qs = {q_batch_stride, q_token_stride, q_head_stride};
+  if (const int st = check_rows(&qs, B, T, heads, cache->head_dim)) return st;
+  if (!aligned(q, 16) || !aligned(lse, 4) || !aligned(cache_len, 4) || !aligned(count, 4) || !aligned(path, 4) ||
+      !aligned(scores, 4))
+    return DFLASH2_ERR_MISALIGNED;
+  if (const int st = wrong_device(h)) return st;
+  a.q = q;
+  a.q_b = qs.b, a.q_t = qs.t, a.q_h = qs.h;
+  a.lse = lse;
+  a.cache_len = cache_len;
+  a.count = count;
+  a.path = path;
+  a.B = B;
+  a.T = static_cast<int32_t>(T);
+  a.heads = static_cast<int32_t>(heads);
+  a.group = static_cast<int32_t>(heads / cache->heads);
+  a.scale = scale;
+  a.scores = scores;
+  a.scores_ld = scores_ld;
+  a.err = h->err;
+  return launched(dflash2::launch_cache_scores(a, cache->head_dim, h->num_sms, as_stream(stream)));
+}
+
+int dflash2_cache_evict(dflash2_handle* h, const float* scores, int64_t scores_ld, const dflash2_kv_cache* cache,
+                        const int32_t* cache_len, const dflash2_kv_cache* dst, int64_t B, int64_t keep,
+                        int64_t recent, int32_t* kept, int32_t* new_len, float* dst_scores, int64_t dst_ld,
+                        void* stream) {
+  const NvtxRange range("dflash2_cache_evict");
+  if (bad_handle(h) || B < 0 || scores_ld < 0 || keep < 1 || recent < 0 || recent > keep ||
+      (dst_scores && dst_ld < keep))
+    return DFLASH2_ERR_INVALID_ARG;
+  dflash2::EvictArgs a;
+  if (const int st = view_cache(cache, B, &a.cache)) return st;
+  if (const int st = view_cache(dst, B, &a.dst)) return st;
+  if (cache->heads != dst->heads || cache->head_dim != dst->head_dim) return DFLASH2_ERR_INVALID_ARG;
+  if (B > 65535 || B * cache->heads >= (int64_t(1) << 24)) return DFLASH2_ERR_UNSUPPORTED;
+  if (B == 0) return DFLASH2_OK;
+  if (keep > a.dst.capacity || !scores || !cache_len || !kept || !new_len || new_len == cache_len ||
+      dst_scores == scores)
+    return DFLASH2_ERR_INVALID_ARG;
+  if (!aligned(scores, 4) || !aligned(cache_len, 4) || !aligned(kept, 4) || !aligned(new_len, 4) ||
+      !aligned(dst_scores, 4))
+    return DFLASH2_ERR_MISALIGNED;
+  if (const int st = wrong_device(h)) return st;
+  a.scores = scores;
+  a.scores_ld = scores_ld;
+  a.cache_len = cache_len;
+  a.B = B;
+  a.keep = static_cast<int32_t>(keep);
+  a.recent = static_cast<int32_t>(recent);
+  a.kept = kept;
+  a.new_len = new_len;
+  a.dst_scores = dst_scores;
+  a.dst_ld = dst_ld;
+  a.err = h->err;
+  return launched(dflash2::launch_cache_evict(a, cache->head_dim, h->num_sms, as_stream(stream)));
 }
 
 }  // extern "C"

@@ -15,6 +15,11 @@
  *   dflash2_verify        block verification -> acceptance lengths
  *   dflash2_lmhead_topk   LM head GEMM with a streaming top-16 epilogue
  *   dflash2_lmhead_topk_gate  the same with the context gate folded in
+ * and, around the verify pass that produces the target's logits:
+ *   dflash2_tree_attention  a block or tree of drafted tokens over a paged cache
+ *   dflash2_cache_commit    the accepted path's keys and values into the cache
+ *   dflash2_cache_scores    attention weight received by each cached position
+ *   dflash2_cache_evict     the positions weighed most, kept in fresh pages
  *
  * Conventions for every call
  *   - Pointers marked "device" are CUDA device pointers on the handle's device;
@@ -71,6 +76,9 @@ enum dflash2_status {
 #define DFLASH2_DEVERR_BAD_TOKEN 0x1u /* a token id outside [0, V) was clamped     */
 #define DFLASH2_DEVERR_TIMEOUT 0x2u   /* a bounded wait (TMA / mbarrier) gave up  */
 #define DFLASH2_DEVERR_BAD_SLOT 0x4u  /* a draft slot outside [0, 16) was clamped */
+#define DFLASH2_DEVERR_BAD_PAGE 0x8u  /* a page id outside [0, num_pages): read as a clamped page, never written */
+#define DFLASH2_DEVERR_BAD_LENGTH 0x10u /* a cache length or count outside its range was clamped */
+#define DFLASH2_DEVERR_BAD_NODE 0x20u /* a path's node outside [0, T) was clamped  */
 
 /* Library version: major * 10000 + minor * 100 + patch. */
 int dflash2_version(void);
@@ -407,6 +415,133 @@ int dflash2_lmhead_topk_noalloc(dflash2_handle* h, const uint16_t* hidden, const
  *          satisfied (never) and bit 2 when the kernel reached its end.
  */
 int dflash2_selftest_wait_timeout(dflash2_handle* h, uint64_t limit_ns, uint32_t* words, void* stream);
+
+/*
+ * A cache of keys and values in pages.  "One-pass verify" (opening section):
+ * the target verifies a whole block in one pass over its cache.  Position j of
+ * sequence b is row j % page_size of page block_table[b * table_ld + j /
+ * page_size]; its head h starts at element
+ *   page * page_stride + (j % page_size) * token_stride + h * head_stride
+ * of k (and of v: both have these strides) and is head_dim contiguous bf16.  A
+ * NULL block_table makes page b the whole of sequence b (max_pages = 1).
+ *   head_dim 64 or 128.  With a block table page_size is a power of two and at
+ *   least 16; without one it is any size.  Strides are in elements, multiples of
+ *   8 and at least head_dim (of no effect where their extent is 1); k and v are
+ *   16-byte aligned.  A sequence's capacity is max_pages * page_size < 2^31 - 256.
+ * The struct is read on the host during the call; k, v and block_table are
+ * device pointers.
+ */
+typedef struct dflash2_kv_cache {
+  uint16_t* k;
+  uint16_t* v;
+  int64_t num_pages;
+  int64_t page_size;
+  int64_t heads;    /* key/value heads */
+  int64_t head_dim;
+  int64_t page_stride;
+  int64_t token_stride;
+  int64_t head_stride;
+  const int32_t* block_table; /* device [B, table_ld], or NULL */
+  int64_t max_pages;          /* entries of a sequence's row of block_table */
+  int64_t table_ld;
+} dflash2_kv_cache;
+
+/*
+ * Attention from a block or tree of drafted tokens to a cache and to one
+ * another: the target's pass over a draft block ("one-pass verify").  Query
+ * head hq of node t attends, with the keys and values of head hq / (heads /
+ * cache->heads), to cached positions j < cache_len[b] and to the drafted nodes
+ * s whose bit is set in node t's mask:
+ *   z_x = scale <q[b,t,hq], key_x>,  lse = log sum_x exp(z_x),
+ *   out[b,t,hq] = sum_x exp(z_x - lse) value_x.
+ * A row that sees nothing, or only keys with z = -inf, gives out = 0 and lse =
+ * -inf.  What a row does not see never reaches it, whatever values it holds.
+ *   q             device bf16 [B, T, heads, head_dim] with the given strides
+ *   cache_len     device int32 [B]; outside [0, capacity]: clamped and flagged
+ *   k_new, v_new  device bf16 [B, T, cache->heads, head_dim], the drafted nodes'
+ *                 keys and values (both with the strides new_*), or both NULL:
+ *                 the queries then attend to the cache alone
+ *   tree_mask     device uint64 [B, T, (T + 63) / 64], bit s % 64 of word s / 64
+ *                 of node t: t sees s; or NULL: a chain (t sees every s <= t)
+ *   scale         finite and > 0
+ *   out           device bf16 [B, T, heads, head_dim], contiguous
+ *   lse           device fp32 [B, T, heads] or NULL
+ *   workspace     device scratch of at least dflash2_tree_attention_workspace()
+ *                 bytes, 256-byte aligned, rewritten by every call; calls that
+ *                 overlap on the GPU must not share it
+ * T <= 128; heads a multiple of cache->heads, at most 128 times as many; B <=
+ * 65535; q, k_new and v_new 16-byte aligned, strides multiples of 8.  Dot
+ * products, sums and statistics are fp32; the weights enter the product with the
+ * values as bf16.  The same inputs give the same bits on every call.
+ */
+size_t dflash2_tree_attention_workspace(const dflash2_handle* h, int64_t B, int64_t T, int64_t heads,
+                                        int64_t kv_heads, int64_t head_dim);
+int dflash2_tree_attention(dflash2_handle* h, const uint16_t* q, int64_t q_batch_stride, int64_t q_token_stride,
+                           int64_t q_head_stride, const dflash2_kv_cache* cache, const int32_t* cache_len,
+                           const uint16_t* k_new, const uint16_t* v_new, int64_t new_batch_stride,
+                           int64_t new_token_stride, int64_t new_head_stride, const uint64_t* tree_mask, int64_t B,
+                           int64_t T, int64_t heads, float scale, uint16_t* out, float* lse, void* workspace,
+                           size_t ws_bytes, void* stream);
+
+/*
+ * Appends the accepted path to the cache.  After verification the accepted
+ * nodes' keys and values join the cache and the rest of the block is dropped:
+ * for i < count[b], node path[b,i] becomes position cache_len[b] + i.
+ *   k_new, v_new  device bf16 [B, T, cache->heads, head_dim] (strides as above)
+ *   count         device int32 [B] (e.g. dflash2_verify's accept_len, when node
+ *                 0 is the last verified token) or NULL: all T
+ *   path          device int32 [B, T] node ids, or NULL: node i is i
+ *   scores        device fp32 [B, cache->heads, scores_ld] or NULL: the appended
+ *                 positions' entries are set to 0
+ *   new_len       device int32 [B]: cache_len + count; must not overlap cache_len
+ * Positions past the capacity (or scores_ld, when scores is given) are dropped,
+ * new_len stops there, and DFLASH2_DEVERR_BAD_LENGTH is flagged.  Two sequences
+ * must not append to the same page.
+ */
+int dflash2_cache_commit(dflash2_handle* h, const uint16_t* k_new, const uint16_t* v_new, int64_t new_batch_stride,
+                         int64_t new_token_stride, int64_t new_head_stride, const dflash2_kv_cache* cache,
+                         const int32_t* cache_len, const int32_t* count, const int32_t* path, int64_t B, int64_t T,
+                         float* scores, int64_t scores_ld, int32_t* new_len, void* stream);
+
+/*
+ * Adds to each cached position the attention weight it received from the
+ * accepted nodes, over all query heads of its key/value head:
+ *   scores[b,h,j] += sum_{i < count[b]} sum_{hq of h} exp(scale <q[b,n,hq],
+ *   k[b,j,h]> - lse[b,n,hq]),  n = path[b,i],  j < cache_len[b].
+ *   q, cache, cache_len, scale as in dflash2_tree_attention, with its lse
+ *   lse     device fp32 [B, T, heads]; a query whose lse is -inf adds nothing
+ *   count, path  as in dflash2_cache_commit
+ *   scores  device fp32 [B, cache->heads, scores_ld]; entries at j >=
+ *           cache_len[b] are left alone.  A length past scores_ld is clamped and
+ *           flagged.
+ * Sums are fp32 in a fixed order.
+ */
+int dflash2_cache_scores(dflash2_handle* h, const uint16_t* q, int64_t q_batch_stride, int64_t q_token_stride,
+                         int64_t q_head_stride, const float* lse, const dflash2_kv_cache* cache,
+                         const int32_t* cache_len, const int32_t* count, const int32_t* path, int64_t B, int64_t T,
+                         int64_t heads, float scale, float* scores, int64_t scores_ld, void* stream);
+
+/*
+ * Shrinks each head's cache to at most `keep` positions: the last `recent`
+ * ones, and of the others those with the largest scores (ties by lowest
+ * position; -0 = +0, NaN below -inf), in their order, copied to the
+ * destination's positions 0 .. min(cache_len, keep) - 1.
+ *   scores      device fp32 [B, cache->heads, scores_ld]
+ *   dst         the destination: same heads and head_dim, capacity >= keep.  Its
+ *               pages must be none of the source's (which other sequences may
+ *               share, and which the call only reads)
+ *   kept        device int32 [B, heads, keep]: the kept positions, ascending,
+ *               then -1
+ *   new_len     device int32 [B]: min(cache_len, keep)
+ *   dst_scores  device fp32 [B, heads, dst_ld], dst_ld >= keep, or NULL: the
+ *               kept positions' scores; must not overlap scores
+ * 1 <= keep, 0 <= recent <= keep; B * heads < 2^24.  A length outside [0,
+ * min(capacity, scores_ld)] is clamped and flagged.
+ */
+int dflash2_cache_evict(dflash2_handle* h, const float* scores, int64_t scores_ld, const dflash2_kv_cache* cache,
+                        const int32_t* cache_len, const dflash2_kv_cache* dst, int64_t B, int64_t keep,
+                        int64_t recent, int32_t* kept, int32_t* new_len, float* dst_scores, int64_t dst_ld,
+                        void* stream);
 
 #ifdef __cplusplus
 }
