@@ -121,7 +121,7 @@ int check_rows(RowStrides* s, int64_t B, int64_t T, int64_t n, int64_t d) {
 // What the query side of attention and scores shares.
 int check_queries(int64_t B, int64_t T, int64_t heads, const dflash2_kv_cache* cache, float scale) {
   if (B < 0 || T < 0 || heads <= 0 || cache == nullptr || cache->heads <= 0 || heads % cache->heads != 0 ||
-      !(scale > 0.0f) || scale > 3.0e38f)
+      !(scale > 0.0f) || scale > 1.0e38f)
     return DFLASH2_ERR_INVALID_ARG;
   if (T > dflash2::kMaxNodes || B > 65535 || heads / cache->heads > 128) return DFLASH2_ERR_UNSUPPORTED;
   return DFLASH2_OK;

@@ -144,6 +144,12 @@ __device__ __forceinline__ void named_bar_sync(int id, int count) {
 bool make_tmap_bf16_2d(CUtensorMap* map, const void* base, uint64_t rows, uint64_t cols, uint64_t ld,
                        uint32_t box_rows);
 
+// A bf16 tensor map of rank 2..5: dims and box innermost first, strides (elements)
+// of dimensions 1.., 128-byte swizzle (box[0] = 64).  Elements of a box beyond a
+// dimension's end read as zero.  Returns false if the driver rejects it.
+bool make_tmap_bf16_nd(CUtensorMap* map, const void* base, int rank, const uint64_t* dims, const uint64_t* strides,
+                       const uint32_t* box);
+
 // A 3-D fp32 tensor map over a dense [d2][d1][d0] array (d0 innermost), box =
 // [box1, box0] in one d2 slice, with the 128-byte swizzle (box0 * 4 <= 128
 // bytes).  Boxes clip at every dimension's end, so a store never crosses

@@ -3,80 +3,926 @@
 //
 //   z_x = scale <q, k_x>,  lse = log sum exp z_x,  out = sum exp(z_x - lse) v_x
 //
-// One warp per query row (b, t, hq).  The row's keys are taken one by one with
-// the running maximum m and sum l of a softmax: o and l are multiplied by
-// exp(m - m') when the maximum rises to m'.
-#include "kvcache.cuh"
-#include "launch.h"
+// The query rows that share a key/value head, (node t, head g of the group) with
+// row t * group + g, are stacked into tiles of up to 128 rows (whole nodes), so
+// that a key is read once for all of them and both products fill the tensor
+// cores' 128 rows.  Keys come in tiles of 128: the cache's tiles, then one tile
+// of the drafted nodes.  An item is (sequence, kv head, pair of row tiles); its
+// key tiles are its units.  All units of the call, item after item, are cut into
+// equal runs, one per CTA (one CTA per SM): ragged lengths balance whatever they
+// are, and an axis is split exactly where runs end.  An item cut by a run's end
+// leaves unnormalised partial sums (fp32 O, m, l) in the workspace, and
+// tree_attn_join_kernel adds them in run order (same bits on every call).
+//
+// tree_attn_kernel, per CTA:
+//   warp 0      TMA producer: the item's query tiles, then each unit's K and V
+//               tiles (128 x D bf16, 128-byte swizzle, one box per page piece,
+//               the lanes issuing in parallel) into a ring.
+//   warps 1, 2  MMA issuers of pipelines 0 and 1: S = Q K^T (128 x 128, fp32 in
+//               TMEM), then O += P V, with P (bf16) read from TMEM where it
+//               replaced S (and, over few keys, what P lost in rounding to bf16).
+//   warps 4-7, 8-11  softmax of pipelines 0 and 1, one row per thread: S from
+//               TMEM, running maximum m and sum l in base 2, P = 2^(S c - m) back
+//               to TMEM.  O is rescaled only when a row's maximum has risen by
+//               more than 2^8 since m was set (P then stays below 2^8, exact in
+//               scale), so most units never touch O outside the tensor cores.
+// The two pipelines alternate on the tensor cores: one's softmax runs under the
+// other's products.  With two row tiles in the item each pipeline takes one of
+// them over every unit; with one row tile the pipelines take alternate units of
+// it and their two (O, m, l) are added at the end.
+//
+// A value no row sees must not reach the sums even as 0 * NaN: cached V rows past
+// the length are zeroed in shared memory, and a drafted node's non-finite values
+// (which only some rows may see) are zeroed there too and added to the rows that
+// do see them when the item is written.
+//
+// Every wait is bounded (DFLASH2_DEVERR_TIMEOUT): after one gives up the CTA
+// stops issuing copies and products, walks its loops to their end, waits for its
+// own copies in flight, frees its TMEM and returns.
 #include "attn.h"
+#include "launch.h"
+#include "tcgen05.cuh"
 
 namespace dflash2 {
 namespace {
 
+constexpr int kTile = 128;              // rows of a query tile, keys of a unit
+constexpr int kThreads = 384;
+constexpr int kMaxSlots = 10;
+constexpr int kMinRun = 1;              // least units per CTA
+constexpr int kTwoTermUnits = 8;        // items of up to so many units carry P in two terms
+constexpr float kRescale = 8.0f;        // log2 of how far P may exceed 1
+
 template <int D>
-__global__ void __launch_bounds__(256) tree_attn_kernel(const AttnArgs a) {
-  constexpr int E = D / 32;   // elements per lane
-  const int lane = threadIdx.x & 31;
-  const int64_t row = static_cast<int64_t>(blockIdx.x) * (blockDim.x / 32) + (threadIdx.x >> 5);
-  if (row >= a.B * a.T * a.heads) return;
-  const int hq = static_cast<int>(row % a.heads);
-  const int t = static_cast<int>(row / a.heads % a.T);
-  const int64_t b = row / a.heads / a.T;
-  const int h = hq / a.group;
-  float q[E], o[E];
-  const uint16_t* qp = a.q + b * a.q_b + t * a.q_t + hq * a.q_h + lane * E;
-#pragma unroll
-  for (int e = 0; e < E; ++e) {
-    q[e] = bf16_bits_to_float(qp[e]) * a.scale;
-    o[e] = 0.0f;
-  }
-  float m = -INFINITY, l = 0.0f;
-  const auto take = [&](const uint16_t* k, const uint16_t* v) {
-    float z = 0.0f;
-#pragma unroll
-    for (int e = 0; e < E; ++e) z += q[e] * bf16_bits_to_float(k[lane * E + e]);
-#pragma unroll
-    for (int s = 16; s > 0; s >>= 1) z += __shfl_xor_sync(0xFFFFFFFFu, z, s);
-    if (z == -INFINITY) return;
-    const float m1 = fmaxf(m, z);   // a NaN z leaves m alone and makes l NaN
-    const float f = expf(m - m1), p = expf(z - m1);
-    m = m1;
-    l = l * f + p;
-#pragma unroll
-    for (int e = 0; e < E; ++e) o[e] = o[e] * f + p * bf16_bits_to_float(v[lane * E + e]);
-  };
+struct Cfg {
+  static constexpr int kHalves = D / 64;                 // 128-byte column blocks of a row
+  static constexpr int kTileBytes = kTile * D * 2;
+  static constexpr int kSlots = D == 128 ? 5 : 10;       // ring of K and V tiles: 160 KB
+  static constexpr size_t kRing = static_cast<size_t>(2 + kSlots) * kTileBytes;
+};
+
+struct AttnSmem {
+  uint64_t kv_full[kMaxSlots], kv_empty[kMaxSlots];
+  uint64_t q_full, q_empty;
+  uint64_t s_full[2], p_ready[2], pv_done[2], drain;
+  float2 ml[2][kTile];
+  uint32_t bad[4];          // drafted nodes that hold a non-finite value
+  int64_t scan[kThreads / 32];
+  int64_t u0, u1, base;
+  int32_t b0;
+  uint32_t tmem;
+  int abort_flag;
+};
+
+struct AttnPlan {
+  AttnArgs a;
+  int32_t tpt;              // nodes per row tile
+  int32_t row_tiles, pairs; // row tiles, and pairs of them
+  int32_t areas;            // partial areas per slot (row tiles of a pair)
+  float c;                  // scale * log2(e)
+  float* part;              // [2 * runs][areas][D / 4][128] float4
+  float2* part_ml;          // [2 * runs][areas][128] (m, l)
+  int32_t box_rows;         // rows of a K or V box
+  uint32_t q_box_bytes;
+};
+
+__device__ __forceinline__ float exp2_approx(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+
+__device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
+  uint32_t r;
+  asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+  return r;
+}
+
+// two independent fp32 operations per instruction
+__device__ __forceinline__ uint64_t pack2(float x, float y) {
+  uint64_t r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(x), "f"(y));
+  return r;
+}
+__device__ __forceinline__ float2 unpack2(uint64_t v) {
+  float2 r;
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(v));
+  return r;
+}
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
+  uint64_t d;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(a), "l"(b), "l"(c));
+  return d;
+}
+__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
+  uint64_t d;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+  return d;
+}
+
+// The bf16 pair of what a pair of fp32 values lost when it was rounded to `hi`.
+__device__ __forceinline__ uint32_t remainder_bf16(uint64_t p, uint32_t hi) {
+  const uint64_t back = pack2(__uint_as_float(hi << 16), __uint_as_float(hi & 0xFFFF0000u));
+  const float2 r = unpack2(fma2(back, pack2(-1.0f, -1.0f), p));
+  return pack_bf16(r.x, r.y);
+}
+
+// Key tiles of sequence b, the drafted one included (at least one, so that every row is written).
+__device__ __forceinline__ int64_t units_of(const AttnArgs& a, int64_t b) {
   const int32_t n = kv_clamp(a.cache_len[b], a.cache.capacity, a.err);
-  for (int32_t j = 0; j < n; ++j) {
-    bool ok;
-    const int64_t off = kv_offset(a.cache, b, j, h, a.err, &ok);
-    take(a.cache.k + off, a.cache.v + off);
+  const int64_t u = (static_cast<int64_t>(n) + kTile - 1) / kTile + (a.k_new != nullptr ? 1 : 0);
+  return u > 0 ? u : 1;
+}
+
+// Cuts all units into runs of equal length and finds the sequence that unit
+// run * length + at_end * length (the run's start or end) falls into: *base =
+// units before that sequence's.  Whole-block; every thread returns the same.
+template <int kT>
+__device__ void find_run(const AttnPlan& p, int64_t run, int64_t runs, int at_end, int64_t* scan, int64_t* out_u0,
+                         int64_t* out_u1, int64_t* out_base, int32_t* out_b) {
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int64_t per_seq = static_cast<int64_t>(p.a.cache.heads) * p.pairs;
+  const int64_t chunk = (p.a.B + kT - 1) / kT;
+  const int64_t b_lo = tid * chunk, b_hi = imin64(p.a.B, b_lo + chunk);
+  int64_t sum = 0;
+  for (int64_t b = b_lo; b < b_hi; ++b) sum += units_of(p.a, b) * per_seq;
+  int64_t incl = sum;
+#pragma unroll
+  for (int s = 1; s < 32; s <<= 1) {
+    const int64_t o = __shfl_up_sync(0xFFFFFFFFu, incl, s);
+    if (lane >= s) incl += o;
   }
-  if (a.k_new != nullptr) {
-    const int words = (a.T + 63) / 64;
-    for (int s = 0; s < a.T; ++s) {
-      const bool sees = a.mask == nullptr ? s <= t : (a.mask[(b * a.T + t) * words + s / 64] >> (s % 64)) & 1;
-      const int64_t off = b * a.new_b + s * a.new_t + h * a.new_h;
-      if (sees) take(a.k_new + off, a.v_new + off);
+  if (lane == 31) scan[warp] = incl;
+  __syncthreads();
+  int64_t before = incl - sum, total = 0;
+  for (int w = 0; w < kT / 32; ++w) {
+    if (w < warp) before += scan[w];
+    total += scan[w];
+  }
+  const int64_t len = imax64((total + runs - 1) / runs, kMinRun);
+  const int64_t u0 = imin64(run * len, total), u1 = imin64(u0 + len, total);
+  const int64_t u = at_end ? u1 : u0;
+  if (u >= before && u < before + sum) {
+    int64_t base = before, b = b_lo;
+    for (;; ++b) {
+      const int64_t n = units_of(p.a, b) * per_seq;
+      if (u < base + n) break;
+      base += n;
+    }
+    *out_base = base;
+    *out_b = static_cast<int32_t>(b);
+  }
+  if (tid == 0) {
+    *out_u0 = u0;
+    *out_u1 = u1;
+  }
+  __syncthreads();
+}
+
+// One item's stretch of a run.
+struct Segment {
+  int32_t b, h, pair;
+  int32_t s, e, n;          // units [s, e) of n
+  int32_t tiles;            // row tiles (2: one per pipeline; 1: shared by both)
+  int32_t len;              // cached positions
+  bool first;               // the run's first segment
+  // Whether P enters the product with V as two bf16 terms.  Rounding P to bf16
+  // perturbs each weight by up to 2^-8 on its own: over many keys that averages
+  // out below the output's own rounding, over few it does not.
+  __device__ __forceinline__ bool two_terms() const { return n <= kTwoTermUnits; }
+  __device__ __forceinline__ int count() const { return e - s; }
+  // units that pipeline i takes
+  __device__ __forceinline__ int count(int i) const { return tiles == 2 ? e - s : (e - s + 1 - i) >> 1; }
+};
+
+// Walks a run's segments; each role of the CTA keeps its own.
+struct Walk {
+  int64_t u, u1, u_first, base, n_seq;
+  int32_t b, n;
+  __device__ __forceinline__ void start(const AttnPlan& p, const AttnSmem& s) {
+    u = u_first = s.u0;
+    u1 = s.u1;
+    base = s.base;
+    b = s.b0;
+    if (u < u1) load(p);
+  }
+  __device__ __forceinline__ void load(const AttnPlan& p) {
+    const int64_t k = units_of(p.a, b);
+    n = static_cast<int32_t>(k);
+    n_seq = k * p.a.cache.heads * p.pairs;
+  }
+  __device__ __forceinline__ bool next(const AttnPlan& p, Segment* g) {
+    if (u >= u1) return false;
+    if (u >= base + n_seq) {
+      base += n_seq;
+      ++b;
+      load(p);
+    }
+    const int64_t rel = u - base;
+    const int64_t item = rel / n;
+    g->s = static_cast<int32_t>(rel - item * n);
+    g->e = static_cast<int32_t>(imin64(n, g->s + (u1 - u)));
+    g->n = n;
+    g->b = b;
+    g->pair = static_cast<int32_t>(item % p.pairs);
+    g->h = static_cast<int32_t>(item / p.pairs);
+    g->tiles = min(2, p.row_tiles - 2 * g->pair);
+    g->len = kv_clamp(p.a.cache_len[b], p.a.cache.capacity, nullptr);
+    g->first = u == u_first;
+    u += g->e - g->s;
+    return true;
+  }
+};
+
+// A bounded wait that also gives up when another role of the CTA has; once one
+// has given up (*live = false) later waits return at once.
+__device__ __forceinline__ void wait_live(uint64_t* bar, uint32_t parity, bool* live, volatile int* abort_flag,
+                                          uint32_t* err) {
+  if (!*live || mbar_try_wait(bar, parity)) return;
+  const uint64_t start = global_timer_ns();
+  for (uint32_t it = 1;; ++it) {
+    if (mbar_try_wait(bar, parity)) return;
+    if ((it & 63u) == 0) {
+      if (*abort_flag) {
+        *live = false;
+        return;
+      }
+      if (global_timer_ns() - start > kWaitLimitNs) {
+        raise_error(err, DFLASH2_DEVERR_TIMEOUT);
+        *abort_flag = 1;
+        *live = false;
+        return;
+      }
     }
   }
-  const float r = l == 0.0f ? 0.0f : 1.0f / l;
+}
+
+__device__ __forceinline__ void tma_load_4d(void* dst, const CUtensorMap* map, int x, int y, int z, int w,
+                                            uint64_t* bar) {
+  asm volatile(
+      "cp.async.bulk.tensor.4d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
+      " [%0], [%1, {%2, %3, %4, %5}], [%6];" ::"r"(smem_addr(dst)),
+      "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(z), "r"(w), "r"(smem_addr(bar))
+      : "memory");
+}
+
+__device__ __forceinline__ void tma_load_5d(void* dst, const CUtensorMap* map, int x, int y, int z, int w, int v,
+                                            uint64_t* bar) {
+  asm volatile(
+      "cp.async.bulk.tensor.5d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
+      " [%0], [%1, {%2, %3, %4, %5, %6}], [%7];" ::"r"(smem_addr(dst)),
+      "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(z), "r"(w), "r"(v), "r"(smem_addr(bar))
+      : "memory");
+}
+
+// D[tmem] (+)= A[tmem] * B[smem]: A is 128 rows of 16 bf16 (8 columns), B is
+// 16 x N with N contiguous (MN-major).
+__device__ __forceinline__ void umma_bf16_ts(uint32_t tmem_d, uint32_t tmem_a, uint64_t bdesc, uint32_t idesc,
+                                             uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "setp.ne.b32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(tmem_d),
+      "r"(tmem_a), "l"(bdesc), "r"(idesc), "r"(accumulate)
+      : "memory");
+}
+
+// Descriptor of an MN-major operand with the 128-byte swizzle: 8 x 64 atoms of
+// 1024 bytes; leading offset = distance between 64-element column blocks, stride
+// offset = distance between groups of 8 rows (K).
+__device__ __forceinline__ uint64_t umma_desc_mn_sw128(uint32_t saddr, uint32_t block_bytes) {
+  uint64_t d = 0;
+  d |= static_cast<uint64_t>((saddr & 0x3FFFFu) >> 4);
+  d |= static_cast<uint64_t>(block_bytes >> 4) << 16;
+  d |= static_cast<uint64_t>(1024 >> 4) << 32;
+  d |= static_cast<uint64_t>(1) << 46;
+  d |= static_cast<uint64_t>(2) << 61;
+  return d;
+}
+
+__device__ __forceinline__ void tmem_st_x16(uint32_t taddr, const uint32_t (&r)[16]) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, "
+      "%15, %16};" ::"r"(taddr),
+      "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]),
+      "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
+      : "memory");
+}
+__device__ __forceinline__ void tmem_st_wait() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
+
+// Keeps uses of loaded values after the wait that precedes this in the program.
+__device__ __forceinline__ void pin(float (&v)[32]) {
 #pragma unroll
-  for (int e = 0; e < E; ++e)
-    a.out[row * D + lane * E + e] = __bfloat16_as_ushort(__float2bfloat16_rn(o[e] * r));
-  if (a.lse != nullptr && lane == 0) a.lse[row] = m + logf(l);
+  for (int i = 0; i < 32; i += 8)
+    asm volatile("" : "+f"(v[i]), "+f"(v[i + 1]), "+f"(v[i + 2]), "+f"(v[i + 3]), "+f"(v[i + 4]), "+f"(v[i + 5]),
+                 "+f"(v[i + 6]), "+f"(v[i + 7]));
+}
+
+__device__ __forceinline__ bool finite_bf16(uint32_t bits) { return (bits & 0x7F80u) != 0x7F80u; }
+
+// Zeroes the rows [from, 128) of a V tile (this thread's share of `threads`).
+template <int D>
+__device__ __forceinline__ void zero_rows(uint8_t* tile, int from, int tid, int threads) {
+  const int n = (kTile - from) * 8;   // 16-byte pieces per column block
+#pragma unroll
+  for (int half = 0; half < Cfg<D>::kHalves; ++half)
+    for (int x = tid; x < n; x += threads)
+      *reinterpret_cast<uint4*>(tile + half * kTile * 128 + from * 128 + x * 16) = make_uint4(0, 0, 0, 0);
+}
+
+// 227 KB, the opt-in limit of a block, is just enough at D = 128
+static_assert(Cfg<128>::kRing + sizeof(AttnSmem) <= 232448, "shared memory");
+
+template <int D>
+__global__ void __launch_bounds__(kThreads, 1)
+    tree_attn_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmK,
+                     const __grid_constant__ CUtensorMap tmV, const __grid_constant__ CUtensorMap tmKn,
+                     const __grid_constant__ CUtensorMap tmVn, const __grid_constant__ AttnPlan p) {
+  using C = Cfg<D>;
+  constexpr int S = C::kSlots;
+  extern __shared__ __align__(1024) uint8_t q_smem[];   // no static shared memory: the base is 1024-byte aligned
+  uint8_t* ring = q_smem + 2 * C::kTileBytes;
+  AttnSmem& s = *reinterpret_cast<AttnSmem*>(q_smem + C::kRing);
+  const AttnArgs& a = p.a;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  volatile int* abort_flag = &s.abort_flag;
+
+  if (threadIdx.x == 0) {
+    for (int i = 0; i < S; ++i) {
+      mbar_init(&s.kv_full[i], 1);
+      mbar_init(&s.kv_empty[i], 2);
+    }
+    mbar_init(&s.q_full, 1);
+    mbar_init(&s.q_empty, 2);
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(&s.s_full[i], 1);
+      mbar_init(&s.p_ready[i], kTile);
+      mbar_init(&s.pv_done[i], 1);
+    }
+    mbar_init(&s.drain, 2);
+    s.abort_flag = 0;
+    fence_mbar_init();
+    tma_prefetch_desc(&tmQ);
+    tma_prefetch_desc(&tmK);
+    tma_prefetch_desc(&tmV);
+    tma_prefetch_desc(&tmKn);
+    tma_prefetch_desc(&tmVn);
+  }
+  if (warp == 3) {
+    tmem_alloc(&s.tmem, 512);
+    tmem_relinquish();
+  }
+  pdl_wait();
+  pdl_launch_dependents();
+  tc_fence_before();
+  find_run<kThreads>(p, blockIdx.x, gridDim.x, 0, s.scan, &s.u0, &s.u1, &s.base, &s.b0);
+  tc_fence_after();
+  const uint32_t tmem = s.tmem;
+  Walk walk;
+  walk.start(p, s);
+  Segment g;
+  bool live = true;
+
+  if (warp == 0) {
+    // ---- producer ----
+    uint32_t it = 0;      // K and V tiles so far
+    uint32_t issued = 0;  // those whose copies were started
+    int seg = 0, q_issued = 0;
+    for (; walk.next(p, &g); ++seg) {
+      if (seg > 0) wait_live(&s.q_empty, (seg - 1) & 1, &live, abort_flag, a.err);
+      live = __all_sync(0xFFFFFFFFu, live);
+      if (live) q_issued = seg + 1;
+      if (lane == 0 && live) {
+        mbar_arrive_expect_tx(&s.q_full, g.tiles * p.q_box_bytes);
+        for (int i = 0; i < g.tiles; ++i)
+          for (int half = 0; half < C::kHalves; ++half)
+            tma_load_5d(q_smem + i * C::kTileBytes + half * kTile * 128, &tmQ, half * 64, 0,
+                        (2 * g.pair + i) * p.tpt, g.h, g.b, &s.q_full);
+      }
+      __syncwarp();
+      const int cached = (g.len + kTile - 1) / kTile;
+      // lane -> (page piece of the tile, column block)
+      const int half = lane % C::kHalves, piece = lane / C::kHalves;
+      const int row = piece * p.box_rows;       // first row of the lane's box
+      for (int u = g.s; u < g.e; ++u) {
+        const bool drafted = u >= cached && a.k_new != nullptr;
+        bool has;
+        int y = 0, z = g.h, w = g.b;
+        uint32_t bytes;
+        if (drafted) {
+          has = lane < C::kHalves;
+          bytes = kTile * 128;
+        } else {
+          const int j = u * kTile + row;
+          has = row < kTile && j < g.len;
+          bytes = p.box_rows * 128;
+          y = j;
+          if (has && a.cache.table != nullptr) {
+            bool ok;
+            w = kv_page(a.cache, g.b, j, a.err, &ok);
+            y = j & (a.cache.page_size - 1);
+          }
+        }
+        const uint32_t boxes = __popc(__ballot_sync(0xFFFFFFFFu, has));
+#pragma unroll
+        for (int kv = 0; kv < 2; ++kv, ++it) {
+          const int slot = it % S;
+          if (it >= S) wait_live(&s.kv_empty[slot], (it / S - 1) & 1, &live, abort_flag, a.err);
+          live = __all_sync(0xFFFFFFFFu, live);
+          if (!live) continue;
+          issued = it + 1;
+          if (lane == 0) mbar_arrive_expect_tx(&s.kv_full[slot], boxes * bytes);
+          __syncwarp();
+          if (has)
+            tma_load_4d(ring + slot * C::kTileBytes + half * kTile * 128 + (drafted ? 0 : row * 128),
+                        drafted ? (kv ? &tmVn : &tmKn) : (kv ? &tmV : &tmK), half * 64, y, z, w, &s.kv_full[slot]);
+        }
+      }
+    }
+    // after a wait that gave up: this CTA's copies have landed before it exits (else the products have used them)
+    if (lane == 0 && !live) {
+      if (q_issued > 0) mbar_wait_bounded(&s.q_full, (q_issued - 1) & 1, a.err);
+      for (uint32_t j = issued > S ? issued - S : 0; j < issued; ++j)
+        mbar_wait_bounded(&s.kv_full[j % S], (j / S) & 1, a.err);
+    }
+    __syncwarp();
+  } else if (warp <= 2) {
+    // ---- MMA issuer of pipeline i ----
+    const int i = warp - 1;
+    if (lane == 0) {
+      const uint32_t tm_s = tmem + i * kTile, tm_o = tmem + 2 * kTile + i * D;
+      const uint32_t idesc_s = umma_idesc_bf16(128, kTile);
+      const uint32_t idesc_o = umma_idesc_bf16(128, D) | (1u << 16);   // B is MN-major
+      uint32_t unit0 = 0;    // units of the segments so far
+      uint32_t n = 0;        // units of this pipeline so far
+      int seg = 0;
+      for (; walk.next(p, &g); ++seg) {
+        const int step = g.tiles == 2 ? 1 : 2, off = g.tiles == 2 ? 0 : i;
+        const int cnt = g.count(i);
+        wait_live(&s.q_full, seg & 1, &live, abort_flag, a.err);
+        if (cnt == 0) mbar_arrive(&s.q_empty);
+        const uint32_t q_base = smem_addr(q_smem + (g.tiles == 2 ? i : 0) * C::kTileBytes);
+        for (int j = 0; j < cnt; ++j, ++n) {
+          const uint32_t it = 2 * (unit0 + j * step + off);
+          const uint32_t ks = it % S, vs = (it + 1) % S;
+          wait_live(&s.kv_full[ks], (it / S) & 1, &live, abort_flag, a.err);
+          // P of the last unit lies in S's columns until its product is done
+          if (n > 0) wait_live(&s.pv_done[i], (n - 1) & 1, &live, abort_flag, a.err);
+          if (!live) continue;
+          tc_fence_after();
+          const uint32_t k_base = smem_addr(ring + ks * C::kTileBytes);
+#pragma unroll
+          for (int k = 0; k < D / 16; ++k) {
+            const uint32_t o = (k >> 2) * kTile * 128 + (k & 3) * 32;
+            umma_bf16(tm_s, umma_desc_sw128(q_base + o), umma_desc_sw128(k_base + o), idesc_s, k > 0 ? 1u : 0u);
+          }
+          umma_commit(&s.s_full[i]);
+          umma_commit(&s.kv_empty[ks]);
+          if (g.tiles == 1) umma_commit(&s.kv_empty[ks]);
+          if (j == cnt - 1) umma_commit(&s.q_empty);
+          wait_live(&s.p_ready[i], n & 1, &live, abort_flag, a.err);
+          wait_live(&s.kv_full[vs], ((it + 1) / S) & 1, &live, abort_flag, a.err);
+          if (!live) continue;
+          tc_fence_after();
+          const uint32_t v_base = smem_addr(ring + vs * C::kTileBytes);
+#pragma unroll
+          for (int k = 0; k < kTile / 16; ++k)
+            umma_bf16_ts(tm_o, tm_s + k * 8, umma_desc_mn_sw128(v_base + k * 2048, kTile * 128), idesc_o,
+                         (j > 0 || k > 0) ? 1u : 0u);
+          if (g.two_terms()) {
+#pragma unroll
+            for (int k = 0; k < kTile / 16; ++k)
+              umma_bf16_ts(tm_o, tm_s + 64 + k * 8, umma_desc_mn_sw128(v_base + k * 2048, kTile * 128), idesc_o, 1u);
+          }
+          umma_commit(&s.pv_done[i]);
+          umma_commit(&s.kv_empty[vs]);
+          if (g.tiles == 1) umma_commit(&s.kv_empty[vs]);
+        }
+        unit0 += g.count();
+      }
+      umma_commit(&s.drain);
+    }
+    __syncwarp();
+  } else if (warp >= 4) {
+    // ---- softmax of pipeline i, one row per thread ----
+    const int i = warp >= 8 ? 1 : 0;
+    const int r = threadIdx.x & (kTile - 1);
+    const uint32_t lanes = static_cast<uint32_t>((warp & 3) * 32) << 16;
+    const uint32_t tm_s = tmem + i * kTile + lanes, tm_o = tmem + 2 * kTile + lanes;
+    uint32_t unit0 = 0, n0 = 0, n1 = 0;   // units so far: all, pipeline 0's, pipeline 1's
+    const int t_r = r / a.group;
+    for (; walk.next(p, &g);) {
+      const int step = g.tiles == 2 ? 1 : 2, off = g.tiles == 2 ? 0 : i;
+      const int cnt = g.count(i);
+      const int node = (2 * g.pair + (g.tiles == 2 ? i : 0)) * p.tpt + t_r;
+      const bool row_ok = r < p.tpt * a.group && node < a.T;
+      const int cached = (g.len + kTile - 1) / kTile;
+      const bool two = g.two_terms();
+      uint32_t n = i ? n1 : n0;
+      float m = -INFINITY, l = 0.0f;
+      uint32_t vis[4] = {0, 0, 0, 0}, bad_seen = 0;   // the drafted tile's mask; whether a visible node is non-finite
+      for (int j = 0; j < cnt; ++j, ++n) {
+        const int u = g.s + j * step + off;
+        const bool drafted = u >= cached && a.k_new != nullptr;
+        const int valid = drafted ? a.T : min(kTile, g.len - u * kTile);
+        const bool partial_tile = drafted || valid < kTile;
+        if (partial_tile) {
+          // what the row sees of the tile, and a V tile without what nobody may see
+          const uint32_t it = 2 * (unit0 + j * step + off) + 1;
+          uint8_t* v_tile = ring + (it % S) * C::kTileBytes;
+          wait_live(&s.kv_full[it % S], (it / S) & 1, &live, abort_flag, a.err);
+          const int upto = drafted && a.mask == nullptr ? min(valid, node + 1) : valid;
+#pragma unroll
+          for (int w = 0; w < 4; ++w) {
+            const int k = upto - 32 * w;
+            vis[w] = k >= 32 ? 0xFFFFFFFFu : k <= 0 ? 0u : (1u << k) - 1u;
+          }
+          if (drafted) {
+            if (a.mask != nullptr) {
+              const int words = (a.T + 63) >> 6;
+              const uint64_t* mk = a.mask + (static_cast<int64_t>(g.b) * a.T + node) * words;
+              const uint64_t w0 = row_ok ? mk[0] : 0ull, w1 = row_ok && words > 1 ? mk[1] : 0ull;
+              vis[0] &= static_cast<uint32_t>(w0);
+              vis[1] &= static_cast<uint32_t>(w0 >> 32);
+              vis[2] &= static_cast<uint32_t>(w1);
+              vis[3] &= static_cast<uint32_t>(w1 >> 32);
+            }
+            // the pipelines that take the drafted tile look through it together
+            const int threads = g.tiles == 2 ? 2 * kTile : kTile;
+            const int tid = g.tiles == 2 ? static_cast<int>(threadIdx.x) - kTile : r;
+            const int bar = g.tiles == 2 ? 1 : 2 + i;
+            if (tid < 4) s.bad[tid] = 0;
+            named_bar_sync(bar, threads);
+#pragma unroll
+            for (int half = 0; half < C::kHalves; ++half)
+              for (int x = tid; x < a.T * 8; x += threads) {
+                uint4* at = reinterpret_cast<uint4*>(v_tile + half * kTile * 128 + x * 16);
+                uint4 q = *at;
+                uint32_t* e = &q.x;
+                bool hit = false;
+#pragma unroll
+                for (int y = 0; y < 4; ++y) {
+                  if (!finite_bf16(e[y])) e[y] &= 0xFFFF0000u, hit = true;
+                  if (!finite_bf16(e[y] >> 16)) e[y] &= 0x0000FFFFu, hit = true;
+                }
+                if (hit) {
+                  *at = q;
+                  atomicOr(&s.bad[x >> 8], 1u << ((x >> 3) & 31));
+                }
+              }
+            asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+            named_bar_sync(bar, threads);
+#pragma unroll
+            for (int w = 0; w < 4; ++w) bad_seen |= vis[w] & s.bad[w];
+          } else {
+            zero_rows<D>(v_tile, max(valid, 0), r, kTile);
+            asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+          }
+        }
+        wait_live(&s.s_full[i], n & 1, &live, abort_flag, a.err);
+        __syncwarp();
+        tc_fence_after();
+        float z[4][32];
+#pragma unroll
+        for (int x = 0; x < 4; ++x) tmem_ld_x32(tm_s + 32 * x, z[x]);
+        tmem_ld_wait();
+#pragma unroll
+        for (int x = 0; x < 4; ++x) pin(z[x]);
+        if (partial_tile) {
+#pragma unroll
+          for (int x = 0; x < 4; ++x)
+#pragma unroll
+            for (int y = 0; y < 32; ++y)
+              if (!(vis[x] >> y & 1u)) z[x][y] = -INFINITY;
+        }
+        float top = -INFINITY;
+#pragma unroll
+        for (int x = 0; x < 4; ++x)
+#pragma unroll
+          for (int y = 0; y < 32; y += 2) top = fmaxf(top, fmaxf(z[x][y], z[x][y + 1]));
+        top *= p.c;
+        if (j == 0) {
+          m = top;
+        } else if (__any_sync(0xFFFFFFFFu, top > m + kRescale)) {
+          // a row's maximum rose far: O and l move to the new one
+          const float m1 = fmaxf(m, top);
+          const float f = m == -INFINITY ? 1.0f : exp2_approx(m - m1);
+          m = m1;
+          l *= f;
+          wait_live(&s.pv_done[i], (n - 1) & 1, &live, abort_flag, a.err);
+          __syncwarp();
+          tc_fence_after();
+#pragma unroll 1
+          for (int x = 0; x < D; x += 32) {
+            float o[32];
+            tmem_ld_x32(tm_o + i * D + x, o);
+            tmem_ld_wait();
+            pin(o);
+#pragma unroll
+            for (int w = 0; w < 32; w += 16) {
+              uint32_t ob[16];
+#pragma unroll
+              for (int y = 0; y < 16; ++y) ob[y] = __float_as_uint(o[w + y] * f);
+              tmem_st_x16(tm_o + i * D + x + w, ob);
+            }
+          }
+        }
+        const float mm = m == -INFINITY ? 0.0f : m;   // a row that has seen nothing: all its P are 2^-inf
+        const uint64_t c2 = pack2(p.c, p.c), m2 = pack2(-mm, -mm);
+        uint64_t sum0 = pack2(0.0f, 0.0f), sum1 = sum0;
+#pragma unroll
+        for (int x = 0; x < 4; ++x) {
+          uint32_t hi[16], lo[16];
+#pragma unroll
+          for (int y = 0; y < 32; y += 4) {
+            const float2 e0 = unpack2(fma2(pack2(z[x][y], z[x][y + 1]), c2, m2));
+            const float2 e1 = unpack2(fma2(pack2(z[x][y + 2], z[x][y + 3]), c2, m2));
+            const uint64_t p0 = pack2(exp2_approx(e0.x), exp2_approx(e0.y));
+            const uint64_t p1 = pack2(exp2_approx(e1.x), exp2_approx(e1.y));
+            sum0 = add2(sum0, p0);
+            sum1 = add2(sum1, p1);
+            hi[y / 2] = pack_bf16(unpack2(p0).x, unpack2(p0).y);
+            hi[y / 2 + 1] = pack_bf16(unpack2(p1).x, unpack2(p1).y);
+            if (two) {
+              lo[y / 2] = remainder_bf16(p0, hi[y / 2]);
+              lo[y / 2 + 1] = remainder_bf16(p1, hi[y / 2 + 1]);
+            }
+          }
+          tmem_st_x16(tm_s + 16 * x, hi);
+          if (two) tmem_st_x16(tm_s + 64 + 16 * x, lo);
+        }
+        const float2 sum = unpack2(add2(sum0, sum1));
+        l += sum.x + sum.y;
+        tmem_st_wait();
+        tc_fence_before();
+        mbar_arrive(&s.p_ready[i]);
+      }
+      unit0 += g.count();
+      n0 += g.count(0);
+      n1 += g.count(1);
+
+      // ---- the item's (or the run's part of the item's) sums ----
+      const bool whole = g.s == 0 && g.e == g.n;
+      const int slot = 2 * blockIdx.x + (g.first ? 0 : 1);
+      const bool merge = g.tiles == 1;
+      float f0 = 1.0f, f1 = 0.0f;     // weights of O0 and O1 (one tile), or of O_i
+      if (merge) {
+        s.ml[i][r] = make_float2(m, l);
+        if (n0 > 0) wait_live(&s.pv_done[0], (n0 - 1) & 1, &live, abort_flag, a.err);
+        if (g.count(1) > 0) wait_live(&s.pv_done[1], (n1 - 1) & 1, &live, abort_flag, a.err);
+        named_bar_sync(1, 2 * kTile);
+        const float2 x0 = s.ml[0][r], x1 = s.ml[1][r];
+        m = fmaxf(x0.x, x1.x);
+        f0 = x0.x == -INFINITY ? 0.0f : exp2_approx(x0.x - m);
+        f1 = x1.x == -INFINITY ? 0.0f : exp2_approx(x1.x - m);
+        l = x0.y * f0 + x1.y * f1;
+        // a row that only saw NaN scores has no maximum and a NaN sum
+        if (x0.y != x0.y || x1.y != x1.y) l = f0 = NAN;
+        if (g.count(1) == 0) f1 = 0.0f;
+      } else {
+        wait_live(&s.pv_done[i], ((i ? n1 : n0) - 1) & 1, &live, abort_flag, a.err);
+      }
+      __syncwarp();
+      tc_fence_after();
+      const bool empty = l == 0.0f;   // the row saw nothing: 0, whatever the values were
+      const float inv = whole ? (l == 0.0f ? 0.0f : 1.0f / l) : 1.0f;
+      f0 *= inv;
+      f1 *= inv;
+      const int c0 = merge ? i * (D / 2) : 0, c1 = merge ? c0 + D / 2 : D;
+      const int64_t orow = (static_cast<int64_t>(g.b) * a.T + node) * a.heads + g.h * a.group + r % a.group;
+      const int area = merge ? 0 : i;
+      if (!merge || i == 0) {
+        if (whole) {
+          if (row_ok && a.lse != nullptr)
+            a.lse[orow] = l == 0.0f ? -INFINITY : (m + log2f(l)) * 0.69314718055994531f;
+        } else {
+          p.part_ml[(static_cast<int64_t>(slot) * p.areas + area) * kTile + r] = make_float2(m, l);
+        }
+      }
+      // with one tile only the pipeline that took the drafted tile knows what its rows saw there
+      bool fix = bad_seen != 0;
+      if (merge) fix = a.k_new != nullptr && g.e == g.n && (s.bad[0] | s.bad[1] | s.bad[2] | s.bad[3]) != 0;
+#pragma unroll 1
+      for (int x = c0; x < c1; x += 32) {
+        float o[32];
+        tmem_ld_x32(tm_o + (merge ? 0 : i * D) + x, o);
+        tmem_ld_wait();
+        pin(o);
+#pragma unroll
+        for (int y = 0; y < 32; ++y) o[y] *= f0;
+        if (merge && g.count(1) > 0) {
+          float o1[32];
+          tmem_ld_x32(tm_o + D + x, o1);
+          tmem_ld_wait();
+          pin(o1);
+#pragma unroll
+          for (int y = 0; y < 32; ++y) o[y] = fmaf(o1[y], f1, o[y]);
+        }
+        if (empty) {
+#pragma unroll
+          for (int y = 0; y < 32; ++y) o[y] = 0.0f;
+        }
+        if (fix && row_ok) {
+#pragma unroll 1
+          for (int sn = 0; sn < a.T; ++sn) {
+            if (!(s.bad[sn >> 5] >> (sn & 31) & 1u)) continue;
+            const bool sees = a.mask == nullptr
+                                  ? sn <= node
+                                  : a.mask[(static_cast<int64_t>(g.b) * a.T + node) * ((a.T + 63) >> 6) + (sn >> 6)] >>
+                                            (sn & 63) & 1;
+            if (!sees) continue;
+            const uint16_t* vn = a.v_new + g.b * a.new_b + sn * a.new_t + g.h * a.new_h + x;
+#pragma unroll
+            for (int y = 0; y < 32; ++y)
+              if (!finite_bf16(vn[y])) o[y] += bf16_bits_to_float(vn[y]);
+          }
+        }
+        if (whole) {
+          if (row_ok) {
+            uint4* dst = reinterpret_cast<uint4*>(a.out + orow * D + x);
+#pragma unroll
+            for (int y = 0; y < 32; y += 8)
+              dst[y / 8] = make_uint4(pack_bf16(o[y], o[y + 1]), pack_bf16(o[y + 2], o[y + 3]),
+                                      pack_bf16(o[y + 4], o[y + 5]), pack_bf16(o[y + 6], o[y + 7]));
+          }
+        } else {
+          float4* dst = reinterpret_cast<float4*>(p.part) +
+                        ((static_cast<int64_t>(slot) * p.areas + area) * (D / 4) + x / 4) * kTile + r;
+#pragma unroll
+          for (int y = 0; y < 32; y += 4) dst[(y / 4) * kTile] = make_float4(o[y], o[y + 1], o[y + 2], o[y + 3]);
+        }
+      }
+      tc_fence_before();
+      // O and the shared statistics may be overwritten once both pipelines have read them
+      named_bar_sync(1, 2 * kTile);
+    }
+  }
+
+  __syncthreads();
+  if (threadIdx.x == 0) mbar_wait_bounded(&s.drain, 0, a.err);   // the tensor cores have finished
+  __syncthreads();
+  if (warp == 3) {
+    tc_fence_after();
+    tmem_dealloc(tmem, 512);
+  }
+}
+
+// Adds the parts of the items that runs cut.  CTA (c, y): if the boundary
+// between runs c and c + 1 is the first inside an item, that item's row tile y /
+// (D / 16), columns 16 (y % (D / 16)) on; one row per thread.
+template <int D>
+__global__ void __launch_bounds__(kTile) tree_attn_join_kernel(const __grid_constant__ AttnPlan p, int runs) {
+  __shared__ int64_t scan[kTile / 32];
+  __shared__ int64_t s_u0, s_u1, s_base;
+  __shared__ int32_t s_b;
+  const AttnArgs& a = p.a;
+  pdl_wait();
+  pdl_launch_dependents();
+  if (threadIdx.x == 0) s_b = -1;
+  __syncthreads();
+  find_run<kTile>(p, blockIdx.x, runs, 1, scan, &s_u0, &s_u1, &s_base, &s_b);
+  const int64_t u0 = s_u0, u1 = s_u1, len = u1 - u0;
+  if (s_b < 0 || len == 0) return;         // the last run ends everything
+  const int32_t b = s_b;
+  const int64_t n = units_of(a, b);
+  const int64_t item = (u1 - s_base) / n;
+  const int64_t start = s_base + item * n, end = start + n;
+  if (start == u1 || start < u0) return;   // cut at its start, or an earlier boundary's
+  const int pair = static_cast<int>(item % p.pairs), h = static_cast<int>(item / p.pairs);
+  const int tile = blockIdx.y / (D / 16), x = blockIdx.y % (D / 16) * 16;
+  if (2 * pair + tile >= p.row_tiles) return;
+  const int r = threadIdx.x;
+  const int node = (2 * pair + tile) * p.tpt + r / a.group;
+  if (r >= p.tpt * a.group || node >= a.T) return;
+  const int64_t c0 = blockIdx.x, c1 = (end - 1) / len;   // the runs that hold parts
+  const auto part_of = [&](int64_t c) { return 2 * c + (c == c0 && start != u0 ? 1 : 0); };
+  float m = -INFINITY;
+  bool nan = false;
+  for (int64_t c = c0; c <= c1; ++c) {
+    const float2 ml = p.part_ml[(part_of(c) * p.areas + tile) * kTile + r];
+    m = fmaxf(m, ml.x);
+    nan |= ml.y != ml.y;
+  }
+  float l = 0.0f, o[16];
+#pragma unroll
+  for (int y = 0; y < 16; ++y) o[y] = 0.0f;
+  for (int64_t c = c0; c <= c1; ++c) {
+    const int64_t at = part_of(c) * p.areas + tile;
+    const float2 ml = p.part_ml[at * kTile + r];
+    const float f = ml.x == -INFINITY ? 0.0f : exp2_approx(ml.x - m);
+    l += ml.y * f;
+    if (ml.x == -INFINITY) continue;       // it saw nothing (its sums are 0)
+    const float4* src = reinterpret_cast<const float4*>(p.part) + (at * (D / 4) + x / 4) * kTile + r;
+#pragma unroll
+    for (int y = 0; y < 16; y += 4) {
+      const float4 v = src[(y / 4) * kTile];
+      o[y] = fmaf(v.x, f, o[y]);
+      o[y + 1] = fmaf(v.y, f, o[y + 1]);
+      o[y + 2] = fmaf(v.z, f, o[y + 2]);
+      o[y + 3] = fmaf(v.w, f, o[y + 3]);
+    }
+  }
+  if (nan) l = NAN;
+  const float inv = l == 0.0f ? 0.0f : 1.0f / l;
+  const int64_t orow = (static_cast<int64_t>(b) * a.T + node) * a.heads + h * a.group + r % a.group;
+  uint4* dst = reinterpret_cast<uint4*>(a.out + orow * D + x);
+#pragma unroll
+  for (int y = 0; y < 16; y += 8)
+    dst[y / 8] = make_uint4(pack_bf16(o[y] * inv, o[y + 1] * inv), pack_bf16(o[y + 2] * inv, o[y + 3] * inv),
+                            pack_bf16(o[y + 4] * inv, o[y + 5] * inv), pack_bf16(o[y + 6] * inv, o[y + 7] * inv));
+  if (x == 0 && a.lse != nullptr) a.lse[orow] = l == 0.0f ? -INFINITY : (m + log2f(l)) * 0.69314718055994531f;
+}
+
+struct Tiling {
+  int32_t tpt, row_tiles, pairs, areas;
+};
+
+Tiling tile_rows(int64_t T, int64_t group) {
+  Tiling t;
+  t.tpt = static_cast<int32_t>(kTile / group);
+  t.row_tiles = static_cast<int32_t>((T + t.tpt - 1) / t.tpt);
+  t.pairs = (t.row_tiles + 1) / 2;
+  t.areas = t.row_tiles > 1 ? 2 : 1;
+  return t;
+}
+
+template <int D>
+cudaError_t launch(const AttnArgs& a, void* workspace, int num_sms, cudaStream_t stream) {
+  using C = Cfg<D>;
+  const Tiling t = tile_rows(a.T, a.group);
+  AttnPlan p;
+  p.a = a;
+  p.tpt = t.tpt;
+  p.row_tiles = t.row_tiles;
+  p.pairs = t.pairs;
+  p.areas = t.areas;
+  p.c = a.scale * 1.4426950408889634f;
+  const KvView& c = a.cache;
+  const bool paged = c.table != nullptr;
+  p.box_rows = paged && c.page_size < kTile ? c.page_size : kTile;
+  p.q_box_bytes = static_cast<uint32_t>(t.tpt * a.group) * D * 2;
+  const int64_t most = a.B * c.heads * t.pairs * ((static_cast<int64_t>(c.capacity) + kTile - 1) / kTile + 1);
+  const int runs = static_cast<int>(imin64(num_sms, imax64(most, 1)));
+  p.part = static_cast<float*>(workspace);
+  p.part_ml = reinterpret_cast<float2*>(p.part + static_cast<size_t>(2) * num_sms * t.areas * kTile * D);
+
+  CUtensorMap tmQ, tmK, tmV, tmKn, tmVn;
+  const uint64_t qd[5] = {D, static_cast<uint64_t>(a.group), static_cast<uint64_t>(a.T),
+                          static_cast<uint64_t>(c.heads), static_cast<uint64_t>(a.B)};
+  const uint64_t qs[4] = {static_cast<uint64_t>(a.q_h), static_cast<uint64_t>(a.q_t),
+                          static_cast<uint64_t>(a.q_h) * a.group, static_cast<uint64_t>(a.q_b)};
+  const uint32_t qb[5] = {64, static_cast<uint32_t>(a.group), static_cast<uint32_t>(t.tpt), 1, 1};
+  if (!make_tmap_bf16_nd(&tmQ, a.q, 5, qd, qs, qb)) return cudaErrorInvalidValue;
+  const uint64_t kd[4] = {D, static_cast<uint64_t>(imax64(c.page_size, 1)), static_cast<uint64_t>(c.heads),
+                          static_cast<uint64_t>(imax64(c.num_pages, 1))};
+  const uint64_t ks[3] = {static_cast<uint64_t>(c.token_stride), static_cast<uint64_t>(c.head_stride),
+                          static_cast<uint64_t>(c.page_stride)};
+  const uint32_t kb[4] = {64, static_cast<uint32_t>(p.box_rows), 1, 1};
+  // an empty cache has no memory to describe: any valid address will do, nothing is read
+  const void* k = c.capacity > 0 ? c.k : a.q;
+  const void* v = c.capacity > 0 ? c.v : a.q;
+  if (!make_tmap_bf16_nd(&tmK, k, 4, kd, ks, kb) || !make_tmap_bf16_nd(&tmV, v, 4, kd, ks, kb))
+    return cudaErrorInvalidValue;
+  tmKn = tmK;
+  tmVn = tmV;
+  if (a.k_new != nullptr) {
+    const uint64_t nd[4] = {D, static_cast<uint64_t>(a.T), static_cast<uint64_t>(c.heads), static_cast<uint64_t>(a.B)};
+    const uint64_t ns[3] = {static_cast<uint64_t>(a.new_t), static_cast<uint64_t>(a.new_h),
+                            static_cast<uint64_t>(a.new_b)};
+    const uint32_t nb[4] = {64, kTile, 1, 1};
+    if (!make_tmap_bf16_nd(&tmKn, a.k_new, 4, nd, ns, nb) || !make_tmap_bf16_nd(&tmVn, a.v_new, 4, nd, ns, nb))
+      return cudaErrorInvalidValue;
+  }
+
+  const size_t smem = C::kRing + sizeof(AttnSmem);
+  cudaError_t e = set_smem_limit<tree_attn_kernel<D>>(smem);
+  if (e != cudaSuccess) return e;
+  cudaLaunchAttribute attr = pdl_attribute();
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(runs, 1, 1);
+  cfg.blockDim = dim3(kThreads, 1, 1);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = stream;
+  cfg.attrs = &attr;
+  cfg.numAttrs = 1;
+  e = cudaLaunchKernelEx(&cfg, tree_attn_kernel<D>, tmQ, tmK, tmV, tmKn, tmVn, p);
+  if (e != cudaSuccess || runs == 1) return e;
+  cfg.gridDim = dim3(runs - 1, t.areas * (D / 16), 1);
+  cfg.blockDim = dim3(kTile, 1, 1);
+  cfg.dynamicSmemBytes = 0;
+  return cudaLaunchKernelEx(&cfg, tree_attn_join_kernel<D>, p, runs);
 }
 
 }  // namespace
 
-size_t tree_attn_workspace_bytes(int64_t, int64_t, int64_t, int64_t, int64_t, int) { return 0; }
+size_t tree_attn_workspace_bytes(int64_t, int64_t T, int64_t heads, int64_t kv_heads, int64_t head_dim, int num_sms) {
+  const int64_t group = heads / kv_heads;
+  if (group > kTile) return 0;
+  return static_cast<size_t>(2) * num_sms * tile_rows(T, group).areas * kTile * (head_dim * 4 + 8);
+}
 
-cudaError_t launch_tree_attn(const AttnArgs& a, int64_t head_dim, void*, int, cudaStream_t stream) {
-  const int64_t blocks = (a.B * a.T * a.heads + 7) / 8;
-  if (head_dim == 64)
-    tree_attn_kernel<64><<<static_cast<unsigned>(blocks), 256, 0, stream>>>(a);
-  else
-    tree_attn_kernel<128><<<static_cast<unsigned>(blocks), 256, 0, stream>>>(a);
-  return cudaGetLastError();
+cudaError_t launch_tree_attn(const AttnArgs& a, int64_t head_dim, void* workspace, int num_sms, cudaStream_t stream) {
+  return head_dim == 64 ? launch<64>(a, workspace, num_sms, stream) : launch<128>(a, workspace, num_sms, stream);
 }
 
 }  // namespace dflash2

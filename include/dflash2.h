@@ -463,7 +463,7 @@ typedef struct dflash2_kv_cache {
  *                 the queries then attend to the cache alone
  *   tree_mask     device uint64 [B, T, (T + 63) / 64], bit s % 64 of word s / 64
  *                 of node t: t sees s; or NULL: a chain (t sees every s <= t)
- *   scale         finite and > 0
+ *   scale         > 0 and at most 1e38
  *   out           device bf16 [B, T, heads, head_dim], contiguous
  *   lse           device fp32 [B, T, heads] or NULL
  *   workspace     device scratch of at least dflash2_tree_attention_workspace()

@@ -231,7 +231,8 @@ def test_scores_at_the_lowest_value_and_large_scores(handle):
     rows[0][0][77] = 100.0
     write_rows(cache, 0, 0, *rows[0])
     out, lse = api.tree_attention(handle, q, cache, cl, scale=1.0)
-    assert torch.equal(out[0, 0, 0], rows[0][1][77, 0]) and (lse == 6400.0).all()
+    v = rows[0][1][77, 0].float()
+    assert ((out[0, 0] - v).abs() <= 2.0 ** -8 * v.abs()).all() and ((lse - 6400.0).abs() <= 6401e-6).all()
     # a maximum that keeps rising along the axis rescales the sums again and again
     rows[0][0][:] = (torch.arange(150, device="cuda") * 0.5)[:, None, None].to(torch.bfloat16)
     write_rows(cache, 0, 0, *rows[0])
