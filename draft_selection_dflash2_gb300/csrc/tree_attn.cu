@@ -49,6 +49,10 @@ namespace {
 constexpr int kTile = 128;              // rows of a query tile, keys of a unit
 constexpr int kThreads = 384;
 constexpr int kMaxSlots = 10;
+// The block is launched with 168 registers a thread; warps 0-3 give some to the
+// softmax warps: 128 x 72 + 256 x 216 = 384 x 168.
+constexpr int kLaunchRegs = 168, kLowRegs = 72, kHighRegs = 216;
+static_assert(128 * kLowRegs + 256 * kHighRegs <= kThreads * kLaunchRegs, "register split");
 constexpr int kMinRun = 1;              // least units per CTA
 constexpr int kTwoTermUnits = 8;        // items of up to so many units carry P in two terms
 constexpr float kRescale = 8.0f;        // log2 of how far P may exceed 1
@@ -62,7 +66,7 @@ struct Cfg {
 };
 
 struct AttnSmem {
-  uint64_t kv_full[kMaxSlots], kv_empty[kMaxSlots];
+  uint64_t kv_full[2 * kMaxSlots], kv_empty[kMaxSlots];
   uint64_t q_full, q_empty;
   uint64_t s_full[2], p_ready[2], pv_done[2], drain;
   float2 ml[2][kTile];
@@ -120,11 +124,10 @@ __device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
   return d;
 }
 
-// The bf16 pair of what a pair of fp32 values lost when it was rounded to `hi`.
-__device__ __forceinline__ uint32_t remainder_bf16(uint64_t p, uint32_t hi) {
-  const uint64_t back = pack2(__uint_as_float(hi << 16), __uint_as_float(hi & 0xFFFF0000u));
-  const float2 r = unpack2(fma2(back, pack2(-1.0f, -1.0f), p));
-  return pack_bf16(r.x, r.y);
+// The bf16 pair of what two fp32 values lose when they are rounded to bf16.
+__device__ __forceinline__ uint32_t remainder_bf16(float x, float y) {
+  const uint32_t hi = pack_bf16(x, y);
+  return pack_bf16(x - __uint_as_float(hi << 16), y - __uint_as_float(hi & 0xFFFF0000u));
 }
 
 // Key tiles of sequence b, the drafted one included (at least one, so that every row is written).
@@ -238,16 +241,17 @@ struct Walk {
 // has given up (*live = false) later waits return at once.
 __device__ __forceinline__ void wait_live(uint64_t* bar, uint32_t parity, bool* live, volatile int* abort_flag,
                                           uint32_t* err) {
-  if (!*live || mbar_try_wait(bar, parity)) return;
-  const uint64_t start = global_timer_ns();
-  for (uint32_t it = 1;; ++it) {
-    if (mbar_try_wait(bar, parity)) return;
-    if ((it & 63u) == 0) {
+  if (!*live) return;
+  uint64_t start = 0;
+  for (uint32_t it = 1; !mbar_try_wait(bar, parity); ++it) {
+    if ((it & 255u) == 0) {   // rarely: reading the timer takes longer than most of these waits
       if (*abort_flag) {
         *live = false;
         return;
       }
-      if (global_timer_ns() - start > kWaitLimitNs) {
+      const uint64_t now = global_timer_ns();
+      if (start == 0) start = now;
+      if (now - start > kWaitLimitNs) {
         raise_error(err, DFLASH2_DEVERR_TIMEOUT);
         *abort_flag = 1;
         *live = false;
@@ -255,6 +259,22 @@ __device__ __forceinline__ void wait_live(uint64_t* bar, uint32_t parity, bool* 
       }
     }
   }
+}
+
+// The barrier on which tile `it` of the ring lands, and its parity.  A parity
+// wait can only tell a phase from the one before it, and the pipelines do not
+// look at every tile when they share a row tile.  So a slot's uses alternate
+// between two barriers: when a pipeline asks for a slot's use k the producer has
+// issued use k - 1 (it issues in order, and the pipeline has seen a later tile or
+// the item's queries), for which use k - 2 had landed and been used, and use k
+// cannot be passed by without this pipeline.
+template <int S>
+__device__ __forceinline__ uint64_t* tile_bar(uint64_t* kv_full, uint32_t it) {
+  return &kv_full[(it % S) * 2 + (it / S & 1)];
+}
+template <int S>
+__device__ __forceinline__ uint32_t tile_parity(uint32_t it) {
+  return it / S >> 1 & 1;
 }
 
 __device__ __forceinline__ void tma_load_4d(void* dst, const CUtensorMap* map, int x, int y, int z, int w,
@@ -349,7 +369,8 @@ __global__ void __launch_bounds__(kThreads, 1)
 
   if (threadIdx.x == 0) {
     for (int i = 0; i < S; ++i) {
-      mbar_init(&s.kv_full[i], 1);
+      mbar_init(&s.kv_full[2 * i], 1);
+      mbar_init(&s.kv_full[2 * i + 1], 1);
       mbar_init(&s.kv_empty[i], 2);
     }
     mbar_init(&s.q_full, 1);
@@ -383,6 +404,11 @@ __global__ void __launch_bounds__(kThreads, 1)
   Segment g;
   bool live = true;
 
+  // the softmax warps take the registers that the others leave
+  if (warp < 4)
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kLowRegs));
+  else
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kHighRegs));
   if (warp == 0) {
     // ---- producer ----
     uint32_t it = 0;      // K and V tiles so far
@@ -431,11 +457,12 @@ __global__ void __launch_bounds__(kThreads, 1)
           live = __all_sync(0xFFFFFFFFu, live);
           if (!live) continue;
           issued = it + 1;
-          if (lane == 0) mbar_arrive_expect_tx(&s.kv_full[slot], boxes * bytes);
+          uint64_t* full = tile_bar<S>(s.kv_full, it);
+          if (lane == 0) mbar_arrive_expect_tx(full, boxes * bytes);
           __syncwarp();
           if (has)
             tma_load_4d(ring + slot * C::kTileBytes + half * kTile * 128 + (drafted ? 0 : row * 128),
-                        drafted ? (kv ? &tmVn : &tmKn) : (kv ? &tmV : &tmK), half * 64, y, z, w, &s.kv_full[slot]);
+                        drafted ? (kv ? &tmVn : &tmKn) : (kv ? &tmV : &tmK), half * 64, y, z, w, full);
         }
       }
     }
@@ -443,7 +470,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (lane == 0 && !live) {
       if (q_issued > 0) mbar_wait_bounded(&s.q_full, (q_issued - 1) & 1, a.err);
       for (uint32_t j = issued > S ? issued - S : 0; j < issued; ++j)
-        mbar_wait_bounded(&s.kv_full[j % S], (j / S) & 1, a.err);
+        mbar_wait_bounded(tile_bar<S>(s.kv_full, j), tile_parity<S>(j), a.err);
     }
     __syncwarp();
   } else if (warp <= 2) {
@@ -465,7 +492,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         for (int j = 0; j < cnt; ++j, ++n) {
           const uint32_t it = 2 * (unit0 + j * step + off);
           const uint32_t ks = it % S, vs = (it + 1) % S;
-          wait_live(&s.kv_full[ks], (it / S) & 1, &live, abort_flag, a.err);
+          wait_live(tile_bar<S>(s.kv_full, it), tile_parity<S>(it), &live, abort_flag, a.err);
           // P of the last unit lies in S's columns until its product is done
           if (n > 0) wait_live(&s.pv_done[i], (n - 1) & 1, &live, abort_flag, a.err);
           if (!live) continue;
@@ -481,7 +508,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           if (g.tiles == 1) umma_commit(&s.kv_empty[ks]);
           if (j == cnt - 1) umma_commit(&s.q_empty);
           wait_live(&s.p_ready[i], n & 1, &live, abort_flag, a.err);
-          wait_live(&s.kv_full[vs], ((it + 1) / S) & 1, &live, abort_flag, a.err);
+          wait_live(tile_bar<S>(s.kv_full, it + 1), tile_parity<S>(it + 1), &live, abort_flag, a.err);
           if (!live) continue;
           tc_fence_after();
           const uint32_t v_base = smem_addr(ring + vs * C::kTileBytes);
@@ -509,7 +536,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int r = threadIdx.x & (kTile - 1);
     const uint32_t lanes = static_cast<uint32_t>((warp & 3) * 32) << 16;
     const uint32_t tm_s = tmem + i * kTile + lanes, tm_o = tmem + 2 * kTile + lanes;
-    uint32_t unit0 = 0, n0 = 0, n1 = 0;   // units so far: all, pipeline 0's, pipeline 1's
+    uint32_t unit0 = 0, n = 0;   // units so far: all, this pipeline's
     const int t_r = r / a.group;
     for (; walk.next(p, &g);) {
       const int step = g.tiles == 2 ? 1 : 2, off = g.tiles == 2 ? 0 : i;
@@ -518,7 +545,6 @@ __global__ void __launch_bounds__(kThreads, 1)
       const bool row_ok = r < p.tpt * a.group && node < a.T;
       const int cached = (g.len + kTile - 1) / kTile;
       const bool two = g.two_terms();
-      uint32_t n = i ? n1 : n0;
       float m = -INFINITY, l = 0.0f;
       uint32_t vis[4] = {0, 0, 0, 0}, bad_seen = 0;   // the drafted tile's mask; whether a visible node is non-finite
       for (int j = 0; j < cnt; ++j, ++n) {
@@ -526,11 +552,12 @@ __global__ void __launch_bounds__(kThreads, 1)
         const bool drafted = u >= cached && a.k_new != nullptr;
         const int valid = drafted ? a.T : min(kTile, g.len - u * kTile);
         const bool partial_tile = drafted || valid < kTile;
+        wait_live(&s.s_full[i], n & 1, &live, abort_flag, a.err);
         if (partial_tile) {
           // what the row sees of the tile, and a V tile without what nobody may see
           const uint32_t it = 2 * (unit0 + j * step + off) + 1;
           uint8_t* v_tile = ring + (it % S) * C::kTileBytes;
-          wait_live(&s.kv_full[it % S], (it / S) & 1, &live, abort_flag, a.err);
+          wait_live(tile_bar<S>(s.kv_full, it), tile_parity<S>(it), &live, abort_flag, a.err);
           const int upto = drafted && a.mask == nullptr ? min(valid, node + 1) : valid;
 #pragma unroll
           for (int w = 0; w < 4; ++w) {
@@ -552,6 +579,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             const int tid = g.tiles == 2 ? static_cast<int>(threadIdx.x) - kTile : r;
             const int bar = g.tiles == 2 ? 1 : 2 + i;
             if (tid < 4) s.bad[tid] = 0;
+            __syncwarp();
             named_bar_sync(bar, threads);
 #pragma unroll
             for (int half = 0; half < C::kHalves; ++half)
@@ -570,6 +598,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                   atomicOr(&s.bad[x >> 8], 1u << ((x >> 3) & 31));
                 }
               }
+            __syncwarp();
             asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
             named_bar_sync(bar, threads);
 #pragma unroll
@@ -579,7 +608,6 @@ __global__ void __launch_bounds__(kThreads, 1)
             asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
           }
         }
-        wait_live(&s.s_full[i], n & 1, &live, abort_flag, a.err);
         __syncwarp();
         tc_fence_after();
         float z[4][32];
@@ -632,24 +660,30 @@ __global__ void __launch_bounds__(kThreads, 1)
         uint64_t sum0 = pack2(0.0f, 0.0f), sum1 = sum0;
 #pragma unroll
         for (int x = 0; x < 4; ++x) {
-          uint32_t hi[16], lo[16];
+          uint32_t hi[16];
 #pragma unroll
           for (int y = 0; y < 32; y += 4) {
             const float2 e0 = unpack2(fma2(pack2(z[x][y], z[x][y + 1]), c2, m2));
             const float2 e1 = unpack2(fma2(pack2(z[x][y + 2], z[x][y + 3]), c2, m2));
-            const uint64_t p0 = pack2(exp2_approx(e0.x), exp2_approx(e0.y));
-            const uint64_t p1 = pack2(exp2_approx(e1.x), exp2_approx(e1.y));
-            sum0 = add2(sum0, p0);
-            sum1 = add2(sum1, p1);
-            hi[y / 2] = pack_bf16(unpack2(p0).x, unpack2(p0).y);
-            hi[y / 2 + 1] = pack_bf16(unpack2(p1).x, unpack2(p1).y);
-            if (two) {
-              lo[y / 2] = remainder_bf16(p0, hi[y / 2]);
-              lo[y / 2 + 1] = remainder_bf16(p1, hi[y / 2 + 1]);
-            }
+            z[x][y] = exp2_approx(e0.x);
+            z[x][y + 1] = exp2_approx(e0.y);
+            z[x][y + 2] = exp2_approx(e1.x);
+            z[x][y + 3] = exp2_approx(e1.y);
+            sum0 = add2(sum0, pack2(z[x][y], z[x][y + 1]));
+            sum1 = add2(sum1, pack2(z[x][y + 2], z[x][y + 3]));
+            hi[y / 2] = pack_bf16(z[x][y], z[x][y + 1]);
+            hi[y / 2 + 1] = pack_bf16(z[x][y + 2], z[x][y + 3]);
           }
           tmem_st_x16(tm_s + 16 * x, hi);
-          if (two) tmem_st_x16(tm_s + 64 + 16 * x, lo);
+        }
+        if (two) {
+#pragma unroll
+          for (int x = 0; x < 4; ++x) {
+            uint32_t lo[16];
+#pragma unroll
+            for (int y = 0; y < 32; y += 2) lo[y / 2] = remainder_bf16(z[x][y], z[x][y + 1]);
+            tmem_st_x16(tm_s + 64 + 16 * x, lo);
+          }
         }
         const float2 sum = unpack2(add2(sum0, sum1));
         l += sum.x + sum.y;
@@ -658,18 +692,18 @@ __global__ void __launch_bounds__(kThreads, 1)
         mbar_arrive(&s.p_ready[i]);
       }
       unit0 += g.count();
-      n0 += g.count(0);
-      n1 += g.count(1);
 
       // ---- the item's (or the run's part of the item's) sums ----
       const bool whole = g.s == 0 && g.e == g.n;
       const int slot = 2 * blockIdx.x + (g.first ? 0 : 1);
       const bool merge = g.tiles == 1;
       float f0 = 1.0f, f1 = 0.0f;     // weights of O0 and O1 (one tile), or of O_i
+      if (cnt > 0) wait_live(&s.pv_done[i], (n - 1) & 1, &live, abort_flag, a.err);
+      __syncwarp();
       if (merge) {
+        // each pipeline has waited for its own products
         s.ml[i][r] = make_float2(m, l);
-        if (n0 > 0) wait_live(&s.pv_done[0], (n0 - 1) & 1, &live, abort_flag, a.err);
-        if (g.count(1) > 0) wait_live(&s.pv_done[1], (n1 - 1) & 1, &live, abort_flag, a.err);
+        tc_fence_before();
         named_bar_sync(1, 2 * kTile);
         const float2 x0 = s.ml[0][r], x1 = s.ml[1][r];
         m = fmaxf(x0.x, x1.x);
@@ -679,10 +713,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         // a row that only saw NaN scores has no maximum and a NaN sum
         if (x0.y != x0.y || x1.y != x1.y) l = f0 = NAN;
         if (g.count(1) == 0) f1 = 0.0f;
-      } else {
-        wait_live(&s.pv_done[i], ((i ? n1 : n0) - 1) & 1, &live, abort_flag, a.err);
       }
-      __syncwarp();
       tc_fence_after();
       const bool empty = l == 0.0f;   // the row saw nothing: 0, whatever the values were
       const float inv = whole ? (l == 0.0f ? 0.0f : 1.0f / l) : 1.0f;
@@ -705,6 +736,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll 1
       for (int x = c0; x < c1; x += 32) {
         float o[32];
+        __syncwarp();
         tmem_ld_x32(tm_o + (merge ? 0 : i * D) + x, o);
         tmem_ld_wait();
         pin(o);
@@ -752,6 +784,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           for (int y = 0; y < 32; y += 4) dst[(y / 4) * kTile] = make_float4(o[y], o[y + 1], o[y + 2], o[y + 3]);
         }
       }
+      __syncwarp();
       tc_fence_before();
       // O and the shared statistics may be overwritten once both pipelines have read them
       named_bar_sync(1, 2 * kTile);
@@ -894,6 +927,12 @@ cudaError_t launch(const AttnArgs& a, void* workspace, int num_sms, cudaStream_t
       return cudaErrorInvalidValue;
   }
 
+  // the register split must not exceed what the block is launched with (it would wait forever)
+  static const int regs = [] {
+    cudaFuncAttributes fa;
+    return cudaFuncGetAttributes(&fa, tree_attn_kernel<D>) == cudaSuccess ? fa.numRegs : 0;
+  }();
+  if (regs < kLaunchRegs) return cudaErrorInvalidConfiguration;
   const size_t smem = C::kRing + sizeof(AttnSmem);
   cudaError_t e = set_smem_limit<tree_attn_kernel<D>>(smem);
   if (e != cudaSuccess) return e;
