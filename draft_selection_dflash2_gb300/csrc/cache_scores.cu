@@ -3,58 +3,360 @@
 //
 //   scores[b,h,j] += sum_r exp(scale <q_r, k_j> - lse_r)
 //
-// over the rows r = (accepted node, query head of the group) of h.  One warp per
-// position, rows in order.
-#include "attn.h"
+// over the rows r = (accepted node i, head g of the group) of key/value head h.
+// The sum runs over rows, so the product is taken keys by rows, S^T = K Q^T: a
+// key is a TMEM lane and one thread adds up its key's columns with no exchange
+// between threads.  A unit is 128 keys of one (sequence, head); its rows are taken
+// in chunks of 128 columns (the last one narrower).  All units are cut into equal
+// runs, one per CTA.
+//   warp 0      TMA producer of K tiles (128 x D, one box per page piece).
+//   warp 1      MMA issuer: one 128 x N accumulator (fp32) per chunk, four
+//               128-column buffers in TMEM, two for each half of the epilogue.
+//   warps 4-7, 8-11  epilogue: alternate units; exp2(S c - lse c') per column,
+//               summed in fp32 in column order.
+// When a run enters another (sequence, head) the epilogue warps lay that head's
+// query rows out in shared memory (up to 512 rows; more rows take one launch per
+// 512) and their lse beside them.
+#include "attn_common.cuh"
 #include "launch.h"
 
 namespace dflash2 {
 namespace {
 
+constexpr int kThreads = 384;
+constexpr int kMaxChunks = 4;           // row chunks per launch
+constexpr int kMaxSlots = 12;
+constexpr int kSmemLimit = 232448;      // 227 KB
+
+struct ScoresSmem {
+  uint64_t k_full[kMaxSlots], k_empty[kMaxSlots];
+  uint64_t q_full, s_full[4], s_free[4], drain;
+  float lse[kMaxChunks * kTile];        // in base 2; +inf for rows that add nothing
+  int64_t scan[kThreads / 32];
+  int64_t u0, u1, base;
+  int32_t b0;
+  uint32_t tmem;
+  int abort_flag;
+};
+
+struct ScoresPlan {
+  ScoresArgs a;
+  float c;                  // scale * log2(e)
+  int32_t limit;            // positions a length may reach
+  int32_t row0;             // first row of this launch
+  int32_t chunks;           // row chunks that shared memory holds
+  int32_t slots;            // ring of K tiles
+  int32_t box_rows;
+};
+
+// Rows of sequence b that this launch takes.
+__device__ __forceinline__ int32_t rows_of(const ScoresPlan& p, int64_t b) {
+  const int32_t count = p.a.count == nullptr ? p.a.T : kv_clamp(p.a.count[b], p.a.T, p.a.err);
+  return max(0, min(count * p.a.group - p.row0, p.chunks * kTile));
+}
+
+__device__ __forceinline__ int64_t units_of(const ScoresPlan& p, int64_t b) {
+  const int32_t n = kv_clamp(p.a.cache_len[b], p.limit, p.a.err);
+  return rows_of(p, b) > 0 ? (n + kTile - 1) / kTile : 0;
+}
+
+struct Segment {
+  int32_t b, h, s, e;       // units [s, e) of (b, h)
+  int32_t len, rows;
+};
+
+struct Walk {
+  int64_t u, u1, base, n_seq;
+  int32_t b, n;
+  __device__ __forceinline__ void start(const ScoresPlan& p, const ScoresSmem& s) {
+    u = s.u0;
+    u1 = s.u1;
+    base = s.base;
+    b = s.b0;
+    if (u < u1) load(p);
+  }
+  __device__ __forceinline__ void load(const ScoresPlan& p) {
+    n = static_cast<int32_t>(units_of(p, b));
+    n_seq = static_cast<int64_t>(n) * p.a.cache.heads;
+  }
+  __device__ __forceinline__ bool next(const ScoresPlan& p, Segment* g) {
+    if (u >= u1) return false;
+    while (u >= base + n_seq) {   // sequences without units are passed over
+      base += n_seq;
+      ++b;
+      load(p);
+    }
+    const int64_t rel = u - base;
+    g->h = static_cast<int32_t>(rel / n);
+    g->s = static_cast<int32_t>(rel % n);
+    g->e = static_cast<int32_t>(imin64(n, g->s + (u1 - u)));
+    g->b = b;
+    g->len = kv_clamp(p.a.cache_len[b], p.limit, nullptr);
+    g->rows = rows_of(p, b);
+    u += g->e - g->s;
+    return true;
+  }
+};
+
+// 32 lanes x 16 consecutive fp32 columns.
+__device__ __forceinline__ void tmem_ld_x16(uint32_t taddr, float (&v)[16]) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, "
+      "[%16];"
+      : "=f"(v[0]), "=f"(v[1]), "=f"(v[2]), "=f"(v[3]), "=f"(v[4]), "=f"(v[5]), "=f"(v[6]), "=f"(v[7]), "=f"(v[8]),
+        "=f"(v[9]), "=f"(v[10]), "=f"(v[11]), "=f"(v[12]), "=f"(v[13]), "=f"(v[14]), "=f"(v[15])
+      : "r"(taddr)
+      : "memory");
+}
+
+__device__ __forceinline__ void pin16(float (&v)[16]) {
+#pragma unroll
+  for (int i = 0; i < 16; i += 8)
+    asm volatile("" : "+f"(v[i]), "+f"(v[i + 1]), "+f"(v[i + 2]), "+f"(v[i + 3]), "+f"(v[i + 4]), "+f"(v[i + 5]),
+                 "+f"(v[i + 6]), "+f"(v[i + 7]));
+}
+
+// columns of chunk c of `rows` rows
+__device__ __forceinline__ int chunk_cols(int rows, int c) { return min(kTile, (rows - c * kTile + 15) & ~15); }
+
 template <int D>
-__global__ void __launch_bounds__(256) cache_scores_kernel(const ScoresArgs a, int64_t limit) {
-  constexpr int E = D / 32;
-  const int lane = threadIdx.x & 31;
-  const int h = blockIdx.x % a.cache.heads;
-  const int64_t b = blockIdx.x / a.cache.heads;
-  const int32_t n = kv_clamp(a.cache_len[b], static_cast<int32_t>(limit), a.err);
-  const int32_t count = a.count == nullptr ? a.T : kv_clamp(a.count[b], a.T, a.err);
-  for (int32_t j = blockIdx.y * 8 + (threadIdx.x >> 5); j < n; j += gridDim.y * 8) {
-  bool ok;
-  const uint16_t* kp = a.cache.k + kv_offset(a.cache, b, j, h, a.err, &ok) + lane * E;
-  float k[E];
+__global__ void __launch_bounds__(kThreads, 1)
+    cache_scores_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ ScoresPlan p) {
+  constexpr int kHalves = D / 64;
+  constexpr int kTileBytes = kTile * D * 2;
+  extern __shared__ __align__(1024) uint8_t q_smem[];   // no static shared memory: the base is 1024-byte aligned
+  const ScoresArgs& a = p.a;
+  const int S = p.slots;
+  uint8_t* ring = q_smem + p.chunks * kTileBytes;
+  ScoresSmem& s = *reinterpret_cast<ScoresSmem*>(ring + S * kTileBytes);
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  volatile int* abort_flag = &s.abort_flag;
+
+  if (threadIdx.x == 0) {
+    for (int i = 0; i < S; ++i) {
+      mbar_init(&s.k_full[i], 1);
+      mbar_init(&s.k_empty[i], 1);
+    }
+    mbar_init(&s.q_full, 2 * kTile);
+    for (int i = 0; i < 4; ++i) {
+      mbar_init(&s.s_full[i], 1);
+      mbar_init(&s.s_free[i], kTile);
+    }
+    mbar_init(&s.drain, 1);
+    s.abort_flag = 0;
+    fence_mbar_init();
+    tma_prefetch_desc(&tmK);
+  }
+  if (warp == 3) {
+    tmem_alloc(&s.tmem, 512);
+    tmem_relinquish();
+  }
+  pdl_wait();
+  pdl_launch_dependents();
+  tc_fence_before();
+  find_run<kThreads>([&](int64_t b) { return units_of(p, b); }, a.B, a.cache.heads, 1, blockIdx.x, gridDim.x, 0,
+                     s.scan, &s.u0, &s.u1, &s.base, &s.b0);
+  tc_fence_after();
+  const uint32_t tmem = s.tmem;
+  Walk walk;
+  walk.start(p, s);
+  Segment g;
+  bool live = true;
+
+  if (warp == 0) {
+    // ---- producer ----
+    uint32_t it = 0, issued = 0;
+    const int half = lane % kHalves, row = lane / kHalves * p.box_rows;
+    while (walk.next(p, &g)) {
+      for (int u = g.s; u < g.e; ++u, ++it) {
+        const int j = u * kTile + row;
+        const bool has = row < kTile && j < g.len;
+        int y = j, w = g.b;
+        if (has && a.cache.table != nullptr) {
+          bool ok;
+          w = kv_page(a.cache, g.b, j, a.err, &ok);
+          y = j & (a.cache.page_size - 1);
+        }
+        const uint32_t boxes = __popc(__ballot_sync(0xFFFFFFFFu, has));
+        const int slot = it % S;
+        if (it >= static_cast<uint32_t>(S)) wait_live(&s.k_empty[slot], (it / S - 1) & 1, &live, abort_flag, a.err);
+        live = __all_sync(0xFFFFFFFFu, live);
+        if (!live) continue;
+        issued = it + 1;
+        if (lane == 0) mbar_arrive_expect_tx(&s.k_full[slot], boxes * p.box_rows * 128);
+        __syncwarp();
+        if (has)
+          tma_load_4d(ring + slot * kTileBytes + half * kTile * 128 + row * 128, &tmK, half * 64, y, g.h, w,
+                      &s.k_full[slot]);
+      }
+    }
+    if (lane == 0 && !live) {
+      for (uint32_t j = issued > static_cast<uint32_t>(S) ? issued - S : 0; j < issued; ++j)
+        mbar_wait_bounded(&s.k_full[j % S], (j / S) & 1, a.err);
+    }
+    __syncwarp();
+  } else if (warp == 1) {
+    // ---- MMA issuer ----
+    if (lane == 0) {
+      uint32_t it = 0;
+      uint32_t used[2] = {0, 0};    // chunks given to each half of the epilogue so far
+      int seg = 0;
+      for (; walk.next(p, &g); ++seg) {
+        wait_live(&s.q_full, seg & 1, &live, abort_flag, a.err);
+        const int chunks = (g.rows + kTile - 1) / kTile;
+        for (int u = g.s; u < g.e; ++u, ++it) {
+          const int slot = it % S, e = it & 1;
+          wait_live(&s.k_full[slot], (it / S) & 1, &live, abort_flag, a.err);
+          const uint32_t k_base = smem_addr(ring + slot * kTileBytes);
+          for (int c = 0; c < chunks; ++c) {
+            const uint32_t n = used[e]++;
+            const int buf = 2 * e + (n & 1);
+            if (n >= 2) wait_live(&s.s_free[buf], ((n >> 1) - 1) & 1, &live, abort_flag, a.err);
+            if (!live) continue;
+            tc_fence_after();
+            const uint32_t q_base = smem_addr(q_smem + c * kTileBytes);
+            const uint32_t idesc = umma_idesc_bf16(128, chunk_cols(g.rows, c));
 #pragma unroll
-  for (int e = 0; e < E; ++e) k[e] = bf16_bits_to_float(kp[e]) * a.scale;
-  float w = 0.0f;
-  for (int i = 0; i < count; ++i) {
-    const int t = a.path == nullptr ? i : clamp_node(a.path[b * a.T + i], a.T, a.err);
-    for (int g = 0; g < a.group; ++g) {
-      const int hq = h * a.group + g;
-      const uint16_t* qp = a.q + b * a.q_b + t * a.q_t + hq * a.q_h + lane * E;
-      float z = 0.0f;
+            for (int k = 0; k < D / 16; ++k) {
+              const uint32_t o = (k >> 2) * kTile * 128 + (k & 3) * 32;
+              umma_bf16(tmem + buf * kTile, umma_desc_sw128(k_base + o), umma_desc_sw128(q_base + o), idesc,
+                        k > 0 ? 1u : 0u);
+            }
+            umma_commit(&s.s_full[buf]);
+          }
+          if (live) umma_commit(&s.k_empty[slot]);
+        }
+      }
+      umma_commit(&s.drain);
+    }
+    __syncwarp();
+  } else if (warp >= 4) {
+    // ---- epilogue half e: one key per thread ----
+    const int e = warp >= 8 ? 1 : 0;
+    const int r = threadIdx.x & (kTile - 1);
+    const int tid = static_cast<int>(threadIdx.x) - kTile;
+    const uint32_t lanes = static_cast<uint32_t>((warp & 3) * 32) << 16;
+    uint32_t it = 0, n = 0;
+    while (walk.next(p, &g)) {
+      // both halves have read every product of the last segment: its query rows may go
+      __syncwarp();
+      named_bar_sync(1, 2 * kTile);
+      const int padded = (g.rows + 15) & ~15;
+      constexpr int kPieces = D / 8;
+      for (int x = tid; x < padded * kPieces; x += 2 * kTile) {
+        const int row = x / kPieces, piece = x % kPieces;
+        uint4 v = make_uint4(0, 0, 0, 0);
+        float l2 = INFINITY;
+        if (row < g.rows) {
+          const int i = (p.row0 + row) / a.group, hq = g.h * a.group + (p.row0 + row) % a.group;
+          const int t = a.path == nullptr ? i : clamp_node(a.path[static_cast<int64_t>(g.b) * a.T + i], a.T, a.err);
+          const float lse = a.lse[(static_cast<int64_t>(g.b) * a.T + t) * a.heads + hq];
+          if (lse != -INFINITY) {    // a query that saw nothing adds nothing
+            l2 = lse * 1.4426950408889634f;
+            v = *reinterpret_cast<const uint4*>(a.q + g.b * a.q_b + t * a.q_t + hq * a.q_h + piece * 8);
+          }
+        }
+        const int rr = row & (kTile - 1);
+        *reinterpret_cast<uint4*>(q_smem + (row / kTile) * kTileBytes + (piece >> 3) * kTile * 128 + rr * 128 +
+                                  (((piece & 7) ^ (rr & 7)) << 4)) = v;
+        if (piece == 0) s.lse[row] = -l2;
+      }
+      __syncwarp();
+      asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+      mbar_arrive(&s.q_full);
+      named_bar_sync(1, 2 * kTile);      // the rows' lse is there
+      const int chunks = (g.rows + kTile - 1) / kTile;
+      for (int u = g.s; u < g.e; ++u, ++it) {
+        if ((it & 1) != static_cast<uint32_t>(e)) continue;
+        uint64_t sum0 = pack2(0.0f, 0.0f), sum1 = sum0;
+        const uint64_t c2 = pack2(p.c, p.c);
+        for (int c = 0; c < chunks; ++c, ++n) {
+          const int buf = 2 * e + (n & 1);
+          wait_live(&s.s_full[buf], (n >> 1) & 1, &live, abort_flag, a.err);
+          __syncwarp();
+          tc_fence_after();
+          const int cols = chunk_cols(g.rows, c);
+          const float* l2 = s.lse + c * kTile;
+#pragma unroll 1
+          for (int x = 0; x < cols; x += 16) {
+            float z[16];
+            tmem_ld_x16(tmem + buf * kTile + x + lanes, z);
+            tmem_ld_wait();
+            pin16(z);
+            if (x + 16 >= cols) {        // read out: the buffer goes back
+              tc_fence_before();
+              mbar_arrive(&s.s_free[buf]);
+            }
 #pragma unroll
-      for (int e = 0; e < E; ++e) z += k[e] * bf16_bits_to_float(qp[e]);
-#pragma unroll
-      for (int s = 16; s > 0; s >>= 1) z += __shfl_xor_sync(0xFFFFFFFFu, z, s);
-      const float lse = a.lse[(b * a.T + t) * a.heads + hq];
-      if (lse != -INFINITY) w += expf(z - lse);
+            for (int y = 0; y < 16; y += 4) {
+              const float4 l = *reinterpret_cast<const float4*>(l2 + x + y);
+              const float2 e0 = unpack2(fma2(pack2(z[y], z[y + 1]), c2, pack2(l.x, l.y)));
+              const float2 e1 = unpack2(fma2(pack2(z[y + 2], z[y + 3]), c2, pack2(l.z, l.w)));
+              sum0 = add2(sum0, pack2(exp2_approx(e0.x), exp2_approx(e0.y)));
+              sum1 = add2(sum1, pack2(exp2_approx(e1.x), exp2_approx(e1.y)));
+            }
+          }
+        }
+        const float2 sum = unpack2(add2(sum0, sum1));
+        const int j = u * kTile + r;
+        if (j < g.len)
+          a.scores[(static_cast<int64_t>(g.b) * a.cache.heads + g.h) * a.scores_ld + j] += sum.x + sum.y;
+      }
     }
   }
-  if (lane == 0) a.scores[(b * a.cache.heads + h) * a.scores_ld + j] += w;
+
+  __syncthreads();
+  if (threadIdx.x == 0) mbar_wait_bounded(&s.drain, 0, a.err);   // the tensor cores have finished
+  __syncthreads();
+  if (warp == 3) {
+    tc_fence_after();
+    tmem_dealloc(tmem, 512);
   }
+}
+
+template <int D>
+cudaError_t launch(const ScoresArgs& a, int num_sms, cudaStream_t stream) {
+  constexpr int kTileBytes = kTile * D * 2;
+  const KvView& c = a.cache;
+  ScoresPlan p;
+  p.a = a;
+  p.c = a.scale * 1.4426950408889634f;
+  p.limit = static_cast<int32_t>(imin64(c.capacity, a.scores_ld));
+  if (p.limit == 0) return cudaSuccess;
+  const int32_t rows = a.T * a.group;
+  p.chunks = min((rows + kTile - 1) / kTile, kMaxChunks);
+  p.slots = min(kMaxSlots, static_cast<int>((kSmemLimit - sizeof(ScoresSmem)) / kTileBytes) - p.chunks);
+  p.box_rows = c.table != nullptr && c.page_size < kTile ? c.page_size : kTile;
+  CUtensorMap tmK;
+  const uint64_t kd[4] = {D, static_cast<uint64_t>(c.page_size), static_cast<uint64_t>(c.heads),
+                          static_cast<uint64_t>(c.num_pages)};
+  const uint64_t ks[3] = {static_cast<uint64_t>(c.token_stride), static_cast<uint64_t>(c.head_stride),
+                          static_cast<uint64_t>(c.page_stride)};
+  const uint32_t kb[4] = {64, static_cast<uint32_t>(p.box_rows), 1, 1};
+  if (!make_tmap_bf16_nd(&tmK, c.k, 4, kd, ks, kb)) return cudaErrorInvalidValue;
+  const size_t smem = static_cast<size_t>(p.chunks + p.slots) * kTileBytes + sizeof(ScoresSmem);
+  const cudaError_t e = set_smem_limit<cache_scores_kernel<D>>(kSmemLimit);
+  if (e != cudaSuccess) return e;
+  const int64_t most = a.B * c.heads * ((static_cast<int64_t>(p.limit) + kTile - 1) / kTile);
+  cudaLaunchAttribute attr = pdl_attribute();
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(static_cast<unsigned>(imin64(num_sms, most)), 1, 1);
+  cfg.blockDim = dim3(kThreads, 1, 1);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = stream;
+  cfg.attrs = &attr;
+  cfg.numAttrs = 1;
+  for (p.row0 = 0; p.row0 < rows; p.row0 += kMaxChunks * kTile) {
+    const cudaError_t st = cudaLaunchKernelEx(&cfg, cache_scores_kernel<D>, tmK, p);
+    if (st != cudaSuccess) return st;
+  }
+  return cudaSuccess;
 }
 
 }  // namespace
 
-cudaError_t launch_cache_scores(const ScoresArgs& a, int64_t head_dim, int, cudaStream_t stream) {
-  const int64_t limit = imin64(a.cache.capacity, a.scores_ld);
-  if (limit == 0) return cudaSuccess;
-  const dim3 grid(static_cast<unsigned>(a.B * a.cache.heads), static_cast<unsigned>(imin64((limit + 7) / 8, 65535)));
-  if (head_dim == 64)
-    cache_scores_kernel<64><<<grid, 256, 0, stream>>>(a, limit);
-  else
-    cache_scores_kernel<128><<<grid, 256, 0, stream>>>(a, limit);
-  return cudaGetLastError();
+cudaError_t launch_cache_scores(const ScoresArgs& a, int64_t head_dim, int num_sms, cudaStream_t stream) {
+  return head_dim == 64 ? launch<64>(a, num_sms, stream) : launch<128>(a, num_sms, stream);
 }
 
 }  // namespace dflash2

@@ -39,14 +39,12 @@
 // Every wait is bounded (DFLASH2_DEVERR_TIMEOUT): after one gives up the CTA
 // stops issuing copies and products, walks its loops to their end, waits for its
 // own copies in flight, frees its TMEM and returns.
-#include "attn.h"
+#include "attn_common.cuh"
 #include "launch.h"
-#include "tcgen05.cuh"
 
 namespace dflash2 {
 namespace {
 
-constexpr int kTile = 128;              // rows of a query tile, keys of a unit
 constexpr int kThreads = 384;
 constexpr int kMaxSlots = 10;
 // The block is launched with 168 registers a thread; warps 0-3 give some to the
@@ -90,40 +88,6 @@ struct AttnPlan {
   uint32_t q_box_bytes;
 };
 
-__device__ __forceinline__ float exp2_approx(float x) {
-  float y;
-  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-  return y;
-}
-
-__device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
-  uint32_t r;
-  asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
-  return r;
-}
-
-// two independent fp32 operations per instruction
-__device__ __forceinline__ uint64_t pack2(float x, float y) {
-  uint64_t r;
-  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(x), "f"(y));
-  return r;
-}
-__device__ __forceinline__ float2 unpack2(uint64_t v) {
-  float2 r;
-  asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(v));
-  return r;
-}
-__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
-  uint64_t d;
-  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(a), "l"(b), "l"(c));
-  return d;
-}
-__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
-  uint64_t d;
-  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
-  return d;
-}
-
 // The bf16 pair of what two fp32 values lose when they are rounded to bf16.
 __device__ __forceinline__ uint32_t remainder_bf16(float x, float y) {
   const uint32_t hi = pack_bf16(x, y);
@@ -135,51 +99,6 @@ __device__ __forceinline__ int64_t units_of(const AttnArgs& a, int64_t b) {
   const int32_t n = kv_clamp(a.cache_len[b], a.cache.capacity, a.err);
   const int64_t u = (static_cast<int64_t>(n) + kTile - 1) / kTile + (a.k_new != nullptr ? 1 : 0);
   return u > 0 ? u : 1;
-}
-
-// Cuts all units into runs of equal length and finds the sequence that unit
-// run * length + at_end * length (the run's start or end) falls into: *base =
-// units before that sequence's.  Whole-block; every thread returns the same.
-template <int kT>
-__device__ void find_run(const AttnPlan& p, int64_t run, int64_t runs, int at_end, int64_t* scan, int64_t* out_u0,
-                         int64_t* out_u1, int64_t* out_base, int32_t* out_b) {
-  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  const int64_t per_seq = static_cast<int64_t>(p.a.cache.heads) * p.pairs;
-  const int64_t chunk = (p.a.B + kT - 1) / kT;
-  const int64_t b_lo = tid * chunk, b_hi = imin64(p.a.B, b_lo + chunk);
-  int64_t sum = 0;
-  for (int64_t b = b_lo; b < b_hi; ++b) sum += units_of(p.a, b) * per_seq;
-  int64_t incl = sum;
-#pragma unroll
-  for (int s = 1; s < 32; s <<= 1) {
-    const int64_t o = __shfl_up_sync(0xFFFFFFFFu, incl, s);
-    if (lane >= s) incl += o;
-  }
-  if (lane == 31) scan[warp] = incl;
-  __syncthreads();
-  int64_t before = incl - sum, total = 0;
-  for (int w = 0; w < kT / 32; ++w) {
-    if (w < warp) before += scan[w];
-    total += scan[w];
-  }
-  const int64_t len = imax64((total + runs - 1) / runs, kMinRun);
-  const int64_t u0 = imin64(run * len, total), u1 = imin64(u0 + len, total);
-  const int64_t u = at_end ? u1 : u0;
-  if (u >= before && u < before + sum) {
-    int64_t base = before, b = b_lo;
-    for (;; ++b) {
-      const int64_t n = units_of(p.a, b) * per_seq;
-      if (u < base + n) break;
-      base += n;
-    }
-    *out_base = base;
-    *out_b = static_cast<int32_t>(b);
-  }
-  if (tid == 0) {
-    *out_u0 = u0;
-    *out_u1 = u1;
-  }
-  __syncthreads();
 }
 
 // One item's stretch of a run.
@@ -237,64 +156,6 @@ struct Walk {
   }
 };
 
-// A bounded wait that also gives up when another role of the CTA has; once one
-// has given up (*live = false) later waits return at once.
-__device__ __forceinline__ void wait_live(uint64_t* bar, uint32_t parity, bool* live, volatile int* abort_flag,
-                                          uint32_t* err) {
-  if (!*live) return;
-  uint64_t start = 0;
-  for (uint32_t it = 1; !mbar_try_wait(bar, parity); ++it) {
-    if ((it & 255u) == 0) {   // rarely: reading the timer takes longer than most of these waits
-      if (*abort_flag) {
-        *live = false;
-        return;
-      }
-      const uint64_t now = global_timer_ns();
-      if (start == 0) start = now;
-      if (now - start > kWaitLimitNs) {
-        raise_error(err, DFLASH2_DEVERR_TIMEOUT);
-        *abort_flag = 1;
-        *live = false;
-        return;
-      }
-    }
-  }
-}
-
-// The barrier on which tile `it` of the ring lands, and its parity.  A parity
-// wait can only tell a phase from the one before it, and the pipelines do not
-// look at every tile when they share a row tile.  So a slot's uses alternate
-// between two barriers: when a pipeline asks for a slot's use k the producer has
-// issued use k - 1 (it issues in order, and the pipeline has seen a later tile or
-// the item's queries), for which use k - 2 had landed and been used, and use k
-// cannot be passed by without this pipeline.
-template <int S>
-__device__ __forceinline__ uint64_t* tile_bar(uint64_t* kv_full, uint32_t it) {
-  return &kv_full[(it % S) * 2 + (it / S & 1)];
-}
-template <int S>
-__device__ __forceinline__ uint32_t tile_parity(uint32_t it) {
-  return it / S >> 1 & 1;
-}
-
-__device__ __forceinline__ void tma_load_4d(void* dst, const CUtensorMap* map, int x, int y, int z, int w,
-                                            uint64_t* bar) {
-  asm volatile(
-      "cp.async.bulk.tensor.4d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
-      " [%0], [%1, {%2, %3, %4, %5}], [%6];" ::"r"(smem_addr(dst)),
-      "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(z), "r"(w), "r"(smem_addr(bar))
-      : "memory");
-}
-
-__device__ __forceinline__ void tma_load_5d(void* dst, const CUtensorMap* map, int x, int y, int z, int w, int v,
-                                            uint64_t* bar) {
-  asm volatile(
-      "cp.async.bulk.tensor.5d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
-      " [%0], [%1, {%2, %3, %4, %5, %6}], [%7];" ::"r"(smem_addr(dst)),
-      "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(z), "r"(w), "r"(v), "r"(smem_addr(bar))
-      : "memory");
-}
-
 // D[tmem] (+)= A[tmem] * B[smem]: A is 128 rows of 16 bf16 (8 columns), B is
 // 16 x N with N contiguous (MN-major).
 __device__ __forceinline__ void umma_bf16_ts(uint32_t tmem_d, uint32_t tmem_a, uint64_t bdesc, uint32_t idesc,
@@ -329,14 +190,6 @@ __device__ __forceinline__ void tmem_st_x16(uint32_t taddr, const uint32_t (&r)[
       : "memory");
 }
 __device__ __forceinline__ void tmem_st_wait() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
-
-// Keeps uses of loaded values after the wait that precedes this in the program.
-__device__ __forceinline__ void pin(float (&v)[32]) {
-#pragma unroll
-  for (int i = 0; i < 32; i += 8)
-    asm volatile("" : "+f"(v[i]), "+f"(v[i + 1]), "+f"(v[i + 2]), "+f"(v[i + 3]), "+f"(v[i + 4]), "+f"(v[i + 5]),
-                 "+f"(v[i + 6]), "+f"(v[i + 7]));
-}
 
 __device__ __forceinline__ bool finite_bf16(uint32_t bits) { return (bits & 0x7F80u) != 0x7F80u; }
 
@@ -396,7 +249,8 @@ __global__ void __launch_bounds__(kThreads, 1)
   pdl_wait();
   pdl_launch_dependents();
   tc_fence_before();
-  find_run<kThreads>(p, blockIdx.x, gridDim.x, 0, s.scan, &s.u0, &s.u1, &s.base, &s.b0);
+  find_run<kThreads>([&](int64_t b) { return units_of(a, b); }, a.B, static_cast<int64_t>(a.cache.heads) * p.pairs,
+                     kMinRun, blockIdx.x, gridDim.x, 0, s.scan, &s.u0, &s.u1, &s.base, &s.b0);
   tc_fence_after();
   const uint32_t tmem = s.tmem;
   Walk walk;
@@ -813,7 +667,8 @@ __global__ void __launch_bounds__(kTile) tree_attn_join_kernel(const __grid_cons
   pdl_launch_dependents();
   if (threadIdx.x == 0) s_b = -1;
   __syncthreads();
-  find_run<kTile>(p, blockIdx.x, runs, 1, scan, &s_u0, &s_u1, &s_base, &s_b);
+  find_run<kTile>([&](int64_t b) { return units_of(a, b); }, a.B, static_cast<int64_t>(a.cache.heads) * p.pairs,
+                  kMinRun, blockIdx.x, runs, 1, scan, &s_u0, &s_u1, &s_base, &s_b);
   const int64_t u0 = s_u0, u1 = s_u1, len = u1 - u0;
   if (s_b < 0 || len == 0) return;         // the last run ends everything
   const int32_t b = s_b;

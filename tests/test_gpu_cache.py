@@ -581,3 +581,21 @@ def test_a_pool_past_32_bits(handle):
         w = kept[0, h].long()
         assert torch.equal(dk[:, h], rows[0][0][w, h]) and torch.equal(dv[:, h], rows[0][1][w, h])
     assert m.tolist() == [64] and handle.device_error() == 0
+
+
+@pytest.mark.parametrize("lens,T,heads,H,D", [([100000, 70001], 1, 16, 8, 64), ([60000, 90000], 3, 8, 8, 128),
+                                              ([30000], 40, 32, 8, 128)])
+def test_long_runs(handle, lens, T, heads, H, D):
+    # tens of tiles per CTA: the two pipelines drift apart within the ring
+    gen = torch.Generator(device="cuda").manual_seed(14)
+    B = len(lens)
+    cache, rows = make_cache(gen, lens, H, D, 0, max(lens))
+    q, kn, vn = randn(gen, B, T, heads, D), randn(gen, B, T, H, D), randn(gen, B, T, H, D)
+    sees = np.tril(np.ones((T, T), bool))[None].repeat(B, 0)
+    cl = torch.tensor(lens, dtype=torch.int32, device="cuda")
+    got = api.tree_attention(handle, q, cache, cl, kn, vn)
+    for _ in range(3):
+        again = api.tree_attention(handle, q, cache, cl, kn, vn)
+        assert torch.equal(got[0], again[0]) and torch.equal(got[1], again[1])
+    check_attention(got, reference(q, rows, kn, vn, sees, D ** -0.5))
+    assert handle.device_error() == 0
