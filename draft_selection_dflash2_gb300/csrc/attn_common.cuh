@@ -148,6 +148,41 @@ __device__ __forceinline__ void tma_load_5d(void* dst, const CUtensorMap* map, i
       : "memory");
 }
 
+// The pages of consecutive tiles of one sequence, for a whole warp: 32 entries of
+// its row of the block table a window, a lane each, and the next window's loads in
+// flight while this one's are used (one by one they would cost a memory latency
+// per tile).
+struct PageFeed {
+  const int32_t* row;       // the sequence's row; nullptr without a table
+  int32_t base, last;       // the window's first entry; the last entry that may be read
+  int32_t cur, next;        // entries base + lane and base + 32 + lane
+  __device__ __forceinline__ int32_t fetch(int32_t i) const { return i <= last ? row[i] : 0; }
+  // Tiles from `tile` on of sequence b, which holds len positions.
+  __device__ __forceinline__ void start(const KvView& c, int64_t b, int32_t tile, int32_t len, int lane) {
+    row = c.table == nullptr || len <= 0 ? nullptr : c.table + b * c.table_ld;
+    if (row == nullptr) return;
+    base = (tile * kTile) >> c.page_shift;
+    last = (len - 1) >> c.page_shift;
+    cur = fetch(base + lane);
+    next = fetch(base + 32 + lane);
+  }
+  // The page of position j of the tile that starts at position `first` (a tile's
+  // pages lie in one window: windows start at a tile, and a tile's pages, a power
+  // of two of at most 8, or a page's tiles divide it).  Whole warp; ids outside the
+  // cache are clamped and, where `used`, flagged.
+  __device__ __forceinline__ int32_t page(const KvView& c, int32_t first, int32_t j, bool used, int lane, uint32_t* err) {
+    if ((first >> c.page_shift) >= base + 32) {
+      base += 32;
+      cur = next;
+      next = fetch(base + 32 + lane);
+    }
+    const int32_t p = __shfl_sync(0xFFFFFFFFu, cur, ((j >> c.page_shift) - base) & 31);
+    if (static_cast<uint32_t>(p) < static_cast<uint32_t>(c.num_pages)) return p;
+    if (used) raise_error(err, DFLASH2_DEVERR_BAD_PAGE);
+    return p < 0 ? 0 : c.num_pages - 1;
+  }
+};
+
 // Keeps uses of loaded values after the wait that precedes this in the program.
 __device__ __forceinline__ void pin(float (&v)[32]) {
 #pragma unroll

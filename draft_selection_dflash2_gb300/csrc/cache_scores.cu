@@ -167,14 +167,15 @@ __global__ void __launch_bounds__(kThreads, 1)
     // ---- producer ----
     uint32_t it = 0, issued = 0;
     const int half = lane % kHalves, row = lane / kHalves * p.box_rows;
+    PageFeed pages;
     while (walk.next(p, &g)) {
+      pages.start(a.cache, g.b, g.s, g.len, lane);
       for (int u = g.s; u < g.e; ++u, ++it) {
         const int j = u * kTile + row;
         const bool has = row < kTile && j < g.len;
         int y = j, w = g.b;
-        if (has && a.cache.table != nullptr) {
-          bool ok;
-          w = kv_page(a.cache, g.b, j, a.err, &ok);
+        if (pages.row != nullptr) {
+          w = pages.page(a.cache, u * kTile, j, has, lane, a.err);
           y = j & (a.cache.page_size - 1);
         }
         const uint32_t boxes = __popc(__ballot_sync(0xFFFFFFFFu, has));

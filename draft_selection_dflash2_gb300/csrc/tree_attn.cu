@@ -268,6 +268,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     uint32_t it = 0;      // K and V tiles so far
     uint32_t issued = 0;  // those whose copies were started
     int seg = 0, q_issued = 0;
+    PageFeed pages;
     for (; walk.next(p, &g); ++seg) {
       if (seg > 0) wait_live(&s.q_empty, (seg - 1) & 1, &live, abort_flag, a.err);
       live = __all_sync(0xFFFFFFFFu, live);
@@ -284,6 +285,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       // lane -> (page piece of the tile, column block)
       const int half = lane % C::kHalves, piece = lane / C::kHalves;
       const int row = piece * p.box_rows;       // first row of the lane's box
+      pages.start(a.cache, g.b, g.s, g.len, lane);
       for (int u = g.s; u < g.e; ++u) {
         const bool drafted = u >= cached && a.k_new != nullptr;
         bool has;
@@ -297,9 +299,8 @@ __global__ void __launch_bounds__(kThreads, 1)
           has = row < kTile && j < g.len;
           bytes = p.box_rows * 128;
           y = j;
-          if (has && a.cache.table != nullptr) {
-            bool ok;
-            w = kv_page(a.cache, g.b, j, a.err, &ok);
+          if (pages.row != nullptr) {
+            w = pages.page(a.cache, u * kTile, j, has, lane, a.err);
             y = j & (a.cache.page_size - 1);
           }
         }
