@@ -372,14 +372,33 @@ class KVCache:
         self.ref = ctypes.byref(s)
 
 
+_I32, _I64, _F32, _BF16 = torch.int32, torch.int64, torch.float32, torch.bfloat16
+
+
 def _rows(name, t, heads, dim):
-    _need(_is16(t) and t.dim() == 4 and t.shape[3] == dim and (heads is None or t.shape[2] == heads) and
-          t.stride(3) == 1, f"{name}: bf16 [B, T, heads, {dim}], unit stride along the last dimension")
-    return t.shape
+    """Checks a [B, T, heads, dim] bf16 operand -> its shape (heads None: any)."""
+    shape = t.shape
+    if (len(shape) != 4 or shape[3] != dim or (heads is not None and shape[2] != heads) or t.stride(3) != 1 or
+            not _is16(t) or not t.is_cuda):
+        raise ValueError(f"{name}: CUDA bf16 [B, T, {'heads' if heads is None else heads}, {dim}], unit stride along "
+                         "the last dimension")
+    return shape
 
 
-def _vec(name, t, dtype, shape):
-    _need(t.dtype == dtype and tuple(t.shape) == shape and t.is_contiguous(), f"{name}: contiguous {dtype} {shape}")
+def _dense(name, t, dtype, shape):
+    """Checks a contiguous CUDA tensor of one type and shape -> its address."""
+    if t.dtype is not dtype or t.shape != shape or not t.is_contiguous() or not t.is_cuda:
+        raise ValueError(f"{name}: contiguous CUDA {dtype} {tuple(shape)}")
+    return t.data_ptr()
+
+
+def _opt(name, t, dtype, shape):
+    return None if t is None else _dense(name, t, dtype, shape)
+
+
+def _raw_stream(h, stream):
+    """The stream's handle; None: the current stream of the handle's device (which has to be the current one)."""
+    return torch._C._cuda_getCurrentRawStream(h.device) if stream is None else stream.cuda_stream
 
 
 def _new_on(stream, shape, dtype, dev):
@@ -389,6 +408,11 @@ def _new_on(stream, shape, dtype, dev):
         return torch.empty(shape, dtype=dtype, device=dev)
     with torch.cuda.stream(stream):
         return torch.empty(shape, dtype=dtype, device=dev)
+
+
+def _cache_for(cache, B):
+    if cache.batch < B:
+        raise ValueError(f"cache: {cache.batch} sequences, {B} wanted")
 
 
 def tree_attention_workspace(h: Handle, B: int, T: int, heads: int, kv_heads: int, head_dim: int) -> int:
@@ -402,34 +426,36 @@ def tree_attention(h: Handle, q, cache: KVCache, cache_len, k_new=None, v_new=No
     q [B, T, heads, dim]; k_new, v_new [B, T, kv_heads, dim] (equal strides; None: the cache alone); tree_mask
     int64 [B, T, (T + 63) // 64], bit s % 64 of word s // 64 of node t set where t sees s (None: a chain).
     scale: 1 / sqrt(dim) when None.  workspace: device bytes of at least tree_attention_workspace(...)."""
-    B, T, heads, dim = _rows("q", q, None, cache.dim)
-    _need(cache.batch >= B, "cache: fewer sequences than q")
-    _vec("cache_len", cache_len, torch.int32, (B,))
+    dim = cache.dim
+    shape = _rows("q", q, None, dim)
+    B, T, heads, _ = shape
+    _cache_for(cache, B)
     qs = q.stride()
-    ns = (0, 0, 0)
+    kp = vp = None
+    ns = qs
     if k_new is not None or v_new is not None:
-        _need(k_new is not None and v_new is not None and k_new.stride() == v_new.stride(),
-              "k_new, v_new: both or neither, with equal strides")
-        for name, t in (("k_new", k_new), ("v_new", v_new)):
-            _need(_rows(name, t, cache.heads, dim)[:2] == (B, T), f"{name}: [B, T] of q")
+        if k_new is None or v_new is None:
+            raise ValueError("k_new, v_new: both or neither")
         ns = k_new.stride()
-    if tree_mask is not None:
-        _vec("tree_mask", tree_mask, torch.int64, (B, T, (T + 63) // 64))
+        want = (B, T, cache.heads, dim)
+        if (_rows("k_new", k_new, cache.heads, dim) != want or _rows("v_new", v_new, cache.heads, dim) != want or
+                v_new.stride() != ns):
+            raise ValueError(f"k_new, v_new: {want} with equal strides")
+        kp, vp = k_new.data_ptr(), v_new.data_ptr()
     if out is None:
-        out = _new_on(stream, (B, T, heads, dim), torch.bfloat16, q.device)
-    else:
-        _need(_is16(out) and out.shape == q.shape and out.is_contiguous(), "out: contiguous bf16 of q's shape")
+        out = _new_on(stream, shape, _BF16, q.device)
+    elif out.shape != shape or not _is16(out) or not out.is_contiguous() or not out.is_cuda:
+        raise ValueError(f"out: contiguous CUDA bf16 {tuple(shape)}")
     if lse is None:
-        lse = _new_on(stream, (B, T, heads), torch.float32, q.device)
-    else:
-        _vec("lse", lse, torch.float32, (B, T, heads))
+        lse = _new_on(stream, (B, T, heads), _F32, q.device)
     if workspace is None:
         workspace = _new_on(stream, (max(tree_attention_workspace(h, B, T, heads, cache.heads, dim), 256),),
                             torch.uint8, q.device)
     _check(h._lib.dflash2_tree_attention(
-        h.ptr, _ptr(q), qs[0], qs[1], qs[2], cache.ref, _ptr(cache_len), _ptr(k_new), _ptr(v_new), ns[0], ns[1], ns[2],
-        _ptr(tree_mask), B, T, heads, dim ** -0.5 if scale is None else scale, _ptr(out), _ptr(lse), _ptr(workspace),
-        workspace.numel() * workspace.element_size(), _stream(stream)), "dflash2_tree_attention")
+        h._h, q.data_ptr(), qs[0], qs[1], qs[2], cache.ref, _dense("cache_len", cache_len, _I32, (B,)), kp, vp,
+        ns[0], ns[1], ns[2], _opt("tree_mask", tree_mask, _I64, (B, T, (T + 63) // 64)), B, T, heads,
+        dim ** -0.5 if scale is None else scale, out.data_ptr(), _dense("lse", lse, _F32, (B, T, heads)),
+        _ptr(workspace), workspace.nbytes, _raw_stream(h, stream)), "dflash2_tree_attention")
     return out, lse
 
 
@@ -439,27 +465,22 @@ def cache_commit(h: Handle, k_new, v_new, cache: KVCache, cache_len, count=None,
 
     k_new, v_new [B, T, kv_heads, dim]; count int32 [B] accepted nodes (None: T); path int32 [B, T] their ids
     (None: 0, 1, ...); scores fp32 [B, kv_heads, ld]: the appended positions' entries become 0."""
-    B, T = _rows("k_new", k_new, cache.heads, cache.dim)[:2]
-    _need(_rows("v_new", v_new, cache.heads, cache.dim)[:2] == (B, T) and k_new.stride() == v_new.stride(),
-          "v_new: shape and strides of k_new")
-    _need(cache.batch >= B, "cache: fewer sequences than k_new")
-    _vec("cache_len", cache_len, torch.int32, (B,))
-    if count is not None:
-        _vec("count", count, torch.int32, (B,))
-    if path is not None:
-        _vec("path", path, torch.int32, (B, T))
-    ld = 0
+    shape = _rows("k_new", k_new, cache.heads, cache.dim)
+    s = k_new.stride()
+    if _rows("v_new", v_new, cache.heads, cache.dim) != shape or v_new.stride() != s:
+        raise ValueError("v_new: shape and strides of k_new")
+    B, T, heads, _ = shape
+    _cache_for(cache, B)
+    ld, sp = 0, None
     if scores is not None:
         ld = scores.shape[-1]
-        _vec("scores", scores, torch.float32, (B, cache.heads, ld))
+        sp = _dense("scores", scores, _F32, (B, heads, ld))
     if new_len is None:
-        new_len = _new_on(stream, (B,), torch.int32, k_new.device)
-    else:
-        _vec("new_len", new_len, torch.int32, (B,))
-    s = k_new.stride()
-    _check(h._lib.dflash2_cache_commit(h.ptr, _ptr(k_new), _ptr(v_new), s[0], s[1], s[2], cache.ref, _ptr(cache_len),
-                                       _ptr(count), _ptr(path), B, T, _ptr(scores), ld, _ptr(new_len),
-                                       _stream(stream)), "dflash2_cache_commit")
+        new_len = _new_on(stream, (B,), _I32, k_new.device)
+    _check(h._lib.dflash2_cache_commit(
+        h._h, k_new.data_ptr(), v_new.data_ptr(), s[0], s[1], s[2], cache.ref,
+        _dense("cache_len", cache_len, _I32, (B,)), _opt("count", count, _I32, (B,)), _opt("path", path, _I32, (B, T)),
+        B, T, sp, ld, _dense("new_len", new_len, _I32, (B,)), _raw_stream(h, stream)), "dflash2_cache_commit")
     return new_len
 
 
@@ -467,20 +488,16 @@ def cache_scores(h: Handle, q, lse, cache: KVCache, cache_len, scores, count=Non
                  stream=None):
     """Adds to scores fp32 [B, kv_heads, ld] the attention weight that each cached position received from the
     accepted nodes (q and lse as in tree_attention, count and path as in cache_commit) -> scores."""
-    B, T, heads, dim = _rows("q", q, None, cache.dim)
-    _need(cache.batch >= B, "cache: fewer sequences than q")
-    _vec("lse", lse, torch.float32, (B, T, heads))
-    _vec("cache_len", cache_len, torch.int32, (B,))
+    dim = cache.dim
+    B, T, heads, _ = _rows("q", q, None, dim)
+    _cache_for(cache, B)
     ld = scores.shape[-1]
-    _vec("scores", scores, torch.float32, (B, cache.heads, ld))
-    if count is not None:
-        _vec("count", count, torch.int32, (B,))
-    if path is not None:
-        _vec("path", path, torch.int32, (B, T))
     s = q.stride()
-    _check(h._lib.dflash2_cache_scores(h.ptr, _ptr(q), s[0], s[1], s[2], _ptr(lse), cache.ref, _ptr(cache_len),
-                                       _ptr(count), _ptr(path), B, T, heads, dim ** -0.5 if scale is None else scale,
-                                       _ptr(scores), ld, _stream(stream)), "dflash2_cache_scores")
+    _check(h._lib.dflash2_cache_scores(
+        h._h, q.data_ptr(), s[0], s[1], s[2], _dense("lse", lse, _F32, (B, T, heads)), cache.ref,
+        _dense("cache_len", cache_len, _I32, (B,)), _opt("count", count, _I32, (B,)), _opt("path", path, _I32, (B, T)),
+        B, T, heads, dim ** -0.5 if scale is None else scale, _dense("scores", scores, _F32, (B, cache.heads, ld)), ld,
+        _raw_stream(h, stream)), "dflash2_cache_scores")
     return scores
 
 
@@ -490,29 +507,25 @@ def cache_evict(h: Handle, scores, cache: KVCache, cache_len, dst: KVCache, keep
     (kept int32 [B, kv_heads, keep], new_len int32 [B], dst_scores fp32 [B, kv_heads, keep] or None).
 
     scores fp32 [B, kv_heads, ld]; dst's pages must be none of the source's."""
+    heads = cache.heads
     B, ld = scores.shape[0], scores.shape[-1]
-    _vec("scores", scores, torch.float32, (B, cache.heads, ld))
-    _need(cache.batch >= B and dst.batch >= B, "cache, dst: fewer sequences than scores")
-    _vec("cache_len", cache_len, torch.int32, (B,))
-    shape = (B, cache.heads, keep)
+    _cache_for(cache, B)
+    _cache_for(dst, B)
+    shape = (B, heads, max(keep, 0))
     if kept is None:
-        kept = _new_on(stream, shape, torch.int32, scores.device)
-    else:
-        _vec("kept", kept, torch.int32, shape)
+        kept = _new_on(stream, shape, _I32, scores.device)
     if new_len is None:
-        new_len = _new_on(stream, (B,), torch.int32, scores.device)
-    else:
-        _vec("new_len", new_len, torch.int32, (B,))
-    dst_ld = keep
+        new_len = _new_on(stream, (B,), _I32, scores.device)
+    if dst_scores is None and want_scores:
+        dst_scores = _new_on(stream, shape, _F32, scores.device)
+    dst_ld, dp = keep, None
     if dst_scores is not None:
         dst_ld = dst_scores.shape[-1]
-        _need(dst_ld >= keep, "dst_scores: [B, kv_heads, at least keep]")
-        _vec("dst_scores", dst_scores, torch.float32, (B, cache.heads, dst_ld))
-    elif want_scores:
-        dst_scores = _new_on(stream, shape, torch.float32, scores.device)
-    _check(h._lib.dflash2_cache_evict(h.ptr, _ptr(scores), ld, cache.ref, _ptr(cache_len), dst.ref, B, keep, recent,
-                                      _ptr(kept), _ptr(new_len), _ptr(dst_scores), dst_ld, _stream(stream)),
-           "dflash2_cache_evict")
+        dp = _dense("dst_scores", dst_scores, _F32, (B, heads, dst_ld))
+    _check(h._lib.dflash2_cache_evict(
+        h._h, _dense("scores", scores, _F32, (B, heads, ld)), ld, cache.ref,
+        _dense("cache_len", cache_len, _I32, (B,)), dst.ref, B, keep, recent, _dense("kept", kept, _I32, shape),
+        _dense("new_len", new_len, _I32, (B,)), dp, dst_ld, _raw_stream(h, stream)), "dflash2_cache_evict")
     return kept, new_len, dst_scores
 
 
