@@ -2,6 +2,7 @@
 // smaller cache: the commit of an accepted path, and eviction.
 #include "attn.h"
 #include "launch.h"
+#include "tcgen05.cuh"
 
 namespace dflash2 {
 namespace {
@@ -33,106 +34,236 @@ __global__ void __launch_bounds__(256) cache_commit_kernel(const CommitArgs a, i
 }
 
 // ---------------------------------------------------------------------------
-// eviction, step 1: which positions stay.  One CTA per (b, h).  The r-th largest
-// key (order-preserving image of the score) among the positions before the
-// recent ones is found digit by digit from the top (a histogram of 256 digits
-// per pass); then positions are listed in order: those above it, the first ones
-// equal to it, and the recent ones.
+// eviction, step 1: which positions stay.  A cluster of CTAs per (b, h), each
+// with a contiguous slice of its positions.  The r-th largest key (the
+// order-preserving image of the score) among the positions before the recent
+// ones is found in three digits from the top (11, 11 and 10 bits): each CTA counts
+// its slice's keys that share the digits so far by their next digit, the cluster
+// adds the counts through distributed shared memory, and every CTA finds the
+// digit that the r-th key has.  Then the kept positions are listed in order: those
+// above that key, the first ones equal to it, and the recent ones; a warp takes
+// consecutive positions, and its place in the list is the number kept before them.
+// The scores are read once: a slice's keys stay in shared memory (slices of more
+// than kSelKeys positions are read again by each step).
 // ---------------------------------------------------------------------------
 constexpr int kSelThreads = 1024;
+constexpr int kSelWarps = kSelThreads / 32;
+constexpr int kSelBins = 2048;
+constexpr int kSelKeys = 45056;          // 176 KB of keys
+constexpr int kSelMaxCluster = 8;
 
-__global__ void __launch_bounds__(kSelThreads) evict_select_kernel(const EvictArgs a) {
-  __shared__ uint32_t hist[256];
-  __shared__ uint32_t s_prefix, s_need, warp_sel[32], warp_eq[32];
-  const int h = blockIdx.x % a.cache.heads;
-  const int64_t b = blockIdx.x / a.cache.heads;
+struct SelSmem {
+  uint32_t hist[2][kSelBins];            // by turns: a CTA may still read the last one when the next is filled
+  uint32_t warp_sum[kSelWarps];
+  uint32_t gt[kSelWarps], eq[kSelWarps]; // per warp: positions above the threshold (or recent), and equal to it
+  uint32_t all_gt, all_eq;               // this CTA's
+  uint32_t digit, need;
+};
+
+// The word at `p` of cluster CTA `rank`'s shared memory.
+__device__ __forceinline__ uint32_t ld_cluster(const uint32_t* p, uint32_t rank) {
+  uint32_t at, v;
+  asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(at) : "r"(smem_addr(p)), "r"(rank));
+  asm volatile("ld.shared::cluster.u32 %0, [%1];" : "=r"(v) : "r"(at) : "memory");
+  return v;
+}
+
+__global__ void __launch_bounds__(kSelThreads, 1) evict_select_kernel(const EvictArgs a, int cluster, int key_slots) {
+  extern __shared__ __align__(16) uint8_t sel_smem[];
+  SelSmem& s = *reinterpret_cast<SelSmem*>(sel_smem);
+  uint32_t* keys = reinterpret_cast<uint32_t*>(sel_smem + sizeof(SelSmem));
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const uint32_t rank = blockIdx.x % cluster;
+  const int64_t row = blockIdx.x / cluster;
+  const int64_t b = row / a.cache.heads;
+  pdl_wait();
+  pdl_launch_dependents();
   const int32_t limit = static_cast<int32_t>(imin64(a.cache.capacity, a.scores_ld));
   const int32_t n = kv_clamp(a.cache_len[b], limit, a.err);
   const int32_t kept_n = n < a.keep ? n : a.keep;
-  int32_t* kept = a.kept + (b * a.cache.heads + h) * a.keep;
-  const float* sc = a.scores + (b * a.cache.heads + h) * a.scores_ld;
-  if (h == 0 && tid == 0) a.new_len[b] = kept_n;
-  for (int i = kept_n + tid; i < a.keep; i += kSelThreads) kept[i] = -1;
-  if (n <= a.keep) {
-    for (int i = tid; i < n; i += kSelThreads) kept[i] = i;
+  int32_t* kept = a.kept + row * a.keep;
+  const float* sc = a.scores + row * a.scores_ld;
+  if (row % a.cache.heads == 0 && rank == 0 && tid == 0) a.new_len[b] = kept_n;
+  const int first = static_cast<int>(rank) * kSelThreads + tid, step = cluster * kSelThreads;
+  for (int64_t i = kept_n + static_cast<int64_t>(first); i < a.keep; i += step) kept[i] = -1;
+  if (n <= a.keep) {                     // the whole cluster leaves together
+    for (int64_t i = first; i < n; i += step) kept[i] = static_cast<int32_t>(i);
     return;
   }
-  const int32_t m = n - a.recent;
-  if (tid == 0) {
-    s_prefix = 0;
-    s_need = a.keep - a.recent;
+  const int32_t m = n - a.recent;        // candidates: positions [0, m)
+  // warps take consecutive groups of 32 positions
+  const int32_t groups = (n + 31) >> 5;
+  const int32_t per_warp = (groups + cluster * kSelWarps - 1) / (cluster * kSelWarps);
+  const int32_t g0 = static_cast<int32_t>(rank) * kSelWarps * per_warp;       // the CTA's first group
+  const int32_t w0 = min(groups, g0 + warp * per_warp), w1 = min(groups, w0 + per_warp);
+  const bool held = per_warp * kSelThreads <= key_slots;
+  const auto key_at = [&](int32_t group) -> uint32_t {
+    const int32_t j = group * 32 + lane;
+    if (held) return keys[(group - g0) * 32 + lane];
+    return j < m ? score_order(sc[j]) : 0u;
+  };
+
+  uint32_t prefix = 0, need = static_cast<uint32_t>(a.keep - a.recent);
+  const int rounds = need > 0 ? 3 : 0;
+  if (need == 0) prefix = 0xFFFFFFFFu;   // only the recent ones stay: no key is above this one
+#pragma unroll 1
+  for (int round = 0; round < rounds; ++round) {
+    const int shift = round == 0 ? 21 : round == 1 ? 10 : 0;
+    const int bits = round == 2 ? 10 : 11;
+    uint32_t* hist = s.hist[round & 1];
+    for (int x = tid; x < kSelBins; x += kSelThreads) hist[x] = 0;
+    __syncthreads();
+    if (round == 0) {
+#pragma unroll 4
+      for (int32_t g = w0; g < w1; ++g) {
+        const int32_t j = g * 32 + lane;
+        const uint32_t key = j < m ? score_order(__ldg(sc + j)) : 0u;
+        if (held) keys[(g - g0) * 32 + lane] = key;
+        if (j < m) atomicAdd(&hist[key >> 21], 1u);
+      }
+    } else {
+#pragma unroll 4
+      for (int32_t g = w0; g < w1; ++g) {
+        const uint32_t key = key_at(g);
+        if (g * 32 + lane < m && key >> (shift + bits) == prefix >> (shift + bits))
+          atomicAdd(&hist[key >> shift & ((1u << bits) - 1)], 1u);
+      }
+    }
+    __syncthreads();
+    if (cluster > 1) {
+      cluster_arrive();
+      cluster_wait();
+    }
+    // thread t adds up bins 2 t and 2 t + 1 over the cluster; a scan from the top
+    // finds the bin that holds the need-th key
+    uint32_t c0 = hist[2 * tid], c1 = hist[2 * tid + 1];
+    if (cluster > 1) {
+      c0 = c1 = 0;
+      for (int r = 0; r < cluster; ++r) {
+        c0 += ld_cluster(&hist[2 * tid], r);
+        c1 += ld_cluster(&hist[2 * tid + 1], r);
+      }
+    }
+    const uint32_t own = c0 + c1;
+    uint32_t incl = own;                 // over lanes, from the top lane down
+#pragma unroll
+    for (int d = 1; d < 32; d <<= 1) {
+      const uint32_t o = __shfl_down_sync(0xFFFFFFFFu, incl, d);
+      if (lane + d < 32) incl += o;
+    }
+    if (lane == 0) s.warp_sum[warp] = incl;
+    __syncthreads();
+    uint32_t above = incl - own;         // keys in higher bins
+    for (int w = warp + 1; w < kSelWarps; ++w) above += s.warp_sum[w];
+    if (above < need && above + own >= need) {
+      const bool high = above + c1 >= need;
+      s.digit = 2 * tid + (high ? 1 : 0);
+      s.need = need - above - (high ? 0 : c1);
+    }
+    __syncthreads();
+    prefix |= s.digit << shift;
+    need = s.need;                       // how many of the keys that share the prefix stay
+  }
+
+  // counts per warp, their sums per CTA, and the CTAs before this one
+  uint32_t gt = 0, eq = 0;
+#pragma unroll 4
+  for (int32_t g = w0; g < w1; ++g) {
+    const int32_t j = g * 32 + lane;
+    const uint32_t key = key_at(g);
+    gt += __popc(__ballot_sync(0xFFFFFFFFu, j < n && (j >= m || key > prefix)));
+    eq += __popc(__ballot_sync(0xFFFFFFFFu, j < m && key == prefix));
+  }
+  if (lane == 0) {
+    s.gt[warp] = gt;
+    s.eq[warp] = eq;
   }
   __syncthreads();
-  for (int shift = 24; shift >= 0; shift -= 8) {
-    if (tid < 256) hist[tid] = 0;
-    __syncthreads();
-    const uint32_t prefix = s_prefix;
-    for (int32_t j = tid; j < m; j += kSelThreads) {
-      const uint32_t key = score_order(sc[j]);
-      if (shift == 24 || key >> (shift + 8) == prefix >> (shift + 8)) atomicAdd(&hist[key >> shift & 255], 1u);
-    }
-    __syncthreads();
-    if (tid == 0) {
-      uint32_t need = s_need;
-      int d = 255;
-      while (d > 0 && hist[d] < need) need -= hist[d--];
-      s_need = need;
-      s_prefix = prefix | static_cast<uint32_t>(d) << shift;
-    }
-    __syncthreads();
+  uint32_t gt_before = 0, eq_before = 0;
+  for (int w = 0; w < warp; ++w) {
+    gt_before += s.gt[w];
+    eq_before += s.eq[w];
   }
-  const uint32_t T = s_prefix;
-  const uint32_t need_eq = s_need;   // how many of the keys equal to T stay
-  uint32_t base_sel = 0, base_eq = 0;
-  for (int32_t j0 = 0; j0 < n; j0 += kSelThreads) {
-    const int32_t j = j0 + tid;
-    const uint32_t key = j < m ? score_order(sc[j]) : 0u;
-    const bool eq = j < m && key == T;
-    const uint32_t eqs = __ballot_sync(0xFFFFFFFFu, eq);
-    if (lane == 0) warp_eq[warp] = __popc(eqs);
-    __syncthreads();
-    uint32_t eq_rank = base_eq + __popc(eqs & ((1u << lane) - 1));
-    uint32_t eq_all = 0;
-    for (int w = 0; w < 32; ++w) {
-      if (w < warp) eq_rank += warp_eq[w];
-      eq_all += warp_eq[w];
+  if (cluster > 1) {
+    if (tid == kSelThreads - 32) {
+      s.all_gt = gt_before + gt;
+      s.all_eq = eq_before + eq;
     }
-    base_eq += eq_all;
-    const bool sel = j < n && (j >= m || key > T || (eq && eq_rank < need_eq));
-    const uint32_t sels = __ballot_sync(0xFFFFFFFFu, sel);
-    if (lane == 0) warp_sel[warp] = __popc(sels);
     __syncthreads();
-    uint32_t rank = base_sel + __popc(sels & ((1u << lane) - 1));
-    uint32_t sel_all = 0;
-    for (int w = 0; w < 32; ++w) {
-      if (w < warp) rank += warp_sel[w];
-      sel_all += warp_sel[w];
+    cluster_arrive();
+    cluster_wait();
+    for (uint32_t r = 0; r < rank; ++r) {
+      gt_before += ld_cluster(&s.all_gt, r);
+      eq_before += ld_cluster(&s.all_eq, r);
     }
-    base_sel += sel_all;
-    if (sel) kept[rank] = j;
-    __syncthreads();
+  }
+#pragma unroll 2
+  for (int32_t g = w0; g < w1; ++g) {
+    const int32_t j = g * 32 + lane;
+    const uint32_t key = key_at(g);
+    const bool is_gt = j < n && (j >= m || key > prefix), is_eq = j < m && key == prefix;
+    const uint32_t gts = __ballot_sync(0xFFFFFFFFu, is_gt), eqs = __ballot_sync(0xFFFFFFFFu, is_eq);
+    const uint32_t below = (1u << lane) - 1;
+    const uint32_t eq_rank = eq_before + __popc(eqs & below);
+    if (is_gt || (is_eq && eq_rank < need))
+      kept[gt_before + __popc(gts & below) + min(eq_rank, need)] = j;
+    gt_before += __popc(gts);
+    eq_before += __popc(eqs);
+  }
+  if (cluster > 1) {                     // nobody leaves while its counts may still be read
+    cluster_arrive();
+    cluster_wait();
   }
 }
 
-// eviction, step 2: the kept rows to the destination.  One thread per 16 bytes.
-__global__ void __launch_bounds__(256) evict_gather_kernel(const EvictArgs a, int vecs) {
-  const int h = blockIdx.x % a.cache.heads;
-  const int64_t b = blockIdx.x / a.cache.heads;
-  const int64_t row = b * a.cache.heads + h;
-  const int piece = threadIdx.x % vecs, step = blockDim.x / vecs;
-  for (int i = blockIdx.y * step + threadIdx.x / vecs; i < a.keep; i += gridDim.y * step) {
-  const int32_t j = a.kept[row * a.keep + i];
-  if (j < 0) return;
-  bool ok, ok_dst;
-  const int64_t src = kv_offset(a.cache, b, j, h, a.err, &ok) + piece * 8;
-  const int64_t dst = kv_offset(a.dst, b, i, h, a.err, &ok_dst) + piece * 8;
-  if (ok_dst) {
-    *reinterpret_cast<uint4*>(a.dst.k + dst) = *reinterpret_cast<const uint4*>(a.cache.k + src);
-    *reinterpret_cast<uint4*>(a.dst.v + dst) = *reinterpret_cast<const uint4*>(a.cache.v + src);
+// eviction, step 2: the kept rows to the destination.  A CTA takes kGatherRows
+// kept positions of one (b, h); a thread has several rows' 16 bytes of K and of V in
+// flight, so that the chain position -> page -> row is walked once for all of them.
+constexpr int kGatherThreads = 256;
+
+template <int D>
+__global__ void __launch_bounds__(kGatherThreads) evict_gather_kernel(const EvictArgs a, int32_t blocks_per_row) {
+  constexpr int kVecs = D / 8, kRowsPerPass = kGatherThreads / kVecs, kPasses = 4;
+  constexpr int kRows = kRowsPerPass * kPasses;
+  const int64_t row = blockIdx.x / blocks_per_row;
+  const int32_t i0 = static_cast<int32_t>(blockIdx.x % blocks_per_row) * kRows;
+  const int h = static_cast<int>(row % a.cache.heads);
+  const int64_t b = row / a.cache.heads;
+  const int piece = threadIdx.x % kVecs;
+  pdl_wait();
+  pdl_launch_dependents();
+  int32_t j[kPasses];
+  int64_t src[kPasses], dst[kPasses];
+  bool ok[kPasses];
+#pragma unroll
+  for (int x = 0; x < kPasses; ++x) {
+    const int32_t i = i0 + x * kRowsPerPass + threadIdx.x / kVecs;
+    j[x] = i < a.keep ? a.kept[row * a.keep + i] : -1;
   }
-  if (a.dst_scores != nullptr && piece == 0) a.dst_scores[row * a.dst_ld + i] = a.scores[row * a.scores_ld + j];
+#pragma unroll
+  for (int x = 0; x < kPasses; ++x) {
+    const int32_t i = i0 + x * kRowsPerPass + threadIdx.x / kVecs;
+    ok[x] = false;
+    if (j[x] >= 0) {
+      bool any;
+      src[x] = kv_offset(a.cache, b, j[x], h, a.err, &any) + piece * 8;
+      dst[x] = kv_offset(a.dst, b, i, h, a.err, &ok[x]) + piece * 8;
+      if (a.dst_scores != nullptr && piece == 0) a.dst_scores[row * a.dst_ld + i] = a.scores[row * a.scores_ld + j[x]];
+    }
   }
+  uint4 k[kPasses], v[kPasses];
+#pragma unroll
+  for (int x = 0; x < kPasses; ++x)
+    if (ok[x]) {
+      k[x] = __ldcs(reinterpret_cast<const uint4*>(a.cache.k + src[x]));
+      v[x] = __ldcs(reinterpret_cast<const uint4*>(a.cache.v + src[x]));
+    }
+#pragma unroll
+  for (int x = 0; x < kPasses; ++x)
+    if (ok[x]) {
+      __stcs(reinterpret_cast<uint4*>(a.dst.k + dst[x]), k[x]);
+      __stcs(reinterpret_cast<uint4*>(a.dst.v + dst[x]), v[x]);
+    }
 }
 
 }  // namespace
@@ -145,14 +276,43 @@ cudaError_t launch_cache_commit(const CommitArgs& a, int64_t head_dim, cudaStrea
   return cudaGetLastError();
 }
 
-cudaError_t launch_cache_evict(const EvictArgs& a, int64_t head_dim, int, cudaStream_t stream) {
-  const int vecs = static_cast<int>(head_dim / 8);
+cudaError_t launch_cache_evict(const EvictArgs& a, int64_t head_dim, int num_sms, cudaStream_t stream) {
   const int64_t rows = a.B * a.cache.heads;
-  evict_select_kernel<<<static_cast<unsigned>(rows), kSelThreads, 0, stream>>>(a);
-  const dim3 grid(static_cast<unsigned>(rows),
-                  static_cast<unsigned>(imin64((static_cast<int64_t>(a.keep) * vecs + 255) / 256, 65535)));
-  evict_gather_kernel<<<grid, 256, 0, stream>>>(a, vecs);
-  return cudaGetLastError();
+  const int64_t limit = imin64(a.cache.capacity, a.scores_ld);
+  // CTAs per row: while they all fit at once and a slice is still some thousand positions
+  int cluster = 1;
+  while (cluster < kSelMaxCluster && rows * cluster * 2 <= num_sms && limit >= 4096 * cluster) cluster *= 2;
+  const int64_t slice = ((limit + 31) / 32 + cluster * kSelWarps - 1) / (cluster * kSelWarps) * kSelThreads;
+  const int key_slots = static_cast<int>(imin64(slice, kSelKeys));
+  const size_t smem = sizeof(SelSmem) + static_cast<size_t>(key_slots) * 4;
+  cudaError_t e = set_smem_limit<evict_select_kernel>(sizeof(SelSmem) + kSelKeys * 4);
+  if (e != cudaSuccess) return e;
+  cudaLaunchAttribute attr[2];
+  attr[0] = pdl_attribute();
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = cluster;
+  attr[1].val.clusterDim.y = 1;
+  attr[1].val.clusterDim.z = 1;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(static_cast<unsigned>(rows * cluster), 1, 1);
+  cfg.blockDim = dim3(kSelThreads, 1, 1);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = stream;
+  cfg.attrs = attr;
+  cfg.numAttrs = 2;
+  e = cudaLaunchKernelEx(&cfg, evict_select_kernel, a, cluster, key_slots);
+  if (e != cudaSuccess) return e;
+  const int vecs = static_cast<int>(head_dim / 8);
+  const int per_cta = kGatherThreads / vecs * 4;
+  // grid.x holds 2^31 - 1 blocks
+  const int64_t blocks = (a.keep + per_cta - 1) / per_cta;
+  if (rows * blocks >= (int64_t(1) << 31)) return cudaErrorInvalidConfiguration;
+  cfg.gridDim = dim3(static_cast<unsigned>(rows * blocks), 1, 1);
+  cfg.blockDim = dim3(kGatherThreads, 1, 1);
+  cfg.dynamicSmemBytes = 0;
+  cfg.numAttrs = 1;
+  return head_dim == 64 ? cudaLaunchKernelEx(&cfg, evict_gather_kernel<64>, a, static_cast<int32_t>(blocks))
+                        : cudaLaunchKernelEx(&cfg, evict_gather_kernel<128>, a, static_cast<int32_t>(blocks));
 }
 
 }  // namespace dflash2
