@@ -46,11 +46,10 @@ __device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
 
 // Cuts the units of B sequences, units(b) * per_seq each, into runs of equal
 // length (at least min_run) and finds the sequence that run `run`'s first unit
-// (at_end = 0) or the unit after its last (at_end = 1) falls into: *out_base =
-// units before that sequence's.  Whole-block.
+// falls into: *out_base = units before that sequence's.  Whole-block.
 template <int kT, class Units>
 __device__ void find_run(const Units& units, int64_t B, int64_t per_seq, int64_t min_run, int64_t run, int64_t runs,
-                         int at_end, int64_t* scan, int64_t* out_u0, int64_t* out_u1, int64_t* out_base,
+                         int64_t* scan, int64_t* out_u0, int64_t* out_u1, int64_t* out_base,
                          int32_t* out_b) {
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int64_t chunk = (B + kT - 1) / kT;
@@ -72,12 +71,11 @@ __device__ void find_run(const Units& units, int64_t B, int64_t per_seq, int64_t
   }
   const int64_t len = imax64((total + runs - 1) / runs, min_run);
   const int64_t u0 = imin64(run * len, total), u1 = imin64(u0 + len, total);
-  const int64_t u = at_end ? u1 : u0;
-  if (u >= before && u < before + sum) {
+  if (u0 >= before && u0 < before + sum) {
     int64_t base = before, b = b_lo;
     for (;; ++b) {
       const int64_t n = units(b) * per_seq;
-      if (u < base + n) break;
+      if (u0 < base + n) break;
       base += n;
     }
     *out_base = base;

@@ -9,28 +9,50 @@ namespace {
 
 // ---------------------------------------------------------------------------
 // commit: node path[b, i] becomes position cache_len[b] + i, for i < count[b].
-// One thread per 16 bytes of a row (of K or of V).  Grid (row blocks, B).
+// A CTA takes (sequence, a few accepted nodes); a thread takes 16 bytes of K and of
+// V of kCommitPieces rows at once, so that the chain path -> page -> row is walked
+// once for all of them.
 // ---------------------------------------------------------------------------
-__global__ void __launch_bounds__(256) cache_commit_kernel(const CommitArgs a, int vecs) {
-  const int64_t b = blockIdx.y;
+constexpr int kCommitThreads = 256, kCommitPieces = 4;
+
+template <int D>
+__global__ void __launch_bounds__(kCommitThreads) cache_commit_kernel(const CommitArgs a, int blocks_per_seq) {
+  constexpr int kVecs = D / 8;
+  const int64_t b = blockIdx.x / blocks_per_seq;
+  const int block = blockIdx.x % blocks_per_seq;
+  pdl_wait();
+  pdl_launch_dependents();
   const int32_t count = a.count == nullptr ? a.T : kv_clamp(a.count[b], a.T, a.err);
   int32_t limit = a.cache.capacity;
   if (a.scores != nullptr && a.scores_ld < limit) limit = static_cast<int32_t>(a.scores_ld);
   const int32_t len = kv_clamp(a.cache_len[b], limit, a.err);
   const int32_t end = kv_clamp(len + count, limit, a.err);
-  if (blockIdx.x == 0 && threadIdx.x == 0) a.new_len[b] = end;
-  const int row = a.cache.heads * vecs;   // 16-byte pieces of one node's K (or V) rows
-  for (int x = blockIdx.x * blockDim.x + threadIdx.x; x < (end - len) * 2 * row; x += gridDim.x * blockDim.x) {
-    const int piece = x % vecs, h = x / vecs % a.cache.heads, kv = x / row & 1, i = x / (2 * row);
+  if (block == 0 && threadIdx.x == 0) a.new_len[b] = end;
+  const int row = a.cache.heads * kVecs;            // 16-byte pieces of one node's K (or V) rows
+  const int x0 = block * kCommitThreads * kCommitPieces + threadIdx.x;
+  if (x0 >= (end - len) * row) return;
+  int64_t dst[kCommitPieces];
+  uint4 k[kCommitPieces], v[kCommitPieces];
+  bool ok[kCommitPieces];
+#pragma unroll
+  for (int y = 0; y < kCommitPieces; ++y) {
+    const int x = x0 + y * kCommitThreads;
+    ok[y] = false;
+    if (x >= (end - len) * row) continue;
+    const int piece = x % kVecs, h = x / kVecs % a.cache.heads, i = x / row;
     const int t = a.path == nullptr ? i : clamp_node(a.path[b * a.T + i], a.T, a.err);
-    bool ok;
-    const int64_t dst = kv_offset(a.cache, b, len + i, h, a.err, &ok) + piece * 8;
     const int64_t src = b * a.new_b + t * a.new_t + h * a.new_h + piece * 8;
-    if (ok)
-      *reinterpret_cast<uint4*>((kv ? a.cache.v : a.cache.k) + dst) =
-          *reinterpret_cast<const uint4*>((kv ? a.v_new : a.k_new) + src);
-    if (a.scores != nullptr && kv == 0 && piece == 0) a.scores[(b * a.cache.heads + h) * a.scores_ld + len + i] = 0.0f;
+    k[y] = *reinterpret_cast<const uint4*>(a.k_new + src);
+    v[y] = *reinterpret_cast<const uint4*>(a.v_new + src);
+    dst[y] = kv_offset(a.cache, b, len + i, h, a.err, &ok[y]) + piece * 8;
+    if (a.scores != nullptr && piece == 0) a.scores[(b * a.cache.heads + h) * a.scores_ld + len + i] = 0.0f;
   }
+#pragma unroll
+  for (int y = 0; y < kCommitPieces; ++y)
+    if (ok[y]) {
+      *reinterpret_cast<uint4*>(a.cache.k + dst[y]) = k[y];
+      *reinterpret_cast<uint4*>(a.cache.v + dst[y]) = v[y];
+    }
 }
 
 // ---------------------------------------------------------------------------
@@ -269,11 +291,18 @@ __global__ void __launch_bounds__(kGatherThreads) evict_gather_kernel(const Evic
 }  // namespace
 
 cudaError_t launch_cache_commit(const CommitArgs& a, int64_t head_dim, cudaStream_t stream) {
-  const int vecs = static_cast<int>(head_dim / 8);
-  const int64_t pieces = static_cast<int64_t>(a.T) * 2 * a.cache.heads * vecs;
-  const dim3 grid(static_cast<unsigned>(imax64(1, imin64((pieces + 255) / 256, 1024))), static_cast<unsigned>(a.B));
-  cache_commit_kernel<<<grid, 256, 0, stream>>>(a, vecs);
-  return cudaGetLastError();
+  const int64_t pieces = static_cast<int64_t>(a.T) * a.cache.heads * (head_dim / 8);
+  const int blocks = static_cast<int>(imax64(1, (pieces + kCommitThreads * kCommitPieces - 1) /
+                                                    (kCommitThreads * kCommitPieces)));
+  cudaLaunchAttribute attr = pdl_attribute();
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(static_cast<unsigned>(a.B * blocks), 1, 1);
+  cfg.blockDim = dim3(kCommitThreads, 1, 1);
+  cfg.stream = stream;
+  cfg.attrs = &attr;
+  cfg.numAttrs = 1;
+  return head_dim == 64 ? cudaLaunchKernelEx(&cfg, cache_commit_kernel<64>, a, blocks)
+                        : cudaLaunchKernelEx(&cfg, cache_commit_kernel<128>, a, blocks);
 }
 
 cudaError_t launch_cache_evict(const EvictArgs& a, int64_t head_dim, int num_sms, cudaStream_t stream) {

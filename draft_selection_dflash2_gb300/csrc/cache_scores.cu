@@ -154,7 +154,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   pdl_wait();
   pdl_launch_dependents();
   tc_fence_before();
-  find_run<kThreads>([&](int64_t b) { return units_of(p, b); }, a.B, a.cache.heads, 1, blockIdx.x, gridDim.x, 0,
+  find_run<kThreads>([&](int64_t b) { return units_of(p, b); }, a.B, a.cache.heads, 1, blockIdx.x, gridDim.x,
                      s.scan, &s.u0, &s.u1, &s.base, &s.b0);
   tc_fence_after();
   const uint32_t tmem = s.tmem;

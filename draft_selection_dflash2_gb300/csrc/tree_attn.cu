@@ -51,6 +51,7 @@ constexpr int kMaxSlots = 10;
 // softmax warps: 128 x 72 + 256 x 216 = 384 x 168.
 constexpr int kLaunchRegs = 168, kLowRegs = 72, kHighRegs = 216;
 static_assert(128 * kLowRegs + 256 * kHighRegs <= kThreads * kLaunchRegs, "register split");
+constexpr int kMaxRuns = 512;           // most CTAs
 constexpr int kMinRun = 1;              // least units per CTA
 constexpr int kTwoTermUnits = 8;        // items of up to so many units carry P in two terms
 constexpr float kRescale = 8.0f;        // log2 of how far P may exceed 1
@@ -84,6 +85,8 @@ struct AttnPlan {
   float c;                  // scale * log2(e)
   float* part;              // [2 * runs][areas][D / 4][128] float4
   float2* part_ml;          // [2 * runs][areas][128] (m, l)
+  int4* cuts;               // per run, of the item that it begins and does not end: sequence, head * pairs + pair,
+                            // the last run with a part of it, the slot of its own part; or x = -1
   int32_t box_rows;         // rows of a K or V box
   uint32_t q_box_bytes;
 };
@@ -250,7 +253,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   pdl_launch_dependents();
   tc_fence_before();
   find_run<kThreads>([&](int64_t b) { return units_of(a, b); }, a.B, static_cast<int64_t>(a.cache.heads) * p.pairs,
-                     kMinRun, blockIdx.x, gridDim.x, 0, s.scan, &s.u0, &s.u1, &s.base, &s.b0);
+                     kMinRun, blockIdx.x, gridDim.x, s.scan, &s.u0, &s.u1, &s.base, &s.b0);
   tc_fence_after();
   const uint32_t tmem = s.tmem;
   Walk walk;
@@ -258,6 +261,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   Segment g;
   bool live = true;
 
+  if (threadIdx.x == 0 && s.u0 == s.u1) p.cuts[blockIdx.x] = make_int4(-1, 0, 0, 0);
   // the softmax warps take the registers that the others leave
   if (warp < 4)
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kLowRegs));
@@ -585,6 +589,13 @@ __global__ void __launch_bounds__(kThreads, 1)
           p.part_ml[(static_cast<int64_t>(slot) * p.areas + area) * kTile + r] = make_float2(m, l);
         }
       }
+      if (threadIdx.x == kTile && walk.u >= walk.u1) {   // the run's last segment
+        const int64_t len = walk.u1 - walk.u_first;
+        p.cuts[blockIdx.x] = g.s == 0 && g.e < g.n
+                                 ? make_int4(g.b, g.h * p.pairs + g.pair,
+                                             static_cast<int>((walk.u1 + g.n - g.e - 1) / len), slot)
+                                 : make_int4(-1, 0, 0, 0);
+      }
       // with one tile only the pipeline that took the drafted tile knows what its rows saw there
       bool fix = bad_seen != 0;
       if (merge) fix = a.k_new != nullptr && g.e == g.n && (s.bad[0] | s.bad[1] | s.bad[2] | s.bad[3]) != 0;
@@ -655,71 +666,94 @@ __global__ void __launch_bounds__(kThreads, 1)
   }
 }
 
-// Adds the parts of the items that runs cut.  CTA (c, y): if the boundary
-// between runs c and c + 1 is the first inside an item, that item's row tile y /
-// (D / 16), columns 16 (y % (D / 16)) on; one row per thread.
+// Adds the parts of the items that runs cut.  Every CTA lists the cut items from
+// the runs' records; a task is one of them, one of its row tiles and 8 columns.
+// Thread (r, y): row r, every kJoinSplit-th part from the y-th on, so that an item
+// of many parts (few heads, a long cache) is read by many threads at once; the
+// kJoinSplit sums are added in order.
+constexpr int kJoinSplit = 4, kJoinThreads = kTile * kJoinSplit, kJoinCols = 8;
+
 template <int D>
-__global__ void __launch_bounds__(kTile) tree_attn_join_kernel(const __grid_constant__ AttnPlan p, int runs) {
-  __shared__ int64_t scan[kTile / 32];
-  __shared__ int64_t s_u0, s_u1, s_base;
-  __shared__ int32_t s_b;
+__global__ void __launch_bounds__(kJoinThreads) tree_attn_join_kernel(const __grid_constant__ AttnPlan p, int runs) {
+  __shared__ int32_t list[kMaxRuns];
+  __shared__ int32_t warp_n[kJoinThreads / 32];
+  __shared__ float s_m[kJoinSplit][kTile];
+  __shared__ float s_o[kJoinSplit][kJoinCols + 1][kTile];
   const AttnArgs& a = p.a;
+  const int tid = threadIdx.x, r = tid & (kTile - 1), y = tid / kTile;
   pdl_wait();
   pdl_launch_dependents();
-  if (threadIdx.x == 0) s_b = -1;
+  const bool cut = tid < runs && p.cuts[tid].x >= 0;
+  const uint32_t cuts = __ballot_sync(0xFFFFFFFFu, cut);
+  if ((tid & 31) == 0) warp_n[tid >> 5] = __popc(cuts);
   __syncthreads();
-  find_run<kTile>([&](int64_t b) { return units_of(a, b); }, a.B, static_cast<int64_t>(a.cache.heads) * p.pairs,
-                  kMinRun, blockIdx.x, runs, 1, scan, &s_u0, &s_u1, &s_base, &s_b);
-  const int64_t u0 = s_u0, u1 = s_u1, len = u1 - u0;
-  if (s_b < 0 || len == 0) return;         // the last run ends everything
-  const int32_t b = s_b;
-  const int64_t n = units_of(a, b);
-  const int64_t item = (u1 - s_base) / n;
-  const int64_t start = s_base + item * n, end = start + n;
-  if (start == u1 || start < u0) return;   // cut at its start, or an earlier boundary's
-  const int pair = static_cast<int>(item % p.pairs), h = static_cast<int>(item / p.pairs);
-  const int tile = blockIdx.y / (D / 16), x = blockIdx.y % (D / 16) * 16;
-  if (2 * pair + tile >= p.row_tiles) return;
-  const int r = threadIdx.x;
-  const int node = (2 * pair + tile) * p.tpt + r / a.group;
-  if (r >= p.tpt * a.group || node >= a.T) return;
-  const int64_t c0 = blockIdx.x, c1 = (end - 1) / len;   // the runs that hold parts
-  const auto part_of = [&](int64_t c) { return 2 * c + (c == c0 && start != u0 ? 1 : 0); };
-  float m = -INFINITY;
-  bool nan = false;
-  for (int64_t c = c0; c <= c1; ++c) {
-    const float2 ml = p.part_ml[(part_of(c) * p.areas + tile) * kTile + r];
-    m = fmaxf(m, ml.x);
-    nan |= ml.y != ml.y;
+  int n = 0, at = __popc(cuts & ((1u << (tid & 31)) - 1));
+  for (int w = 0; w < kJoinThreads / 32; ++w) {
+    if (w < tid >> 5) at += warp_n[w];
+    n += warp_n[w];
   }
-  float l = 0.0f, o[16];
-#pragma unroll
-  for (int y = 0; y < 16; ++y) o[y] = 0.0f;
-  for (int64_t c = c0; c <= c1; ++c) {
-    const int64_t at = part_of(c) * p.areas + tile;
-    const float2 ml = p.part_ml[at * kTile + r];
-    const float f = ml.x == -INFINITY ? 0.0f : exp2_approx(ml.x - m);
-    l += ml.y * f;
-    if (ml.x == -INFINITY) continue;       // it saw nothing (its sums are 0)
-    const float4* src = reinterpret_cast<const float4*>(p.part) + (at * (D / 4) + x / 4) * kTile + r;
-#pragma unroll
-    for (int y = 0; y < 16; y += 4) {
-      const float4 v = src[(y / 4) * kTile];
-      o[y] = fmaf(v.x, f, o[y]);
-      o[y + 1] = fmaf(v.y, f, o[y + 1]);
-      o[y + 2] = fmaf(v.z, f, o[y + 2]);
-      o[y + 3] = fmaf(v.w, f, o[y + 3]);
+  if (cut) list[at] = tid;
+  __syncthreads();
+  constexpr int kGroups = D / kJoinCols;
+  for (int task = blockIdx.x; task < n * p.areas * kGroups; task += gridDim.x) {
+    const int x = task % kGroups * kJoinCols, tile = task / kGroups % p.areas, c0 = list[task / kGroups / p.areas];
+    const int4 d = p.cuts[c0];
+    const int pair = d.y % p.pairs, h = d.y / p.pairs, c1 = d.z;
+    if (2 * pair + tile >= p.row_tiles) continue;
+    const int node = (2 * pair + tile) * p.tpt + r / a.group;
+    const bool row_ok = r < p.tpt * a.group && node < a.T;
+    // a run's first segment leaves its parts in slot 2 c, its last one in 2 c + 1
+    const auto part_of = [&](int c) { return static_cast<int64_t>(c == c0 ? d.w : 2 * c) * p.areas + tile; };
+    float m = -INFINITY;
+    if (row_ok) {
+#pragma unroll 4
+      for (int c = c0 + y; c <= c1; c += kJoinSplit) m = fmaxf(m, p.part_ml[part_of(c) * kTile + r].x);
     }
-  }
-  if (nan) l = NAN;
-  const float inv = l == 0.0f ? 0.0f : 1.0f / l;
-  const int64_t orow = (static_cast<int64_t>(b) * a.T + node) * a.heads + h * a.group + r % a.group;
-  uint4* dst = reinterpret_cast<uint4*>(a.out + orow * D + x);
+    s_m[y][r] = m;
+    __syncthreads();
 #pragma unroll
-  for (int y = 0; y < 16; y += 8)
-    dst[y / 8] = make_uint4(pack_bf16(o[y] * inv, o[y + 1] * inv), pack_bf16(o[y + 2] * inv, o[y + 3] * inv),
-                            pack_bf16(o[y + 4] * inv, o[y + 5] * inv), pack_bf16(o[y + 6] * inv, o[y + 7] * inv));
-  if (x == 0 && a.lse != nullptr) a.lse[orow] = l == 0.0f ? -INFINITY : (m + log2f(l)) * 0.69314718055994531f;
+    for (int w = 0; w < kJoinSplit; ++w) m = fmaxf(m, s_m[w][r]);
+    float l = 0.0f, o[kJoinCols];
+#pragma unroll
+    for (int k = 0; k < kJoinCols; ++k) o[k] = 0.0f;
+    if (row_ok) {
+#pragma unroll 2
+      for (int c = c0 + y; c <= c1; c += kJoinSplit) {
+        const float2 ml = p.part_ml[part_of(c) * kTile + r];
+        const float4* src = reinterpret_cast<const float4*>(p.part) + (part_of(c) * (D / 4) + x / 4) * kTile + r;
+        const bool some = ml.x != -INFINITY;     // else it saw nothing, and its sums are not looked at
+        const float f = some ? exp2_approx(ml.x - m) : 0.0f;
+        l += some ? ml.y * f : (ml.y != ml.y ? ml.y : 0.0f);
+#pragma unroll
+        for (int k = 0; k < kJoinCols; k += 4) {
+          const float4 v = src[(k / 4) * kTile];
+          o[k] = fmaf(some ? v.x : 0.0f, f, o[k]);
+          o[k + 1] = fmaf(some ? v.y : 0.0f, f, o[k + 1]);
+          o[k + 2] = fmaf(some ? v.z : 0.0f, f, o[k + 2]);
+          o[k + 3] = fmaf(some ? v.w : 0.0f, f, o[k + 3]);
+        }
+      }
+    }
+#pragma unroll
+    for (int k = 0; k < kJoinCols; ++k) s_o[y][k][r] = o[k];
+    s_o[y][kJoinCols][r] = l;
+    __syncthreads();
+    if (y == 0 && row_ok) {
+#pragma unroll
+      for (int w = 1; w < kJoinSplit; ++w) {
+        l += s_o[w][kJoinCols][r];
+#pragma unroll
+        for (int k = 0; k < kJoinCols; ++k) o[k] += s_o[w][k][r];
+      }
+      const float inv = l == 0.0f ? 0.0f : 1.0f / l;
+      const int64_t orow = (static_cast<int64_t>(d.x) * a.T + node) * a.heads + h * a.group + r % a.group;
+      *reinterpret_cast<uint4*>(a.out + orow * D + x) =
+          make_uint4(pack_bf16(o[0] * inv, o[1] * inv), pack_bf16(o[2] * inv, o[3] * inv),
+                     pack_bf16(o[4] * inv, o[5] * inv), pack_bf16(o[6] * inv, o[7] * inv));
+      if (x == 0 && a.lse != nullptr) a.lse[orow] = l == 0.0f ? -INFINITY : (m + log2f(l)) * 0.69314718055994531f;
+    }
+    __syncthreads();
+  }
 }
 
 struct Tiling {
@@ -751,9 +785,10 @@ cudaError_t launch(const AttnArgs& a, void* workspace, int num_sms, cudaStream_t
   p.box_rows = paged && c.page_size < kTile ? c.page_size : kTile;
   p.q_box_bytes = static_cast<uint32_t>(t.tpt * a.group) * D * 2;
   const int64_t most = a.B * c.heads * t.pairs * ((static_cast<int64_t>(c.capacity) + kTile - 1) / kTile + 1);
-  const int runs = static_cast<int>(imin64(num_sms, imax64(most, 1)));
+  const int runs = static_cast<int>(imin64(imin64(num_sms, kMaxRuns), imax64(most, 1)));
   p.part = static_cast<float*>(workspace);
   p.part_ml = reinterpret_cast<float2*>(p.part + static_cast<size_t>(2) * num_sms * t.areas * kTile * D);
+  p.cuts = reinterpret_cast<int4*>(p.part_ml + static_cast<size_t>(2) * num_sms * t.areas * kTile);
 
   CUtensorMap tmQ, tmK, tmV, tmKn, tmVn;
   const uint64_t qd[5] = {D, static_cast<uint64_t>(a.group), static_cast<uint64_t>(a.T),
@@ -802,8 +837,10 @@ cudaError_t launch(const AttnArgs& a, void* workspace, int num_sms, cudaStream_t
   cfg.numAttrs = 1;
   e = cudaLaunchKernelEx(&cfg, tree_attn_kernel<D>, tmQ, tmK, tmV, tmKn, tmVn, p);
   if (e != cudaSuccess || runs == 1) return e;
-  cfg.gridDim = dim3(runs - 1, t.areas * (D / 16), 1);
-  cfg.blockDim = dim3(kTile, 1, 1);
+  // one CTA per task up to two per SM; at most runs - 1 items are cut
+  cfg.gridDim = dim3(static_cast<unsigned>(imin64(2 * num_sms, static_cast<int64_t>(runs - 1) * t.areas * (D / kJoinCols))),
+                     1, 1);
+  cfg.blockDim = dim3(kJoinThreads, 1, 1);
   cfg.dynamicSmemBytes = 0;
   return cudaLaunchKernelEx(&cfg, tree_attn_join_kernel<D>, p, runs);
 }
@@ -813,7 +850,8 @@ cudaError_t launch(const AttnArgs& a, void* workspace, int num_sms, cudaStream_t
 size_t tree_attn_workspace_bytes(int64_t, int64_t T, int64_t heads, int64_t kv_heads, int64_t head_dim, int num_sms) {
   const int64_t group = heads / kv_heads;
   if (group > kTile) return 0;
-  return static_cast<size_t>(2) * num_sms * tile_rows(T, group).areas * kTile * (head_dim * 4 + 8);
+  return static_cast<size_t>(2) * num_sms * tile_rows(T, group).areas * kTile * (head_dim * 4 + 8) +
+         static_cast<size_t>(num_sms) * sizeof(int4);
 }
 
 cudaError_t launch_tree_attn(const AttnArgs& a, int64_t head_dim, void* workspace, int num_sms, cudaStream_t stream) {
