@@ -18,14 +18,16 @@
 //   warp 0      TMA producer: the item's query tiles, then each unit's K and V
 //               tiles (128 x D bf16, 128-byte swizzle, one box per page piece,
 //               the lanes issuing in parallel) into a ring.
-//   warps 1, 2  MMA issuers of pipelines 0 and 1: S = Q K^T (128 x 128, fp32 in
-//               TMEM), then O += P V, with P (bf16) read from TMEM where it
-//               replaced S (and, over few keys, what P lost in rounding to bf16).
+//   warps 1, 2  MMA issuers of pipelines 0 and 1: S = Q K^T for 64 keys at a time
+//               (fp32, two 64-column TMEM buffers per pipeline, so that the next
+//               S is computed under a softmax), then O += P V, with P (bf16) read
+//               from TMEM where it replaced S (and, over few keys, what P lost in
+//               rounding to bf16).
 //   warps 4-7, 8-11  softmax of pipelines 0 and 1, one row per thread: S from
 //               TMEM, running maximum m and sum l in base 2, P = 2^(S c - m) back
 //               to TMEM.  O is rescaled only when a row's maximum has risen by
 //               more than 2^8 since m was set (P then stays below 2^8, exact in
-//               scale), so most units never touch O outside the tensor cores.
+//               scale), so most chunks never touch O outside the tensor cores.
 // The two pipelines alternate on the tensor cores: one's softmax runs under the
 // other's products.  With two row tiles in the item each pipeline takes one of
 // them over every unit; with one row tile the pipelines take alternate units of
@@ -46,11 +48,8 @@ namespace dflash2 {
 namespace {
 
 constexpr int kThreads = 384;
+constexpr int kChunk = 64;              // keys of an S product
 constexpr int kMaxSlots = 10;
-// The block is launched with 168 registers a thread; warps 0-3 give some to the
-// softmax warps: 128 x 72 + 256 x 216 = 384 x 168.
-constexpr int kLaunchRegs = 168, kLowRegs = 72, kHighRegs = 216;
-static_assert(128 * kLowRegs + 256 * kHighRegs <= kThreads * kLaunchRegs, "register split");
 constexpr int kMaxRuns = 512;           // most CTAs
 constexpr int kMinRun = 1;              // least units per CTA
 constexpr int kTwoTermUnits = 8;        // items of up to so many units carry P in two terms
@@ -67,7 +66,7 @@ struct Cfg {
 struct AttnSmem {
   uint64_t kv_full[2 * kMaxSlots], kv_empty[kMaxSlots];
   uint64_t q_full, q_empty;
-  uint64_t s_full[2], p_ready[2], pv_done[2], drain;
+  uint64_t s_full[2][2], p_ready[2][2], pv_done[2][2], drain;   // [pipeline][S buffer]
   float2 ml[2][kTile];
   uint32_t bad[4];          // drafted nodes that hold a non-finite value
   int64_t scan[kThreads / 32];
@@ -116,6 +115,13 @@ struct Segment {
   // out below the output's own rounding, over few it does not.
   __device__ __forceinline__ bool two_terms() const { return n <= kTwoTermUnits; }
   __device__ __forceinline__ int count() const { return e - s; }
+  // keys of unit u: cached ones, or (the last unit, with drafted nodes) the nodes
+  __device__ __forceinline__ bool drafted(const AttnArgs& a, int u) const {
+    return a.k_new != nullptr && u == n - 1;
+  }
+  __device__ __forceinline__ int keys(const AttnArgs& a, int u) const {
+    return drafted(a, u) ? a.T : max(0, min(kTile, len - u * kTile));
+  }
   // units that pipeline i takes
   __device__ __forceinline__ int count(int i) const { return tiles == 2 ? e - s : (e - s + 1 - i) >> 1; }
 };
@@ -196,10 +202,10 @@ __device__ __forceinline__ void tmem_st_wait() { asm volatile("tcgen05.wait::st.
 
 __device__ __forceinline__ bool finite_bf16(uint32_t bits) { return (bits & 0x7F80u) != 0x7F80u; }
 
-// Zeroes the rows [from, 128) of a V tile (this thread's share of `threads`).
+// Zeroes the rows [from, to) of a V tile (this thread's share of `threads`).
 template <int D>
-__device__ __forceinline__ void zero_rows(uint8_t* tile, int from, int tid, int threads) {
-  const int n = (kTile - from) * 8;   // 16-byte pieces per column block
+__device__ __forceinline__ void zero_rows(uint8_t* tile, int from, int to, int tid, int threads) {
+  const int n = (to - from) * 8;   // 16-byte pieces per column block
 #pragma unroll
   for (int half = 0; half < Cfg<D>::kHalves; ++half)
     for (int x = tid; x < n; x += threads)
@@ -232,9 +238,11 @@ __global__ void __launch_bounds__(kThreads, 1)
     mbar_init(&s.q_full, 1);
     mbar_init(&s.q_empty, 2);
     for (int i = 0; i < 2; ++i) {
-      mbar_init(&s.s_full[i], 1);
-      mbar_init(&s.p_ready[i], kTile);
-      mbar_init(&s.pv_done[i], 1);
+      for (int buf = 0; buf < 2; ++buf) {
+        mbar_init(&s.s_full[i][buf], 1);
+        mbar_init(&s.p_ready[i][buf], kTile);
+        mbar_init(&s.pv_done[i][buf], 1);
+      }
     }
     mbar_init(&s.drain, 2);
     s.abort_flag = 0;
@@ -262,11 +270,6 @@ __global__ void __launch_bounds__(kThreads, 1)
   bool live = true;
 
   if (threadIdx.x == 0 && s.u0 == s.u1) p.cuts[blockIdx.x] = make_int4(-1, 0, 0, 0);
-  // the softmax warps take the registers that the others leave
-  if (warp < 4)
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kLowRegs));
-  else
-    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kHighRegs));
   if (warp == 0) {
     // ---- producer ----
     uint32_t it = 0;      // K and V tiles so far
@@ -285,13 +288,12 @@ __global__ void __launch_bounds__(kThreads, 1)
                         (2 * g.pair + i) * p.tpt, g.h, g.b, &s.q_full);
       }
       __syncwarp();
-      const int cached = (g.len + kTile - 1) / kTile;
       // lane -> (page piece of the tile, column block)
       const int half = lane % C::kHalves, piece = lane / C::kHalves;
       const int row = piece * p.box_rows;       // first row of the lane's box
       pages.start(a.cache, g.b, g.s, g.len, lane);
       for (int u = g.s; u < g.e; ++u) {
-        const bool drafted = u >= cached && a.k_new != nullptr;
+        const bool drafted = g.drafted(a, u);
         bool has;
         int y = 0, z = g.h, w = g.b;
         uint32_t bytes;
@@ -337,10 +339,10 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int i = warp - 1;
     if (lane == 0) {
       const uint32_t tm_s = tmem + i * kTile, tm_o = tmem + 2 * kTile + i * D;
-      const uint32_t idesc_s = umma_idesc_bf16(128, kTile);
+      const uint32_t idesc_s = umma_idesc_bf16(128, kChunk);
       const uint32_t idesc_o = umma_idesc_bf16(128, D) | (1u << 16);   // B is MN-major
-      uint32_t unit0 = 0;    // units of the segments so far
-      uint32_t n = 0;        // units of this pipeline so far
+      uint32_t unit0 = 0;      // units of the segments so far
+      uint32_t n_s = 0, n_o = 0;   // chunks of this pipeline so far: S issued, O issued
       int seg = 0;
       for (; walk.next(p, &g); ++seg) {
         const int step = g.tiles == 2 ? 1 : 2, off = g.tiles == 2 ? 0 : i;
@@ -348,41 +350,69 @@ __global__ void __launch_bounds__(kThreads, 1)
         wait_live(&s.q_full, seg & 1, &live, abort_flag, a.err);
         if (cnt == 0) mbar_arrive(&s.q_empty);
         const uint32_t q_base = smem_addr(q_smem + (g.tiles == 2 ? i : 0) * C::kTileBytes);
-        for (int j = 0; j < cnt; ++j, ++n) {
-          const uint32_t it = 2 * (unit0 + j * step + off);
-          const uint32_t ks = it % S, vs = (it + 1) % S;
+        // the S product of the segment's next chunk: unit js, chunk cs
+        int js = 0, cs = 0;
+        const auto next_s = [&]() {
+          if (js == cnt) return;
+          const int u = g.s + js * step + off;
+          const uint32_t it = 2 * (unit0 + js * step + off);
+          const int buf = n_s & 1;
           wait_live(tile_bar<S>(s.kv_full, it), tile_parity<S>(it), &live, abort_flag, a.err);
-          // P of the last unit lies in S's columns until its product is done
-          if (n > 0) wait_live(&s.pv_done[i], (n - 1) & 1, &live, abort_flag, a.err);
-          if (!live) continue;
-          tc_fence_after();
-          const uint32_t k_base = smem_addr(ring + ks * C::kTileBytes);
+          // P of the chunk before the last lies in the buffer until its product is done
+          if (n_s >= 2) wait_live(&s.pv_done[i][buf], ((n_s >> 1) - 1) & 1, &live, abort_flag, a.err);
+          const bool last = cs == 1 || g.keys(a, u) <= kChunk;
+          if (live) {
+            tc_fence_after();
+            const uint32_t k_base = smem_addr(ring + (it % S) * C::kTileBytes) + cs * kChunk * 128;
 #pragma unroll
-          for (int k = 0; k < D / 16; ++k) {
-            const uint32_t o = (k >> 2) * kTile * 128 + (k & 3) * 32;
-            umma_bf16(tm_s, umma_desc_sw128(q_base + o), umma_desc_sw128(k_base + o), idesc_s, k > 0 ? 1u : 0u);
+            for (int k = 0; k < D / 16; ++k) {
+              const uint32_t o = (k >> 2) * kTile * 128 + (k & 3) * 32;
+              umma_bf16(tm_s + buf * kChunk, umma_desc_sw128(q_base + o), umma_desc_sw128(k_base + o), idesc_s,
+                        k > 0 ? 1u : 0u);
+            }
+            umma_commit(&s.s_full[i][buf]);
+            if (last) {
+              umma_commit(&s.kv_empty[it % S]);
+              if (g.tiles == 1) umma_commit(&s.kv_empty[it % S]);
+              if (js == cnt - 1) umma_commit(&s.q_empty);
+            }
           }
-          umma_commit(&s.s_full[i]);
-          umma_commit(&s.kv_empty[ks]);
-          if (g.tiles == 1) umma_commit(&s.kv_empty[ks]);
-          if (j == cnt - 1) umma_commit(&s.q_empty);
-          wait_live(&s.p_ready[i], n & 1, &live, abort_flag, a.err);
-          wait_live(tile_bar<S>(s.kv_full, it + 1), tile_parity<S>(it + 1), &live, abort_flag, a.err);
-          if (!live) continue;
-          tc_fence_after();
-          const uint32_t v_base = smem_addr(ring + vs * C::kTileBytes);
+          ++n_s;
+          cs = last ? 0 : 1;
+          js += last ? 1 : 0;
+        };
+        next_s();
+        next_s();
+        for (int j = 0; j < cnt; ++j) {
+          const int u = g.s + j * step + off;
+          const uint32_t it = 2 * (unit0 + j * step + off) + 1;
+          const int chunks = g.keys(a, u) <= kChunk ? 1 : 2;
+          for (int c = 0; c < chunks; ++c, ++n_o) {
+            const int buf = n_o & 1;
+            wait_live(&s.p_ready[i][buf], (n_o >> 1) & 1, &live, abort_flag, a.err);
+            wait_live(tile_bar<S>(s.kv_full, it), tile_parity<S>(it), &live, abort_flag, a.err);
+            if (live) {
+              tc_fence_after();
+              const uint32_t v_base = smem_addr(ring + (it % S) * C::kTileBytes) + c * kChunk * 128;
+              const uint32_t tm_p = tm_s + buf * kChunk;
 #pragma unroll
-          for (int k = 0; k < kTile / 16; ++k)
-            umma_bf16_ts(tm_o, tm_s + k * 8, umma_desc_mn_sw128(v_base + k * 2048, kTile * 128), idesc_o,
-                         (j > 0 || k > 0) ? 1u : 0u);
-          if (g.two_terms()) {
+              for (int k = 0; k < kChunk / 16; ++k)
+                umma_bf16_ts(tm_o, tm_p + k * 8, umma_desc_mn_sw128(v_base + k * 2048, kTile * 128), idesc_o,
+                             (j > 0 || c > 0 || k > 0) ? 1u : 0u);
+              if (g.two_terms()) {
 #pragma unroll
-            for (int k = 0; k < kTile / 16; ++k)
-              umma_bf16_ts(tm_o, tm_s + 64 + k * 8, umma_desc_mn_sw128(v_base + k * 2048, kTile * 128), idesc_o, 1u);
+                for (int k = 0; k < kChunk / 16; ++k)
+                  umma_bf16_ts(tm_o, tm_p + kChunk / 2 + k * 8, umma_desc_mn_sw128(v_base + k * 2048, kTile * 128),
+                               idesc_o, 1u);
+              }
+              umma_commit(&s.pv_done[i][buf]);
+              if (c == chunks - 1) {
+                umma_commit(&s.kv_empty[it % S]);
+                if (g.tiles == 1) umma_commit(&s.kv_empty[it % S]);
+              }
+            }
+            next_s();
           }
-          umma_commit(&s.pv_done[i]);
-          umma_commit(&s.kv_empty[vs]);
-          if (g.tiles == 1) umma_commit(&s.kv_empty[vs]);
         }
         unit0 += g.count();
       }
@@ -395,23 +425,23 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int r = threadIdx.x & (kTile - 1);
     const uint32_t lanes = static_cast<uint32_t>((warp & 3) * 32) << 16;
     const uint32_t tm_s = tmem + i * kTile + lanes, tm_o = tmem + 2 * kTile + lanes;
-    uint32_t unit0 = 0, n = 0;   // units so far: all, this pipeline's
+    uint32_t unit0 = 0, n = 0;   // units so far; this pipeline's chunks so far
     const int t_r = r / a.group;
     for (; walk.next(p, &g);) {
       const int step = g.tiles == 2 ? 1 : 2, off = g.tiles == 2 ? 0 : i;
       const int cnt = g.count(i);
       const int node = (2 * g.pair + (g.tiles == 2 ? i : 0)) * p.tpt + t_r;
       const bool row_ok = r < p.tpt * a.group && node < a.T;
-      const int cached = (g.len + kTile - 1) / kTile;
       const bool two = g.two_terms();
       float m = -INFINITY, l = 0.0f;
       uint32_t vis[4] = {0, 0, 0, 0}, bad_seen = 0;   // the drafted tile's mask; whether a visible node is non-finite
-      for (int j = 0; j < cnt; ++j, ++n) {
+      for (int j = 0; j < cnt; ++j) {
         const int u = g.s + j * step + off;
-        const bool drafted = u >= cached && a.k_new != nullptr;
-        const int valid = drafted ? a.T : min(kTile, g.len - u * kTile);
-        const bool partial_tile = drafted || valid < kTile;
-        wait_live(&s.s_full[i], n & 1, &live, abort_flag, a.err);
+        const bool drafted = g.drafted(a, u);
+        const int valid = g.keys(a, u);
+        const int chunks = valid <= kChunk ? 1 : 2;
+        const bool partial_tile = drafted || valid < chunks * kChunk;
+        wait_live(&s.s_full[i][n & 1], (n >> 1) & 1, &live, abort_flag, a.err);
         if (partial_tile) {
           // what the row sees of the tile, and a V tile without what nobody may see
           const uint32_t it = 2 * (unit0 + j * step + off) + 1;
@@ -463,92 +493,98 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
             for (int w = 0; w < 4; ++w) bad_seen |= vis[w] & s.bad[w];
           } else {
-            zero_rows<D>(v_tile, max(valid, 0), r, kTile);
+            zero_rows<D>(v_tile, valid, chunks * kChunk, r, kTile);
             asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
           }
         }
-        __syncwarp();
-        tc_fence_after();
-        float z[4][32];
-#pragma unroll
-        for (int x = 0; x < 4; ++x) tmem_ld_x32(tm_s + 32 * x, z[x]);
-        tmem_ld_wait();
-#pragma unroll
-        for (int x = 0; x < 4; ++x) pin(z[x]);
-        if (partial_tile) {
-#pragma unroll
-          for (int x = 0; x < 4; ++x)
-#pragma unroll
-            for (int y = 0; y < 32; ++y)
-              if (!(vis[x] >> y & 1u)) z[x][y] = -INFINITY;
-        }
-        float top = -INFINITY;
-#pragma unroll
-        for (int x = 0; x < 4; ++x)
-#pragma unroll
-          for (int y = 0; y < 32; y += 2) top = fmaxf(top, fmaxf(z[x][y], z[x][y + 1]));
-        top *= p.c;
-        if (j == 0) {
-          m = top;
-        } else if (__any_sync(0xFFFFFFFFu, top > m + kRescale)) {
-          // a row's maximum rose far: O and l move to the new one
-          const float m1 = fmaxf(m, top);
-          const float f = m == -INFINITY ? 1.0f : exp2_approx(m - m1);
-          m = m1;
-          l *= f;
-          wait_live(&s.pv_done[i], (n - 1) & 1, &live, abort_flag, a.err);
+#pragma unroll 1
+        for (int c = 0; c < chunks; ++c, ++n) {
+          const int buf = n & 1;
+          const uint32_t tm_sb = tm_s + buf * kChunk;
+          wait_live(&s.s_full[i][buf], (n >> 1) & 1, &live, abort_flag, a.err);
           __syncwarp();
           tc_fence_after();
-#pragma unroll 1
-          for (int x = 0; x < D; x += 32) {
-            float o[32];
-            tmem_ld_x32(tm_o + i * D + x, o);
-            tmem_ld_wait();
-            pin(o);
+          float z[2][32];
+          tmem_ld_x32(tm_sb, z[0]);
+          tmem_ld_x32(tm_sb + 32, z[1]);
+          tmem_ld_wait();
+          pin(z[0]);
+          pin(z[1]);
+          if (partial_tile) {
+            const uint32_t v0 = c ? vis[2] : vis[0], v1 = c ? vis[3] : vis[1];
 #pragma unroll
-            for (int w = 0; w < 32; w += 16) {
-              uint32_t ob[16];
-#pragma unroll
-              for (int y = 0; y < 16; ++y) ob[y] = __float_as_uint(o[w + y] * f);
-              tmem_st_x16(tm_o + i * D + x + w, ob);
+            for (int y = 0; y < 32; ++y) {
+              if (!(v0 >> y & 1u)) z[0][y] = -INFINITY;
+              if (!(v1 >> y & 1u)) z[1][y] = -INFINITY;
             }
           }
-        }
-        const float mm = m == -INFINITY ? 0.0f : m;   // a row that has seen nothing: all its P are 2^-inf
-        const uint64_t c2 = pack2(p.c, p.c), m2 = pack2(-mm, -mm);
-        uint64_t sum0 = pack2(0.0f, 0.0f), sum1 = sum0;
+          float top = -INFINITY;
 #pragma unroll
-        for (int x = 0; x < 4; ++x) {
-          uint32_t hi[16];
+          for (int y = 0; y < 32; ++y) top = fmaxf(top, fmaxf(z[0][y], z[1][y]));
+          top *= p.c;
+          if (j == 0 && c == 0) {
+            m = top;
+          } else if (__any_sync(0xFFFFFFFFu, row_ok && top > m + kRescale)) {
+            // a row's maximum rose far: the warp's O and l move to the new ones (rows of the
+            // tile that are no query's hold whatever shared memory held, and have no say)
+            const float m1 = fmaxf(m, top);
+            const float f = m == -INFINITY ? 1.0f : exp2_approx(m - m1);
+            m = m1;
+            l *= f;
+            wait_live(&s.pv_done[i][buf ^ 1], ((n - 1) >> 1) & 1, &live, abort_flag, a.err);
+            __syncwarp();
+            tc_fence_after();
+#pragma unroll 1
+            for (int x = 0; x < D; x += 32) {
+              float o[32];
+              tmem_ld_x32(tm_o + i * D + x, o);
+              tmem_ld_wait();
+              pin(o);
 #pragma unroll
-          for (int y = 0; y < 32; y += 4) {
-            const float2 e0 = unpack2(fma2(pack2(z[x][y], z[x][y + 1]), c2, m2));
-            const float2 e1 = unpack2(fma2(pack2(z[x][y + 2], z[x][y + 3]), c2, m2));
-            z[x][y] = exp2_approx(e0.x);
-            z[x][y + 1] = exp2_approx(e0.y);
-            z[x][y + 2] = exp2_approx(e1.x);
-            z[x][y + 3] = exp2_approx(e1.y);
-            sum0 = add2(sum0, pack2(z[x][y], z[x][y + 1]));
-            sum1 = add2(sum1, pack2(z[x][y + 2], z[x][y + 3]));
-            hi[y / 2] = pack_bf16(z[x][y], z[x][y + 1]);
-            hi[y / 2 + 1] = pack_bf16(z[x][y + 2], z[x][y + 3]);
+              for (int w = 0; w < 32; w += 16) {
+                uint32_t ob[16];
+#pragma unroll
+                for (int y = 0; y < 16; ++y) ob[y] = __float_as_uint(o[w + y] * f);
+                tmem_st_x16(tm_o + i * D + x + w, ob);
+              }
+            }
           }
-          tmem_st_x16(tm_s + 16 * x, hi);
-        }
-        if (two) {
+          const float mm = m == -INFINITY ? 0.0f : m;   // a row that has seen nothing: all its P are 2^-inf
+          const uint64_t c2 = pack2(p.c, p.c), m2 = pack2(-mm, -mm);
+          uint64_t sum0 = pack2(0.0f, 0.0f), sum1 = sum0;
 #pragma unroll
-          for (int x = 0; x < 4; ++x) {
-            uint32_t lo[16];
+          for (int x = 0; x < 2; ++x) {
+            uint32_t hi[16];
 #pragma unroll
-            for (int y = 0; y < 32; y += 2) lo[y / 2] = remainder_bf16(z[x][y], z[x][y + 1]);
-            tmem_st_x16(tm_s + 64 + 16 * x, lo);
+            for (int y = 0; y < 32; y += 4) {
+              const float2 e0 = unpack2(fma2(pack2(z[x][y], z[x][y + 1]), c2, m2));
+              const float2 e1 = unpack2(fma2(pack2(z[x][y + 2], z[x][y + 3]), c2, m2));
+              z[x][y] = exp2_approx(e0.x);
+              z[x][y + 1] = exp2_approx(e0.y);
+              z[x][y + 2] = exp2_approx(e1.x);
+              z[x][y + 3] = exp2_approx(e1.y);
+              sum0 = add2(sum0, pack2(z[x][y], z[x][y + 1]));
+              sum1 = add2(sum1, pack2(z[x][y + 2], z[x][y + 3]));
+              hi[y / 2] = pack_bf16(z[x][y], z[x][y + 1]);
+              hi[y / 2 + 1] = pack_bf16(z[x][y + 2], z[x][y + 3]);
+            }
+            tmem_st_x16(tm_sb + 16 * x, hi);
           }
+          if (two) {
+#pragma unroll
+            for (int x = 0; x < 2; ++x) {
+              uint32_t lo[16];
+#pragma unroll
+              for (int y = 0; y < 32; y += 2) lo[y / 2] = remainder_bf16(z[x][y], z[x][y + 1]);
+              tmem_st_x16(tm_sb + kChunk / 2 + 16 * x, lo);
+            }
+          }
+          const float2 sum = unpack2(add2(sum0, sum1));
+          l += sum.x + sum.y;
+          tmem_st_wait();
+          tc_fence_before();
+          mbar_arrive(&s.p_ready[i][buf]);
         }
-        const float2 sum = unpack2(add2(sum0, sum1));
-        l += sum.x + sum.y;
-        tmem_st_wait();
-        tc_fence_before();
-        mbar_arrive(&s.p_ready[i]);
       }
       unit0 += g.count();
 
@@ -557,7 +593,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       const int slot = 2 * blockIdx.x + (g.first ? 0 : 1);
       const bool merge = g.tiles == 1;
       float f0 = 1.0f, f1 = 0.0f;     // weights of O0 and O1 (one tile), or of O_i
-      if (cnt > 0) wait_live(&s.pv_done[i], (n - 1) & 1, &live, abort_flag, a.err);
+      // products complete in the order of their issue: the last one's is enough
+      if (cnt > 0) wait_live(&s.pv_done[i][(n - 1) & 1], ((n - 1) >> 1) & 1, &live, abort_flag, a.err);
       __syncwarp();
       if (merge) {
         // each pipeline has waited for its own products
@@ -818,12 +855,6 @@ cudaError_t launch(const AttnArgs& a, void* workspace, int num_sms, cudaStream_t
       return cudaErrorInvalidValue;
   }
 
-  // the register split must not exceed what the block is launched with (it would wait forever)
-  static const int regs = [] {
-    cudaFuncAttributes fa;
-    return cudaFuncGetAttributes(&fa, tree_attn_kernel<D>) == cudaSuccess ? fa.numRegs : 0;
-  }();
-  if (regs < kLaunchRegs) return cudaErrorInvalidConfiguration;
   const size_t smem = C::kRing + sizeof(AttnSmem);
   cudaError_t e = set_smem_limit<tree_attn_kernel<D>>(smem);
   if (e != cudaSuccess) return e;
