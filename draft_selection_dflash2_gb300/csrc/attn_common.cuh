@@ -181,6 +181,70 @@ struct PageFeed {
   }
 };
 
+// Lane 0's value, which the compiler then knows to be the whole warp's.
+template <class T>
+__device__ __forceinline__ T uniform(T x) {
+  return __shfl_sync(0xFFFFFFFFu, x, 0);
+}
+
+// Products are issued by whole warps of which one elected lane acts: the code
+// around them stays warp-uniform, so operands are computed in uniform registers,
+// and a product costs a few instructions instead of the tens that one lane alone
+// takes (a batch of 8 + 4 products beside busy softmax warps: 876 against 1160
+// cycles).
+__device__ __forceinline__ uint32_t elect_lane() {
+  uint32_t p;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "elect.sync _|p, 0xFFFFFFFF;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(p));
+  return p;
+}
+
+// The words of a shared-memory matrix descriptor with the 128-byte swizzle: the
+// address and leading offset change, the rest (stride offset 1024, version 1,
+// swizzle mode 2) does not.  A K-major operand's leading offset is not used (1); an
+// MN-major one's is the distance between its 64-element column blocks.
+constexpr uint32_t kDescHi = (1024 >> 4) | (1u << 14) | (2u << 29);
+__device__ __forceinline__ uint32_t desc_lo(uint32_t saddr, uint32_t leading = 16) {
+  return ((saddr & 0x3FFFFu) >> 4) | ((leading >> 4) << 16);
+}
+
+// D[tmem] (+)= A[smem] * B[smem]^T and D[tmem] (+)= A[tmem] * B[smem], one K = 16
+// step, by the lane whose `lead` is set.  A in TMEM is 128 rows of 16 bf16 (8 columns).
+__device__ __forceinline__ void umma_ss(uint32_t d, uint32_t a_lo, uint32_t b_lo, uint32_t idesc, uint32_t accumulate,
+                                        uint32_t lead) {
+  asm volatile(
+      "{\n\t.reg .pred p, q;\n\t.reg .b64 x, y;\n\t"
+      "setp.ne.b32 p, %5, 0;\n\t"
+      "setp.ne.b32 q, %6, 0;\n\t"
+      "mov.b64 x, {%1, %3};\n\t"
+      "mov.b64 y, {%2, %3};\n\t"
+      "@q tcgen05.mma.cta_group::1.kind::f16 [%0], x, y, %4, p;\n\t}" ::"r"(d),
+      "r"(a_lo), "r"(b_lo), "r"(kDescHi), "r"(idesc), "r"(accumulate), "r"(lead)
+      : "memory");
+}
+__device__ __forceinline__ void umma_ts(uint32_t d, uint32_t a_tmem, uint32_t b_lo, uint32_t idesc, uint32_t accumulate,
+                                        uint32_t lead) {
+  asm volatile(
+      "{\n\t.reg .pred p, q;\n\t.reg .b64 y;\n\t"
+      "setp.ne.b32 p, %5, 0;\n\t"
+      "setp.ne.b32 q, %6, 0;\n\t"
+      "mov.b64 y, {%2, %3};\n\t"
+      "@q tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], y, %4, p;\n\t}" ::"r"(d),
+      "r"(a_tmem), "r"(b_lo), "r"(kDescHi), "r"(idesc), "r"(accumulate), "r"(lead)
+      : "memory");
+}
+__device__ __forceinline__ void umma_commit_if(uint64_t* bar, uint32_t lead) {
+  asm volatile(
+      "{\n\t.reg .pred q;\n\t"
+      "setp.ne.b32 q, %1, 0;\n\t"
+      "@q tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n\t}" ::"r"(smem_addr(bar)),
+      "r"(lead)
+      : "memory");
+}
+
 // Keeps uses of loaded values after the wait that precedes this in the program.
 __device__ __forceinline__ void pin(float (&v)[32]) {
 #pragma unroll

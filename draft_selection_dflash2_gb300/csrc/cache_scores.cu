@@ -65,18 +65,19 @@ struct Segment {
   int32_t len, rows;
 };
 
+// Walks a run's segments; each warp keeps its own (whole warps call it).
 struct Walk {
   int64_t u, u1, base, n_seq;
   int32_t b, n;
   __device__ __forceinline__ void start(const ScoresPlan& p, const ScoresSmem& s) {
-    u = s.u0;
-    u1 = s.u1;
-    base = s.base;
-    b = s.b0;
+    u = uniform(s.u0);
+    u1 = uniform(s.u1);
+    base = uniform(s.base);
+    b = uniform(s.b0);
     if (u < u1) load(p);
   }
   __device__ __forceinline__ void load(const ScoresPlan& p) {
-    n = static_cast<int32_t>(units_of(p, b));
+    n = static_cast<int32_t>(uniform(units_of(p, b)));
     n_seq = static_cast<int64_t>(n) * p.a.cache.heads;
   }
   __device__ __forceinline__ bool next(const ScoresPlan& p, Segment* g) {
@@ -91,8 +92,8 @@ struct Walk {
     g->s = static_cast<int32_t>(rel % n);
     g->e = static_cast<int32_t>(imin64(n, g->s + (u1 - u)));
     g->b = b;
-    g->len = kv_clamp(p.a.cache_len[b], p.limit, nullptr);
-    g->rows = rows_of(p, b);
+    g->len = uniform(kv_clamp(p.a.cache_len[b], p.limit, nullptr));
+    g->rows = uniform(rows_of(p, b));
     u += g->e - g->s;
     return true;
   }
@@ -129,7 +130,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   const int S = p.slots;
   uint8_t* ring = q_smem + p.chunks * kTileBytes;
   ScoresSmem& s = *reinterpret_cast<ScoresSmem*>(ring + S * kTileBytes);
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int warp = uniform(static_cast<int>(threadIdx.x >> 5)), lane = threadIdx.x & 31;
   volatile int* abort_flag = &s.abort_flag;
 
   if (threadIdx.x == 0) {
@@ -157,7 +158,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   find_run<kThreads>([&](int64_t b) { return units_of(p, b); }, a.B, a.cache.heads, 1, blockIdx.x, gridDim.x,
                      s.scan, &s.u0, &s.u1, &s.base, &s.b0);
   tc_fence_after();
-  const uint32_t tmem = s.tmem;
+  const uint32_t tmem = uniform(s.tmem);
   Walk walk;
   walk.start(p, s);
   Segment g;
@@ -198,38 +199,38 @@ __global__ void __launch_bounds__(kThreads, 1)
     __syncwarp();
   } else if (warp == 1) {
     // ---- MMA issuer ----
-    if (lane == 0) {
-      uint32_t it = 0;
-      uint32_t used[2] = {0, 0};    // chunks given to each half of the epilogue so far
-      int seg = 0;
-      for (; walk.next(p, &g); ++seg) {
-        wait_live(&s.q_full, seg & 1, &live, abort_flag, a.err);
-        const int chunks = (g.rows + kTile - 1) / kTile;
-        for (int u = g.s; u < g.e; ++u, ++it) {
-          const int slot = it % S, e = it & 1;
-          wait_live(&s.k_full[slot], (it / S) & 1, &live, abort_flag, a.err);
-          const uint32_t k_base = smem_addr(ring + slot * kTileBytes);
-          for (int c = 0; c < chunks; ++c) {
-            const uint32_t n = used[e]++;
-            const int buf = 2 * e + (n & 1);
-            if (n >= 2) wait_live(&s.s_free[buf], ((n >> 1) - 1) & 1, &live, abort_flag, a.err);
-            if (!live) continue;
-            tc_fence_after();
-            const uint32_t q_base = smem_addr(q_smem + c * kTileBytes);
-            const uint32_t idesc = umma_idesc_bf16(128, chunk_cols(g.rows, c));
+    const uint32_t elected = elect_lane();
+    const uint32_t ring_addr = uniform(smem_addr(ring)), q_addr = uniform(smem_addr(q_smem));
+    uint32_t it = 0;
+    uint32_t used0 = 0, used1 = 0;    // chunks given to each half of the epilogue so far
+    int seg = 0;
+    for (; walk.next(p, &g); ++seg) {
+      wait_live(&s.q_full, seg & 1, &live, abort_flag, a.err);
+      const int chunks = (g.rows + kTile - 1) / kTile;
+      for (int u = g.s; u < g.e; ++u, ++it) {
+        const int slot = it % S, e = it & 1;
+        wait_live(&s.k_full[slot], (it / S) & 1, &live, abort_flag, a.err);
+        const uint32_t k_lo = desc_lo(ring_addr + slot * kTileBytes);
+        for (int c = 0; c < chunks; ++c) {
+          const uint32_t n = e ? used1++ : used0++;
+          const int buf = 2 * e + (n & 1);
+          if (n >= 2) wait_live(&s.s_free[buf], ((n >> 1) - 1) & 1, &live, abort_flag, a.err);
+          __syncwarp();
+          tc_fence_after();
+          const uint32_t lead = live ? elected : 0u;
+          const uint32_t q_lo = desc_lo(q_addr + c * kTileBytes);
+          const uint32_t idesc = umma_idesc_bf16(128, chunk_cols(g.rows, c));
 #pragma unroll
-            for (int k = 0; k < D / 16; ++k) {
-              const uint32_t o = (k >> 2) * kTile * 128 + (k & 3) * 32;
-              umma_bf16(tmem + buf * kTile, umma_desc_sw128(k_base + o), umma_desc_sw128(q_base + o), idesc,
-                        k > 0 ? 1u : 0u);
-            }
-            umma_commit(&s.s_full[buf]);
+          for (int k = 0; k < D / 16; ++k) {
+            const uint32_t o = ((k >> 2) * kTile * 128 + (k & 3) * 32) >> 4;
+            umma_ss(tmem + buf * kTile, k_lo + o, q_lo + o, idesc, k > 0 ? 1u : 0u, lead);
           }
-          if (live) umma_commit(&s.k_empty[slot]);
+          umma_commit_if(&s.s_full[buf], lead);
         }
+        umma_commit_if(&s.k_empty[slot], live ? elected : 0u);
       }
-      umma_commit(&s.drain);
     }
+    umma_commit_if(&s.drain, elected);
     __syncwarp();
   } else if (warp >= 4) {
     // ---- epilogue half e: one key per thread ----

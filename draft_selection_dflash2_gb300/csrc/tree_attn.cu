@@ -126,21 +126,20 @@ struct Segment {
   __device__ __forceinline__ int count(int i) const { return tiles == 2 ? e - s : (e - s + 1 - i) >> 1; }
 };
 
-// Walks a run's segments; each role of the CTA keeps its own.
+// Walks a run's segments; each warp of the CTA keeps its own (whole warps call it).
 struct Walk {
   int64_t u, u1, u_first, base, n_seq;
   int32_t b, n;
   __device__ __forceinline__ void start(const AttnPlan& p, const AttnSmem& s) {
-    u = u_first = s.u0;
-    u1 = s.u1;
-    base = s.base;
-    b = s.b0;
+    u = u_first = uniform(s.u0);
+    u1 = uniform(s.u1);
+    base = uniform(s.base);
+    b = uniform(s.b0);
     if (u < u1) load(p);
   }
   __device__ __forceinline__ void load(const AttnPlan& p) {
-    const int64_t k = units_of(p.a, b);
-    n = static_cast<int32_t>(k);
-    n_seq = k * p.a.cache.heads * p.pairs;
+    n = static_cast<int32_t>(uniform(units_of(p.a, b)));
+    n_seq = static_cast<int64_t>(n) * p.a.cache.heads * p.pairs;
   }
   __device__ __forceinline__ bool next(const AttnPlan& p, Segment* g) {
     if (u >= u1) return false;
@@ -158,37 +157,12 @@ struct Walk {
     g->pair = static_cast<int32_t>(item % p.pairs);
     g->h = static_cast<int32_t>(item / p.pairs);
     g->tiles = min(2, p.row_tiles - 2 * g->pair);
-    g->len = kv_clamp(p.a.cache_len[b], p.a.cache.capacity, nullptr);
+    g->len = uniform(kv_clamp(p.a.cache_len[b], p.a.cache.capacity, nullptr));
     g->first = u == u_first;
     u += g->e - g->s;
     return true;
   }
 };
-
-// D[tmem] (+)= A[tmem] * B[smem]: A is 128 rows of 16 bf16 (8 columns), B is
-// 16 x N with N contiguous (MN-major).
-__device__ __forceinline__ void umma_bf16_ts(uint32_t tmem_d, uint32_t tmem_a, uint64_t bdesc, uint32_t idesc,
-                                             uint32_t accumulate) {
-  asm volatile(
-      "{\n\t.reg .pred p;\n\t"
-      "setp.ne.b32 p, %4, 0;\n\t"
-      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(tmem_d),
-      "r"(tmem_a), "l"(bdesc), "r"(idesc), "r"(accumulate)
-      : "memory");
-}
-
-// Descriptor of an MN-major operand with the 128-byte swizzle: 8 x 64 atoms of
-// 1024 bytes; leading offset = distance between 64-element column blocks, stride
-// offset = distance between groups of 8 rows (K).
-__device__ __forceinline__ uint64_t umma_desc_mn_sw128(uint32_t saddr, uint32_t block_bytes) {
-  uint64_t d = 0;
-  d |= static_cast<uint64_t>((saddr & 0x3FFFFu) >> 4);
-  d |= static_cast<uint64_t>(block_bytes >> 4) << 16;
-  d |= static_cast<uint64_t>(1024 >> 4) << 32;
-  d |= static_cast<uint64_t>(1) << 46;
-  d |= static_cast<uint64_t>(2) << 61;
-  return d;
-}
 
 __device__ __forceinline__ void tmem_st_x16(uint32_t taddr, const uint32_t (&r)[16]) {
   asm volatile(
@@ -226,7 +200,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   uint8_t* ring = q_smem + 2 * C::kTileBytes;
   AttnSmem& s = *reinterpret_cast<AttnSmem*>(q_smem + C::kRing);
   const AttnArgs& a = p.a;
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int warp = uniform(static_cast<int>(threadIdx.x >> 5)), lane = threadIdx.x & 31;
   volatile int* abort_flag = &s.abort_flag;
 
   if (threadIdx.x == 0) {
@@ -263,7 +237,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   find_run<kThreads>([&](int64_t b) { return units_of(a, b); }, a.B, static_cast<int64_t>(a.cache.heads) * p.pairs,
                      kMinRun, blockIdx.x, gridDim.x, s.scan, &s.u0, &s.u1, &s.base, &s.b0);
   tc_fence_after();
-  const uint32_t tmem = s.tmem;
+  const uint32_t tmem = uniform(s.tmem);
   Walk walk;
   walk.start(p, s);
   Segment g;
@@ -337,87 +311,87 @@ __global__ void __launch_bounds__(kThreads, 1)
   } else if (warp <= 2) {
     // ---- MMA issuer of pipeline i ----
     const int i = warp - 1;
-    if (lane == 0) {
-      const uint32_t tm_s = tmem + i * kTile, tm_o = tmem + 2 * kTile + i * D;
-      const uint32_t idesc_s = umma_idesc_bf16(128, kChunk);
-      const uint32_t idesc_o = umma_idesc_bf16(128, D) | (1u << 16);   // B is MN-major
-      uint32_t unit0 = 0;      // units of the segments so far
-      uint32_t n_s = 0, n_o = 0;   // chunks of this pipeline so far: S issued, O issued
-      int seg = 0;
-      for (; walk.next(p, &g); ++seg) {
-        const int step = g.tiles == 2 ? 1 : 2, off = g.tiles == 2 ? 0 : i;
-        const int cnt = g.count(i);
-        wait_live(&s.q_full, seg & 1, &live, abort_flag, a.err);
-        if (cnt == 0) mbar_arrive(&s.q_empty);
-        const uint32_t q_base = smem_addr(q_smem + (g.tiles == 2 ? i : 0) * C::kTileBytes);
-        // the S product of the segment's next chunk: unit js, chunk cs
-        int js = 0, cs = 0;
-        const auto next_s = [&]() {
-          if (js == cnt) return;
-          const int u = g.s + js * step + off;
-          const uint32_t it = 2 * (unit0 + js * step + off);
-          const int buf = n_s & 1;
-          wait_live(tile_bar<S>(s.kv_full, it), tile_parity<S>(it), &live, abort_flag, a.err);
-          // P of the chunk before the last lies in the buffer until its product is done
-          if (n_s >= 2) wait_live(&s.pv_done[i][buf], ((n_s >> 1) - 1) & 1, &live, abort_flag, a.err);
-          const bool last = cs == 1 || g.keys(a, u) <= kChunk;
-          if (live) {
-            tc_fence_after();
-            const uint32_t k_base = smem_addr(ring + (it % S) * C::kTileBytes) + cs * kChunk * 128;
+    const uint32_t elected = elect_lane();
+    const uint32_t tm_s = tmem + i * kTile, tm_o = tmem + 2 * kTile + i * D;
+    const uint32_t idesc_s = umma_idesc_bf16(128, kChunk);
+    const uint32_t idesc_o = umma_idesc_bf16(128, D) | (1u << 16);   // B is MN-major
+    const uint32_t ring_addr = uniform(smem_addr(ring)), q_addr = uniform(smem_addr(q_smem));
+    uint32_t unit0 = 0;          // units of the segments so far
+    uint32_t n_s = 0, n_o = 0;   // chunks of this pipeline so far: S issued, O issued
+    int seg = 0;
+    for (; walk.next(p, &g); ++seg) {
+      const int step = g.tiles == 2 ? 1 : 2, off = g.tiles == 2 ? 0 : i;
+      const int cnt = g.count(i);
+      wait_live(&s.q_full, seg & 1, &live, abort_flag, a.err);
+      __syncwarp();
+      if (cnt == 0 && elected) mbar_arrive(&s.q_empty);
+      const uint32_t q_lo = desc_lo(q_addr + (g.tiles == 2 ? i : 0) * C::kTileBytes);
+      // the S product of the segment's next chunk: unit js, chunk cs
+      int js = 0, cs = 0;
+      const auto next_s = [&]() {
+        if (js == cnt) return;
+        const int u = g.s + js * step + off;
+        const uint32_t it = 2 * (unit0 + js * step + off);
+        const uint32_t slot = it % S;
+        const int buf = n_s & 1;
+        wait_live(tile_bar<S>(s.kv_full, it), tile_parity<S>(it), &live, abort_flag, a.err);
+        // P of the chunk before the last lies in the buffer until its product is done
+        if (n_s >= 2) wait_live(&s.pv_done[i][buf], ((n_s >> 1) - 1) & 1, &live, abort_flag, a.err);
+        __syncwarp();
+        tc_fence_after();
+        const bool last = cs == 1 || g.keys(a, u) <= kChunk;
+        const uint32_t lead = live ? elected : 0u;
+        const uint32_t k_lo = desc_lo(ring_addr + slot * C::kTileBytes + cs * kChunk * 128);
 #pragma unroll
-            for (int k = 0; k < D / 16; ++k) {
-              const uint32_t o = (k >> 2) * kTile * 128 + (k & 3) * 32;
-              umma_bf16(tm_s + buf * kChunk, umma_desc_sw128(q_base + o), umma_desc_sw128(k_base + o), idesc_s,
-                        k > 0 ? 1u : 0u);
-            }
-            umma_commit(&s.s_full[i][buf]);
-            if (last) {
-              umma_commit(&s.kv_empty[it % S]);
-              if (g.tiles == 1) umma_commit(&s.kv_empty[it % S]);
-              if (js == cnt - 1) umma_commit(&s.q_empty);
-            }
-          }
-          ++n_s;
-          cs = last ? 0 : 1;
-          js += last ? 1 : 0;
-        };
-        next_s();
-        next_s();
-        for (int j = 0; j < cnt; ++j) {
-          const int u = g.s + j * step + off;
-          const uint32_t it = 2 * (unit0 + j * step + off) + 1;
-          const int chunks = g.keys(a, u) <= kChunk ? 1 : 2;
-          for (int c = 0; c < chunks; ++c, ++n_o) {
-            const int buf = n_o & 1;
-            wait_live(&s.p_ready[i][buf], (n_o >> 1) & 1, &live, abort_flag, a.err);
-            wait_live(tile_bar<S>(s.kv_full, it), tile_parity<S>(it), &live, abort_flag, a.err);
-            if (live) {
-              tc_fence_after();
-              const uint32_t v_base = smem_addr(ring + (it % S) * C::kTileBytes) + c * kChunk * 128;
-              const uint32_t tm_p = tm_s + buf * kChunk;
-#pragma unroll
-              for (int k = 0; k < kChunk / 16; ++k)
-                umma_bf16_ts(tm_o, tm_p + k * 8, umma_desc_mn_sw128(v_base + k * 2048, kTile * 128), idesc_o,
-                             (j > 0 || c > 0 || k > 0) ? 1u : 0u);
-              if (g.two_terms()) {
-#pragma unroll
-                for (int k = 0; k < kChunk / 16; ++k)
-                  umma_bf16_ts(tm_o, tm_p + kChunk / 2 + k * 8, umma_desc_mn_sw128(v_base + k * 2048, kTile * 128),
-                               idesc_o, 1u);
-              }
-              umma_commit(&s.pv_done[i][buf]);
-              if (c == chunks - 1) {
-                umma_commit(&s.kv_empty[it % S]);
-                if (g.tiles == 1) umma_commit(&s.kv_empty[it % S]);
-              }
-            }
-            next_s();
-          }
+        for (int k = 0; k < D / 16; ++k) {
+          const uint32_t o = ((k >> 2) * kTile * 128 + (k & 3) * 32) >> 4;
+          umma_ss(tm_s + buf * kChunk, q_lo + o, k_lo + o, idesc_s, k > 0 ? 1u : 0u, lead);
         }
-        unit0 += g.count();
+        umma_commit_if(&s.s_full[i][buf], lead);
+        if (last) {
+          umma_commit_if(&s.kv_empty[slot], lead);
+          if (g.tiles == 1) umma_commit_if(&s.kv_empty[slot], lead);
+          if (js == cnt - 1) umma_commit_if(&s.q_empty, lead);
+        }
+        ++n_s;
+        cs = last ? 0 : 1;
+        js += last ? 1 : 0;
+      };
+      next_s();
+      next_s();
+      for (int j = 0; j < cnt; ++j) {
+        const int u = g.s + j * step + off;
+        const uint32_t it = 2 * (unit0 + j * step + off) + 1;
+        const uint32_t slot = it % S;
+        const int chunks = g.keys(a, u) <= kChunk ? 1 : 2;
+        for (int c = 0; c < chunks; ++c, ++n_o) {
+          const int buf = n_o & 1;
+          if (c == 0) wait_live(tile_bar<S>(s.kv_full, it), tile_parity<S>(it), &live, abort_flag, a.err);
+          wait_live(&s.p_ready[i][buf], (n_o >> 1) & 1, &live, abort_flag, a.err);
+          __syncwarp();
+          tc_fence_after();
+          const uint32_t lead = live ? elected : 0u;
+          const uint32_t v_lo = desc_lo(ring_addr + slot * C::kTileBytes + c * kChunk * 128, kTile * 128);
+          const uint32_t tm_p = tm_s + buf * kChunk;
+#pragma unroll
+          for (int k = 0; k < kChunk / 16; ++k)
+            umma_ts(tm_o, tm_p + k * 8, v_lo + k * (2048 >> 4), idesc_o, (j > 0 || c > 0 || k > 0) ? 1u : 0u, lead);
+          if (g.two_terms()) {
+#pragma unroll
+            for (int k = 0; k < kChunk / 16; ++k)
+              umma_ts(tm_o, tm_p + kChunk / 2 + k * 8, v_lo + k * (2048 >> 4), idesc_o, 1u, lead);
+          }
+          umma_commit_if(&s.pv_done[i][buf], lead);
+          if (c == chunks - 1) {
+            umma_commit_if(&s.kv_empty[slot], lead);
+            if (g.tiles == 1) umma_commit_if(&s.kv_empty[slot], lead);
+          }
+          next_s();
+        }
       }
-      umma_commit(&s.drain);
+      unit0 += g.count();
     }
+    umma_commit_if(&s.drain, elected);
     __syncwarp();
   } else if (warp >= 4) {
     // ---- softmax of pipeline i, one row per thread ----
