@@ -112,21 +112,31 @@ __device__ __forceinline__ void wait_live(uint64_t* bar, uint32_t parity, bool* 
   }
 }
 
-// The barrier on which tile `it` of the ring lands, and its parity.  A parity
-// wait can only tell a phase from the one before it, and the pipelines do not
-// look at every tile when they share a row tile.  So a slot's uses alternate
-// between two barriers: when a pipeline asks for a slot's use k the producer has
-// issued use k - 1 (it issues in order, and the pipeline has seen a later tile or
-// the item's queries), for which use k - 2 had landed and been used, and use k
-// cannot be passed by without this pipeline.
+// A place in the sequence of tiles that go through a ring of S slots, and the
+// barrier on which that tile lands.  A parity wait can only tell a phase from the
+// one before it, and the pipelines do not look at every tile when they share a row
+// tile.  So a slot's uses alternate between two barriers: when a pipeline asks for a
+// slot's use k the producer has issued use k - 1 (it issues in order, and the
+// pipeline has seen a later tile or the item's queries), for which use k - 2 had
+// landed and been used, and use k cannot be passed by without this pipeline.
 template <int S>
-__device__ __forceinline__ uint64_t* tile_bar(uint64_t* kv_full, uint32_t it) {
-  return &kv_full[(it % S) * 2 + (it / S & 1)];
-}
-template <int S>
-__device__ __forceinline__ uint32_t tile_parity(uint32_t it) {
-  return it / S >> 1 & 1;
-}
+struct RingPos {
+  uint32_t slot = 0, use = 0;
+  __device__ __forceinline__ void advance(uint32_t n) {   // n < S
+    slot += n;
+    if (slot >= S) {
+      slot -= S;
+      ++use;
+    }
+  }
+  __device__ __forceinline__ void advance_far(uint32_t n) {
+    slot += n;
+    use += slot / S;
+    slot %= S;
+  }
+  __device__ __forceinline__ uint64_t* full(uint64_t* bars) const { return &bars[2 * slot + (use & 1)]; }
+  __device__ __forceinline__ uint32_t parity() const { return use >> 1 & 1; }
+};
 
 __device__ __forceinline__ void tma_load_4d(void* dst, const CUtensorMap* map, int x, int y, int z, int w,
                                             uint64_t* bar) {

@@ -246,8 +246,8 @@ __global__ void __launch_bounds__(kThreads, 1)
   if (threadIdx.x == 0 && s.u0 == s.u1) p.cuts[blockIdx.x] = make_int4(-1, 0, 0, 0);
   if (warp == 0) {
     // ---- producer ----
-    uint32_t it = 0;      // K and V tiles so far
-    uint32_t issued = 0;  // those whose copies were started
+    RingPos<S> at;
+    uint32_t issued = 0;  // tiles whose copies were started
     int seg = 0, q_issued = 0;
     PageFeed pages;
     for (; walk.next(p, &g); ++seg) {
@@ -286,13 +286,13 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         const uint32_t boxes = __popc(__ballot_sync(0xFFFFFFFFu, has));
 #pragma unroll
-        for (int kv = 0; kv < 2; ++kv, ++it) {
-          const int slot = it % S;
-          if (it >= S) wait_live(&s.kv_empty[slot], (it / S - 1) & 1, &live, abort_flag, a.err);
+        for (int kv = 0; kv < 2; ++kv, at.advance(1)) {
+          const uint32_t slot = at.slot;
+          if (at.use > 0) wait_live(&s.kv_empty[slot], (at.use - 1) & 1, &live, abort_flag, a.err);
           live = __all_sync(0xFFFFFFFFu, live);
           if (!live) continue;
-          issued = it + 1;
-          uint64_t* full = tile_bar<S>(s.kv_full, it);
+          ++issued;
+          uint64_t* full = at.full(s.kv_full);
           if (lane == 0) mbar_arrive_expect_tx(full, boxes * bytes);
           __syncwarp();
           if (has)
@@ -304,8 +304,11 @@ __global__ void __launch_bounds__(kThreads, 1)
     // after a wait that gave up: this CTA's copies have landed before it exits (else the products have used them)
     if (lane == 0 && !live) {
       if (q_issued > 0) mbar_wait_bounded(&s.q_full, (q_issued - 1) & 1, a.err);
-      for (uint32_t j = issued > S ? issued - S : 0; j < issued; ++j)
-        mbar_wait_bounded(tile_bar<S>(s.kv_full, j), tile_parity<S>(j), a.err);
+      RingPos<S> last;
+      const uint32_t first = issued > S ? issued - S : 0;
+      last.advance_far(first);
+      for (uint32_t j = first; j < issued; ++j, last.advance(1))
+        mbar_wait_bounded(last.full(s.kv_full), last.parity(), a.err);
     }
     __syncwarp();
   } else if (warp <= 2) {
@@ -316,12 +319,17 @@ __global__ void __launch_bounds__(kThreads, 1)
     const uint32_t idesc_s = umma_idesc_bf16(128, kChunk);
     const uint32_t idesc_o = umma_idesc_bf16(128, D) | (1u << 16);   // B is MN-major
     const uint32_t ring_addr = uniform(smem_addr(ring)), q_addr = uniform(smem_addr(q_smem));
-    uint32_t unit0 = 0;          // units of the segments so far
+    RingPos<S> seg_k;            // the segment's first K tile
     uint32_t n_s = 0, n_o = 0;   // chunks of this pipeline so far: S issued, O issued
     int seg = 0;
     for (; walk.next(p, &g); ++seg) {
       const int step = g.tiles == 2 ? 1 : 2, off = g.tiles == 2 ? 0 : i;
       const int cnt = g.count(i);
+      RingPos<S> at_k = seg_k;   // K tile of the next S product
+      at_k.advance(2 * off);
+      RingPos<S> at_v = at_k;    // V tile of the next O product
+      at_v.advance(1);
+      const uint32_t releases = g.tiles == 2 ? 1 : 2;   // a tile goes back after two: one per pipeline, or both by one
       wait_live(&s.q_full, seg & 1, &live, abort_flag, a.err);
       __syncwarp();
       if (cnt == 0 && elected) mbar_arrive(&s.q_empty);
@@ -330,18 +338,15 @@ __global__ void __launch_bounds__(kThreads, 1)
       int js = 0, cs = 0;
       const auto next_s = [&]() {
         if (js == cnt) return;
-        const int u = g.s + js * step + off;
-        const uint32_t it = 2 * (unit0 + js * step + off);
-        const uint32_t slot = it % S;
         const int buf = n_s & 1;
-        wait_live(tile_bar<S>(s.kv_full, it), tile_parity<S>(it), &live, abort_flag, a.err);
+        if (cs == 0) wait_live(at_k.full(s.kv_full), at_k.parity(), &live, abort_flag, a.err);
         // P of the chunk before the last lies in the buffer until its product is done
         if (n_s >= 2) wait_live(&s.pv_done[i][buf], ((n_s >> 1) - 1) & 1, &live, abort_flag, a.err);
         __syncwarp();
         tc_fence_after();
-        const bool last = cs == 1 || g.keys(a, u) <= kChunk;
+        const bool last = cs == 1 || g.keys(a, g.s + js * step + off) <= kChunk;
         const uint32_t lead = live ? elected : 0u;
-        const uint32_t k_lo = desc_lo(ring_addr + slot * C::kTileBytes + cs * kChunk * 128);
+        const uint32_t k_lo = desc_lo(ring_addr + at_k.slot * C::kTileBytes + cs * kChunk * 128);
 #pragma unroll
         for (int k = 0; k < D / 16; ++k) {
           const uint32_t o = ((k >> 2) * kTile * 128 + (k & 3) * 32) >> 4;
@@ -349,9 +354,10 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         umma_commit_if(&s.s_full[i][buf], lead);
         if (last) {
-          umma_commit_if(&s.kv_empty[slot], lead);
-          if (g.tiles == 1) umma_commit_if(&s.kv_empty[slot], lead);
+          umma_commit_if(&s.kv_empty[at_k.slot], lead);
+          if (releases == 2) umma_commit_if(&s.kv_empty[at_k.slot], lead);
           if (js == cnt - 1) umma_commit_if(&s.q_empty, lead);
+          at_k.advance(2 * step);
         }
         ++n_s;
         cs = last ? 0 : 1;
@@ -360,18 +366,15 @@ __global__ void __launch_bounds__(kThreads, 1)
       next_s();
       next_s();
       for (int j = 0; j < cnt; ++j) {
-        const int u = g.s + j * step + off;
-        const uint32_t it = 2 * (unit0 + j * step + off) + 1;
-        const uint32_t slot = it % S;
-        const int chunks = g.keys(a, u) <= kChunk ? 1 : 2;
+        const int chunks = g.keys(a, g.s + j * step + off) <= kChunk ? 1 : 2;
         for (int c = 0; c < chunks; ++c, ++n_o) {
           const int buf = n_o & 1;
-          if (c == 0) wait_live(tile_bar<S>(s.kv_full, it), tile_parity<S>(it), &live, abort_flag, a.err);
+          if (c == 0) wait_live(at_v.full(s.kv_full), at_v.parity(), &live, abort_flag, a.err);
           wait_live(&s.p_ready[i][buf], (n_o >> 1) & 1, &live, abort_flag, a.err);
           __syncwarp();
           tc_fence_after();
           const uint32_t lead = live ? elected : 0u;
-          const uint32_t v_lo = desc_lo(ring_addr + slot * C::kTileBytes + c * kChunk * 128, kTile * 128);
+          const uint32_t v_lo = desc_lo(ring_addr + at_v.slot * C::kTileBytes + c * kChunk * 128, kTile * 128);
           const uint32_t tm_p = tm_s + buf * kChunk;
 #pragma unroll
           for (int k = 0; k < kChunk / 16; ++k)
@@ -383,13 +386,14 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
           umma_commit_if(&s.pv_done[i][buf], lead);
           if (c == chunks - 1) {
-            umma_commit_if(&s.kv_empty[slot], lead);
-            if (g.tiles == 1) umma_commit_if(&s.kv_empty[slot], lead);
+            umma_commit_if(&s.kv_empty[at_v.slot], lead);
+            if (releases == 2) umma_commit_if(&s.kv_empty[at_v.slot], lead);
           }
           next_s();
         }
+        at_v.advance(2 * step);
       }
-      unit0 += g.count();
+      seg_k.advance_far(2 * g.count());
     }
     umma_commit_if(&s.drain, elected);
     __syncwarp();
@@ -399,7 +403,9 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int r = threadIdx.x & (kTile - 1);
     const uint32_t lanes = static_cast<uint32_t>((warp & 3) * 32) << 16;
     const uint32_t tm_s = tmem + i * kTile + lanes, tm_o = tmem + 2 * kTile + lanes;
-    uint32_t unit0 = 0, n = 0;   // units so far; this pipeline's chunks so far
+    RingPos<S> seg_v;            // the segment's first V tile
+    seg_v.advance(1);
+    uint32_t n = 0;              // this pipeline's chunks so far
     const int t_r = r / a.group;
     for (; walk.next(p, &g);) {
       const int step = g.tiles == 2 ? 1 : 2, off = g.tiles == 2 ? 0 : i;
@@ -418,9 +424,10 @@ __global__ void __launch_bounds__(kThreads, 1)
         wait_live(&s.s_full[i][n & 1], (n >> 1) & 1, &live, abort_flag, a.err);
         if (partial_tile) {
           // what the row sees of the tile, and a V tile without what nobody may see
-          const uint32_t it = 2 * (unit0 + j * step + off) + 1;
-          uint8_t* v_tile = ring + (it % S) * C::kTileBytes;
-          wait_live(tile_bar<S>(s.kv_full, it), tile_parity<S>(it), &live, abort_flag, a.err);
+          RingPos<S> at_v = seg_v;
+          at_v.advance_far(2 * (j * step + off));
+          uint8_t* v_tile = ring + at_v.slot * C::kTileBytes;
+          wait_live(at_v.full(s.kv_full), at_v.parity(), &live, abort_flag, a.err);
           const int upto = drafted && a.mask == nullptr ? min(valid, node + 1) : valid;
 #pragma unroll
           for (int w = 0; w < 4; ++w) {
@@ -560,7 +567,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           mbar_arrive(&s.p_ready[i][buf]);
         }
       }
-      unit0 += g.count();
+      seg_v.advance_far(2 * g.count());
 
       // ---- the item's (or the run's part of the item's) sums ----
       const bool whole = g.s == 0 && g.e == g.n;
