@@ -18,11 +18,13 @@
 //   warp 0      TMA producer: the item's query tiles, then each unit's K and V
 //               tiles (128 x D bf16, 128-byte swizzle, one box per page piece,
 //               the lanes issuing in parallel) into a ring.
-//   warps 1, 2  MMA issuers of pipelines 0 and 1: S = Q K^T for 64 keys at a time
+//   warps 1, 2  S products of pipelines 0 and 1: S = Q K^T for 64 keys at a time
 //               (fp32, two 64-column TMEM buffers per pipeline, so that the next
-//               S is computed under a softmax), then O += P V, with P (bf16) read
-//               from TMEM where it replaced S (and, over few keys, what P lost in
-//               rounding to bf16).
+//               S is computed under a softmax).
+//   warps 3, 12 O products: O += P V, with P (bf16) read from TMEM where it
+//               replaced S (and, over few keys, what P lost in rounding to bf16).
+//               Each kind of product has its own warp per pipeline: the waits
+//               around a batch take about as long to execute as the batch itself.
 //   warps 4-7, 8-11  softmax of pipelines 0 and 1, one row per thread: S from
 //               TMEM, running maximum m and sum l in base 2, P = 2^(S c - m) back
 //               to TMEM.  O is rescaled only when a row's maximum has risen by
@@ -47,7 +49,7 @@
 namespace dflash2 {
 namespace {
 
-constexpr int kThreads = 384;
+constexpr int kThreads = 416;
 constexpr int kChunk = 64;              // keys of an S product
 constexpr int kMaxSlots = 10;
 constexpr int kMaxRuns = 512;           // most CTAs
@@ -218,7 +220,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         mbar_init(&s.pv_done[i][buf], 1);
       }
     }
-    mbar_init(&s.drain, 2);
+    mbar_init(&s.drain, 4);
     s.abort_flag = 0;
     fence_mbar_init();
     tma_prefetch_desc(&tmQ);
@@ -227,7 +229,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     tma_prefetch_desc(&tmKn);
     tma_prefetch_desc(&tmVn);
   }
-  if (warp == 3) {
+  if (warp == 0) {
     tmem_alloc(&s.tmem, 512);
     tmem_relinquish();
   }
@@ -312,92 +314,100 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     __syncwarp();
   } else if (warp <= 2) {
-    // ---- MMA issuer of pipeline i ----
+    // ---- S products of pipeline i ----
     const int i = warp - 1;
     const uint32_t elected = elect_lane();
-    const uint32_t tm_s = tmem + i * kTile, tm_o = tmem + 2 * kTile + i * D;
-    const uint32_t idesc_s = umma_idesc_bf16(128, kChunk);
-    const uint32_t idesc_o = umma_idesc_bf16(128, D) | (1u << 16);   // B is MN-major
+    const uint32_t tm_s = tmem + i * kTile;
+    const uint32_t idesc = umma_idesc_bf16(128, kChunk);
     const uint32_t ring_addr = uniform(smem_addr(ring)), q_addr = uniform(smem_addr(q_smem));
     RingPos<S> seg_k;            // the segment's first K tile
-    uint32_t n_s = 0, n_o = 0;   // chunks of this pipeline so far: S issued, O issued
+    uint32_t n = 0;              // this pipeline's chunks so far
     int seg = 0;
     for (; walk.next(p, &g); ++seg) {
       const int step = g.tiles == 2 ? 1 : 2, off = g.tiles == 2 ? 0 : i;
       const int cnt = g.count(i);
-      RingPos<S> at_k = seg_k;   // K tile of the next S product
-      at_k.advance(2 * off);
-      RingPos<S> at_v = at_k;    // V tile of the next O product
-      at_v.advance(1);
-      const uint32_t releases = g.tiles == 2 ? 1 : 2;   // a tile goes back after two: one per pipeline, or both by one
+      RingPos<S> at = seg_k;
+      at.advance(2 * off);
       wait_live(&s.q_full, seg & 1, &live, abort_flag, a.err);
       __syncwarp();
       if (cnt == 0 && elected) mbar_arrive(&s.q_empty);
       const uint32_t q_lo = desc_lo(q_addr + (g.tiles == 2 ? i : 0) * C::kTileBytes);
-      // the S product of the segment's next chunk: unit js, chunk cs
-      int js = 0, cs = 0;
-      const auto next_s = [&]() {
-        if (js == cnt) return;
-        const int buf = n_s & 1;
-        if (cs == 0) wait_live(at_k.full(s.kv_full), at_k.parity(), &live, abort_flag, a.err);
-        // P of the chunk before the last lies in the buffer until its product is done
-        if (n_s >= 2) wait_live(&s.pv_done[i][buf], ((n_s >> 1) - 1) & 1, &live, abort_flag, a.err);
-        __syncwarp();
-        tc_fence_after();
-        const bool last = cs == 1 || g.keys(a, g.s + js * step + off) <= kChunk;
-        const uint32_t lead = live ? elected : 0u;
-        const uint32_t k_lo = desc_lo(ring_addr + at_k.slot * C::kTileBytes + cs * kChunk * 128);
-#pragma unroll
-        for (int k = 0; k < D / 16; ++k) {
-          const uint32_t o = ((k >> 2) * kTile * 128 + (k & 3) * 32) >> 4;
-          umma_ss(tm_s + buf * kChunk, q_lo + o, k_lo + o, idesc_s, k > 0 ? 1u : 0u, lead);
-        }
-        umma_commit_if(&s.s_full[i][buf], lead);
-        if (last) {
-          umma_commit_if(&s.kv_empty[at_k.slot], lead);
-          if (releases == 2) umma_commit_if(&s.kv_empty[at_k.slot], lead);
-          if (js == cnt - 1) umma_commit_if(&s.q_empty, lead);
-          at_k.advance(2 * step);
-        }
-        ++n_s;
-        cs = last ? 0 : 1;
-        js += last ? 1 : 0;
-      };
-      next_s();
-      next_s();
       for (int j = 0; j < cnt; ++j) {
         const int chunks = g.keys(a, g.s + j * step + off) <= kChunk ? 1 : 2;
-        for (int c = 0; c < chunks; ++c, ++n_o) {
-          const int buf = n_o & 1;
-          if (c == 0) wait_live(at_v.full(s.kv_full), at_v.parity(), &live, abort_flag, a.err);
-          wait_live(&s.p_ready[i][buf], (n_o >> 1) & 1, &live, abort_flag, a.err);
+        const uint32_t k_lo = desc_lo(ring_addr + at.slot * C::kTileBytes);
+        wait_live(at.full(s.kv_full), at.parity(), &live, abort_flag, a.err);
+        for (int c = 0; c < chunks; ++c, ++n) {
+          const int buf = n & 1;
+          // P of the chunk before the last lies in the buffer until its product is done
+          if (n >= 2) wait_live(&s.pv_done[i][buf], ((n >> 1) - 1) & 1, &live, abort_flag, a.err);
           __syncwarp();
           tc_fence_after();
           const uint32_t lead = live ? elected : 0u;
-          const uint32_t v_lo = desc_lo(ring_addr + at_v.slot * C::kTileBytes + c * kChunk * 128, kTile * 128);
-          const uint32_t tm_p = tm_s + buf * kChunk;
 #pragma unroll
-          for (int k = 0; k < kChunk / 16; ++k)
-            umma_ts(tm_o, tm_p + k * 8, v_lo + k * (2048 >> 4), idesc_o, (j > 0 || c > 0 || k > 0) ? 1u : 0u, lead);
-          if (g.two_terms()) {
-#pragma unroll
-            for (int k = 0; k < kChunk / 16; ++k)
-              umma_ts(tm_o, tm_p + kChunk / 2 + k * 8, v_lo + k * (2048 >> 4), idesc_o, 1u, lead);
+          for (int k = 0; k < D / 16; ++k) {
+            const uint32_t o = ((k >> 2) * kTile * 128 + (k & 3) * 32) >> 4;
+            umma_ss(tm_s + buf * kChunk, q_lo + o, k_lo + ((c * kChunk * 128) >> 4) + o, idesc, k > 0 ? 1u : 0u, lead);
           }
-          umma_commit_if(&s.pv_done[i][buf], lead);
-          if (c == chunks - 1) {
-            umma_commit_if(&s.kv_empty[at_v.slot], lead);
-            if (releases == 2) umma_commit_if(&s.kv_empty[at_v.slot], lead);
-          }
-          next_s();
+          umma_commit_if(&s.s_full[i][buf], lead);
         }
-        at_v.advance(2 * step);
+        // a tile goes back after two releases: one per pipeline, or both by the one that has it to itself
+        const uint32_t lead = live ? elected : 0u;
+        umma_commit_if(&s.kv_empty[at.slot], lead);
+        if (g.tiles == 1) umma_commit_if(&s.kv_empty[at.slot], lead);
+        if (j == cnt - 1) umma_commit_if(&s.q_empty, lead);
+        at.advance(2 * step);
       }
       seg_k.advance_far(2 * g.count());
     }
     umma_commit_if(&s.drain, elected);
     __syncwarp();
-  } else if (warp >= 4) {
+  } else if (warp == 3 || warp == 12) {
+    // ---- O products of pipeline i ----
+    const int i = warp == 3 ? 0 : 1;
+    const uint32_t elected = elect_lane();
+    const uint32_t tm_s = tmem + i * kTile, tm_o = tmem + 2 * kTile + i * D;
+    const uint32_t idesc = umma_idesc_bf16(128, D) | (1u << 16);   // B is MN-major
+    const uint32_t ring_addr = uniform(smem_addr(ring));
+    RingPos<S> seg_v;            // the segment's first V tile
+    seg_v.advance(1);
+    uint32_t n = 0;
+    while (walk.next(p, &g)) {
+      const int step = g.tiles == 2 ? 1 : 2, off = g.tiles == 2 ? 0 : i;
+      const int cnt = g.count(i);
+      const bool two = g.two_terms();
+      RingPos<S> at = seg_v;
+      at.advance(2 * off);
+      for (int j = 0; j < cnt; ++j) {
+        const int chunks = g.keys(a, g.s + j * step + off) <= kChunk ? 1 : 2;
+        const uint32_t v_lo = desc_lo(ring_addr + at.slot * C::kTileBytes, kTile * 128);
+        for (int c = 0; c < chunks; ++c, ++n) {
+          const int buf = n & 1;
+          wait_live(&s.p_ready[i][buf], (n >> 1) & 1, &live, abort_flag, a.err);
+          if (c == 0) wait_live(at.full(s.kv_full), at.parity(), &live, abort_flag, a.err);
+          __syncwarp();
+          tc_fence_after();
+          const uint32_t lead = live ? elected : 0u;
+          const uint32_t v_c = v_lo + c * ((kChunk * 128) >> 4), tm_p = tm_s + buf * kChunk;
+#pragma unroll
+          for (int k = 0; k < kChunk / 16; ++k)
+            umma_ts(tm_o, tm_p + k * 8, v_c + k * (2048 >> 4), idesc, (j > 0 || c > 0 || k > 0) ? 1u : 0u, lead);
+          if (two) {
+#pragma unroll
+            for (int k = 0; k < kChunk / 16; ++k)
+              umma_ts(tm_o, tm_p + kChunk / 2 + k * 8, v_c + k * (2048 >> 4), idesc, 1u, lead);
+          }
+          umma_commit_if(&s.pv_done[i][buf], lead);
+        }
+        const uint32_t lead = live ? elected : 0u;
+        umma_commit_if(&s.kv_empty[at.slot], lead);
+        if (g.tiles == 1) umma_commit_if(&s.kv_empty[at.slot], lead);
+        at.advance(2 * step);
+      }
+      seg_v.advance_far(2 * g.count());
+    }
+    umma_commit_if(&s.drain, elected);
+    __syncwarp();
+  } else if (warp >= 4 && warp < 12) {
     // ---- softmax of pipeline i, one row per thread ----
     const int i = warp >= 8 ? 1 : 0;
     const int r = threadIdx.x & (kTile - 1);
@@ -678,7 +688,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   __syncthreads();
   if (threadIdx.x == 0) mbar_wait_bounded(&s.drain, 0, a.err);   // the tensor cores have finished
   __syncthreads();
-  if (warp == 3) {
+  if (warp == 0) {
     tc_fence_after();
     tmem_dealloc(tmem, 512);
   }
