@@ -509,10 +509,10 @@ __global__ void __launch_bounds__(kThreads, 1)
               if (!(v1 >> y & 1u)) z[1][y] = -INFINITY;
             }
           }
-          float top = -INFINITY;
+          float tops[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};   // four chains of dependent maxima
 #pragma unroll
-          for (int y = 0; y < 32; ++y) top = fmaxf(top, fmaxf(z[0][y], z[1][y]));
-          top *= p.c;
+          for (int y = 0; y < 32; ++y) tops[y & 3] = fmaxf(tops[y & 3], fmaxf(z[0][y], z[1][y]));
+          const float top = fmaxf(fmaxf(tops[0], tops[1]), fmaxf(tops[2], tops[3])) * p.c;
           if (j == 0 && c == 0) {
             m = top;
           } else if (__any_sync(0xFFFFFFFFu, row_ok && top > m + kRescale)) {
@@ -671,7 +671,7 @@ __global__ void __launch_bounds__(kThreads, 1)
               dst[y / 8] = make_uint4(pack_bf16(o[y], o[y + 1]), pack_bf16(o[y + 2], o[y + 3]),
                                       pack_bf16(o[y + 4], o[y + 5]), pack_bf16(o[y + 6], o[y + 7]));
           }
-        } else {
+        } else if (row_ok) {
           float4* dst = reinterpret_cast<float4*>(p.part) +
                         ((static_cast<int64_t>(slot) * p.areas + area) * (D / 4) + x / 4) * kTile + r;
 #pragma unroll
@@ -695,18 +695,40 @@ __global__ void __launch_bounds__(kThreads, 1)
 }
 
 // Adds the parts of the items that runs cut.  Every CTA lists the cut items from
-// the runs' records; a task is one of them, one of its row tiles and 8 columns.
-// Thread (r, y): row r, every kJoinSplit-th part from the y-th on, so that an item
-// of many parts (few heads, a long cache) is read by many threads at once; the
-// kJoinSplit sums are added in order.
+// the runs' records; a task is one of them, one of its row tiles and a group of
+// columns; a thread takes a row and 8 columns, and adds parts as the softmax adds
+// keys.  With many cut items (of few parts each) a task is 32 columns and a thread
+// takes every part.  With few (a few heads, a long cache, many parts each) it is 8
+// columns, thread (r, y) takes every 4th part from the y-th on, and the four sums
+// are added in order: 1 x 17 over 8191 positions, 17 parts per head, 10 us with
+// one thread per row and column group against 5.
 constexpr int kJoinSplit = 4, kJoinThreads = kTile * kJoinSplit, kJoinCols = 8;
+
+struct PartSum {
+  float m, l, o[kJoinCols];
+  __device__ __forceinline__ void clear() {
+    m = -INFINITY;
+    l = 0.0f;
+#pragma unroll
+    for (int k = 0; k < kJoinCols; ++k) o[k] = 0.0f;
+  }
+  // Adds sums (m1, l1, v); with m1 = -inf they saw nothing, and v is not looked at.
+  __device__ __forceinline__ void add(float m1, float l1, const float (&v)[kJoinCols]) {
+    const bool some = m1 != -INFINITY;
+    const float top = fmaxf(m, m1);
+    const float f0 = m == -INFINITY ? 0.0f : exp2_approx(m - top), f1 = some ? exp2_approx(m1 - top) : 0.0f;
+    m = top;
+    l = l * f0 + (some || l1 != l1 ? l1 * (some ? f1 : 1.0f) : 0.0f);   // only NaN scores: l1 is NaN
+#pragma unroll
+    for (int k = 0; k < kJoinCols; ++k) o[k] = fmaf(some ? v[k] : 0.0f, f1, o[k] * f0);
+  }
+};
 
 template <int D>
 __global__ void __launch_bounds__(kJoinThreads) tree_attn_join_kernel(const __grid_constant__ AttnPlan p, int runs) {
   __shared__ int32_t list[kMaxRuns];
   __shared__ int32_t warp_n[kJoinThreads / 32];
-  __shared__ float s_m[kJoinSplit][kTile];
-  __shared__ float s_o[kJoinSplit][kJoinCols + 1][kTile];
+  __shared__ float s_o[kJoinSplit][kJoinCols + 2][kTile];
   const AttnArgs& a = p.a;
   const int tid = threadIdx.x, r = tid & (kTile - 1), y = tid / kTile;
   pdl_wait();
@@ -722,65 +744,57 @@ __global__ void __launch_bounds__(kJoinThreads) tree_attn_join_kernel(const __gr
   }
   if (cut) list[at] = tid;
   __syncthreads();
-  constexpr int kGroups = D / kJoinCols;
-  for (int task = blockIdx.x; task < n * p.areas * kGroups; task += gridDim.x) {
-    const int x = task % kGroups * kJoinCols, tile = task / kGroups % p.areas, c0 = list[task / kGroups / p.areas];
+  const bool wide = n * p.areas * (D / (kJoinCols * kJoinSplit)) >= static_cast<int>(gridDim.x);
+  const int cols = wide ? kJoinCols * kJoinSplit : kJoinCols;
+  const int groups = D / cols;
+  for (int task = blockIdx.x; task < n * p.areas * groups; task += gridDim.x) {
+    const int x = task % groups * cols + (wide ? y * kJoinCols : 0), tile = task / groups % p.areas;
+    const int c0 = list[task / groups / p.areas];
     const int4 d = p.cuts[c0];
     const int pair = d.y % p.pairs, h = d.y / p.pairs, c1 = d.z;
     if (2 * pair + tile >= p.row_tiles) continue;
     const int node = (2 * pair + tile) * p.tpt + r / a.group;
     const bool row_ok = r < p.tpt * a.group && node < a.T;
-    // a run's first segment leaves its parts in slot 2 c, its last one in 2 c + 1
-    const auto part_of = [&](int c) { return static_cast<int64_t>(c == c0 ? d.w : 2 * c) * p.areas + tile; };
-    float m = -INFINITY;
-    if (row_ok) {
-#pragma unroll 4
-      for (int c = c0 + y; c <= c1; c += kJoinSplit) m = fmaxf(m, p.part_ml[part_of(c) * kTile + r].x);
-    }
-    s_m[y][r] = m;
-    __syncthreads();
-#pragma unroll
-    for (int w = 0; w < kJoinSplit; ++w) m = fmaxf(m, s_m[w][r]);
-    float l = 0.0f, o[kJoinCols];
-#pragma unroll
-    for (int k = 0; k < kJoinCols; ++k) o[k] = 0.0f;
+    PartSum sum;
+    sum.clear();
     if (row_ok) {
 #pragma unroll 2
-      for (int c = c0 + y; c <= c1; c += kJoinSplit) {
-        const float2 ml = p.part_ml[part_of(c) * kTile + r];
-        const float4* src = reinterpret_cast<const float4*>(p.part) + (part_of(c) * (D / 4) + x / 4) * kTile + r;
-        const bool some = ml.x != -INFINITY;     // else it saw nothing, and its sums are not looked at
-        const float f = some ? exp2_approx(ml.x - m) : 0.0f;
-        l += some ? ml.y * f : (ml.y != ml.y ? ml.y : 0.0f);
+      for (int c = c0 + (wide ? 0 : y); c <= c1; c += wide ? 1 : kJoinSplit) {
+        // a run's first segment leaves its parts in slot 2 c, its last one in 2 c + 1
+        const int64_t part = static_cast<int64_t>(c == c0 ? d.w : 2 * c) * p.areas + tile;
+        const float2 ml = p.part_ml[part * kTile + r];
+        const float4* src = reinterpret_cast<const float4*>(p.part) + (part * (D / 4) + x / 4) * kTile + r;
+        const float4 v0 = src[0], v1 = src[kTile];
+        const float v[kJoinCols] = {v0.x, v0.y, v0.z, v0.w, v1.x, v1.y, v1.z, v1.w};
+        sum.add(ml.x, ml.y, v);
+      }
+    }
+    if (!wide) {
+      s_o[y][kJoinCols][r] = sum.m;
+      s_o[y][kJoinCols + 1][r] = sum.l;
 #pragma unroll
-        for (int k = 0; k < kJoinCols; k += 4) {
-          const float4 v = src[(k / 4) * kTile];
-          o[k] = fmaf(some ? v.x : 0.0f, f, o[k]);
-          o[k + 1] = fmaf(some ? v.y : 0.0f, f, o[k + 1]);
-          o[k + 2] = fmaf(some ? v.z : 0.0f, f, o[k + 2]);
-          o[k + 3] = fmaf(some ? v.w : 0.0f, f, o[k + 3]);
+      for (int k = 0; k < kJoinCols; ++k) s_o[y][k][r] = sum.o[k];
+      __syncthreads();
+      if (y == 0) {
+#pragma unroll
+        for (int w = 1; w < kJoinSplit; ++w) {
+          float v[kJoinCols];
+#pragma unroll
+          for (int k = 0; k < kJoinCols; ++k) v[k] = s_o[w][k][r];
+          sum.add(s_o[w][kJoinCols][r], s_o[w][kJoinCols + 1][r], v);
         }
       }
+      __syncthreads();
     }
-#pragma unroll
-    for (int k = 0; k < kJoinCols; ++k) s_o[y][k][r] = o[k];
-    s_o[y][kJoinCols][r] = l;
-    __syncthreads();
-    if (y == 0 && row_ok) {
-#pragma unroll
-      for (int w = 1; w < kJoinSplit; ++w) {
-        l += s_o[w][kJoinCols][r];
-#pragma unroll
-        for (int k = 0; k < kJoinCols; ++k) o[k] += s_o[w][k][r];
-      }
-      const float inv = l == 0.0f ? 0.0f : 1.0f / l;
+    if (row_ok && (wide || y == 0)) {
+      const float inv = sum.l == 0.0f ? 0.0f : 1.0f / sum.l;
       const int64_t orow = (static_cast<int64_t>(d.x) * a.T + node) * a.heads + h * a.group + r % a.group;
       *reinterpret_cast<uint4*>(a.out + orow * D + x) =
-          make_uint4(pack_bf16(o[0] * inv, o[1] * inv), pack_bf16(o[2] * inv, o[3] * inv),
-                     pack_bf16(o[4] * inv, o[5] * inv), pack_bf16(o[6] * inv, o[7] * inv));
-      if (x == 0 && a.lse != nullptr) a.lse[orow] = l == 0.0f ? -INFINITY : (m + log2f(l)) * 0.69314718055994531f;
+          make_uint4(pack_bf16(sum.o[0] * inv, sum.o[1] * inv), pack_bf16(sum.o[2] * inv, sum.o[3] * inv),
+                     pack_bf16(sum.o[4] * inv, sum.o[5] * inv), pack_bf16(sum.o[6] * inv, sum.o[7] * inv));
+      if (x == 0 && a.lse != nullptr)
+        a.lse[orow] = sum.l == 0.0f ? -INFINITY : (sum.m + log2f(sum.l)) * 0.69314718055994531f;
     }
-    __syncthreads();
   }
 }
 
