@@ -423,6 +423,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       const int node = (2 * g.pair + (g.tiles == 2 ? i : 0)) * p.tpt + t_r;
       const bool row_ok = r < p.tpt * a.group && node < a.T;
       const bool two = g.two_terms();
+      // a warp none of whose rows is a query's has nothing to do but to keep step
+      const bool busy = (warp & 3) * 32 < min(p.tpt, a.T - (node - t_r)) * a.group;
       float m = -INFINITY, l = 0.0f;
       uint32_t vis[4] = {0, 0, 0, 0}, bad_seen = 0;   // the drafted tile's mask; whether a visible node is non-finite
       for (int j = 0; j < cnt; ++j) {
@@ -495,83 +497,85 @@ __global__ void __launch_bounds__(kThreads, 1)
           wait_live(&s.s_full[i][buf], (n >> 1) & 1, &live, abort_flag, a.err);
           __syncwarp();
           tc_fence_after();
-          float z[2][32];
-          tmem_ld_x32(tm_sb, z[0]);
-          tmem_ld_x32(tm_sb + 32, z[1]);
-          tmem_ld_wait();
-          pin(z[0]);
-          pin(z[1]);
-          if (partial_tile) {
-            const uint32_t v0 = c ? vis[2] : vis[0], v1 = c ? vis[3] : vis[1];
+          if (busy) {
+            float z[2][32];
+            tmem_ld_x32(tm_sb, z[0]);
+            tmem_ld_x32(tm_sb + 32, z[1]);
+            tmem_ld_wait();
+            pin(z[0]);
+            pin(z[1]);
+            if (partial_tile) {
+              const uint32_t v0 = c ? vis[2] : vis[0], v1 = c ? vis[3] : vis[1];
 #pragma unroll
-            for (int y = 0; y < 32; ++y) {
-              if (!(v0 >> y & 1u)) z[0][y] = -INFINITY;
-              if (!(v1 >> y & 1u)) z[1][y] = -INFINITY;
-            }
-          }
-          float tops[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};   // four chains of dependent maxima
-#pragma unroll
-          for (int y = 0; y < 32; ++y) tops[y & 3] = fmaxf(tops[y & 3], fmaxf(z[0][y], z[1][y]));
-          const float top = fmaxf(fmaxf(tops[0], tops[1]), fmaxf(tops[2], tops[3])) * p.c;
-          if (j == 0 && c == 0) {
-            m = top;
-          } else if (__any_sync(0xFFFFFFFFu, row_ok && top > m + kRescale)) {
-            // a row's maximum rose far: the warp's O and l move to the new ones (rows of the
-            // tile that are no query's hold whatever shared memory held, and have no say)
-            const float m1 = fmaxf(m, top);
-            const float f = m == -INFINITY ? 1.0f : exp2_approx(m - m1);
-            m = m1;
-            l *= f;
-            wait_live(&s.pv_done[i][buf ^ 1], ((n - 1) >> 1) & 1, &live, abort_flag, a.err);
-            __syncwarp();
-            tc_fence_after();
-#pragma unroll 1
-            for (int x = 0; x < D; x += 32) {
-              float o[32];
-              tmem_ld_x32(tm_o + i * D + x, o);
-              tmem_ld_wait();
-              pin(o);
-#pragma unroll
-              for (int w = 0; w < 32; w += 16) {
-                uint32_t ob[16];
-#pragma unroll
-                for (int y = 0; y < 16; ++y) ob[y] = __float_as_uint(o[w + y] * f);
-                tmem_st_x16(tm_o + i * D + x + w, ob);
+              for (int y = 0; y < 32; ++y) {
+                if (!(v0 >> y & 1u)) z[0][y] = -INFINITY;
+                if (!(v1 >> y & 1u)) z[1][y] = -INFINITY;
               }
             }
-          }
-          const float mm = m == -INFINITY ? 0.0f : m;   // a row that has seen nothing: all its P are 2^-inf
-          const uint64_t c2 = pack2(p.c, p.c), m2 = pack2(-mm, -mm);
-          uint64_t sum0 = pack2(0.0f, 0.0f), sum1 = sum0;
+            float tops[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};   // four chains of dependent maxima
 #pragma unroll
-          for (int x = 0; x < 2; ++x) {
-            uint32_t hi[16];
+            for (int y = 0; y < 32; ++y) tops[y & 3] = fmaxf(tops[y & 3], fmaxf(z[0][y], z[1][y]));
+            const float top = fmaxf(fmaxf(tops[0], tops[1]), fmaxf(tops[2], tops[3])) * p.c;
+            if (j == 0 && c == 0) {
+              m = top;
+            } else if (__any_sync(0xFFFFFFFFu, row_ok && top > m + kRescale)) {
+              // a row's maximum rose far: the warp's O and l move to the new ones (rows of the
+              // tile that are no query's hold whatever shared memory held, and have no say)
+              const float m1 = fmaxf(m, top);
+              const float f = m == -INFINITY ? 1.0f : exp2_approx(m - m1);
+              m = m1;
+              l *= f;
+              wait_live(&s.pv_done[i][buf ^ 1], ((n - 1) >> 1) & 1, &live, abort_flag, a.err);
+              __syncwarp();
+              tc_fence_after();
+#pragma unroll 1
+              for (int x = 0; x < D; x += 32) {
+                float o[32];
+                tmem_ld_x32(tm_o + i * D + x, o);
+                tmem_ld_wait();
+                pin(o);
 #pragma unroll
-            for (int y = 0; y < 32; y += 4) {
-              const float2 e0 = unpack2(fma2(pack2(z[x][y], z[x][y + 1]), c2, m2));
-              const float2 e1 = unpack2(fma2(pack2(z[x][y + 2], z[x][y + 3]), c2, m2));
-              z[x][y] = exp2_approx(e0.x);
-              z[x][y + 1] = exp2_approx(e0.y);
-              z[x][y + 2] = exp2_approx(e1.x);
-              z[x][y + 3] = exp2_approx(e1.y);
-              sum0 = add2(sum0, pack2(z[x][y], z[x][y + 1]));
-              sum1 = add2(sum1, pack2(z[x][y + 2], z[x][y + 3]));
-              hi[y / 2] = pack_bf16(z[x][y], z[x][y + 1]);
-              hi[y / 2 + 1] = pack_bf16(z[x][y + 2], z[x][y + 3]);
+                for (int w = 0; w < 32; w += 16) {
+                  uint32_t ob[16];
+#pragma unroll
+                  for (int y = 0; y < 16; ++y) ob[y] = __float_as_uint(o[w + y] * f);
+                  tmem_st_x16(tm_o + i * D + x + w, ob);
+                }
+              }
             }
-            tmem_st_x16(tm_sb + 16 * x, hi);
-          }
-          if (two) {
+            const float mm = m == -INFINITY ? 0.0f : m;   // a row that has seen nothing: all its P are 2^-inf
+            const uint64_t c2 = pack2(p.c, p.c), m2 = pack2(-mm, -mm);
+            uint64_t sum0 = pack2(0.0f, 0.0f), sum1 = sum0;
 #pragma unroll
             for (int x = 0; x < 2; ++x) {
-              uint32_t lo[16];
+              uint32_t hi[16];
 #pragma unroll
-              for (int y = 0; y < 32; y += 2) lo[y / 2] = remainder_bf16(z[x][y], z[x][y + 1]);
-              tmem_st_x16(tm_sb + kChunk / 2 + 16 * x, lo);
+              for (int y = 0; y < 32; y += 4) {
+                const float2 e0 = unpack2(fma2(pack2(z[x][y], z[x][y + 1]), c2, m2));
+                const float2 e1 = unpack2(fma2(pack2(z[x][y + 2], z[x][y + 3]), c2, m2));
+                z[x][y] = exp2_approx(e0.x);
+                z[x][y + 1] = exp2_approx(e0.y);
+                z[x][y + 2] = exp2_approx(e1.x);
+                z[x][y + 3] = exp2_approx(e1.y);
+                sum0 = add2(sum0, pack2(z[x][y], z[x][y + 1]));
+                sum1 = add2(sum1, pack2(z[x][y + 2], z[x][y + 3]));
+                hi[y / 2] = pack_bf16(z[x][y], z[x][y + 1]);
+                hi[y / 2 + 1] = pack_bf16(z[x][y + 2], z[x][y + 3]);
+              }
+              tmem_st_x16(tm_sb + 16 * x, hi);
             }
+            if (two) {
+#pragma unroll
+              for (int x = 0; x < 2; ++x) {
+                uint32_t lo[16];
+#pragma unroll
+                for (int y = 0; y < 32; y += 2) lo[y / 2] = remainder_bf16(z[x][y], z[x][y + 1]);
+                tmem_st_x16(tm_sb + kChunk / 2 + 16 * x, lo);
+              }
+            }
+            const float2 sum = unpack2(add2(sum0, sum1));
+            l += sum.x + sum.y;
           }
-          const float2 sum = unpack2(add2(sum0, sum1));
-          l += sum.x + sum.y;
           tmem_st_wait();
           tc_fence_before();
           mbar_arrive(&s.p_ready[i][buf]);
