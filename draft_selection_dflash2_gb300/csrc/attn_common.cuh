@@ -44,15 +44,33 @@ __device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
   return d;
 }
 
-// Cuts the units of B sequences, units(b) * per_seq each, into runs of equal
-// length (at least min_run) and finds the sequence that run `run`'s first unit
-// falls into: *out_base = units before that sequence's.  Whole-block.
+// Lane 0's value, which the compiler then knows to be the whole warp's.
+template <class T>
+__device__ __forceinline__ T uniform(T x) {
+  return __shfl_sync(0xFFFFFFFFu, x, 0);
+}
+
+// Non-negative quotient; a 64-bit division takes several times as long as a 32-bit one.
+__device__ __forceinline__ int64_t quotient(int64_t x, int64_t y) {
+  if (((x | y) >> 31) == 0) return static_cast<uint32_t>(x) / static_cast<uint32_t>(y);
+  return x / y;
+}
+
+// Where a run starts: unit `rel` of sequence b, whose items have n units each, and
+// how many units the run has.
+struct RunStart {
+  int64_t scan[16];         // scratch
+  int64_t rel, units;
+  int32_t b, n;
+};
+
+// Cuts the units of B sequences, per_seq items of units(b) each, into runs of equal
+// length and finds run `run`.  Whole-block.
 template <int kT, class Units>
-__device__ void find_run(const Units& units, int64_t B, int64_t per_seq, int64_t min_run, int64_t run, int64_t runs,
-                         int64_t* scan, int64_t* out_u0, int64_t* out_u1, int64_t* out_base,
-                         int32_t* out_b) {
+__device__ __forceinline__ void find_run(const Units& units, int64_t B, int64_t per_seq, int64_t run, int64_t runs,
+                                         RunStart* out) {
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  const int64_t chunk = (B + kT - 1) / kT;
+  const int64_t chunk = quotient(B + kT - 1, kT);
   const int64_t b_lo = tid * chunk, b_hi = imin64(B, b_lo + chunk);
   int64_t sum = 0;
   for (int64_t b = b_lo; b < b_hi; ++b) sum += units(b) * per_seq;
@@ -62,31 +80,55 @@ __device__ void find_run(const Units& units, int64_t B, int64_t per_seq, int64_t
     const int64_t o = __shfl_up_sync(0xFFFFFFFFu, incl, s);
     if (lane >= s) incl += o;
   }
-  if (lane == 31) scan[warp] = incl;
+  if (lane == 31) out->scan[warp] = incl;
   __syncthreads();
   int64_t before = incl - sum, total = 0;
+#pragma unroll
   for (int w = 0; w < kT / 32; ++w) {
-    if (w < warp) before += scan[w];
-    total += scan[w];
+    if (w < warp) before += out->scan[w];
+    total += out->scan[w];
   }
-  const int64_t len = imax64((total + runs - 1) / runs, min_run);
-  const int64_t u0 = imin64(run * len, total), u1 = imin64(u0 + len, total);
+  const int64_t len = quotient(total + runs - 1, runs);
+  const int64_t u0 = imin64(run * len, total);
   if (u0 >= before && u0 < before + sum) {
     int64_t base = before, b = b_lo;
-    for (;; ++b) {
-      const int64_t n = units(b) * per_seq;
-      if (u0 < base + n) break;
-      base += n;
+    int64_t n = units(b);
+    while (u0 >= base + n * per_seq) {
+      base += n * per_seq;
+      n = units(++b);
     }
-    *out_base = base;
-    *out_b = static_cast<int32_t>(b);
+    out->rel = u0 - base;
+    out->b = static_cast<int32_t>(b);
+    out->n = static_cast<int32_t>(n);
   }
-  if (tid == 0) {
-    *out_u0 = u0;
-    *out_u1 = u1;
-  }
+  if (tid == 0) out->units = imin64(len, total - u0);
   __syncthreads();
 }
+
+// Walks a run's stretches of items; each warp keeps its own (whole warps call it).
+struct RunWalk {
+  int64_t left;             // units of the run still to come
+  int32_t b, item, s, n;    // the next stretch: from unit s of n of the sequence's item
+  __device__ __forceinline__ void start(const RunStart& r) {
+    left = uniform(r.units);
+    if (left <= 0) return;
+    b = uniform(r.b);
+    n = uniform(r.n);
+    const int64_t rel = uniform(r.rel);
+    item = static_cast<int32_t>(quotient(rel, n));
+    s = static_cast<int32_t>(rel - static_cast<int64_t>(item) * n);
+  }
+  // The item after this one (sequences without units are passed over).
+  template <class Units>
+  __device__ __forceinline__ void next_item(const Units& units, int32_t per_seq) {
+    s = 0;
+    if (++item < per_seq) return;
+    item = 0;
+    do {
+      n = static_cast<int32_t>(uniform(units(++b)));
+    } while (n == 0);
+  }
+};
 
 // A bounded wait that also gives up when another role of the CTA has; once one
 // has given up (*live = false) later waits return at once.
@@ -190,12 +232,6 @@ struct PageFeed {
     return p < 0 ? 0 : c.num_pages - 1;
   }
 };
-
-// Lane 0's value, which the compiler then knows to be the whole warp's.
-template <class T>
-__device__ __forceinline__ T uniform(T x) {
-  return __shfl_sync(0xFFFFFFFFu, x, 0);
-}
 
 // Products are issued by whole warps of which one elected lane acts: the code
 // around them stays warp-uniform, so operands are computed in uniform registers,

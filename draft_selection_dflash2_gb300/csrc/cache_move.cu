@@ -57,36 +57,53 @@ __global__ void __launch_bounds__(kCommitThreads) cache_commit_kernel(const Comm
 
 // ---------------------------------------------------------------------------
 // eviction, step 1: which positions stay.  A cluster of CTAs per (b, h), each
-// with a contiguous slice of its positions.  The r-th largest key (the
+// with a contiguous slice of its positions.  Wanted is the r-th largest key (the
 // order-preserving image of the score) among the positions before the recent
-// ones is found in three digits from the top (11, 11 and 10 bits): each CTA counts
-// its slice's keys that share the digits so far by their next digit, the cluster
-// adds the counts through distributed shared memory, and every CTA finds the
-// digit that the r-th key has.  Then the kept positions are listed in order: those
-// above that key, the first ones equal to it, and the recent ones; a warp takes
-// consecutive positions, and its place in the list is the number kept before them.
-// The scores are read once: a slice's keys stay in shared memory (slices of more
-// than kSelKeys positions are read again by each step).
+// ones.  Its leading digit (11 bits) comes from counting all keys by theirs: each
+// CTA its slice's, the cluster's counts added through distributed shared memory,
+// and every CTA finds the digit that the r-th key has.  The keys that share it are
+// usually few: they are collected, and each of up to kSelCands is ranked against
+// all the others (by key, then position), which ends the search; where there are
+// more, another digit is taken first.  Then the kept positions are listed in order:
+// those above that key, the first ones equal to it, and the recent ones; a warp
+// takes consecutive positions, and its place in the list is the number kept before
+// them.  The scores are read once: a slice's keys stay in shared memory (slices of
+// more than kSelKeys positions are read again by each step).
 // ---------------------------------------------------------------------------
 constexpr int kSelThreads = 1024;
 constexpr int kSelWarps = kSelThreads / 32;
 constexpr int kSelBins = 2048;
-constexpr int kSelKeys = 45056;          // 176 KB of keys
+constexpr int kSelCopies = 4;            // of the counts, by lane: scores share few leading digits
+constexpr int kSelCands = 1024;
+constexpr int kSelKeys = 36864;          // 144 KB of keys
 constexpr int kSelMaxCluster = 8;
 
 struct SelSmem {
-  uint32_t hist[2][kSelBins];            // by turns: a CTA may still read the last one when the next is filled
+  uint32_t hist[2][kSelCopies][kSelBins + 8];   // by turns: a CTA may still read the last one when the next is filled
+  uint64_t cand[kSelCands];              // this CTA's candidates: key, then the complement of the position
+  uint64_t all[kSelCands];               // the cluster's
   uint32_t warp_sum[kSelWarps];
   uint32_t gt[kSelWarps], eq[kSelWarps]; // per warp: positions above the threshold (or recent), and equal to it
   uint32_t all_gt, all_eq;               // this CTA's
-  uint32_t digit, need;
+  uint32_t cands, digit, in_digit, need, key;
 };
 
+static_assert(sizeof(SelSmem) + kSelKeys * 4 <= 232448, "shared memory");
+
+__device__ __forceinline__ uint32_t cluster_word(const void* p, uint32_t rank) {
+  uint32_t at;
+  asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(at) : "r"(smem_addr(p)), "r"(rank));
+  return at;
+}
 // The word at `p` of cluster CTA `rank`'s shared memory.
 __device__ __forceinline__ uint32_t ld_cluster(const uint32_t* p, uint32_t rank) {
-  uint32_t at, v;
-  asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(at) : "r"(smem_addr(p)), "r"(rank));
-  asm volatile("ld.shared::cluster.u32 %0, [%1];" : "=r"(v) : "r"(at) : "memory");
+  uint32_t v;
+  asm volatile("ld.shared::cluster.u32 %0, [%1];" : "=r"(v) : "r"(cluster_word(p, rank)) : "memory");
+  return v;
+}
+__device__ __forceinline__ uint64_t ld_cluster(const uint64_t* p, uint32_t rank) {
+  uint64_t v;
+  asm volatile("ld.shared::cluster.u64 %0, [%1];" : "=l"(v) : "r"(cluster_word(p, rank)) : "memory");
   return v;
 }
 
@@ -98,6 +115,8 @@ __global__ void __launch_bounds__(kSelThreads, 1) evict_select_kernel(const Evic
   const uint32_t rank = blockIdx.x % cluster;
   const int64_t row = blockIdx.x / cluster;
   const int64_t b = row / a.cache.heads;
+  for (int x = tid; x < kSelCopies * (kSelBins + 8); x += kSelThreads) (&s.hist[0][0][0])[x] = 0;
+  if (tid == 0) s.cands = 0;
   pdl_wait();
   pdl_launch_dependents();
   const int32_t limit = static_cast<int32_t>(imin64(a.cache.capacity, a.scores_ld));
@@ -124,46 +143,68 @@ __global__ void __launch_bounds__(kSelThreads, 1) evict_select_kernel(const Evic
     if (held) return keys[(group - g0) * 32 + lane];
     return j < m ? score_order(sc[j]) : 0u;
   };
+  const auto sync_cluster = [&]() {
+    if (cluster > 1) {
+      cluster_arrive();
+      cluster_wait();
+    } else {
+      __syncthreads();
+    }
+  };
 
+  // keys above `prefix` stay, and `need` of those equal to it, once `shift` is 0 or
+  // the candidates have been ranked; until then those that share the bits from
+  // `shift` on are candidates
   uint32_t prefix = 0, need = static_cast<uint32_t>(a.keep - a.recent);
-  const int rounds = need > 0 ? 3 : 0;
-  if (need == 0) prefix = 0xFFFFFFFFu;   // only the recent ones stay: no key is above this one
+  int shift = 32;
+  if (need == 0) {                       // only the recent ones stay: no key is above this one
+    prefix = 0xFFFFFFFFu;
+    shift = 0;
+  }
+  __syncthreads();
 #pragma unroll 1
-  for (int round = 0; round < rounds; ++round) {
-    const int shift = round == 0 ? 21 : round == 1 ? 10 : 0;
-    const int bits = round == 2 ? 10 : 11;
-    uint32_t* hist = s.hist[round & 1];
-    for (int x = tid; x < kSelBins; x += kSelThreads) hist[x] = 0;
-    __syncthreads();
+  for (int round = 0; shift > 0; ++round) {
+    const int bits = shift == 10 ? 10 : 11;
+    auto* hist = s.hist[round & 1];
+    if (round > 0) {
+      for (int x = tid; x < kSelCopies * (kSelBins + 8); x += kSelThreads) (&hist[0][0])[x] = 0;
+      __syncthreads();
+    }
+    uint32_t* mine = hist[lane & (kSelCopies - 1)];
     if (round == 0) {
 #pragma unroll 4
       for (int32_t g = w0; g < w1; ++g) {
         const int32_t j = g * 32 + lane;
         const uint32_t key = j < m ? score_order(__ldg(sc + j)) : 0u;
         if (held) keys[(g - g0) * 32 + lane] = key;
-        if (j < m) atomicAdd(&hist[key >> 21], 1u);
+        if (j < m) atomicAdd(&mine[key >> 21], 1u);
       }
     } else {
 #pragma unroll 4
       for (int32_t g = w0; g < w1; ++g) {
         const uint32_t key = key_at(g);
-        if (g * 32 + lane < m && key >> (shift + bits) == prefix >> (shift + bits))
-          atomicAdd(&hist[key >> shift & ((1u << bits) - 1)], 1u);
+        if (g * 32 + lane < m && key >> shift == prefix >> shift)
+          atomicAdd(&mine[key >> (shift - bits) & ((1u << bits) - 1)], 1u);
       }
     }
+    shift -= bits;
     __syncthreads();
-    if (cluster > 1) {
-      cluster_arrive();
-      cluster_wait();
+    // thread t has bins 2 t and 2 t + 1, over the copies and then over the cluster; a scan
+    // from the top finds the bin that holds the need-th key
+    uint32_t c0 = 0, c1 = 0;
+#pragma unroll
+    for (int x = 0; x < kSelCopies; ++x) {
+      c0 += hist[x][2 * tid];
+      c1 += hist[x][2 * tid + 1];
     }
-    // thread t adds up bins 2 t and 2 t + 1 over the cluster; a scan from the top
-    // finds the bin that holds the need-th key
-    uint32_t c0 = hist[2 * tid], c1 = hist[2 * tid + 1];
     if (cluster > 1) {
-      c0 = c1 = 0;
-      for (int r = 0; r < cluster; ++r) {
-        c0 += ld_cluster(&hist[2 * tid], r);
-        c1 += ld_cluster(&hist[2 * tid + 1], r);
+      hist[0][2 * tid] = c0;
+      hist[0][2 * tid + 1] = c1;
+      sync_cluster();
+      for (int r = 1; r < cluster; ++r) {
+        const uint32_t other = (rank + r) % cluster;
+        c0 += ld_cluster(&hist[0][2 * tid], other);
+        c1 += ld_cluster(&hist[0][2 * tid + 1], other);
       }
     }
     const uint32_t own = c0 + c1;
@@ -175,16 +216,52 @@ __global__ void __launch_bounds__(kSelThreads, 1) evict_select_kernel(const Evic
     }
     if (lane == 0) s.warp_sum[warp] = incl;
     __syncthreads();
-    uint32_t above = incl - own;         // keys in higher bins
-    for (int w = warp + 1; w < kSelWarps; ++w) above += s.warp_sum[w];
+    uint32_t above = warp + 1 + lane < kSelWarps ? s.warp_sum[warp + 1 + lane] : 0u;   // keys in higher bins
+#pragma unroll
+    for (int d = 16; d > 0; d >>= 1) above += __shfl_xor_sync(0xFFFFFFFFu, above, d);
+    above += incl - own;
     if (above < need && above + own >= need) {
       const bool high = above + c1 >= need;
       s.digit = 2 * tid + (high ? 1 : 0);
+      s.in_digit = high ? c1 : c0;
       s.need = need - above - (high ? 0 : c1);
     }
     __syncthreads();
     prefix |= s.digit << shift;
     need = s.need;                       // how many of the keys that share the prefix stay
+    const uint32_t count = s.in_digit;
+    if (shift == 0 || count > kSelCands) continue;
+
+    // few candidates: rank them (all CTAs of the cluster do, and find the same)
+#pragma unroll 4
+    for (int32_t g = w0; g < w1; ++g) {
+      const uint32_t key = key_at(g);
+      const int32_t j = g * 32 + lane;
+      if (j < m && key >> shift == prefix >> shift)
+        s.cand[atomicAdd(&s.cands, 1u)] = static_cast<uint64_t>(key) << 32 | ~static_cast<uint32_t>(j);
+    }
+    sync_cluster();
+    uint32_t at = 0;
+    for (int r = 0; r < cluster; ++r) {
+      const uint32_t c = cluster > 1 ? ld_cluster(&s.cands, r) : s.cands;
+      if (static_cast<uint32_t>(tid) < c) s.all[at + tid] = cluster > 1 ? ld_cluster(&s.cand[tid], r) : s.cand[tid];
+      at += c;
+    }
+    __syncthreads();
+    uint64_t my = 0;
+    uint32_t before = 0;
+    if (static_cast<uint32_t>(tid) < count) {
+      my = s.all[tid];
+#pragma unroll 4
+      for (uint32_t x = 0; x < count; ++x) before += s.all[x] > my ? 1u : 0u;
+      if (before == need - 1) s.key = static_cast<uint32_t>(my >> 32);
+    }
+    __syncthreads();
+    prefix = s.key;
+    // of the keys equal to it, those that rank before it, and it, stay
+    need = __syncthreads_count(static_cast<uint32_t>(tid) < count && before < need &&
+                               static_cast<uint32_t>(my >> 32) == prefix);
+    shift = 0;
   }
 
   // counts per warp, their sums per CTA, and the CTAs before this one
@@ -201,19 +278,18 @@ __global__ void __launch_bounds__(kSelThreads, 1) evict_select_kernel(const Evic
     s.eq[warp] = eq;
   }
   __syncthreads();
-  uint32_t gt_before = 0, eq_before = 0;
-  for (int w = 0; w < warp; ++w) {
-    gt_before += s.gt[w];
-    eq_before += s.eq[w];
+  uint32_t gt_before = lane < warp ? s.gt[lane] : 0u, eq_before = lane < warp ? s.eq[lane] : 0u;
+#pragma unroll
+  for (int d = 16; d > 0; d >>= 1) {
+    gt_before += __shfl_xor_sync(0xFFFFFFFFu, gt_before, d);
+    eq_before += __shfl_xor_sync(0xFFFFFFFFu, eq_before, d);
   }
   if (cluster > 1) {
     if (tid == kSelThreads - 32) {
       s.all_gt = gt_before + gt;
       s.all_eq = eq_before + eq;
     }
-    __syncthreads();
-    cluster_arrive();
-    cluster_wait();
+    sync_cluster();
     for (uint32_t r = 0; r < rank; ++r) {
       gt_before += ld_cluster(&s.all_gt, r);
       eq_before += ld_cluster(&s.all_eq, r);
@@ -232,10 +308,7 @@ __global__ void __launch_bounds__(kSelThreads, 1) evict_select_kernel(const Evic
     gt_before += __popc(gts);
     eq_before += __popc(eqs);
   }
-  if (cluster > 1) {                     // nobody leaves while its counts may still be read
-    cluster_arrive();
-    cluster_wait();
-  }
+  if (cluster > 1) sync_cluster();       // nobody leaves while its counts may still be read
 }
 
 // eviction, step 2: the kept rows to the destination.  A CTA takes kGatherRows
@@ -310,7 +383,7 @@ cudaError_t launch_cache_evict(const EvictArgs& a, int64_t head_dim, int num_sms
   const int64_t limit = imin64(a.cache.capacity, a.scores_ld);
   // CTAs per row: while they all fit at once and a slice is still some thousand positions
   int cluster = 1;
-  while (cluster < kSelMaxCluster && rows * cluster * 2 <= num_sms && limit >= 4096 * cluster) cluster *= 2;
+  while (cluster < kSelMaxCluster && rows * cluster * 2 <= num_sms && limit > 8192 * cluster) cluster *= 2;
   const int64_t slice = ((limit + 31) / 32 + cluster * kSelWarps - 1) / (cluster * kSelWarps) * kSelThreads;
   const int key_slots = static_cast<int>(imin64(slice, kSelKeys));
   const size_t smem = sizeof(SelSmem) + static_cast<size_t>(key_slots) * 4;

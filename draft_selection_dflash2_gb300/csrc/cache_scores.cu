@@ -7,13 +7,14 @@
 // The sum runs over rows, so the product is taken keys by rows, S^T = K Q^T: a
 // key is a TMEM lane and one thread adds up its key's columns with no exchange
 // between threads.  A unit is 128 keys of one (sequence, head); its rows are taken
-// in chunks of 128 columns (the last one narrower).  All units are cut into equal
-// runs, one per CTA.
+// in chunks of up to 128 or, where there are more rows, 256 columns.  All units are
+// cut into equal runs, one per CTA.
 //   warp 0      TMA producer of K tiles (128 x D, one box per page piece).
-//   warp 1      MMA issuer: one 128 x N accumulator (fp32) per chunk, four
-//               128-column buffers in TMEM, two for each half of the epilogue.
-//   warps 4-7, 8-11  epilogue: alternate units; exp2(S c - lse c') per column,
-//               summed in fp32 in column order.
+//   warps 1, 2  MMA issuers of the even and the odd units (one warp for both was
+//               the slowest part at 136 rows: 2560 cycles a unit).
+//   warps 4-7, 8-11  epilogues of the even and the odd units: exp2(S c - lse c')
+//               per column, summed in fp32 in column order.  Each has 256 TMEM
+//               columns: two chunks of 128, or one of 256.
 // When a run enters another (sequence, head) the epilogue warps lay that head's
 // query rows out in shared memory (up to 512 rows; more rows take one launch per
 // 512) and their lse beside them.
@@ -24,17 +25,15 @@ namespace dflash2 {
 namespace {
 
 constexpr int kThreads = 384;
-constexpr int kMaxChunks = 4;           // row chunks per launch
+constexpr int kMaxQTiles = 4;           // 128-row tiles of queries per launch
 constexpr int kMaxSlots = 12;
 constexpr int kSmemLimit = 232448;      // 227 KB
 
 struct ScoresSmem {
-  uint64_t k_full[kMaxSlots], k_empty[kMaxSlots];
-  uint64_t q_full, s_full[4], s_free[4], drain;
-  float lse[kMaxChunks * kTile];        // in base 2; +inf for rows that add nothing
-  int64_t scan[kThreads / 32];
-  int64_t u0, u1, base;
-  int32_t b0;
+  uint64_t k_full[2 * kMaxSlots], k_empty[kMaxSlots];
+  uint64_t q_full, s_full[2][2], s_free[2][2], drain;   // [epilogue][TMEM buffer]
+  float lse[kMaxQTiles * kTile];        // negated, in base 2: -inf for rows that add nothing
+  RunStart run;
   uint32_t tmem;
   int abort_flag;
 };
@@ -44,7 +43,7 @@ struct ScoresPlan {
   float c;                  // scale * log2(e)
   int32_t limit;            // positions a length may reach
   int32_t row0;             // first row of this launch
-  int32_t chunks;           // row chunks that shared memory holds
+  int32_t q_tiles;          // 128-row tiles of queries that shared memory holds
   int32_t slots;            // ring of K tiles
   int32_t box_rows;
 };
@@ -52,7 +51,7 @@ struct ScoresPlan {
 // Rows of sequence b that this launch takes.
 __device__ __forceinline__ int32_t rows_of(const ScoresPlan& p, int64_t b) {
   const int32_t count = p.a.count == nullptr ? p.a.T : kv_clamp(p.a.count[b], p.a.T, p.a.err);
-  return max(0, min(count * p.a.group - p.row0, p.chunks * kTile));
+  return max(0, min(count * p.a.group - p.row0, p.q_tiles * kTile));
 }
 
 __device__ __forceinline__ int64_t units_of(const ScoresPlan& p, int64_t b) {
@@ -65,36 +64,18 @@ struct Segment {
   int32_t len, rows;
 };
 
-// Walks a run's segments; each warp keeps its own (whole warps call it).
-struct Walk {
-  int64_t u, u1, base, n_seq;
-  int32_t b, n;
-  __device__ __forceinline__ void start(const ScoresPlan& p, const ScoresSmem& s) {
-    u = uniform(s.u0);
-    u1 = uniform(s.u1);
-    base = uniform(s.base);
-    b = uniform(s.b0);
-    if (u < u1) load(p);
-  }
-  __device__ __forceinline__ void load(const ScoresPlan& p) {
-    n = static_cast<int32_t>(uniform(units_of(p, b)));
-    n_seq = static_cast<int64_t>(n) * p.a.cache.heads;
-  }
+struct Walk : RunWalk {
   __device__ __forceinline__ bool next(const ScoresPlan& p, Segment* g) {
-    if (u >= u1) return false;
-    while (u >= base + n_seq) {   // sequences without units are passed over
-      base += n_seq;
-      ++b;
-      load(p);
-    }
-    const int64_t rel = u - base;
-    g->h = static_cast<int32_t>(rel / n);
-    g->s = static_cast<int32_t>(rel % n);
-    g->e = static_cast<int32_t>(imin64(n, g->s + (u1 - u)));
-    g->b = b;
+    if (left <= 0) return false;
+    if (s == n) next_item([&](int64_t i) { return units_of(p, i); }, p.a.cache.heads);
+    g->h = uniform(item);
+    g->s = uniform(s);
+    g->e = uniform(static_cast<int32_t>(imin64(n, s + left)));
+    g->b = uniform(b);
     g->len = uniform(kv_clamp(p.a.cache_len[b], p.limit, nullptr));
     g->rows = uniform(rows_of(p, b));
-    u += g->e - g->s;
+    left -= g->e - s;
+    s = g->e;
     return true;
   }
 };
@@ -117,8 +98,43 @@ __device__ __forceinline__ void pin16(float (&v)[16]) {
                  "+f"(v[i + 6]), "+f"(v[i + 7]));
 }
 
-// columns of chunk c of `rows` rows
-__device__ __forceinline__ int chunk_cols(int rows, int c) { return min(kTile, (rows - c * kTile + 15) & ~15); }
+// How a segment's rows are cut into chunks of columns, and the epilogue's TMEM
+// buffers: their barriers' phases are counted apart, since segments of more than 128
+// rows use the first one alone.
+struct Chunks {
+  int width, count, rows;
+  __device__ __forceinline__ void set(int rows_) {
+    rows = rows_;
+    width = rows > kTile ? 2 * kTile : kTile;
+    count = (rows + width - 1) / width;
+  }
+  __device__ __forceinline__ int cols(int c) const { return min(width, (rows - c * width + 15) & ~15); }
+};
+struct Buffers {
+  uint32_t turn = 0, uses[2] = {0, 0};
+  // The next chunk's buffer and how often it has been used.
+  __device__ __forceinline__ int next(int width, uint32_t* use) {
+    const int buf = width == kTile ? static_cast<int>(turn++ & 1) : 0;
+    *use = buf ? uses[1]++ : uses[0]++;
+    return buf;
+  }
+};
+
+// A place in the sequence of K tiles through a ring of S slots.  As each issuer
+// looks at every other tile only, a slot's uses alternate between two landing
+// barriers (see RingPos).
+struct KPos {
+  uint32_t slot = 0, use = 0;
+  __device__ __forceinline__ void advance(uint32_t n, uint32_t S) {   // n <= S
+    slot += n;
+    if (slot >= S) {
+      slot -= S;
+      ++use;
+    }
+  }
+  __device__ __forceinline__ uint64_t* full(uint64_t* bars) const { return &bars[2 * slot + (use & 1)]; }
+  __device__ __forceinline__ uint32_t parity() const { return use >> 1 & 1; }
+};
 
 template <int D>
 __global__ void __launch_bounds__(kThreads, 1)
@@ -127,23 +143,25 @@ __global__ void __launch_bounds__(kThreads, 1)
   constexpr int kTileBytes = kTile * D * 2;
   extern __shared__ __align__(1024) uint8_t q_smem[];   // no static shared memory: the base is 1024-byte aligned
   const ScoresArgs& a = p.a;
-  const int S = p.slots;
-  uint8_t* ring = q_smem + p.chunks * kTileBytes;
+  const uint32_t S = p.slots;
+  const uint32_t q_half = p.q_tiles * kTile * 128;      // bytes of a 64-column block of the query rows
+  uint8_t* ring = q_smem + p.q_tiles * kTileBytes;
   ScoresSmem& s = *reinterpret_cast<ScoresSmem*>(ring + S * kTileBytes);
   const int warp = uniform(static_cast<int>(threadIdx.x >> 5)), lane = threadIdx.x & 31;
   volatile int* abort_flag = &s.abort_flag;
 
   if (threadIdx.x == 0) {
-    for (int i = 0; i < S; ++i) {
-      mbar_init(&s.k_full[i], 1);
+    for (uint32_t i = 0; i < S; ++i) {
+      mbar_init(&s.k_full[2 * i], 1);
+      mbar_init(&s.k_full[2 * i + 1], 1);
       mbar_init(&s.k_empty[i], 1);
     }
     mbar_init(&s.q_full, 2 * kTile);
     for (int i = 0; i < 4; ++i) {
-      mbar_init(&s.s_full[i], 1);
-      mbar_init(&s.s_free[i], kTile);
+      mbar_init(&s.s_full[i >> 1][i & 1], 1);
+      mbar_init(&s.s_free[i >> 1][i & 1], kTile);
     }
-    mbar_init(&s.drain, 1);
+    mbar_init(&s.drain, 2);
     s.abort_flag = 0;
     fence_mbar_init();
     tma_prefetch_desc(&tmK);
@@ -155,23 +173,23 @@ __global__ void __launch_bounds__(kThreads, 1)
   pdl_wait();
   pdl_launch_dependents();
   tc_fence_before();
-  find_run<kThreads>([&](int64_t b) { return units_of(p, b); }, a.B, a.cache.heads, 1, blockIdx.x, gridDim.x,
-                     s.scan, &s.u0, &s.u1, &s.base, &s.b0);
+  find_run<kThreads>([&](int64_t b) { return units_of(p, b); }, a.B, a.cache.heads, blockIdx.x, gridDim.x, &s.run);
   tc_fence_after();
   const uint32_t tmem = uniform(s.tmem);
   Walk walk;
-  walk.start(p, s);
+  walk.start(s.run);
   Segment g;
   bool live = true;
 
   if (warp == 0) {
     // ---- producer ----
-    uint32_t it = 0, issued = 0;
+    KPos at;
+    uint32_t issued = 0;
     const int half = lane % kHalves, row = lane / kHalves * p.box_rows;
     PageFeed pages;
     while (walk.next(p, &g)) {
       pages.start(a.cache, g.b, g.s, g.len, lane);
-      for (int u = g.s; u < g.e; ++u, ++it) {
+      for (int u = g.s; u < g.e; ++u, at.advance(1, S)) {
         const int j = u * kTile + row;
         const bool has = row < kTile && j < g.len;
         int y = j, w = g.b;
@@ -180,55 +198,61 @@ __global__ void __launch_bounds__(kThreads, 1)
           y = j & (a.cache.page_size - 1);
         }
         const uint32_t boxes = __popc(__ballot_sync(0xFFFFFFFFu, has));
-        const int slot = it % S;
-        if (it >= static_cast<uint32_t>(S)) wait_live(&s.k_empty[slot], (it / S - 1) & 1, &live, abort_flag, a.err);
+        if (at.use > 0) wait_live(&s.k_empty[at.slot], (at.use - 1) & 1, &live, abort_flag, a.err);
         live = __all_sync(0xFFFFFFFFu, live);
         if (!live) continue;
-        issued = it + 1;
-        if (lane == 0) mbar_arrive_expect_tx(&s.k_full[slot], boxes * p.box_rows * 128);
+        ++issued;
+        uint64_t* full = at.full(s.k_full);
+        if (lane == 0) mbar_arrive_expect_tx(full, boxes * p.box_rows * 128);
         __syncwarp();
-        if (has)
-          tma_load_4d(ring + slot * kTileBytes + half * kTile * 128 + row * 128, &tmK, half * 64, y, g.h, w,
-                      &s.k_full[slot]);
+        if (has) tma_load_4d(ring + at.slot * kTileBytes + half * kTile * 128 + row * 128, &tmK, half * 64, y, g.h, w, full);
       }
     }
+    // after a wait that gave up: this CTA's copies have landed before it exits (else the products have used them)
     if (lane == 0 && !live) {
-      for (uint32_t j = issued > static_cast<uint32_t>(S) ? issued - S : 0; j < issued; ++j)
-        mbar_wait_bounded(&s.k_full[j % S], (j / S) & 1, a.err);
+      KPos last;
+      const uint32_t first = issued > S ? issued - S : 0;
+      last.slot = first % S;
+      last.use = first / S;
+      for (uint32_t j = first; j < issued; ++j, last.advance(1, S))
+        mbar_wait_bounded(last.full(s.k_full), last.parity(), a.err);
     }
     __syncwarp();
-  } else if (warp == 1) {
-    // ---- MMA issuer ----
+  } else if (warp <= 2) {
+    // ---- MMA issuer of the units whose number in the run has parity e ----
+    const int e = warp - 1;
     const uint32_t elected = elect_lane();
     const uint32_t ring_addr = uniform(smem_addr(ring)), q_addr = uniform(smem_addr(q_smem));
-    uint32_t it = 0;
-    uint32_t used0 = 0, used1 = 0;    // chunks given to each half of the epilogue so far
+    KPos at;
+    at.advance(e, S);
+    Buffers bufs;
+    Chunks ch;
+    uint32_t it0 = 0;             // the run's units before this segment
     int seg = 0;
     for (; walk.next(p, &g); ++seg) {
       wait_live(&s.q_full, seg & 1, &live, abort_flag, a.err);
-      const int chunks = (g.rows + kTile - 1) / kTile;
-      for (int u = g.s; u < g.e; ++u, ++it) {
-        const int slot = it % S, e = it & 1;
-        wait_live(&s.k_full[slot], (it / S) & 1, &live, abort_flag, a.err);
-        const uint32_t k_lo = desc_lo(ring_addr + slot * kTileBytes);
-        for (int c = 0; c < chunks; ++c) {
-          const uint32_t n = e ? used1++ : used0++;
-          const int buf = 2 * e + (n & 1);
-          if (n >= 2) wait_live(&s.s_free[buf], ((n >> 1) - 1) & 1, &live, abort_flag, a.err);
+      ch.set(g.rows);
+      for (int u = g.s + ((it0 ^ e) & 1); u < g.e; u += 2, at.advance(2, S)) {
+        wait_live(at.full(s.k_full), at.parity(), &live, abort_flag, a.err);
+        const uint32_t k_lo = desc_lo(ring_addr + at.slot * kTileBytes);
+        for (int c = 0; c < ch.count; ++c) {
+          uint32_t use;
+          const int buf = bufs.next(ch.width, &use);
+          if (use > 0) wait_live(&s.s_free[e][buf], (use - 1) & 1, &live, abort_flag, a.err);
           __syncwarp();
           tc_fence_after();
           const uint32_t lead = live ? elected : 0u;
-          const uint32_t q_lo = desc_lo(q_addr + c * kTileBytes);
-          const uint32_t idesc = umma_idesc_bf16(128, chunk_cols(g.rows, c));
+          const uint32_t q_lo = desc_lo(q_addr + c * ch.width * 128);
+          const uint32_t idesc = umma_idesc_bf16(128, ch.cols(c));
 #pragma unroll
-          for (int k = 0; k < D / 16; ++k) {
-            const uint32_t o = ((k >> 2) * kTile * 128 + (k & 3) * 32) >> 4;
-            umma_ss(tmem + buf * kTile, k_lo + o, q_lo + o, idesc, k > 0 ? 1u : 0u, lead);
-          }
-          umma_commit_if(&s.s_full[buf], lead);
+          for (int k = 0; k < D / 16; ++k)
+            umma_ss(tmem + e * 2 * kTile + buf * kTile, k_lo + (((k >> 2) * kTile * 128 + (k & 3) * 32) >> 4),
+                    q_lo + (((k >> 2) * q_half + (k & 3) * 32) >> 4), idesc, k > 0 ? 1u : 0u, lead);
+          umma_commit_if(&s.s_full[e][buf], lead);
         }
-        umma_commit_if(&s.k_empty[slot], live ? elected : 0u);
+        umma_commit_if(&s.k_empty[at.slot], live ? elected : 0u);
       }
+      it0 += g.e - g.s;
     }
     umma_commit_if(&s.drain, elected);
     __syncwarp();
@@ -238,7 +262,9 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int r = threadIdx.x & (kTile - 1);
     const int tid = static_cast<int>(threadIdx.x) - kTile;
     const uint32_t lanes = static_cast<uint32_t>((warp & 3) * 32) << 16;
-    uint32_t it = 0, n = 0;
+    uint32_t it0 = 0;             // the run's units before this segment
+    Buffers bufs;
+    Chunks ch;
     while (walk.next(p, &g)) {
       // both halves have read every product of the last segment: its query rows may go
       __syncwarp();
@@ -258,52 +284,62 @@ __global__ void __launch_bounds__(kThreads, 1)
             v = *reinterpret_cast<const uint4*>(a.q + g.b * a.q_b + t * a.q_t + hq * a.q_h + piece * 8);
           }
         }
-        const int rr = row & (kTile - 1);
-        *reinterpret_cast<uint4*>(q_smem + (row / kTile) * kTileBytes + (piece >> 3) * kTile * 128 + rr * 128 +
-                                  (((piece & 7) ^ (rr & 7)) << 4)) = v;
+        *reinterpret_cast<uint4*>(q_smem + (piece >> 3) * q_half + row * 128 + (((piece & 7) ^ (row & 7)) << 4)) = v;
         if (piece == 0) s.lse[row] = -l2;
       }
       __syncwarp();
       asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
       mbar_arrive(&s.q_full);
       named_bar_sync(1, 2 * kTile);      // the rows' lse is there
-      const int chunks = (g.rows + kTile - 1) / kTile;
-      for (int u = g.s; u < g.e; ++u, ++it) {
-        if ((it & 1) != static_cast<uint32_t>(e)) continue;
+      ch.set(g.rows);
+      for (int u = g.s + ((it0 ^ e) & 1); u < g.e; u += 2) {
         uint64_t sum0 = pack2(0.0f, 0.0f), sum1 = sum0;
         const uint64_t c2 = pack2(p.c, p.c);
-        for (int c = 0; c < chunks; ++c, ++n) {
-          const int buf = 2 * e + (n & 1);
-          wait_live(&s.s_full[buf], (n >> 1) & 1, &live, abort_flag, a.err);
+        for (int c = 0; c < ch.count; ++c) {
+          uint32_t use;
+          const int buf = bufs.next(ch.width, &use);
+          wait_live(&s.s_full[e][buf], use & 1, &live, abort_flag, a.err);
           __syncwarp();
           tc_fence_after();
-          const int cols = chunk_cols(g.rows, c);
-          const float* l2 = s.lse + c * kTile;
-#pragma unroll 1
-          for (int x = 0; x < cols; x += 16) {
-            float z[16];
-            tmem_ld_x16(tmem + buf * kTile + x + lanes, z);
-            tmem_ld_wait();
-            pin16(z);
-            if (x + 16 >= cols) {        // read out: the buffer goes back
-              tc_fence_before();
-              mbar_arrive(&s.s_free[buf]);
-            }
+          const int cols = ch.cols(c);
+          const float* l2 = s.lse + c * ch.width;
+          const uint32_t tm = tmem + e * 2 * kTile + buf * kTile + lanes;
+          const auto add16 = [&](const float* z, const float* l2x) {
 #pragma unroll
             for (int y = 0; y < 16; y += 4) {
-              const float4 l = *reinterpret_cast<const float4*>(l2 + x + y);
+              const float4 l = *reinterpret_cast<const float4*>(l2x + y);
               const float2 e0 = unpack2(fma2(pack2(z[y], z[y + 1]), c2, pack2(l.x, l.y)));
               const float2 e1 = unpack2(fma2(pack2(z[y + 2], z[y + 3]), c2, pack2(l.z, l.w)));
               sum0 = add2(sum0, pack2(exp2_approx(e0.x), exp2_approx(e0.y)));
               sum1 = add2(sum1, pack2(exp2_approx(e1.x), exp2_approx(e1.y)));
             }
+          };
+          int x = 0;
+#pragma unroll 1
+          for (; x + 32 <= cols; x += 32) {
+            float z[32];
+            tmem_ld_x32(tm + x, z);
+            tmem_ld_wait();
+            pin(z);
+            add16(z, l2 + x);
+            add16(z + 16, l2 + x + 16);
           }
+          if (x < cols) {
+            float z[16];
+            tmem_ld_x16(tm + x, z);
+            tmem_ld_wait();
+            pin16(z);
+            add16(z, l2 + x);
+          }
+          tc_fence_before();
+          mbar_arrive(&s.s_free[e][buf]);
         }
         const float2 sum = unpack2(add2(sum0, sum1));
         const int j = u * kTile + r;
         if (j < g.len)
           a.scores[(static_cast<int64_t>(g.b) * a.cache.heads + g.h) * a.scores_ld + j] += sum.x + sum.y;
       }
+      it0 += g.e - g.s;
     }
   }
 
@@ -326,8 +362,8 @@ cudaError_t launch(const ScoresArgs& a, int num_sms, cudaStream_t stream) {
   p.limit = static_cast<int32_t>(imin64(c.capacity, a.scores_ld));
   if (p.limit == 0) return cudaSuccess;
   const int32_t rows = a.T * a.group;
-  p.chunks = min((rows + kTile - 1) / kTile, kMaxChunks);
-  p.slots = min(kMaxSlots, static_cast<int>((kSmemLimit - sizeof(ScoresSmem)) / kTileBytes) - p.chunks);
+  p.q_tiles = min((rows + kTile - 1) / kTile, kMaxQTiles);
+  p.slots = min(kMaxSlots, static_cast<int>((kSmemLimit - sizeof(ScoresSmem)) / kTileBytes) - p.q_tiles);
   p.box_rows = c.table != nullptr && c.page_size < kTile ? c.page_size : kTile;
   CUtensorMap tmK;
   const uint64_t kd[4] = {D, static_cast<uint64_t>(c.page_size), static_cast<uint64_t>(c.heads),
@@ -336,7 +372,7 @@ cudaError_t launch(const ScoresArgs& a, int num_sms, cudaStream_t stream) {
                           static_cast<uint64_t>(c.page_stride)};
   const uint32_t kb[4] = {64, static_cast<uint32_t>(p.box_rows), 1, 1};
   if (!make_tmap_bf16_nd(&tmK, c.k, 4, kd, ks, kb)) return cudaErrorInvalidValue;
-  const size_t smem = static_cast<size_t>(p.chunks + p.slots) * kTileBytes + sizeof(ScoresSmem);
+  const size_t smem = static_cast<size_t>(p.q_tiles + p.slots) * kTileBytes + sizeof(ScoresSmem);
   const cudaError_t e = set_smem_limit<cache_scores_kernel<D>>(kSmemLimit);
   if (e != cudaSuccess) return e;
   const int64_t most = a.B * c.heads * ((static_cast<int64_t>(p.limit) + kTile - 1) / kTile);
@@ -348,7 +384,7 @@ cudaError_t launch(const ScoresArgs& a, int num_sms, cudaStream_t stream) {
   cfg.stream = stream;
   cfg.attrs = &attr;
   cfg.numAttrs = 1;
-  for (p.row0 = 0; p.row0 < rows; p.row0 += kMaxChunks * kTile) {
+  for (p.row0 = 0; p.row0 < rows; p.row0 += kMaxQTiles * kTile) {
     const cudaError_t st = cudaLaunchKernelEx(&cfg, cache_scores_kernel<D>, tmK, p);
     if (st != cudaSuccess) return st;
   }

@@ -53,7 +53,7 @@ constexpr int kThreads = 416;
 constexpr int kChunk = 64;              // keys of an S product
 constexpr int kMaxSlots = 10;
 constexpr int kMaxRuns = 512;           // most CTAs
-constexpr int kMinRun = 1;              // least units per CTA
+constexpr int kWholeUnits = 2;           // items of up to so many units are never cut
 constexpr int kTwoTermUnits = 8;        // items of up to so many units carry P in two terms
 constexpr float kRescale = 8.0f;        // log2 of how far P may exceed 1
 
@@ -71,9 +71,7 @@ struct AttnSmem {
   uint64_t s_full[2][2], p_ready[2][2], pv_done[2][2], drain;   // [pipeline][S buffer]
   float2 ml[2][kTile];
   uint32_t bad[4];          // drafted nodes that hold a non-finite value
-  int64_t scan[kThreads / 32];
-  int64_t u0, u1, base;
-  int32_t b0;
+  RunStart run;
   uint32_t tmem;
   int abort_flag;
 };
@@ -88,6 +86,7 @@ struct AttnPlan {
   float2* part_ml;          // [2 * runs][areas][128] (m, l)
   int4* cuts;               // per run, of the item that it begins and does not end: sequence, head * pairs + pair,
                             // the last run with a part of it, the slot of its own part; or x = -1
+  bool whole;               // runs take whole items (those that start in them)
   int32_t box_rows;         // rows of a K or V box
   uint32_t q_box_bytes;
 };
@@ -128,40 +127,31 @@ struct Segment {
   __device__ __forceinline__ int count(int i) const { return tiles == 2 ? e - s : (e - s + 1 - i) >> 1; }
 };
 
-// Walks a run's segments; each warp of the CTA keeps its own (whole warps call it).
-struct Walk {
-  int64_t u, u1, u_first, base, n_seq;
-  int32_t b, n;
-  __device__ __forceinline__ void start(const AttnPlan& p, const AttnSmem& s) {
-    u = u_first = uniform(s.u0);
-    u1 = uniform(s.u1);
-    base = uniform(s.base);
-    b = uniform(s.b0);
-    if (u < u1) load(p);
-  }
-  __device__ __forceinline__ void load(const AttnPlan& p) {
-    n = static_cast<int32_t>(uniform(units_of(p.a, b)));
-    n_seq = static_cast<int64_t>(n) * p.a.cache.heads * p.pairs;
-  }
+struct Walk : RunWalk {
+  bool begun = false;
   __device__ __forceinline__ bool next(const AttnPlan& p, Segment* g) {
-    if (u >= u1) return false;
-    if (u >= base + n_seq) {
-      base += n_seq;
-      ++b;
-      load(p);
+    const auto units = [&](int64_t i) { return units_of(p.a, i); };
+    const int32_t per_seq = p.a.cache.heads * p.pairs;
+    if (left <= 0) return false;
+    if (s == n) {
+      next_item(units, per_seq);
+    } else if (p.whole && s > 0) {   // the item is the run's that it starts in
+      left -= n - s;
+      if (left <= 0) return false;
+      next_item(units, per_seq);
     }
-    const int64_t rel = u - base;
-    const int64_t item = rel / n;
-    g->s = static_cast<int32_t>(rel - item * n);
-    g->e = static_cast<int32_t>(imin64(n, g->s + (u1 - u)));
+    g->s = s;
+    g->e = p.whole ? n : static_cast<int32_t>(imin64(n, s + left));
     g->n = n;
     g->b = b;
-    g->pair = static_cast<int32_t>(item % p.pairs);
-    g->h = static_cast<int32_t>(item / p.pairs);
+    g->pair = item % p.pairs;
+    g->h = item / p.pairs;
     g->tiles = min(2, p.row_tiles - 2 * g->pair);
     g->len = uniform(kv_clamp(p.a.cache_len[b], p.a.cache.capacity, nullptr));
-    g->first = u == u_first;
-    u += g->e - g->s;
+    g->first = !begun;
+    begun = true;
+    left -= g->e - s;
+    s = g->e;
     return true;
   }
 };
@@ -237,15 +227,15 @@ __global__ void __launch_bounds__(kThreads, 1)
   pdl_launch_dependents();
   tc_fence_before();
   find_run<kThreads>([&](int64_t b) { return units_of(a, b); }, a.B, static_cast<int64_t>(a.cache.heads) * p.pairs,
-                     kMinRun, blockIdx.x, gridDim.x, s.scan, &s.u0, &s.u1, &s.base, &s.b0);
+                     blockIdx.x, gridDim.x, &s.run);
   tc_fence_after();
   const uint32_t tmem = uniform(s.tmem);
   Walk walk;
-  walk.start(p, s);
+  walk.start(s.run);
   Segment g;
   bool live = true;
 
-  if (threadIdx.x == 0 && s.u0 == s.u1) p.cuts[blockIdx.x] = make_int4(-1, 0, 0, 0);
+  if (threadIdx.x == 0 && s.run.units == 0) p.cuts[blockIdx.x] = make_int4(-1, 0, 0, 0);
   if (warp == 0) {
     // ---- producer ----
     RingPos<S> at;
@@ -621,13 +611,12 @@ __global__ void __launch_bounds__(kThreads, 1)
           p.part_ml[(static_cast<int64_t>(slot) * p.areas + area) * kTile + r] = make_float2(m, l);
         }
       }
-      if (threadIdx.x == kTile && walk.u >= walk.u1) {   // the run's last segment
-        const int64_t len = walk.u1 - walk.u_first;
-        p.cuts[blockIdx.x] = g.s == 0 && g.e < g.n
-                                 ? make_int4(g.b, g.h * p.pairs + g.pair,
-                                             static_cast<int>((walk.u1 + g.n - g.e - 1) / len), slot)
-                                 : make_int4(-1, 0, 0, 0);
-      }
+      if (threadIdx.x == kTile && walk.left <= 0)        // the run's last segment
+        p.cuts[blockIdx.x] =
+            g.s == 0 && g.e < g.n
+                ? make_int4(g.b, g.h * p.pairs + g.pair,
+                            static_cast<int>(blockIdx.x + quotient(g.n - g.e + s.run.units - 1, s.run.units)), slot)
+                : make_int4(-1, 0, 0, 0);
       // with one tile only the pipeline that took the drafted tile knows what its rows saw there
       bool fix = bad_seen != 0;
       if (merge) fix = a.k_new != nullptr && g.e == g.n && (s.bad[0] | s.bad[1] | s.bad[2] | s.bad[3]) != 0;
@@ -831,6 +820,9 @@ cudaError_t launch(const AttnArgs& a, void* workspace, int num_sms, cudaStream_t
   p.box_rows = paged && c.page_size < kTile ? c.page_size : kTile;
   p.q_box_bytes = static_cast<uint32_t>(t.tpt * a.group) * D * 2;
   const int64_t most = a.B * c.heads * t.pairs * ((static_cast<int64_t>(c.capacity) + kTile - 1) / kTile + 1);
+  // Items of at most one unit per pipeline are left whole: nothing is gained by cutting them, and nothing has to
+  // be joined.  (Longer ones are worth it: 1 x 1 over 500 positions, 5 units, 12.3 us cut, 14.9 us whole.)
+  p.whole = (static_cast<int64_t>(c.capacity) + kTile - 1) / kTile + (a.k_new != nullptr) <= kWholeUnits;
   const int runs = static_cast<int>(imin64(imin64(num_sms, kMaxRuns), imax64(most, 1)));
   p.part = static_cast<float*>(workspace);
   p.part_ml = reinterpret_cast<float2*>(p.part + static_cast<size_t>(2) * num_sms * t.areas * kTile * D);
@@ -876,7 +868,7 @@ cudaError_t launch(const AttnArgs& a, void* workspace, int num_sms, cudaStream_t
   cfg.attrs = &attr;
   cfg.numAttrs = 1;
   e = cudaLaunchKernelEx(&cfg, tree_attn_kernel<D>, tmQ, tmK, tmV, tmKn, tmVn, p);
-  if (e != cudaSuccess || runs == 1) return e;
+  if (e != cudaSuccess || runs == 1 || p.whole) return e;
   // one CTA per task up to two per SM; at most runs - 1 items are cut
   cfg.gridDim = dim3(static_cast<unsigned>(imin64(2 * num_sms, static_cast<int64_t>(runs - 1) * t.areas * (D / kJoinCols))),
                      1, 1);

@@ -599,3 +599,36 @@ def test_long_runs(handle, lens, T, heads, H, D):
         assert torch.equal(got[0], again[0]) and torch.equal(got[1], again[1])
     check_attention(got, reference(q, rows, kn, vn, sees, D ** -0.5))
     assert handle.device_error() == 0
+
+
+@pytest.mark.parametrize("n,keep,recent", [(3000, 1500, 0), (60000, 30000, 10), (300000, 123457, 4000)])
+def test_evict_where_most_scores_are_equal(handle, n, keep, recent):
+    # thousands of equal scores around the threshold: ties go to the lowest positions
+    gen = torch.Generator(device="cuda").manual_seed(n)
+    rng = np.random.default_rng(n)
+    s = np.where(rng.random((1, 2, n)) < 0.2, rng.standard_normal((1, 2, n)), 0.25).astype(np.float32)
+    cache, rows = make_cache(gen, [n], 2, 64, 0, n)
+    dst, _ = make_cache(gen, [0], 2, 64, 0, keep)
+    cl = torch.tensor([n], dtype=torch.int32, device="cuda")
+    kept, _, _ = api.cache_evict(handle, torch.from_numpy(s).cuda(), cache, cl, dst, keep, recent)
+    for h in range(2):
+        x = s[0, h, :n - recent]
+        order = np.lexsort((np.arange(n - recent), -x.astype(np.float64)))[:keep - recent]
+        want = np.concatenate([np.sort(order), np.arange(n - recent, n)])
+        assert np.array_equal(kept[0, h].cpu().numpy(), want)
+        w = torch.from_numpy(want).cuda()
+        assert torch.equal(dst.k[0, :keep, h], rows[0][0][w, h])
+    assert handle.device_error() == 0
+
+
+@pytest.mark.parametrize("lens,cap,T,heads,H,D", [([100, 0, 17], 100, 1, 8, 4, 128), ([128] * 40, 128, 17, 16, 2, 64),
+                                                  ([128, 120], 128, 40, 32, 4, 128)])
+def test_short_caches_are_taken_whole(handle, lens, cap, T, heads, H, D):
+    gen = torch.Generator(device="cuda").manual_seed(T)
+    B = len(lens)
+    cache, rows = make_cache(gen, lens, H, D, 0, cap)
+    q, kn, vn = randn(gen, B, T, heads, D), randn(gen, B, T, H, D), randn(gen, B, T, H, D)
+    sees = np.tril(np.ones((T, T), bool))[None].repeat(B, 0)
+    cl = torch.tensor(lens, dtype=torch.int32, device="cuda")
+    check_attention(api.tree_attention(handle, q, cache, cl, kn, vn), reference(q, rows, kn, vn, sees, D ** -0.5))
+    assert handle.device_error() == 0
