@@ -73,13 +73,12 @@ __global__ void __launch_bounds__(kCommitThreads) cache_commit_kernel(const Comm
 constexpr int kSelThreads = 1024;
 constexpr int kSelWarps = kSelThreads / 32;
 constexpr int kSelBins = 2048;
-constexpr int kSelCopies = 4;            // of the counts, by lane: scores share few leading digits
-constexpr int kSelCands = 1024;
+constexpr int kSelCands = 128;          // (at 1024, ranking took longer than another digit: 40 us over 32768 positions)
 constexpr int kSelKeys = 36864;          // 144 KB of keys
 constexpr int kSelMaxCluster = 8;
 
 struct SelSmem {
-  uint32_t hist[2][kSelCopies][kSelBins + 8];   // by turns: a CTA may still read the last one when the next is filled
+  uint32_t hist[2][kSelBins];            // by turns: a CTA may still read the last one when the next is filled
   uint64_t cand[kSelCands];              // this CTA's candidates: key, then the complement of the position
   uint64_t all[kSelCands];               // the cluster's
   uint32_t warp_sum[kSelWarps];
@@ -88,6 +87,7 @@ struct SelSmem {
   uint32_t cands, digit, in_digit, need, key;
 };
 
+static_assert(kSelBins == 2 * kSelThreads, "two bins a thread");
 static_assert(sizeof(SelSmem) + kSelKeys * 4 <= 232448, "shared memory");
 
 __device__ __forceinline__ uint32_t cluster_word(const void* p, uint32_t rank) {
@@ -115,7 +115,7 @@ __global__ void __launch_bounds__(kSelThreads, 1) evict_select_kernel(const Evic
   const uint32_t rank = blockIdx.x % cluster;
   const int64_t row = blockIdx.x / cluster;
   const int64_t b = row / a.cache.heads;
-  for (int x = tid; x < kSelCopies * (kSelBins + 8); x += kSelThreads) (&s.hist[0][0][0])[x] = 0;
+  s.hist[0][tid] = s.hist[0][tid + kSelThreads] = 0;
   if (tid == 0) s.cands = 0;
   pdl_wait();
   pdl_launch_dependents();
@@ -165,46 +165,38 @@ __global__ void __launch_bounds__(kSelThreads, 1) evict_select_kernel(const Evic
 #pragma unroll 1
   for (int round = 0; shift > 0; ++round) {
     const int bits = shift == 10 ? 10 : 11;
-    auto* hist = s.hist[round & 1];
+    uint32_t* hist = s.hist[round & 1];
     if (round > 0) {
-      for (int x = tid; x < kSelCopies * (kSelBins + 8); x += kSelThreads) (&hist[0][0])[x] = 0;
+      hist[tid] = hist[tid + kSelThreads] = 0;
       __syncthreads();
     }
-    uint32_t* mine = hist[lane & (kSelCopies - 1)];
     if (round == 0) {
 #pragma unroll 4
       for (int32_t g = w0; g < w1; ++g) {
         const int32_t j = g * 32 + lane;
         const uint32_t key = j < m ? score_order(__ldg(sc + j)) : 0u;
         if (held) keys[(g - g0) * 32 + lane] = key;
-        if (j < m) atomicAdd(&mine[key >> 21], 1u);
+        if (j < m) atomicAdd(&hist[key >> 21], 1u);
       }
     } else {
 #pragma unroll 4
       for (int32_t g = w0; g < w1; ++g) {
         const uint32_t key = key_at(g);
         if (g * 32 + lane < m && key >> shift == prefix >> shift)
-          atomicAdd(&mine[key >> (shift - bits) & ((1u << bits) - 1)], 1u);
+          atomicAdd(&hist[key >> (shift - bits) & ((1u << bits) - 1)], 1u);
       }
     }
     shift -= bits;
     __syncthreads();
-    // thread t has bins 2 t and 2 t + 1, over the copies and then over the cluster; a scan
-    // from the top finds the bin that holds the need-th key
-    uint32_t c0 = 0, c1 = 0;
-#pragma unroll
-    for (int x = 0; x < kSelCopies; ++x) {
-      c0 += hist[x][2 * tid];
-      c1 += hist[x][2 * tid + 1];
-    }
+    // thread t has bins 2 t and 2 t + 1, added up over the cluster; a scan from the top
+    // finds the bin that holds the need-th key
+    uint32_t c0 = hist[2 * tid], c1 = hist[2 * tid + 1];
     if (cluster > 1) {
-      hist[0][2 * tid] = c0;
-      hist[0][2 * tid + 1] = c1;
       sync_cluster();
       for (int r = 1; r < cluster; ++r) {
         const uint32_t other = (rank + r) % cluster;
-        c0 += ld_cluster(&hist[0][2 * tid], other);
-        c1 += ld_cluster(&hist[0][2 * tid + 1], other);
+        c0 += ld_cluster(&hist[2 * tid], other);
+        c1 += ld_cluster(&hist[2 * tid + 1], other);
       }
     }
     const uint32_t own = c0 + c1;
