@@ -375,14 +375,16 @@ class KVCache:
 _I32, _I64, _F32, _BF16 = torch.int32, torch.int64, torch.float32, torch.bfloat16
 
 
-def _rows(name, t, heads, dim):
-    """Checks a [B, T, heads, dim] bf16 operand -> its shape (heads None: any)."""
-    shape = t.shape
-    if (len(shape) != 4 or shape[3] != dim or (heads is not None and shape[2] != heads) or t.stride(3) != 1 or
-            not _is16(t) or not t.is_cuda):
-        raise ValueError(f"{name}: CUDA bf16 [B, T, {'heads' if heads is None else heads}, {dim}], unit stride along "
-                         "the last dimension")
-    return shape
+def _bad_rows(name, dim):
+    raise ValueError(f"{name}: CUDA bf16 [B, T, heads, {dim}] with the cache's heads and dim, unit stride along the last "
+                     "dimension")
+
+
+def _pair(k_new, v_new, shape, stride, dim):
+    """Checks the drafted nodes' keys and values: CUDA bf16 of one shape and layout."""
+    if (k_new.dtype is not _BF16 and not _is16(k_new)) or v_new.dtype is not k_new.dtype or k_new.shape != shape or \
+            v_new.shape != shape or stride[3] != 1 or v_new.stride() != stride or not (k_new.is_cuda and v_new.is_cuda):
+        raise ValueError(f"k_new, v_new: CUDA bf16 {tuple(shape)} with equal strides, unit stride along the last dimension")
 
 
 def _dense(name, t, dtype, shape):
@@ -427,24 +429,23 @@ def tree_attention(h: Handle, q, cache: KVCache, cache_len, k_new=None, v_new=No
     int64 [B, T, (T + 63) // 64], bit s % 64 of word s // 64 of node t set where t sees s (None: a chain).
     scale: 1 / sqrt(dim) when None.  workspace: device bytes of at least tree_attention_workspace(...)."""
     dim = cache.dim
-    shape = _rows("q", q, None, dim)
+    shape, qs = q.shape, q.stride()
+    if len(shape) != 4 or shape[3] != dim or qs[3] != 1 or not q.is_cuda or (q.dtype is not _BF16 and not _is16(q)):
+        _bad_rows("q", dim)
     B, T, heads, _ = shape
-    _cache_for(cache, B)
-    qs = q.stride()
+    if cache.batch < B:
+        _cache_for(cache, B)
     kp = vp = None
     ns = qs
-    if k_new is not None or v_new is not None:
-        if k_new is None or v_new is None:
-            raise ValueError("k_new, v_new: both or neither")
+    if k_new is not None and v_new is not None:
         ns = k_new.stride()
-        want = (B, T, cache.heads, dim)
-        if (_rows("k_new", k_new, cache.heads, dim) != want or _rows("v_new", v_new, cache.heads, dim) != want or
-                v_new.stride() != ns):
-            raise ValueError(f"k_new, v_new: {want} with equal strides")
+        _pair(k_new, v_new, (B, T, cache.heads, dim), ns, dim)
         kp, vp = k_new.data_ptr(), v_new.data_ptr()
+    elif k_new is not None or v_new is not None:
+        raise ValueError("k_new, v_new: both or neither")
     if out is None:
         out = _new_on(stream, shape, _BF16, q.device)
-    elif out.shape != shape or not _is16(out) or not out.is_contiguous() or not out.is_cuda:
+    elif out.shape != shape or (out.dtype is not _BF16 and not _is16(out)) or not out.is_contiguous() or not out.is_cuda:
         raise ValueError(f"out: contiguous CUDA bf16 {tuple(shape)}")
     if lse is None:
         lse = _new_on(stream, (B, T, heads), _F32, q.device)
@@ -465,12 +466,14 @@ def cache_commit(h: Handle, k_new, v_new, cache: KVCache, cache_len, count=None,
 
     k_new, v_new [B, T, kv_heads, dim]; count int32 [B] accepted nodes (None: T); path int32 [B, T] their ids
     (None: 0, 1, ...); scores fp32 [B, kv_heads, ld]: the appended positions' entries become 0."""
-    shape = _rows("k_new", k_new, cache.heads, cache.dim)
-    s = k_new.stride()
-    if _rows("v_new", v_new, cache.heads, cache.dim) != shape or v_new.stride() != s:
-        raise ValueError("v_new: shape and strides of k_new")
+    shape, s = k_new.shape, k_new.stride()
+    dim = cache.dim
+    if len(shape) != 4 or shape[3] != dim or shape[2] != cache.heads:
+        _bad_rows("k_new", dim)
+    _pair(k_new, v_new, shape, s, dim)
     B, T, heads, _ = shape
-    _cache_for(cache, B)
+    if cache.batch < B:
+        _cache_for(cache, B)
     ld, sp = 0, None
     if scores is not None:
         ld = scores.shape[-1]
@@ -489,10 +492,13 @@ def cache_scores(h: Handle, q, lse, cache: KVCache, cache_len, scores, count=Non
     """Adds to scores fp32 [B, kv_heads, ld] the attention weight that each cached position received from the
     accepted nodes (q and lse as in tree_attention, count and path as in cache_commit) -> scores."""
     dim = cache.dim
-    B, T, heads, _ = _rows("q", q, None, dim)
-    _cache_for(cache, B)
+    shape, s = q.shape, q.stride()
+    if len(shape) != 4 or shape[3] != dim or s[3] != 1 or not q.is_cuda or (q.dtype is not _BF16 and not _is16(q)):
+        _bad_rows("q", dim)
+    B, T, heads, _ = shape
+    if cache.batch < B:
+        _cache_for(cache, B)
     ld = scores.shape[-1]
-    s = q.stride()
     _check(h._lib.dflash2_cache_scores(
         h._h, q.data_ptr(), s[0], s[1], s[2], _dense("lse", lse, _F32, (B, T, heads)), cache.ref,
         _dense("cache_len", cache_len, _I32, (B,)), _opt("count", count, _I32, (B,)), _opt("path", path, _I32, (B, T)),
