@@ -59,50 +59,45 @@ __device__ __forceinline__ int64_t quotient(int64_t x, int64_t y) {
 // Where a run starts: unit `rel` of sequence b, whose items have n units each, and
 // how many units the run has.
 struct RunStart {
-  int64_t scan[16];         // scratch
   int64_t rel, units;
   int32_t b, n;
 };
 
 // Cuts the units of B sequences, per_seq items of units(b) each, into runs of equal
-// length and finds run `run`.  Whole-block.
-template <int kT, class Units>
-__device__ __forceinline__ void find_run(const Units& units, int64_t B, int64_t per_seq, int64_t run, int64_t runs,
-                                         RunStart* out) {
-  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  const int64_t chunk = quotient(B + kT - 1, kT);
-  const int64_t b_lo = tid * chunk, b_hi = imin64(B, b_lo + chunk);
-  int64_t sum = 0;
-  for (int64_t b = b_lo; b < b_hi; ++b) sum += units(b) * per_seq;
-  int64_t incl = sum;
+// length and finds run `run`.  Every warp does this for itself (32 sequences a
+// step), so that no block-wide step stands between the lengths and the first copy.
+template <class Units>
+__device__ __forceinline__ RunStart find_run(const Units& units, int64_t B, int64_t per_seq, int64_t run, int64_t runs) {
+  const int lane = threadIdx.x & 31;
+  int64_t total = 0;
+  for (int64_t b = lane; b < B; b += 32) total += units(b);
 #pragma unroll
-  for (int s = 1; s < 32; s <<= 1) {
-    const int64_t o = __shfl_up_sync(0xFFFFFFFFu, incl, s);
-    if (lane >= s) incl += o;
-  }
-  if (lane == 31) out->scan[warp] = incl;
-  __syncthreads();
-  int64_t before = incl - sum, total = 0;
+  for (int s = 16; s > 0; s >>= 1) total += __shfl_xor_sync(0xFFFFFFFFu, total, s);
+  total = uniform(total) * per_seq;
+  RunStart r = {0, 0, 0, 0};
+  const int64_t len = quotient(total + runs - 1, runs), u0 = imin64(run * len, total);
+  r.units = imin64(len, total - u0);
+  if (r.units == 0) return r;
+  int64_t base = 0;              // units before the 32 sequences at hand
+  for (int64_t b0 = 0; b0 < B; b0 += 32) {
+    const int64_t n = b0 + lane < B ? units(b0 + lane) : 0;
+    int64_t incl = n * per_seq;
 #pragma unroll
-  for (int w = 0; w < kT / 32; ++w) {
-    if (w < warp) before += out->scan[w];
-    total += out->scan[w];
-  }
-  const int64_t len = quotient(total + runs - 1, runs);
-  const int64_t u0 = imin64(run * len, total);
-  if (u0 >= before && u0 < before + sum) {
-    int64_t base = before, b = b_lo;
-    int64_t n = units(b);
-    while (u0 >= base + n * per_seq) {
-      base += n * per_seq;
-      n = units(++b);
+    for (int s = 1; s < 32; s <<= 1) {
+      const int64_t o = __shfl_up_sync(0xFFFFFFFFu, incl, s);
+      if (lane >= s) incl += o;
     }
-    out->rel = u0 - base;
-    out->b = static_cast<int32_t>(b);
-    out->n = static_cast<int32_t>(n);
+    const uint32_t past = __ballot_sync(0xFFFFFFFFu, u0 < base + incl);
+    if (past != 0) {             // the first lane whose sequence ends beyond u0
+      const int at = __ffs(past) - 1;
+      r.b = static_cast<int32_t>(b0) + at;
+      r.n = static_cast<int32_t>(__shfl_sync(0xFFFFFFFFu, n, at));
+      r.rel = u0 - base - (__shfl_sync(0xFFFFFFFFu, incl, at) - static_cast<int64_t>(r.n) * per_seq);
+      return r;
+    }
+    base += __shfl_sync(0xFFFFFFFFu, incl, 31);
   }
-  if (tid == 0) out->units = imin64(len, total - u0);
-  __syncthreads();
+  return r;
 }
 
 // Walks a run's stretches of items; each warp keeps its own (whole warps call it).

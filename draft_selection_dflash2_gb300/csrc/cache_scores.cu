@@ -33,7 +33,6 @@ struct ScoresSmem {
   uint64_t k_full[2 * kMaxSlots], k_empty[kMaxSlots];
   uint64_t q_full, s_full[2][2], s_free[2][2], drain;   // [epilogue][TMEM buffer]
   float lse[kMaxQTiles * kTile];        // negated, in base 2: -inf for rows that add nothing
-  RunStart run;
   uint32_t tmem;
   int abort_flag;
 };
@@ -170,14 +169,15 @@ __global__ void __launch_bounds__(kThreads, 1)
     tmem_alloc(&s.tmem, 512);
     tmem_relinquish();
   }
-  pdl_wait();
-  pdl_launch_dependents();
   tc_fence_before();
-  find_run<kThreads>([&](int64_t b) { return units_of(p, b); }, a.B, a.cache.heads, blockIdx.x, gridDim.x, &s.run);
+  __syncthreads();
   tc_fence_after();
   const uint32_t tmem = uniform(s.tmem);
+  pdl_wait();
+  pdl_launch_dependents();
+  const RunStart run = find_run([&](int64_t b) { return units_of(p, b); }, a.B, a.cache.heads, blockIdx.x, gridDim.x);
   Walk walk;
-  walk.start(s.run);
+  walk.start(run);
   Segment g;
   bool live = true;
 

@@ -52,6 +52,8 @@ namespace {
 constexpr int kThreads = 416;
 constexpr int kChunk = 64;              // keys of an S product
 constexpr int kMaxSlots = 10;
+constexpr int kBufs = 2;                // S buffers per pipeline (a third one, at D = 64, gained nothing)
+constexpr uint32_t kTmemO = 2 * kBufs * kChunk;   // first TMEM column of O: pipeline i's at kTmemO + i D
 constexpr int kMaxRuns = 512;           // most CTAs
 constexpr int kWholeUnits = 2;           // items of up to so many units are never cut
 constexpr int kTwoTermUnits = 8;        // items of up to so many units carry P in two terms
@@ -68,10 +70,9 @@ struct Cfg {
 struct AttnSmem {
   uint64_t kv_full[2 * kMaxSlots], kv_empty[kMaxSlots];
   uint64_t q_full, q_empty;
-  uint64_t s_full[2][2], p_ready[2][2], pv_done[2][2], drain;   // [pipeline][S buffer]
+  uint64_t s_full[2][kBufs], p_ready[2][kBufs], pv_done[2][kBufs], drain;   // [pipeline][S buffer]
   float2 ml[2][kTile];
   uint32_t bad[4];          // drafted nodes that hold a non-finite value
-  RunStart run;
   uint32_t tmem;
   int abort_flag;
 };
@@ -89,6 +90,19 @@ struct AttnPlan {
   bool whole;               // runs take whole items (those that start in them)
   int32_t box_rows;         // rows of a K or V box
   uint32_t q_box_bytes;
+};
+
+// A chunk's S buffer, and how often that has been used before.
+struct BufPos {
+  int buf = 0;
+  uint32_t use = 0;
+  __device__ __forceinline__ void advance() {
+    if (++buf == kBufs) {
+      buf = 0;
+      ++use;
+    }
+  }
+  __device__ __forceinline__ BufPos before() const { return {buf == 0 ? kBufs - 1 : buf - 1, buf == 0 ? use - 1 : use}; }
 };
 
 // The bf16 pair of what two fp32 values lose when they are rounded to bf16.
@@ -204,7 +218,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     mbar_init(&s.q_full, 1);
     mbar_init(&s.q_empty, 2);
     for (int i = 0; i < 2; ++i) {
-      for (int buf = 0; buf < 2; ++buf) {
+      for (int buf = 0; buf < kBufs; ++buf) {
         mbar_init(&s.s_full[i][buf], 1);
         mbar_init(&s.p_ready[i][buf], kTile);
         mbar_init(&s.pv_done[i][buf], 1);
@@ -223,19 +237,20 @@ __global__ void __launch_bounds__(kThreads, 1)
     tmem_alloc(&s.tmem, 512);
     tmem_relinquish();
   }
-  pdl_wait();
-  pdl_launch_dependents();
   tc_fence_before();
-  find_run<kThreads>([&](int64_t b) { return units_of(a, b); }, a.B, static_cast<int64_t>(a.cache.heads) * p.pairs,
-                     blockIdx.x, gridDim.x, &s.run);
+  __syncthreads();
   tc_fence_after();
   const uint32_t tmem = uniform(s.tmem);
+  pdl_wait();
+  pdl_launch_dependents();
+  const RunStart run = find_run([&](int64_t b) { return units_of(a, b); }, a.B,
+                                static_cast<int64_t>(a.cache.heads) * p.pairs, blockIdx.x, gridDim.x);
   Walk walk;
-  walk.start(s.run);
+  walk.start(run);
   Segment g;
   bool live = true;
 
-  if (threadIdx.x == 0 && s.run.units == 0) p.cuts[blockIdx.x] = make_int4(-1, 0, 0, 0);
+  if (threadIdx.x == 0 && run.units == 0) p.cuts[blockIdx.x] = make_int4(-1, 0, 0, 0);
   if (warp == 0) {
     // ---- producer ----
     RingPos<S> at;
@@ -307,11 +322,11 @@ __global__ void __launch_bounds__(kThreads, 1)
     // ---- S products of pipeline i ----
     const int i = warp - 1;
     const uint32_t elected = elect_lane();
-    const uint32_t tm_s = tmem + i * kTile;
+    const uint32_t tm_s = tmem + i * kBufs * kChunk;
     const uint32_t idesc = umma_idesc_bf16(128, kChunk);
     const uint32_t ring_addr = uniform(smem_addr(ring)), q_addr = uniform(smem_addr(q_smem));
     RingPos<S> seg_k;            // the segment's first K tile
-    uint32_t n = 0;              // this pipeline's chunks so far
+    BufPos at_s;       // the pipeline's next chunk
     int seg = 0;
     for (; walk.next(p, &g); ++seg) {
       const int step = g.tiles == 2 ? 1 : 2, off = g.tiles == 2 ? 0 : i;
@@ -326,10 +341,10 @@ __global__ void __launch_bounds__(kThreads, 1)
         const int chunks = g.keys(a, g.s + j * step + off) <= kChunk ? 1 : 2;
         const uint32_t k_lo = desc_lo(ring_addr + at.slot * C::kTileBytes);
         wait_live(at.full(s.kv_full), at.parity(), &live, abort_flag, a.err);
-        for (int c = 0; c < chunks; ++c, ++n) {
-          const int buf = n & 1;
-          // P of the chunk before the last lies in the buffer until its product is done
-          if (n >= 2) wait_live(&s.pv_done[i][buf], ((n >> 1) - 1) & 1, &live, abort_flag, a.err);
+        for (int c = 0; c < chunks; ++c, at_s.advance()) {
+          const int buf = at_s.buf;
+          // P of the chunk that had the buffer lies in it until its product is done
+          if (at_s.use > 0) wait_live(&s.pv_done[i][buf], (at_s.use - 1) & 1, &live, abort_flag, a.err);
           __syncwarp();
           tc_fence_after();
           const uint32_t lead = live ? elected : 0u;
@@ -355,12 +370,12 @@ __global__ void __launch_bounds__(kThreads, 1)
     // ---- O products of pipeline i ----
     const int i = warp == 3 ? 0 : 1;
     const uint32_t elected = elect_lane();
-    const uint32_t tm_s = tmem + i * kTile, tm_o = tmem + 2 * kTile + i * D;
+    const uint32_t tm_s = tmem + i * kBufs * kChunk, tm_o = tmem + kTmemO + i * D;
     const uint32_t idesc = umma_idesc_bf16(128, D) | (1u << 16);   // B is MN-major
     const uint32_t ring_addr = uniform(smem_addr(ring));
     RingPos<S> seg_v;            // the segment's first V tile
     seg_v.advance(1);
-    uint32_t n = 0;
+    BufPos at_s;
     while (walk.next(p, &g)) {
       const int step = g.tiles == 2 ? 1 : 2, off = g.tiles == 2 ? 0 : i;
       const int cnt = g.count(i);
@@ -370,9 +385,9 @@ __global__ void __launch_bounds__(kThreads, 1)
       for (int j = 0; j < cnt; ++j) {
         const int chunks = g.keys(a, g.s + j * step + off) <= kChunk ? 1 : 2;
         const uint32_t v_lo = desc_lo(ring_addr + at.slot * C::kTileBytes, kTile * 128);
-        for (int c = 0; c < chunks; ++c, ++n) {
-          const int buf = n & 1;
-          wait_live(&s.p_ready[i][buf], (n >> 1) & 1, &live, abort_flag, a.err);
+        for (int c = 0; c < chunks; ++c, at_s.advance()) {
+          const int buf = at_s.buf;
+          wait_live(&s.p_ready[i][buf], at_s.use & 1, &live, abort_flag, a.err);
           if (c == 0) wait_live(at.full(s.kv_full), at.parity(), &live, abort_flag, a.err);
           __syncwarp();
           tc_fence_after();
@@ -402,10 +417,10 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int i = warp >= 8 ? 1 : 0;
     const int r = threadIdx.x & (kTile - 1);
     const uint32_t lanes = static_cast<uint32_t>((warp & 3) * 32) << 16;
-    const uint32_t tm_s = tmem + i * kTile + lanes, tm_o = tmem + 2 * kTile + lanes;
+    const uint32_t tm_s = tmem + i * kBufs * kChunk + lanes, tm_o = tmem + kTmemO + lanes;
     RingPos<S> seg_v;            // the segment's first V tile
     seg_v.advance(1);
-    uint32_t n = 0;              // this pipeline's chunks so far
+    BufPos at_s;       // the pipeline's next chunk
     const int t_r = r / a.group;
     for (; walk.next(p, &g);) {
       const int step = g.tiles == 2 ? 1 : 2, off = g.tiles == 2 ? 0 : i;
@@ -423,7 +438,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         const int valid = g.keys(a, u);
         const int chunks = valid <= kChunk ? 1 : 2;
         const bool partial_tile = drafted || valid < chunks * kChunk;
-        wait_live(&s.s_full[i][n & 1], (n >> 1) & 1, &live, abort_flag, a.err);
+        wait_live(&s.s_full[i][at_s.buf], at_s.use & 1, &live, abort_flag, a.err);
         if (partial_tile) {
           // what the row sees of the tile, and a V tile without what nobody may see
           RingPos<S> at_v = seg_v;
@@ -481,10 +496,10 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
         }
 #pragma unroll 1
-        for (int c = 0; c < chunks; ++c, ++n) {
-          const int buf = n & 1;
+        for (int c = 0; c < chunks; ++c, at_s.advance()) {
+          const int buf = at_s.buf;
           const uint32_t tm_sb = tm_s + buf * kChunk;
-          wait_live(&s.s_full[i][buf], (n >> 1) & 1, &live, abort_flag, a.err);
+          if (c > 0) wait_live(&s.s_full[i][buf], at_s.use & 1, &live, abort_flag, a.err);
           __syncwarp();
           tc_fence_after();
           if (busy) {
@@ -515,7 +530,8 @@ __global__ void __launch_bounds__(kThreads, 1)
               const float f = m == -INFINITY ? 1.0f : exp2_approx(m - m1);
               m = m1;
               l *= f;
-              wait_live(&s.pv_done[i][buf ^ 1], ((n - 1) >> 1) & 1, &live, abort_flag, a.err);
+              const BufPos prev = at_s.before();
+              wait_live(&s.pv_done[i][prev.buf], prev.use & 1, &live, abort_flag, a.err);
               __syncwarp();
               tc_fence_after();
 #pragma unroll 1
@@ -579,7 +595,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       const bool merge = g.tiles == 1;
       float f0 = 1.0f, f1 = 0.0f;     // weights of O0 and O1 (one tile), or of O_i
       // products complete in the order of their issue: the last one's is enough
-      if (cnt > 0) wait_live(&s.pv_done[i][(n - 1) & 1], ((n - 1) >> 1) & 1, &live, abort_flag, a.err);
+      const BufPos prev = at_s.before();
+      if (cnt > 0) wait_live(&s.pv_done[i][prev.buf], prev.use & 1, &live, abort_flag, a.err);
       __syncwarp();
       if (merge) {
         // each pipeline has waited for its own products
@@ -615,7 +632,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         p.cuts[blockIdx.x] =
             g.s == 0 && g.e < g.n
                 ? make_int4(g.b, g.h * p.pairs + g.pair,
-                            static_cast<int>(blockIdx.x + quotient(g.n - g.e + s.run.units - 1, s.run.units)), slot)
+                            static_cast<int>(blockIdx.x + quotient(g.n - g.e + run.units - 1, run.units)), slot)
                 : make_int4(-1, 0, 0, 0);
       // with one tile only the pipeline that took the drafted tile knows what its rows saw there
       bool fix = bad_seen != 0;
@@ -689,104 +706,128 @@ __global__ void __launch_bounds__(kThreads, 1)
 
 // Adds the parts of the items that runs cut.  Every CTA lists the cut items from
 // the runs' records; a task is one of them, one of its row tiles and a group of
-// columns; a thread takes a row and 8 columns, and adds parts as the softmax adds
-// keys.  With many cut items (of few parts each) a task is 32 columns and a thread
-// takes every part.  With few (a few heads, a long cache, many parts each) it is 8
-// columns, thread (r, y) takes every 4th part from the y-th on, and the four sums
-// are added in order: 1 x 17 over 8191 positions, 17 parts per head, 10 us with
-// one thread per row and column group against 5.
-constexpr int kJoinSplit = 4, kJoinThreads = kTile * kJoinSplit, kJoinCols = 8;
+// columns; a thread takes a row and a few columns and adds parts as the softmax adds
+// keys.  With many cut items (of few parts each) a task is 32 columns, 8 a thread,
+// and a thread takes every part.  With few (a few heads, a long cache, many parts
+// each) it is 4 columns, thread (r, y) takes every 4th part from the y-th on, and
+// the four sums are added in order.
+constexpr int kJoinSplit = 4, kJoinThreads = kTile * kJoinSplit, kWideCols = 8, kNarrowCols = 4;
 
+template <int N>
 struct PartSum {
-  float m, l, o[kJoinCols];
-  __device__ __forceinline__ void clear() {
-    m = -INFINITY;
-    l = 0.0f;
-#pragma unroll
-    for (int k = 0; k < kJoinCols; ++k) o[k] = 0.0f;
-  }
+  float m = -INFINITY, l = 0.0f, o[N] = {};
   // Adds sums (m1, l1, v); with m1 = -inf they saw nothing, and v is not looked at.
-  __device__ __forceinline__ void add(float m1, float l1, const float (&v)[kJoinCols]) {
+  __device__ __forceinline__ void add(float m1, float l1, const float (&v)[N]) {
     const bool some = m1 != -INFINITY;
     const float top = fmaxf(m, m1);
     const float f0 = m == -INFINITY ? 0.0f : exp2_approx(m - top), f1 = some ? exp2_approx(m1 - top) : 0.0f;
     m = top;
     l = l * f0 + (some || l1 != l1 ? l1 * (some ? f1 : 1.0f) : 0.0f);   // only NaN scores: l1 is NaN
 #pragma unroll
-    for (int k = 0; k < kJoinCols; ++k) o[k] = fmaf(some ? v[k] : 0.0f, f1, o[k] * f0);
+    for (int k = 0; k < N; ++k) o[k] = fmaf(some ? v[k] : 0.0f, f1, o[k] * f0);
+  }
+  // Row r's parts of columns x.. in runs c, c + step, .. c1, kBatch loads at a time.
+  template <int D, int kBatch>
+  __device__ __forceinline__ void add_parts(const AttnPlan& p, const int4& d, int c0, int c, int step, int tile, int x,
+                                            int r) {
+    for (; c <= d.z; c += kBatch * step) {
+      float2 ml[kBatch];
+      float v[kBatch][N];
+#pragma unroll
+      for (int w = 0; w < kBatch; ++w) {
+        const int cw = c + w * step;
+        ml[w] = make_float2(-INFINITY, 0.0f);
+        if (cw > d.z) continue;
+        // a run's first segment leaves its parts in slot 2 c, its last one in 2 c + 1
+        const int64_t part = static_cast<int64_t>(cw == c0 ? d.w : 2 * cw) * p.areas + tile;
+        ml[w] = p.part_ml[part * kTile + r];
+        const float4* src = reinterpret_cast<const float4*>(p.part) + (part * (D / 4) + x / 4) * kTile + r;
+#pragma unroll
+        for (int k = 0; k < N; k += 4) *reinterpret_cast<float4*>(&v[w][k]) = src[k / 4 * kTile];
+      }
+#pragma unroll
+      for (int w = 0; w < kBatch; ++w)
+        if (c + w * step <= d.z) add(ml[w].x, ml[w].y, v[w]);
+    }
+  }
+  __device__ __forceinline__ void write(const AttnArgs& a, int64_t orow, int D, int x) const {
+    const float inv = l == 0.0f ? 0.0f : 1.0f / l;
+    uint32_t out[N / 2];
+#pragma unroll
+    for (int k = 0; k < N; k += 2) out[k / 2] = pack_bf16(o[k] * inv, o[k + 1] * inv);
+    uint32_t* dst = reinterpret_cast<uint32_t*>(a.out + orow * D + x);
+    if constexpr (N == 8)
+      *reinterpret_cast<uint4*>(dst) = make_uint4(out[0], out[1], out[2], out[3]);
+    else
+      *reinterpret_cast<uint2*>(dst) = make_uint2(out[0], out[1]);
+    if (x == 0 && a.lse != nullptr) a.lse[orow] = l == 0.0f ? -INFINITY : (m + log2f(l)) * 0.69314718055994531f;
   }
 };
 
 template <int D>
-__global__ void __launch_bounds__(kJoinThreads) tree_attn_join_kernel(const __grid_constant__ AttnPlan p, int runs) {
-  __shared__ int32_t list[kMaxRuns];
+__global__ void __launch_bounds__(kJoinThreads, 2) tree_attn_join_kernel(const __grid_constant__ AttnPlan p, int runs) {
+  __shared__ int4 list[kMaxRuns];
+  __shared__ int32_t list_run[kMaxRuns];
   __shared__ int32_t warp_n[kJoinThreads / 32];
-  __shared__ float s_o[kJoinSplit][kJoinCols + 2][kTile];
+  __shared__ float s_o[kJoinSplit][kNarrowCols + 2][kTile];
   const AttnArgs& a = p.a;
   const int tid = threadIdx.x, r = tid & (kTile - 1), y = tid / kTile;
   pdl_wait();
   pdl_launch_dependents();
-  const bool cut = tid < runs && p.cuts[tid].x >= 0;
+  const int4 mine = tid < runs ? p.cuts[tid] : make_int4(-1, 0, 0, 0);
+  const bool cut = mine.x >= 0;
   const uint32_t cuts = __ballot_sync(0xFFFFFFFFu, cut);
   if ((tid & 31) == 0) warp_n[tid >> 5] = __popc(cuts);
   __syncthreads();
   int n = 0, at = __popc(cuts & ((1u << (tid & 31)) - 1));
+#pragma unroll
   for (int w = 0; w < kJoinThreads / 32; ++w) {
     if (w < tid >> 5) at += warp_n[w];
     n += warp_n[w];
   }
-  if (cut) list[at] = tid;
+  if (cut) {
+    list[at] = mine;
+    list_run[at] = tid;
+  }
   __syncthreads();
-  const bool wide = n * p.areas * (D / (kJoinCols * kJoinSplit)) >= static_cast<int>(gridDim.x);
-  const int cols = wide ? kJoinCols * kJoinSplit : kJoinCols;
-  const int groups = D / cols;
+  const bool wide = 2 * n * p.areas * (D / (kWideCols * kJoinSplit)) >= static_cast<int>(gridDim.x);
+  const int groups = wide ? D / (kWideCols * kJoinSplit) : D / kNarrowCols;
   for (int task = blockIdx.x; task < n * p.areas * groups; task += gridDim.x) {
-    const int x = task % groups * cols + (wide ? y * kJoinCols : 0), tile = task / groups % p.areas;
-    const int c0 = list[task / groups / p.areas];
-    const int4 d = p.cuts[c0];
-    const int pair = d.y % p.pairs, h = d.y / p.pairs, c1 = d.z;
+    const int group = task % groups, tile = task / groups % p.areas;
+    const int4 d = list[task / groups / p.areas];
+    const int c0 = list_run[task / groups / p.areas];
+    const int pair = d.y % p.pairs, h = d.y / p.pairs;
     if (2 * pair + tile >= p.row_tiles) continue;
     const int node = (2 * pair + tile) * p.tpt + r / a.group;
     const bool row_ok = r < p.tpt * a.group && node < a.T;
-    PartSum sum;
-    sum.clear();
-    if (row_ok) {
-#pragma unroll 2
-      for (int c = c0 + (wide ? 0 : y); c <= c1; c += wide ? 1 : kJoinSplit) {
-        // a run's first segment leaves its parts in slot 2 c, its last one in 2 c + 1
-        const int64_t part = static_cast<int64_t>(c == c0 ? d.w : 2 * c) * p.areas + tile;
-        const float2 ml = p.part_ml[part * kTile + r];
-        const float4* src = reinterpret_cast<const float4*>(p.part) + (part * (D / 4) + x / 4) * kTile + r;
-        const float4 v0 = src[0], v1 = src[kTile];
-        const float v[kJoinCols] = {v0.x, v0.y, v0.z, v0.w, v1.x, v1.y, v1.z, v1.w};
-        sum.add(ml.x, ml.y, v);
+    const int64_t orow = (static_cast<int64_t>(d.x) * a.T + node) * a.heads + h * a.group + r % a.group;
+    if (wide) {
+      const int x = group * kWideCols * kJoinSplit + y * kWideCols;
+      PartSum<kWideCols> sum;
+      if (row_ok) {
+        sum.template add_parts<D, 2>(p, d, c0, c0, 1, tile, x, r);
+        sum.write(a, orow, D, x);
       }
-    }
-    if (!wide) {
-      s_o[y][kJoinCols][r] = sum.m;
-      s_o[y][kJoinCols + 1][r] = sum.l;
+    } else {
+      const int x = group * kNarrowCols;
+      PartSum<kNarrowCols> sum;
+      if (row_ok) sum.template add_parts<D, 4>(p, d, c0, c0 + y, kJoinSplit, tile, x, r);
+      s_o[y][kNarrowCols][r] = sum.m;
+      s_o[y][kNarrowCols + 1][r] = sum.l;
 #pragma unroll
-      for (int k = 0; k < kJoinCols; ++k) s_o[y][k][r] = sum.o[k];
+      for (int k = 0; k < kNarrowCols; ++k) s_o[y][k][r] = sum.o[k];
       __syncthreads();
-      if (y == 0) {
+      if (y == 0 && row_ok) {
 #pragma unroll
         for (int w = 1; w < kJoinSplit; ++w) {
-          float v[kJoinCols];
+          float v[kNarrowCols];
 #pragma unroll
-          for (int k = 0; k < kJoinCols; ++k) v[k] = s_o[w][k][r];
-          sum.add(s_o[w][kJoinCols][r], s_o[w][kJoinCols + 1][r], v);
+          for (int k = 0; k < kNarrowCols; ++k) v[k] = s_o[w][k][r];
+          sum.add(s_o[w][kNarrowCols][r], s_o[w][kNarrowCols + 1][r], v);
         }
+        sum.write(a, orow, D, x);
       }
       __syncthreads();
-    }
-    if (row_ok && (wide || y == 0)) {
-      const float inv = sum.l == 0.0f ? 0.0f : 1.0f / sum.l;
-      const int64_t orow = (static_cast<int64_t>(d.x) * a.T + node) * a.heads + h * a.group + r % a.group;
-      *reinterpret_cast<uint4*>(a.out + orow * D + x) =
-          make_uint4(pack_bf16(sum.o[0] * inv, sum.o[1] * inv), pack_bf16(sum.o[2] * inv, sum.o[3] * inv),
-                     pack_bf16(sum.o[4] * inv, sum.o[5] * inv), pack_bf16(sum.o[6] * inv, sum.o[7] * inv));
-      if (x == 0 && a.lse != nullptr)
-        a.lse[orow] = sum.l == 0.0f ? -INFINITY : (sum.m + log2f(sum.l)) * 0.69314718055994531f;
     }
   }
 }
@@ -870,7 +911,7 @@ cudaError_t launch(const AttnArgs& a, void* workspace, int num_sms, cudaStream_t
   e = cudaLaunchKernelEx(&cfg, tree_attn_kernel<D>, tmQ, tmK, tmV, tmKn, tmVn, p);
   if (e != cudaSuccess || runs == 1 || p.whole) return e;
   // one CTA per task up to two per SM; at most runs - 1 items are cut
-  cfg.gridDim = dim3(static_cast<unsigned>(imin64(2 * num_sms, static_cast<int64_t>(runs - 1) * t.areas * (D / kJoinCols))),
+  cfg.gridDim = dim3(static_cast<unsigned>(imin64(2 * num_sms, static_cast<int64_t>(runs - 1) * t.areas * (D / kNarrowCols))),
                      1, 1);
   cfg.blockDim = dim3(kJoinThreads, 1, 1);
   cfg.dynamicSmemBytes = 0;
