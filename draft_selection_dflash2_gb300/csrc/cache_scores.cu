@@ -7,14 +7,15 @@
 // The sum runs over rows, so the product is taken keys by rows, S^T = K Q^T: a
 // key is a TMEM lane and one thread adds up its key's columns with no exchange
 // between threads.  A unit is 128 keys of one (sequence, head); its rows are taken
-// in chunks of up to 128 or, where there are more rows, 256 columns.  All units are
-// cut into equal runs, one per CTA.
+// in equal chunks of up to 128 columns.  All units are cut into equal runs, one per
+// CTA.
 //   warp 0      TMA producer of K tiles (128 x D, one box per page piece).
 //   warps 1, 2  MMA issuers of the even and the odd units (one warp for both was
 //               the slowest part at 136 rows: 2560 cycles a unit).
 //   warps 4-7, 8-11  epilogues of the even and the odd units: exp2(S c - lse c')
-//               per column, summed in fp32 in column order.  Each has 256 TMEM
-//               columns: two chunks of 128, or one of 256.
+//               per column, summed in fp32 in column order.  Each has two TMEM buffers
+//               of 128 columns, so that a chunk's product runs under the last one's
+//               exponentials (with one buffer of 256: 1724 cycles a unit at 136 rows).
 // When a run enters another (sequence, head) the epilogue warps lay that head's
 // query rows out in shared memory (up to 512 rows; more rows take one launch per
 // 512) and their lse beside them.
@@ -97,26 +98,16 @@ __device__ __forceinline__ void pin16(float (&v)[16]) {
                  "+f"(v[i + 6]), "+f"(v[i + 7]));
 }
 
-// How a segment's rows are cut into chunks of columns, and the epilogue's TMEM
-// buffers: their barriers' phases are counted apart, since segments of more than 128
-// rows use the first one alone.
+// How a segment's rows are cut into chunks of columns.
 struct Chunks {
   int width, count, rows;
   __device__ __forceinline__ void set(int rows_) {
     rows = rows_;
-    width = rows > kTile ? 2 * kTile : kTile;
+    count = (rows + kTile - 1) / kTile;
+    width = ((rows + count - 1) / count + 15) & ~15;
     count = (rows + width - 1) / width;
   }
   __device__ __forceinline__ int cols(int c) const { return min(width, (rows - c * width + 15) & ~15); }
-};
-struct Buffers {
-  uint32_t turn = 0, uses[2] = {0, 0};
-  // The next chunk's buffer and how often it has been used.
-  __device__ __forceinline__ int next(int width, uint32_t* use) {
-    const int buf = width == kTile ? static_cast<int>(turn++ & 1) : 0;
-    *use = buf ? uses[1]++ : uses[0]++;
-    return buf;
-  }
 };
 
 // A place in the sequence of K tiles through a ring of S slots.  As each issuer
@@ -225,7 +216,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     const uint32_t ring_addr = uniform(smem_addr(ring)), q_addr = uniform(smem_addr(q_smem));
     KPos at;
     at.advance(e, S);
-    Buffers bufs;
+    uint32_t n = 0;               // chunks so far
     Chunks ch;
     uint32_t it0 = 0;             // the run's units before this segment
     int seg = 0;
@@ -235,10 +226,9 @@ __global__ void __launch_bounds__(kThreads, 1)
       for (int u = g.s + ((it0 ^ e) & 1); u < g.e; u += 2, at.advance(2, S)) {
         wait_live(at.full(s.k_full), at.parity(), &live, abort_flag, a.err);
         const uint32_t k_lo = desc_lo(ring_addr + at.slot * kTileBytes);
-        for (int c = 0; c < ch.count; ++c) {
-          uint32_t use;
-          const int buf = bufs.next(ch.width, &use);
-          if (use > 0) wait_live(&s.s_free[e][buf], (use - 1) & 1, &live, abort_flag, a.err);
+        for (int c = 0; c < ch.count; ++c, ++n) {
+          const int buf = n & 1;
+          if (n >= 2) wait_live(&s.s_free[e][buf], ((n >> 1) - 1) & 1, &live, abort_flag, a.err);
           __syncwarp();
           tc_fence_after();
           const uint32_t lead = live ? elected : 0u;
@@ -263,7 +253,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int tid = static_cast<int>(threadIdx.x) - kTile;
     const uint32_t lanes = static_cast<uint32_t>((warp & 3) * 32) << 16;
     uint32_t it0 = 0;             // the run's units before this segment
-    Buffers bufs;
+    uint32_t n = 0;               // chunks so far
     Chunks ch;
     while (walk.next(p, &g)) {
       // both halves have read every product of the last segment: its query rows may go
@@ -293,12 +283,15 @@ __global__ void __launch_bounds__(kThreads, 1)
       named_bar_sync(1, 2 * kTile);      // the rows' lse is there
       ch.set(g.rows);
       for (int u = g.s + ((it0 ^ e) & 1); u < g.e; u += 2) {
+        // the key's total so far, on its way while the products are waited for
+        const int j = u * kTile + r;
+        float* total = a.scores + (static_cast<int64_t>(g.b) * a.cache.heads + g.h) * a.scores_ld + j;
+        const float before = j < g.len ? *total : 0.0f;
         uint64_t sum0 = pack2(0.0f, 0.0f), sum1 = sum0;
         const uint64_t c2 = pack2(p.c, p.c);
-        for (int c = 0; c < ch.count; ++c) {
-          uint32_t use;
-          const int buf = bufs.next(ch.width, &use);
-          wait_live(&s.s_full[e][buf], use & 1, &live, abort_flag, a.err);
+        for (int c = 0; c < ch.count; ++c, ++n) {
+          const int buf = n & 1;
+          wait_live(&s.s_full[e][buf], (n >> 1) & 1, &live, abort_flag, a.err);
           __syncwarp();
           tc_fence_after();
           const int cols = ch.cols(c);
@@ -335,9 +328,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           mbar_arrive(&s.s_free[e][buf]);
         }
         const float2 sum = unpack2(add2(sum0, sum1));
-        const int j = u * kTile + r;
-        if (j < g.len)
-          a.scores[(static_cast<int64_t>(g.b) * a.cache.heads + g.h) * a.scores_ld + j] += sum.x + sum.y;
+        if (j < g.len) *total = before + (sum.x + sum.y);
       }
       it0 += g.e - g.s;
     }
