@@ -482,6 +482,9 @@ int dflash2_tree_attention(dflash2_handle* h, const uint16_t* q, int64_t q_batch
   dflash2::AttnArgs a;
   if (const int st = view_cache(cache, B, &a.cache)) return st;
   if (B == 0 || T == 0) return DFLASH2_OK;
+  // one 32-bit number counts the tiles of 128 keys over all sequences, kv heads and pairs of row tiles
+  if (dflash2::tree_attn_units(B, T, heads / cache->heads, cache->heads, a.cache.capacity) >= (int64_t(1) << 31))
+    return DFLASH2_ERR_UNSUPPORTED;
   if (!q || !cache_len || !out || (k_new == nullptr) != (v_new == nullptr) || (tree_mask && !k_new))
     return DFLASH2_ERR_INVALID_ARG;
   RowStrides qs = {q_batch_stride, q_token_stride, q_head_stride};
@@ -556,6 +559,8 @@ int dflash2_cache_scores(dflash2_handle* h, const uint16_t* q, int64_t q_batch_s
   dflash2::ScoresArgs a;
   if (const int st = view_cache(cache, B, &a.cache)) return st;
   if (B == 0 || T == 0) return DFLASH2_OK;
+  if (dflash2::tree_attn_units(B, 1, 1, cache->heads, a.cache.capacity) >= (int64_t(1) << 31))
+    return DFLASH2_ERR_UNSUPPORTED;
   if (!q || !lse || !cache_len || !scores) return DFLASH2_ERR_INVALID_ARG;
   RowStrides qs = {q_batch_stride, q_token_stride, q_head_stride};
   if (const int st = check_rows(&qs, B, T, heads, cache->head_dim)) return st;

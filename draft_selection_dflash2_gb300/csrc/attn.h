@@ -71,6 +71,8 @@ struct EvictArgs {
   uint32_t* err;
 };
 
+// Most key tiles that a call's items can have: fewer than 2^31.
+int64_t tree_attn_units(int64_t B, int64_t T, int64_t group, int64_t kv_heads, int64_t capacity);
 size_t tree_attn_workspace_bytes(int64_t B, int64_t T, int64_t heads, int64_t kv_heads, int64_t head_dim, int num_sms);
 cudaError_t launch_tree_attn(const AttnArgs& a, int64_t head_dim, void* workspace, int num_sms, cudaStream_t stream);
 cudaError_t launch_cache_scores(const ScoresArgs& a, int64_t head_dim, int num_sms, cudaStream_t stream);

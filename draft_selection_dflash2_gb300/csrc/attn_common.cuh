@@ -50,68 +50,70 @@ __device__ __forceinline__ T uniform(T x) {
   return __shfl_sync(0xFFFFFFFFu, x, 0);
 }
 
-// Non-negative quotient; a 64-bit division takes several times as long as a 32-bit one.
-__device__ __forceinline__ int64_t quotient(int64_t x, int64_t y) {
-  if (((x | y) >> 31) == 0) return static_cast<uint32_t>(x) / static_cast<uint32_t>(y);
-  return x / y;
-}
-
 // Where a run starts: unit `rel` of sequence b, whose items have n units each, and
 // how many units the run has.
 struct RunStart {
-  int64_t rel, units;
-  int32_t b, n;
+  int32_t rel, units, b, n;
 };
 
-// Cuts the units of B sequences, per_seq items of units(b) each, into runs of equal
-// length and finds run `run`.  Every warp does this for itself (32 sequences a
-// step), so that no block-wide step stands between the lengths and the first copy.
+// Cuts the units of B sequences, per_seq items of units(b) each (fewer than 2^31 in
+// all), into runs of equal length and finds run `run`.  Every warp does this for
+// itself, so that no block-wide step stands between the lengths and the first copy;
+// it is kept short, since a small call meets it with an empty instruction cache.
 template <class Units>
-__device__ __forceinline__ RunStart find_run(const Units& units, int64_t B, int64_t per_seq, int64_t run, int64_t runs) {
+__device__ __forceinline__ RunStart find_run(const Units& units, int32_t B, int32_t per_seq, int32_t run, int32_t runs) {
   const int lane = threadIdx.x & 31;
-  int64_t total = 0;
-  for (int64_t b = lane; b < B; b += 32) total += units(b);
-#pragma unroll
-  for (int s = 16; s > 0; s >>= 1) total += __shfl_xor_sync(0xFFFFFFFFu, total, s);
-  total = uniform(total) * per_seq;
-  RunStart r = {0, 0, 0, 0};
-  const int64_t len = quotient(total + runs - 1, runs), u0 = imin64(run * len, total);
-  r.units = imin64(len, total - u0);
-  if (r.units == 0) return r;
-  int64_t base = 0;              // units before the 32 sequences at hand
-  for (int64_t b0 = 0; b0 < B; b0 += 32) {
-    const int64_t n = b0 + lane < B ? units(b0 + lane) : 0;
-    int64_t incl = n * per_seq;
+  // the lane's sequence of the 32 at hand, and the units (of one item) up to and with it
+  int32_t n = 0, incl = 0, before = 0, b0 = 0;
+  const auto scan = [&]() {
+    n = b0 + lane < B ? units(b0 + lane) : 0;
+    incl = n;
 #pragma unroll
     for (int s = 1; s < 32; s <<= 1) {
-      const int64_t o = __shfl_up_sync(0xFFFFFFFFu, incl, s);
+      const int32_t o = __shfl_up_sync(0xFFFFFFFFu, incl, s);
       if (lane >= s) incl += o;
     }
-    const uint32_t past = __ballot_sync(0xFFFFFFFFu, u0 < base + incl);
-    if (past != 0) {             // the first lane whose sequence ends beyond u0
-      const int at = __ffs(past) - 1;
-      r.b = static_cast<int32_t>(b0) + at;
-      r.n = static_cast<int32_t>(__shfl_sync(0xFFFFFFFFu, n, at));
-      r.rel = u0 - base - (__shfl_sync(0xFFFFFFFFu, incl, at) - static_cast<int64_t>(r.n) * per_seq);
-      return r;
-    }
-    base += __shfl_sync(0xFFFFFFFFu, incl, 31);
+    incl += before;
+  };
+#pragma unroll 1
+  for (;; b0 += 32) {
+    scan();
+    if (b0 + 32 >= B) break;
+    before = __shfl_sync(0xFFFFFFFFu, incl, 31);
   }
+  const uint32_t total = uniform(__shfl_sync(0xFFFFFFFFu, incl, 31)) * static_cast<uint32_t>(per_seq);
+  const uint32_t len = (total + runs - 1) / runs;
+  const uint32_t u0 = min(run * len, total);
+  RunStart r = {0, static_cast<int32_t>(min(len, total - u0)), 0, 0};
+  if (r.units == 0) return r;
+  if (B > 32) {                  // again from the first 32, up to those that hold u0
+    before = 0;
+#pragma unroll 1
+    for (b0 = 0;; b0 += 32) {
+      scan();
+      before = __shfl_sync(0xFFFFFFFFu, incl, 31);
+      if (u0 < static_cast<uint32_t>(before * per_seq)) break;
+    }
+  }
+  // the first lane whose sequence ends beyond u0
+  const int at = __ffs(__ballot_sync(0xFFFFFFFFu, u0 < static_cast<uint32_t>(incl * per_seq))) - 1;
+  r.b = b0 + at;
+  r.n = __shfl_sync(0xFFFFFFFFu, n, at);
+  r.rel = static_cast<int32_t>(u0) - (__shfl_sync(0xFFFFFFFFu, incl, at) - r.n) * per_seq;
   return r;
 }
 
 // Walks a run's stretches of items; each warp keeps its own (whole warps call it).
 struct RunWalk {
-  int64_t left;             // units of the run still to come
+  int32_t left;             // units of the run still to come
   int32_t b, item, s, n;    // the next stretch: from unit s of n of the sequence's item
   __device__ __forceinline__ void start(const RunStart& r) {
-    left = uniform(r.units);
+    left = r.units;
     if (left <= 0) return;
-    b = uniform(r.b);
-    n = uniform(r.n);
-    const int64_t rel = uniform(r.rel);
-    item = static_cast<int32_t>(quotient(rel, n));
-    s = static_cast<int32_t>(rel - static_cast<int64_t>(item) * n);
+    b = r.b;
+    n = r.n;
+    item = static_cast<uint32_t>(r.rel) / static_cast<uint32_t>(n);
+    s = r.rel - item * n;
   }
   // The item after this one (sequences without units are passed over).
   template <class Units>
@@ -120,7 +122,7 @@ struct RunWalk {
     if (++item < per_seq) return;
     item = 0;
     do {
-      n = static_cast<int32_t>(uniform(units(++b)));
+      n = uniform(units(++b));
     } while (n == 0);
   }
 };

@@ -54,7 +54,7 @@ __device__ __forceinline__ int32_t rows_of(const ScoresPlan& p, int64_t b) {
   return max(0, min(count * p.a.group - p.row0, p.q_tiles * kTile));
 }
 
-__device__ __forceinline__ int64_t units_of(const ScoresPlan& p, int64_t b) {
+__device__ __forceinline__ int32_t units_of(const ScoresPlan& p, int32_t b) {
   const int32_t n = kv_clamp(p.a.cache_len[b], p.limit, p.a.err);
   return rows_of(p, b) > 0 ? (n + kTile - 1) / kTile : 0;
 }
@@ -67,10 +67,10 @@ struct Segment {
 struct Walk : RunWalk {
   __device__ __forceinline__ bool next(const ScoresPlan& p, Segment* g) {
     if (left <= 0) return false;
-    if (s == n) next_item([&](int64_t i) { return units_of(p, i); }, p.a.cache.heads);
+    if (s == n) next_item([&](int32_t i) { return units_of(p, i); }, p.a.cache.heads);
     g->h = uniform(item);
     g->s = uniform(s);
-    g->e = uniform(static_cast<int32_t>(imin64(n, s + left)));
+    g->e = uniform(min(n, s + left));
     g->b = uniform(b);
     g->len = uniform(kv_clamp(p.a.cache_len[b], p.limit, nullptr));
     g->rows = uniform(rows_of(p, b));
@@ -166,7 +166,8 @@ __global__ void __launch_bounds__(kThreads, 1)
   const uint32_t tmem = uniform(s.tmem);
   pdl_wait();
   pdl_launch_dependents();
-  const RunStart run = find_run([&](int64_t b) { return units_of(p, b); }, a.B, a.cache.heads, blockIdx.x, gridDim.x);
+  const RunStart run = find_run([&](int32_t b) { return units_of(p, b); }, static_cast<int32_t>(a.B), a.cache.heads,
+                                blockIdx.x, gridDim.x);
   Walk walk;
   walk.start(run);
   Segment g;

@@ -112,10 +112,9 @@ __device__ __forceinline__ uint32_t remainder_bf16(float x, float y) {
 }
 
 // Key tiles of sequence b, the drafted one included (at least one, so that every row is written).
-__device__ __forceinline__ int64_t units_of(const AttnArgs& a, int64_t b) {
+__device__ __forceinline__ int32_t units_of(const AttnArgs& a, int32_t b) {
   const int32_t n = kv_clamp(a.cache_len[b], a.cache.capacity, a.err);
-  const int64_t u = (static_cast<int64_t>(n) + kTile - 1) / kTile + (a.k_new != nullptr ? 1 : 0);
-  return u > 0 ? u : 1;
+  return max(1, (n + kTile - 1) / kTile + (a.k_new != nullptr ? 1 : 0));
 }
 
 // One item's stretch of a run.
@@ -144,7 +143,7 @@ struct Segment {
 struct Walk : RunWalk {
   bool begun = false;
   __device__ __forceinline__ bool next(const AttnPlan& p, Segment* g) {
-    const auto units = [&](int64_t i) { return units_of(p.a, i); };
+    const auto units = [&](int32_t i) { return units_of(p.a, i); };
     const int32_t per_seq = p.a.cache.heads * p.pairs;
     if (left <= 0) return false;
     if (s == n) {
@@ -155,11 +154,11 @@ struct Walk : RunWalk {
       next_item(units, per_seq);
     }
     g->s = s;
-    g->e = p.whole ? n : static_cast<int32_t>(imin64(n, s + left));
+    g->e = p.whole ? n : min(n, s + left);
     g->n = n;
     g->b = b;
-    g->pair = item % p.pairs;
-    g->h = item / p.pairs;
+    g->h = p.pairs == 1 ? item : item / p.pairs;
+    g->pair = item - g->h * p.pairs;
     g->tiles = min(2, p.row_tiles - 2 * g->pair);
     g->len = uniform(kv_clamp(p.a.cache_len[b], p.a.cache.capacity, nullptr));
     g->first = !begun;
@@ -243,8 +242,8 @@ __global__ void __launch_bounds__(kThreads, 1)
   const uint32_t tmem = uniform(s.tmem);
   pdl_wait();
   pdl_launch_dependents();
-  const RunStart run = find_run([&](int64_t b) { return units_of(a, b); }, a.B,
-                                static_cast<int64_t>(a.cache.heads) * p.pairs, blockIdx.x, gridDim.x);
+  const RunStart run = find_run([&](int32_t b) { return units_of(a, b); }, static_cast<int32_t>(a.B),
+                                a.cache.heads * p.pairs, blockIdx.x, gridDim.x);
   Walk walk;
   walk.start(run);
   Segment g;
@@ -632,7 +631,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         p.cuts[blockIdx.x] =
             g.s == 0 && g.e < g.n
                 ? make_int4(g.b, g.h * p.pairs + g.pair,
-                            static_cast<int>(blockIdx.x + quotient(g.n - g.e + run.units - 1, run.units)), slot)
+                            static_cast<int>(blockIdx.x + (g.n - g.e + run.units - 1) / run.units), slot)
                 : make_int4(-1, 0, 0, 0);
       // with one tile only the pipeline that took the drafted tile knows what its rows saw there
       bool fix = bad_seen != 0;
@@ -860,7 +859,8 @@ cudaError_t launch(const AttnArgs& a, void* workspace, int num_sms, cudaStream_t
   const bool paged = c.table != nullptr;
   p.box_rows = paged && c.page_size < kTile ? c.page_size : kTile;
   p.q_box_bytes = static_cast<uint32_t>(t.tpt * a.group) * D * 2;
-  const int64_t most = a.B * c.heads * t.pairs * ((static_cast<int64_t>(c.capacity) + kTile - 1) / kTile + 1);
+  const int64_t most = tree_attn_units(a.B, a.T, a.group, c.heads, c.capacity);
+  if (most >= (int64_t(1) << 31)) return cudaErrorInvalidConfiguration;   // the entry point has refused it
   // Items of at most one unit per pipeline are left whole: nothing is gained by cutting them, and nothing has to
   // be joined.  (Longer ones are worth it: 1 x 1 over 500 positions, 5 units, 12.3 us cut, 14.9 us whole.)
   p.whole = (static_cast<int64_t>(c.capacity) + kTile - 1) / kTile + (a.k_new != nullptr) <= kWholeUnits;
@@ -919,6 +919,10 @@ cudaError_t launch(const AttnArgs& a, void* workspace, int num_sms, cudaStream_t
 }
 
 }  // namespace
+
+int64_t tree_attn_units(int64_t B, int64_t T, int64_t group, int64_t kv_heads, int64_t capacity) {
+  return B * kv_heads * tile_rows(T, group).pairs * ((capacity + kTile - 1) / kTile + 1);
+}
 
 size_t tree_attn_workspace_bytes(int64_t, int64_t T, int64_t heads, int64_t kv_heads, int64_t head_dim, int num_sms) {
   const int64_t group = heads / kv_heads;

@@ -470,7 +470,8 @@ typedef struct dflash2_kv_cache {
  *                 bytes, 256-byte aligned, rewritten by every call; calls that
  *                 overlap on the GPU must not share it
  * T <= 128; heads a multiple of cache->heads, at most 128 times as many; B <=
- * 65535; q, k_new and v_new 16-byte aligned, strides multiples of 8.  Dot
+ * 65535; B * cache->heads * (capacity / 128 + 1) * (pairs of 128 query rows per kv
+ * head) < 2^31; q, k_new and v_new 16-byte aligned, strides multiples of 8.  Dot
  * products, sums and statistics are fp32; the weights enter the product with the
  * values as bf16.  The same inputs give the same bits on every call.
  */
