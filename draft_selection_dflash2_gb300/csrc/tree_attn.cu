@@ -191,6 +191,46 @@ __device__ __forceinline__ void zero_rows(uint8_t* tile, int from, int to, int t
       *reinterpret_cast<uint4*>(tile + half * kTile * 128 + from * 128 + x * 16) = make_uint4(0, 0, 0, 0);
 }
 
+// The warp's rows of O (`cols` columns at tm) times f.  Out of line: it is rarely called.
+__device__ __noinline__ void rescale_rows(uint32_t tm, int cols, float f) {
+#pragma unroll 1
+  for (int x = 0; x < cols; x += 32) {
+    float o[32];
+    tmem_ld_x32(tm + x, o);
+    tmem_ld_wait();
+    pin(o);
+#pragma unroll
+    for (int w = 0; w < 32; w += 16) {
+      uint32_t ob[16];
+#pragma unroll
+      for (int y = 0; y < 16; ++y) ob[y] = __float_as_uint(o[w + y] * f);
+      tmem_st_x16(tm + x + w, ob);
+    }
+  }
+}
+
+// Adds the non-finite values of the drafted nodes in `bad` that node `node` sees to
+// its row's columns [c0, c1): of the output (part = nullptr), or of the run's part,
+// four columns every kTile float4.  Out of line: it is hardly ever called.
+__device__ __noinline__ void add_non_finite(const AttnArgs& a, const uint32_t* bad, int b, int h, int node, int c0, int c1,
+                                            uint16_t* out, float* part) {
+  for (int sn = 0; sn < a.T; ++sn) {
+    if (!(bad[sn >> 5] >> (sn & 31) & 1u)) continue;
+    const bool sees = a.mask == nullptr ? sn <= node
+                                        : a.mask[(static_cast<int64_t>(b) * a.T + node) * ((a.T + 63) >> 6) + (sn >> 6)] >>
+                                                  (sn & 63) & 1;
+    if (!sees) continue;
+    const uint16_t* v = a.v_new + b * a.new_b + sn * a.new_t + h * a.new_h;
+    for (int x = c0; x < c1; ++x) {
+      if (finite_bf16(v[x])) continue;
+      if (part != nullptr)
+        part[static_cast<int64_t>(x >> 2) * kTile * 4 + (x & 3)] += bf16_bits_to_float(v[x]);
+      else
+        out[x] = __bfloat16_as_ushort(__float2bfloat16_rn(bf16_bits_to_float(out[x]) + bf16_bits_to_float(v[x])));
+    }
+  }
+}
+
 // 227 KB, the opt-in limit of a block, is just enough at D = 128
 static_assert(Cfg<128>::kRing + sizeof(AttnSmem) <= 232448, "shared memory");
 
@@ -533,20 +573,7 @@ __global__ void __launch_bounds__(kThreads, 1)
               wait_live(&s.pv_done[i][prev.buf], prev.use & 1, &live, abort_flag, a.err);
               __syncwarp();
               tc_fence_after();
-#pragma unroll 1
-              for (int x = 0; x < D; x += 32) {
-                float o[32];
-                tmem_ld_x32(tm_o + i * D + x, o);
-                tmem_ld_wait();
-                pin(o);
-#pragma unroll
-                for (int w = 0; w < 32; w += 16) {
-                  uint32_t ob[16];
-#pragma unroll
-                  for (int y = 0; y < 16; ++y) ob[y] = __float_as_uint(o[w + y] * f);
-                  tmem_st_x16(tm_o + i * D + x + w, ob);
-                }
-              }
+              rescale_rows(tm_o + i * D, D, f);
             }
             const float mm = m == -INFINITY ? 0.0f : m;   // a row that has seen nothing: all its P are 2^-inf
             const uint64_t c2 = pack2(p.c, p.c), m2 = pack2(-mm, -mm);
@@ -657,21 +684,6 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
           for (int y = 0; y < 32; ++y) o[y] = 0.0f;
         }
-        if (fix && row_ok) {
-#pragma unroll 1
-          for (int sn = 0; sn < a.T; ++sn) {
-            if (!(s.bad[sn >> 5] >> (sn & 31) & 1u)) continue;
-            const bool sees = a.mask == nullptr
-                                  ? sn <= node
-                                  : a.mask[(static_cast<int64_t>(g.b) * a.T + node) * ((a.T + 63) >> 6) + (sn >> 6)] >>
-                                            (sn & 63) & 1;
-            if (!sees) continue;
-            const uint16_t* vn = a.v_new + g.b * a.new_b + sn * a.new_t + g.h * a.new_h + x;
-#pragma unroll
-            for (int y = 0; y < 32; ++y)
-              if (!finite_bf16(vn[y])) o[y] += bf16_bits_to_float(vn[y]);
-          }
-        }
         if (whole) {
           if (row_ok) {
             uint4* dst = reinterpret_cast<uint4*>(a.out + orow * D + x);
@@ -687,6 +699,10 @@ __global__ void __launch_bounds__(kThreads, 1)
           for (int y = 0; y < 32; y += 4) dst[(y / 4) * kTile] = make_float4(o[y], o[y + 1], o[y + 2], o[y + 3]);
         }
       }
+      if (fix && row_ok)
+        add_non_finite(a, s.bad, g.b, g.h, node, c0, c1, a.out + orow * D,
+                       whole ? nullptr
+                             : p.part + (((static_cast<int64_t>(slot) * p.areas + area) * (D / 4)) * kTile + r) * 4);
       __syncwarp();
       tc_fence_before();
       // O and the shared statistics may be overwritten once both pipelines have read them
