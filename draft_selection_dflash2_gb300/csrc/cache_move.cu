@@ -398,9 +398,7 @@ cudaError_t launch_cache_evict(const EvictArgs& a, int64_t head_dim, int num_sms
   if (e != cudaSuccess) return e;
   const int vecs = static_cast<int>(head_dim / 8);
   const int per_cta = kGatherThreads / vecs * 4;
-  // grid.x holds 2^31 - 1 blocks
-  const int64_t blocks = (a.keep + per_cta - 1) / per_cta;
-  if (rows * blocks >= (int64_t(1) << 31)) return cudaErrorInvalidConfiguration;
+  const int64_t blocks = (a.keep + per_cta - 1) / per_cta;   // grid.x: rows * blocks < 2^31 (checked by the entry point)
   cfg.gridDim = dim3(static_cast<unsigned>(rows * blocks), 1, 1);
   cfg.blockDim = dim3(kGatherThreads, 1, 1);
   cfg.dynamicSmemBytes = 0;

@@ -56,7 +56,7 @@ constexpr int kBufs = 2;                // S buffers per pipeline (a third one, 
 constexpr uint32_t kTmemO = 2 * kBufs * kChunk;   // first TMEM column of O: pipeline i's at kTmemO + i D
 constexpr int kMaxRuns = 512;           // most CTAs
 constexpr int kWholeUnits = 2;           // items of up to so many units are never cut
-constexpr int kTwoTermUnits = 8;        // items of up to so many units carry P in two terms
+constexpr int kTwoTermUnits = 4;        // items of up to so many units carry P in two terms
 constexpr float kRescale = 8.0f;        // log2 of how far P may exceed 1
 
 template <int D>

@@ -632,3 +632,23 @@ def test_short_caches_are_taken_whole(handle, lens, cap, T, heads, H, D):
     cl = torch.tensor(lens, dtype=torch.int32, device="cuda")
     check_attention(api.tree_attention(handle, q, cache, cl, kn, vn), reference(q, rows, kn, vn, sees, D ** -0.5))
     assert handle.device_error() == 0
+
+
+def test_refusals_of_what_passes_the_counters(handle):
+    # 2^24 tiles of 128 keys a sequence, 4 kv heads, 64 sequences: 2^32 units
+    k = torch.zeros(4, 128, 4, 64, dtype=torch.bfloat16, device="cuda")
+    cache = api.KVCache(k, k.clone(), torch.zeros(64, 4, dtype=torch.int32, device="cuda"))
+    cache.struct.max_pages = cache.struct.table_ld = (1 << 24) - 2
+    q = torch.zeros(64, 1, 4, 64, dtype=torch.bfloat16, device="cuda")
+    cl = torch.zeros(64, dtype=torch.int32, device="cuda")
+    with pytest.raises(api.Dflash2Error) as e:
+        api.tree_attention(handle, q, cache, cl)
+    assert e.value.status == -2
+    with pytest.raises(api.Dflash2Error) as e:
+        api.cache_scores(handle, q, torch.zeros(64, 1, 4, device="cuda"), cache, cl, torch.zeros(64, 4, 8, device="cuda"))
+    assert e.value.status == -2
+    cache.struct.max_pages = 1 << 24                     # a capacity of 2^31
+    with pytest.raises(api.Dflash2Error) as e:
+        api.tree_attention(handle, q[:1], cache, cl[:1])
+    assert e.value.status == -2
+    assert handle.device_error() == 0
