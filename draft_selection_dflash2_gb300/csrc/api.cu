@@ -598,7 +598,7 @@ int dflash2_cache_evict(dflash2_handle* h, const float* scores, int64_t scores_l
   if (const int st = view_cache(dst, B, &a.dst)) return st;
   if (cache->heads != dst->heads || cache->head_dim != dst->head_dim) return DFLASH2_ERR_INVALID_ARG;
   if (B > 65535 || B * cache->heads >= (int64_t(1) << 24) ||
-      B * cache->heads * (keep / 64 + 1) >= (int64_t(1) << 31))
+      B * cache->heads * (keep / 16 + 1) >= (int64_t(1) << 31))
     return DFLASH2_ERR_UNSUPPORTED;
   if (B == 0) return DFLASH2_OK;
   if (keep > a.dst.capacity || !scores || !cache_len || !kept || !new_len || new_len == cache_len ||

@@ -303,14 +303,15 @@ __global__ void __launch_bounds__(kSelThreads, 1) evict_select_kernel(const Evic
   if (cluster > 1) sync_cluster();       // nobody leaves while its counts may still be read
 }
 
-// eviction, step 2: the kept rows to the destination.  A CTA takes kGatherRows
-// kept positions of one (b, h); a thread has several rows' 16 bytes of K and of V in
-// flight, so that the chain position -> page -> row is walked once for all of them.
-constexpr int kGatherThreads = 256;
+// eviction, step 2: the kept rows to the destination.  A thread takes 16 bytes of K
+// and of V of kGatherPasses kept positions at once, so that the chain position ->
+// page -> row is walked once for all of them (2 positions in CTAs of 128 threads:
+// 192 us for the whole eviction of 16 x 32768 to 8001; 4 in 256: 198, 1 in 256: 198).
+constexpr int kGatherThreads = 128, kGatherPasses = 2;
 
 template <int D>
 __global__ void __launch_bounds__(kGatherThreads) evict_gather_kernel(const EvictArgs a, int32_t blocks_per_row) {
-  constexpr int kVecs = D / 8, kRowsPerPass = kGatherThreads / kVecs, kPasses = 4;
+  constexpr int kVecs = D / 8, kRowsPerPass = kGatherThreads / kVecs, kPasses = kGatherPasses;
   constexpr int kRows = kRowsPerPass * kPasses;
   const int64_t row = blockIdx.x / blocks_per_row;
   const int32_t i0 = static_cast<int32_t>(blockIdx.x % blocks_per_row) * kRows;
@@ -397,7 +398,7 @@ cudaError_t launch_cache_evict(const EvictArgs& a, int64_t head_dim, int num_sms
   e = cudaLaunchKernelEx(&cfg, evict_select_kernel, a, cluster, key_slots);
   if (e != cudaSuccess) return e;
   const int vecs = static_cast<int>(head_dim / 8);
-  const int per_cta = kGatherThreads / vecs * 4;
+  const int per_cta = kGatherThreads / vecs * kGatherPasses;
   const int64_t blocks = (a.keep + per_cta - 1) / per_cta;   // grid.x: rows * blocks < 2^31 (checked by the entry point)
   cfg.gridDim = dim3(static_cast<unsigned>(rows * blocks), 1, 1);
   cfg.blockDim = dim3(kGatherThreads, 1, 1);

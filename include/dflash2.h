@@ -536,7 +536,7 @@ int dflash2_cache_scores(dflash2_handle* h, const uint16_t* q, int64_t q_batch_s
  *   new_len     device int32 [B]: min(cache_len, keep)
  *   dst_scores  device fp32 [B, heads, dst_ld], dst_ld >= keep, or NULL: the
  *               kept positions' scores; must not overlap scores
- * 1 <= keep, 0 <= recent <= keep; B * heads < 2^24; B * heads * (keep / 64 + 1) <
+ * 1 <= keep, 0 <= recent <= keep; B * heads < 2^24; B * heads * (keep / 16 + 1) <
  * 2^31.  A length outside [0, min(capacity, scores_ld)] is clamped and flagged.
  */
 int dflash2_cache_evict(dflash2_handle* h, const float* scores, int64_t scores_ld, const dflash2_kv_cache* cache,
