@@ -1,14 +1,17 @@
-"""ctypes loader for libdflash2.so (the CUDA kernels behind the C ABI).
+"""Loaders of libdflash2.so (the CUDA kernels behind the C ABI; ctypes) and of
+_dflash2_bind.so (compiled argument marshalling for the calls whose kernels are shortest).
 
 There is no fallback: if the library has not been built for this machine,
 loading raises immediately.
 """
 import ctypes
+import importlib.util
 import os
 import re
 
 HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(HERE, "libdflash2.so")
+BIND_PATH = os.path.join(HERE, "_dflash2_bind.so")
 HEADER = os.path.join(os.path.dirname(HERE), "include", "dflash2.h")
 
 P = ctypes.c_void_p
@@ -86,3 +89,24 @@ def load():
             fn.argtypes = args
         _lib = lib
     return _lib
+
+
+_bind = None
+
+
+def load_bind():
+    """The compiled half of the binding, calling the loaded library's entry points."""
+    global _bind
+    if _bind is None:
+        import torch  # noqa: F401  (the module's symbols come from torch's libraries)
+        lib = load()
+        if not os.path.exists(BIND_PATH):
+            raise RuntimeError(f"{BIND_PATH} is missing: build it first "
+                               "(python -c 'import __graft_entry__ as g; g.build()')")
+        spec = importlib.util.spec_from_file_location("_dflash2_bind", BIND_PATH)
+        mod = importlib.util.module_from_spec(spec)
+        spec.loader.exec_module(mod)
+        mod.init(*(ctypes.cast(getattr(lib, "dflash2_" + f), P).value
+                   for f in ("tree_attention", "cache_commit", "cache_scores", "cache_evict")))
+        _bind = mod
+    return _bind

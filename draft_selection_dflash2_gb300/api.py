@@ -2,7 +2,8 @@
 
 Every function has the name of the C entry point it calls (without the
 ``dflash2_`` prefix) and runs entirely in the CUDA library: torch tensors only
-supply device memory and the current stream.  bf16 tensors may be given as
+supply device memory and the current stream.  The cache operators' arguments are
+checked and passed on by the compiled module _dflash2_bind.  bf16 tensors may be given as
 torch.bfloat16 or as int16/uint16 bit patterns.  Outputs that are not passed in
 are allocated with torch before the call (the library itself never allocates).
 """
@@ -70,6 +71,8 @@ class Handle:
         h = ctypes.c_void_p()
         _check(self._lib.dflash2_create(device, ctypes.byref(h)), "dflash2_create")
         self._h = h
+        self.raw = h.value
+        self._bind = _lib.load_bind()
 
     @property
     def ptr(self):
@@ -89,6 +92,7 @@ class Handle:
         if self._h is not None and self._h.value:
             _check(self._lib.dflash2_destroy(self._h), "dflash2_destroy")
         self._h = None
+        self.raw = 0
 
     def __enter__(self):
         return self
@@ -369,33 +373,8 @@ class KVCache:
         self.batch = pages if block_table is None else block_table.shape[0]
         self.capacity = page * s.max_pages
         self.heads, self.dim = heads, dim
-        self.ref = ctypes.byref(s)
+        self.addr = ctypes.addressof(s)
 
-
-_I32, _I64, _F32, _BF16 = torch.int32, torch.int64, torch.float32, torch.bfloat16
-
-
-def _bad_rows(name, dim):
-    raise ValueError(f"{name}: CUDA bf16 [B, T, heads, {dim}] with the cache's heads and dim, unit stride along the last "
-                     "dimension")
-
-
-def _pair(k_new, v_new, shape, stride, dim):
-    """Checks the drafted nodes' keys and values: CUDA bf16 of one shape and layout."""
-    if (k_new.dtype is not _BF16 and not _is16(k_new)) or v_new.dtype is not k_new.dtype or k_new.shape != shape or \
-            v_new.shape != shape or stride[3] != 1 or v_new.stride() != stride or not (k_new.is_cuda and v_new.is_cuda):
-        raise ValueError(f"k_new, v_new: CUDA bf16 {tuple(shape)} with equal strides, unit stride along the last dimension")
-
-
-def _dense(name, t, dtype, shape):
-    """Checks a contiguous CUDA tensor of one type and shape -> its address."""
-    if t.dtype is not dtype or t.shape != shape or not t.is_contiguous() or not t.is_cuda:
-        raise ValueError(f"{name}: contiguous CUDA {dtype} {tuple(shape)}")
-    return t.data_ptr()
-
-
-def _opt(name, t, dtype, shape):
-    return None if t is None else _dense(name, t, dtype, shape)
 
 
 def _raw_stream(h, stream):
@@ -412,11 +391,6 @@ def _new_on(stream, shape, dtype, dev):
         return torch.empty(shape, dtype=dtype, device=dev)
 
 
-def _cache_for(cache, B):
-    if cache.batch < B:
-        raise ValueError(f"cache: {cache.batch} sequences, {B} wanted")
-
-
 def tree_attention_workspace(h: Handle, B: int, T: int, heads: int, kv_heads: int, head_dim: int) -> int:
     return int(h._lib.dflash2_tree_attention_workspace(h.ptr, B, T, heads, kv_heads, head_dim))
 
@@ -428,35 +402,21 @@ def tree_attention(h: Handle, q, cache: KVCache, cache_len, k_new=None, v_new=No
     q [B, T, heads, dim]; k_new, v_new [B, T, kv_heads, dim] (equal strides; None: the cache alone); tree_mask
     int64 [B, T, (T + 63) // 64], bit s % 64 of word s // 64 of node t set where t sees s (None: a chain).
     scale: 1 / sqrt(dim) when None.  workspace: device bytes of at least tree_attention_workspace(...)."""
-    dim = cache.dim
-    shape, qs = q.shape, q.stride()
-    if len(shape) != 4 or shape[3] != dim or qs[3] != 1 or not q.is_cuda or (q.dtype is not _BF16 and not _is16(q)):
-        _bad_rows("q", dim)
-    B, T, heads, _ = shape
-    if cache.batch < B:
-        _cache_for(cache, B)
-    kp = vp = None
-    ns = qs
-    if k_new is not None and v_new is not None:
-        ns = k_new.stride()
-        _pair(k_new, v_new, (B, T, cache.heads, dim), ns, dim)
-        kp, vp = k_new.data_ptr(), v_new.data_ptr()
-    elif k_new is not None or v_new is not None:
-        raise ValueError("k_new, v_new: both or neither")
-    if out is None:
-        out = _new_on(stream, shape, _BF16, q.device)
-    elif out.shape != shape or (out.dtype is not _BF16 and not _is16(out)) or not out.is_contiguous() or not out.is_cuda:
-        raise ValueError(f"out: contiguous CUDA bf16 {tuple(shape)}")
-    if lse is None:
-        lse = _new_on(stream, (B, T, heads), _F32, q.device)
-    if workspace is None:
-        workspace = _new_on(stream, (max(tree_attention_workspace(h, B, T, heads, cache.heads, dim), 256),),
-                            torch.uint8, q.device)
-    _check(h._lib.dflash2_tree_attention(
-        h._h, q.data_ptr(), qs[0], qs[1], qs[2], cache.ref, _dense("cache_len", cache_len, _I32, (B,)), kp, vp,
-        ns[0], ns[1], ns[2], _opt("tree_mask", tree_mask, _I64, (B, T, (T + 63) // 64)), B, T, heads,
-        dim ** -0.5 if scale is None else scale, out.data_ptr(), _dense("lse", lse, _F32, (B, T, heads)),
-        _ptr(workspace), workspace.nbytes, _raw_stream(h, stream)), "dflash2_tree_attention")
+    if out is None or lse is None or workspace is None:
+        _need(q.dim() == 4 and q.is_cuda, "q: CUDA bf16 [B, T, heads, dim]")
+        B, T, heads, dim = q.shape
+        if out is None:
+            out = _new_on(stream, q.shape, torch.bfloat16, q.device)
+        if lse is None:
+            lse = _new_on(stream, (B, T, heads), torch.float32, q.device)
+        if workspace is None:
+            workspace = _new_on(stream, (max(tree_attention_workspace(h, B, T, heads, cache.heads, dim), 256),),
+                                torch.uint8, q.device)
+    status = h._bind.tree_attention(h.raw, cache.addr, cache.batch, q, cache_len, k_new, v_new, tree_mask,
+                                    cache.dim ** -0.5 if scale is None else scale, out, lse, workspace,
+                                    _raw_stream(h, stream))
+    if status:
+        _check(status, "dflash2_tree_attention")
     return out, lse
 
 
@@ -466,24 +426,12 @@ def cache_commit(h: Handle, k_new, v_new, cache: KVCache, cache_len, count=None,
 
     k_new, v_new [B, T, kv_heads, dim]; count int32 [B] accepted nodes (None: T); path int32 [B, T] their ids
     (None: 0, 1, ...); scores fp32 [B, kv_heads, ld]: the appended positions' entries become 0."""
-    shape, s = k_new.shape, k_new.stride()
-    dim = cache.dim
-    if len(shape) != 4 or shape[3] != dim or shape[2] != cache.heads:
-        _bad_rows("k_new", dim)
-    _pair(k_new, v_new, shape, s, dim)
-    B, T, heads, _ = shape
-    if cache.batch < B:
-        _cache_for(cache, B)
-    ld, sp = 0, None
-    if scores is not None:
-        ld = scores.shape[-1]
-        sp = _dense("scores", scores, _F32, (B, heads, ld))
     if new_len is None:
-        new_len = _new_on(stream, (B,), _I32, k_new.device)
-    _check(h._lib.dflash2_cache_commit(
-        h._h, k_new.data_ptr(), v_new.data_ptr(), s[0], s[1], s[2], cache.ref,
-        _dense("cache_len", cache_len, _I32, (B,)), _opt("count", count, _I32, (B,)), _opt("path", path, _I32, (B, T)),
-        B, T, sp, ld, _dense("new_len", new_len, _I32, (B,)), _raw_stream(h, stream)), "dflash2_cache_commit")
+        new_len = _new_on(stream, (k_new.shape[0],), torch.int32, k_new.device)
+    status = h._bind.cache_commit(h.raw, cache.addr, cache.batch, k_new, v_new, cache_len, count, path, scores, new_len,
+                                  _raw_stream(h, stream))
+    if status:
+        _check(status, "dflash2_cache_commit")
     return new_len
 
 
@@ -491,19 +439,10 @@ def cache_scores(h: Handle, q, lse, cache: KVCache, cache_len, scores, count=Non
                  stream=None):
     """Adds to scores fp32 [B, kv_heads, ld] the attention weight that each cached position received from the
     accepted nodes (q and lse as in tree_attention, count and path as in cache_commit) -> scores."""
-    dim = cache.dim
-    shape, s = q.shape, q.stride()
-    if len(shape) != 4 or shape[3] != dim or s[3] != 1 or not q.is_cuda or (q.dtype is not _BF16 and not _is16(q)):
-        _bad_rows("q", dim)
-    B, T, heads, _ = shape
-    if cache.batch < B:
-        _cache_for(cache, B)
-    ld = scores.shape[-1]
-    _check(h._lib.dflash2_cache_scores(
-        h._h, q.data_ptr(), s[0], s[1], s[2], _dense("lse", lse, _F32, (B, T, heads)), cache.ref,
-        _dense("cache_len", cache_len, _I32, (B,)), _opt("count", count, _I32, (B,)), _opt("path", path, _I32, (B, T)),
-        B, T, heads, dim ** -0.5 if scale is None else scale, _dense("scores", scores, _F32, (B, cache.heads, ld)), ld,
-        _raw_stream(h, stream)), "dflash2_cache_scores")
+    status = h._bind.cache_scores(h.raw, cache.addr, cache.batch, q, lse, cache_len, scores, count, path,
+                                  cache.dim ** -0.5 if scale is None else scale, _raw_stream(h, stream))
+    if status:
+        _check(status, "dflash2_cache_scores")
     return scores
 
 
@@ -513,25 +452,18 @@ def cache_evict(h: Handle, scores, cache: KVCache, cache_len, dst: KVCache, keep
     (kept int32 [B, kv_heads, keep], new_len int32 [B], dst_scores fp32 [B, kv_heads, keep] or None).
 
     scores fp32 [B, kv_heads, ld]; dst's pages must be none of the source's."""
-    heads = cache.heads
-    B, ld = scores.shape[0], scores.shape[-1]
-    _cache_for(cache, B)
-    _cache_for(dst, B)
-    shape = (B, heads, max(keep, 0))
-    if kept is None:
-        kept = _new_on(stream, shape, _I32, scores.device)
-    if new_len is None:
-        new_len = _new_on(stream, (B,), _I32, scores.device)
-    if dst_scores is None and want_scores:
-        dst_scores = _new_on(stream, shape, _F32, scores.device)
-    dst_ld, dp = keep, None
-    if dst_scores is not None:
-        dst_ld = dst_scores.shape[-1]
-        dp = _dense("dst_scores", dst_scores, _F32, (B, heads, dst_ld))
-    _check(h._lib.dflash2_cache_evict(
-        h._h, _dense("scores", scores, _F32, (B, heads, ld)), ld, cache.ref,
-        _dense("cache_len", cache_len, _I32, (B,)), dst.ref, B, keep, recent, _dense("kept", kept, _I32, shape),
-        _dense("new_len", new_len, _I32, (B,)), dp, dst_ld, _raw_stream(h, stream)), "dflash2_cache_evict")
+    if kept is None or new_len is None or (dst_scores is None and want_scores):
+        B, shape = scores.shape[0], (scores.shape[0], cache.heads, max(keep, 0))
+        if kept is None:
+            kept = _new_on(stream, shape, torch.int32, scores.device)
+        if new_len is None:
+            new_len = _new_on(stream, (B,), torch.int32, scores.device)
+        if dst_scores is None and want_scores:
+            dst_scores = _new_on(stream, shape, torch.float32, scores.device)
+    status = h._bind.cache_evict(h.raw, cache.addr, cache.batch, dst.addr, dst.batch, scores, cache_len, keep, recent, kept,
+                                 new_len, dst_scores, _raw_stream(h, stream))
+    if status:
+        _check(status, "dflash2_cache_evict")
     return kept, new_len, dst_scores
 
 
