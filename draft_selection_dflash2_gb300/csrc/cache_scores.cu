@@ -16,6 +16,11 @@
 //               per column, summed in fp32 in column order.  Each has two TMEM buffers
 //               of 128 columns, so that a chunk's product runs under the last one's
 //               exponentials (with one buffer of 256: 1724 cycles a unit at 136 rows).
+// Bound by memory while a unit's products and exponentials hide under its keys (up
+// to about 128 rows): 16 blocks of 17 nodes, 1 to 17 of them accepted, in groups of 8
+// over 8 kv heads and ragged lengths up to 32768: 125 us for 625 MB, 5.0 TB/s (75% of
+// a copy's rate; the runs with the most rows, 136, are the slowest).  One block over
+// 4000 positions: 4.5 us, the latency of the first tiles.
 // When a run enters another (sequence, head) the epilogue warps lay that head's
 // query rows out in shared memory (up to 512 rows; more rows take one launch per
 // 512) and their lse beside them.
