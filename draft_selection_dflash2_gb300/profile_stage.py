@@ -11,7 +11,13 @@ best-path walk on N(0, 4) scores of B sequences), eval (the Table 1 selector
 evaluation of B sequences of 7 positions with uniform candidate ids and the
 true token in slot 0 of 80% of the rows), proj (projection-form pair scores
 of B sequences: A, B projected from an N(0, 1) [V, d] embedding) and gemm_conv
-(the conv fused into an output projection with K = d).
+(the conv fused into an output projection with K = d).  The cache operators have
+shapes of their own (64 query heads over 8 kv heads of 128, N(0, 1) inputs, pages
+of 64): attention (2 sequences of 131072 positions, one token each),
+attention_block (64 blocks of 17 over lengths of 1500 to 12000), attention_tree (8
+trees of 64 nodes over 16384 positions), commit (256 paths of 1 to 64 nodes),
+scores (16 blocks of 17, 1 to 17 accepted, over lengths of 4096 to 32768) and
+evict (16 sequences of 4096 to 32768 positions to 8001).
 """
 import argparse
 import os
@@ -30,13 +36,59 @@ def bf(torch, a):
     return torch.from_numpy(np.ascontiguousarray(a).view(np.int16)).cuda().view(torch.bfloat16)
 
 
+def cache_stage(torch, h, rng, stage):
+    """One cache operator's call (see the module's text for its shape)."""
+    B, T, n = {"attention": (2, 1, 131072), "attention_block": (64, 17, 12000), "attention_tree": (8, 64, 16384),
+               "commit": (256, 64, 1000), "scores": (16, 17, 32768), "evict": (16, 0, 32768)}[stage]
+    heads, H, dim, page, keep = 64, 8, 128, 64, 8001
+    g = torch.Generator(device="cuda")
+    g.manual_seed(8)
+
+    def randn(*shape):
+        return torch.empty(shape, dtype=torch.bfloat16, device="cuda").normal_(generator=g)
+
+    def pool(positions):
+        pages = -(-positions // page)
+        table = torch.from_numpy(rng.permutation(B * pages).reshape(B, pages).astype(np.int32)).cuda()
+        return api.KVCache(randn(B * pages, page, H, dim), randn(B * pages, page, H, dim), table)
+
+    cache = pool(n + T)
+    ragged = stage in ("attention_block", "scores", "evict")
+    lens = torch.from_numpy((rng.integers(n // 8, n + 1, B) if ragged else np.full(B, n)).astype(np.int32)).cuda()
+    if stage == "evict":
+        dst = pool(keep)
+        scores = torch.rand((B, H, n), generator=g, device="cuda")
+        return lambda: api.cache_evict(h, scores, cache, lens, dst, keep, 500)
+    count = torch.from_numpy(rng.integers(1, T + 1, B).astype(np.int32)).cuda()
+    q, k, v = randn(B, T, heads, dim), randn(B, T, H, dim), randn(B, T, H, dim)
+    scores = torch.zeros((B, H, n + T), device="cuda")
+    if stage == "commit":
+        return lambda: api.cache_commit(h, k, v, cache, lens, count, scores=scores)
+    if stage == "scores":
+        lse = torch.full((B, T, heads), 10.0, device="cuda")
+        return lambda: api.cache_scores(h, q, lse, cache, lens, scores, count)
+    mask = None
+    if stage == "attention_tree":
+        # node t's parent is one of the six before it
+        sees = np.zeros((B, T, T), bool)
+        for t in range(T):
+            if t:
+                parent = t - 1 - np.minimum(rng.integers(0, 6, B), t - 1)
+                sees[:, t] = sees[np.arange(B), parent]
+            sees[:, t, t] = True
+        mask = torch.from_numpy(np.packbits(sees, axis=-1, bitorder="little").view(np.int64).copy()).cuda()
+    ws = torch.empty(api.tree_attention_workspace(h, B, T, heads, H, dim), dtype=torch.uint8, device="cuda")
+    return lambda: api.tree_attention(h, q, cache, lens, k, v, tree_mask=mask, workspace=ws)
+
+
 def main():
     import torch
 
     ap = argparse.ArgumentParser()
     ap.add_argument("--stage", required=True,
                     choices=["topk", "pairs", "walk0", "walk1", "conv", "verify0", "verify1", "lmhead",
-                             "lmhead_gate", "viterbi", "eval", "proj", "gemm_conv"])
+                             "lmhead_gate", "viterbi", "eval", "proj", "gemm_conv", "attention", "attention_block",
+                             "attention_tree", "commit", "scores", "evict"])
     ap.add_argument("--B", type=int, default=128)
     ap.add_argument("--reps", type=int, default=3)
     args = ap.parse_args()
@@ -44,7 +96,9 @@ def main():
     B = args.B
     h = api.Handle(0)
     rng = np.random.default_rng(0)
-    if args.stage == "topk":
+    if args.stage in ("attention", "attention_block", "attention_tree", "commit", "scores", "evict"):
+        run = cache_stage(torch, h, rng, args.stage)
+    elif args.stage == "topk":
         U = bf(torch, synth.logits_planted(rng, B * L, V))
         run = lambda: api.topk(h, U)  # noqa: E731
     elif args.stage in ("pairs", "walk0", "walk1"):
