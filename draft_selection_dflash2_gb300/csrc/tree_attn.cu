@@ -10,7 +10,8 @@
 // of the drafted nodes.  An item is (sequence, kv head, pair of row tiles); its
 // key tiles are its units.  All units of the call, item after item, are cut into
 // equal runs, one per CTA (one CTA per SM): ragged lengths balance whatever they
-// are, and an axis is split exactly where runs end.  An item cut by a run's end
+// are, and an axis is split exactly where runs end.  With more than one pair each
+// pair has runs of its own, beside one another (see Lanes).  An item cut by a run's end
 // leaves unnormalised partial sums (fp32 O, m, l) in the workspace, and
 // tree_attn_join_kernel adds them in run order (same bits on every call).
 //
@@ -97,10 +98,23 @@ struct AttnSmem {
   int abort_flag;
 };
 
+// How CTAs are dealt to the pairs of row tiles of a kv head.  With lanes.n = 0 a run
+// holds all pairs' units, pair after pair.  Otherwise each pair's units are cut into
+// runs of their own: n pairs into `runs` each, run after run, pair beside pair, so
+// that the CTAs that read the same keys do so at the same time; and, where a single
+// row tile is left over, that one into the CTAs that remain.
+struct Lanes {
+  int32_t n, runs;
+  __device__ __forceinline__ int32_t pair(int32_t cta) const { return cta < n * runs ? cta % n : n; }
+  // CTAs from one run to the next (with n = 0 too)
+  __device__ __forceinline__ int32_t step(int32_t pair) const { return pair < n ? n : 1; }
+};
+
 struct AttnPlan {
   AttnArgs a;
   int32_t tpt;              // nodes per row tile
   int32_t row_tiles, pairs; // row tiles, and pairs of them
+  Lanes lanes;
   int32_t areas;            // partial areas per slot (row tiles of a pair)
   float c;                  // scale * log2(e)
   float* part;              // [2 * runs][areas][D / 4][128] float4
@@ -164,7 +178,7 @@ struct Walk : RunWalk {
   bool begun = false;
   __device__ __forceinline__ bool next(const AttnPlan& p, Segment* g) {
     const auto units = [&](int32_t i) { return units_of(p.a, i); };
-    const int32_t per_seq = p.a.cache.heads * p.pairs;
+    const int32_t per_seq = p.a.cache.heads * (p.lanes.n == 0 ? p.pairs : 1);
     if (left <= 0) return false;
     if (s == n) {
       next_item(units, per_seq);
@@ -177,8 +191,8 @@ struct Walk : RunWalk {
     g->e = p.whole ? n : min(n, s + left);
     g->n = n;
     g->b = b;
-    g->h = p.pairs == 1 ? item : item / p.pairs;
-    g->pair = item - g->h * p.pairs;
+    g->h = p.lanes.n == 0 ? item / p.pairs : item;
+    g->pair = p.lanes.n == 0 ? item - g->h * p.pairs : p.lanes.pair(blockIdx.x);
     g->tiles = min(2, p.row_tiles - 2 * g->pair);
     g->len = uniform(kv_clamp(p.a.cache_len[b], p.a.cache.capacity, nullptr));
     g->first = !begun;
@@ -302,8 +316,15 @@ __global__ void __launch_bounds__(kThreads, 1)
   const uint32_t tmem = uniform(s.tmem);
   pdl_wait();
   pdl_launch_dependents();
-  const RunStart run = find_run([&](int32_t b) { return units_of(a, b); }, static_cast<int32_t>(a.B),
-                                a.cache.heads * p.pairs, blockIdx.x, gridDim.x);
+  int32_t run_at = blockIdx.x, runs = gridDim.x, per_seq = a.cache.heads * p.pairs;
+  if (p.lanes.n > 0) {
+    const int32_t dealt = p.lanes.n * p.lanes.runs;
+    per_seq = a.cache.heads;
+    runs = run_at < dealt ? p.lanes.runs : runs - dealt;
+    run_at = run_at < dealt ? run_at / p.lanes.n : run_at - dealt;
+  }
+  const RunStart run =
+      find_run([&](int32_t b) { return units_of(a, b); }, static_cast<int32_t>(a.B), per_seq, run_at, runs);
   Walk walk;
   walk.start(run);
   Segment g;
@@ -678,7 +699,9 @@ __global__ void __launch_bounds__(kThreads, 1)
         p.cuts[blockIdx.x] =
             g.s == 0 && g.e < g.n
                 ? make_int4(g.b, g.h * p.pairs + g.pair,
-                            static_cast<int>(blockIdx.x + (g.n - g.e + run.units - 1) / run.units), slot)
+                            static_cast<int>(blockIdx.x) +
+                                p.lanes.step(g.pair) * ((g.n - g.e + run.units - 1) / run.units),
+                            slot)
                 : make_int4(-1, 0, 0, 0);
       // with one tile only the pipeline that took the drafted tile knows what its rows saw there
       bool fix = bad_seen != 0;
@@ -833,6 +856,7 @@ __global__ void __launch_bounds__(kJoinThreads, 2) tree_attn_join_kernel(const _
     const int c0 = list_run[task / groups / p.areas];
     const int pair = d.y % p.pairs, h = d.y / p.pairs;
     if (2 * pair + tile >= p.row_tiles) continue;
+    const int step = p.lanes.step(pair);
     const int node = (2 * pair + tile) * p.tpt + r / a.group;
     const bool row_ok = r < p.tpt * a.group && node < a.T;
     const int64_t orow = (static_cast<int64_t>(d.x) * a.T + node) * a.heads + h * a.group + r % a.group;
@@ -840,13 +864,13 @@ __global__ void __launch_bounds__(kJoinThreads, 2) tree_attn_join_kernel(const _
       const int x = group * kWideCols * kJoinSplit + y * kWideCols;
       PartSum<kWideCols> sum;
       if (row_ok) {
-        sum.template add_parts<D, 2>(p, d, c0, c0, 1, tile, x, r);
+        sum.template add_parts<D, 2>(p, d, c0, c0, step, tile, x, r);
         sum.write(a, orow, D, x);
       }
     } else {
       const int x = group * kNarrowCols;
       PartSum<kNarrowCols> sum;
-      if (row_ok) sum.template add_parts<D, 4>(p, d, c0, c0 + y, kJoinSplit, tile, x, r);
+      if (row_ok) sum.template add_parts<D, 4>(p, d, c0, c0 + y * step, kJoinSplit * step, tile, x, r);
       s_o[y][kNarrowCols][r] = sum.m;
       s_o[y][kNarrowCols + 1][r] = sum.l;
 #pragma unroll
@@ -865,6 +889,24 @@ __global__ void __launch_bounds__(kJoinThreads, 2) tree_attn_join_kernel(const _
       __syncthreads();
     }
   }
+}
+
+// A unit with one row tile takes about kSingle / 16 of the time of one with two (8, 9 and 11
+// balanced the runs of 3 row tiles less well).
+constexpr int kSingle = 10;
+
+// Measured against runs that hold all pairs' units (8 sequences of 16384, 8 heads of 128 in groups of
+// 8): 64 nodes, 4 row tiles, 208 us against 217 (the second pair finds the keys in L2); 48 nodes, 3 row
+// tiles, 185 against 210 (the runs of the full pair took the longest); 65 nodes, 5 row tiles, 275
+// against 300.  64 short sequences of 48 nodes, whose runs hold many items, are the exception: 120
+// against 117.
+Lanes deal_lanes(int32_t row_tiles, int32_t runs) {
+  if (row_tiles <= 2) return {1, runs};
+  Lanes l = {row_tiles / 2, 0};
+  const int32_t weight = 16 * l.n + (row_tiles % 2) * kSingle;   // of all pairs
+  l.runs = 16 * runs / weight;
+  // where the CTAs do not divide well (more than 3% lost), all pairs share all runs
+  return l.runs * weight * 33 >= 16 * 32 * runs ? l : Lanes{0, 0};
 }
 
 struct Tiling {
@@ -900,7 +942,9 @@ cudaError_t launch(const AttnArgs& a, void* workspace, int num_sms, cudaStream_t
   // Items of at most one unit per pipeline are left whole: nothing is gained by cutting them, and nothing has to
   // be joined.  (Longer ones are worth it: 1 x 1 over 500 positions, 5 units, 12.3 us cut, 14.9 us whole.)
   p.whole = (static_cast<int64_t>(c.capacity) + kTile - 1) / kTile + (a.k_new != nullptr) <= kWholeUnits;
-  const int runs = static_cast<int>(imin64(imin64(num_sms, kMaxRuns), imax64(most, 1)));
+  int runs = static_cast<int>(imin64(imin64(num_sms, kMaxRuns), imax64(most, 1)));
+  p.lanes = deal_lanes(t.row_tiles, runs);
+  if (p.lanes.n == t.pairs) runs = p.lanes.n * p.lanes.runs;
   p.part = static_cast<float*>(workspace);
   p.part_ml = reinterpret_cast<float2*>(p.part + static_cast<size_t>(2) * num_sms * t.areas * kTile * D);
   p.cuts = reinterpret_cast<int4*>(p.part_ml + static_cast<size_t>(2) * num_sms * t.areas * kTile);

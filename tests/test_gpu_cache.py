@@ -652,3 +652,20 @@ def test_refusals_of_what_passes_the_counters(handle):
         api.tree_attention(handle, q[:1], cache, cl[:1])
     assert e.value.status == -2
     assert handle.device_error() == 0
+
+
+@pytest.mark.parametrize("T,heads,H", [(48, 16, 2), (65, 8, 1), (112, 16, 2), (128, 8, 1), (9, 128, 1), (128, 64, 1)])
+def test_row_tiles_with_runs_of_their_own(handle, T, heads, H):
+    # 3, 5, 7, 8, 9 and 64 row tiles: pairs beside one another, a single tile left over, too many pairs to deal out
+    gen = torch.Generator(device="cuda").manual_seed(T)
+    lens = [6000, 0, 1, 2511]
+    B = len(lens)
+    cache, rows = make_cache(gen, lens, H, 128, 64, 6000)
+    q, kn, vn = randn(gen, B, T, heads, 128), randn(gen, B, T, H, 128), randn(gen, B, T, H, 128)
+    sees = np.tril(np.ones((T, T), bool))[None].repeat(B, 0)
+    cl = torch.tensor(lens, dtype=torch.int32, device="cuda")
+    got = api.tree_attention(handle, q, cache, cl, kn, vn)
+    again = api.tree_attention(handle, q, cache, cl, kn, vn)
+    assert torch.equal(got[0], again[0]) and torch.equal(got[1], again[1])
+    check_attention(got, reference(q, rows, kn, vn, sees, 128 ** -0.5))
+    assert handle.device_error() == 0
