@@ -8,7 +8,8 @@
 // key is a TMEM lane and one thread adds up its key's columns with no exchange
 // between threads.  A unit is 128 keys of one (sequence, head); its rows are taken
 // in equal chunks of up to 128 columns.  All units are cut into equal runs, one per
-// CTA.
+// CTA: equal in weight where sequences may differ in rows and the call is large (a unit
+// of 136 rows takes a fifth longer than one of 8), else in units.
 //   warp 0      TMA producer of K tiles (128 x D, one box per page piece).
 //   warps 1, 2  MMA issuers of the even and the odd units (one warp for both was
 //               the slowest part at 136 rows: 2560 cycles a unit).
@@ -18,8 +19,11 @@
 //               exponentials (with one buffer of 256: 1724 cycles a unit at 136 rows).
 // Bound by memory while a unit's products and exponentials hide under its keys (up
 // to about 128 rows): 16 blocks of 17 nodes, 1 to 17 of them accepted, in groups of 8
-// over 8 kv heads and ragged lengths up to 32768: 125 us for 625 MB, 5.0 TB/s (75% of
-// a copy's rate; the runs with the most rows, 136, are the slowest).  One block over
+// over 8 kv heads and ragged lengths up to 32768: 110 us for 625 MB, 5.7 TB/s (85% of
+// a copy's rate; 118 us with runs equal in units, and 124 when a thread also waited for
+// each piece of the query rows before it asked for the next).  With one node accepted
+// everywhere a batch that takes 83 us takes 97 with all 17 accepted: the change from one
+// head's rows to the next's drains the products, once or twice a run.  One block over
 // 4000 positions: 4.5 us, the latency of the first tiles.
 // When a run enters another (sequence, head) the epilogue warps lay that head's
 // query rows out in shared memory (up to 512 rows; more rows take one launch per
@@ -33,6 +37,7 @@ namespace {
 constexpr int kThreads = 384;
 constexpr int kMaxQTiles = 4;           // 128-row tiles of queries per launch
 constexpr int kMaxSlots = 12;
+constexpr int kQBatch = 4;              // 16-byte pieces of query rows that a thread loads at once
 constexpr int kSmemLimit = 232448;      // 227 KB
 
 struct ScoresSmem {
@@ -47,6 +52,7 @@ struct ScoresPlan {
   ScoresArgs a;
   float c;                  // scale * log2(e)
   int32_t limit;            // positions a length may reach
+  float inv_group;          // 1 / group
   int32_t row0;             // first row of this launch
   int32_t q_tiles;          // 128-row tiles of queries that shared memory holds
   int32_t slots;            // ring of K tiles
@@ -59,9 +65,15 @@ __device__ __forceinline__ int32_t rows_of(const ScoresPlan& p, int64_t b) {
   return max(0, min(count * p.a.group - p.row0, p.q_tiles * kTile));
 }
 
-__device__ __forceinline__ int32_t units_of(const ScoresPlan& p, int32_t b) {
+// Units of each of sequence b's heads, and what one takes in runs of equal weight: 32 for
+// its keys, 1 for 10 rows (1 for 20 or 5 balanced less well: 112 us each in the case above).
+constexpr int kMostWeight = 84;
+template <bool kWeighted>
+__device__ __forceinline__ int32_t units_of(const ScoresPlan& p, int32_t b, int32_t* weight) {
   const int32_t n = kv_clamp(p.a.cache_len[b], p.limit, p.a.err);
-  return rows_of(p, b) > 0 ? (n + kTile - 1) / kTile : 0;
+  const int32_t rows = rows_of(p, b);
+  *weight = kWeighted ? 32 + rows / 10 : 1;
+  return rows > 0 ? (n + kTile - 1) / kTile : 0;
 }
 
 struct Segment {
@@ -69,17 +81,29 @@ struct Segment {
   int32_t len, rows;
 };
 
+// A run is a stretch of weight; the units that begin in it are its own.
+template <bool kWeighted>
 struct Walk : RunWalk {
+  int32_t w;                // a unit's weight; `left` is one too
+  __device__ __forceinline__ void start(const ScoresPlan& p, const RunStart& r) {
+    RunWalk::start(r);
+    w = 1;
+    if (!kWeighted || left <= 0) return;
+    n = uniform(units_of<kWeighted>(p, b, &w));
+    const int32_t at = s;   // in weight
+    s = (at + w - 1) / w;
+    left -= s * w - at;
+  }
   __device__ __forceinline__ bool next(const ScoresPlan& p, Segment* g) {
     if (left <= 0) return false;
-    if (s == n) next_item([&](int32_t i) { return units_of(p, i); }, p.a.cache.heads);
+    if (s == n) next_item([&](int32_t i) { return units_of<kWeighted>(p, i, &w); }, p.a.cache.heads);
     g->h = uniform(item);
     g->s = uniform(s);
-    g->e = uniform(min(n, s + left));
+    g->e = uniform(min(n, s + (left + w - 1) / w));
     g->b = uniform(b);
     g->len = uniform(kv_clamp(p.a.cache_len[b], p.limit, nullptr));
     g->rows = uniform(rows_of(p, b));
-    left -= g->e - s;
+    left -= (g->e - s) * w;
     s = g->e;
     return true;
   }
@@ -131,7 +155,7 @@ struct KPos {
   __device__ __forceinline__ uint32_t parity() const { return use >> 1 & 1; }
 };
 
-template <int D>
+template <int D, bool kWeighted>
 __global__ void __launch_bounds__(kThreads, 1)
     cache_scores_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ ScoresPlan p) {
   constexpr int kHalves = D / 64;
@@ -171,10 +195,13 @@ __global__ void __launch_bounds__(kThreads, 1)
   const uint32_t tmem = uniform(s.tmem);
   pdl_wait();
   pdl_launch_dependents();
-  const RunStart run = find_run([&](int32_t b) { return units_of(p, b); }, static_cast<int32_t>(a.B), a.cache.heads,
-                                blockIdx.x, gridDim.x);
-  Walk walk;
-  walk.start(run);
+  const auto weight = [&](int32_t b) {
+    int32_t w;
+    const int32_t n = units_of<kWeighted>(p, b, &w);
+    return n * w;
+  };
+  Walk<kWeighted> walk;
+  walk.start(p, find_run(weight, static_cast<int32_t>(a.B), a.cache.heads, blockIdx.x, gridDim.x));
   Segment g;
   bool live = true;
 
@@ -266,22 +293,39 @@ __global__ void __launch_bounds__(kThreads, 1)
       __syncwarp();
       named_bar_sync(1, 2 * kTile);
       const int padded = (g.rows + 15) & ~15;
-      constexpr int kPieces = D / 8;
-      for (int x = tid; x < padded * kPieces; x += 2 * kTile) {
-        const int row = x / kPieces, piece = x % kPieces;
-        uint4 v = make_uint4(0, 0, 0, 0);
-        float l2 = INFINITY;
-        if (row < g.rows) {
-          const int i = (p.row0 + row) / a.group, hq = g.h * a.group + (p.row0 + row) % a.group;
-          const int t = a.path == nullptr ? i : clamp_node(a.path[static_cast<int64_t>(g.b) * a.T + i], a.T, a.err);
-          const float lse = a.lse[(static_cast<int64_t>(g.b) * a.T + t) * a.heads + hq];
-          if (lse != -INFINITY) {    // a query that saw nothing adds nothing
-            l2 = lse * 1.4426950408889634f;
-            v = *reinterpret_cast<const uint4*>(a.q + g.b * a.q_b + t * a.q_t + hq * a.q_h + piece * 8);
-          }
+      constexpr int kPieces = D / 8, kRowStep = 2 * kTile / kPieces;
+      const int piece = tid % kPieces;
+      // kQBatch pieces a thread, so that their chains path -> lse and query run together
+      for (int row0 = tid / kPieces; row0 < padded; row0 += kQBatch * kRowStep) {
+        int t[kQBatch], hq[kQBatch];
+        float lse[kQBatch];
+        uint4 v[kQBatch];
+#pragma unroll
+        for (int y = 0; y < kQBatch; ++y) {
+          const int row = row0 + y * kRowStep;
+          t[y] = hq[y] = 0;
+          if (row >= g.rows) continue;
+          const int i = static_cast<int>((p.row0 + row + 0.5f) * p.inv_group);   // (exact: rows < 2^14)
+          hq[y] = g.h * a.group + (p.row0 + row) - i * a.group;
+          t[y] = a.path == nullptr ? i : a.path[static_cast<int64_t>(g.b) * a.T + i];
         }
-        *reinterpret_cast<uint4*>(q_smem + (piece >> 3) * q_half + row * 128 + (((piece & 7) ^ (row & 7)) << 4)) = v;
-        if (piece == 0) s.lse[row] = -l2;
+#pragma unroll
+        for (int y = 0; y < kQBatch; ++y) {
+          lse[y] = -INFINITY;
+          if (row0 + y * kRowStep >= g.rows) continue;
+          const int node = clamp_node(t[y], a.T, a.err);
+          lse[y] = a.lse[(static_cast<int64_t>(g.b) * a.T + node) * a.heads + hq[y]];
+          v[y] = *reinterpret_cast<const uint4*>(a.q + g.b * a.q_b + node * a.q_t + hq[y] * a.q_h + piece * 8);
+        }
+#pragma unroll
+        for (int y = 0; y < kQBatch; ++y) {
+          const int row = row0 + y * kRowStep;
+          if (row >= padded) break;
+          // a query that saw nothing adds nothing, nor do the rows past the last
+          if (lse[y] == -INFINITY) v[y] = make_uint4(0, 0, 0, 0);
+          *reinterpret_cast<uint4*>(q_smem + (piece >> 3) * q_half + row * 128 + (((piece & 7) ^ (row & 7)) << 4)) = v[y];
+          if (piece == 0) s.lse[row] = lse[y] == -INFINITY ? -INFINITY : lse[y] * -1.4426950408889634f;
+        }
       }
       __syncwarp();
       asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
@@ -349,14 +393,24 @@ __global__ void __launch_bounds__(kThreads, 1)
   }
 }
 
-template <int D>
+// Positions that a length may reach.
+int32_t length_limit(const ScoresArgs& a) {
+  return static_cast<int32_t>(imin64(a.cache.capacity, a.scores_ld));
+}
+
+int64_t most_units(const ScoresArgs& a) {
+  return a.B * a.cache.heads * ((static_cast<int64_t>(length_limit(a)) + kTile - 1) / kTile);
+}
+
+template <int D, bool kWeighted>
 cudaError_t launch(const ScoresArgs& a, int num_sms, cudaStream_t stream) {
   constexpr int kTileBytes = kTile * D * 2;
   const KvView& c = a.cache;
   ScoresPlan p;
   p.a = a;
   p.c = a.scale * 1.4426950408889634f;
-  p.limit = static_cast<int32_t>(imin64(c.capacity, a.scores_ld));
+  p.inv_group = 1.0f / static_cast<float>(a.group);
+  p.limit = length_limit(a);
   if (p.limit == 0) return cudaSuccess;
   const int32_t rows = a.T * a.group;
   p.q_tiles = min((rows + kTile - 1) / kTile, kMaxQTiles);
@@ -370,9 +424,9 @@ cudaError_t launch(const ScoresArgs& a, int num_sms, cudaStream_t stream) {
   const uint32_t kb[4] = {64, static_cast<uint32_t>(p.box_rows), 1, 1};
   if (!make_tmap_bf16_nd(&tmK, c.k, 4, kd, ks, kb)) return cudaErrorInvalidValue;
   const size_t smem = static_cast<size_t>(p.q_tiles + p.slots) * kTileBytes + sizeof(ScoresSmem);
-  const cudaError_t e = set_smem_limit<cache_scores_kernel<D>>(kSmemLimit);
+  const cudaError_t e = set_smem_limit<cache_scores_kernel<D, kWeighted>>(kSmemLimit);
   if (e != cudaSuccess) return e;
-  const int64_t most = a.B * c.heads * ((static_cast<int64_t>(p.limit) + kTile - 1) / kTile);
+  const int64_t most = most_units(a);
   cudaLaunchAttribute attr = pdl_attribute();
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(static_cast<unsigned>(imin64(num_sms, most)), 1, 1);
@@ -382,7 +436,7 @@ cudaError_t launch(const ScoresArgs& a, int num_sms, cudaStream_t stream) {
   cfg.attrs = &attr;
   cfg.numAttrs = 1;
   for (p.row0 = 0; p.row0 < rows; p.row0 += kMaxQTiles * kTile) {
-    const cudaError_t st = cudaLaunchKernelEx(&cfg, cache_scores_kernel<D>, tmK, p);
+    const cudaError_t st = cudaLaunchKernelEx(&cfg, cache_scores_kernel<D, kWeighted>, tmK, p);
     if (st != cudaSuccess) return st;
   }
   return cudaSuccess;
@@ -391,7 +445,12 @@ cudaError_t launch(const ScoresArgs& a, int num_sms, cudaStream_t stream) {
 }  // namespace
 
 cudaError_t launch_cache_scores(const ScoresArgs& a, int64_t head_dim, int num_sms, cudaStream_t stream) {
-  return head_dim == 64 ? launch<64>(a, num_sms, stream) : launch<128>(a, num_sms, stream);
+  const int64_t most = most_units(a);
+  // In short runs a weight only breaks the runs' ends away from the heads' (one block over 4000 positions: 6.4 us
+  // against 4.5), and the weights' sum has to fit.
+  const bool weighted = a.B > 1 && most >= 8 * num_sms && most * kMostWeight < (int64_t(1) << 31);
+  if (head_dim == 64) return weighted ? launch<64, true>(a, num_sms, stream) : launch<64, false>(a, num_sms, stream);
+  return weighted ? launch<128, true>(a, num_sms, stream) : launch<128, false>(a, num_sms, stream);
 }
 
 }  // namespace dflash2

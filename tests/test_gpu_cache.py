@@ -669,3 +669,10 @@ def test_row_tiles_with_runs_of_their_own(handle, T, heads, H):
     assert torch.equal(got[0], again[0]) and torch.equal(got[1], again[1])
     check_attention(got, reference(q, rows, kn, vn, sees, 128 ** -0.5))
     assert handle.device_error() == 0
+
+
+@pytest.mark.parametrize("T,heads,H,D,page,tree", [(17, 32, 4, 128, 64, False), (100, 24, 4, 64, 0, True)])
+def test_scores_of_blocks_that_differ_in_accepted_nodes(handle, T, heads, H, D, page, tree):
+    # enough units that runs are cut by weight: sequences of many and of few rows, empty ones among them
+    lens = [4096, 0, 130, 3000, 4000, 1, 4096, 2500, 0, 129, 3583, 2048]
+    test_scores(handle, lens, T, heads, H, D, page, tree)
