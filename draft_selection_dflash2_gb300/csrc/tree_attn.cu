@@ -44,18 +44,18 @@
 // What bounds it, and what it measured (GB300, heads in groups of 8 over 8 kv heads,
 // D = 128 unless said otherwise):
 //   memory   up to about 128 query rows per kv head: 2 sequences of 131072
-//            positions, one token each, 165 us = 6.5 TB/s (97% of a copy's rate).
-//   tensor cores beyond: 8 trees of 64 nodes over 16384 positions, 242 us = 1.14
-//            PFLOP/s; the tensor pipe is active 57% of the time and another 20% is
+//            positions, one token each, 162 us = 6.6 TB/s (99% of a copy's rate).
+//   tensor cores beyond: 8 trees of 64 nodes over 16384 positions, 208 us = 1.32
+//            PFLOP/s; the tensor pipe is active 59% of the time and another 20% is
 //            waiting for S's operands (64-key products read 6 KB of shared memory
 //            per 32 cycles of products, at 128 B a cycle).  64 keys and not 128
 //            because two S buffers of 128 per pipeline and the O accumulators do not
 //            fit 512 columns, and with one buffer the softmax and the products of a
-//            pipeline wait for one another (337 us).
+//            pipeline wait for one another (337 us against 242 then).
 //   latency  in small calls: one token over 500 positions takes 11 us, of which 1.6
 //            until the run is known, 2 until the first S, 1.2 for the units' softmax
 //            and products, 1.5 for writing parts and 3 for the join.
-//   64 blocks of 17 over ragged lengths up to 12000, 136 rows per kv head: 358 us
+//   64 blocks of 17 over ragged lengths up to 12000, 136 rows per kv head: 342 us
 //   against 271 for its bytes; the second row tile holds 8 rows but takes the tensor
 //   cores as long as a full one.
 // Splitting every item in equal runs, rather than by whole items, is what ragged
