@@ -13,7 +13,10 @@
 // are, and an axis is split exactly where runs end.  With more than one pair each
 // pair has runs of its own, beside one another (see Lanes).  An item cut by a run's end
 // leaves unnormalised partial sums (fp32 O, m, l) in the workspace, and
-// tree_attn_join_kernel adds them in run order (same bits on every call).
+// tree_attn_join_kernel adds them in run order (same bits on every call).  Where a
+// call has few and short items (a sequence or a few), a cluster of CTAs takes each
+// item instead: its CTAs leave their sums in their own shared memory and add them
+// from there, so that no second kernel has to start (see team_size).
 //
 // tree_attn_kernel, per CTA:
 //   warp 0      TMA producer: the item's query tiles, then each unit's K and V
@@ -52,9 +55,9 @@
 //            because two S buffers of 128 per pipeline and the O accumulators do not
 //            fit 512 columns, and with one buffer the softmax and the products of a
 //            pipeline wait for one another (337 us against 242 then).
-//   latency  in small calls: one token over 500 positions takes 11 us, of which 1.6
-//            until the run is known, 2 until the first S, 1.2 for the units' softmax
-//            and products, 1.5 for writing parts and 3 for the join.
+//   latency  in small calls: one token over 500 positions takes 8 us (10.8 with runs
+//            and a join: 1.6 until the run is known, 2 until the first S, 1.2 for the
+//            units' softmax and products, 1.5 for writing parts and 3 for the join).
 //   64 blocks of 17 over ragged lengths up to 12000, 136 rows per kv head: 342 us
 //   against 271 for its bytes; the second row tile holds 8 rows but takes the tensor
 //   cores as long as a full one.
@@ -64,6 +67,8 @@
 // Every wait is bounded (DFLASH2_DEVERR_TIMEOUT): after one gives up the CTA
 // stops issuing copies and products, walks its loops to their end, waits for its
 // own copies in flight, frees its TMEM and returns.
+#include <mutex>
+
 #include "attn_common.cuh"
 #include "launch.h"
 
@@ -76,6 +81,7 @@ constexpr int kMaxSlots = 10;
 constexpr int kBufs = 2;                // S buffers per pipeline (a third one, at D = 64, gained nothing)
 constexpr uint32_t kTmemO = 2 * kBufs * kChunk;   // first TMEM column of O: pipeline i's at kTmemO + i D
 constexpr int kMaxRuns = 512;           // most CTAs
+constexpr int kMaxTeam = 8;              // most CTAs of a team (a power of 2)
 constexpr int kWholeUnits = 2;           // items of up to so many units are never cut
 constexpr int kTwoTermUnits = 4;        // items of up to so many units carry P in two terms
 constexpr float kRescale = 8.0f;        // log2 of how far P may exceed 1
@@ -115,6 +121,7 @@ struct AttnPlan {
   int32_t tpt;              // nodes per row tile
   int32_t row_tiles, pairs; // row tiles, and pairs of them
   Lanes lanes;
+  int32_t team;             // CTAs of a cluster that takes one item between them, or 0: runs
   int32_t areas;            // partial areas per slot (row tiles of a pair)
   float c;                  // scale * log2(e)
   float* part;              // [2 * runs][areas][D / 4][128] float4
@@ -176,6 +183,17 @@ struct Segment {
 
 struct Walk : RunWalk {
   bool begun = false;
+  // The units of a team's item that are one CTA's.
+  __device__ __forceinline__ void start_team(const AttnPlan& p, int32_t at, int32_t rank) {
+    const int32_t per_seq = p.a.cache.heads * p.pairs;
+    b = at / per_seq;
+    item = at - b * per_seq;
+    n = uniform(units_of(p.a, b));
+    const int32_t share = team_share(p);
+    s = min(n, rank * share);
+    left = min(n - s, share);
+  }
+  __device__ __forceinline__ int32_t team_share(const AttnPlan& p) const { return (n + p.team - 1) / p.team; }
   __device__ __forceinline__ bool next(const AttnPlan& p, Segment* g) {
     const auto units = [&](int32_t i) { return units_of(p.a, i); };
     const int32_t per_seq = p.a.cache.heads * (p.lanes.n == 0 ? p.pairs : 1);
@@ -265,10 +283,115 @@ __device__ __noinline__ void add_non_finite(const AttnArgs& a, const uint32_t* b
   }
 }
 
+// Partial sums of a row's N columns, added as the softmax adds keys.
+template <int N>
+struct PartSum {
+  float m = -INFINITY, l = 0.0f, o[N] = {};
+  // Adds sums (m1, l1, v); with m1 = -inf they saw nothing, and v is not looked at.
+  __device__ __forceinline__ void add(float m1, float l1, const float (&v)[N]) {
+    const bool some = m1 != -INFINITY;
+    const float top = fmaxf(m, m1);
+    const float f0 = m == -INFINITY ? 0.0f : exp2_approx(m - top), f1 = some ? exp2_approx(m1 - top) : 0.0f;
+    m = top;
+    l = l * f0 + (some || l1 != l1 ? l1 * (some ? f1 : 1.0f) : 0.0f);   // only NaN scores: l1 is NaN
+#pragma unroll
+    for (int k = 0; k < N; ++k) o[k] = fmaf(some ? v[k] : 0.0f, f1, o[k] * f0);
+  }
+  // Row r's parts of columns x.. in runs c, c + step, .. c1, kBatch loads at a time.
+  template <int D, int kBatch>
+  __device__ __forceinline__ void add_parts(const AttnPlan& p, const int4& d, int c0, int c, int step, int tile, int x,
+                                            int r) {
+    for (; c <= d.z; c += kBatch * step) {
+      float2 ml[kBatch];
+      float v[kBatch][N];
+#pragma unroll
+      for (int w = 0; w < kBatch; ++w) {
+        const int cw = c + w * step;
+        ml[w] = make_float2(-INFINITY, 0.0f);
+        if (cw > d.z) continue;
+        // a run's first segment leaves its parts in slot 2 c, its last one in 2 c + 1
+        const int64_t part = static_cast<int64_t>(cw == c0 ? d.w : 2 * cw) * p.areas + tile;
+        ml[w] = p.part_ml[part * kTile + r];
+        const float4* src = reinterpret_cast<const float4*>(p.part) + (part * (D / 4) + x / 4) * kTile + r;
+#pragma unroll
+        for (int k = 0; k < N; k += 4) *reinterpret_cast<float4*>(&v[w][k]) = src[k / 4 * kTile];
+      }
+#pragma unroll
+      for (int w = 0; w < kBatch; ++w)
+        if (c + w * step <= d.z) add(ml[w].x, ml[w].y, v[w]);
+    }
+  }
+  __device__ __forceinline__ void write(const AttnArgs& a, int64_t orow, int D, int x) const {
+    const float inv = l == 0.0f ? 0.0f : 1.0f / l;
+    uint32_t out[N / 2];
+#pragma unroll
+    for (int k = 0; k < N; k += 2) out[k / 2] = pack_bf16(o[k] * inv, o[k + 1] * inv);
+    uint32_t* dst = reinterpret_cast<uint32_t*>(a.out + orow * D + x);
+    if constexpr (N == 8)
+      *reinterpret_cast<uint4*>(dst) = make_uint4(out[0], out[1], out[2], out[3]);
+    else
+      *reinterpret_cast<uint2*>(dst) = make_uint2(out[0], out[1]);
+    if (x == 0 && a.lse != nullptr) a.lse[orow] = l == 0.0f ? -INFINITY : (m + log2f(l)) * 0.69314718055994531f;
+  }
+};
+
+// Two or four words at p of the shared memory of the cluster's CTA `rank`.
+__device__ __forceinline__ uint32_t cluster_addr(const void* p, uint32_t rank) {
+  uint32_t at;
+  asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(at) : "r"(smem_addr(p)), "r"(rank));
+  return at;
+}
+__device__ __forceinline__ float2 ld_cluster(const float2* p, uint32_t rank) {
+  float2 v;
+  asm volatile("ld.shared::cluster.v2.f32 {%0, %1}, [%2];" : "=f"(v.x), "=f"(v.y) : "r"(cluster_addr(p, rank)) : "memory");
+  return v;
+}
+__device__ __forceinline__ float4 ld_cluster(const float4* p, uint32_t rank) {
+  float4 v;
+  asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];"
+               : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w)
+               : "r"(cluster_addr(p, rank))
+               : "memory");
+  return v;
+}
+
+// Adds the parts that a team's CTAs left in their shared memory, in their order: each CTA
+// takes every team-th four columns, a thread four columns of a row at a time.
+template <int D>
+__device__ __forceinline__ void join_team(const AttnPlan& p, const Walk& walk, const uint8_t* ring) {
+  const AttnArgs& a = p.a;
+  const float4* parts = reinterpret_cast<const float4*>(ring);
+  const float2* part_ml = reinterpret_cast<const float2*>(ring + 2 * kTile * D * 4);
+  const int share = walk.team_share(p), ranks = (walk.n + share - 1) / share;
+  const int h = walk.item / p.pairs, pair = walk.item - h * p.pairs;
+  for (int tile = 0; tile < 2; ++tile) {
+    const int node0 = (2 * pair + tile) * p.tpt;
+    const int rows = min(p.tpt, a.T - node0) * a.group;      // (none: the pair has one tile)
+    for (int task = threadIdx.x; task < rows * (D / 4) / p.team; task += kThreads) {
+      const int y = task / rows, r = task - y * rows;
+      const int x = y * p.team + blockIdx.x % p.team;
+      const int t = r / a.group;
+      PartSum<4> sum;
+      float2 ml[kMaxTeam];
+      float v[kMaxTeam][4];
+#pragma unroll
+      for (int w = 0; w < kMaxTeam; ++w) {
+        if (w >= ranks) continue;
+        ml[w] = ld_cluster(&part_ml[tile * kTile + r], w);
+        *reinterpret_cast<float4*>(v[w]) = ld_cluster(&parts[(tile * (D / 4) + x) * kTile + r], w);
+      }
+#pragma unroll
+      for (int w = 0; w < kMaxTeam; ++w)
+        if (w < ranks) sum.add(ml[w].x, ml[w].y, v[w]);
+      sum.write(a, (static_cast<int64_t>(walk.b) * a.T + node0 + t) * a.heads + h * a.group + r - t * a.group, D, 4 * x);
+    }
+  }
+}
+
 // 227 KB, the opt-in limit of a block, is just enough at D = 128
 static_assert(Cfg<128>::kRing + sizeof(AttnSmem) <= 232448, "shared memory");
 
-template <int D>
+template <int D, bool kTeam>
 __global__ void __launch_bounds__(kThreads, 1)
     tree_attn_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmK,
                      const __grid_constant__ CUtensorMap tmV, const __grid_constant__ CUtensorMap tmKn,
@@ -316,21 +439,25 @@ __global__ void __launch_bounds__(kThreads, 1)
   const uint32_t tmem = uniform(s.tmem);
   pdl_wait();
   pdl_launch_dependents();
-  int32_t run_at = blockIdx.x, runs = gridDim.x, per_seq = a.cache.heads * p.pairs;
-  if (p.lanes.n > 0) {
-    const int32_t dealt = p.lanes.n * p.lanes.runs;
-    per_seq = a.cache.heads;
-    runs = run_at < dealt ? p.lanes.runs : runs - dealt;
-    run_at = run_at < dealt ? run_at / p.lanes.n : run_at - dealt;
-  }
-  const RunStart run =
-      find_run([&](int32_t b) { return units_of(a, b); }, static_cast<int32_t>(a.B), per_seq, run_at, runs);
   Walk walk;
-  walk.start(run);
+  RunStart run = {0, 0, 0, 0};
+  if constexpr (kTeam) {
+    walk.start_team(p, blockIdx.x / p.team, blockIdx.x % p.team);
+  } else {
+    int32_t run_at = blockIdx.x, runs = gridDim.x, per_seq = a.cache.heads * p.pairs;
+    if (p.lanes.n > 0) {
+      const int32_t dealt = p.lanes.n * p.lanes.runs;
+      per_seq = a.cache.heads;
+      runs = run_at < dealt ? p.lanes.runs : runs - dealt;
+      run_at = run_at < dealt ? run_at / p.lanes.n : run_at - dealt;
+    }
+    run = find_run([&](int32_t b) { return units_of(a, b); }, static_cast<int32_t>(a.B), per_seq, run_at, runs);
+    walk.start(run);
+    if (threadIdx.x == 0 && run.units == 0) p.cuts[blockIdx.x] = make_int4(-1, 0, 0, 0);
+  }
   Segment g;
   bool live = true;
 
-  if (threadIdx.x == 0 && run.units == 0) p.cuts[blockIdx.x] = make_int4(-1, 0, 0, 0);
   if (warp == 0) {
     // ---- producer ----
     RingPos<S> at;
@@ -657,8 +784,10 @@ __global__ void __launch_bounds__(kThreads, 1)
       seg_v.advance_far(2 * g.count());
 
       // ---- the item's (or the run's part of the item's) sums ----
-      const bool whole = g.s == 0 && g.e == g.n;
-      const int slot = 2 * blockIdx.x + (g.first ? 0 : 1);
+      const bool whole = !kTeam && g.s == 0 && g.e == g.n;
+      const int slot = kTeam ? 0 : 2 * blockIdx.x + (g.first ? 0 : 1);
+      float4* const parts = kTeam ? reinterpret_cast<float4*>(ring) : reinterpret_cast<float4*>(p.part);
+      float2* const part_ml = kTeam ? reinterpret_cast<float2*>(ring + 2 * kTile * D * 4) : p.part_ml;
       const bool merge = g.tiles == 1;
       float f0 = 1.0f, f1 = 0.0f;     // weights of O0 and O1 (one tile), or of O_i
       // products complete in the order of their issue: the last one's is enough
@@ -678,6 +807,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         // a row that only saw NaN scores has no maximum and a NaN sum
         if (x0.y != x0.y || x1.y != x1.y) l = f0 = NAN;
         if (g.count(1) == 0) f1 = 0.0f;
+      } else if (kTeam) {
+        named_bar_sync(1, 2 * kTile);     // the parts go where the other pipeline's tiles were
       }
       tc_fence_after();
       const bool empty = l == 0.0f;   // the row saw nothing: 0, whatever the values were
@@ -692,10 +823,10 @@ __global__ void __launch_bounds__(kThreads, 1)
           if (row_ok && a.lse != nullptr)
             a.lse[orow] = l == 0.0f ? -INFINITY : (m + log2f(l)) * 0.69314718055994531f;
         } else {
-          p.part_ml[(static_cast<int64_t>(slot) * p.areas + area) * kTile + r] = make_float2(m, l);
+          part_ml[(static_cast<int64_t>(slot) * p.areas + area) * kTile + r] = make_float2(m, l);
         }
       }
-      if (threadIdx.x == kTile && walk.left <= 0)        // the run's last segment
+      if (!kTeam && threadIdx.x == kTile && walk.left <= 0)        // the run's last segment
         p.cuts[blockIdx.x] =
             g.s == 0 && g.e < g.n
                 ? make_int4(g.b, g.h * p.pairs + g.pair,
@@ -736,8 +867,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                                       pack_bf16(o[y + 4], o[y + 5]), pack_bf16(o[y + 6], o[y + 7]));
           }
         } else if (row_ok) {
-          float4* dst = reinterpret_cast<float4*>(p.part) +
-                        ((static_cast<int64_t>(slot) * p.areas + area) * (D / 4) + x / 4) * kTile + r;
+          float4* dst = parts + ((static_cast<int64_t>(slot) * p.areas + area) * (D / 4) + x / 4) * kTile + r;
 #pragma unroll
           for (int y = 0; y < 32; y += 4) dst[(y / 4) * kTile] = make_float4(o[y], o[y + 1], o[y + 2], o[y + 3]);
         }
@@ -745,7 +875,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (fix && row_ok)
         add_non_finite(a, s.bad, g.b, g.h, node, c0, c1, a.out + orow * D,
                        whole ? nullptr
-                             : p.part + (((static_cast<int64_t>(slot) * p.areas + area) * (D / 4)) * kTile + r) * 4);
+                             : reinterpret_cast<float*>(
+                                   parts + (static_cast<int64_t>(slot) * p.areas + area) * (D / 4) * kTile + r));
       __syncwarp();
       tc_fence_before();
       // O and the shared statistics may be overwritten once both pipelines have read them
@@ -753,6 +884,15 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
   }
 
+  if constexpr (kTeam) {
+    __syncwarp();
+    cluster_arrive();
+    cluster_wait();
+    join_team<D>(p, walk, ring);
+    __syncwarp();
+    cluster_arrive();                     // nobody leaves while its parts may still be read
+    cluster_wait();
+  }
   __syncthreads();
   if (threadIdx.x == 0) mbar_wait_bounded(&s.drain, 0, a.err);   // the tensor cores have finished
   __syncthreads();
@@ -770,57 +910,6 @@ __global__ void __launch_bounds__(kThreads, 1)
 // each) it is 4 columns, thread (r, y) takes every 4th part from the y-th on, and
 // the four sums are added in order.
 constexpr int kJoinSplit = 4, kJoinThreads = kTile * kJoinSplit, kWideCols = 8, kNarrowCols = 4;
-
-template <int N>
-struct PartSum {
-  float m = -INFINITY, l = 0.0f, o[N] = {};
-  // Adds sums (m1, l1, v); with m1 = -inf they saw nothing, and v is not looked at.
-  __device__ __forceinline__ void add(float m1, float l1, const float (&v)[N]) {
-    const bool some = m1 != -INFINITY;
-    const float top = fmaxf(m, m1);
-    const float f0 = m == -INFINITY ? 0.0f : exp2_approx(m - top), f1 = some ? exp2_approx(m1 - top) : 0.0f;
-    m = top;
-    l = l * f0 + (some || l1 != l1 ? l1 * (some ? f1 : 1.0f) : 0.0f);   // only NaN scores: l1 is NaN
-#pragma unroll
-    for (int k = 0; k < N; ++k) o[k] = fmaf(some ? v[k] : 0.0f, f1, o[k] * f0);
-  }
-  // Row r's parts of columns x.. in runs c, c + step, .. c1, kBatch loads at a time.
-  template <int D, int kBatch>
-  __device__ __forceinline__ void add_parts(const AttnPlan& p, const int4& d, int c0, int c, int step, int tile, int x,
-                                            int r) {
-    for (; c <= d.z; c += kBatch * step) {
-      float2 ml[kBatch];
-      float v[kBatch][N];
-#pragma unroll
-      for (int w = 0; w < kBatch; ++w) {
-        const int cw = c + w * step;
-        ml[w] = make_float2(-INFINITY, 0.0f);
-        if (cw > d.z) continue;
-        // a run's first segment leaves its parts in slot 2 c, its last one in 2 c + 1
-        const int64_t part = static_cast<int64_t>(cw == c0 ? d.w : 2 * cw) * p.areas + tile;
-        ml[w] = p.part_ml[part * kTile + r];
-        const float4* src = reinterpret_cast<const float4*>(p.part) + (part * (D / 4) + x / 4) * kTile + r;
-#pragma unroll
-        for (int k = 0; k < N; k += 4) *reinterpret_cast<float4*>(&v[w][k]) = src[k / 4 * kTile];
-      }
-#pragma unroll
-      for (int w = 0; w < kBatch; ++w)
-        if (c + w * step <= d.z) add(ml[w].x, ml[w].y, v[w]);
-    }
-  }
-  __device__ __forceinline__ void write(const AttnArgs& a, int64_t orow, int D, int x) const {
-    const float inv = l == 0.0f ? 0.0f : 1.0f / l;
-    uint32_t out[N / 2];
-#pragma unroll
-    for (int k = 0; k < N; k += 2) out[k / 2] = pack_bf16(o[k] * inv, o[k + 1] * inv);
-    uint32_t* dst = reinterpret_cast<uint32_t*>(a.out + orow * D + x);
-    if constexpr (N == 8)
-      *reinterpret_cast<uint4*>(dst) = make_uint4(out[0], out[1], out[2], out[3]);
-    else
-      *reinterpret_cast<uint2*>(dst) = make_uint2(out[0], out[1]);
-    if (x == 0 && a.lse != nullptr) a.lse[orow] = l == 0.0f ? -INFINITY : (m + log2f(l)) * 0.69314718055994531f;
-  }
-};
 
 template <int D>
 __global__ void __launch_bounds__(kJoinThreads, 2) tree_attn_join_kernel(const __grid_constant__ AttnPlan p, int runs) {
@@ -909,6 +998,50 @@ Lanes deal_lanes(int32_t row_tiles, int32_t runs) {
   return l.runs * weight * 33 >= 16 * 32 * runs ? l : Lanes{0, 0};
 }
 
+// Clusters of k = 2, 4 or 8 CTAs that the GPU holds at once (cluster sizes must fit its parts).
+template <int D>
+int clusters_at_once(int k, size_t smem) {
+  static std::mutex mu;
+  static int known[kMaxDevices][kMaxTeam + 1] = {};      // the number + 1
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= kMaxDevices) return 0;
+  std::lock_guard<std::mutex> lock(mu);
+  int& n = known[dev][k];
+  if (n == 0) {
+    cudaLaunchAttribute attr = {};
+    attr.id = cudaLaunchAttributeClusterDimension;
+    attr.val.clusterDim.x = k;
+    attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(k, 1, 1);
+    cfg.blockDim = dim3(kThreads, 1, 1);
+    cfg.dynamicSmemBytes = smem;
+    cfg.attrs = &attr;
+    cfg.numAttrs = 1;
+    int at_once = 0;
+    if (cudaOccupancyMaxActiveClusters(&at_once, tree_attn_kernel<D, true>, &cfg) != cudaSuccess) {
+      cudaGetLastError();
+      at_once = 0;
+    }
+    n = at_once + 1;
+  }
+  return n - 1;
+}
+
+// Size of the clusters that take an item each, or 0: equal runs and a join.  A team needs no
+// second kernel, which saves about 5 us, but its CTAs may have more units each than a run would;
+// a unit takes 0.9 us with one row tile and 1.5 with two.  Measured, runs against teams (8 heads of
+// 128 in groups of 4): 1 x 1 over 500 positions 10.8 and 8.0 us, 1 x 17 over 2000 13.0 and 10.4,
+// over 8191 17.1 and 16.5, over 16384 20.1 and 23.6, 4 x 17 over 2000 22.0 and 14.0.
+template <int D>
+int team_size(int64_t items, int64_t units, bool two_tiles, int num_sms, size_t smem) {
+  const int64_t run = (items * units + num_sms - 1) / num_sms;
+  for (int k = kMaxTeam; k >= 2; k /= 2)
+    if (items * k <= num_sms && items <= clusters_at_once<D>(k, smem))
+      return (units + k - 1) / k - run <= (two_tiles ? 3 : 5) ? k : 0;
+  return 0;
+}
+
 struct Tiling {
   int32_t tpt, row_tiles, pairs, areas;
 };
@@ -940,11 +1073,17 @@ cudaError_t launch(const AttnArgs& a, void* workspace, int num_sms, cudaStream_t
   const int64_t most = tree_attn_units(a.B, a.T, a.group, c.heads, c.capacity);
   if (most >= (int64_t(1) << 31)) return cudaErrorInvalidConfiguration;   // the entry point has refused it
   // Items of at most one unit per pipeline are left whole: nothing is gained by cutting them, and nothing has to
-  // be joined.  (Longer ones are worth it: 1 x 1 over 500 positions, 5 units, 12.3 us cut, 14.9 us whole.)
+  // be joined.  (1 x 1 over 500 positions, 5 units: 14.9 us whole, 12.3 in runs then, 8 in teams now.)
   p.whole = (static_cast<int64_t>(c.capacity) + kTile - 1) / kTile + (a.k_new != nullptr) <= kWholeUnits;
   int runs = static_cast<int>(imin64(imin64(num_sms, kMaxRuns), imax64(most, 1)));
   p.lanes = deal_lanes(t.row_tiles, runs);
   if (p.lanes.n == t.pairs) runs = p.lanes.n * p.lanes.runs;
+  const size_t smem = C::kRing + sizeof(AttnSmem);
+  cudaError_t e = set_smem_limit<tree_attn_kernel<D, true>>(smem);
+  if (e != cudaSuccess) return e;
+  const int64_t items = a.B * c.heads * t.pairs;
+  p.team = p.whole ? 0 : team_size<D>(items, most / items, t.row_tiles > 1, num_sms, smem);
+  if (p.team > 0) p.lanes = {0, 0};
   p.part = static_cast<float*>(workspace);
   p.part_ml = reinterpret_cast<float2*>(p.part + static_cast<size_t>(2) * num_sms * t.areas * kTile * D);
   p.cuts = reinterpret_cast<int4*>(p.part_ml + static_cast<size_t>(2) * num_sms * t.areas * kTile);
@@ -977,18 +1116,29 @@ cudaError_t launch(const AttnArgs& a, void* workspace, int num_sms, cudaStream_t
       return cudaErrorInvalidValue;
   }
 
-  const size_t smem = C::kRing + sizeof(AttnSmem);
-  cudaError_t e = set_smem_limit<tree_attn_kernel<D>>(smem);
-  if (e != cudaSuccess) return e;
-  cudaLaunchAttribute attr = pdl_attribute();
+  cudaLaunchAttribute attr[2] = {pdl_attribute(), {}};
   cudaLaunchConfig_t cfg = {};
+  if (p.team > 0) {
+    attr[1].id = cudaLaunchAttributeClusterDimension;
+    attr[1].val.clusterDim.x = p.team;
+    attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
+    cfg.gridDim = dim3(static_cast<unsigned>(items * p.team), 1, 1);
+    cfg.blockDim = dim3(kThreads, 1, 1);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = stream;
+    cfg.attrs = attr;
+    cfg.numAttrs = 2;
+    return cudaLaunchKernelEx(&cfg, tree_attn_kernel<D, true>, tmQ, tmK, tmV, tmKn, tmVn, p);
+  }
+  e = set_smem_limit<tree_attn_kernel<D, false>>(smem);
+  if (e != cudaSuccess) return e;
   cfg.gridDim = dim3(runs, 1, 1);
   cfg.blockDim = dim3(kThreads, 1, 1);
   cfg.dynamicSmemBytes = smem;
   cfg.stream = stream;
-  cfg.attrs = &attr;
+  cfg.attrs = attr;
   cfg.numAttrs = 1;
-  e = cudaLaunchKernelEx(&cfg, tree_attn_kernel<D>, tmQ, tmK, tmV, tmKn, tmVn, p);
+  e = cudaLaunchKernelEx(&cfg, tree_attn_kernel<D, false>, tmQ, tmK, tmV, tmKn, tmVn, p);
   if (e != cudaSuccess || runs == 1 || p.whole) return e;
   // one CTA per task up to two per SM; at most runs - 1 items are cut
   cfg.gridDim = dim3(static_cast<unsigned>(imin64(2 * num_sms, static_cast<int64_t>(runs - 1) * t.areas * (D / kNarrowCols))),

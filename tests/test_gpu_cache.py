@@ -676,3 +676,20 @@ def test_scores_of_blocks_that_differ_in_accepted_nodes(handle, T, heads, H, D, 
     # enough units that runs are cut by weight: sequences of many and of few rows, empty ones among them
     lens = [4096, 0, 130, 3000, 4000, 1, 4096, 2500, 0, 129, 3583, 2048]
     test_scores(handle, lens, T, heads, H, D, page, tree)
+
+
+@pytest.mark.parametrize("lens,T,heads,H,D", [([900], 1, 8, 2, 128), ([1500, 0], 17, 32, 8, 128), ([700, 1, 128, 640, 0, 511], 5, 24, 8, 64),
+                                              ([1200, 300], 33, 16, 2, 128), ([129], 128, 16, 1, 64), ([260, 0], 3, 2, 1, 128)])
+def test_short_items_shared_by_a_cluster(handle, lens, T, heads, H, D):
+    # a few items of a few tiles: CTAs without a tile of their item, one tile each, several
+    gen = torch.Generator(device="cuda").manual_seed(T + 40)
+    B = len(lens)
+    cache, rows = make_cache(gen, lens, H, D, 16, max(lens))
+    q, kn, vn = randn(gen, B, T, heads, D), randn(gen, B, T, H, D), randn(gen, B, T, H, D)
+    sees = np.tril(np.ones((T, T), bool))[None].repeat(B, 0)
+    cl = torch.tensor(lens, dtype=torch.int32, device="cuda")
+    got = api.tree_attention(handle, q, cache, cl, kn, vn)
+    again = api.tree_attention(handle, q, cache, cl, kn, vn)
+    assert torch.equal(got[0], again[0]) and torch.equal(got[1], again[1])
+    check_attention(got, reference(q, rows, kn, vn, sees, D ** -0.5))
+    assert handle.device_error() == 0
