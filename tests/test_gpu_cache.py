@@ -693,3 +693,20 @@ def test_short_items_shared_by_a_cluster(handle, lens, T, heads, H, D):
     assert torch.equal(got[0], again[0]) and torch.equal(got[1], again[1])
     check_attention(got, reference(q, rows, kn, vn, sees, D ** -0.5))
     assert handle.device_error() == 0
+
+
+@pytest.mark.parametrize("T,heads,H,D", [(5, 24, 4, 128), (33, 32, 4, 64)])
+def test_many_items_cut_by_runs(handle, T, heads, H, D):
+    # more items than clusters fit: equal runs cut many of them, each into a few parts
+    gen = torch.Generator(device="cuda").manual_seed(T + 50)
+    lens = [1000 - 37 * i for i in range(26)] + [0, 1]
+    B = len(lens)
+    cache, rows = make_cache(gen, lens, H, D, 32, max(lens))
+    q, kn, vn = randn(gen, B, T, heads, D), randn(gen, B, T, H, D), randn(gen, B, T, H, D)
+    sees = np.tril(np.ones((T, T), bool))[None].repeat(B, 0)
+    cl = torch.tensor(lens, dtype=torch.int32, device="cuda")
+    got = api.tree_attention(handle, q, cache, cl, kn, vn)
+    again = api.tree_attention(handle, q, cache, cl, kn, vn)
+    assert torch.equal(got[0], again[0]) and torch.equal(got[1], again[1])
+    check_attention(got, reference(q, rows, kn, vn, sees, D ** -0.5))
+    assert handle.device_error() == 0
