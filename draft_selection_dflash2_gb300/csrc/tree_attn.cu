@@ -25,8 +25,8 @@
 //   warps 1, 2  S products of pipelines 0 and 1: S = Q K^T for 64 keys at a time
 //               (fp32, two 64-column TMEM buffers per pipeline, so that the next
 //               S is computed under a softmax).
-//   warps 3, 12 O products: O += P V, with P (bf16) read from TMEM where it
-//               replaced S (and, over few keys, what P lost in rounding to bf16).
+//   warps 3, 12 O products: O += P V, with P read from TMEM where it replaced S,
+//               as two bf16 terms (P rounded, and what that lost).
 //               Each kind of product has its own warp per pipeline: the waits
 //               around a batch take about as long to execute as the batch itself.
 //   warps 4-7, 8-11  softmax of pipelines 0 and 1, one row per thread: S from
@@ -34,6 +34,11 @@
 //               to TMEM.  O is rescaled only when a row's maximum has risen by
 //               more than 2^8 since m was set (P then stays below 2^8, exact in
 //               scale), so most chunks never touch O outside the tensor cores.
+// P needs both terms: rounded to bf16 alone each weight is off by up to 2^-8, as much
+// as the output's own rounding, and nothing averages that out where the weights gather on a
+// few keys or many keys are alike (a P of 2^5.3 a thousand times is off the same way a
+// thousand times). With the second term it is 2^-16, and the output is the fp32 sum's
+// rounded once. That costs the tensor cores half as much again.
 // The two pipelines alternate on the tensor cores: one's softmax runs under the
 // other's products.  With two row tiles in the item each pipeline takes one of
 // them over every unit; with one row tile the pipelines take alternate units of
@@ -83,7 +88,6 @@ constexpr uint32_t kTmemO = 2 * kBufs * kChunk;   // first TMEM column of O: pip
 constexpr int kMaxRuns = 512;           // most CTAs
 constexpr int kMaxTeam = 8;              // most CTAs of a team (a power of 2)
 constexpr int kWholeUnits = 2;           // items of up to so many units are never cut
-constexpr int kTwoTermUnits = 12;       // items of up to so many units carry P in two terms
 constexpr float kRescale = 8.0f;        // log2 of how far P may exceed 1
 
 template <int D>
@@ -146,12 +150,6 @@ struct BufPos {
   __device__ __forceinline__ BufPos before() const { return {buf == 0 ? kBufs - 1 : buf - 1, buf == 0 ? use - 1 : use}; }
 };
 
-// The bf16 pair of what two fp32 values lose when they are rounded to bf16.
-__device__ __forceinline__ uint32_t remainder_bf16(float x, float y) {
-  const uint32_t hi = pack_bf16(x, y);
-  return pack_bf16(x - __uint_as_float(hi << 16), y - __uint_as_float(hi & 0xFFFF0000u));
-}
-
 // Key tiles of sequence b, the drafted one included (at least one, so that every row is written).
 __device__ __forceinline__ int32_t units_of(const AttnArgs& a, int32_t b) {
   const int32_t n = kv_clamp(a.cache_len[b], a.cache.capacity, a.err);
@@ -165,12 +163,6 @@ struct Segment {
   int32_t tiles;            // row tiles (2: one per pipeline; 1: shared by both)
   int32_t len;              // cached positions
   bool first;               // the run's first segment
-  // Whether P enters the product with V as two bf16 terms.  Rounding P to bf16
-  // perturbs each weight by up to 2^-8 on its own: over many keys that averages
-  // out below the output's own rounding, over few it does not: with up to 1000 keys
-  // a few of a million outputs were off by 1.2 to 1.4 times 2^-9 (|out| + sum p |v|).
-  // The second term costs 24 x 9 nodes over up to 3001 positions 3 us of 25.
-  __device__ __forceinline__ bool two_terms() const { return n <= kTwoTermUnits; }
   __device__ __forceinline__ int count() const { return e - s; }
   // keys of unit u: cached ones, or (the last unit, with drafted nodes) the nodes
   __device__ __forceinline__ bool drafted(const AttnArgs& a, int u) const {
@@ -588,7 +580,6 @@ __global__ void __launch_bounds__(kThreads, 1)
     while (walk.next(p, &g)) {
       const int step = g.tiles == 2 ? 1 : 2, off = g.tiles == 2 ? 0 : i;
       const int cnt = g.count(i);
-      const bool two = g.two_terms();
       RingPos<S> at = seg_v;
       at.advance(2 * off);
       for (int j = 0; j < cnt; ++j) {
@@ -605,11 +596,9 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
           for (int k = 0; k < kChunk / 16; ++k)
             umma_ts(tm_o, tm_p + k * 8, v_c + k * (2048 >> 4), idesc, (j > 0 || c > 0 || k > 0) ? 1u : 0u, lead);
-          if (two) {
 #pragma unroll
-            for (int k = 0; k < kChunk / 16; ++k)
-              umma_ts(tm_o, tm_p + kChunk / 2 + k * 8, v_c + k * (2048 >> 4), idesc, 1u, lead);
-          }
+          for (int k = 0; k < kChunk / 16; ++k)
+            umma_ts(tm_o, tm_p + kChunk / 2 + k * 8, v_c + k * (2048 >> 4), idesc, 1u, lead);
           umma_commit_if(&s.pv_done[i][buf], lead);
         }
         const uint32_t lead = live ? elected : 0u;
@@ -636,7 +625,6 @@ __global__ void __launch_bounds__(kThreads, 1)
       const int cnt = g.count(i);
       const int node = (2 * g.pair + (g.tiles == 2 ? i : 0)) * p.tpt + t_r;
       const bool row_ok = r < p.tpt * a.group && node < a.T;
-      const bool two = g.two_terms();
       // a warp none of whose rows is a query's has nothing to do but to keep step
       const bool busy = (warp & 3) * 32 < min(p.tpt, a.T - (node - t_r)) * a.group;
       float m = -INFINITY, l = 0.0f;
@@ -750,30 +738,24 @@ __global__ void __launch_bounds__(kThreads, 1)
             uint64_t sum0 = pack2(0.0f, 0.0f), sum1 = sum0;
 #pragma unroll
             for (int x = 0; x < 2; ++x) {
-              uint32_t hi[16];
+              uint32_t hi[16], lo[16];
 #pragma unroll
-              for (int y = 0; y < 32; y += 4) {
-                const float2 e0 = unpack2(fma2(pack2(z[x][y], z[x][y + 1]), c2, m2));
-                const float2 e1 = unpack2(fma2(pack2(z[x][y + 2], z[x][y + 3]), c2, m2));
-                z[x][y] = exp2_approx(e0.x);
-                z[x][y + 1] = exp2_approx(e0.y);
-                z[x][y + 2] = exp2_approx(e1.x);
-                z[x][y + 3] = exp2_approx(e1.y);
-                sum0 = add2(sum0, pack2(z[x][y], z[x][y + 1]));
-                sum1 = add2(sum1, pack2(z[x][y + 2], z[x][y + 3]));
-                hi[y / 2] = pack_bf16(z[x][y], z[x][y + 1]);
-                hi[y / 2 + 1] = pack_bf16(z[x][y + 2], z[x][y + 3]);
+              for (int y = 0; y < 32; y += 2) {
+                const float2 e = unpack2(fma2(pack2(z[x][y], z[x][y + 1]), c2, m2));
+                const float p0 = exp2_approx(e.x), p1 = exp2_approx(e.y);
+                const uint64_t pp = pack2(p0, p1);
+                if (y & 2)
+                  sum1 = add2(sum1, pp);
+                else
+                  sum0 = add2(sum0, pp);
+                // what P loses when it is rounded to bf16 is the second term
+                const uint32_t h = pack_bf16(p0, p1);
+                const float2 d = unpack2(add2(pp, pack2(-__uint_as_float(h << 16), -__uint_as_float(h & 0xFFFF0000u))));
+                hi[y / 2] = h;
+                lo[y / 2] = pack_bf16(d.x, d.y);
               }
               tmem_st_x16(tm_sb + 16 * x, hi);
-            }
-            if (two) {
-#pragma unroll
-              for (int x = 0; x < 2; ++x) {
-                uint32_t lo[16];
-#pragma unroll
-                for (int y = 0; y < 32; y += 2) lo[y / 2] = remainder_bf16(z[x][y], z[x][y + 1]);
-                tmem_st_x16(tm_sb + kChunk / 2 + 16 * x, lo);
-              }
+              tmem_st_x16(tm_sb + kChunk / 2 + 16 * x, lo);
             }
             const float2 sum = unpack2(add2(sum0, sum1));
             l += sum.x + sum.y;

@@ -473,7 +473,8 @@ typedef struct dflash2_kv_cache {
  * 65535; B * cache->heads * (capacity / 128 + 1) * (pairs of 128 query rows per kv
  * head) < 2^31; q, k_new and v_new 16-byte aligned, strides multiples of 8.  Dot
  * products, sums and statistics are fp32; the weights enter the product with the
- * values as bf16.  The same inputs give the same bits on every call.
+ * values to 16 bits (two bf16 terms), so that out is within one rounding to bf16,
+ * 2^-8 |out|, of the fp32 sum.  The same inputs give the same bits on every call.
  */
 size_t dflash2_tree_attention_workspace(const dflash2_handle* h, int64_t B, int64_t T, int64_t heads,
                                         int64_t kv_heads, int64_t head_dim);

@@ -1,0 +1,102 @@
+"""The cache operators where weights and values are at their limits.
+
+Definition (what a row sees: cached positions below the length, nodes of its mask):
+a key with z = -inf adds nothing, whatever its value; any other key adds
+exp(z - lse) value, so an infinite or NaN value of it reaches the row.
+
+Bounds, per element, from the number formats alone (no averaging is counted on):
+  z      a fp32 dot product of D terms: dz = D 2^-23 max(scale <|q|, |k|>)
+  out    2^-8 |out| (one rounding to bf16, 8 significant bits) +
+         (2 dz + 2^-15 + n 2^-24) A, A = sum p |v| over n keys: the weights' own error,
+         weights in two bf16 terms (2^-16) and fp32 sums
+"""
+import math
+
+import pytest
+import torch
+
+from draft_selection_dflash2_gb300 import api
+from gpu_common import handle  # noqa: F401
+from test_gpu_cache import make_cache, randn, write_rows
+
+pytestmark = pytest.mark.gpu
+INF = math.inf
+
+
+def lengths(lens):
+    return torch.tensor(lens, dtype=torch.int32, device="cuda")
+
+
+def definition(q, rows, k_new, v_new, sees, scale):
+    """fp64 (out, A, dz, n) of the definition above; non-finite values arrive as themselves."""
+    B, T, heads, D = q.shape
+    H = rows[0][0].shape[1]
+    G = heads // H
+    out = torch.zeros(B, T, heads, D, dtype=torch.float64, device="cuda")
+    A, dz = torch.zeros_like(out), torch.zeros(B, T, heads, dtype=torch.float64, device="cuda")
+    most = 0
+    for b in range(B):
+        for h in range(H):
+            qq = q[b, :, h * G:(h + 1) * G].double().reshape(T * G, D)
+            kk, vv = rows[b][0][:, h].double(), rows[b][1][:, h].double()
+            vis = torch.ones(T * G, kk.shape[0], dtype=torch.bool, device="cuda")
+            if k_new is not None:
+                kk, vv = torch.cat([kk, k_new[b, :, h].double()]), torch.cat([vv, v_new[b, :, h].double()])
+                s = torch.ones(T, T, dtype=torch.bool, device="cuda").tril() if sees is None else sees[b]
+                vis = torch.cat([vis, s.repeat_interleave(G, 0)], 1)
+            most = max(most, kk.shape[0])
+            z = qq @ kk.T * scale
+            adds = vis & (z != -INF)
+            z = torch.where(adds, z, -INF)
+            p = torch.softmax(z, 1).nan_to_num(0.0)           # a row without a key that adds: 0
+            o, a = p @ vv.nan_to_num(0.0, 0.0, 0.0), p @ vv.abs().nan_to_num(0.0, 0.0, 0.0)
+            for j in (~torch.isfinite(vv)).any(1).nonzero().flatten().tolist():
+                o += torch.where(adds[:, j:j + 1] & ~torch.isfinite(vv[j]), vv[j], 0.0)
+            out[b, :, h * G:(h + 1) * G] = o.reshape(T, G, D)
+            A[b, :, h * G:(h + 1) * G] = a.reshape(T, G, D)
+            zabs = torch.where(adds, qq.abs() @ kk.abs().nan_to_num(0.0, 0.0, 0.0).T * scale, 0.0)
+            dz[b, :, h * G:(h + 1) * G] = (D * 2.0 ** -23 * zabs.amax(1)).reshape(T, G)
+    return out, A, dz, most
+
+
+def check(got, want):
+    ro, A, dz, n = want
+    o = got.double()
+    live = torch.isfinite(ro)
+    assert torch.equal(torch.isnan(o), torch.isnan(ro))
+    assert torch.equal(torch.where(live | torch.isnan(o), 0.0, o), torch.where(live | torch.isnan(ro), 0.0, ro))
+    tol = 2.0 ** -8 * ro.abs() + (2 * dz[..., None] + 2.0 ** -15 + n * 2.0 ** -24) * A
+    err = torch.where(live, o - ro, 0.0).abs()
+    assert (err <= tol)[live].all(), ((err - tol)[live].max(), (err / tol)[live].nan_to_num(0.0).max())
+
+
+# ---------------------------------------------------------------------------
+# weights that gather on few keys
+# ---------------------------------------------------------------------------
+@pytest.mark.parametrize("n,T,heads,H,D,keys", [
+    (300, 1, 8, 8, 128, 1), (4000, 1, 8, 8, 128, 1), (4000, 1, 8, 8, 128, 2), (20000, 1, 8, 8, 64, 1),
+    (20000, 1, 8, 8, 64, 2), (6000, 34, 64, 8, 128, 1), (6000, 34, 64, 8, 128, 2), (6000, 34, 64, 8, 128, 900)])
+def test_weights_on_few_keys(handle, n, T, heads, H, D, keys):
+    # each (sequence, head) has one key, two, or many equal ones, 3 to 8 powers of two above the first key of every
+    # tile, and all others far below: with the maximum of a tile's start P is no power of two, and no error of
+    # another key averages it out
+    gen = torch.Generator(device="cuda").manual_seed(n + keys)
+    B, G = 4, heads // H
+    cache, rows = make_cache(gen, [n] * B, H, D, 64, n)
+    q = randn(gen, B, 1, H, D).repeat_interleave(G, 2).repeat(1, T, 1, 1)       # a kv head's rows are alike
+    above = torch.linspace(3.0, 8.0, B * H, device="cuda").reshape(B, H) * math.log(2.0)
+    at = sorted({200 + (n - 250) * i // max(keys, 1) for i in range(keys)})
+    for b in range(B):
+        kk, vv = rows[b]
+        for h in range(H):
+            qh = q[b, 0, h * G].float()
+            unit = qh / (qh @ qh * D ** -0.5)                  # a key with z = 1
+            kk[:, h] = (-12.0 * unit).to(torch.bfloat16)
+            kk[::128, h] = 0.0
+            kk[at, h] = (above[b, h] * unit).to(torch.bfloat16)
+        if keys == 900:
+            vv[at] = vv[at[:1]]
+        write_rows(cache, b, 0, kk, vv)
+    out, _ = api.tree_attention(handle, q.contiguous(), cache, lengths([n] * B))
+    check(out, definition(q, rows, None, None, None, D ** -0.5))
+    assert handle.device_error() == 0
