@@ -230,6 +230,20 @@ struct PageFeed {
   }
 };
 
+// A named barrier whose threads learn whether any of them brought `x`.
+__device__ __forceinline__ bool named_bar_or(int id, int count, bool x) {
+  uint32_t any;
+  asm volatile(
+      "{\n\t.reg .pred p, q;\n\t"
+      "setp.ne.b32 q, %3, 0;\n\t"
+      "bar.red.or.pred p, %1, %2, q;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(any)
+      : "r"(id), "r"(count), "r"(static_cast<uint32_t>(x))
+      : "memory");
+  return any != 0;
+}
+
 // Products are issued by whole warps of which one elected lane acts: the code
 // around them stays warp-uniform, so operands are computed in uniform registers,
 // and a product costs a few instructions instead of the tens that one lane alone

@@ -27,7 +27,9 @@
 // 4000 positions: 4.5 us, the latency of the first tiles.
 // When a run enters another (sequence, head) the epilogue warps lay that head's
 // query rows out in shared memory (up to 512 rows; more rows take one launch per
-// 512) and their lse beside them.
+// 512) and their lse beside them.  Rows that add nothing (their lse is -inf, and those
+// that fill the last 16 up) are zero there; as 0 times an infinite key is NaN, not 0,
+// their products are set to 0 before they are used.
 #include "attn_common.cuh"
 #include "launch.h"
 
@@ -295,6 +297,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       const int padded = (g.rows + 15) & ~15;
       constexpr int kPieces = D / 8, kRowStep = 2 * kTile / kPieces;
       const int piece = tid % kPieces;
+      bool empty = false;                // whether one of the thread's rows adds nothing
       // kQBatch pieces a thread, so that their chains path -> lse and query run together
       for (int row0 = tid / kPieces; row0 < padded; row0 += kQBatch * kRowStep) {
         int t[kQBatch], hq[kQBatch];
@@ -323,6 +326,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           if (row >= padded) break;
           // a query that saw nothing adds nothing, nor do the rows past the last
           if (lse[y] == -INFINITY) v[y] = make_uint4(0, 0, 0, 0);
+          empty |= row < g.rows && lse[y] == -INFINITY;
           *reinterpret_cast<uint4*>(q_smem + (piece >> 3) * q_half + row * 128 + (((piece & 7) ^ (row & 7)) << 4)) = v[y];
           if (piece == 0) s.lse[row] = lse[y] == -INFINITY ? -INFINITY : lse[y] * -1.4426950408889634f;
         }
@@ -330,7 +334,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       __syncwarp();
       asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
       mbar_arrive(&s.q_full);
-      named_bar_sync(1, 2 * kTile);      // the rows' lse is there
+      empty = named_bar_or(1, 2 * kTile, empty);      // the rows' lse is there
       ch.set(g.rows);
       for (int u = g.s + ((it0 ^ e) & 1); u < g.e; u += 2) {
         // the key's total so far, on its way while the products are waited for
@@ -345,6 +349,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           __syncwarp();
           tc_fence_after();
           const int cols = ch.cols(c);
+          const int sure = empty ? 0 : g.rows - c * ch.width;   // columns below this one add something
           const float* l2 = s.lse + c * ch.width;
           const uint32_t tm = tmem + e * 2 * kTile + buf * kTile + lanes;
           const auto add16 = [&](const float* z, const float* l2x) {
@@ -357,6 +362,11 @@ __global__ void __launch_bounds__(kThreads, 1)
               sum1 = add2(sum1, pack2(exp2_approx(e1.x), exp2_approx(e1.y)));
             }
           };
+          const auto clear_empty = [&](auto& z, const float* l2x) {
+#pragma unroll
+            for (int y = 0; y < static_cast<int>(sizeof(z) / sizeof(z[0])); ++y)
+              if (l2x[y] == -INFINITY) z[y] = 0.0f;
+          };
           int x = 0;
 #pragma unroll 1
           for (; x + 32 <= cols; x += 32) {
@@ -364,6 +374,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             tmem_ld_x32(tm + x, z);
             tmem_ld_wait();
             pin(z);
+            if (x + 32 > sure) clear_empty(z, l2 + x);
             add16(z, l2 + x);
             add16(z + 16, l2 + x + 16);
           }
@@ -372,6 +383,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             tmem_ld_x16(tm + x, z);
             tmem_ld_wait();
             pin16(z);
+            if (x + 16 > sure) clear_empty(z, l2 + x);
             add16(z, l2 + x);
           }
           tc_fence_before();

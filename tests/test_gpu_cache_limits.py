@@ -9,6 +9,7 @@ Bounds, per element, from the number formats alone (no averaging is counted on):
   out    2^-8 |out| (one rounding to bf16, 8 significant bits) +
          (2 dz + 2^-15 + n 2^-24) A, A = sum p |v| over n keys: the weights' own error,
          weights in two bf16 terms (2^-16) and fp32 sums
+  score  (dz + 2^-20) w + 2^-22 (w + what was there)
 """
 import math
 
@@ -100,3 +101,52 @@ def test_weights_on_few_keys(handle, n, T, heads, H, D, keys):
     out, _ = api.tree_attention(handle, q.contiguous(), cache, lengths([n] * B))
     check(out, definition(q, rows, None, None, None, D ** -0.5))
     assert handle.device_error() == 0
+
+
+# ---------------------------------------------------------------------------
+# scores
+# ---------------------------------------------------------------------------
+@pytest.mark.parametrize("T,heads,H,D", [(1, 8, 1, 128), (2, 16, 1, 64), (5, 6, 2, 64), (17, 16, 2, 128)])
+def test_scores_of_infinite_keys(handle, T, heads, H, D):
+    # keys with z = -inf for every query, row counts that are and are not multiples of 16, queries that saw nothing
+    gen = torch.Generator(device="cuda").manual_seed(T)
+    G, n = heads // H, 150
+    cache, rows = make_cache(gen, [n], H, D, 16, n)
+    q = randn(gen, 1, T, heads, D)
+    q[..., 7] = q[..., 7].abs() + 0.5
+    kk, vv = rows[0]
+    dead = [0, 3, 127, 128, n - 1]
+    kk[dead, :, 7] = -INF
+    write_rows(cache, 0, 0, kk, vv)
+    _, lse = api.tree_attention(handle, q, cache, lengths([n]))
+    assert torch.isfinite(lse).all()
+    start = torch.rand(1, H, n, generator=gen, device="cuda")
+    for empty in (None, 0, T - 1):
+        if empty is not None:
+            lse[0, empty] = -INF
+        scores = start.clone()
+        api.cache_scores(handle, q, lse, cache, lengths([n]), scores)
+        for h in range(H):
+            qq, ll = q[0, :, h * G:(h + 1) * G].double().reshape(-1, D), lse[0, :, h * G:(h + 1) * G].double().reshape(-1, 1)
+            z = qq @ kk[:, h].double().T * D ** -0.5
+            w = torch.where(torch.isinf(ll), 0.0, torch.exp(z - ll)).sum(0)
+            assert (w[dead] == 0).all()
+            zabs = torch.where(torch.isinf(z), 0.0, qq.abs() @ kk[:, h].double().abs().nan_to_num(0.0, 0.0, 0.0).T * D ** -0.5)
+            dz, was = D * 2.0 ** -23 * zabs.amax(), start[0, h].double()
+            err = (scores[0, h].double() - was - w).abs()
+            assert (err <= (dz + 2.0 ** -20) * w + 2.0 ** -22 * (w + was)).all(), err.max()
+    assert handle.device_error() == 0
+
+
+@pytest.mark.parametrize("T,heads", [(1, 8), (2, 16)])
+def test_scores_of_what_attention_found_empty(handle, T, heads):
+    # a cache whose keys put every z at -inf: attention leaves lse = -inf, and nothing is added with it
+    cache, rows = make_cache(torch.Generator(device="cuda").manual_seed(1), [140], 1, 64, 16, 140)
+    rows[0][0][:] = -INF
+    write_rows(cache, 0, 0, *rows[0])
+    q = torch.ones(1, T, heads, 64, dtype=torch.bfloat16, device="cuda")
+    out, lse = api.tree_attention(handle, q, cache, lengths([140]))
+    assert (out == 0).all() and torch.isneginf(lse).all()
+    scores = torch.full((1, 1, 140), 2.0, device="cuda")
+    api.cache_scores(handle, q, lse, cache, lengths([140]), scores)
+    assert (scores == 2.0).all() and handle.device_error() == 0
