@@ -30,6 +30,8 @@
 // 512) and their lse beside them.  Rows that add nothing (their lse is -inf, and those
 // that fill the last 16 up) are zero there; as 0 times an infinite key is NaN, not 0,
 // their products are set to 0 before they are used.
+#include <cstddef>
+
 #include "attn_common.cuh"
 #include "launch.h"
 
@@ -44,11 +46,13 @@ constexpr int kSmemLimit = 232448;      // 227 KB
 
 struct ScoresSmem {
   uint64_t k_full[2 * kMaxSlots], k_empty[kMaxSlots];
-  uint64_t q_full, s_full[2][2], s_free[2][2], drain;   // [epilogue][TMEM buffer]
-  float lse[kMaxQTiles * kTile];        // negated, in base 2: -inf for rows that add nothing
+  uint64_t q_full[2], s_full[2][2], s_free[2][2], drain;   // q: segments by turns; s: [epilogue][TMEM buffer]
+  alignas(16) float lse[kMaxQTiles * kTile];   // negated, in base 2: -inf for rows that add nothing (read by fours)
   uint32_t tmem;
   int abort_flag;
 };
+
+static_assert(offsetof(ScoresSmem, lse) % 16 == 0, "read as float4");
 
 struct ScoresPlan {
   ScoresArgs a;
@@ -177,7 +181,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       mbar_init(&s.k_full[2 * i + 1], 1);
       mbar_init(&s.k_empty[i], 1);
     }
-    mbar_init(&s.q_full, 2 * kTile);
+    mbar_init(&s.q_full[0], 2 * kTile);
+    mbar_init(&s.q_full[1], 2 * kTile);
     for (int i = 0; i < 4; ++i) {
       mbar_init(&s.s_full[i >> 1][i & 1], 1);
       mbar_init(&s.s_free[i >> 1][i & 1], kTile);
@@ -256,7 +261,10 @@ __global__ void __launch_bounds__(kThreads, 1)
     uint32_t it0 = 0;             // the run's units before this segment
     int seg = 0;
     for (; walk.next(p, &g); ++seg) {
-      wait_live(&s.q_full, seg & 1, &live, abort_flag, a.err);
+      // Nothing holds the epilogues back for an issuer without a unit in the segment: they may have laid out
+      // the next one's rows before it looks.  They cannot be two ahead, as of two units in turn one is the
+      // issuer's; so segments alternate between two barriers, and a phase cannot be mistaken for the next.
+      wait_live(&s.q_full[seg & 1], seg >> 1 & 1, &live, abort_flag, a.err);
       ch.set(g.rows);
       for (int u = g.s + ((it0 ^ e) & 1); u < g.e; u += 2, at.advance(2, S)) {
         wait_live(at.full(s.k_full), at.parity(), &live, abort_flag, a.err);
@@ -290,7 +298,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     uint32_t it0 = 0;             // the run's units before this segment
     uint32_t n = 0;               // chunks so far
     Chunks ch;
-    while (walk.next(p, &g)) {
+    for (int seg = 0; walk.next(p, &g); ++seg) {
       // both halves have read every product of the last segment: its query rows may go
       __syncwarp();
       named_bar_sync(1, 2 * kTile);
@@ -333,7 +341,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       __syncwarp();
       asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
-      mbar_arrive(&s.q_full);
+      mbar_arrive(&s.q_full[seg & 1]);
       empty = named_bar_or(1, 2 * kTile, empty);      // the rows' lse is there
       ch.set(g.rows);
       for (int u = g.s + ((it0 ^ e) & 1); u < g.e; u += 2) {

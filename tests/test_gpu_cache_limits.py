@@ -150,3 +150,28 @@ def test_scores_of_what_attention_found_empty(handle, T, heads):
     scores = torch.full((1, 1, 140), 2.0, device="cuda")
     api.cache_scores(handle, q, lse, cache, lengths([140]), scores)
     assert (scores == 2.0).all() and handle.device_error() == 0
+
+
+@pytest.mark.parametrize("B,n,T,heads,H,D", [(40, 128, 1, 32, 16, 128), (60, 100, 17, 32, 16, 64), (33, 129, 3, 60, 20, 128)])
+def test_scores_of_many_short_heads(handle, B, n, T, heads, H, D):
+    # runs of several (sequence, head) of one tile each: an issuer of products is idle in every other one
+    gen = torch.Generator(device="cuda").manual_seed(B)
+    G = heads // H
+    lens = [n - 7 * b % 30 for b in range(B)]
+    cache, rows = make_cache(gen, lens, H, D, 0, n)
+    q = randn(gen, B, T, heads, D)
+    _, lse = api.tree_attention(handle, q, cache, lengths(lens))
+    first = None
+    for _ in range(20):
+        scores = torch.zeros(B, H, n, device="cuda")
+        api.cache_scores(handle, q, lse, cache, lengths(lens), scores)
+        first = scores if first is None else first
+        assert torch.equal(scores, first)
+    for b in range(B):
+        qq = q[b].double().reshape(T, H, G, D)
+        z = torch.einsum("thgd,jhd->hjtg", qq, rows[b][0].double()) * D ** -0.5
+        w = torch.exp(z - lse[b].double().reshape(T, H, 1, G).permute(1, 2, 0, 3)).sum((2, 3))
+        dz = D * 2.0 ** -23 * torch.einsum("thgd,jhd->hjtg", qq.abs(), rows[b][0].double().abs()).max() * D ** -0.5
+        assert ((first[b, :, :lens[b]].double() - w).abs() <= (dz + 2.0 ** -20) * w + 2.0 ** -22 * w).all()
+        assert (first[b, :, lens[b]:] == 0).all()
+    assert handle.device_error() == 0
