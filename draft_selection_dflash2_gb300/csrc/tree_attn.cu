@@ -45,9 +45,14 @@
 // it and their two (O, m, l) are added at the end.
 //
 // A value no row sees must not reach the sums even as 0 * NaN: cached V rows past
-// the length are zeroed in shared memory, and a drafted node's non-finite values
-// (which only some rows may see) are zeroed there too and added to the rows that
-// do see them when the item is written.
+// the length are zeroed in shared memory, and so are a drafted node's non-finite values,
+// which only some rows may see.  Nor may a key that a row does see reach it as 0 * inf
+// (z = -inf, or P's second term) or inf - inf (both terms), and a
+// finite value times a P of 2^8 may not become infinite.  So where a row's O is not finite
+// at the end, or the row sees a drafted node that was zeroed, the CTA takes the row's sums
+// again at the end of its run, key by key (sum_again): a key with z = -inf is passed over,
+// an infinite or NaN value of another one is added as it is, and m is the maximum so far.
+// That costs the usual call one operation per element of O.
 //
 // What bounds it, and what it measured (GB300, heads in groups of 8 over 8 kv heads,
 // D = 128 unless said otherwise):
@@ -106,6 +111,7 @@ struct AttnSmem {
   uint32_t bad[4];          // drafted nodes that hold a non-finite value
   uint32_t tmem;
   int abort_flag;
+  int odd;                  // whether some row's sums have to be taken again
 };
 
 // How CTAs are dealt to the pairs of row tiles of a kv head.  With lanes.n = 0 a run
@@ -255,24 +261,125 @@ __device__ __noinline__ void rescale_rows(uint32_t tm, int cols, float f) {
   }
 }
 
-// Adds the non-finite values of the drafted nodes in `bad` that node `node` sees to
-// its row's columns [c0, c1): of the output (part = nullptr), or of the run's part,
-// four columns every kTile float4.  Out of line: it is hardly ever called.
-__device__ __noinline__ void add_non_finite(const AttnArgs& a, const uint32_t* bad, int b, int h, int node, int c0, int c1,
-                                            uint16_t* out, float* part) {
-  for (int sn = 0; sn < a.T; ++sn) {
-    if (!(bad[sn >> 5] >> (sn & 31) & 1u)) continue;
-    const bool sees = a.mask == nullptr ? sn <= node
-                                        : a.mask[(static_cast<int64_t>(b) * a.T + node) * ((a.T + 63) >> 6) + (sn >> 6)] >>
-                                                  (sn & 63) & 1;
-    if (!sees) continue;
-    const uint16_t* v = a.v_new + b * a.new_b + sn * a.new_t + h * a.new_h;
-    for (int x = c0; x < c1; ++x) {
-      if (finite_bf16(v[x])) continue;
-      if (part != nullptr)
-        part[static_cast<int64_t>(x >> 2) * kTile * 4 + (x & 3)] += bf16_bits_to_float(v[x]);
-      else
-        out[x] = __bfloat16_as_ushort(__float2bfloat16_rn(bf16_bits_to_float(out[x]) + bf16_bits_to_float(v[x])));
+// A sum's part v, to be weighted by f >= 0.  An infinity stays one where f underflows
+// (the weights of the definition do not).
+__device__ __forceinline__ float weighted(float v, float f) { return fabsf(v) < INFINITY ? v * f : v; }
+
+// Where a segment's sums go: to the output, or to its parts, a run's in the workspace
+// (the first segment's in slot 2 c, another's in 2 c + 1), a team's CTA's in its ring.
+template <int D, bool kTeam>
+struct PartPlace {
+  bool whole;
+  int slot;
+  float4* parts;
+  float2* mls;
+  __device__ __forceinline__ PartPlace(const AttnPlan& p, const Segment& g, uint8_t* ring)
+      : whole(!kTeam && g.s == 0 && g.e == g.n),
+        slot(kTeam ? 0 : 2 * static_cast<int>(blockIdx.x) + (g.first ? 0 : 1)),
+        parts(reinterpret_cast<float4*>(kTeam ? ring : reinterpret_cast<uint8_t*>(p.part))),
+        mls(kTeam ? reinterpret_cast<float2*>(ring + 2 * kTile * D * 4) : p.part_ml) {}
+  // The tile's O, four columns every kTile float4, and row r's m and l.
+  __device__ __forceinline__ float4* part(const AttnPlan& p, int tile) const {
+    return parts + (static_cast<int64_t>(slot) * p.areas + tile) * (D / 4) * kTile;
+  }
+  __device__ __forceinline__ float2* ml(const AttnPlan& p, int tile, int r) const {
+    return mls + (static_cast<int64_t>(slot) * p.areas + tile) * kTile + r;
+  }
+};
+
+// <q, k> over D bf16 each.
+template <int D>
+__device__ __forceinline__ float dot_bf16(const uint16_t* q, const uint16_t* k) {
+  float z = 0.0f;
+#pragma unroll 4
+  for (int x = 0; x < D; x += 8) {
+    const uint4 a = *reinterpret_cast<const uint4*>(q + x), b = *reinterpret_cast<const uint4*>(k + x);
+    const uint32_t u[4] = {a.x, a.y, a.z, a.w}, w[4] = {b.x, b.y, b.z, b.w};
+#pragma unroll
+    for (int y = 0; y < 4; ++y) {
+      z = fmaf(bf16_bits_to_float(u[y]), bf16_bits_to_float(w[y]), z);
+      z = fmaf(__uint_as_float(u[y] & 0xFFFF0000u), __uint_as_float(w[y] & 0xFFFF0000u), z);
+    }
+  }
+  return z;
+}
+
+// Takes the sums of the run's rows that hold a non-finite value again, each by a warp of
+// the softmax: 32 keys at a time, a lane each, then all lanes on each key's value.  Out of
+// line: it is hardly ever called.
+template <int D, bool kTeam>
+__device__ __noinline__ void sum_again(const AttnPlan& p, Walk walk, uint8_t* ring) {
+  constexpr int E = D / 32;              // columns of a lane
+  const AttnArgs& a = p.a;
+  const int lane = threadIdx.x & 31;
+  Segment g;
+  while (walk.next(p, &g)) {
+    const PartPlace<D, kTeam> place(p, g, ring);
+    for (int tile = 0; tile < g.tiles; ++tile) {
+      const int node0 = (2 * g.pair + tile) * p.tpt, rows = min(p.tpt, a.T - node0) * a.group;
+#pragma unroll 1
+      for (int r = (threadIdx.x >> 5) - 4; r < rows; r += 2 * kTile / 32) {
+        const int t = r / a.group, node = node0 + t, hq = g.h * a.group + r - t * a.group;
+        uint16_t* out = a.out + ((static_cast<int64_t>(g.b) * a.T + node) * a.heads + hq) * D + lane * E;
+        float* part = reinterpret_cast<float*>(place.part(p, tile) + lane * E / 4 * kTile + r) + lane * E % 4;
+        bool finite = true;
+#pragma unroll
+        for (int e = 0; e < E; ++e) finite &= place.whole ? finite_bf16(out[e]) : fabsf(part[e]) < INFINITY;
+        if (__all_sync(0xFFFFFFFFu, finite)) continue;
+        const uint16_t* q = a.q + g.b * a.q_b + node * a.q_t + hq * a.q_h;
+        float m = -INFINITY, l = 0.0f, o[E] = {};   // l: of the lane's keys
+#pragma unroll 1
+        for (int u = g.s; u < g.e; ++u) {
+          const bool drafted = g.drafted(a, u);
+          const int keys = g.keys(a, u);
+#pragma unroll 1
+          for (int x = lane; x - lane < keys; x += 32) {
+            bool adds = x < keys;
+            if (adds && drafted)
+              adds = a.mask == nullptr ? x <= node
+                                       : a.mask[(static_cast<int64_t>(g.b) * a.T + node) * ((a.T + 63) >> 6) + (x >> 6)] >>
+                                                 (x & 63) & 1;
+            const uint16_t* v = nullptr;
+            float z = -INFINITY;
+            if (adds) {
+              bool ok;
+              const int64_t at = drafted ? g.b * a.new_b + x * a.new_t + g.h * a.new_h
+                                         : kv_offset(a.cache, g.b, u * kTile + x, g.h, nullptr, &ok);
+              v = (drafted ? a.v_new : a.cache.v) + at;
+              z = dot_bf16<D>(q, (drafted ? a.k_new : a.cache.k) + at);
+              adds = z * a.scale != -INFINITY;
+            }
+            float top = m;
+            if (adds) top = fmaxf(top, z * p.c);
+#pragma unroll
+            for (int d = 16; d > 0; d >>= 1) top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, d));
+            const float f = m == -INFINITY ? 1.0f : exp2_approx(m - top);
+            const float w = adds ? exp2_approx(fmaf(z, p.c, top == -INFINITY ? 0.0f : -top)) : 0.0f;
+            m = top;
+            l = l * f + w;
+#pragma unroll
+            for (int e = 0; e < E; ++e) o[e] = weighted(o[e], f);
+            for (uint32_t some = __ballot_sync(0xFFFFFFFFu, adds); some != 0; some &= some - 1) {
+              const int y = __ffs(some) - 1;
+              const auto* vy =
+                  reinterpret_cast<const uint16_t*>(__shfl_sync(0xFFFFFFFFu, reinterpret_cast<unsigned long long>(v), y));
+              const float wy = __shfl_sync(0xFFFFFFFFu, w, y);
+#pragma unroll
+              for (int e = 0; e < E; ++e) o[e] += weighted(bf16_bits_to_float(vy[lane * E + e]), wy);
+            }
+          }
+        }
+#pragma unroll
+        for (int d = 16; d > 0; d >>= 1) l += __shfl_xor_sync(0xFFFFFFFFu, l, d);
+        if (place.whole) {
+#pragma unroll
+          for (int e = 0; e < E; ++e) out[e] = __bfloat16_as_ushort(__float2bfloat16_rn(l == 0.0f ? 0.0f : o[e] / l));
+        } else {
+#pragma unroll
+          for (int e = 0; e < E; ++e) part[e] = o[e];
+          if (lane == 0) *place.ml(p, tile, r) = make_float2(m, -l);   // (see PartSum::add)
+        }
+      }
     }
   }
 }
@@ -281,11 +388,18 @@ __device__ __noinline__ void add_non_finite(const AttnArgs& a, const uint32_t* b
 template <int N>
 struct PartSum {
   float m = -INFINITY, l = 0.0f, o[N] = {};
+  bool odd = false;          // whether an infinity may be in o
   // Adds sums (m1, l1, v); with m1 = -inf they saw nothing, and v is not looked at.
+  // A negative l1 says that v may hold infinities.
   __device__ __forceinline__ void add(float m1, float l1, const float (&v)[N]) {
+    odd |= l1 < 0.0f;
+    l1 = fabsf(l1);
     const bool some = m1 != -INFINITY;
     const float top = fmaxf(m, m1);
-    const float f0 = m == -INFINITY ? 0.0f : exp2_approx(m - top), f1 = some ? exp2_approx(m1 - top) : 0.0f;
+    // an infinity stays one where its weight underflows: that of the definition does not
+    const float least = odd ? 1.4e-45f : 0.0f;
+    const float f0 = m == -INFINITY ? 0.0f : fmaxf(exp2_approx(m - top), least);
+    const float f1 = some ? fmaxf(exp2_approx(m1 - top), least) : 0.0f;
     m = top;
     l = l * f0 + (some || l1 != l1 ? l1 * (some ? f1 : 1.0f) : 0.0f);   // only NaN scores: l1 is NaN
 #pragma unroll
@@ -416,6 +530,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     mbar_init(&s.drain, 4);
     s.abort_flag = 0;
+    s.odd = 0;
     fence_mbar_init();
     tma_prefetch_desc(&tmQ);
     tma_prefetch_desc(&tmK);
@@ -768,10 +883,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       seg_v.advance_far(2 * g.count());
 
       // ---- the item's (or the run's part of the item's) sums ----
-      const bool whole = !kTeam && g.s == 0 && g.e == g.n;
-      const int slot = kTeam ? 0 : 2 * blockIdx.x + (g.first ? 0 : 1);
-      float4* const parts = kTeam ? reinterpret_cast<float4*>(ring) : reinterpret_cast<float4*>(p.part);
-      float2* const part_ml = kTeam ? reinterpret_cast<float2*>(ring + 2 * kTile * D * 4) : p.part_ml;
+      const PartPlace<D, kTeam> place(p, g, ring);
+      const bool whole = place.whole;
       const bool merge = g.tiles == 1;
       float f0 = 1.0f, f1 = 0.0f;     // weights of O0 and O1 (one tile), or of O_i
       // products complete in the order of their issue: the last one's is enough
@@ -807,7 +920,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           if (row_ok && a.lse != nullptr)
             a.lse[orow] = l == 0.0f ? -INFINITY : (m + log2f(l)) * 0.69314718055994531f;
         } else {
-          part_ml[(static_cast<int64_t>(slot) * p.areas + area) * kTile + r] = make_float2(m, l);
+          *place.ml(p, area, r) = make_float2(m, l);
         }
       }
       if (!kTeam && threadIdx.x == kTile && walk.left <= 0)        // the run's last segment
@@ -816,11 +929,9 @@ __global__ void __launch_bounds__(kThreads, 1)
                 ? make_int4(g.b, g.h * p.pairs + g.pair,
                             static_cast<int>(blockIdx.x) +
                                 p.lanes.step(g.pair) * ((g.n - g.e + run.units - 1) / run.units),
-                            slot)
+                            place.slot)
                 : make_int4(-1, 0, 0, 0);
-      // with one tile only the pipeline that took the drafted tile knows what its rows saw there
-      bool fix = bad_seen != 0;
-      if (merge) fix = a.k_new != nullptr && g.e == g.n && (s.bad[0] | s.bad[1] | s.bad[2] | s.bad[3]) != 0;
+      uint64_t odd[4] = {};           // 0, or NaN once an element of O is not finite (four chains of pairs)
 #pragma unroll 1
       for (int x = c0; x < c1; x += 32) {
         float o[32];
@@ -842,6 +953,9 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
           for (int y = 0; y < 32; ++y) o[y] = 0.0f;
         }
+        if (bad_seen != 0 && !empty) o[0] = NAN;   // the row lacks the values of nodes that were zeroed
+#pragma unroll
+        for (int y = 0; y < 32; y += 2) odd[y / 2 & 3] = fma2(pack2(o[y], o[y + 1]), 0ull, odd[y / 2 & 3]);
         if (whole) {
           if (row_ok) {
             uint4* dst = reinterpret_cast<uint4*>(a.out + orow * D + x);
@@ -851,20 +965,25 @@ __global__ void __launch_bounds__(kThreads, 1)
                                       pack_bf16(o[y + 4], o[y + 5]), pack_bf16(o[y + 6], o[y + 7]));
           }
         } else if (row_ok) {
-          float4* dst = parts + ((static_cast<int64_t>(slot) * p.areas + area) * (D / 4) + x / 4) * kTile + r;
+          float4* dst = place.part(p, area) + x / 4 * kTile + r;
 #pragma unroll
           for (int y = 0; y < 32; y += 4) dst[(y / 4) * kTile] = make_float4(o[y], o[y + 1], o[y + 2], o[y + 3]);
         }
       }
-      if (fix && row_ok)
-        add_non_finite(a, s.bad, g.b, g.h, node, c0, c1, a.out + orow * D,
-                       whole ? nullptr
-                             : reinterpret_cast<float*>(
-                                   parts + (static_cast<int64_t>(slot) * p.areas + area) * (D / 4) * kTile + r));
+      const float2 odds = unpack2(add2(add2(odd[0], odd[1]), add2(odd[2], odd[3])));
+      if (odds.x + odds.y != 0.0f && row_ok && l == l) s.odd = 1;   // (with a NaN score the row is NaN throughout)
       __syncwarp();
       tc_fence_before();
       // O and the shared statistics may be overwritten once both pipelines have read them
       named_bar_sync(1, 2 * kTile);
+    }
+    if (s.odd != 0) {   // written before the last segment's barrier
+      Walk anew;
+      if constexpr (kTeam)
+        anew.start_team(p, blockIdx.x / p.team, blockIdx.x % p.team);
+      else
+        anew.start(run);
+      sum_again<D, kTeam>(p, anew, ring);
     }
   }
 
@@ -945,7 +1064,7 @@ __global__ void __launch_bounds__(kJoinThreads, 2) tree_attn_join_kernel(const _
       PartSum<kNarrowCols> sum;
       if (row_ok) sum.template add_parts<D, 4>(p, d, c0, c0 + y * step, kJoinSplit * step, tile, x, r);
       s_o[y][kNarrowCols][r] = sum.m;
-      s_o[y][kNarrowCols + 1][r] = sum.l;
+      s_o[y][kNarrowCols + 1][r] = sum.odd ? -sum.l : sum.l;
 #pragma unroll
       for (int k = 0; k < kNarrowCols; ++k) s_o[y][k][r] = sum.o[k];
       __syncthreads();

@@ -455,7 +455,10 @@ typedef struct dflash2_kv_cache {
  *   z_x = scale <q[b,t,hq], key_x>,  lse = log sum_x exp(z_x),
  *   out[b,t,hq] = sum_x exp(z_x - lse) value_x.
  * A row that sees nothing, or only keys with z = -inf, gives out = 0 and lse =
- * -inf.  What a row does not see never reaches it, whatever values it holds.
+ * -inf.  What a row does not see never reaches it, whatever values it holds, nor
+ * does the value of a key with z = -inf; an infinite or NaN value of any other key
+ * that it sees does, however small the key's weight.  (A z below -2^127 log 2 counts as -inf,
+ * one above 2^127 log 2 gives NaN.)
  *   q             device bf16 [B, T, heads, head_dim] with the given strides
  *   cache_len     device int32 [B]; outside [0, capacity]: clamped and flagged
  *   k_new, v_new  device bf16 [B, T, cache->heads, head_dim], the drafted nodes'

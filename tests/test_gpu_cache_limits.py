@@ -21,7 +21,7 @@ from gpu_common import handle  # noqa: F401
 from test_gpu_cache import make_cache, randn, write_rows
 
 pytestmark = pytest.mark.gpu
-INF = math.inf
+INF, NAN = math.inf, math.nan
 
 
 def lengths(lens):
@@ -100,6 +100,128 @@ def test_weights_on_few_keys(handle, n, T, heads, H, D, keys):
         write_rows(cache, b, 0, kk, vv)
     out, _ = api.tree_attention(handle, q.contiguous(), cache, lengths([n] * B))
     check(out, definition(q, rows, None, None, None, D ** -0.5))
+    assert handle.device_error() == 0
+
+
+# ---------------------------------------------------------------------------
+# infinities
+# ---------------------------------------------------------------------------
+SHAPES = [
+    # lens, capacity, T, heads, H, D, page
+    ([300], 300, 1, 8, 2, 128, 16),                 # a cluster per item, one row tile
+    ([900, 140], 900, 40, 16, 2, 64, 32),           # clusters, two row tiles
+    ([120] * 24, 128, 3, 16, 4, 64, 0),             # whole items
+    ([128, 100], 128, 40, 32, 4, 128, 0),           # whole items of three row tiles
+    ([3000, 2500, 700], 30000, 17, 16, 2, 128, 64), # runs, two row tiles
+    ([1000 - 30 * i for i in range(20)], 30000, 3, 24, 4, 128, 16),   # many items, cut into a few parts each
+    ([40000], 40000, 2, 8, 1, 64, 64),              # one head, many parts
+]
+
+
+@pytest.mark.parametrize("lens,cap,T,heads,H,D,page", SHAPES)
+@pytest.mark.parametrize("drafted", [False, True])
+def test_infinite_values_of_cached_keys(handle, lens, cap, T, heads, H, D, page, drafted):
+    gen = torch.Generator(device="cuda").manual_seed(len(lens) + T)
+    B = len(lens)
+    cache, rows = make_cache(gen, lens, H, D, page, cap)
+    q, kn, vn = randn(gen, B, T, heads, D), randn(gen, B, T, H, D), randn(gen, B, T, H, D)
+    if not drafted:
+        kn = vn = None
+    finite, _ = api.tree_attention(handle, q, cache, lengths(lens), kn, vn)
+    for b in range(B):
+        n, (kk, vv) = lens[b], rows[b]
+        vv[n // 2, :, 3] = INF
+        vv[5, :, 3] = INF
+        vv[n - 1, :, D - 1] = -INF
+        vv[70, 0, 20] = INF                       # +inf and -inf in one column: NaN
+        vv[n - 2, 0, 20] = -INF
+        vv[9, H - 1, 33] = NAN
+        write_rows(cache, b, 0, kk, vv)
+    out, _ = api.tree_attention(handle, q, cache, lengths(lens), kn, vn)
+    again, _ = api.tree_attention(handle, q, cache, lengths(lens), kn, vn)
+    assert torch.equal(out.view(torch.int16), again.view(torch.int16))
+    check(out, definition(q, rows, kn, vn, None, D ** -0.5))
+    assert torch.isposinf(out[..., 3]).all() and torch.isneginf(out[..., D - 1]).all()
+    assert torch.isfinite(finite).all() and handle.device_error() == 0
+
+
+@pytest.mark.parametrize("lens,cap,T,heads,H,D,page", SHAPES)
+def test_values_of_keys_at_minus_infinity_add_nothing(handle, lens, cap, T, heads, H, D, page):
+    # cached and drafted keys whose z is -inf hold infinities and NaN
+    gen = torch.Generator(device="cuda").manual_seed(len(lens) * 10 + T)
+    B = len(lens)
+    cache, rows = make_cache(gen, lens, H, D, page, cap)
+    q, kn, vn = randn(gen, B, T, heads, D), randn(gen, B, T, H, D), randn(gen, B, T, H, D)
+    q[..., 7] = q[..., 7].abs() + 0.5
+    for b in range(B):
+        n, (kk, vv) = lens[b], rows[b]
+        for j, x in ((3, INF), (n // 2, -INF), (n - 1, NAN)):
+            kk[j, :, 7] = -INF
+            vv[j] = x
+        write_rows(cache, b, 0, kk, vv)
+    kn[:, T // 2, :, 7] = -INF
+    vn[:, T // 2] = INF
+    out, _ = api.tree_attention(handle, q, cache, lengths(lens), kn, vn)
+    assert torch.isfinite(out).all()
+    check(out, definition(q, rows, kn, vn, None, D ** -0.5))
+    assert handle.device_error() == 0
+
+
+@pytest.mark.parametrize("lens,cap,T,heads,H,D,page", SHAPES)
+def test_an_infinity_far_below_the_maximum_arrives(handle, lens, cap, T, heads, H, D, page):
+    # its weight underflows in fp32 but is not 0; the parts of a cut item meet in both orders
+    gen = torch.Generator(device="cuda").manual_seed(len(lens) * 20 + T)
+    B = len(lens)
+    cache, rows = make_cache(gen, lens, H, D, page, cap)
+    q = randn(gen, B, T, heads, D).abs() + 0.25
+    for where in (0, -1):
+        for b in range(B):
+            n, (kk, vv) = lens[b], rows[b]
+            kk[0 if where else n - 1] = 16.0      # z of 200 and more
+            vv[where % n, :, 11] = -INF
+            write_rows(cache, b, 0, kk, vv)
+        out, _ = api.tree_attention(handle, q, cache, lengths(lens))
+        check(out, definition(q, rows, None, None, None, D ** -0.5))
+        assert torch.isneginf(out[..., 11]).all()
+        for b in range(B):
+            rows[b][0].copy_(randn(gen, *rows[b][0].shape))
+            rows[b][1].copy_(randn(gen, *rows[b][1].shape))
+    assert handle.device_error() == 0
+
+
+@pytest.mark.parametrize("lens,cap,T,heads,H,D,page", SHAPES)
+def test_values_near_the_largest(handle, lens, cap, T, heads, H, D, page):
+    # one key takes nearly all the weight; its value times what P may reach would pass the type's range
+    gen = torch.Generator(device="cuda").manual_seed(len(lens) * 30 + T)
+    B = len(lens)
+    cache, rows = make_cache(gen, lens, H, D, page, cap)
+    q = randn(gen, B, T, heads, D).abs() + 0.25
+    for b in range(B):
+        kk, vv = rows[b]
+        kk.mul_(0.01)
+        j = min(100, lens[b] - 1)
+        kk[j] = 4.6 / D ** 0.5 / q.float().mean().item()      # P of about 2^6.6 where the tile's start set the maximum
+        vv[j] = 3.0e38
+        vv[j, :, 1] = -3.0e38
+        write_rows(cache, b, 0, kk, vv)
+    out, _ = api.tree_attention(handle, q, cache, lengths(lens))
+    assert torch.isfinite(out).all()
+    check(out, definition(q, rows, None, None, None, D ** -0.5))
+    assert handle.device_error() == 0
+
+
+def test_rows_that_see_only_infinite_nodes_at_minus_infinity(handle):
+    # nothing is added: out = 0 and lse = -inf, beside rows that see more
+    gen = torch.Generator(device="cuda").manual_seed(2)
+    for T, lens in ((3, [0, 0]), (40, [0, 200])):
+        cache, rows = make_cache(gen, lens, 2, 64, 16, 208)
+        q, kn, vn = randn(gen, 2, T, 16, 64), randn(gen, 2, T, 2, 64), randn(gen, 2, T, 2, 64)
+        q[..., 7] = q[..., 7].abs() + 0.5
+        kn[:, 0, :, 7] = -INF
+        vn[:, 0] = INF
+        out, lse = api.tree_attention(handle, q, cache, lengths(lens), kn, vn)
+        assert (out[0, 0] == 0).all() and torch.isneginf(lse[0, 0]).all() and torch.isfinite(out).all()
+        check(out, definition(q, rows, kn, vn, None, 0.125))
     assert handle.device_error() == 0
 
 
