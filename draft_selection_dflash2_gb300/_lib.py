@@ -98,14 +98,19 @@ def load_bind():
     """The compiled half of the binding, calling the loaded library's entry points."""
     global _bind
     if _bind is None:
-        import torch  # noqa: F401  (the module's symbols come from torch's libraries)
+        import torch  # (the module's symbols come from torch's libraries)
         lib = load()
+        again = "build it (python -c 'import __graft_entry__ as g; g.build()')"
         if not os.path.exists(BIND_PATH):
-            raise RuntimeError(f"{BIND_PATH} is missing: build it first "
-                               "(python -c 'import __graft_entry__ as g; g.build()')")
-        spec = importlib.util.spec_from_file_location("_dflash2_bind", BIND_PATH)
-        mod = importlib.util.module_from_spec(spec)
-        spec.loader.exec_module(mod)
+            raise RuntimeError(f"{BIND_PATH} is missing: {again}")
+        try:
+            spec = importlib.util.spec_from_file_location("_dflash2_bind", BIND_PATH)
+            mod = importlib.util.module_from_spec(spec)
+            spec.loader.exec_module(mod)
+        except ImportError as e:
+            raise RuntimeError(f"{BIND_PATH} does not load with torch {torch.__version__}: {again}") from e
+        if mod.torch_version != torch.__version__:
+            raise RuntimeError(f"{BIND_PATH} was built for torch {mod.torch_version}, not {torch.__version__}: {again}")
         mod.init(*(ctypes.cast(getattr(lib, "dflash2_" + f), P).value
                    for f in ("tree_attention", "cache_commit", "cache_scores", "cache_evict")))
         _bind = mod

@@ -8,6 +8,7 @@ torch.bfloat16 or as int16/uint16 bit patterns.  Outputs that are not passed in
 are allocated with torch before the call (the library itself never allocates).
 """
 import ctypes
+from functools import cached_property
 
 import torch
 
@@ -72,7 +73,11 @@ class Handle:
         _check(self._lib.dflash2_create(device, ctypes.byref(h)), "dflash2_create")
         self._h = h
         self.raw = h.value
-        self._bind = _lib.load_bind()
+
+    @cached_property
+    def _bind(self):
+        """The compiled half of the binding, loaded by the handle's first cache operator: the others do without it."""
+        return _lib.load_bind()
 
     @property
     def ptr(self):

@@ -10,6 +10,7 @@ import concurrent.futures
 import glob
 import os
 import subprocess
+import warnings
 
 HERE = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(HERE)
@@ -42,21 +43,23 @@ def _stale(target, deps):
     return any(os.path.getmtime(d) > t for d in deps)
 
 
-def _build_bind(force: bool = False):
-    """The extension module that checks torch tensors and calls the C ABI (needs torch's and Python's headers)."""
+def build_bind(force: bool = False) -> str:
+    """The extension module that checks the cache operators' tensors and calls the C ABI (needs g++ and the headers of
+    torch and Python)."""
     import sysconfig
 
     import torch
     torch_dir = os.path.dirname(torch.__file__)
+    os.makedirs(BUILD, exist_ok=True)
     stamp = f"// torch {torch.__version__}, Python {sysconfig.get_python_version()}\n"
     stamp_file = os.path.join(BUILD, "bind.stamp")
     same = os.path.exists(stamp_file) and open(stamp_file).read() == stamp
     if not force and same and not _stale(BIND, [BIND_SRC, os.path.join(INCLUDE, "dflash2.h"), __file__]):
-        return
+        return BIND
     include = os.path.join(torch_dir, "include")
     tmp = BIND + f".tmp{os.getpid()}"
     cmd = [os.environ.get("CXX", "g++"), "-O2", "-std=c++17", "-fPIC", "-shared", "-fvisibility=hidden",
-           f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}", "-I", INCLUDE, "-isystem", include,
+           f'-DDFLASH2_TORCH="{torch.__version__}"', f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}", "-I", INCLUDE, "-isystem", include,
            "-isystem", os.path.join(include, "torch", "csrc", "api", "include"), "-isystem",
            sysconfig.get_paths()["include"], BIND_SRC, "-o", tmp, "-L", os.path.join(torch_dir, "lib"), "-ltorch_python",
            "-ltorch_cpu", "-lc10"]
@@ -66,13 +69,22 @@ def _build_bind(force: bool = False):
     os.replace(tmp, BIND)
     with open(stamp_file, "w") as f:
         f.write(stamp)
+    return BIND
+
+
+def _try_bind(force: bool = False):
+    try:
+        build_bind(force)
+    except (RuntimeError, OSError, ImportError) as e:
+        warnings.warn(f"the cache operators' binding was not built, everything else was: {e}")
 
 
 def build(force: bool = False, verbose: bool = False, extra_flags=()) -> str:
+    """Builds the library, which has to succeed, and the binding, without which only the cache operators are missing."""
     srcs, hdrs = _sources(), _headers()
     os.makedirs(BUILD, exist_ok=True)
     if not force and not _stale(LIB, srcs + hdrs + [__file__]):
-        _build_bind()
+        _try_bind()
         return LIB
 
     def compile_one(src):
@@ -87,7 +99,7 @@ def build(force: bool = False, verbose: bool = False, extra_flags=()) -> str:
         return obj
 
     with concurrent.futures.ThreadPoolExecutor(max_workers=min(8, len(srcs) + 1)) as ex:
-        bind = ex.submit(_build_bind, force)
+        bind = ex.submit(_try_bind, force)
         objs = list(ex.map(compile_one, srcs))
         bind.result()
     tmp = LIB + f".tmp{os.getpid()}"

@@ -3,7 +3,7 @@
 //
 // A cache operator's kernel takes a few microseconds for one sequence, and reading
 // its tensors' attributes from Python took about as long again (a commit call: 7.0
-// us through ctypes, 3.6 here).  Nothing but argument marshalling happens here.  The
+// us through ctypes, 2.8 here).  Nothing but argument marshalling happens here.  The
 // entry points' addresses come from the loaded libdflash2.so (init), so that this
 // module needs no link to it.
 #define PY_SSIZE_T_CLEAN
@@ -233,4 +233,12 @@ PyModuleDef module = {PyModuleDef_HEAD_INIT, "_dflash2_bind", nullptr, -1, metho
 
 }  // namespace
 
-PyMODINIT_FUNC PyInit__dflash2_bind() { return PyModule_Create(&module); }
+PyMODINIT_FUNC PyInit__dflash2_bind() {
+  PyObject* m = PyModule_Create(&module);
+  // the torch whose tensors it reads: another one's may be laid out otherwise
+  if (m != nullptr && PyModule_AddStringConstant(m, "torch_version", DFLASH2_TORCH) != 0) {
+    Py_DECREF(m);
+    return nullptr;
+  }
+  return m;
+}
