@@ -24,6 +24,7 @@ namespace {
 constexpr int kK = 16;
 constexpr int64_t kMaxL = 64;
 constexpr int64_t kMaxKvHeads = 4096;
+constexpr int64_t kMaxElements = int64_t(1) << 36;   // of 4 bytes: no memory holds more
 constexpr int64_t kMaxCapacity = (int64_t(1) << 31) - 256;
 
 bool aligned(const void* p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p) & (a - 1)) == 0; }
@@ -102,6 +103,12 @@ int view_cache(const dflash2_kv_cache* c, int64_t B, dflash2::KvView* out) {
   out->capacity = static_cast<int32_t>(capacity);
   out->heads = static_cast<int32_t>(c->heads);
   return DFLASH2_OK;
+}
+
+// Whether n 4-byte elements at p and m at q share memory (null shares none).
+bool overlap(const void* p, int64_t n, const void* q, int64_t m) {
+  const auto a = reinterpret_cast<uintptr_t>(p), b = reinterpret_cast<uintptr_t>(q);
+  return p != nullptr && q != nullptr && a < b + 4 * static_cast<uintptr_t>(m) && b < a + 4 * static_cast<uintptr_t>(n);
 }
 
 // Strides of a [B, T, n, d] bf16 operand.
@@ -527,7 +534,9 @@ int dflash2_cache_commit(dflash2_handle* h, const uint16_t* k_new, const uint16_
   dflash2::CommitArgs a;
   if (const int st = view_cache(cache, B, &a.cache)) return st;
   if (B == 0) return DFLASH2_OK;
-  if (!cache_len || !new_len || cache_len == new_len || (T > 0 && (!k_new || !v_new))) return DFLASH2_ERR_INVALID_ARG;
+  if (!cache_len || !new_len || (T > 0 && (!k_new || !v_new))) return DFLASH2_ERR_INVALID_ARG;
+  // one CTA of a sequence writes its new length while others may still read these
+  if (overlap(new_len, B, cache_len, B) || overlap(new_len, B, count, B)) return DFLASH2_ERR_INVALID_ARG;
   RowStrides ns = {new_batch_stride, new_token_stride, new_head_stride};
   if (const int st = check_rows(&ns, B, T, cache->heads, cache->head_dim)) return st;
   if (!aligned(k_new, 16) || !aligned(v_new, 16) || !aligned(cache_len, 4) || !aligned(count, 4) ||
@@ -601,8 +610,9 @@ int dflash2_cache_evict(dflash2_handle* h, const float* scores, int64_t scores_l
       B * cache->heads * (keep / 16 + 1) >= (int64_t(1) << 31))
     return DFLASH2_ERR_UNSUPPORTED;
   if (B == 0) return DFLASH2_OK;
-  if (keep > a.dst.capacity || !scores || !cache_len || !kept || !new_len || new_len == cache_len ||
-      dst_scores == scores)
+  if (keep > a.dst.capacity || !scores || !cache_len || !kept || !new_len || overlap(new_len, B, cache_len, B) ||
+      overlap(dst_scores, B * cache->heads * dflash2::imin64(dst_ld, kMaxElements), scores,
+              B * cache->heads * dflash2::imin64(scores_ld, kMaxElements)))
     return DFLASH2_ERR_INVALID_ARG;
   if (!aligned(scores, 4) || !aligned(cache_len, 4) || !aligned(kept, 4) || !aligned(new_len, 4) ||
       !aligned(dst_scores, 4))

@@ -498,7 +498,7 @@ int dflash2_tree_attention(dflash2_handle* h, const uint16_t* q, int64_t q_batch
  *   path          device int32 [B, T] node ids, or NULL: node i is i
  *   scores        device fp32 [B, cache->heads, scores_ld] or NULL: the appended
  *                 positions' entries are set to 0
- *   new_len       device int32 [B]: cache_len + count; must not overlap cache_len
+ *   new_len       device int32 [B]: cache_len + count; must overlap neither
  * Positions past the capacity (or scores_ld, when scores is given) are dropped,
  * new_len stops there, and DFLASH2_DEVERR_BAD_LENGTH is flagged.  Two sequences
  * must not append to the same page.
@@ -537,7 +537,7 @@ int dflash2_cache_scores(dflash2_handle* h, const uint16_t* q, int64_t q_batch_s
  *               share, and which the call only reads)
  *   kept        device int32 [B, heads, keep]: the kept positions, ascending,
  *               then -1
- *   new_len     device int32 [B]: min(cache_len, keep)
+ *   new_len     device int32 [B]: min(cache_len, keep); must not overlap cache_len
  *   dst_scores  device fp32 [B, heads, dst_ld], dst_ld >= keep, or NULL: the
  *               kept positions' scores; must not overlap scores
  * 1 <= keep, 0 <= recent <= keep; B * heads < 2^24; B * heads * (keep / 16 + 1) <

@@ -297,3 +297,36 @@ def test_scores_of_many_short_heads(handle, B, n, T, heads, H, D):
         assert ((first[b, :, :lens[b]].double() - w).abs() <= (dz + 2.0 ** -20) * w + 2.0 ** -22 * w).all()
         assert (first[b, :, lens[b]:] == 0).all()
     assert handle.device_error() == 0
+
+
+# ---------------------------------------------------------------------------
+# buffers that may not be shared
+# ---------------------------------------------------------------------------
+def test_outputs_that_overlap_inputs_are_refused(handle):
+    # a CTA would read what another one of the same sequence has written
+    gen = torch.Generator(device="cuda").manual_seed(1)
+    cache, _ = make_cache(gen, [8, 8], 2, 64, 16, 32)
+    dst, _ = make_cache(gen, [0, 0], 2, 64, 16, 16)
+    kn, vn = randn(gen, 2, 4, 2, 64), randn(gen, 2, 4, 2, 64)
+    ints = torch.tensor([8, 8, 3, 3, 0, 0], dtype=torch.int32, device="cuda")
+    floats = torch.zeros(2 * 2 * 32 + 2 * 2 * 16, device="cuda")
+    scores = floats[:128].view(2, 2, 32)
+    before = cache.k.clone()
+
+    def refused(fn):
+        with pytest.raises(api.Dflash2Error) as e:
+            fn()
+        assert e.value.status == -1
+
+    commit = lambda new: api.cache_commit(handle, kn, vn, cache, ints[:2], ints[2:4], new_len=new)  # noqa: E731
+    evict = lambda new, ds: api.cache_evict(handle, scores, cache, ints[:2], dst, 4, 1, new_len=new, dst_scores=ds)  # noqa: E731
+    for new in (ints[:2], ints[1:3], ints[2:4], ints[3:5]):
+        refused(lambda: commit(new))
+    refused(lambda: evict(ints[1:3], None))
+    refused(lambda: evict(ints[4:], floats[64:128].view(2, 2, 16)))
+    refused(lambda: evict(ints[4:], floats[127:191].view(2, 2, 16)))
+    torch.cuda.synchronize()
+    assert torch.equal(cache.k.view(torch.int16), before.view(torch.int16)) and ints.tolist() == [8, 8, 3, 3, 0, 0]
+    assert commit(ints[4:]).tolist() == [11, 11]
+    assert evict(ints[4:], floats[128:].view(2, 2, 16))[1].tolist() == [4, 4]
+    assert handle.device_error() == 0
