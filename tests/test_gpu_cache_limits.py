@@ -45,6 +45,8 @@ def definition(q, rows, k_new, v_new, sees, scale):
                 kk, vv = torch.cat([kk, k_new[b, :, h].double()]), torch.cat([vv, v_new[b, :, h].double()])
                 s = torch.ones(T, T, dtype=torch.bool, device="cuda").tril() if sees is None else sees[b]
                 vis = torch.cat([vis, s.repeat_interleave(G, 0)], 1)
+            if kk.shape[0] == 0:
+                continue
             most = max(most, kk.shape[0])
             z = qq @ kk.T * scale
             adds = vis & (z != -INF)
@@ -249,11 +251,13 @@ def test_scores_of_infinite_keys(handle, T, heads, H, D):
         scores = start.clone()
         api.cache_scores(handle, q, lse, cache, lengths([n]), scores)
         for h in range(H):
-            qq, ll = q[0, :, h * G:(h + 1) * G].double().reshape(-1, D), lse[0, :, h * G:(h + 1) * G].double().reshape(-1, 1)
+            qq = q[0, :, h * G:(h + 1) * G].double().reshape(-1, D)
+            ll = lse[0, :, h * G:(h + 1) * G].double().reshape(-1, 1)
             z = qq @ kk[:, h].double().T * D ** -0.5
             w = torch.where(torch.isinf(ll), 0.0, torch.exp(z - ll)).sum(0)
             assert (w[dead] == 0).all()
-            zabs = torch.where(torch.isinf(z), 0.0, qq.abs() @ kk[:, h].double().abs().nan_to_num(0.0, 0.0, 0.0).T * D ** -0.5)
+            kabs = kk[:, h].double().abs().nan_to_num(0.0, 0.0, 0.0)
+            zabs = torch.where(torch.isinf(z), 0.0, qq.abs() @ kabs.T * D ** -0.5)
             dz, was = D * 2.0 ** -23 * zabs.amax(), start[0, h].double()
             err = (scores[0, h].double() - was - w).abs()
             assert (err <= (dz + 2.0 ** -20) * w + 2.0 ** -22 * (w + was)).all(), err.max()
@@ -274,7 +278,8 @@ def test_scores_of_what_attention_found_empty(handle, T, heads):
     assert (scores == 2.0).all() and handle.device_error() == 0
 
 
-@pytest.mark.parametrize("B,n,T,heads,H,D", [(40, 128, 1, 32, 16, 128), (60, 100, 17, 32, 16, 64), (33, 129, 3, 60, 20, 128)])
+@pytest.mark.parametrize("B,n,T,heads,H,D", [(40, 128, 1, 32, 16, 128), (60, 100, 17, 32, 16, 64),
+                                             (33, 129, 3, 60, 20, 128)])
 def test_scores_of_many_short_heads(handle, B, n, T, heads, H, D):
     # runs of several (sequence, head) of one tile each: an issuer of products is idle in every other one
     gen = torch.Generator(device="cuda").manual_seed(B)
@@ -318,8 +323,12 @@ def test_outputs_that_overlap_inputs_are_refused(handle):
             fn()
         assert e.value.status == -1
 
-    commit = lambda new: api.cache_commit(handle, kn, vn, cache, ints[:2], ints[2:4], new_len=new)  # noqa: E731
-    evict = lambda new, ds: api.cache_evict(handle, scores, cache, ints[:2], dst, 4, 1, new_len=new, dst_scores=ds)  # noqa: E731
+    def commit(new):
+        return api.cache_commit(handle, kn, vn, cache, ints[:2], ints[2:4], new_len=new)
+
+    def evict(new, ds):
+        return api.cache_evict(handle, scores, cache, ints[:2], dst, 4, 1, new_len=new, dst_scores=ds)
+
     for new in (ints[:2], ints[1:3], ints[2:4], ints[3:5]):
         refused(lambda: commit(new))
     refused(lambda: evict(ints[1:3], None))
@@ -329,4 +338,28 @@ def test_outputs_that_overlap_inputs_are_refused(handle):
     assert torch.equal(cache.k.view(torch.int16), before.view(torch.int16)) and ints.tolist() == [8, 8, 3, 3, 0, 0]
     assert commit(ints[4:]).tolist() == [11, 11]
     assert evict(ints[4:], floats[128:].view(2, 2, 16))[1].tolist() == [4, 4]
+    assert handle.device_error() == 0
+
+
+@pytest.mark.parametrize("lens,T,heads,H,D", [([500], 1, 8, 2, 128), ([100, 0, 17], 40, 32, 4, 64)])
+def test_a_capacity_far_above_the_lengths(handle, lens, T, heads, H, D):
+    # how a call is cut goes by the capacity: clusters and whole items for a tight one, runs for a table of 65536 positions
+    gen = torch.Generator(device="cuda").manual_seed(T)
+    B = len(lens)
+    tight, rows = make_cache(gen, lens, H, D, 64, max(lens))
+    table = torch.full((B, 1024), -1, dtype=torch.int32, device="cuda")     # entries past a length are not looked at
+    table[:, :tight.block_table.shape[1]] = tight.block_table
+    q, kn, vn = randn(gen, B, T, heads, D), randn(gen, B, T, H, D), randn(gen, B, T, H, D)
+    want = definition(q, rows, kn, vn, None, D ** -0.5)
+    for cache in (tight, api.KVCache(tight.k, tight.v, table)):
+        out, lse = api.tree_attention(handle, q, cache, lengths(lens), kn, vn)
+        check(out, want)
+        scores = torch.zeros(B, H, 512, device="cuda")
+        api.cache_scores(handle, q, lse, cache, lengths(lens), scores)
+        # a row's weights on the cache and on the block's own nodes are 1 together
+        total = scores.sum((1, 2)).double()
+        for b in range(B):
+            z = torch.einsum("thgd,jhd->thgj", q[b].double().reshape(T, H, -1, D), rows[b][0].double()) * D ** -0.5
+            w = torch.exp(z - lse[b].double().reshape(T, H, -1, 1)).sum()
+            assert (total[b] - w).abs() <= 1e-4 * w
     assert handle.device_error() == 0
