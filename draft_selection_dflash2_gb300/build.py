@@ -59,7 +59,8 @@ def build_bind(force: bool = False) -> str:
     include = os.path.join(torch_dir, "include")
     tmp = BIND + f".tmp{os.getpid()}"
     cmd = [os.environ.get("CXX", "g++"), "-O2", "-std=c++17", "-fPIC", "-shared", "-fvisibility=hidden",
-           f'-DDFLASH2_TORCH="{torch.__version__}"', f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}", "-I", INCLUDE, "-isystem", include,
+           f'-DDFLASH2_TORCH="{torch.__version__}"',
+           f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}", "-I", INCLUDE, "-isystem", include,
            "-isystem", os.path.join(include, "torch", "csrc", "api", "include"), "-isystem",
            sysconfig.get_paths()["include"], BIND_SRC, "-o", tmp, "-L", os.path.join(torch_dir, "lib"), "-ltorch_python",
            "-ltorch_cpu", "-lc10"]

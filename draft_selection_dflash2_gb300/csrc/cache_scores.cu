@@ -19,12 +19,13 @@
 //               exponentials (with one buffer of 256: 1724 cycles a unit at 136 rows).
 // Bound by memory while a unit's products and exponentials hide under its keys (up
 // to about 128 rows): 16 blocks of 17 nodes, 1 to 17 of them accepted, in groups of 8
-// over 8 kv heads and ragged lengths up to 32768: 110 us for 625 MB, 5.7 TB/s (85% of
+// over 8 kv heads and ragged lengths up to 32768: 109 us for 625 MB, 5.7 TB/s (86% of
 // a copy's rate; 118 us with runs equal in units, and 124 when a thread also waited for
 // each piece of the query rows before it asked for the next).  With one node accepted
 // everywhere a batch that takes 83 us takes 97 with all 17 accepted: the change from one
 // head's rows to the next's drains the products, once or twice a run.  One block over
-// 4000 positions: 4.5 us, the latency of the first tiles.
+// 4000 positions: 4.6 us in a replayed graph, 5.2 to 5.7 a call, the latency of the first
+// tiles.
 // When a run enters another (sequence, head) the epilogue warps lay that head's
 // query rows out in shared memory (up to 512 rows; more rows take one launch per
 // 512) and their lse beside them.  Rows that add nothing (their lse is -inf, and those
@@ -467,7 +468,7 @@ cudaError_t launch(const ScoresArgs& a, int num_sms, cudaStream_t stream) {
 cudaError_t launch_cache_scores(const ScoresArgs& a, int64_t head_dim, int num_sms, cudaStream_t stream) {
   const int64_t most = most_units(a);
   // In short runs a weight only breaks the runs' ends away from the heads' (one block over 4000 positions: 6.4 us
-  // against 4.5), and the weights' sum has to fit.
+  // against 4.6), and the weights' sum has to fit.
   const bool weighted = a.B > 1 && most >= 8 * num_sms && most * kMostWeight < (int64_t(1) << 31);
   if (head_dim == 64) return weighted ? launch<64, true>(a, num_sms, stream) : launch<64, false>(a, num_sms, stream);
   return weighted ? launch<128, true>(a, num_sms, stream) : launch<128, false>(a, num_sms, stream);

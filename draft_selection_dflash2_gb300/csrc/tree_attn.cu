@@ -35,10 +35,10 @@
 //               more than 2^8 since m was set (P then stays below 2^8, exact in
 //               scale), so most chunks never touch O outside the tensor cores.
 // P needs both terms: rounded to bf16 alone each weight is off by up to 2^-8, as much
-// as the output's own rounding, and nothing averages that out where the weights gather on a
-// few keys or many keys are alike (a P of 2^5.3 a thousand times is off the same way a
-// thousand times). With the second term it is 2^-16, and the output is the fp32 sum's
-// rounded once. That costs the tensor cores half as much again.
+// as the output's own rounding, and nothing averages that out where the weights gather on
+// a few keys or many keys are alike (a P of 2^5.3 is off the same way each time).  With
+// the second term it is 2^-16, and the output is the fp32 sum's rounded once.  It costs the
+// tensor cores half as much again: 8 trees of 64 nodes 270 us against 208 with one term.
 // The two pipelines alternate on the tensor cores: one's softmax runs under the
 // other's products.  With two row tiles in the item each pipeline takes one of
 // them over every unit; with one row tile the pipelines take alternate units of
@@ -46,29 +46,30 @@
 //
 // A value no row sees must not reach the sums even as 0 * NaN: cached V rows past
 // the length are zeroed in shared memory, and so are a drafted node's non-finite values,
-// which only some rows may see.  Nor may a key that a row does see reach it as 0 * inf
-// (z = -inf, or P's second term) or inf - inf (both terms), and a
-// finite value times a P of 2^8 may not become infinite.  So where a row's O is not finite
-// at the end, or the row sees a drafted node that was zeroed, the CTA takes the row's sums
-// again at the end of its run, key by key (sum_again): a key with z = -inf is passed over,
-// an infinite or NaN value of another one is added as it is, and m is the maximum so far.
-// That costs the usual call one operation per element of O.
+// which only some rows may see.  A key that a row does see must not reach it as 0 * inf
+// (z = -inf, or P's second term) or inf - inf (the two terms), and a finite value times a
+// P of 2^8 must not become infinite.  So where a row's O is not finite at the end, or the
+// row sees a drafted node that was zeroed, its sums are taken again when the run is done,
+// key by key (sum_again): a key with z = -inf is passed over, an infinite or NaN value of
+// another one is added as it is, and m is the maximum so far.  The usual call pays one
+// operation per two elements of O, which does not show in its time.
 //
 // What bounds it, and what it measured (GB300, heads in groups of 8 over 8 kv heads,
-// D = 128 unless said otherwise):
+// D = 128 unless said otherwise; replays of a graph, calls through the binding take up to
+// 10% longer where the clocks drop under load):
 //   memory   up to about 128 query rows per kv head: 2 sequences of 131072
-//            positions, one token each, 162 us = 6.6 TB/s (99% of a copy's rate).
-//   tensor cores beyond: 8 trees of 64 nodes over 16384 positions, 208 us = 1.32
-//            PFLOP/s; the tensor pipe is active 59% of the time and another 20% is
-//            waiting for S's operands (64-key products read 6 KB of shared memory
-//            per 32 cycles of products, at 128 B a cycle).  64 keys and not 128
-//            because two S buffers of 128 per pipeline and the O accumulators do not
-//            fit 512 columns, and with one buffer the softmax and the products of a
-//            pipeline wait for one another (337 us against 242 then).
-//   latency  in small calls: one token over 500 positions takes 8 us (10.8 with runs
-//            and a join: 1.6 until the run is known, 2 until the first S, 1.2 for the
-//            units' softmax and products, 1.5 for writing parts and 3 for the join).
-//   64 blocks of 17 over ragged lengths up to 12000, 136 rows per kv head: 342 us
+//            positions, one token each, 167 us = 6.4 TB/s (96% of a copy's rate).
+//   tensor cores beyond: 8 trees of 64 nodes over 16384 positions, 270 us = 1.02
+//            PFLOP/s of the definition's products, 1.53 with P's second term; the tensor
+//            pipe is active 66% of the time, and much of the rest is waiting for S's operands
+//            (64-key products read 6 KB of shared memory per 32 cycles of products, at
+//            128 B a cycle).  64 keys and not 128 because two S buffers of 128 per
+//            pipeline and the O accumulators do not fit 512 columns, and with one buffer the
+//            softmax and the products of a pipeline wait for one another (with one term 337 us
+//            against 242).
+//   latency  in small calls: one token over 500 positions, groups of 4, takes 8.5 us (11.5
+//            with runs and a join, of which the join and the writing of parts are 4).
+//   64 blocks of 17 over ragged lengths up to 12000, 136 rows per kv head: 420 us
 //   against 271 for its bytes; the second row tile holds 8 rows but takes the tensor
 //   cores as long as a full one.
 // Splitting every item in equal runs, rather than by whole items, is what ragged
@@ -1083,15 +1084,14 @@ __global__ void __launch_bounds__(kJoinThreads, 2) tree_attn_join_kernel(const _
   }
 }
 
-// A unit with one row tile takes about kSingle / 16 of the time of one with two (8, 9 and 11
-// balanced the runs of 3 row tiles less well).
+// A unit with one row tile takes about kSingle / 16 of the time of one with two (48 nodes, 3 row tiles, over
+// 16384 and over 700 positions: 233 and 135 us; with 9 228 and 144, with 11 238 and 138).
 constexpr int kSingle = 10;
 
 // Measured against runs that hold all pairs' units (8 sequences of 16384, 8 heads of 128 in groups of
-// 8): 64 nodes, 4 row tiles, 208 us against 217 (the second pair finds the keys in L2); 48 nodes, 3 row
-// tiles, 185 against 210 (the runs of the full pair took the longest); 65 nodes, 5 row tiles, 275
-// against 300.  64 short sequences of 48 nodes, whose runs hold many items, are the exception: 120
-// against 117.
+// 8): 64 nodes, 4 row tiles, 270 us against 279 (the second pair finds the keys in L2); 48 nodes, 3 row
+// tiles, 233 against 269 (the runs of the full pair took the longest); 65 nodes, 5 row tiles, 353
+// against 390; 64 short sequences of 48 nodes, whose runs hold many items, 132 to 138 against 136 to 139.
 Lanes deal_lanes(int32_t row_tiles, int32_t runs) {
   if (row_tiles <= 2) return {1, runs};
   Lanes l = {row_tiles / 2, 0};
@@ -1132,10 +1132,10 @@ int clusters_at_once(int k, size_t smem) {
 }
 
 // Size of the clusters that take an item each, or 0: equal runs and a join.  A team needs no
-// second kernel, which saves about 5 us, but its CTAs may have more units each than a run would;
-// a unit takes 0.9 us with one row tile and 1.5 with two.  Measured, runs against teams (8 heads of
-// 128 in groups of 4): 1 x 1 over 500 positions 10.8 and 8.0 us, 1 x 17 over 2000 13.0 and 10.4,
-// over 8191 17.1 and 16.5, over 16384 20.1 and 23.6, 4 x 17 over 2000 22.0 and 14.0.
+// second kernel, which saves 3 to 8 us, but its CTAs may have more units each than a run would; a
+// unit takes 1.1 us with one row tile, and more with two.  Measured, runs against teams (8 heads of
+// 128 in groups of 4): 1 x 1 over 500 positions 11.5 and 8.5 us, 1 x 17 over 2000 14.0 and 11.5,
+// over 8191 18.7 and 18.6, over 16384 22.1 and 29.4, 4 x 17 over 2000 23.6 and 15.5.
 template <int D>
 int team_size(int64_t items, int64_t units, bool two_tiles, int num_sms, size_t smem) {
   const int64_t run = (items * units + num_sms - 1) / num_sms;
@@ -1176,7 +1176,7 @@ cudaError_t launch(const AttnArgs& a, void* workspace, int num_sms, cudaStream_t
   const int64_t most = tree_attn_units(a.B, a.T, a.group, c.heads, c.capacity);
   if (most >= (int64_t(1) << 31)) return cudaErrorInvalidConfiguration;   // the entry point has refused it
   // Items of at most one unit per pipeline are left whole: nothing is gained by cutting them, and nothing has to
-  // be joined.  (1 x 1 over 500 positions, 5 units: 14.9 us whole, 12.3 in runs then, 8 in teams now.)
+  // be joined.  (1 x 1 over 500 positions, 5 units, before there were teams: 14.9 us whole, 12.3 in runs.)
   p.whole = (static_cast<int64_t>(c.capacity) + kTile - 1) / kTile + (a.k_new != nullptr) <= kWholeUnits;
   int runs = static_cast<int>(imin64(imin64(num_sms, kMaxRuns), imax64(most, 1)));
   p.lanes = deal_lanes(t.row_tiles, runs);

@@ -519,6 +519,8 @@ int dflash2_cache_commit(dflash2_handle* h, const uint16_t* k_new, const uint16_
  *   scores  device fp32 [B, cache->heads, scores_ld]; entries at j >=
  *           cache_len[b] are left alone.  A length past scores_ld is clamped and
  *           flagged.
+ * Only cached positions receive weight: what the block's nodes gave to one another (and
+ * to themselves) before the commit is not added, and appended positions start at 0.
  * Sums are fp32 in a fixed order.
  */
 int dflash2_cache_scores(dflash2_handle* h, const uint16_t* q, int64_t q_batch_stride, int64_t q_token_stride,
