@@ -20,6 +20,7 @@ U64 = ctypes.c_uint64
 I32 = ctypes.c_int
 U32P = ctypes.POINTER(ctypes.c_uint32)
 F32 = ctypes.c_float
+F64 = ctypes.c_double
 SZ = ctypes.c_size_t
 
 # name -> (restype, argtypes); mirrors include/dflash2.h
@@ -54,6 +55,13 @@ SIGNATURES = {
     "dflash2_cache_commit": (I32, [P, P, P, I64, I64, I64, P, P, P, P, I64, I64, P, I64, P, P]),
     "dflash2_cache_scores": (I32, [P, P, I64, I64, I64, P, P, P, P, P, I64, I64, I64, F32, P, I64, P]),
     "dflash2_cache_evict": (I32, [P, P, I64, P, P, P, I64, I64, I64, P, P, P, I64, P]),
+    "dflash2_rope_turns": (I32, [I64, F64, P, P, P]),
+    "dflash2_rope": (I32, [P, P, P, I64, I64, I64, P, I64, I64, I64, P, P, I64, I64, I64, I64, I32, P]),
+    "dflash2_cache_append": (I32, [P, P, P, I64, I64, I64, P, P, P, P, P, I64, I64, P, I64, I64, I64, P, I64, I64, I64,
+                                   I64, P, I64, P, P]),
+    "dflash2_logits_adjust": (I32, [P, P, I64, I64, I64, I64, I64, P, I64, P, P, P, P, P, P, I64, P, I64, I64, P, I64,
+                                    I64, P]),
+    "dflash2_token_counts": (I32, [P, P, P, P, I64, I64, I64, I32, P, I64, P]),
     "dflash2_selftest_wait_timeout": (I32, [P, U64, P, P]),
 }
 
@@ -63,6 +71,17 @@ class KvCacheStruct(ctypes.Structure):
     _fields_ = [("k", P), ("v", P), ("num_pages", I64), ("page_size", I64), ("heads", I64), ("head_dim", I64),
                 ("page_stride", I64), ("token_stride", I64), ("head_stride", I64), ("block_table", P),
                 ("max_pages", I64), ("table_ld", I64)]
+
+
+class RopeTableStruct(ctypes.Structure):
+    """dflash2_rope_table."""
+    _fields_ = [("turns", P), ("rotary_dim", I64), ("interleaved", ctypes.c_int32), ("factor", F32)]
+
+
+class RopeScalingStruct(ctypes.Structure):
+    """dflash2_rope_scaling."""
+    _fields_ = [("kind", ctypes.c_int32), ("factor", F64), ("original", F64), ("fast", F64), ("slow", F64), ("low", F64),
+                ("high", F64)]
 
 
 _lib = None
@@ -112,6 +131,7 @@ def load_bind():
         if mod.torch_version != torch.__version__:
             raise RuntimeError(f"{BIND_PATH} was built for torch {mod.torch_version}, not {torch.__version__}: {again}")
         mod.init(*(ctypes.cast(getattr(lib, "dflash2_" + f), P).value
-                   for f in ("tree_attention", "cache_commit", "cache_scores", "cache_evict")))
+                   for f in ("tree_attention", "cache_commit", "cache_scores", "cache_evict", "rope", "cache_append",
+                             "logits_adjust", "token_counts")))
         _bind = mod
     return _bind

@@ -472,6 +472,109 @@ def cache_evict(h: Handle, scores, cache: KVCache, cache_len, dst: KVCache, keep
     return kept, new_len, dst_scores
 
 
+class Rope:
+    """Rotary positions of one model: rates per pair, layout, and the factor of cos and sin.
+
+    rotary_dim: rotated elements of a head, from its first one on.  interleaved: pairs are neighbours, not half the
+    rotated part apart.  scaling, for longer contexts than trained on: None, or a dict with "kind" and its numbers:
+    "linear" and "ntk": factor; "yarn": factor, original, fast (32), slow (1); "wavelength": factor, original, low, high
+    (the formulas stand at dflash2_rope_scaling in include/dflash2.h)."""
+
+    KINDS = {"linear": 1, "ntk": 2, "yarn": 3, "wavelength": 4}
+
+    def __init__(self, rotary_dim, theta=10000.0, interleaved=False, scaling=None, device=None):
+        s = _lib.RopeScalingStruct()
+        if scaling is not None:
+            given = dict(scaling)
+            kind = given.pop("kind", None)
+            _need(kind in self.KINDS, f"scaling: kind is one of {', '.join(self.KINDS)}")
+            s.kind = self.KINDS[kind]
+            if kind == "yarn":
+                s.fast, s.slow = 32.0, 1.0
+            takes = {"yarn": ("factor", "original", "fast", "slow"), "wavelength": ("factor", "original", "low", "high")}
+            for name, value in given.items():
+                _need(name in takes.get(kind, ("factor",)), f"scaling: {kind} takes no {name}")
+                setattr(s, name, float(value))
+        _need(0 < rotary_dim <= 512, "rotary_dim: 2 .. 512")
+        turns = torch.empty(max(rotary_dim // 2, 1), dtype=torch.int64)
+        factor = ctypes.c_float()
+        _check(_lib.load().dflash2_rope_turns(rotary_dim, float(theta), ctypes.byref(s), ctypes.c_void_p(turns.data_ptr()),
+                                              ctypes.byref(factor)), "dflash2_rope_turns")
+        self.rotary_dim, self.interleaved, self.factor = rotary_dim, bool(interleaved), factor.value
+        self.turns = turns.to(torch.device("cuda", torch.cuda.current_device()) if device is None else device)
+        r = self.struct = _lib.RopeTableStruct()
+        r.turns, r.rotary_dim, r.interleaved, r.factor = self.turns.data_ptr(), rotary_dim, self.interleaved, self.factor
+        self.addr = ctypes.addressof(r)
+        self.device = self.turns.device.index
+
+
+def rope(h: Handle, x, rope: Rope, base=None, depth=None, inverse: bool = False, out=None, stream=None):
+    """x [B, T, heads, dim] rotated by its positions base[b] + depth[b, t] -> out, bf16 of the same shape.
+
+    base int32 [B] (None: 0), depth int32 [B, T] (None: t; a tree's nodes have their depths).  out may be x.
+    inverse: by the negated angles, which is the gradient (and undoes the rotation, but for the scaling's factor)."""
+    _need(rope.device == h.device, "rope: expected one on the handle's device")
+    if out is None:
+        out = _new_on(stream, x.shape, torch.bfloat16, x.device)
+    status = h._bind.rope(h.raw, h.device, rope.addr, x, out, base, depth, inverse, _raw_stream(h, stream))
+    if status:
+        _check(status, "dflash2_rope")
+    return out
+
+
+def cache_append(h: Handle, k_new, v_new, cache: KVCache, cache_len, rope: Rope = None, count=None, position=None, q=None,
+                 q_out=None, scores=None, new_len=None, stream=None):
+    """Appends new tokens' keys (rotated by `rope`) and values to the cache -> (new_len int32 [B], q_out or None).
+
+    k_new, v_new [B, T, kv_heads, dim]; count int32 [B] tokens of each sequence (None: T); position int32 [B] of its first
+    one (None: cache_len); q [B, T, heads, dim]: the tokens' queries, rotated to q_out, which may be q (rows past count are
+    left alone; zeros where q_out is allocated here); scores as in cache_commit."""
+    _need(rope is None or rope.device == h.device, "rope: expected one on the handle's device")
+    if new_len is None:
+        new_len = _new_on(stream, (k_new.shape[0],), torch.int32, k_new.device)
+    if q is not None and q_out is None:
+        q_out = _new_on(stream, q.shape, torch.bfloat16, q.device)
+        if count is not None:
+            with torch.cuda.stream(stream):
+                q_out.zero_()
+    status = h._bind.cache_append(h.raw, h.device, cache.addr, cache.batch, k_new, v_new, cache_len,
+                                  0 if rope is None else rope.addr, count, position, q, q_out, scores, new_len,
+                                  _raw_stream(h, stream))
+    if status:
+        _check(status, "dflash2_cache_append")
+    return new_len, q_out
+
+
+def logits_adjust(h: Handle, logits, counts=None, tokens=None, tree_mask=None, repetition=None, frequency=None,
+                  presence=None, bias=None, allowed=None, out=None, stream=None):
+    """The target's logits [B, T, V] after a request's penalties, biases and allowed tokens -> out, bf16 [B, T, V].
+
+    counts int32 [B, V] as token_counts keeps them; tokens int32 [B, T], the nodes' own, of which a node counts those it
+    sees (tree_mask as in tree_attention; None: a chain); repetition, frequency, presence fp32 [B]; bias fp32 [B, V] or
+    [1, V]; allowed int32 [B or 1, T or 1, (V + 31) // 32], a bit per token.  Rows of logits, out, counts and bias lie a
+    multiple of 8 elements apart, which an odd V gets as a slice of a wider tensor.  out may be logits."""
+    if out is None:
+        _need(logits.dim() == 3, "logits: [B, T, V]")
+        B, T, V = logits.shape
+        out = _new_on(stream, (B, T, (V + 7) // 8 * 8), torch.bfloat16, logits.device)[..., :V]
+    status = h._bind.logits_adjust(h.raw, h.device, logits, counts, tokens, tree_mask, repetition, frequency, presence,
+                                   bias, allowed, out, _raw_stream(h, stream))
+    if status:
+        _check(status, "dflash2_logits_adjust")
+    return out
+
+
+def token_counts(h: Handle, tokens, counts, count=None, path=None, prompt: bool = False, stream=None):
+    """Adds tokens int32 [B, N] to counts int32 [B, V] -> counts: bits 0-30 how often each was emitted, or, with prompt,
+    bit 31 (the sign): it occurs in the prompt.
+
+    count int32 [B] (None: N) and path int32 [B, N] (None: 0, 1, ...) choose tokens as in cache_commit."""
+    status = h._bind.token_counts(h.raw, h.device, tokens, counts, count, path, prompt, _raw_stream(h, stream))
+    if status:
+        _check(status, "dflash2_token_counts")
+    return counts
+
+
 def selftest_wait_timeout(h: Handle, limit_ns: int, words=None, stream=None):
     """Runs the library's bounded-wait self-test: one kernel whose two waits
     cannot be satisfied gives up after limit_ns each.  Returns the result word

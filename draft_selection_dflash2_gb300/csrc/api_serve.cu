@@ -1,0 +1,250 @@
+// api_serve.cu -- the C ABI's entry points for rotary positions, the append, logit
+// adjustment and token counts: host-side argument validation and dispatch.
+#include <cmath>
+
+#include "host_checks.h"
+#include "serve.h"
+
+namespace {
+
+constexpr int64_t kGrid = int64_t(1) << 31;
+
+// Bytes that a [B, T, n, d] operand of 16-bit elements spans.
+int64_t span_bytes(const RowStrides& s, int64_t B, int64_t T, int64_t n, int64_t d) {
+  return 2 * ((B - 1) * s.b + (T - 1) * s.t + (n - 1) * s.h + d);
+}
+
+bool ranges_meet(const void* p, int64_t n, const void* q, int64_t m) {
+  const auto a = reinterpret_cast<uintptr_t>(p), b = reinterpret_cast<uintptr_t>(q);
+  return p != nullptr && q != nullptr && a < b + static_cast<uintptr_t>(m) && b < a + static_cast<uintptr_t>(n);
+}
+
+// Whether rows read at x and written at y are neither the same ones nor apart.
+bool half_aliased(const void* x, const RowStrides& xs, const void* y, const RowStrides& ys, int64_t B, int64_t T, int64_t n,
+                  int64_t d) {
+  if (x == y && xs.b == ys.b && xs.t == ys.t && xs.h == ys.h) return false;
+  return ranges_meet(x, span_bytes(xs, B, T, n, d), y, span_bytes(ys, B, T, n, d));
+}
+
+int view_rope(const dflash2_rope_table* r, int64_t dim, dflash2::RopeView* out) {
+  *out = {nullptr, 0, 0, 1.0f};
+  if (r == nullptr) return DFLASH2_OK;
+  if (r->turns == nullptr || r->rotary_dim < 2 || r->rotary_dim % 2 != 0 || r->rotary_dim > dim || !std::isfinite(r->factor))
+    return DFLASH2_ERR_INVALID_ARG;
+  if (r->rotary_dim > 512) return DFLASH2_ERR_UNSUPPORTED;
+  if (!aligned(r->turns, 8)) return DFLASH2_ERR_MISALIGNED;
+  out->turns = r->turns;
+  out->rd = static_cast<int32_t>(r->rotary_dim);
+  out->interleaved = r->interleaved != 0;
+  out->factor = r->factor;
+  return DFLASH2_OK;
+}
+
+}  // namespace
+
+extern "C" {
+
+int dflash2_rope_turns(int64_t rotary_dim, double theta, const dflash2_rope_scaling* scaling, uint64_t* turns,
+                       float* factor) {
+  const int kind = scaling == nullptr ? DFLASH2_ROPE_NONE : scaling->kind;
+  if (turns == nullptr || factor == nullptr || rotary_dim < 2 || rotary_dim % 2 != 0 || !(theta > 1.0) ||
+      !std::isfinite(theta) || kind < DFLASH2_ROPE_NONE || kind > DFLASH2_ROPE_WAVELENGTH)
+    return DFLASH2_ERR_INVALID_ARG;
+  if (rotary_dim > 512 || (kind == DFLASH2_ROPE_NTK && rotary_dim < 4)) return DFLASH2_ERR_UNSUPPORTED;
+  const double f = kind == DFLASH2_ROPE_NONE ? 1.0 : scaling->factor;
+  if (!(f >= 1.0) || !std::isfinite(f)) return DFLASH2_ERR_INVALID_ARG;
+  const bool yarn = kind == DFLASH2_ROPE_YARN, wavelength = kind == DFLASH2_ROPE_WAVELENGTH;
+  if ((yarn || wavelength) && (!(scaling->original >= 1.0) || !std::isfinite(scaling->original))) return DFLASH2_ERR_INVALID_ARG;
+  if (yarn && (!(scaling->slow > 0.0) || !(scaling->fast > scaling->slow) || !std::isfinite(scaling->fast)))
+    return DFLASH2_ERR_INVALID_ARG;
+  if (wavelength && (!(scaling->low > 0.0) || !(scaling->high > scaling->low) || !std::isfinite(scaling->high)))
+    return DFLASH2_ERR_INVALID_ARG;
+  const double pi2 = 6.283185307179586476925286766559, dim = static_cast<double>(rotary_dim);
+  if (kind == DFLASH2_ROPE_NTK) theta *= std::pow(f, dim / (dim - 2.0));
+  if (!std::isfinite(theta)) return DFLASH2_ERR_INVALID_ARG;
+  double first = 0.0, last = 0.0;
+  if (yarn) {
+    const auto index = [&](double n) { return dim * std::log(scaling->original / (pi2 * n)) / (2.0 * std::log(theta)); };
+    first = std::fmax(std::floor(index(scaling->fast)), 0.0);
+    last = std::fmin(std::ceil(index(scaling->slow)), dim - 1.0);
+  }
+  for (int64_t i = 0; i < rotary_dim / 2; ++i) {
+    double rate = std::pow(theta, -2.0 * static_cast<double>(i) / dim);
+    if (kind == DFLASH2_ROPE_LINEAR) rate /= f;
+    if (yarn) {
+      const double r = std::fmin(std::fmax((static_cast<double>(i) - first) / std::fmax(last - first, 0.001), 0.0), 1.0);
+      rate = rate / f * r + rate * (1.0 - r);
+    }
+    if (wavelength) {
+      const double s = std::fmin(std::fmax((scaling->original * rate / pi2 - scaling->low) / (scaling->high - scaling->low), 0.0), 1.0);
+      rate = rate / f * (1.0 - s) + rate * s;
+    }
+    turns[i] = static_cast<uint64_t>(std::ldexp(rate / pi2, 64));   // rate <= 1: below 2^62
+  }
+  *factor = yarn ? static_cast<float>(0.1 * std::log(f) + 1.0) : 1.0f;
+  return DFLASH2_OK;
+}
+
+int dflash2_rope(dflash2_handle* h, const dflash2_rope_table* rope, const uint16_t* x, int64_t x_batch_stride,
+                 int64_t x_token_stride, int64_t x_head_stride, uint16_t* out, int64_t out_batch_stride,
+                 int64_t out_token_stride, int64_t out_head_stride, const int32_t* base, const int32_t* depth,
+                 int64_t B, int64_t T, int64_t heads, int64_t head_dim, int inverse, void* stream) {
+  const NvtxRange range("dflash2_rope");
+  if (bad_handle(h) || rope == nullptr || B < 0 || T < 0 || heads < 0 || head_dim <= 0) return DFLASH2_ERR_INVALID_ARG;
+  if (head_dim % 8 != 0 || head_dim > 512 || heads > 65536 || B >= kGrid || T >= kGrid || (T > 0 && B > (kGrid - 1) / T))
+    return DFLASH2_ERR_UNSUPPORTED;
+  dflash2::RotateArgs a = {};
+  if (const int st = view_rope(rope, head_dim, &a.rope)) return st;
+  if (B == 0 || T == 0 || heads == 0) return DFLASH2_OK;
+  if (!x || !out) return DFLASH2_ERR_INVALID_ARG;
+  RowStrides xs = {x_batch_stride, x_token_stride, x_head_stride}, os = {out_batch_stride, out_token_stride, out_head_stride};
+  if (const int st = check_rows(&xs, B, T, heads, head_dim)) return st;
+  if (const int st = check_rows(&os, B, T, heads, head_dim)) return st;
+  if (!aligned(x, 16) || !aligned(out, 16) || !aligned(base, 4) || !aligned(depth, 4)) return DFLASH2_ERR_MISALIGNED;
+  if (half_aliased(x, xs, out, os, B, T, heads, head_dim)) return DFLASH2_ERR_INVALID_ARG;
+  if (const int st = wrong_device(h)) return st;
+  a.x = x;
+  a.x_b = xs.b, a.x_t = xs.t, a.x_h = xs.h;
+  a.out = out;
+  a.out_b = os.b, a.out_t = os.t, a.out_h = os.h;
+  a.base = base;
+  a.depth = depth;
+  a.B = B;
+  a.T = static_cast<int32_t>(T);
+  a.heads = static_cast<int32_t>(heads);
+  a.dim = static_cast<int32_t>(head_dim);
+  a.inverse = inverse != 0;
+  a.err = h->err;
+  return launched(dflash2::launch_rope(a, h->num_sms, as_stream(stream)));
+}
+
+int dflash2_cache_append(dflash2_handle* h, const uint16_t* k_new, const uint16_t* v_new, int64_t new_batch_stride,
+                         int64_t new_token_stride, int64_t new_head_stride, const dflash2_kv_cache* cache,
+                         const int32_t* cache_len, const dflash2_rope_table* rope, const int32_t* count,
+                         const int32_t* position, int64_t B, int64_t T, const uint16_t* q, int64_t q_batch_stride,
+                         int64_t q_token_stride, int64_t q_head_stride, uint16_t* q_out, int64_t q_out_batch_stride,
+                         int64_t q_out_token_stride, int64_t q_out_head_stride, int64_t heads, float* scores,
+                         int64_t scores_ld, int32_t* new_len, void* stream) {
+  const NvtxRange range("dflash2_cache_append");
+  if (bad_handle(h) || B < 0 || T < 0 || (q == nullptr) != (q_out == nullptr) || (q && heads <= 0) ||
+      (scores && scores_ld < 0))
+    return DFLASH2_ERR_INVALID_ARG;
+  if (B > 65535 || T >= kGrid || (B > 0 && T > (kGrid - 1) / B) || (q && heads > 65536)) return DFLASH2_ERR_UNSUPPORTED;
+  dflash2::RotateArgs a = {};
+  if (const int st = view_cache(cache, B, &a.cache)) return st;
+  if (const int st = view_rope(rope, cache->head_dim, &a.rope)) return st;
+  if (B == 0) return DFLASH2_OK;
+  if (!cache_len || !new_len || (T > 0 && (!k_new || !v_new))) return DFLASH2_ERR_INVALID_ARG;
+  // one CTA writes a sequence's new length while others may still read these
+  if (overlap(new_len, B, cache_len, B) || overlap(new_len, B, count, B) || overlap(new_len, B, position, B))
+    return DFLASH2_ERR_INVALID_ARG;
+  RowStrides ns = {new_batch_stride, new_token_stride, new_head_stride};
+  if (const int st = check_rows(&ns, B, T, cache->heads, cache->head_dim)) return st;
+  if (!aligned(k_new, 16) || !aligned(v_new, 16) || !aligned(cache_len, 4) || !aligned(count, 4) || !aligned(position, 4) ||
+      !aligned(scores, 4) || !aligned(new_len, 4) || !aligned(q, 16) || !aligned(q_out, 16))
+    return DFLASH2_ERR_MISALIGNED;
+  if (q && T > 0) {
+    RowStrides qs = {q_batch_stride, q_token_stride, q_head_stride};
+    RowStrides os = {q_out_batch_stride, q_out_token_stride, q_out_head_stride};
+    if (const int st = check_rows(&qs, B, T, heads, cache->head_dim)) return st;
+    if (const int st = check_rows(&os, B, T, heads, cache->head_dim)) return st;
+    if (half_aliased(q, qs, q_out, os, B, T, heads, cache->head_dim)) return DFLASH2_ERR_INVALID_ARG;
+    a.x = q;
+    a.x_b = qs.b, a.x_t = qs.t, a.x_h = qs.h;
+    a.out = q_out;
+    a.out_b = os.b, a.out_t = os.t, a.out_h = os.h;
+    a.heads = static_cast<int32_t>(heads);
+  }
+  if (const int st = wrong_device(h)) return st;
+  a.base = position != nullptr ? position : cache_len;
+  a.B = B;
+  a.T = static_cast<int32_t>(T);
+  a.dim = static_cast<int32_t>(cache->head_dim);
+  a.k_new = k_new;
+  a.v_new = v_new;
+  a.new_b = ns.b, a.new_t = ns.t, a.new_h = ns.h;
+  a.cache_len = cache_len;
+  a.count = count;
+  a.scores = scores;
+  a.scores_ld = scores_ld;
+  a.new_len = new_len;
+  a.err = h->err;
+  return launched(dflash2::launch_cache_append(a, h->num_sms, as_stream(stream)));
+}
+
+int dflash2_logits_adjust(dflash2_handle* h, const uint16_t* logits, int64_t logits_batch_stride,
+                          int64_t logits_node_stride, int64_t B, int64_t T, int64_t V, const int32_t* counts,
+                          int64_t counts_ld, const int32_t* tokens, const uint64_t* tree_mask, const float* repetition,
+                          const float* frequency, const float* presence, const float* bias, int64_t bias_ld,
+                          const uint32_t* allowed, int64_t allowed_batch_stride, int64_t allowed_node_stride,
+                          uint16_t* out, int64_t out_batch_stride, int64_t out_node_stride, void* stream) {
+  const NvtxRange range("dflash2_logits_adjust");
+  if (bad_handle(h) || B < 0 || T < 0 || V < 0 || (tree_mask && !tokens)) return DFLASH2_ERR_INVALID_ARG;
+  if (T > dflash2::kMaxNodes || B > 65535 || V >= kGrid - 4096 || B * (V / 2048 + 1) >= kGrid) return DFLASH2_ERR_UNSUPPORTED;
+  if (B == 0 || T == 0 || V == 0) return DFLASH2_OK;
+  if (!logits || !out) return DFLASH2_ERR_INVALID_ARG;
+  // (vectors of 8 columns are read whole)
+  const int64_t row = (V + 7) / 8 * 8, words = (V + 31) / 32, most = int64_t(1) << 38;
+  RowStrides xs = {logits_batch_stride, logits_node_stride, 0}, os = {out_batch_stride, out_node_stride, 0};
+  if (const int st = check_rows(&xs, B, T, 1, row)) return st;
+  if (const int st = check_rows(&os, B, T, 1, row)) return st;
+  if (counts && (counts_ld < (B > 1 ? row : 0) || counts_ld >= most)) return DFLASH2_ERR_INVALID_ARG;
+  if (bias && ((bias_ld != 0 && bias_ld < row) || bias_ld >= most)) return DFLASH2_ERR_INVALID_ARG;
+  if (allowed && (allowed_batch_stride < 0 || allowed_node_stride < 0 || allowed_batch_stride >= most ||
+                  allowed_node_stride >= most || (B > 1 && allowed_batch_stride != 0 && allowed_batch_stride < words) ||
+                  (T > 1 && allowed_node_stride != 0 && allowed_node_stride < words)))
+    return DFLASH2_ERR_INVALID_ARG;
+  if (!aligned(logits, 16) || !aligned(out, 16) || !aligned(counts, 16) || !aligned(bias, 16) || !aligned(tokens, 4) ||
+      !aligned(tree_mask, 8) || !aligned(repetition, 4) || !aligned(frequency, 4) || !aligned(presence, 4) ||
+      !aligned(allowed, 4) || (counts && B > 1 && counts_ld % 8 != 0) || (bias && bias_ld % 8 != 0))
+    return DFLASH2_ERR_MISALIGNED;
+  if (half_aliased(logits, xs, out, os, B, T, 1, row)) return DFLASH2_ERR_INVALID_ARG;
+  if (const int st = wrong_device(h)) return st;
+  dflash2::LogitsArgs a;
+  a.logits = logits;
+  a.x_b = xs.b, a.x_t = xs.t;
+  a.out = out;
+  a.out_b = os.b, a.out_t = os.t;
+  a.B = B;
+  a.T = static_cast<int32_t>(T);
+  a.V = static_cast<int32_t>(V);
+  a.counts = counts;
+  a.counts_ld = counts_ld;
+  a.tokens = tokens;
+  a.mask = tree_mask;
+  a.repetition = repetition;
+  a.frequency = frequency;
+  a.presence = presence;
+  a.bias = bias;
+  a.bias_ld = bias_ld;
+  a.allowed = allowed;
+  a.allowed_b = allowed_batch_stride;
+  a.allowed_t = allowed_node_stride;
+  a.err = h->err;
+  return launched(dflash2::launch_logits_adjust(a, h->num_sms, as_stream(stream)));
+}
+
+int dflash2_token_counts(dflash2_handle* h, const int32_t* tokens, const int32_t* count, const int32_t* path, int64_t B,
+                         int64_t N, int64_t V, int prompt, int32_t* counts, int64_t counts_ld, void* stream) {
+  const NvtxRange range("dflash2_token_counts");
+  if (bad_handle(h) || B < 0 || N < 0 || V < 0) return DFLASH2_ERR_INVALID_ARG;
+  if (B > 65535 || N >= kGrid || (B > 0 && N > (kGrid - 1) / B) || V >= kGrid) return DFLASH2_ERR_UNSUPPORTED;
+  if (B == 0 || N == 0) return DFLASH2_OK;
+  if (!tokens || !counts || (B > 1 && counts_ld < V) || counts_ld >= (int64_t(1) << 38)) return DFLASH2_ERR_INVALID_ARG;
+  if (!aligned(tokens, 4) || !aligned(count, 4) || !aligned(path, 4) || !aligned(counts, 4)) return DFLASH2_ERR_MISALIGNED;
+  if (const int st = wrong_device(h)) return st;
+  dflash2::CountArgs a;
+  a.tokens = tokens;
+  a.count = count;
+  a.path = path;
+  a.B = B;
+  a.N = static_cast<int32_t>(N);
+  a.V = static_cast<int32_t>(V);
+  a.prompt = prompt != 0;
+  a.counts = counts;
+  a.counts_ld = counts_ld;
+  a.err = h->err;
+  return launched(dflash2::launch_token_counts(a, as_stream(stream)));
+}
+
+}  // extern "C"

@@ -1,5 +1,6 @@
-// bind.cpp -- the Python side of the cache operators: checks torch tensors and
-// calls the C ABI with their addresses and strides.
+// bind.cpp -- the Python side of the cache operators and of those around them (rotary
+// positions, appending, logits, counts): checks torch tensors and calls the C ABI with their
+// addresses and strides.
 //
 // A cache operator's kernel takes a few microseconds for one sequence, and reading
 // its tensors' attributes from Python took about as long again (a commit call: 7.0
@@ -22,6 +23,10 @@ decltype(&dflash2_tree_attention) f_attention = nullptr;
 decltype(&dflash2_cache_commit) f_commit = nullptr;
 decltype(&dflash2_cache_scores) f_scores = nullptr;
 decltype(&dflash2_cache_evict) f_evict = nullptr;
+decltype(&dflash2_rope) f_rope = nullptr;
+decltype(&dflash2_cache_append) f_append = nullptr;
+decltype(&dflash2_logits_adjust) f_logits = nullptr;
+decltype(&dflash2_token_counts) f_counts = nullptr;
 
 // A failed check: the Python error has been set.
 struct Refused {};
@@ -207,13 +212,160 @@ PyObject* cache_evict(PyObject*, PyObject* const* a, Py_ssize_t n) {
   });
 }
 
-// addresses of the four entry points, in this order
+// A call's tensors have to be on the handle's device.
+const at::Tensor& here(const at::Tensor& t, int64_t device, const char* name) {
+  if (t.get_device() != device) refuse(name, "expected a tensor on the handle's device");
+  return t;
+}
+const at::Tensor& here(PyObject* o, int64_t device, const char* name) { return here(tensor(o, name), device, name); }
+template <class T>
+T* dense_here(PyObject* o, int64_t device, const char* name, at::ScalarType type, at::IntArrayRef shape) {
+  if (o == Py_None) return nullptr;
+  here(o, device, name);
+  return static_cast<T*>(dense(o, name, type, shape));
+}
+
+// A bf16 [B, T, heads, dim] tensor with unit stride along its last dimension.
+const at::Tensor& heads_of(PyObject* o, int64_t device, const char* name) {
+  const at::Tensor& t = here(o, device, name);
+  if (!is_bf16(t) || t.dim() != 4 || (t.stride(3) != 1 && t.size(3) != 1))
+    refuse(name, "expected bf16 [B, T, heads, dim], unit stride along the last dimension");
+  return t;
+}
+
+// A two- or three-dimensional operand with columns at unit stride.
+const at::Tensor& columns(PyObject* o, int64_t device, const char* name, int64_t dims) {
+  const at::Tensor& t = here(o, device, name);
+  if (t.dim() != dims || (t.stride(dims - 1) != 1 && t.size(dims - 1) != 1)) refuse(name, "wrong shape or strides");
+  return t;
+}
+
+// handle, device, rope, x, out, base, depth, inverse, stream
+PyObject* rope(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  return guarded(n, 9, [&]() {
+    const int64_t device = integer(a[1]);
+    const at::Tensor &x = heads_of(a[3], device, "x"), &out = heads_of(a[4], device, "out");
+    if (out.sizes() != x.sizes()) refuse("out", "expected x's shape");
+    const int64_t B = x.size(0), T = x.size(1);
+    return f_rope(address<dflash2_handle>(a[0]), address<dflash2_rope_table>(a[2]), bits(x), x.stride(0), x.stride(1),
+                  x.stride(2), bits(out), out.stride(0), out.stride(1), out.stride(2),
+                  dense_here<int32_t>(a[5], device, "base", at::kInt, {B}),
+                  dense_here<int32_t>(a[6], device, "depth", at::kInt, {B, T}), B, T, x.size(2), x.size(3),
+                  static_cast<int>(integer(a[7])), address<void>(a[8]));
+  });
+}
+
+// handle, device, cache, cache_batch, k_new, v_new, cache_len, rope, count, position, q, q_out, scores, new_len, stream
+PyObject* cache_append(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  return guarded(n, 15, [&]() {
+    const int64_t device = integer(a[1]);
+    const auto* cache = address<dflash2_kv_cache>(a[2]);
+    const at::Tensor &k = here(rows(a[4], "k_new", cache->head_dim), device, "k_new"),
+                     &v = here(rows(a[5], "v_new", cache->head_dim), device, "v_new");
+    const int64_t B = k.size(0), T = k.size(1);
+    pair(k, v, B, T, cache->heads);
+    sequences(integer(a[3]), B, "cache");
+    const uint16_t* q = nullptr;
+    uint16_t* q_out = nullptr;
+    int64_t qs[3] = {0, 0, 0}, os[3] = {0, 0, 0}, heads = 0;
+    if ((a[10] == Py_None) != (a[11] == Py_None)) refuse("q, q_out", "both or neither");
+    if (a[10] != Py_None) {
+      const at::Tensor &x = heads_of(a[10], device, "q"), &y = heads_of(a[11], device, "q_out");
+      heads = x.size(2);
+      if (x.sizes() != y.sizes() || x.size(0) != B || x.size(1) != T || x.size(3) != cache->head_dim)
+        refuse("q, q_out", "expected [B, T, heads, dim] of k_new's B, T and dim");
+      q = bits(x);
+      q_out = bits(y);
+      for (int i = 0; i < 3; ++i) qs[i] = x.stride(i), os[i] = y.stride(i);
+    }
+    float* scores = nullptr;
+    int64_t ld = 0;
+    if (a[12] != Py_None) {
+      const at::Tensor& s = here(a[12], device, "scores");
+      ld = s.dim() == 3 ? s.size(2) : 0;
+      scores = static_cast<float*>(dense(a[12], "scores", at::kFloat, {B, cache->heads, ld}));
+    }
+    if (a[6] == Py_None || a[13] == Py_None) refuse("cache_len, new_len", "expected a tensor");
+    return f_append(address<dflash2_handle>(a[0]), bits(k), bits(v), k.stride(0), k.stride(1), k.stride(2), cache,
+                    dense_here<int32_t>(a[6], device, "cache_len", at::kInt, {B}), address<dflash2_rope_table>(a[7]),
+                    dense_here<int32_t>(a[8], device, "count", at::kInt, {B}),
+                    dense_here<int32_t>(a[9], device, "position", at::kInt, {B}), B, T, q, qs[0], qs[1], qs[2], q_out,
+                    os[0], os[1], os[2], heads, scores, ld,
+                    dense_here<int32_t>(a[13], device, "new_len", at::kInt, {B}), address<void>(a[14]));
+  });
+}
+
+// handle, device, logits, counts, tokens, tree_mask, repetition, frequency, presence, bias, allowed, out, stream
+PyObject* logits_adjust(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  return guarded(n, 13, [&]() {
+    const int64_t device = integer(a[1]);
+    const at::Tensor &x = columns(a[2], device, "logits", 3), &out = columns(a[11], device, "out", 3);
+    if (!is_bf16(x) || !is_bf16(out) || out.sizes() != x.sizes()) refuse("logits, out", "expected bf16 [B, T, V]");
+    const int64_t B = x.size(0), T = x.size(1), V = x.size(2);
+    const int32_t* counts = nullptr;
+    const float* bias = nullptr;
+    const uint32_t* allowed = nullptr;
+    int64_t counts_ld = 0, bias_ld = 0, allowed_b = 0, allowed_t = 0;
+    if (a[3] != Py_None) {
+      const at::Tensor& t = columns(a[3], device, "counts", 2);
+      if (t.scalar_type() != at::kInt || t.size(0) != B || t.size(1) != V) refuse("counts", "expected int32 [B, V]");
+      counts = static_cast<int32_t*>(t.data_ptr());
+      counts_ld = B > 1 ? t.stride(0) : V;
+    }
+    if (a[9] != Py_None) {
+      const at::Tensor& t = columns(a[9], device, "bias", 2);
+      if (t.scalar_type() != at::kFloat || (t.size(0) != B && t.size(0) != 1) || t.size(1) != V)
+        refuse("bias", "expected fp32 [B, V] or [1, V]");
+      bias = static_cast<float*>(t.data_ptr());
+      bias_ld = t.size(0) > 1 ? t.stride(0) : 0;
+    }
+    if (a[10] != Py_None) {
+      const at::Tensor& t = columns(a[10], device, "allowed", 3);
+      if (t.scalar_type() != at::kInt || (t.size(0) != B && t.size(0) != 1) || (t.size(1) != T && t.size(1) != 1) ||
+          t.size(2) != (V + 31) / 32)
+        refuse("allowed", "expected int32 [B or 1, T or 1, (V + 31) // 32]");
+      allowed = static_cast<uint32_t*>(t.data_ptr());
+      allowed_b = t.size(0) > 1 ? t.stride(0) : 0;
+      allowed_t = t.size(1) > 1 ? t.stride(1) : 0;
+    }
+    return f_logits(address<dflash2_handle>(a[0]), bits(x), x.stride(0), x.stride(1), B, T, V, counts, counts_ld,
+                    dense_here<int32_t>(a[4], device, "tokens", at::kInt, {B, T}),
+                    dense_here<uint64_t>(a[5], device, "tree_mask", at::kLong, {B, T, (T + 63) / 64}),
+                    dense_here<float>(a[6], device, "repetition", at::kFloat, {B}),
+                    dense_here<float>(a[7], device, "frequency", at::kFloat, {B}),
+                    dense_here<float>(a[8], device, "presence", at::kFloat, {B}), bias, bias_ld, allowed, allowed_b,
+                    allowed_t, bits(out), out.stride(0), out.stride(1), address<void>(a[12]));
+  });
+}
+
+// handle, device, tokens, counts, count, path, prompt, stream
+PyObject* token_counts(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  return guarded(n, 8, [&]() {
+    const int64_t device = integer(a[1]);
+    const at::Tensor& tokens = here(a[2], device, "tokens");
+    if (tokens.dim() != 2) refuse("tokens", "expected int32 [B, N]");
+    const int64_t B = tokens.size(0), N = tokens.size(1);
+    const at::Tensor& counts = columns(a[3], device, "counts", 2);
+    if (counts.scalar_type() != at::kInt || counts.size(0) != B) refuse("counts", "expected int32 [B, V]");
+    const int64_t V = counts.size(1);
+    return f_counts(address<dflash2_handle>(a[0]), dense_here<int32_t>(a[2], device, "tokens", at::kInt, {B, N}),
+                    dense_here<int32_t>(a[4], device, "count", at::kInt, {B}),
+                    dense_here<int32_t>(a[5], device, "path", at::kInt, {B, N}), B, N, V, static_cast<int>(integer(a[6])),
+                    static_cast<int32_t*>(counts.data_ptr()), B > 1 ? counts.stride(0) : V, address<void>(a[7]));
+  });
+}
+
+// addresses of the entry points, in this order
 PyObject* init(PyObject*, PyObject* const* a, Py_ssize_t n) {
-  return guarded(n, 4, [&]() {
+  return guarded(n, 8, [&]() {
     f_attention = reinterpret_cast<decltype(f_attention)>(integer(a[0]));
     f_commit = reinterpret_cast<decltype(f_commit)>(integer(a[1]));
     f_scores = reinterpret_cast<decltype(f_scores)>(integer(a[2]));
     f_evict = reinterpret_cast<decltype(f_evict)>(integer(a[3]));
+    f_rope = reinterpret_cast<decltype(f_rope)>(integer(a[4]));
+    f_append = reinterpret_cast<decltype(f_append)>(integer(a[5]));
+    f_logits = reinterpret_cast<decltype(f_logits)>(integer(a[6]));
+    f_counts = reinterpret_cast<decltype(f_counts)>(integer(a[7]));
     return 0;
   });
 }
@@ -228,6 +380,10 @@ PyMethodDef methods[] = {method<init>("init"),
                          method<cache_commit>("cache_commit"),
                          method<cache_scores>("cache_scores"),
                          method<cache_evict>("cache_evict"),
+                         method<rope>("rope"),
+                         method<cache_append>("cache_append"),
+                         method<logits_adjust>("logits_adjust"),
+                         method<token_counts>("token_counts"),
                          {nullptr, nullptr, 0, nullptr}};
 PyModuleDef module = {PyModuleDef_HEAD_INIT, "_dflash2_bind", nullptr, -1, methods, nullptr, nullptr, nullptr, nullptr};
 

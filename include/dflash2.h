@@ -20,6 +20,10 @@
  *   dflash2_cache_commit    the accepted path's keys and values into the cache
  *   dflash2_cache_scores    attention weight received by each cached position
  *   dflash2_cache_evict     the positions weighed most, kept in fresh pages
+ *   dflash2_rope            rotary positions
+ *   dflash2_cache_append    rotated keys and values of new tokens into the cache
+ *   dflash2_logits_adjust   penalties, biases and allowed tokens, node by node
+ *   dflash2_token_counts    the emitted tokens' counts that the penalties read
  *
  * Conventions for every call
  *   - Pointers marked "device" are CUDA device pointers on the handle's device;
@@ -549,6 +553,140 @@ int dflash2_cache_evict(dflash2_handle* h, const float* scores, int64_t scores_l
                         const int32_t* cache_len, const dflash2_kv_cache* dst, int64_t B, int64_t keep,
                         int64_t recent, int32_t* kept, int32_t* new_len, float* dst_scores, int64_t dst_ld,
                         void* stream);
+
+/*
+ * Rotary positions ("RoFormer", Su et al. 2021).  The first rotary_dim elements of a
+ * head are taken in pairs; pair i turns by the angle position * rate_i and is scaled:
+ *   y_1 = factor (x_1 cos - x_2 sin),  y_2 = factor (x_2 cos + x_1 sin);
+ * the rest of the head is copied.  Pair i is elements (i, i + rotary_dim / 2), or (2 i,
+ * 2 i + 1) when `interleaved`.  A rate is given in turns per position times 2^64, so that
+ * position * rate modulo 2^64 is the angle's fraction of a turn exactly, however far the
+ * position and whatever its sign.
+ */
+typedef struct dflash2_rope_table {
+  const uint64_t* turns; /* device [rotary_dim / 2], 8-byte aligned */
+  int64_t rotary_dim;    /* even, 2 .. 512 */
+  int32_t interleaved;
+  float factor;          /* finite */
+} dflash2_rope_table;
+
+/*
+ * Rates of a longer context than was trained on.  With f_i = theta^(-2 i / rotary_dim)
+ * radians per position:
+ *   NONE        f_i
+ *   LINEAR      f_i / factor
+ *   NTK         theta replaced by theta * factor^(rotary_dim / (rotary_dim - 2))
+ *   YARN        ("YaRN", Peng et al. 2023) f_i (r_i / factor + 1 - r_i), r_i rising linearly from 0 at the
+ *               pair that turns a = `fast` times over `original` positions to 1 at the one that turns `slow` times
+ *               (those pairs' indices rounded outwards, at least 0 and at most rotary_dim - 1); cos and sin times
+ *               0.1 ln(factor) + 1
+ *   WAVELENGTH  f_i for wavelengths below original / high, f_i / factor above original / low, and between
+ *               them (1 - s) f_i / factor + s f_i, s = (original / wavelength - low) / (high - low)
+ */
+enum dflash2_rope_scaling_kind {
+  DFLASH2_ROPE_NONE = 0,
+  DFLASH2_ROPE_LINEAR = 1,
+  DFLASH2_ROPE_NTK = 2,
+  DFLASH2_ROPE_YARN = 3,
+  DFLASH2_ROPE_WAVELENGTH = 4
+};
+typedef struct dflash2_rope_scaling {
+  int32_t kind;
+  double factor;     /* >= 1 */
+  double original;   /* YARN, WAVELENGTH: positions of the original context, >= 1 */
+  double fast, slow; /* YARN: fast > slow > 0 */
+  double low, high;  /* WAVELENGTH: high > low > 0 */
+} dflash2_rope_scaling;
+
+/*
+ * Fills turns[rotary_dim / 2] (HOST memory: the caller copies it to the device) and *factor.
+ * Host only, needs no handle.  rotary_dim as above (at least 4 for NTK); theta > 1;
+ * scaling NULL: NONE.
+ */
+int dflash2_rope_turns(int64_t rotary_dim, double theta, const dflash2_rope_scaling* scaling, uint64_t* turns,
+                       float* factor);
+
+/*
+ * Rotates x to out by the positions base[b] + depth[b,t].
+ *   x, out   device bf16 [B, T, heads, head_dim] with the given strides.  out may be x
+ *            (same address, same strides); otherwise their ranges must not overlap
+ *   base     device int32 [B] or NULL: 0
+ *   depth    device int32 [B, T] or NULL: t.  Negative positions are allowed
+ *   inverse  turns by the negated angle (the factor stays): the gradient of the forward
+ *            call, and with factor 1 its inverse
+ * head_dim a multiple of 8, at most 512 and at least rotary_dim; x and out 16-byte aligned, strides
+ * multiples of 8; B * T < 2^31.  Products and sums are fp32, rounded once.
+ */
+int dflash2_rope(dflash2_handle* h, const dflash2_rope_table* rope, const uint16_t* x, int64_t x_batch_stride,
+                 int64_t x_token_stride, int64_t x_head_stride, uint16_t* out, int64_t out_batch_stride,
+                 int64_t out_token_stride, int64_t out_head_stride, const int32_t* base, const int32_t* depth,
+                 int64_t B, int64_t T, int64_t heads, int64_t head_dim, int inverse, void* stream);
+
+/*
+ * Appends new tokens (a prompt, or the next token of each sequence) to the cache:
+ * token i < count[b] becomes position cache_len[b] + i, its key rotated, its value as it is.
+ *   k_new, v_new  device bf16 [B, T, cache->heads, head_dim] (strides as above)
+ *   rope          NULL: nothing is rotated
+ *   count         device int32 [B] or NULL: T; outside [0, T]: clamped and flagged
+ *   position      device int32 [B], the angle's position of token 0, or NULL: cache_len (they
+ *                 differ once positions have been evicted)
+ *   q, q_out      device bf16 [B, T, heads, head_dim] or both NULL: the tokens' queries, rotated
+ *                 like the keys; rows i >= count[b] of q_out are left alone.  q_out may be q
+ *                 (same address, same strides); otherwise their ranges must not overlap
+ *   scores        device fp32 [B, cache->heads, scores_ld] or NULL: the appended
+ *                 positions' entries are set to 0
+ *   new_len       device int32 [B]: cache_len + count; must not overlap cache_len, count or position
+ * Positions past the capacity (or scores_ld) are dropped, new_len stops there, and
+ * DFLASH2_DEVERR_BAD_LENGTH is flagged.  Two sequences must not append to the same page.
+ * B <= 65535, B * T < 2^31; any T.
+ */
+int dflash2_cache_append(dflash2_handle* h, const uint16_t* k_new, const uint16_t* v_new, int64_t new_batch_stride,
+                         int64_t new_token_stride, int64_t new_head_stride, const dflash2_kv_cache* cache,
+                         const int32_t* cache_len, const dflash2_rope_table* rope, const int32_t* count,
+                         const int32_t* position, int64_t B, int64_t T, const uint16_t* q, int64_t q_batch_stride,
+                         int64_t q_token_stride, int64_t q_head_stride, uint16_t* q_out, int64_t q_out_batch_stride,
+                         int64_t q_out_token_stride, int64_t q_out_head_stride, int64_t heads, float* scores,
+                         int64_t scores_ld, int32_t* new_len, void* stream);
+
+/*
+ * What a request's sampling parameters make of the target's logits, before they are
+ * verified or ranked.  Row (b, t) is the distribution after node t.  With n_v = counts[b,v] (bits 0 to
+ * 30) + the number of nodes s that t sees whose token is v:
+ *   x = logits[b,t,v]
+ *   x = x > 0 ? x / repetition[b] : x * repetition[b]   where n_v > 0 or bit 31 of counts[b,v] is set
+ *   x = x - frequency[b] n_v - presence[b] [n_v > 0] + bias[b,v]
+ *   x = -inf                                            where bit v of allowed[b,t] is 0
+ *   logits, out  device bf16 [B, T, V] with the given strides.  out may be logits (same address,
+ *                same strides: what does not change is then not written); otherwise their ranges must not overlap
+ *   counts       device int32 [B, counts_ld] (see dflash2_token_counts) or NULL: 0
+ *   tokens       device int32 [B, T], the nodes' tokens, not yet counted, or NULL: none.  An id
+ *                outside [0, V) is flagged and counts nothing
+ *   tree_mask    device uint64 [B, T, (T + 63) / 64] as in dflash2_tree_attention, or NULL: a chain
+ *   repetition, frequency, presence  device fp32 [B] or NULL: 1, 0, 0
+ *   bias         device fp32 [B, bias_ld] (bias_ld 0: one row for all) or NULL: 0
+ *   allowed      device uint32 words, bit v % 32 of word v / 32, (V + 31) / 32 words for each node, with the given
+ *                strides in words (0: shared), or NULL: everything
+ * T <= 128, B <= 65535, V < 2^31 - 4096, B * (V / 2048 + 1) < 2^31.  logits, out, counts and bias 16-byte aligned; strides of logits and out, counts_ld and
+ * bias_ld multiples of 8 and at least V.  Columns from V on are left alone.  Arithmetic is fp32, rounded once.
+ */
+int dflash2_logits_adjust(dflash2_handle* h, const uint16_t* logits, int64_t logits_batch_stride,
+                          int64_t logits_node_stride, int64_t B, int64_t T, int64_t V, const int32_t* counts,
+                          int64_t counts_ld, const int32_t* tokens, const uint64_t* tree_mask, const float* repetition,
+                          const float* frequency, const float* presence, const float* bias, int64_t bias_ld,
+                          const uint32_t* allowed, int64_t allowed_batch_stride, int64_t allowed_node_stride,
+                          uint16_t* out, int64_t out_batch_stride, int64_t out_node_stride, void* stream);
+
+/*
+ * Keeps the counts that dflash2_logits_adjust reads: for i < count[b], with v = tokens[b,
+ * path[b,i]], counts[b,v] += 1, or, with prompt != 0, counts[b,v] |= 2^31.
+ *   tokens  device int32 [B, N]; an id outside [0, V) is flagged and skipped
+ *   count   device int32 [B] or NULL: N; outside [0, N]: clamped and flagged
+ *   path    device int32 [B, N] or NULL: i; a node outside [0, N) is clamped and flagged
+ *   counts  device int32 [B, counts_ld], counts_ld >= V
+ * B <= 65535, B * N < 2^31.  The same token may occur any number of times.
+ */
+int dflash2_token_counts(dflash2_handle* h, const int32_t* tokens, const int32_t* count, const int32_t* path, int64_t B,
+                         int64_t N, int64_t V, int prompt, int32_t* counts, int64_t counts_ld, void* stream);
 
 #ifdef __cplusplus
 }
