@@ -52,6 +52,9 @@ SIGNATURES = {
     "dflash2_tree_attention_workspace": (SZ, [P, I64, I64, I64, I64, I64]),
     "dflash2_tree_attention": (I32, [P, P, I64, I64, I64, P, P, P, P, I64, I64, I64, P, I64, I64, I64, F32, P, P, P,
                                      SZ, P]),
+    "dflash2_prefix_attention_workspace": (SZ, [P, I64, I64, I64, I64, I64]),
+    "dflash2_prefix_attention": (I32, [P, P, I64, I64, I64, P, P, P, P, I64, P, P, I64, I64, I64, P, I64, I64, I64, F32, P,
+                                       P, P, SZ, P]),
     "dflash2_cache_commit": (I32, [P, P, P, I64, I64, I64, P, P, P, P, I64, I64, P, I64, P, P]),
     "dflash2_cache_scores": (I32, [P, P, I64, I64, I64, P, P, P, P, P, I64, I64, I64, F32, P, I64, P]),
     "dflash2_cache_evict": (I32, [P, P, I64, P, P, P, I64, I64, I64, P, P, P, I64, P]),
@@ -132,6 +135,6 @@ def load_bind():
             raise RuntimeError(f"{BIND_PATH} was built for torch {mod.torch_version}, not {torch.__version__}: {again}")
         mod.init(*(ctypes.cast(getattr(lib, "dflash2_" + f), P).value
                    for f in ("tree_attention", "cache_commit", "cache_scores", "cache_evict", "rope", "cache_append",
-                             "logits_adjust", "token_counts")))
+                             "logits_adjust", "token_counts", "prefix_attention")))
         _bind = mod
     return _bind

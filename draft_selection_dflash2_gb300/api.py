@@ -425,6 +425,36 @@ def tree_attention(h: Handle, q, cache: KVCache, cache_len, k_new=None, v_new=No
     return out, lse
 
 
+def prefix_attention_workspace(h: Handle, B: int, T: int, heads: int, kv_heads: int, head_dim: int) -> int:
+    return int(h._lib.dflash2_prefix_attention_workspace(h.ptr, B, T, heads, kv_heads, head_dim))
+
+
+def prefix_attention(h: Handle, q, cache: KVCache, cache_len, prefix_len, prefix_start=None, k_new=None, v_new=None,
+                     tree_mask=None, scale: float = None, out=None, lse=None, workspace=None, stream=None):
+    """tree_attention for sequences that share their beginnings, which are read and multiplied once for a group ->
+    (out bf16 [B, T, heads, dim], lse fp32 [B, T, heads]).
+
+    prefix_len int32 [groups]: how many first positions the sequences prefix_start[g] .. prefix_start[g + 1] - 1 share;
+    prefix_start int32 [groups + 1] (None: one group, the whole batch).  The other arguments are tree_attention's;
+    workspace: device bytes of at least prefix_attention_workspace(...)."""
+    if out is None or lse is None or workspace is None:
+        _need(q.dim() == 4 and q.is_cuda, "q: CUDA bf16 [B, T, heads, dim]")
+        B, T, heads, dim = q.shape
+        if out is None:
+            out = _new_on(stream, q.shape, torch.bfloat16, q.device)
+        if lse is None:
+            lse = _new_on(stream, (B, T, heads), torch.float32, q.device)
+        if workspace is None:
+            workspace = _new_on(stream, (max(prefix_attention_workspace(h, B, T, heads, cache.heads, dim), 256),),
+                                torch.uint8, q.device)
+    status = h._bind.prefix_attention(h.raw, h.device, cache.addr, cache.batch, q, cache_len, prefix_len, prefix_start,
+                                      k_new, v_new, tree_mask, cache.dim ** -0.5 if scale is None else scale, out, lse,
+                                      workspace, _raw_stream(h, stream))
+    if status:
+        _check(status, "dflash2_prefix_attention")
+    return out, lse
+
+
 def cache_commit(h: Handle, k_new, v_new, cache: KVCache, cache_len, count=None, path=None, scores=None,
                  new_len=None, stream=None):
     """Appends the accepted nodes' keys and values to the cache -> new_len int32 [B].

@@ -13,6 +13,42 @@ namespace {
 constexpr int kK = 16;
 constexpr int64_t kMaxL = 64;
 
+// What the two attention entry points check alike; fills all of `a` but err (nothing with B or T = 0).
+int check_attention(const uint16_t* q, RowStrides qs, const dflash2_kv_cache* cache, const int32_t* cache_len,
+                    const uint16_t* k_new, const uint16_t* v_new, RowStrides ns, const uint64_t* tree_mask, int64_t B,
+                    int64_t T, int64_t heads, float scale, uint16_t* out, float* lse, const void* workspace,
+                    dflash2::AttnArgs* a) {
+  if (const int st = check_queries(B, T, heads, cache, scale)) return st;
+  if (const int st = view_cache(cache, B, &a->cache)) return st;
+  if (B == 0 || T == 0) return DFLASH2_OK;
+  // one 32-bit number counts the tiles of 128 keys over all sequences, kv heads and pairs of row tiles
+  if (dflash2::tree_attn_units(B, T, heads / cache->heads, cache->heads, a->cache.capacity) >= (int64_t(1) << 31))
+    return DFLASH2_ERR_UNSUPPORTED;
+  if (!q || !cache_len || !out || (k_new == nullptr) != (v_new == nullptr) || (tree_mask && !k_new))
+    return DFLASH2_ERR_INVALID_ARG;
+  if (const int st = check_rows(&qs, B, T, heads, cache->head_dim)) return st;
+  if (k_new)
+    if (const int st = check_rows(&ns, B, T, cache->heads, cache->head_dim)) return st;
+  if (!aligned(q, 16) || !aligned(k_new, 16) || !aligned(v_new, 16) || !aligned(cache_len, 4) ||
+      !aligned(tree_mask, 8) || !aligned(out, 16) || !aligned(lse, 4) || !aligned(workspace, 256))
+    return DFLASH2_ERR_MISALIGNED;
+  a->q = q;
+  a->q_b = qs.b, a->q_t = qs.t, a->q_h = qs.h;
+  a->cache_len = cache_len;
+  a->k_new = k_new;
+  a->v_new = v_new;
+  a->new_b = ns.b, a->new_t = ns.t, a->new_h = ns.h;
+  a->mask = tree_mask;
+  a->B = B;
+  a->T = static_cast<int32_t>(T);
+  a->heads = static_cast<int32_t>(heads);
+  a->group = static_cast<int32_t>(heads / cache->heads);
+  a->scale = scale;
+  a->out = out;
+  a->lse = lse;
+  return DFLASH2_OK;
+}
+
 }  // namespace
 
 extern "C" {
@@ -364,43 +400,61 @@ int dflash2_tree_attention(dflash2_handle* h, const uint16_t* q, int64_t q_batch
                            size_t ws_bytes, void* stream) {
   const NvtxRange range("dflash2_tree_attention");
   if (bad_handle(h)) return DFLASH2_ERR_INVALID_ARG;
-  if (const int st = check_queries(B, T, heads, cache, scale)) return st;
   dflash2::AttnArgs a;
-  if (const int st = view_cache(cache, B, &a.cache)) return st;
+  if (const int st = check_attention(q, {q_batch_stride, q_token_stride, q_head_stride}, cache, cache_len, k_new, v_new,
+                                     {new_batch_stride, new_token_stride, new_head_stride}, tree_mask, B, T, heads, scale,
+                                     out, lse, workspace, &a))
+    return st;
   if (B == 0 || T == 0) return DFLASH2_OK;
-  // one 32-bit number counts the tiles of 128 keys over all sequences, kv heads and pairs of row tiles
-  if (dflash2::tree_attn_units(B, T, heads / cache->heads, cache->heads, a.cache.capacity) >= (int64_t(1) << 31))
-    return DFLASH2_ERR_UNSUPPORTED;
-  if (!q || !cache_len || !out || (k_new == nullptr) != (v_new == nullptr) || (tree_mask && !k_new))
-    return DFLASH2_ERR_INVALID_ARG;
-  RowStrides qs = {q_batch_stride, q_token_stride, q_head_stride};
-  RowStrides ns = {new_batch_stride, new_token_stride, new_head_stride};
-  if (const int st = check_rows(&qs, B, T, heads, cache->head_dim)) return st;
-  if (k_new)
-    if (const int st = check_rows(&ns, B, T, cache->heads, cache->head_dim)) return st;
-  if (!aligned(q, 16) || !aligned(k_new, 16) || !aligned(v_new, 16) || !aligned(cache_len, 4) ||
-      !aligned(tree_mask, 8) || !aligned(out, 16) || !aligned(lse, 4) || !aligned(workspace, 256))
-    return DFLASH2_ERR_MISALIGNED;
   if (ws_bytes < dflash2::tree_attn_workspace_bytes(B, T, heads, cache->heads, cache->head_dim, h->num_sms) ||
       workspace == nullptr)
     return DFLASH2_ERR_WORKSPACE;
   if (const int st = wrong_device(h)) return st;
-  a.q = q;
-  a.q_b = qs.b, a.q_t = qs.t, a.q_h = qs.h;
-  a.cache_len = cache_len;
-  a.k_new = k_new;
-  a.v_new = v_new;
-  a.new_b = ns.b, a.new_t = ns.t, a.new_h = ns.h;
-  a.mask = tree_mask;
-  a.B = B;
-  a.T = static_cast<int32_t>(T);
-  a.heads = static_cast<int32_t>(heads);
-  a.group = static_cast<int32_t>(heads / cache->heads);
-  a.scale = scale;
-  a.out = out;
-  a.lse = lse;
   a.err = h->err;
   return launched(dflash2::launch_tree_attn(a, cache->head_dim, workspace, h->num_sms, as_stream(stream)));
+}
+
+size_t dflash2_prefix_attention_workspace(const dflash2_handle* h, int64_t B, int64_t T, int64_t heads,
+                                          int64_t kv_heads, int64_t head_dim) {
+  if (bad_handle(h) || B <= 0 || B > 65535 || T <= 0 || T > dflash2::kMaxNodes || kv_heads <= 0 || heads <= 0 ||
+      kv_heads > kMaxKvHeads || heads % kv_heads != 0 || (head_dim != 64 && head_dim != 128))
+    return 0;
+  return dflash2::prefix_attn_workspace_bytes(B, T, heads, kv_heads, head_dim, h->num_sms);
+}
+
+int dflash2_prefix_attention(dflash2_handle* h, const uint16_t* q, int64_t q_batch_stride, int64_t q_token_stride,
+                             int64_t q_head_stride, const dflash2_kv_cache* cache, const int32_t* cache_len,
+                             const int32_t* prefix_len, const int32_t* prefix_start, int64_t groups,
+                             const uint16_t* k_new, const uint16_t* v_new, int64_t new_batch_stride,
+                             int64_t new_token_stride, int64_t new_head_stride, const uint64_t* tree_mask, int64_t B,
+                             int64_t T, int64_t heads, float scale, uint16_t* out, float* lse, void* workspace,
+                             size_t ws_bytes, void* stream) {
+  const NvtxRange range("dflash2_prefix_attention");
+  if (bad_handle(h) || groups < 0 || groups > B || (groups > 1 && !prefix_start) || (groups > 0 && !prefix_len))
+    return DFLASH2_ERR_INVALID_ARG;
+  dflash2::PrefixArgs x;
+  dflash2::AttnArgs& a = x.attn;
+  if (const int st = check_attention(q, {q_batch_stride, q_token_stride, q_head_stride}, cache, cache_len, k_new, v_new,
+                                     {new_batch_stride, new_token_stride, new_head_stride}, tree_mask, B, T, heads, scale,
+                                     out, lse, workspace, &a))
+    return st;
+  if (B == 0 || T == 0) return DFLASH2_OK;
+  if (dflash2::prefix_attn_units(B, T, a.group, cache->heads, a.cache.capacity) >= (int64_t(1) << 27))
+    return DFLASH2_ERR_UNSUPPORTED;
+  // the nodes of a group's sequences are rows of one operand
+  if (B > 1 && T > 1 && a.q_b != T * a.q_t) return DFLASH2_ERR_UNSUPPORTED;
+  if (!aligned(prefix_len, 4) || !aligned(prefix_start, 4)) return DFLASH2_ERR_MISALIGNED;
+  if (ws_bytes < dflash2::prefix_attn_workspace_bytes(B, T, heads, cache->heads, cache->head_dim, h->num_sms) ||
+      workspace == nullptr)
+    return DFLASH2_ERR_WORKSPACE;
+  if (const int st = wrong_device(h)) return st;
+  if (T == 1) a.q_t = a.q_b;
+  a.q_b = a.q_t;
+  x.start = prefix_start;
+  x.len = prefix_len;
+  x.groups = static_cast<int32_t>(groups);
+  a.err = h->err;
+  return launched(dflash2::launch_prefix_attn(x, cache->head_dim, workspace, h->num_sms, as_stream(stream)));
 }
 
 int dflash2_cache_commit(dflash2_handle* h, const uint16_t* k_new, const uint16_t* v_new, int64_t new_batch_stride,

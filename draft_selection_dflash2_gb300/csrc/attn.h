@@ -71,10 +71,21 @@ struct EvictArgs {
   uint32_t* err;
 };
 
+struct PrefixArgs {
+  AttnArgs attn;                  // q_t: from one node to the next, through all sequences
+  const int32_t* start;           // [groups + 1] first sequence of each group; nullptr: one group
+  const int32_t* len;             // [groups] shared positions
+  int32_t groups;
+};
+
 // Most key tiles that a call's items can have: fewer than 2^31.
 int64_t tree_attn_units(int64_t B, int64_t T, int64_t group, int64_t kv_heads, int64_t capacity);
 size_t tree_attn_workspace_bytes(int64_t B, int64_t T, int64_t heads, int64_t kv_heads, int64_t head_dim, int num_sms);
 cudaError_t launch_tree_attn(const AttnArgs& a, int64_t head_dim, void* workspace, int num_sms, cudaStream_t stream);
+// The same with shared prefixes: fewer than 2^27.
+int64_t prefix_attn_units(int64_t B, int64_t T, int64_t group, int64_t kv_heads, int64_t capacity);
+size_t prefix_attn_workspace_bytes(int64_t B, int64_t T, int64_t heads, int64_t kv_heads, int64_t head_dim, int num_sms);
+cudaError_t launch_prefix_attn(const PrefixArgs& a, int64_t head_dim, void* workspace, int num_sms, cudaStream_t stream);
 cudaError_t launch_cache_scores(const ScoresArgs& a, int64_t head_dim, int num_sms, cudaStream_t stream);
 cudaError_t launch_cache_commit(const CommitArgs& a, int64_t head_dim, cudaStream_t stream);
 cudaError_t launch_cache_evict(const EvictArgs& a, int64_t head_dim, int num_sms, cudaStream_t stream);

@@ -23,6 +23,7 @@ decltype(&dflash2_tree_attention) f_attention = nullptr;
 decltype(&dflash2_cache_commit) f_commit = nullptr;
 decltype(&dflash2_cache_scores) f_scores = nullptr;
 decltype(&dflash2_cache_evict) f_evict = nullptr;
+decltype(&dflash2_prefix_attention) f_prefix = nullptr;
 decltype(&dflash2_rope) f_rope = nullptr;
 decltype(&dflash2_cache_append) f_append = nullptr;
 decltype(&dflash2_logits_adjust) f_logits = nullptr;
@@ -355,9 +356,47 @@ PyObject* token_counts(PyObject*, PyObject* const* a, Py_ssize_t n) {
   });
 }
 
+// handle, device, cache, cache_batch, q, cache_len, prefix_len, prefix_start, k_new, v_new, tree_mask, scale, out, lse,
+// workspace, stream
+PyObject* prefix_attention(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  return guarded(n, 16, [&]() {
+    const int64_t device = integer(a[1]);
+    const auto* cache = address<dflash2_kv_cache>(a[2]);
+    const at::Tensor& q = here(rows(a[4], "q", cache->head_dim), device, "q");
+    const int64_t B = q.size(0), T = q.size(1), heads = q.size(2);
+    sequences(integer(a[3]), B, "cache");
+    const at::Tensor& shared = here(a[6], device, "prefix_len");
+    if (shared.dim() != 1) refuse("prefix_len", "expected int32 [groups]");
+    const int64_t groups = shared.size(0);
+    const uint16_t *k = nullptr, *v = nullptr;
+    int64_t ns[3] = {0, 0, 0};
+    if ((a[8] == Py_None) != (a[9] == Py_None)) refuse("k_new, v_new", "both or neither");
+    if (a[8] != Py_None) {
+      const at::Tensor &kn = here(rows(a[8], "k_new", cache->head_dim), device, "k_new"),
+                       &vn = here(rows(a[9], "v_new", cache->head_dim), device, "v_new");
+      pair(kn, vn, B, T, cache->heads);
+      k = bits(kn);
+      v = bits(vn);
+      for (int i = 0; i < 3; ++i) ns[i] = kn.stride(i);
+    }
+    const at::Tensor& out = here(a[12], device, "out");
+    if (!is_bf16(out) || out.sizes() != q.sizes() || !out.is_contiguous()) refuse("out", "expected contiguous bf16 of q's shape");
+    const at::Tensor& ws = here(a[14], device, "workspace");
+    if (!ws.is_contiguous()) refuse("workspace", "expected a contiguous tensor");
+    if (a[5] == Py_None) refuse("cache_len", "expected a tensor");
+    return f_prefix(address<dflash2_handle>(a[0]), bits(q), q.stride(0), q.stride(1), q.stride(2), cache,
+                    dense_here<int32_t>(a[5], device, "cache_len", at::kInt, {B}),
+                    dense_here<int32_t>(a[6], device, "prefix_len", at::kInt, {groups}),
+                    dense_here<int32_t>(a[7], device, "prefix_start", at::kInt, {groups + 1}), groups, k, v, ns[0], ns[1],
+                    ns[2], dense_here<uint64_t>(a[10], device, "tree_mask", at::kLong, {B, T, (T + 63) / 64}), B, T, heads,
+                    number(a[11]), bits(out), dense_here<float>(a[13], device, "lse", at::kFloat, {B, T, heads}),
+                    ws.data_ptr(), ws.nbytes(), address<void>(a[15]));
+  });
+}
+
 // addresses of the entry points, in this order
 PyObject* init(PyObject*, PyObject* const* a, Py_ssize_t n) {
-  return guarded(n, 8, [&]() {
+  return guarded(n, 9, [&]() {
     f_attention = reinterpret_cast<decltype(f_attention)>(integer(a[0]));
     f_commit = reinterpret_cast<decltype(f_commit)>(integer(a[1]));
     f_scores = reinterpret_cast<decltype(f_scores)>(integer(a[2]));
@@ -366,6 +405,7 @@ PyObject* init(PyObject*, PyObject* const* a, Py_ssize_t n) {
     f_append = reinterpret_cast<decltype(f_append)>(integer(a[5]));
     f_logits = reinterpret_cast<decltype(f_logits)>(integer(a[6]));
     f_counts = reinterpret_cast<decltype(f_counts)>(integer(a[7]));
+    f_prefix = reinterpret_cast<decltype(f_prefix)>(integer(a[8]));
     return 0;
   });
 }
@@ -380,6 +420,7 @@ PyMethodDef methods[] = {method<init>("init"),
                          method<cache_commit>("cache_commit"),
                          method<cache_scores>("cache_scores"),
                          method<cache_evict>("cache_evict"),
+                         method<prefix_attention>("prefix_attention"),
                          method<rope>("rope"),
                          method<cache_append>("cache_append"),
                          method<logits_adjust>("logits_adjust"),

@@ -20,6 +20,7 @@
  *   dflash2_cache_commit    the accepted path's keys and values into the cache
  *   dflash2_cache_scores    attention weight received by each cached position
  *   dflash2_cache_evict     the positions weighed most, kept in fresh pages
+ *   dflash2_prefix_attention  the same attention, a shared beginning taken once
  *   dflash2_rope            rotary positions
  *   dflash2_cache_append    rotated keys and values of new tokens into the cache
  *   dflash2_logits_adjust   penalties, biases and allowed tokens, node by node
@@ -491,6 +492,33 @@ int dflash2_tree_attention(dflash2_handle* h, const uint16_t* q, int64_t q_batch
                            int64_t new_token_stride, int64_t new_head_stride, const uint64_t* tree_mask, int64_t B,
                            int64_t T, int64_t heads, float scale, uint16_t* out, float* lse, void* workspace,
                            size_t ws_bytes, void* stream);
+
+/*
+ * dflash2_tree_attention for a batch whose sequences share their beginnings (a system prompt, several
+ * answers to one question): the shared positions' keys and values are read and multiplied once for a
+ * group of sequences.  Group g is sequences prefix_start[g] .. prefix_start[g+1] - 1; their first
+ * prefix_len[g] cached positions hold the same keys and values, in the same pages or in copies (those of
+ * the group's first sequence are read for all of it).  Then the result is what dflash2_tree_attention
+ * gives, to the roundings of its fp32 sums.
+ *   prefix_len    device int32 [groups].  Outside [0, capacity], or above cache_len of a sequence of the group: clamped
+ *                 and flagged (DFLASH2_DEVERR_BAD_LENGTH)
+ *   prefix_start  device int32 [groups + 1], ascending from 0 to B; otherwise flagged as well, and every sequence is
+ *                 taken by itself.  NULL: groups is at most 1, the whole batch
+ *   groups        0 .. B
+ * The other arguments are dflash2_tree_attention's, with a workspace of its own size.  With B and T
+ * above 1 q_batch_stride is T * q_token_stride.  cache->heads * (capacity / 128 + 2) * (2 B + B * (pairs of 128 query rows per kv
+ * head) + B * T / (2 * (nodes of a row tile))) < 2^27.  What a row does not see never reaches it, and infinite or NaN
+ * values reach the rows that see them, as there.  The same inputs give the same bits on every call.
+ */
+size_t dflash2_prefix_attention_workspace(const dflash2_handle* h, int64_t B, int64_t T, int64_t heads,
+                                          int64_t kv_heads, int64_t head_dim);
+int dflash2_prefix_attention(dflash2_handle* h, const uint16_t* q, int64_t q_batch_stride, int64_t q_token_stride,
+                             int64_t q_head_stride, const dflash2_kv_cache* cache, const int32_t* cache_len,
+                             const int32_t* prefix_len, const int32_t* prefix_start, int64_t groups,
+                             const uint16_t* k_new, const uint16_t* v_new, int64_t new_batch_stride,
+                             int64_t new_token_stride, int64_t new_head_stride, const uint64_t* tree_mask, int64_t B,
+                             int64_t T, int64_t heads, float scale, uint16_t* out, float* lse, void* workspace,
+                             size_t ws_bytes, void* stream);
 
 /*
  * Appends the accepted path to the cache.  After verification the accepted
