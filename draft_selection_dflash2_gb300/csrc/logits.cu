@@ -1,12 +1,19 @@
 // logits.cu -- what sampling parameters make of the target's logits, and the token
 // counts that they read.
 //
-// logits_adjust: a CTA takes 2048 columns of one sequence and walks over its T nodes; a
-// thread takes 8 columns.  What does not depend on the node (counts, bias) is read once for
-// all of them.  The drafted tokens that fall among the CTA's columns, usually none, are
-// listed in shared memory, and a thread that has one among its own adds to each node's counts
-// those that the node sees.  Where out is logits, vectors that stay as
-// they are are neither read nor written, and vectors of which nothing is allowed only written.
+// logits_adjust: a CTA takes 2048 columns of one sequence, vectors of 8, and walks over its T nodes.
+// What does not depend on the node (counts, bias) is read once for all of them, and the masks of
+// allowed tokens go through shared memory.  Few vectors hold a token that was emitted, biased or
+// drafted; these are listed.  The CTA's threads share out the listed vectors and their nodes, so
+// that no warp runs the arithmetic for the sake of one lane, and have the first ones' loads
+// under way while each takes its own vector, if that is not listed, through all nodes: there only
+// the mask matters.  Such a vector is copied; where out is logits nothing of it is read, and
+// what is not allowed is written.
+// 128 blocks of 17 nodes over 151936 tokens in place, half of them bound by a grammar, 2000
+// tokens emitted and 2000 in the prompt: 174 us (every thread adjusting its own vector: 470; masks fetched
+// by each thread, partly masked vectors read: 220 to 195; the listed vectors' loads after the others: 189).
+// Memory takes about 95 of it: 330 MB of -inf, 120 MB of counts and masks, and of every listed vector a
+// 32-byte sector each way; the rest is instructions, and at most 4 CTAs on an SM (more of them spill: 184, 204).
 #include "launch.h"
 #include "serve.h"
 
@@ -16,7 +23,8 @@ namespace {
 constexpr int kThreads = 256;
 constexpr int kCols = 8;                // columns of a thread
 constexpr int kBlockCols = kThreads * kCols;
-constexpr int kRows = 4;                // rows of a thread under way at once
+constexpr int kBlockWords = kBlockCols / 32;
+constexpr int kCopyRows = 4, kRows = 2; // rows of a thread under way at once: copied ones, computed ones
 
 struct Draft {
   int16_t col;                          // of the CTA's columns
@@ -24,129 +32,237 @@ struct Draft {
 };
 
 __device__ __forceinline__ uint32_t pack(float lo, float hi) {
-  return static_cast<uint32_t>(__bfloat16_as_ushort(__float2bfloat16_rn(lo))) |
-         static_cast<uint32_t>(__bfloat16_as_ushort(__float2bfloat16_rn(hi))) << 16;
+  uint32_t r;
+  asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+  return r;
 }
 
-__global__ void __launch_bounds__(kThreads) logits_adjust_kernel(const __grid_constant__ LogitsArgs a, int32_t blocks_per_seq) {
+constexpr uint32_t kNone = 0xFF80FF80u;  // two bf16 -inf
+
+// The sequence's parameters.
+struct Penalties {
+  float repetition, inverse, frequency, presence;
+};
+
+// x -> x * (known ? (x > 0 ? 1 / repetition : repetition) : 1) - less.
+__device__ __forceinline__ float adjusted(float x, bool known, float less, const Penalties& p) {
+  return fmaf(x, known ? (x > 0.0f ? p.inverse : p.repetition) : 1.0f, -less);
+}
+
+// What is taken off a token that was emitted n times (bit 31: and is in the prompt).  +0 leaves every x as it is.
+__device__ __forceinline__ float taken_off(int32_t n, float bias, const Penalties& p) {
+  const int32_t emitted = n & 0x7FFFFFFF;
+  return (emitted > 0 ? fmaf(p.frequency, static_cast<float>(emitted), p.presence) : 0.0f) - bias;
+}
+
+__device__ __forceinline__ void load_counts(const LogitsArgs& a, int64_t b, int32_t col, int32_t cols, int32_t (&n)[kCols]) {
+  // (16-byte vectors that start inside a row are read whole)
+  const int4* src = reinterpret_cast<const int4*>(a.counts + b * a.counts_ld + col);
+  const int4 zero = make_int4(0, 0, 0, 0);
+  const int4 x = a.counts == nullptr ? zero : src[0], y = a.counts == nullptr || cols <= 4 ? zero : src[1];
+  n[0] = x.x, n[1] = x.y, n[2] = x.z, n[3] = x.w, n[4] = y.x, n[5] = y.y, n[6] = y.z, n[7] = y.w;
+}
+__device__ __forceinline__ void load_bias(const LogitsArgs& a, int64_t b, int32_t col, int32_t cols, float (&f)[kCols]) {
+  const float4* src = reinterpret_cast<const float4*>(a.bias + b * a.bias_ld + col);
+  const float4 zero = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+  const float4 x = a.bias == nullptr ? zero : src[0], y = a.bias == nullptr || cols <= 4 ? zero : src[1];
+  f[0] = x.x, f[1] = x.y, f[2] = x.z, f[3] = x.w, f[4] = y.x, f[5] = y.y, f[6] = y.z, f[7] = y.w;
+}
+
+__device__ __forceinline__ void store_cols(uint16_t* dst, const uint4& w, int32_t cols) {
+  if (cols == kCols) {
+    *reinterpret_cast<uint4*>(dst) = w;
+    return;
+  }
+  const uint16_t* e = reinterpret_cast<const uint16_t*>(&w);
+#pragma unroll
+  for (int i = 0; i < kCols; ++i)
+    if (i < cols) dst[i] = e[i];
+}
+
+// The vector with -inf where `may` has a 0.
+__device__ __forceinline__ uint4 masked(uint4 w, uint32_t may, uint32_t full) {
+  if (may == full) return w;
+  if (may == 0) return make_uint4(kNone, kNone, kNone, kNone);
+  uint32_t* e = &w.x;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    if (!(may >> (2 * i) & 1u)) e[i] = (e[i] & 0xFFFF0000u) | 0xFF80u;
+    if (!(may >> (2 * i + 1) & 1u)) e[i] = (e[i] & 0x0000FFFFu) | 0xFF800000u;
+  }
+  return w;
+}
+
+// Whether node t sees node s.
+__device__ __forceinline__ bool node_sees(const LogitsArgs& a, int64_t b, int32_t t, int32_t s) {
+  if (a.mask == nullptr) return s <= t;
+  return a.mask[(b * a.T + t) * ((a.T + 63) >> 6) + (s >> 6)] >> (s & 63) & 1ull;
+}
+
+__global__ void __launch_bounds__(kThreads, 4) logits_adjust_kernel(const __grid_constant__ LogitsArgs a, int32_t blocks_per_seq) {
+  extern __shared__ uint32_t masks[];     // [T][kBlockWords], the CTA's columns
   __shared__ Draft drafts[kMaxNodes];
-  __shared__ int32_t num_drafts;
+  __shared__ uint16_t listed[kThreads];   // vectors that hold a token to be adjusted; bit 15: a drafted one
+  __shared__ int32_t num_drafts, num_listed;
   const int64_t b = blockIdx.x / blocks_per_seq;
   const int32_t block = blockIdx.x % blocks_per_seq, c0 = block * kBlockCols;
-  const int32_t col = c0 + threadIdx.x * kCols;
-  const bool inplace = a.out == a.logits;
-  if (threadIdx.x == 0) num_drafts = 0;
+  const int32_t tid = threadIdx.x, lane = tid & 31;
+  const bool inplace = a.out == a.logits, restricted = a.allowed != nullptr;
+  if (tid == 0) num_drafts = num_listed = 0;
   pdl_wait();
   pdl_launch_dependents();
+  if (restricted) {
+    const int32_t words = min(kBlockWords, ((a.V + 31) >> 5) - c0 / 32);
+    const uint32_t* from = a.allowed + b * a.allowed_b + c0 / 32;
+#pragma unroll 4
+    for (int32_t x = tid; x < a.T * kBlockWords; x += kThreads)
+      masks[x] = x % kBlockWords < words ? from[x / kBlockWords * a.allowed_t + x % kBlockWords] : 0u;
+  }
+  const uint8_t* may_of = reinterpret_cast<const uint8_t*>(masks);      // of node t, vector v: [t * kThreads + v]
+  const int32_t col = c0 + tid * kCols, cols = min(kCols, a.V - col);
+  bool some = false, drafted = false;   // whether the thread's own vector is adjusted at every node, or has a drafted token
+  if (cols > 0) {
+    int32_t count[kCols];
+    float bias[kCols];
+    load_counts(a, b, col, cols, count);
+    load_bias(a, b, col, cols, bias);
+    uint32_t any = 0, any_bias = 0;
+#pragma unroll
+    for (int i = 0; i < kCols; ++i) {
+      any |= static_cast<uint32_t>(count[i]);
+      any_bias |= __float_as_uint(bias[i]);
+    }
+    some = (any | (any_bias & 0x7FFFFFFFu)) != 0;
+  }
+  __syncthreads();
   if (a.tokens != nullptr) {
-    __syncthreads();
-    if (threadIdx.x < a.T) {
-      const int32_t tok = a.tokens[b * a.T + threadIdx.x];
+    if (tid < a.T) {
+      const int32_t tok = a.tokens[b * a.T + tid];
       if (tok < 0 || tok >= a.V) {
         if (block == 0) raise_error(a.err, DFLASH2_DEVERR_BAD_TOKEN);
       } else if (tok >= c0 && tok < c0 + kBlockCols) {
-        drafts[atomicAdd(&num_drafts, 1)] = {static_cast<int16_t>(tok - c0), static_cast<int16_t>(threadIdx.x)};
+        drafts[atomicAdd(&num_drafts, 1)] = {static_cast<int16_t>(tok - c0), static_cast<int16_t>(tid)};
+      }
+    }
+    __syncthreads();
+  }
+  for (int i = 0; i < num_drafts; ++i) drafted |= drafts[i].col / kCols == tid;
+  const bool mine = some || drafted;
+  const uint32_t who = __ballot_sync(0xFFFFFFFFu, mine);
+  int32_t at = 0;
+  if (lane == 0 && who != 0) at = atomicAdd(&num_listed, __popc(who));
+  at = __shfl_sync(0xFFFFFFFFu, at, 0) + __popc(who & ((1u << lane) - 1));
+  if (mine) listed[at] = static_cast<uint16_t>(tid | (drafted ? 0x8000 : 0));
+
+  __syncthreads();
+
+  const uint16_t* src = a.logits + b * a.x_b;
+  uint16_t* dst = a.out + b * a.out_b;
+  // The listed vector that the thread adjusts, at every `step`th node: its first rows are under way while the
+  // thread's own vector is copied or masked.
+  const int32_t n = num_listed, step = n > 0 ? kThreads / n : 1, first = n > 0 ? tid / n : a.T;
+  const bool busy = first < step && first < a.T;
+  const uint32_t which = busy ? listed[tid - first * n] : 0u;
+  const int32_t vec = which & 0x7FFF, vec_col = c0 + vec * kCols, vec_cols = min(kCols, a.V - vec_col);
+  const uint32_t vec_full = (1u << vec_cols) - 1;
+  uint32_t may[kRows];
+  uint4 w[kRows];
+  const auto fetch = [&](int32_t t0) {
+#pragma unroll
+    for (int y = 0; y < kRows; ++y) {
+      const int32_t t = t0 + y * step;
+      may[y] = t >= a.T ? 0u : restricted ? may_of[t * kThreads + vec] & vec_full : vec_full;
+      w[y] = make_uint4(0, 0, 0, 0);
+      if (may[y] != 0) w[y] = *reinterpret_cast<const uint4*>(src + t * a.x_t + vec_col);
+    }
+  };
+  if (busy) fetch(first);
+
+  if (!mine && cols > 0) {
+    const uint32_t full = (1u << cols) - 1;
+    if (inplace) {
+      // nothing is read but the masks: a vector of which some columns stay is written column by column
+      uint16_t* to = dst + col;
+#pragma unroll 4
+      for (int32_t t = 0; restricted && t < a.T; ++t, to += a.out_t) {
+        const uint32_t may = may_of[t * kThreads + tid] & full;
+        if (may == 0 && cols == kCols) {
+          *reinterpret_cast<uint4*>(to) = make_uint4(kNone, kNone, kNone, kNone);
+        } else if (may != full) {
+#pragma unroll
+          for (int i = 0; i < kCols; ++i)
+            if (!(may >> i & 1u) && i < cols) to[i] = static_cast<uint16_t>(kNone);
+        }
+      }
+    } else {
+      for (int32_t t0 = 0; t0 < a.T; t0 += kCopyRows) {
+        uint32_t may[kCopyRows];
+        uint4 w[kCopyRows];
+#pragma unroll
+        for (int y = 0; y < kCopyRows; ++y) {
+          const int32_t t = t0 + y;
+          may[y] = t >= a.T ? 0u : restricted ? may_of[t * kThreads + tid] & full : full;
+          w[y] = make_uint4(0, 0, 0, 0);
+          if (may[y] != 0) w[y] = *reinterpret_cast<const uint4*>(src + t * a.x_t + col);
+        }
+#pragma unroll
+        for (int y = 0; y < kCopyRows; ++y)
+          if (t0 + y < a.T) store_cols(dst + (t0 + y) * a.out_t + col, masked(w[y], may[y], full), cols);
       }
     }
   }
-  __syncthreads();
-  if (col >= a.V) return;
-  const int32_t cols = min(kCols, a.V - col);
+  if (!busy) return;
 
-  int32_t count[kCols] = {};
-  float bias[kCols] = {};
-  bool some = false;                    // whether any of the columns changes at every node
-  if (a.counts != nullptr) {            // (16-byte vectors that start inside a row are read whole)
-    const int4* src = reinterpret_cast<const int4*>(a.counts + b * a.counts_ld + col);
-    const int4 x = src[0], y = cols > 4 ? src[1] : make_int4(0, 0, 0, 0);
-    count[0] = x.x, count[1] = x.y, count[2] = x.z, count[3] = x.w;
-    count[4] = y.x, count[5] = y.y, count[6] = y.z, count[7] = y.w;
-  }
-  if (a.bias != nullptr) {
-    const float4* src = reinterpret_cast<const float4*>(a.bias + b * a.bias_ld + col);
-    const float4 x = src[0], y = cols > 4 ? src[1] : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-    bias[0] = x.x, bias[1] = x.y, bias[2] = x.z, bias[3] = x.w;
-    bias[4] = y.x, bias[5] = y.y, bias[6] = y.z, bias[7] = y.w;
-  }
+  Penalties p;
+  p.repetition = a.repetition == nullptr ? 1.0f : a.repetition[b];
+  p.inverse = 1.0f / p.repetition;
+  p.frequency = a.frequency == nullptr ? 0.0f : a.frequency[b];
+  p.presence = a.presence == nullptr ? 0.0f : a.presence[b];
+  int32_t count[kCols];
+  float bias[kCols], less[kCols];
+  load_counts(a, b, vec_col, vec_cols, count);
+  load_bias(a, b, vec_col, vec_cols, bias);
+  uint32_t known = 0;
 #pragma unroll
-  for (int i = 0; i < kCols; ++i) some |= (count[i] != 0 || bias[i] != 0.0f) && i < cols;
-  bool drafted = false;                 // whether one of the columns is a node's token
-  for (int i = 0; i < num_drafts; ++i) drafted |= drafts[i].col >> 3 == threadIdx.x;
-  const float repetition = a.repetition == nullptr ? 1.0f : a.repetition[b];
-  const float frequency = a.frequency == nullptr ? 0.0f : a.frequency[b];
-  const float presence = a.presence == nullptr ? 0.0f : a.presence[b];
-  const uint8_t* allowed = a.allowed == nullptr
-                               ? nullptr
-                               : reinterpret_cast<const uint8_t*>(a.allowed + b * a.allowed_b) + (col >> 3);
-  const uint16_t* src = a.logits + b * a.x_b + col;
-  uint16_t* dst = a.out + b * a.out_b + col;
-  const uint32_t full = (1u << cols) - 1;
-
-  for (int32_t t0 = 0; t0 < a.T; t0 += kRows) {
-    uint32_t may[kRows];
-    uint4 w[kRows];
-    bool change[kRows];
-#pragma unroll
-    for (int y = 0; y < kRows; ++y)
-      may[y] = t0 + y < a.T && allowed != nullptr ? allowed[(t0 + y) * a.allowed_t * 4] & full : full;
+  for (int i = 0; i < kCols; ++i) {
+    less[i] = taken_off(count[i], bias[i], p);
+    known |= count[i] != 0 ? 1u << i : 0u;
+  }
+#pragma unroll 1
+  for (int32_t t0 = first;;) {
 #pragma unroll
     for (int y = 0; y < kRows; ++y) {
-      change[y] = some || drafted || may[y] != full;
-      w[y] = make_uint4(0, 0, 0, 0);
-      if (t0 + y < a.T && may[y] != 0 && (change[y] || !inplace))
-        w[y] = *reinterpret_cast<const uint4*>(src + (t0 + y) * a.x_t);
-    }
+      const int32_t t = t0 + y * step;
+      if (t >= a.T) break;
+      if (may[y] != 0) {
+        float off[kCols];
+        uint32_t knows = known;
 #pragma unroll
-    for (int y = 0; y < kRows; ++y) {
-      const int32_t t = t0 + y;
-      if (t >= a.T || (inplace && !change[y])) continue;
-      if (change[y]) {
-        int32_t n[kCols];
+        for (int i = 0; i < kCols; ++i) off[i] = less[i];
+        if (which & 0x8000u) {
+          load_counts(a, b, vec_col, vec_cols, count);
+          load_bias(a, b, vec_col, vec_cols, bias);
+          for (int i = 0; i < num_drafts; ++i) {
+            const Draft d = drafts[i];
+            if (d.col / kCols != vec || !node_sees(a, b, t, d.node)) continue;
+            knows |= 1u << (d.col & (kCols - 1));
 #pragma unroll
-        for (int i = 0; i < kCols; ++i) n[i] = count[i];
-        if (drafted) {
-          uint64_t sees[2];
-          if (a.mask == nullptr) {
-            sees[0] = t >= 63 ? ~0ull : (2ull << t) - 1;
-            sees[1] = t < 64 ? 0ull : t >= 127 ? ~0ull : (2ull << (t - 64)) - 1;
-          } else {
-            const int words = (a.T + 63) >> 6;
-            const uint64_t* m = a.mask + (b * a.T + t) * words;
-            sees[0] = m[0];
-            sees[1] = words > 1 ? m[1] : 0ull;
+            for (int k = 0; k < kCols; ++k) count[k] += (d.col & (kCols - 1)) == k ? 1 : 0;
           }
-          for (int i = 0; i < num_drafts; ++i)
-            if (drafts[i].col >> 3 == threadIdx.x && (sees[drafts[i].node >> 6] >> (drafts[i].node & 63) & 1ull)) {
 #pragma unroll
-              for (int k = 0; k < kCols; ++k) n[k] += (drafts[i].col & 7) == k ? 1 : 0;
-            }
+          for (int i = 0; i < kCols; ++i) off[i] = taken_off(count[i], bias[i], p);
         }
         uint32_t* e = &w[y].x;
 #pragma unroll
-        for (int i = 0; i < kCols; i += 2) {
-          float x[2] = {__uint_as_float(e[i / 2] << 16), __uint_as_float(e[i / 2] & 0xFFFF0000u)};
-#pragma unroll
-          for (int k = 0; k < 2; ++k) {
-            if (n[i + k] != 0) {
-              const int32_t emitted = n[i + k] & 0x7FFFFFFF;
-              x[k] = x[k] > 0.0f ? x[k] / repetition : x[k] * repetition;
-              if (emitted > 0) x[k] = x[k] - frequency * static_cast<float>(emitted) - presence;
-            }
-            if (bias[i + k] != 0.0f) x[k] += bias[i + k];
-            if (!(may[y] >> (i + k) & 1u)) x[k] = -INFINITY;
-          }
-          e[i / 2] = pack(x[0], x[1]);
-        }
+        for (int i = 0; i < kCols; i += 2)
+          e[i / 2] = pack(adjusted(__uint_as_float(e[i / 2] << 16), knows >> i & 1u, off[i], p),
+                          adjusted(__uint_as_float(e[i / 2] & 0xFFFF0000u), knows >> (i + 1) & 1u, off[i + 1], p));
       }
-      if (cols == kCols) {
-        *reinterpret_cast<uint4*>(dst + t * a.out_t) = w[y];
-      } else {
-        const uint16_t* e = reinterpret_cast<const uint16_t*>(&w[y]);
-#pragma unroll
-        for (int i = 0; i < kCols; ++i)
-          if (i < cols) dst[t * a.out_t + i] = e[i];
-      }
+      store_cols(dst + t * a.out_t + vec_col, masked(w[y], may[y], vec_full), vec_cols);
     }
+    t0 += kRows * step;
+    if (t0 >= a.T) return;
+    fetch(t0);
   }
 }
 
@@ -185,6 +301,7 @@ cudaError_t launch_logits_adjust(const LogitsArgs& a, int, cudaStream_t stream) 
   cfg.gridDim = dim3(static_cast<unsigned>(a.B * blocks), 1, 1);
   cfg.blockDim = dim3(kThreads, 1, 1);
   cfg.stream = stream;
+  cfg.dynamicSmemBytes = a.allowed != nullptr ? static_cast<size_t>(a.T) * kBlockWords * 4 : 0;   // at most 32 KB
   cfg.attrs = &attr;
   cfg.numAttrs = 1;
   return cudaLaunchKernelEx(&cfg, logits_adjust_kernel, a, static_cast<int32_t>(blocks));
