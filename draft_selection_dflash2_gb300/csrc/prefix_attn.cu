@@ -5,38 +5,73 @@
 // split axis (exp's sums with their maxima): the keys of the group's shared positions, as
 // whole tiles of 128, for the query rows of all its sequences' nodes, stacked; and each
 // sequence's own keys from there on (the shared positions after the last whole tile among
-// them) with the drafted nodes.  Both are stretches of items (kv head, pair of row tiles) in
-// one list, the prefixes first.  All their units, weighed by what they cost, are cut into
-// equal runs, one per CTA, so that the few long items of a prefix and the many short ones of
-// the sequences fill the GPU together: the former is bound by the tensor cores, the latter by memory.
-//   prefix_plan_kernel   one CTA: the list, with the cost of everything before each stretch
-//   tree_attn_kernel     kShared: every item's sums to the workspace
-//   prefix_join_kernel   a warp per row of the output: adds its parts, own keys first, in order
-// The same inputs give the same bits on every call.
+// them) with the drafted nodes.  Each of these is a stretch of items: per kv head, pairs of row
+// tiles, and where their number is odd a single one.  The units (key tiles) of all pairs are
+// one list and those of all single tiles another; each list is cut into equal runs, so that the
+// few long items of a prefix and the many short ones of the sequences fill the GPU together,
+// the former bound by the tensor cores, the latter by memory.
+//   prefix_list_kernel   one CTA: the stretches, with the units of everything before each;
+//                        up to kListed of them the next kernel's producers list for themselves
+//   prefix_attn_kernel   every item's sums to the workspace
+//   prefix_join_kernel   adds every row's parts, own keys first, in order
+//
+// prefix_attn_kernel has the roles of tree_attn_kernel (producer, S products, O products and
+// softmax of two pipelines).  A CTA takes a run of the pairs, each pipeline one row tile of every
+// item, and two runs of the single tiles, one for each pipeline, whose units alternate in the
+// ring: a short item is a chain of latencies (keys, S, softmax, O, its sums' way out), and two
+// at once hide each other's.  The same inputs give the same bits on every call.
 #include "tree_attn.cuh"
 
 namespace dflash2 {
 namespace {
 
-constexpr int kPlanThreads = 1024;
+constexpr int kListThreads = 1024;
+constexpr int kListed = 32;              // most stretches that producers list for themselves, a lane each
+constexpr int kSegs = 4;                 // segments that a pipeline's warps may lag behind the producer
 
-struct PrefixPlan {
-  PrefixArgs a;
-  int32_t tpt;
-  int32_t* shared;          // [groups] shared positions, clamped to the lengths of the group's sequences
-  Stretch* stretches;       // [groups + B + 1]
+// A group's shared prefix, seen by all nodes of its sequences, or what one sequence has of its own.
+struct Stretch {
+  uint32_t before[2];       // cost of the stretches before this one: of their pairs, and of their single row tiles
+  int32_t n;                // units of an item (0: no items)
+  int32_t b;                // the sequence whose keys these are, and its first node's sequence
+  int32_t nodes;
+  int32_t tile0, len;       // first key tile, and the end of the cached keys
 };
 
-__device__ __forceinline__ int32_t group_start(const PrefixArgs& a, int32_t g) {
-  return a.start != nullptr ? a.start[g] : g == 0 ? 0 : static_cast<int32_t>(a.attn.B);
+struct PrefixPlan {
+  AttnArgs a;               // q_t: from one node to the next, through all sequences
+  const int32_t* start;
+  const int32_t* shared_len;
+  int32_t groups;
+  int32_t tpt;              // nodes per row tile
+  int32_t num_stretches;    // groups, then sequences
+  float c;                  // scale * log2(e)
+  int32_t box_rows;         // rows of a K or V box
+  uint32_t q_box_bytes;
+  int32_t* shared;          // [groups] shared positions; and the stretches, where CTAs do not list them
+  Stretch* stretches;       // [num_stretches + 1]
+  // every row's first part, of its own keys and of its prefix, by row of the output: O [rows][D], and (m, l, where the other
+  // parts are, whether there is a prefix)
+  float* first_o[2];
+  float4* first_ml[2];
+  // the other parts, one place a run: 2 * runs places of pairs (one per tile), then 2 * runs of halves of runs of single tiles
+  float* part;              // [4 * runs][128][D]
+  float2* part_ml;          // [4 * runs][128]
+};
+
+// ---------------------------------------------------------------------------
+// the list of stretches
+// ---------------------------------------------------------------------------
+__device__ __forceinline__ int32_t group_start(const PrefixPlan& p, int32_t g) {
+  return p.start != nullptr ? p.start[g] : g == 0 ? 0 : static_cast<int32_t>(p.a.B);
 }
 
 // The group of sequence b (the starts ascend from 0 to B).
-__device__ __forceinline__ int32_t group_of(const PrefixArgs& a, int32_t b) {
-  int32_t lo = 0, hi = a.groups;
+__device__ __forceinline__ int32_t group_of(const PrefixPlan& p, int32_t b) {
+  int32_t lo = 0, hi = p.groups;
   while (hi - lo > 1) {
     const int32_t mid = (lo + hi) >> 1;
-    if (group_start(a, mid) <= b)
+    if (group_start(p, mid) <= b)
       lo = mid;
     else
       hi = mid;
@@ -44,112 +79,857 @@ __device__ __forceinline__ int32_t group_of(const PrefixArgs& a, int32_t b) {
   return lo;
 }
 
-__global__ void __launch_bounds__(kPlanThreads) prefix_plan_kernel(const PrefixPlan p) {
-  __shared__ uint32_t warp_sum[kPlanThreads / 32];
-  const PrefixArgs& a = p.a;
-  const AttnArgs& t = a.attn;
-  const int32_t B = static_cast<int32_t>(t.B), tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  pdl_wait();
-  pdl_launch_dependents();
+// Exclusive sums over a warp's lanes, and the warp's total.
+__device__ __forceinline__ uint64_t warp_before(uint64_t x, uint64_t* total) {
+  uint64_t incl = x;
+#pragma unroll
+  for (int d = 1; d < 32; d <<= 1) {
+    const uint64_t o = __shfl_up_sync(0xFFFFFFFFu, incl, d);
+    if ((threadIdx.x & 31) >= static_cast<unsigned>(d)) incl += o;
+  }
+  *total = __shfl_sync(0xFFFFFFFFu, incl, 31);
+  return incl - x;
+}
+
+// What a unit takes, and an item beyond its units, of pairs and of single tiles, in 1/8 us with all SMs at work (the units
+// of pairs are bound by the tensor cores, of single tiles, two at a time, by memory).  Between an item's units starts are a unit
+// apart, and a run of single tiles is cut in halves: a run has to be as long as two of their units and as one of the pairs'.
+enum List { kPairs = 0, kSingles = 1 };
+constexpr uint32_t kLeastRun = 40;
+__device__ __forceinline__ uint32_t unit_cost(List which) { return which == kPairs ? 17 : 10; }
+__device__ __forceinline__ uint32_t ahead_cost(List which) { return which == kPairs ? 24 : 16; }
+__device__ __forceinline__ uint32_t item_cost(List which, int32_t n) { return n * unit_cost(which) + ahead_cost(which); }
+
+// The costs of a stretch's pairs (upper half) and single row tiles.
+__device__ __forceinline__ uint64_t cost_of(const PrefixPlan& p, const Stretch& s) {
+  if (s.n == 0) return 0;
+  const uint32_t tiles = static_cast<uint32_t>((s.nodes + p.tpt - 1) / p.tpt), heads = p.a.cache.heads;
+  return static_cast<uint64_t>(item_cost(kPairs, s.n) * heads * (tiles >> 1)) << 32 |
+         item_cost(kSingles, s.n) * heads * (tiles & 1);
+}
+
+__device__ __forceinline__ Stretch prefix_stretch(const PrefixPlan& p, int32_t s0, int32_t s1, int32_t tiles) {
+  return {{0, 0}, tiles, s0, (s1 - s0) * p.a.T, 0, tiles * kTile};
+}
+__device__ __forceinline__ Stretch own_stretch(const PrefixPlan& p, int32_t b, int32_t tile0, int32_t len) {
+  return {{0, 0}, max(1, (len + kTile - 1) / kTile - tile0 + (p.a.k_new != nullptr ? 1 : 0)), b, p.a.T, tile0, len};
+}
+
+// Lists up to 32 stretches with one warp, a lane each.  Small calls run this with an empty instruction cache, so it
+// is short, and its loads do not wait for one another.
+__device__ __forceinline__ void list_few(const PrefixPlan& p, Stretch* list, bool flag) {
+  const AttnArgs& a = p.a;
+  uint32_t* err = flag ? a.err : nullptr;
+  const int32_t B = static_cast<int32_t>(a.B), lane = threadIdx.x & 31, b = lane - p.groups;
+  const bool is_group = lane < p.groups, is_own = !is_group && b < B;
+  int32_t s0 = 0, s1 = 0, len = 0x7FFFFFFF, most = 0;
+  if (is_group) {
+    s0 = group_start(p, lane);
+    s1 = group_start(p, lane + 1);
+    most = kv_clamp(p.shared_len[lane], a.cache.capacity, err);
+  }
+  if (is_own) len = kv_clamp(a.cache_len[b], a.cache.capacity, err);
+  bool bad = is_group && (s0 < 0 || s1 < s0 || s1 > B || (lane == 0 && s0 != 0) || (lane == p.groups - 1 && s1 != B));
+  bad = __any_sync(0xFFFFFFFFu, bad);                  // starts that are none: nothing is shared
+  Stretch s = {};
+  int32_t tile0 = 0;
+#pragma unroll 1
+  for (int32_t g = 0; g < (bad ? 0 : p.groups); ++g) {
+    const int32_t g0 = __shfl_sync(0xFFFFFFFFu, s0, g), g1 = __shfl_sync(0xFFFFFFFFu, s1, g);
+    const int32_t limit = __shfl_sync(0xFFFFFFFFu, most, g);
+    const bool member = is_own && b >= g0 && b < g1;
+    const int32_t least = min(limit, __reduce_min_sync(0xFFFFFFFFu, member ? len : 0x7FFFFFFF));
+    bad |= least < limit;
+    const int32_t tiles = g1 - g0 < 2 ? 0 : least / kTile;   // a sequence by itself shares nothing
+    if (lane == g) s = prefix_stretch(p, s0, s1, tiles);
+    if (member) tile0 = tiles;
+  }
+  if (bad && lane == 0) raise_error(err, DFLASH2_DEVERR_BAD_LENGTH);
+  if (is_own) s = own_stretch(p, b, tile0, len);
+  uint64_t total;
+  const uint64_t before = warp_before(cost_of(p, s), &total);
+  s.before[0] = static_cast<uint32_t>(before >> 32);
+  s.before[1] = static_cast<uint32_t>(before);
+  list[lane] = s;                                      // (lanes past the last stretch hold the totals)
+  if (lane == 0) {
+    s = {};
+    s.before[0] = static_cast<uint32_t>(total >> 32);
+    s.before[1] = static_cast<uint32_t>(total);
+    list[p.num_stretches] = s;
+  }
+  __syncwarp();
+}
+
+// Lists any number, with one block.
+__device__ __forceinline__ void list_many(const PrefixPlan& p, int32_t* shared, Stretch* list, uint64_t* warp_sum) {
+  const AttnArgs& a = p.a;
+  const int32_t B = static_cast<int32_t>(a.B), tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int32_t capacity = a.cache.capacity;
   bool bad = false;
-  for (int32_t g = tid; g < a.groups; g += kPlanThreads) {
-    const int32_t s0 = group_start(a, g), s1 = group_start(a, g + 1);
-    bad |= s0 < 0 || s1 < s0 || s1 > B || (g == 0 && s0 != 0) || (g == a.groups - 1 && s1 != B);
-    p.shared[g] = kv_clamp(a.len[g], t.cache.capacity, t.err);
+  for (int32_t g = tid; g < p.groups; g += kListThreads) {
+    const int32_t s0 = group_start(p, g), s1 = group_start(p, g + 1);
+    bad |= s0 < 0 || s1 < s0 || s1 > B || (g == 0 && s0 != 0) || (g == p.groups - 1 && s1 != B);
+    shared[g] = kv_clamp(p.shared_len[g], capacity, a.err);
   }
   // starts that are none: nothing is shared
-  const bool none = __syncthreads_or(bad) != 0 || a.groups == 0;
-  if (none && a.groups > 0 && tid == 0) raise_error(t.err, DFLASH2_DEVERR_BAD_LENGTH);
-  if (!none)
-    for (int32_t b = tid; b < B; b += kPlanThreads) {
-      const int32_t g = group_of(a, b), len = kv_clamp(t.cache_len[b], t.cache.capacity, t.err);
-      if (len < p.shared[g]) {        // (only ever lowered: whatever is read here, the least one stays)
-        raise_error(t.err, DFLASH2_DEVERR_BAD_LENGTH);
-        atomicMin(&p.shared[g], len);
-      }
+  const bool none = __syncthreads_or(bad) != 0 || p.groups == 0;
+  if (none && p.groups > 0 && tid == 0) raise_error(a.err, DFLASH2_DEVERR_BAD_LENGTH);
+  for (int32_t b = tid; b < B; b += kListThreads) {
+    const int32_t len = kv_clamp(a.cache_len[b], capacity, a.err);
+    if (none) continue;
+    const int32_t g = group_of(p, b);
+    if (len < shared[g]) {          // (only ever lowered: whatever is read here, the least one stays)
+      raise_error(a.err, DFLASH2_DEVERR_BAD_LENGTH);
+      atomicMin(&shared[g], len);
     }
+  }
   __syncthreads();
   // shared tiles of a group: a sequence by itself shares nothing
   const auto tiles_of = [&](int32_t g) {
-    return none || group_start(a, g + 1) - group_start(a, g) < 2 ? 0 : *static_cast<volatile int32_t*>(&p.shared[g]) / kTile;
+    return none || group_start(p, g + 1) - group_start(p, g) < 2 ? 0 : *static_cast<volatile int32_t*>(&shared[g]) / kTile;
   };
-  uint32_t before = 0;
-  for (int32_t v0 = 0; v0 < a.groups + B; v0 += kPlanThreads) {
+  uint64_t before = 0;
+  for (int32_t v0 = 0; v0 <= p.num_stretches; v0 += kListThreads) {
     const int32_t v = v0 + tid;
     Stretch s = {};
-    if (v < a.groups) {
-      s.n = tiles_of(v);
-      s.b = none ? 0 : group_start(a, v);
-      s.node0 = s.b * t.T;
-      s.nodes = none ? 0 : (group_start(a, v + 1) - s.b) * t.T;
-      s.len = s.n * kTile;
-    } else if (v < a.groups + B) {
-      s.b = v - a.groups;
-      s.node0 = s.b * t.T;
-      s.nodes = t.T;
-      s.tile0 = none ? 0 : tiles_of(group_of(a, s.b));
-      s.len = kv_clamp(t.cache_len[s.b], t.cache.capacity, none ? t.err : nullptr);
-      s.n = max(1, (s.len + kTile - 1) / kTile - s.tile0 + (t.k_new != nullptr ? 1 : 0));
-      s.own = 1;
-    }
-    const uint32_t tiles = static_cast<uint32_t>((s.nodes + p.tpt - 1) / p.tpt);
-    const uint32_t cost = static_cast<uint32_t>(s.n) * t.cache.heads * (kPair * (tiles >> 1) + kSingle * (tiles & 1));
-    uint32_t incl = cost;
-#pragma unroll
-    for (int d = 1; d < 32; d <<= 1) {
-      const uint32_t o = __shfl_up_sync(0xFFFFFFFFu, incl, d);
-      if (lane >= d) incl += o;
-    }
-    if (lane == 31) warp_sum[warp] = incl;
+    if (v < p.groups && !none)
+      s = prefix_stretch(p, group_start(p, v), group_start(p, v + 1), tiles_of(v));
+    else if (v >= p.groups && v < p.num_stretches)
+      s = own_stretch(p, v - p.groups, none ? 0 : tiles_of(group_of(p, v - p.groups)),
+                      kv_clamp(a.cache_len[v - p.groups], capacity, nullptr));
+    uint64_t total, sums;
+    uint64_t at = before + warp_before(cost_of(p, s), &total);
+    if (lane == 0) warp_sum[warp] = total;
     __syncthreads();
-    uint32_t sum = warp_sum[lane];       // 32 warps
-#pragma unroll
-    for (int d = 1; d < 32; d <<= 1) {
-      const uint32_t o = __shfl_up_sync(0xFFFFFFFFu, sum, d);
-      if (lane >= d) sum += o;
-    }
-    const uint32_t warps_before = __shfl_sync(0xFFFFFFFFu, sum, (warp + 31) & 31);
-    s.cost = before + (warp > 0 ? warps_before : 0) + incl - cost;
-    if (v < a.groups + B) p.stretches[v] = s;
-    before += __shfl_sync(0xFFFFFFFFu, sum, 31);
+    const uint64_t warps = warp_before(warp_sum[lane], &sums);
+    at += __shfl_sync(0xFFFFFFFFu, warps, warp);
+    before += sums;
+    s.before[0] = static_cast<uint32_t>(at >> 32);
+    s.before[1] = static_cast<uint32_t>(at);
+    if (v <= p.num_stretches) list[v] = s;
     __syncthreads();
-  }
-  if (tid == 0) {
-    Stretch s = {};
-    s.cost = before;
-    p.stretches[a.groups + B] = s;
   }
 }
 
-constexpr int kJoinThreads = 256;
-
-template <int D>
-__global__ void __launch_bounds__(kJoinThreads) prefix_join_kernel(const __grid_constant__ AttnPlan p, int32_t groups) {
-  constexpr int E = D / 32;              // columns of a lane
-  const AttnArgs& a = p.a;
-  const int lane = threadIdx.x & 31;
-  const int64_t row = static_cast<int64_t>(blockIdx.x) * (kJoinThreads / 32) + (threadIdx.x >> 5);
+__global__ void __launch_bounds__(kListThreads) prefix_list_kernel(const __grid_constant__ PrefixPlan p) {
+  __shared__ uint64_t warp_sum[kListThreads / 32];   // 32 warps
   pdl_wait();
   pdl_launch_dependents();
-  if (row >= a.B * a.T * a.heads) return;
-  const bool shared = p.stretches[groups + row / (static_cast<int64_t>(a.T) * a.heads)].tile0 > 0;
+  list_many(p, p.shared, p.stretches, warp_sum);
+}
+
+// ---------------------------------------------------------------------------
+// walking a run
+// ---------------------------------------------------------------------------
+// One item's part of a run.
+struct SharedSegment {
+  int32_t b, h, pair;       // `pair`: the first of its row tiles is 2 * pair
+  int32_t s, e, n;          // units [s, e) of n
+  int32_t tiles;            // row tiles
+  int32_t tile0, len, node0, nodes;
+  uint32_t others;          // the item's runs, the first one and the last one (10 bits each); bit 28: single tiles
+  int32_t place;            // of its own part, if that is not the item's first
+  bool own;
+  uint32_t ring;            // the ring's unit that is unit s; single tiles' are every second one
+  __device__ __forceinline__ uint32_t ring_unit(int u) const { return ring + (tiles == 1 ? 2 : 1) * (u - s); }
+  __device__ __forceinline__ int position(int u) const { return (tile0 + u) * kTile; }
+  __device__ __forceinline__ int num_nodes(const AttnArgs&) const { return nodes; }
+  __device__ __forceinline__ int64_t node(const AttnArgs&, int t) const { return static_cast<int64_t>(node0) + t; }
+  __device__ __forceinline__ int64_t q_row(const AttnArgs& a, int t) const { return node(a, t) * a.q_t; }
+  __device__ __forceinline__ bool drafted(const AttnArgs& a, int u) const { return own && a.k_new != nullptr && u == n - 1; }
+  __device__ __forceinline__ int keys(const AttnArgs& a, int u) const {
+    return drafted(a, u) ? a.T : max(0, min(kTile, len - position(u)));
+  }
+};
+
+// Where a segment's sums go: an item's first part by row of the output, another to its run's place.
+template <int D>
+struct SharedPlace {
+  static constexpr bool whole = false;
+  static constexpr int kStep = 1;
+  const SharedSegment& g;
+  __device__ __forceinline__ SharedPlace(const PrefixPlan&, const SharedSegment& g, const uint8_t*) : g(g) {}
+  __device__ __forceinline__ float4* part(const PrefixPlan& p, int tile, int r, int64_t orow) const {
+    float* at = g.s == 0 ? p.first_o[g.own ? 0 : 1] + orow * D : p.part + (static_cast<int64_t>(g.place + tile) * kTile + r) * D;
+    return reinterpret_cast<float4*>(at);
+  }
+  __device__ __forceinline__ void put_ml(const PrefixPlan& p, int tile, int r, int64_t orow, float m, float l) const {
+    if (g.s == 0)
+      p.first_ml[g.own ? 0 : 1][orow] = make_float4(
+          m, l, __uint_as_float(g.others | static_cast<uint32_t>(tile * kTile + r) << 20), g.tile0 > 0 ? 1.0f : 0.0f);
+    else
+      p.part_ml[static_cast<int64_t>(g.place + tile) * kTile + r] = make_float2(m, l);
+  }
+};
+
+// How the work is cut: all pairs' items and then all single tiles' are one line of costs, and a unit belongs to the run, one
+// per CTA and all of one length, in which it starts; a run of single tiles to the halves, one for each pipeline.  So
+// between an item's first and last part every run, and every half, has one.
+struct Cuts {
+  uint32_t pairs, all, half;     // the pairs' cost, everybody's, and half a run
+  __device__ __forceinline__ Cuts(const Stretch* list, const PrefixPlan& p, uint32_t runs) {
+    pairs = list[p.num_stretches].before[kPairs];
+    all = pairs + list[p.num_stretches].before[kSingles];
+    half = (max((all + runs - 1) / runs, kLeastRun) + 1) / 2;
+  }
+};
+
+// Walks the segments of one run (whole warps call it).
+struct RunOfList {
+  const Stretch* list;
+  uint32_t at, end;         // costs, from the list's first item on: where the next item's first unit starts; the run's end
+  int32_t v, item, s;       // the next one: stretch (-1: none), item of its items, unit
+  int32_t place;
+  List which;
+  __device__ __forceinline__ uint32_t unit_cost() const { return dflash2::unit_cost(which); }
+  __device__ __forceinline__ uint32_t ahead() const { return ahead_cost(which); }
+  // The units of the list that start at costs [from, to); parts that are no item's first go to place `where`.
+  __device__ __forceinline__ void start(const PrefixPlan& p, const Stretch* l, List w, uint32_t from, uint32_t to, int32_t where) {
+    list = l;
+    which = w;
+    place = where;
+    end = to;
+    v = -1;
+    if (from >= to) return;
+    // the last stretch that begins at or before `from`: 32 places of the range at a time
+    const int lane = threadIdx.x & 31;
+    int32_t lo = 0, hi = p.num_stretches;
+    while (hi - lo > 1) {
+      const int32_t step = (hi - lo + 31) >> 5, x = lo + lane * step;
+      const uint32_t before = __ballot_sync(0xFFFFFFFFu, x < hi && l[x].before[w] <= from);
+      lo += (31 - __clz(before)) * step;               // (lane 0's place is always before)
+      hi = min(hi, lo + step);
+    }
+    v = lo;
+    const uint32_t rel = from - l[v].before[w], cost = item_cost(w, l[v].n);
+    item = static_cast<int32_t>(rel / cost);
+    const uint32_t in_item = rel - item * cost;
+    s = in_item <= ahead() ? 0 : static_cast<int32_t>((in_item - ahead() + unit_cost() - 1) / unit_cost());   // (n: all before)
+    at = from - in_item + ahead();
+    settle(p);
+  }
+  __device__ __forceinline__ int32_t tiles_of(const PrefixPlan& p, const Stretch& st) const {
+    return (st.nodes + p.tpt - 1) / p.tpt;
+  }
+  // Moves on to an item that has units left, and to none where the next unit is not the run's.
+  __device__ __forceinline__ void settle(const PrefixPlan& p) {
+    if (s == list[v].n) {
+      at += s * unit_cost() + ahead();
+      s = 0;
+      ++item;
+      for (;;) {
+        if (at >= end) break;
+        const int32_t tiles = tiles_of(p, list[v]);
+        if (list[v].n > 0 && item < p.a.cache.heads * (which == kPairs ? tiles >> 1 : tiles & 1)) break;
+        item = 0;
+        ++v;
+      }
+    }
+    if (at + s * unit_cost() >= end) v = -1;
+  }
+  __device__ __forceinline__ bool more() const { return v >= 0; }
+  // The next segment (more() holds).
+  __device__ __forceinline__ void next(const PrefixPlan& p, const Cuts& cuts, SharedSegment* g) {
+    const Stretch st = list[v];
+    const int32_t tiles = tiles_of(p, st), per_head = which == kPairs ? tiles >> 1 : 1;
+    g->s = s;
+    g->n = st.n;
+    g->e = static_cast<int32_t>(min(static_cast<uint32_t>(st.n), (end - at + unit_cost() - 1) / unit_cost()));
+    g->b = st.b;
+    g->h = item / per_head;
+    g->pair = which == kPairs ? item - g->h * per_head : tiles >> 1;
+    g->tiles = which == kPairs ? 2 : 1;
+    g->tile0 = st.tile0;
+    g->len = st.len;
+    g->node0 = st.b * p.a.T;
+    g->nodes = st.nodes;
+    g->own = v >= p.groups;
+    const uint32_t last = at + (st.n - 1) * unit_cost();
+    if (which == kPairs)
+      g->others = at / (2 * cuts.half) | last / (2 * cuts.half) << 10;
+    else
+      g->others = (cuts.pairs + at) / cuts.half | (cuts.pairs + last) / cuts.half << 10 | 1u << 28;
+    g->place = place;
+    s = g->e;
+    settle(p);
+  }
+};
+
+// The CTA's run of the pairs (x = 2), or half x of its run of single tiles.
+__device__ __forceinline__ void start_run(const PrefixPlan& p, const Stretch* list, const Cuts& cuts, uint32_t x, RunOfList* run) {
+  const uint32_t cta = blockIdx.x, from = cuts.half * (2 * cta + (x == 1 ? 1 : 0)), to = from + cuts.half * (x == 2 ? 2 : 1);
+  if (x == 2)
+    run->start(p, list, kPairs, min(from, cuts.pairs), min(to, cuts.pairs), 2 * cta);
+  else
+    run->start(p, list, kSingles, max(min(from, cuts.all), cuts.pairs) - cuts.pairs,
+               max(min(to, cuts.all), cuts.pairs) - cuts.pairs, 2 * gridDim.x + 2 * cta + x);
+}
+
+template <int S>
+__device__ __forceinline__ RingPos<S> ring_pos(uint32_t tile) {
+  RingPos<S> at;
+  at.slot = tile % S;
+  at.use = tile / S;
+  return at;
+}
+
+struct PrefixSmem {
+  uint64_t kv_full[2 * kMaxSlots], kv_empty[kMaxSlots];
+  uint64_t q_full[2], q_empty[2];     // of each pipeline
+  uint64_t s_full[2][kBufs], p_ready[2][kBufs], pv_done[2][kBufs], drain;
+  uint64_t seg_full[2][kSegs], seg_empty[2][kSegs];
+  uint64_t seen[3];                   // threads that have seen to a drafted tile: of each pipeline, or of both
+  SharedSegment seg[2][kSegs];        // each pipeline's segments; tiles = 0: no more
+  Stretch list[kListed + 1];
+  uint32_t segs[2], q_issued[2];   // each pipeline's segments so far, and their queries' copies (the producer's)
+  uint32_t bad[3][4];       // drafted nodes that hold a non-finite value: of each pipeline's tile, or of both
+  uint32_t tmem;
+  int abort_flag;
+  int odd;                  // whether some row's sums have to be taken again
+};
+
+// A run under way: its segment, and the next of that segment's units.
+struct Feed {
+  RunOfList run;
+  const SharedSegment* g;
+  int u, e;
+  int32_t page;             // the lane's page of the next unit, fetched while the one before it is loaded
+  __device__ __forceinline__ bool more() const { return u < e || run.more(); }
+};
+
+// The producer warp: walks the CTA's runs, hands every segment to the pipelines that it is for, and loads its
+// queries, keys and values.  The other warps take segments from shared memory: with walks of their own the softmax spilled
+// registers, and local memory is slow where shared memory takes nearly all of the L1 (1.6 times the time of a long context).
+// There is one copy of all this, whichever run and pipeline it is for: the kernel's warps run different code, and
+// have to share the instruction cache (with a copy for each the kernel was 150 KB, and what is run once an item took 4 us).
+template <int D>
+struct Producer {
+  static constexpr int S = Cfg<D>::kSlots;
+  const PrefixPlan& p;
+  const CUtensorMap *q, *k, *v, *kn, *vn;
+  uint8_t *q_smem, *ring;
+  PrefixSmem& s;
+  int lane;
+  bool live = true;
+  uint32_t tiles = 0, issued = 0;       // tiles of the ring so far, and up to the last one whose copies were started
+
+  // Hands pipeline i the segment g, whose first unit is the ring's next one, and loads its queries.  (After a wait that gave up
+  // nothing is written any more.)
+  __device__ __forceinline__ const SharedSegment* hand(int i, SharedSegment g) {
+    const uint32_t x = s.segs[i];
+    SharedSegment* to = &s.seg[i][x % kSegs];
+    if (x >= kSegs) wait_live(&s.seg_empty[i][x % kSegs], (x / kSegs - 1) & 1, &live, &s.abort_flag, p.a.err);
+    live = __all_sync(0xFFFFFFFFu, live);
+    if (lane == 0 && live) {
+      g.ring = tiles / 2;
+      *to = g;
+      s.segs[i] = x + 1;
+      mbar_arrive(&s.seg_full[i][x % kSegs]);
+    }
+    __syncwarp();
+    if (g.tiles == 0) return to;
+    if (x > 0) wait_live(&s.q_empty[i], (x - 1) & 1, &live, &s.abort_flag, p.a.err);
+    live = __all_sync(0xFFFFFFFFu, live);
+    if (lane == 0 && live) {
+      s.q_issued[i] = x + 1;
+      mbar_arrive_expect_tx(&s.q_full[i], p.q_box_bytes);
+#pragma unroll
+      for (int c = 0; c < Cfg<D>::kHalves; ++c)
+        tma_load_5d(q_smem + i * Cfg<D>::kTileBytes + c * kTile * 128, q, c * 64, 0,
+                    g.node0 + (2 * g.pair + (g.tiles == 2 ? i : 0)) * p.tpt, g.h, 0, &s.q_full[i]);
+    }
+    __syncwarp();
+    return to;
+  }
+  // The page of the lane's rows of unit u: as it stands in the table.
+  __device__ __forceinline__ int32_t page_of(const SharedSegment& g, int u) const {
+    const KvView& c = p.a.cache;
+    const int j = g.position(u) + lane / Cfg<D>::kHalves * p.box_rows;
+    return c.table == nullptr || j >= g.len || j >= g.position(u) + kTile ? 0 : c.table[g.b * c.table_ld + (j >> c.page_shift)];
+  }
+  __device__ __forceinline__ void load_unit(Feed& f) {
+    const AttnArgs& a = p.a;
+    const SharedSegment& g = *f.g;
+    // lane -> (page piece of the tile, column block)
+    const int half = lane % Cfg<D>::kHalves, row = lane / Cfg<D>::kHalves * p.box_rows;   // the first row of the lane's box
+    const int u = f.u++;
+    const bool drafted = g.drafted(a, u);
+    int y = g.position(u) + row, w = g.b;
+    bool has = row < kTile && y < g.len;
+    uint32_t bytes = p.box_rows * 128;
+    if (drafted) {
+      has = lane < Cfg<D>::kHalves;
+      bytes = kTile * 128;
+      y = 0;
+    } else if (a.cache.table != nullptr) {
+      y &= a.cache.page_size - 1;
+      w = f.page;
+      if (static_cast<uint32_t>(w) >= static_cast<uint32_t>(a.cache.num_pages)) {
+        if (has) raise_error(a.err, DFLASH2_DEVERR_BAD_PAGE);
+        w = w < 0 ? 0 : a.cache.num_pages - 1;
+      }
+      if (f.u < f.e) f.page = page_of(g, f.u);
+    }
+    const uint32_t boxes = __popc(__ballot_sync(0xFFFFFFFFu, has));
+#pragma unroll 1
+    for (int kv = 0; kv < 2; ++kv, ++tiles) {
+      const RingPos<S> at = ring_pos<S>(tiles);
+      if (at.use > 0) wait_live(&s.kv_empty[at.slot], (at.use - 1) & 1, &live, &s.abort_flag, a.err);
+      live = __all_sync(0xFFFFFFFFu, live);
+      if (!live) continue;
+      issued = tiles + 1;
+      uint64_t* full = at.full(s.kv_full);
+      if (lane == 0) mbar_arrive_expect_tx(full, boxes * bytes);
+      __syncwarp();
+      if (has)
+        tma_load_4d(ring + at.slot * Cfg<D>::kTileBytes + half * kTile * 128 + (drafted ? 0 : row * 128),
+                    drafted ? (kv ? vn : kn) : (kv ? v : k), half * 64, y, g.h, w, full);
+    }
+  }
+  // Passes over a unit of the ring.
+  __device__ __forceinline__ void skip_unit() {
+#pragma unroll 1
+    for (int kv = 0; kv < 2; ++kv, ++tiles) {
+      const RingPos<S> at = ring_pos<S>(tiles);
+      if (at.use > 0) wait_live(&s.kv_empty[at.slot], (at.use - 1) & 1, &live, &s.abort_flag, p.a.err);
+      live = __all_sync(0xFFFFFFFFu, live);
+      if (live) issued = tiles + 1;
+      if (lane == 0 && live) {
+        mbar_arrive(at.full(s.kv_full));
+        mbar_arrive(&s.kv_empty[at.slot]);
+        mbar_arrive(&s.kv_empty[at.slot]);
+      }
+      __syncwarp();
+    }
+  }
+  // The CTA's runs: of the pairs, then both halves of the single tiles, whose units alternate in the ring (where one half
+  // has none left its turns are passed over); then the end.
+  __device__ __forceinline__ void run(const Stretch* list) {
+    const Cuts cuts(list, p, gridDim.x);
+#pragma unroll 1
+    for (int list_at = 0; live && list_at < 3; ++list_at) {
+      const bool end = list_at == 2, pairs = list_at == 0;
+      Feed f, other;        // f: pipeline i's, or both's
+      f.u = f.e = other.u = other.e = 0;
+      f.run.v = other.run.v = -1;
+#pragma unroll 1
+      for (int x = end ? 3 : pairs ? 2 : 0; x < (pairs ? 3 : 2); ++x) {
+        other = f;
+        start_run(p, list, cuts, x, &f.run);
+      }
+      int i = pairs ? 0 : 1;                    // (the second half was started last)
+      if (!pairs && !end) {
+        const Feed swap = f;
+        f = other;
+        other = swap;
+        i = 0;
+      }
+#pragma unroll 1
+      while (live && (end || f.more() || other.more())) {
+        if (end || (f.more() && f.u == f.e)) {
+          SharedSegment g = {};
+          if (!end) f.run.next(p, cuts, &g);
+#pragma unroll 1
+          for (int to = end || pairs ? 0 : i; to < (end || pairs ? 2 : i + 1); ++to) f.g = hand(to, g);
+          if (end) break;
+          f.u = g.s;
+          f.e = g.e;
+          f.page = page_of(g, g.s);
+        }
+        if (!live) break;
+        if (f.u < f.e)
+          load_unit(f);
+        else
+          skip_unit();
+        if (!pairs) {
+          const Feed swap = f;
+          f = other;
+          other = swap;
+          i ^= 1;
+        }
+      }
+    }
+  }
+};
+
+// The next segment of a pipeline, for one of its warps; nullptr: none.
+__device__ __forceinline__ const SharedSegment* next_segment(PrefixSmem& s, int i, uint32_t seg, bool* live, uint32_t* err) {
+  wait_live(&s.seg_full[i][seg % kSegs], seg / kSegs & 1, live, &s.abort_flag, err);
+  if (!__all_sync(0xFFFFFFFFu, *live)) return nullptr;
+  const SharedSegment* g = &s.seg[i][seg % kSegs];
+  return g->tiles > 0 ? g : nullptr;
+}
+// The warp has done with it.
+__device__ __forceinline__ void done_with(PrefixSmem& s, int i, uint32_t seg) {
+  __syncwarp();
+  if ((threadIdx.x & 31) == 0) mbar_arrive(&s.seg_empty[i][seg % kSegs]);
+}
+
+static_assert(Cfg<128>::kRing + sizeof(PrefixSmem) <= 232448, "shared memory");
+
+struct OneRun {
+  using Segment = SharedSegment;
+  template <int D>
+  using Place = SharedPlace<D>;
+  RunOfList run;
+  Cuts cuts;
+  __device__ __forceinline__ bool next(const PrefixPlan& p, SharedSegment* g) {
+    if (!run.more()) return false;
+    run.next(p, cuts, g);
+    return true;
+  }
+};
+
+// The CTA's rows whose sums are not finite.  Out of line: it is hardly ever called.
+template <int D>
+__device__ __noinline__ void take_again(const PrefixPlan& p, const Stretch* list) {
+  const Cuts cuts(list, p, gridDim.x);
+#pragma unroll 1
+  for (int x = 0; x < 3; ++x) {
+    OneRun run = {{}, cuts};
+    start_run(p, list, cuts, x, &run.run);
+    sum_again<D>(p, run, nullptr);
+  }
+}
+
+template <int D>
+__global__ void __launch_bounds__(kThreads, 1)
+    prefix_attn_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmK,
+                       const __grid_constant__ CUtensorMap tmV, const __grid_constant__ CUtensorMap tmKn,
+                       const __grid_constant__ CUtensorMap tmVn, const __grid_constant__ PrefixPlan p) {
+  using C = Cfg<D>;
+  constexpr int S = C::kSlots;
+  extern __shared__ __align__(1024) uint8_t q_smem[];   // no static shared memory: the base is 1024-byte aligned
+  uint8_t* ring = q_smem + 2 * C::kTileBytes;
+  PrefixSmem& s = *reinterpret_cast<PrefixSmem*>(q_smem + C::kRing);
+  const AttnArgs& a = p.a;
+  const int warp = uniform(static_cast<int>(threadIdx.x >> 5)), lane = threadIdx.x & 31;
+  volatile int* abort_flag = &s.abort_flag;
+
+  if (threadIdx.x == 0) {
+    for (int i = 0; i < S; ++i) {
+      mbar_init(&s.kv_full[2 * i], 1);
+      mbar_init(&s.kv_full[2 * i + 1], 1);
+      mbar_init(&s.kv_empty[i], 2);
+    }
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(&s.q_full[i], 1);
+      mbar_init(&s.q_empty[i], 1);
+      for (int buf = 0; buf < kBufs; ++buf) {
+        mbar_init(&s.s_full[i][buf], 1);
+        mbar_init(&s.p_ready[i][buf], kTile);
+        mbar_init(&s.pv_done[i][buf], 1);
+      }
+    }
+    for (int i = 0; i < 2; ++i)
+      for (int x = 0; x < kSegs; ++x) {
+        mbar_init(&s.seg_full[i][x], 1);
+        mbar_init(&s.seg_empty[i][x], 6);      // its two product warps and four softmax warps
+      }
+    mbar_init(&s.seen[0], kTile);
+    mbar_init(&s.seen[1], kTile);
+    mbar_init(&s.seen[2], 2 * kTile);
+    mbar_init(&s.drain, 4);
+    for (int i = 0; i < 2; ++i) s.segs[i] = s.q_issued[i] = 0;
+    s.abort_flag = 0;
+    s.odd = 0;
+    fence_mbar_init();
+    tma_prefetch_desc(&tmQ);
+    tma_prefetch_desc(&tmK);
+    tma_prefetch_desc(&tmV);
+    tma_prefetch_desc(&tmKn);
+    tma_prefetch_desc(&tmVn);
+  }
+  if (warp == 0) {
+    tmem_alloc(&s.tmem, 512);
+    tmem_relinquish();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = uniform(s.tmem);
+  pdl_wait();
+  pdl_launch_dependents();
+  const Stretch* list = p.num_stretches <= kListed ? s.list : p.stretches;
+  bool live = true;
+
+  if (warp == 0) {
+    // ---- producer ----
+    if (p.num_stretches <= kListed) list_few(p, s.list, blockIdx.x == 0);
+    Producer<D> out = {p, &tmQ, &tmK, &tmV, &tmKn, &tmVn, q_smem, ring, s, lane};
+    out.run(list);
+    live = out.live;
+    // after a wait that gave up: this CTA's copies have landed before it exits (else the products have used them)
+    if (lane == 0 && !live) {
+      for (int i = 0; i < 2; ++i)
+        if (s.q_issued[i] > 0) mbar_wait_bounded(&s.q_full[i], (s.q_issued[i] - 1) & 1, a.err);
+      for (uint32_t j = out.issued > S ? out.issued - S : 0; j < out.issued; ++j) {
+        const RingPos<S> last = ring_pos<S>(j);
+        mbar_wait_bounded(last.full(s.kv_full), last.parity(), a.err);
+      }
+    }
+    __syncwarp();
+  } else if (warp <= 2) {
+    // ---- S products of pipeline i ----
+    const int i = warp - 1;
+    const uint32_t elected = elect_lane();
+    const uint32_t tm_s = tmem + i * kBufs * kChunk;
+    const uint32_t idesc = umma_idesc_bf16(128, kChunk);
+    const uint32_t ring_addr = uniform(smem_addr(ring)), q_lo = desc_lo(uniform(smem_addr(q_smem)) + i * C::kTileBytes);
+    BufPos at_s;       // the pipeline's next chunk
+    for (uint32_t seg = 0;; ++seg) {
+      const SharedSegment* at_g = next_segment(s, i, seg, &live, a.err);
+      if (at_g == nullptr) break;
+      const SharedSegment g = *at_g;
+      wait_live(&s.q_full[i], seg & 1, &live, abort_flag, a.err);
+      __syncwarp();
+      for (int u = g.s; u < g.e; ++u) {
+        const RingPos<S> at = ring_pos<S>(2 * g.ring_unit(u));
+        const int chunks = g.keys(a, u) <= kChunk ? 1 : 2;
+        const uint32_t k_lo = desc_lo(ring_addr + at.slot * C::kTileBytes);
+        wait_live(at.full(s.kv_full), at.parity(), &live, abort_flag, a.err);
+        for (int c = 0; c < chunks; ++c, at_s.advance()) {
+          const int buf = at_s.buf;
+          // P of the chunk that had the buffer lies in it until its product is done
+          if (at_s.use > 0) wait_live(&s.pv_done[i][buf], (at_s.use - 1) & 1, &live, abort_flag, a.err);
+          __syncwarp();
+          tc_fence_after();
+          const uint32_t lead = live ? elected : 0u;
+#pragma unroll
+          for (int k = 0; k < D / 16; ++k) {
+            const uint32_t o = ((k >> 2) * kTile * 128 + (k & 3) * 32) >> 4;
+            umma_ss(tm_s + buf * kChunk, q_lo + o, k_lo + ((c * kChunk * 128) >> 4) + o, idesc, k > 0 ? 1u : 0u, lead);
+          }
+          umma_commit_if(&s.s_full[i][buf], lead);
+        }
+        // a tile goes back after two releases: one per pipeline, or both by the one that has it to itself
+        const uint32_t lead = live ? elected : 0u;
+        umma_commit_if(&s.kv_empty[at.slot], lead);
+        if (g.tiles == 1) umma_commit_if(&s.kv_empty[at.slot], lead);
+        if (u == g.e - 1) umma_commit_if(&s.q_empty[i], lead);
+      }
+      done_with(s, i, seg);
+    }
+    umma_commit_if(&s.drain, elected);
+    __syncwarp();
+  } else if (warp == 3 || warp == 12) {
+    // ---- O products of pipeline i ----
+    const int i = warp == 3 ? 0 : 1;
+    const uint32_t elected = elect_lane();
+    const uint32_t tm_s = tmem + i * kBufs * kChunk, tm_o = tmem + kTmemO + i * D;
+    const uint32_t idesc = umma_idesc_bf16(128, D) | (1u << 16);   // B is MN-major
+    const uint32_t ring_addr = uniform(smem_addr(ring));
+    BufPos at_s;
+    for (uint32_t seg = 0;; ++seg) {
+      const SharedSegment* at_g = next_segment(s, i, seg, &live, a.err);
+      if (at_g == nullptr) break;
+      const SharedSegment g = *at_g;
+      for (int u = g.s; u < g.e; ++u) {
+        const RingPos<S> at = ring_pos<S>(2 * g.ring_unit(u) + 1);
+        const int chunks = g.keys(a, u) <= kChunk ? 1 : 2;
+        const uint32_t v_lo = desc_lo(ring_addr + at.slot * C::kTileBytes, kTile * 128);
+        for (int c = 0; c < chunks; ++c, at_s.advance()) {
+          const int buf = at_s.buf;
+          wait_live(&s.p_ready[i][buf], at_s.use & 1, &live, abort_flag, a.err);
+          if (c == 0) wait_live(at.full(s.kv_full), at.parity(), &live, abort_flag, a.err);
+          __syncwarp();
+          tc_fence_after();
+          const uint32_t lead = live ? elected : 0u;
+          const uint32_t v_c = v_lo + c * ((kChunk * 128) >> 4), tm_p = tm_s + buf * kChunk;
+#pragma unroll
+          for (int k = 0; k < kChunk / 16; ++k)
+            umma_ts(tm_o, tm_p + k * 8, v_c + k * (2048 >> 4), idesc, (u > g.s || c > 0 || k > 0) ? 1u : 0u, lead);
+#pragma unroll
+          for (int k = 0; k < kChunk / 16; ++k)
+            umma_ts(tm_o, tm_p + kChunk / 2 + k * 8, v_c + k * (2048 >> 4), idesc, 1u, lead);
+          umma_commit_if(&s.pv_done[i][buf], lead);
+        }
+        const uint32_t lead = live ? elected : 0u;
+        umma_commit_if(&s.kv_empty[at.slot], lead);
+        if (g.tiles == 1) umma_commit_if(&s.kv_empty[at.slot], lead);
+      }
+      done_with(s, i, seg);
+    }
+    umma_commit_if(&s.drain, elected);
+    __syncwarp();
+  } else if (warp >= 4 && warp < 12) {
+    // ---- softmax of pipeline i, one row per thread ----
+    const int i = warp >= 8 ? 1 : 0;
+    const int r = threadIdx.x & (kTile - 1);
+    const uint32_t lanes = static_cast<uint32_t>((warp & 3) * 32) << 16;
+    const uint32_t tm_s = tmem + i * kBufs * kChunk + lanes, tm_o = tmem + kTmemO + i * D + lanes;
+    BufPos at_s;       // the pipeline's next chunk
+    uint32_t met = 0;  // parities of the meetings over drafted tiles: the pipeline's own (bit 0), and both's (bit 1)
+    // What is needed once a unit is read from shared memory there: the loop over the chunks has no registers to spare.
+    const auto field = [](const int32_t& x) { return *const_cast<const volatile int32_t*>(&x); };
+    for (uint32_t seg = 0;; ++seg) {
+      const SharedSegment* at_g = next_segment(s, i, seg, &live, a.err);
+      if (at_g == nullptr) break;
+      const SharedSegment& g = *at_g;
+      const auto row_node = [&]() { return (2 * field(g.pair) + (field(g.tiles) == 2 ? i : 0)) * p.tpt + r / a.group; };
+      const bool row_ok = r < p.tpt * a.group && row_node() < field(g.nodes);
+      // a warp none of whose rows is a query's has nothing to do but to keep step
+      const bool busy = __any_sync(0xFFFFFFFFu, row_ok);
+      float m = -INFINITY, l = 0.0f;
+      bool bad_seen = false;          // whether a node that the row sees is non-finite
+      bool first = true;              // O is not begun yet
+      for (int u = field(g.s); u < field(g.e); ++u) {
+        int valid = kTile;            // keys of the unit; negative: drafted ones
+        wait_live(&s.s_full[i][at_s.buf], at_s.use & 1, &live, abort_flag, a.err);
+        if (u >= field(g.len) / kTile - field(g.tile0)) {
+          const bool drafted = g.drafted(a, u);
+          valid = g.keys(a, u);
+          const int chunks = valid <= kChunk ? 1 : 2;
+          if (drafted || valid < chunks * kChunk) {
+            const RingPos<S> at_v = ring_pos<S>(2 * g.ring_unit(u) + 1);
+            wait_live(at_v.full(s.kv_full), at_v.parity(), &live, abort_flag, a.err);
+            // the pipelines that take the drafted tile look through it together
+            const bool both = g.tiles == 2;
+            bad_seen |= see_tile<D>(a, ring + at_v.slot * C::kTileBytes, drafted, valid, chunks, g.b, row_node(), row_ok,
+                                    both ? static_cast<int>(threadIdx.x) - kTile : r, both ? 2 * kTile : kTile, r,
+                                    s.bad[both ? 2 : i], [&]() {
+                                      uint64_t* bar = &s.seen[both ? 2 : i];
+                                      mbar_arrive(bar);
+                                      wait_live(bar, met >> (both ? 1 : 0) & 1, &live, abort_flag, a.err);
+                                      met ^= both ? 2 : 1;
+                                    });
+          }
+          if (drafted) valid = -valid;
+        }
+        const int chunks = abs(valid) <= kChunk ? 1 : 2;
+#pragma unroll 1
+        for (int c = 0; c < chunks; ++c, at_s.advance()) {
+          const int buf = at_s.buf;
+          if (c > 0) wait_live(&s.s_full[i][buf], at_s.use & 1, &live, abort_flag, a.err);
+          __syncwarp();
+          tc_fence_after();
+          if (busy)
+            softmax_chunk<D>(tm_s + buf * kChunk, tm_o, p.c, valid < chunks * kChunk,
+                             [&](int w) { return seen_keys(a, valid < 0, abs(valid), g.b, row_node(), row_ok, 2 * c + w); },
+                             first, row_ok, &m, &l, [&]() {
+                               const BufPos prev = at_s.before();
+                               wait_live(&s.pv_done[i][prev.buf], prev.use & 1, &live, abort_flag, a.err);
+                             });
+          first = false;
+          tmem_st_wait();
+          tc_fence_before();
+          mbar_arrive(&s.p_ready[i][buf]);
+        }
+      }
+
+      // ---- the part's sums ----
+      // products complete in the order of their issue: the last one's is enough
+      const BufPos prev = at_s.before();
+      wait_live(&s.pv_done[i][prev.buf], prev.use & 1, &live, abort_flag, a.err);
+      __syncwarp();
+      tc_fence_after();
+      if (busy) {
+        const int tile = g.tiles == 2 ? i : 0;
+        const SharedPlace<D> place(p, g, ring);
+        const bool empty = l == 0.0f;   // the row saw nothing: 0, whatever the values were
+        const int64_t orow = g.node(a, row_node()) * a.heads + g.h * a.group + r % a.group;
+        if (row_ok) place.put_ml(p, tile, r, orow, m, l);
+        uint64_t odd[4] = {};           // 0, or NaN once an element of O is not finite (four chains of pairs)
+#pragma unroll 1
+        for (int x = 0; x < D; x += 32) {
+          float o[32];
+          __syncwarp();
+          tmem_ld_x32(tm_o + x, o);
+          tmem_ld_wait();
+          pin(o);
+          if (empty) {
+#pragma unroll
+            for (int y = 0; y < 32; ++y) o[y] = 0.0f;
+          }
+          if (bad_seen && !empty) o[0] = NAN;   // the row lacks the values of nodes that were zeroed
+#pragma unroll
+          for (int y = 0; y < 32; y += 2) odd[y / 2 & 3] = fma2(pack2(o[y], o[y + 1]), 0ull, odd[y / 2 & 3]);
+          if (row_ok) {
+            float4* dst = place.part(p, tile, r, orow) + x / 4;
+#pragma unroll
+            for (int y = 0; y < 32; y += 4) dst[y / 4] = make_float4(o[y], o[y + 1], o[y + 2], o[y + 3]);
+          }
+        }
+        const float2 odds = unpack2(add2(add2(odd[0], odd[1]), add2(odd[2], odd[3])));
+        if (odds.x + odds.y != 0.0f && row_ok && l == l) s.odd = 1;   // (with a NaN score the row is NaN throughout)
+      }
+      done_with(s, i, seg);
+      tc_fence_before();
+    }
+    named_bar_sync(1, 2 * kTile);
+    if (s.odd != 0) take_again<D>(p, list);
+  }
+
+  __syncthreads();
+  if (threadIdx.x == 0) mbar_wait_bounded(&s.drain, 0, a.err);   // the tensor cores have finished
+  __syncthreads();
+  if (warp == 0) {
+    tc_fence_after();
+    tmem_dealloc(tmem, 512);
+  }
+}
+
+// ---------------------------------------------------------------------------
+// the join
+// ---------------------------------------------------------------------------
+constexpr int kJoinThreads = 256, kJoinWarps = kJoinThreads / 32, kJoinBatch = 4;   // parts of a row fetched at once
+
+// A warp takes a row of the output, a lane D / 32 columns.  kSplit = kJoinWarps: a CTA's warps share out the parts of one row
+// and add their sums in order; for few rows, whose items were cut into many parts.
+template <int D, int kSplit>
+__global__ void __launch_bounds__(kJoinThreads) prefix_join_kernel(const __grid_constant__ PrefixPlan p, int32_t runs) {
+  constexpr int E = D / 32;              // columns of a lane
   struct alignas(4 * E) Cols {
     float v[E];
   };
+  const AttnArgs& a = p.a;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int64_t row = kSplit > 1 ? blockIdx.x : static_cast<int64_t>(blockIdx.x) * kJoinWarps + warp;
+  pdl_wait();
+  pdl_launch_dependents();
+  if (row >= a.B * a.T * a.heads) return;
   PartSum<E> sum;
+  // (without a prefix the second one holds anything and is not used)
+  const float4 first[2] = {p.first_ml[0][row], p.first_ml[1][row]};
+  const Cols o[2] = {*reinterpret_cast<const Cols*>(p.first_o[0] + row * D + lane * E),
+                     *reinterpret_cast<const Cols*>(p.first_o[1] + row * D + lane * E)};
 #pragma unroll
-  for (int which = 0; which < 2; ++which) {
-    if (which == 1 && !shared) break;
-    const float4 first = p.first_ml[which][row];
-    const Cols o = *reinterpret_cast<const Cols*>(p.first_o[which] + row * D + lane * E);
-    sum.add(first.x, first.y, o.v);
-    const uint32_t more = __float_as_uint(first.z);
-    const int32_t c1 = more >> 10 & 1023, at = more >> 20;
-    for (int32_t c = (more & 1023) + 1; c <= c1; ++c) {
-      const int64_t part = static_cast<int64_t>(c) * 2 * kTile + at;
-      const float2 ml = p.part_ml[part];
-      const Cols x = *reinterpret_cast<const Cols*>(p.part + part * D + lane * E);
-      sum.add(ml.x, ml.y, x.v);
+  for (int w = 0; w < 2; ++w) {
+    if (w == 1 && first[0].w == 0.0f) break;
+    if (kSplit == 1 || warp == 0) sum.add(first[w].x, first[w].y, o[w].v);
+    const uint32_t others = __float_as_uint(first[w].z);
+    const int32_t c1 = others >> 10 & 1023, at = others >> 20 & 255;
+    const bool single = others >> 28 & 1;
+#pragma unroll 1
+    for (int32_t c = (others & 1023) + 1 + (kSplit > 1 ? warp : 0); c <= c1; c += kJoinBatch * kSplit) {
+      float2 ml[kJoinBatch];
+      Cols part[kJoinBatch];
+#pragma unroll
+      for (int y = 0; y < kJoinBatch; ++y) {
+        const int32_t run = min(c + y * kSplit, c1);
+        const int64_t from = static_cast<int64_t>(single ? 2 * runs + run : 2 * run) * kTile + at;
+        ml[y] = p.part_ml[from];
+        part[y] = *reinterpret_cast<const Cols*>(p.part + from * D + lane * E);
+      }
+#pragma unroll
+      for (int y = 0; y < kJoinBatch; ++y)
+        if (c + y * kSplit <= c1) sum.add(ml[y].x, ml[y].y, part[y].v);
+    }
+  }
+  if constexpr (kSplit > 1) {
+    __shared__ float sums[kSplit][2 + E][32];
+    sums[warp][0][lane] = sum.m;
+    sums[warp][1][lane] = sum.odd ? -sum.l : sum.l;
+#pragma unroll
+    for (int k = 0; k < E; ++k) sums[warp][2 + k][lane] = sum.o[k];
+    __syncthreads();
+    if (warp > 0) return;
+#pragma unroll 1
+    for (int y = 1; y < kSplit; ++y) {
+      float more[E];
+#pragma unroll
+      for (int k = 0; k < E; ++k) more[k] = sums[y][2 + k][lane];
+      sum.add(sums[y][0][lane], sums[y][1][lane], more);
     }
   }
   sum.write(a, row, D, lane * E);
@@ -174,8 +954,8 @@ Layout layout(int64_t B, int64_t T, int64_t heads, int64_t head_dim, int num_sms
     l.first_o[i] = take(rows * head_dim * 4);
     l.first_ml[i] = take(rows * sizeof(float4));
   }
-  l.part = take(runs * 2 * kTile * head_dim * 4);
-  l.part_ml = take(runs * 2 * kTile * sizeof(float2));
+  l.part = take(runs * 4 * kTile * head_dim * 4);
+  l.part_ml = take(runs * 4 * kTile * sizeof(float2));
   l.bytes = at;
   return l;
 }
@@ -186,20 +966,19 @@ cudaError_t launch(const PrefixArgs& x, void* workspace, int num_sms, cudaStream
   const Layout l = layout(a.B, a.T, a.heads, D, num_sms);
   uint8_t* ws = static_cast<uint8_t*>(workspace);
   const Tiling t = tile_rows(a.T, a.group);
-  PrefixPlan plan;
-  plan.a = x;
-  plan.tpt = t.tpt;
-  plan.shared = reinterpret_cast<int32_t*>(ws + l.shared);
-  plan.stretches = reinterpret_cast<Stretch*>(ws + l.stretches);
-  AttnPlan p = {};
+  const int runs = static_cast<int>(imin64(num_sms, kMaxRuns));
+  PrefixPlan p;
   p.a = a;
+  p.start = x.start;
+  p.shared_len = x.len;
+  p.groups = x.groups;
   p.tpt = t.tpt;
-  p.areas = 2;
+  p.num_stretches = x.groups + static_cast<int32_t>(a.B);
   p.c = a.scale * 1.4426950408889634f;
   p.box_rows = box_rows(a.cache);
   p.q_box_bytes = static_cast<uint32_t>(t.tpt * a.group) * D * 2;
-  p.stretches = plan.stretches;
-  p.num_stretches = x.groups + static_cast<int32_t>(a.B);
+  p.shared = reinterpret_cast<int32_t*>(ws + l.shared);
+  p.stretches = reinterpret_cast<Stretch*>(ws + l.stretches);
   for (int i = 0; i < 2; ++i) {
     p.first_o[i] = reinterpret_cast<float*>(ws + l.first_o[i]);
     p.first_ml[i] = reinterpret_cast<float4*>(ws + l.first_ml[i]);
@@ -208,28 +987,32 @@ cudaError_t launch(const PrefixArgs& x, void* workspace, int num_sms, cudaStream
   p.part_ml = reinterpret_cast<float2*>(ws + l.part_ml);
   Maps m;
   if (!make_maps<D>(a, t.tpt, p.box_rows, a.B * a.T, 1, &m)) return cudaErrorInvalidValue;
-  const size_t smem = Cfg<D>::kRing + sizeof(AttnSmem);
-  cudaError_t e = set_smem_limit<tree_attn_kernel<D, kShared>>(smem);
+  const size_t smem = Cfg<D>::kRing + sizeof(PrefixSmem);
+  cudaError_t e = set_smem_limit<prefix_attn_kernel<D>>(smem);
   if (e != cudaSuccess) return e;
   cudaLaunchAttribute attr = pdl_attribute();
   cudaLaunchConfig_t cfg = {};
   cfg.stream = stream;
   cfg.attrs = &attr;
   cfg.numAttrs = 1;
-  cfg.gridDim = dim3(1, 1, 1);
-  cfg.blockDim = dim3(kPlanThreads, 1, 1);
-  e = cudaLaunchKernelEx(&cfg, prefix_plan_kernel, plan);
-  if (e != cudaSuccess) return e;
-  cfg.gridDim = dim3(static_cast<unsigned>(imin64(num_sms, kMaxRuns)), 1, 1);
+  if (p.num_stretches > kListed) {
+    cfg.gridDim = dim3(1, 1, 1);
+    cfg.blockDim = dim3(kListThreads, 1, 1);
+    e = cudaLaunchKernelEx(&cfg, prefix_list_kernel, p);
+    if (e != cudaSuccess) return e;
+  }
+  cfg.gridDim = dim3(runs, 1, 1);
   cfg.blockDim = dim3(kThreads, 1, 1);
   cfg.dynamicSmemBytes = smem;
-  e = cudaLaunchKernelEx(&cfg, tree_attn_kernel<D, kShared>, m.q, m.k, m.v, m.kn, m.vn, p);
+  e = cudaLaunchKernelEx(&cfg, prefix_attn_kernel<D>, m.q, m.k, m.v, m.kn, m.vn, p);
   if (e != cudaSuccess) return e;
-  const int64_t rows = a.B * a.T * a.heads, per_cta = kJoinThreads / 32;
-  cfg.gridDim = dim3(static_cast<unsigned>((rows + per_cta - 1) / per_cta), 1, 1);
+  const int64_t rows = a.B * a.T * a.heads;
+  const bool split = rows <= 8 * num_sms;
+  cfg.gridDim = dim3(static_cast<unsigned>(split ? rows : (rows + kJoinWarps - 1) / kJoinWarps), 1, 1);
   cfg.blockDim = dim3(kJoinThreads, 1, 1);
   cfg.dynamicSmemBytes = 0;
-  return cudaLaunchKernelEx(&cfg, prefix_join_kernel<D>, p, x.groups);
+  return split ? cudaLaunchKernelEx(&cfg, prefix_join_kernel<D, kJoinWarps>, p, static_cast<int32_t>(runs))
+               : cudaLaunchKernelEx(&cfg, prefix_join_kernel<D, 1>, p, static_cast<int32_t>(runs));
 }
 
 }  // namespace

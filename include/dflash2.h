@@ -507,7 +507,7 @@ int dflash2_tree_attention(dflash2_handle* h, const uint16_t* q, int64_t q_batch
  *   groups        0 .. B
  * The other arguments are dflash2_tree_attention's, with a workspace of its own size.  With B and T
  * above 1 q_batch_stride is T * q_token_stride.  cache->heads * (capacity / 128 + 2) * (2 B + B * (pairs of 128 query rows per kv
- * head) + B * T / (2 * (nodes of a row tile))) < 2^27.  What a row does not see never reaches it, and infinite or NaN
+ * head) + B * T / (2 * (nodes of a row tile))) < 2^26, B * T * heads < 2^26.  What a row does not see never reaches it, and infinite or NaN
  * values reach the rows that see them, as there.  The same inputs give the same bits on every call.
  */
 size_t dflash2_prefix_attention_workspace(const dflash2_handle* h, int64_t B, int64_t T, int64_t heads,
