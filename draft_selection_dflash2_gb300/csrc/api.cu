@@ -439,18 +439,11 @@ int dflash2_prefix_attention(dflash2_handle* h, const uint16_t* q, int64_t q_bat
                                      out, lse, workspace, &a))
     return st;
   if (B == 0 || T == 0) return DFLASH2_OK;
-  if (dflash2::prefix_attn_units(B, T, a.group, cache->heads, a.cache.capacity) >= (int64_t(1) << 26) ||
-      B * T * heads >= (int64_t(1) << 26))
-    return DFLASH2_ERR_UNSUPPORTED;
-  // the nodes of a group's sequences are rows of one operand
-  if (B > 1 && T > 1 && a.q_b != T * a.q_t) return DFLASH2_ERR_UNSUPPORTED;
   if (!aligned(prefix_len, 4) || !aligned(prefix_start, 4)) return DFLASH2_ERR_MISALIGNED;
   if (ws_bytes < dflash2::prefix_attn_workspace_bytes(B, T, heads, cache->heads, cache->head_dim, h->num_sms) ||
       workspace == nullptr)
     return DFLASH2_ERR_WORKSPACE;
   if (const int st = wrong_device(h)) return st;
-  if (T == 1) a.q_t = a.q_b;
-  a.q_b = a.q_t;
   x.start = prefix_start;
   x.len = prefix_len;
   x.groups = static_cast<int32_t>(groups);

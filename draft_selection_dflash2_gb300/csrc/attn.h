@@ -72,7 +72,7 @@ struct EvictArgs {
 };
 
 struct PrefixArgs {
-  AttnArgs attn;                  // q_t: from one node to the next, through all sequences
+  AttnArgs attn;
   const int32_t* start;           // [groups + 1] first sequence of each group; nullptr: one group
   const int32_t* len;             // [groups] shared positions
   int32_t groups;
@@ -82,8 +82,6 @@ struct PrefixArgs {
 int64_t tree_attn_units(int64_t B, int64_t T, int64_t group, int64_t kv_heads, int64_t capacity);
 size_t tree_attn_workspace_bytes(int64_t B, int64_t T, int64_t heads, int64_t kv_heads, int64_t head_dim, int num_sms);
 cudaError_t launch_tree_attn(const AttnArgs& a, int64_t head_dim, void* workspace, int num_sms, cudaStream_t stream);
-// The same with shared prefixes: fewer than 2^26.
-int64_t prefix_attn_units(int64_t B, int64_t T, int64_t group, int64_t kv_heads, int64_t capacity);
 size_t prefix_attn_workspace_bytes(int64_t B, int64_t T, int64_t heads, int64_t kv_heads, int64_t head_dim, int num_sms);
 cudaError_t launch_prefix_attn(const PrefixArgs& a, int64_t head_dim, void* workspace, int num_sms, cudaStream_t stream);
 cudaError_t launch_cache_scores(const ScoresArgs& a, int64_t head_dim, int num_sms, cudaStream_t stream);

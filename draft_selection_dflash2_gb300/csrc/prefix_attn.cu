@@ -26,6 +26,7 @@ namespace dflash2 {
 namespace {
 
 constexpr int kListThreads = 1024;
+constexpr int64_t kMostUnits = int64_t(1) << 26, kMostRows = int64_t(1) << 26;
 constexpr int kListed = 32;              // most stretches that producers list for themselves, a lane each
 constexpr int kSegs = 4;                 // segments that a pipeline's warps may lag behind the producer
 
@@ -95,9 +96,9 @@ __device__ __forceinline__ uint64_t warp_before(uint64_t x, uint64_t* total) {
 // of pairs are bound by the tensor cores, of single tiles, two at a time, by memory).  Between an item's units starts are a unit
 // apart, and a run of single tiles is cut in halves: a run has to be as long as two of their units and as one of the pairs'.
 enum List { kPairs = 0, kSingles = 1 };
-constexpr uint32_t kLeastRun = 40;
-__device__ __forceinline__ uint32_t unit_cost(List which) { return which == kPairs ? 17 : 10; }
-__device__ __forceinline__ uint32_t ahead_cost(List which) { return which == kPairs ? 24 : 16; }
+constexpr uint32_t kLeastRun = 22;
+__device__ __forceinline__ uint32_t unit_cost(List which) { return which == kPairs ? 17 : 11; }
+__device__ __forceinline__ uint32_t ahead_cost(List which) { return which == kPairs ? 24 : 20; }
 __device__ __forceinline__ uint32_t item_cost(List which, int32_t n) { return n * unit_cost(which) + ahead_cost(which); }
 
 // The costs of a stretch's pairs (upper half) and single row tiles.
@@ -962,7 +963,9 @@ Layout layout(int64_t B, int64_t T, int64_t heads, int64_t head_dim, int num_sms
 
 template <int D>
 cudaError_t launch(const PrefixArgs& x, void* workspace, int num_sms, cudaStream_t stream) {
-  const AttnArgs& a = x.attn;
+  AttnArgs a = x.attn;
+  if (a.T == 1) a.q_t = a.q_b;       // from one node to the next, through all sequences
+  a.q_b = a.q_t;
   const Layout l = layout(a.B, a.T, a.heads, D, num_sms);
   uint8_t* ws = static_cast<uint8_t*>(workspace);
   const Tiling t = tile_rows(a.T, a.group);
@@ -1015,19 +1018,38 @@ cudaError_t launch(const PrefixArgs& x, void* workspace, int num_sms, cudaStream
                : cudaLaunchKernelEx(&cfg, prefix_join_kernel<D, 1>, p, static_cast<int32_t>(runs));
 }
 
-}  // namespace
 
-int64_t prefix_attn_units(int64_t B, int64_t T, int64_t group, int64_t kv_heads, int64_t capacity) {
-  const Tiling t = tile_rows(T, group);
-  // the prefixes' row tiles: those of all nodes together, and one more for each group
-  return kv_heads * (capacity / kTile + 2) * (B * t.pairs + (B * T + t.tpt - 1) / t.tpt / 2 + B + 1);
+// Whether a call is taken as tree attention, which reads every sequence's keys for itself: where the nodes of a
+// group's sequences are no rows of one operand, where the costs would not fit 32 bits, and where sharing cannot
+// save what it costs.  A unit of one sequence's tiles takes 1.1 us (one row tile) or 2.1 (a pair), and its share of
+// a prefix's full pairs 2.1 us * rows / 256; at most all tiles of all sequences but one of each group are saved.  The lengths
+// are on the device, so the capacity stands for them.  Measured on 60 calls (saved at most, tree attention against this, us): 1.7: 12.1
+// and 16.5; 3.4: 19.0 and 17.0; 4.0: 28.7 and 38.6; 5.5: 23.1 and 19.5; 10.8: 24.4 and 19.7; 21: 48.6 and 31.9; 52: 94 and 32.5;
+// the worst above 5 was 17 groups of few or no shared tiles, 28: 52.6 and 57.8.
+bool as_tree_attn(const PrefixArgs& x, int num_sms) {
+  const AttnArgs& a = x.attn;
+  if (a.B > 1 && a.T > 1 && a.q_b != a.T * a.q_t) return true;
+  const Tiling t = tile_rows(a.T, a.group);
+  const int64_t tiles = a.cache.capacity / kTile + 2, heads = a.cache.heads;
+  // a stretch's items and units, the prefixes' row tiles being those of all nodes and one more a group
+  if (heads * tiles * (a.B * t.pairs + (a.B * a.T + t.tpt - 1) / t.tpt / 2 + a.B + 1) >= kMostUnits || a.B * a.T * a.heads >= kMostRows)
+    return true;
+  const double unit = 2.1 * (t.row_tiles / 2) + 1.1 * (t.row_tiles % 2) - 2.1 / (2 * kTile) * static_cast<double>(a.T) * a.group;
+  return static_cast<double>((a.B - x.groups) * heads * tiles) * unit < 5.0 * num_sms;
 }
 
+}  // namespace
+
 size_t prefix_attn_workspace_bytes(int64_t B, int64_t T, int64_t heads, int64_t kv_heads, int64_t head_dim, int num_sms) {
-  return heads / kv_heads > kTile ? 0 : layout(B, T, heads, head_dim, num_sms).bytes;
+  if (heads / kv_heads > kTile) return 0;
+  const size_t tree = tree_attn_workspace_bytes(B, T, heads, kv_heads, head_dim, num_sms);
+  if (B * T * heads >= kMostRows) return tree;
+  const size_t shared = layout(B, T, heads, head_dim, num_sms).bytes;
+  return shared > tree ? shared : tree;
 }
 
 cudaError_t launch_prefix_attn(const PrefixArgs& a, int64_t head_dim, void* workspace, int num_sms, cudaStream_t stream) {
+  if (as_tree_attn(a, num_sms)) return launch_tree_attn(a.attn, head_dim, workspace, num_sms, stream);
   return head_dim == 64 ? launch<64>(a, workspace, num_sms, stream) : launch<128>(a, workspace, num_sms, stream);
 }
 

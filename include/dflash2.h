@@ -505,10 +505,11 @@ int dflash2_tree_attention(dflash2_handle* h, const uint16_t* q, int64_t q_batch
  *   prefix_start  device int32 [groups + 1], ascending from 0 to B; otherwise flagged as well, and every sequence is
  *                 taken by itself.  NULL: groups is at most 1, the whole batch
  *   groups        0 .. B
- * The other arguments are dflash2_tree_attention's, with a workspace of its own size.  With B and T
- * above 1 q_batch_stride is T * q_token_stride.  cache->heads * (capacity / 128 + 2) * (2 B + B * (pairs of 128 query rows per kv
- * head) + B * T / (2 * (nodes of a row tile))) < 2^26, B * T * heads < 2^26.  What a row does not see never reaches it, and infinite or NaN
- * values reach the rows that see them, as there.  The same inputs give the same bits on every call.
+ * The other arguments and their limits are dflash2_tree_attention's, with a workspace of its own size.  A call
+ * for which sharing cannot pay, by its sizes and the cache's capacity, is taken as dflash2_tree_attention, and
+ * prefix_len and prefix_start are then not looked at (nor flagged); so is one whose q_batch_stride is not
+ * T * q_token_stride (with B and T above 1), and one with B * T * heads >= 2^26.  What a row does not see never reaches it,
+ * and infinite or NaN values reach the rows that see them, as there.  The same inputs give the same bits on every call.
  */
 size_t dflash2_prefix_attention_workspace(const dflash2_handle* h, int64_t B, int64_t T, int64_t heads,
                                           int64_t kv_heads, int64_t head_dim);

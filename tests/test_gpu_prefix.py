@@ -21,11 +21,18 @@ def i32(a):
     return torch.tensor(a, dtype=torch.int32, device="cuda")
 
 
-def shared_cache(gen, groups, H, D, page, capacity, layout="nhd", spoil=None):
+def roomy(groups, H, capacity):
+    """A capacity for which sharing is expected to pay, whatever the lengths."""
+    B = sum(len(own) for _, own in groups)
+    return max(capacity, 128 * (1600 // max(1, (B - len(groups)) * H) + 1))
+
+
+def shared_cache(gen, groups, H, D, page, capacity, layout="nhd", spoil=None, room=None):
     """groups: [(shared positions, [own positions of each sequence])] -> (cache, rows, cache_len, prefix_len, prefix_start).
 
     Whole pages of the shared positions are the same pages; the positions behind them, and everything without a block
-    table, are copies.  spoil(kk, vv): changes a group's shared rows before they are written."""
+    table, are copies.  spoil(kk, vv): changes a group's shared rows before they are written.  room: the capacity that the
+    block table (or, without one, the memory) has, of which only the first `capacity` positions are ever used."""
     B = sum(len(own) for _, own in groups)
     rows, lens, prefix, start = [], [], [], [0]
     for P, own in groups:
@@ -38,7 +45,7 @@ def shared_cache(gen, groups, H, D, page, capacity, layout="nhd", spoil=None):
         prefix.append(P)
         start.append(len(rows))
     if page == 0:
-        pages, size, table = B, capacity, None
+        pages, size, table = B, room or capacity, None
     else:
         per, size = -(-capacity // page), page
         pages = B * per + 2
@@ -46,6 +53,8 @@ def shared_cache(gen, groups, H, D, page, capacity, layout="nhd", spoil=None):
         table = perm[:B * per].reshape(B, per).to(torch.int32).cuda()
         for g, (P, own) in enumerate(groups):
             table[start[g]:start[g + 1], :P // page] = table[start[g]:start[g] + 1, :P // page].clone()
+        if room:
+            table = torch.cat([table, table.new_full((B, max(0, -(-room // page) - per)), pages - 1)], 1)
     shape = (pages, size, H, D) if layout == "nhd" else (pages, H, size, D)
     k = torch.full(shape, NAN, dtype=torch.bfloat16, device="cuda")
     v = torch.full(shape, NAN, dtype=torch.bfloat16, device="cuda")
@@ -108,10 +117,12 @@ CASES = [
 
 @pytest.mark.parametrize("groups,T,heads,H,D,page,layout,tree", CASES)
 @pytest.mark.parametrize("drafted", [True, False])
-def test_prefix_attention(handle, groups, T, heads, H, D, page, layout, tree, drafted):
+@pytest.mark.parametrize("shared", [True, False])
+def test_prefix_attention(handle, groups, T, heads, H, D, page, layout, tree, drafted, shared):
+    """shared: with a capacity for which sharing pays; otherwise the call is taken as tree attention."""
     gen = torch.Generator(device="cuda").manual_seed(T * 100 + heads)
     cap = max(P + max(own, default=0) for P, own in groups) + 3
-    cache, rows, cl, pl, ps = shared_cache(gen, groups, H, D, page, cap, layout)
+    cache, rows, cl, pl, ps = shared_cache(gen, groups, H, D, page, cap, layout, room=roomy(groups, H, cap) if shared else None)
     B = len(rows)
     q, kn, vn = randn(gen, B, T, heads + 2 * H, D).split([heads, H, H], 2)
     sees = mask = None
@@ -133,7 +144,7 @@ def test_prefix_attention(handle, groups, T, heads, H, D, page, layout, tree, dr
 
 def test_the_whole_batch_as_one_group_and_a_scale(handle):
     gen = torch.Generator(device="cuda").manual_seed(1)
-    cache, rows, cl, pl, _ = shared_cache(gen, [(400, [1, 60, 200])], 2, 128, 32, 610)
+    cache, rows, cl, pl, _ = shared_cache(gen, [(400, [1, 60, 200])], 2, 128, 32, 610, room=60000)
     q = randn(gen, 3, 4, 6, 128)
     out, lse = api.prefix_attention(handle, q, cache, cl, pl, scale=0.25)
     check(out, definition(q, rows, None, None, None, 0.25))
@@ -149,7 +160,7 @@ def test_more_sequences_than_the_list_takes_at_once(handle):
     gen = torch.Generator(device="cuda").manual_seed(2)
     rng = np.random.default_rng(0)
     groups = [(int(rng.integers(0, 300)), [int(n) for n in rng.integers(0, 40, 3)]) for _ in range(500)]
-    cache, rows, cl, pl, ps = shared_cache(gen, groups, 1, 64, 16, 345)
+    cache, rows, cl, pl, ps = shared_cache(gen, groups, 1, 64, 16, 345, room=1000)
     q, kn, vn = randn(gen, 1500, 1, 4, 64).split([2, 1, 1], 2)
     out, lse = api.prefix_attention(handle, q, cache, cl, pl, ps, kn, vn)
     want, _ = api.tree_attention(handle, q, cache, cl, kn, vn)
@@ -163,7 +174,7 @@ def test_more_sequences_than_the_list_takes_at_once(handle):
 @pytest.mark.parametrize("bad", [[1, 2, 4], [0, 3, 2], [0, 2, 3], [0, -1, 4], [0, 2, 1 << 30], [0, 1 << 31 - 1, 4]])
 def test_starts_that_do_not_ascend_are_flagged(handle, bad):
     gen = torch.Generator(device="cuda").manual_seed(3)
-    cache, rows, cl, pl, ps = shared_cache(gen, [(300, [5, 6]), (256, [7, 0])], 2, 64, 16, 330)
+    cache, rows, cl, pl, ps = shared_cache(gen, [(300, [5, 6]), (256, [7, 0])], 2, 64, 16, 330, room=60000)
     q = randn(gen, 4, 3, 4, 64)
     out, _ = api.prefix_attention(handle, q, cache, cl, pl, torch.tensor(bad, dtype=torch.int64, device="cuda").to(torch.int32))
     assert handle.device_error() == 0x10
@@ -172,10 +183,10 @@ def test_starts_that_do_not_ascend_are_flagged(handle, bad):
 
 def test_lengths_out_of_range_are_clamped_and_flagged(handle):
     gen = torch.Generator(device="cuda").manual_seed(4)
-    cache, rows, cl, pl, ps = shared_cache(gen, [(300, [5, 0]), (256, [7, 0])], 2, 64, 16, 336)
+    cache, rows, cl, pl, ps = shared_cache(gen, [(300, [5, 0]), (256, [7, 0])], 2, 64, 16, 336, room=60000)
     q = randn(gen, 4, 3, 4, 64)
     want = definition(q, rows, None, None, None, 64 ** -0.5)
-    for lens in ([1 << 30, 256], [300, 257], [-1, 256]):        # above the capacity, above a length, negative
+    for lens in ([1 << 30, 256], [301, 256], [-1, 256]):        # above the capacity, above a length, negative
         out, _ = api.prefix_attention(handle, q, cache, cl, i32(lens), ps)
         assert handle.device_error() == 0x10
         check(out, want)
@@ -195,7 +206,7 @@ def test_lengths_out_of_range_are_clamped_and_flagged(handle):
 
 def test_bad_pages_are_flagged(handle):
     gen = torch.Generator(device="cuda").manual_seed(5)
-    cache, rows, cl, pl, ps = shared_cache(gen, [(256, [20, 20])], 2, 64, 16, 300)
+    cache, rows, cl, pl, ps = shared_cache(gen, [(256, [20, 20])], 2, 64, 16, 300, room=120000)
     q = randn(gen, 2, 1, 4, 64)
     table = cache.block_table.clone()
     table[0, 2], table[1, 17] = -1, 1 << 30
@@ -224,7 +235,7 @@ def test_infinite_and_nan_values(handle, groups, T, heads, H, D, page):
             spoil(kk, vv)
             if full:
                 kk[11] = -INF
-        cache, rows, cl, pl, ps = shared_cache(gen, groups, H, D, page, cap, spoil=rows_of_prefix)
+        cache, rows, cl, pl, ps = shared_cache(gen, groups, H, D, page, cap, spoil=rows_of_prefix, room=roomy(groups, H, cap))
         B = len(rows)
         q, kn, vn = (randn(gen, B, T, n, D) for n in (heads, H, H))
         if full:
@@ -246,7 +257,7 @@ def test_a_graph_replays_on_new_lengths_and_groups(handle):
     gen = torch.Generator(device="cuda").manual_seed(7)
     B, T, heads, H, D = 6, 3, 8, 2, 128
     plans = [[(256, [1, 2, 3]), (300, [9, 0, 77])], [(700, [0, 5, 6, 7, 8, 9]), (0, [])], [(0, [40]), (200, [1, 1, 1, 1, 1])]]
-    sets = [shared_cache(gen, plan, H, D, 16, 720) for plan in plans]
+    sets = [shared_cache(gen, plan, H, D, 16, 720, room=60000) for plan in plans]
     k, v, table = (x.clone() for x in (sets[0][0].k, sets[0][0].v, sets[0][0].block_table))
     cache, cl, pl, ps = api.KVCache(k, v, table), i32([0] * B), i32([0, 0]), i32([0, 3, 6])
     q, kn, vn = randn(gen, B, T, heads + 2 * H, D).split([heads, H, H], 2)
@@ -266,7 +277,7 @@ def test_a_graph_replays_on_new_lengths_and_groups(handle):
 
 def test_two_streams_at_once(handle):
     gen = torch.Generator(device="cuda").manual_seed(8)
-    cache, rows, cl, pl, ps = shared_cache(gen, [(900, [30, 40, 50, 60])], 4, 128, 64, 970)
+    cache, rows, cl, pl, ps = shared_cache(gen, [(900, [30, 40, 50, 60])], 4, 128, 64, 970, room=60000)
     qs = [randn(gen, 4, 5, 16, 128) for _ in range(2)]
     want = [api.prefix_attention(handle, q, cache, cl, pl, ps)[0] for q in qs]
     streams = [torch.cuda.Stream() for _ in range(2)]
@@ -294,12 +305,9 @@ def test_empty_calls_and_refusals(handle):
                       (dict(cache_len=cl.cpu()), ValueError)):
         with pytest.raises(error):
             api.prefix_attention(handle, **{**dict(q=q, cache=cache, cache_len=cl, prefix_len=pl, prefix_start=ps), **kw})
-    # nodes that are not one operand's rows
-    with pytest.raises(api.Dflash2Error) as e:
-        api.prefix_attention(handle, randn(gen, 2, 4, 4, 64)[:, :3], cache, cl, pl, ps)
-    assert e.value.status == -2
-    for shape in ((2, 1), (1, 3)):                          # of one node, or one sequence, any strides will do
+    wide, rows, cl, _, _ = shared_cache(gen, [(128, [3, 4])], 2, 64, 16, 140, room=100000)
+    for shape in ((2, 1), (1, 3), (2, 3)):                  # any strides will do
         x = randn(gen, 5, 5, 4, 64)[:shape[0], 1:1 + shape[1]]
-        out, _ = api.prefix_attention(handle, x, cache, cl[:shape[0]], i32([128 if shape[0] > 1 else 0]))
+        out, _ = api.prefix_attention(handle, x, wide, cl[:shape[0]], i32([128 if shape[0] > 1 else 0]))
         check(out, definition(x, rows[:shape[0]], None, None, None, 64 ** -0.5))
     assert handle.device_error() == 0
