@@ -8,12 +8,12 @@
 // fraction of half a turn go to sincospif.  In fp32 radians the product would be off
 // by 2^-24 of the angle, 0.008 at position 131072, as much as bf16's own rounding.
 //
-// A CTA takes `tokens` consecutive tokens and a stretch of their pieces.  A piece is two
-// vectors of kE elements that hold kE whole pairs in either layout: vectors v and v +
-// rd / 2 / kE of a head (half), or 2 v and 2 v + 1 (interleaved); after the rotated pieces a head's
-// remaining elements are copied two vectors a piece.  The CTA first computes its tokens'
-// cos and sin into shared memory, once for all heads, with its first pieces' loads in
-// flight.  The append's pieces are those of the queries, the keys and the values, in this order.
+// A CTA takes a few consecutive tokens and a stretch of their pieces.  A piece is two vectors of kE
+// elements that hold kE whole pairs in either layout: vectors v and v + rd / 2 / kE of a head (half),
+// or 2 v and 2 v + 1 (interleaved); after the rotated pieces a head's remaining elements are copied two
+// vectors a piece.  The CTA first computes its tokens' cos and sin into shared memory, once for
+// all heads, and for the append their places in the cache.  The append's pieces are those of the queries,
+// the keys and the values, in this order.
 #include "launch.h"
 #include "serve.h"
 
@@ -67,44 +67,62 @@ __device__ __forceinline__ Vec<kE> narrow(const float* x) {
   return v;
 }
 
-// What a CTA does: tokens [first, first + n) of the B T, and of each the pieces [p0, p1).
+// What a CTA does: `tokens` tokens, and of each a stretch of its pieces.
 struct Split {
   int32_t tokens;            // per CTA
   int32_t chunks;            // CTAs that share the same tokens
   int32_t pieces;            // of a token
   int32_t per_chunk;
+  uint32_t by_width, by_head;   // 2^32 / (a chunk's pieces of a token) and / (pieces of a head), rounded up
 };
+
+// x / d for x d < 2^32, with by = 2^32 / d rounded up (d = 1: 0).
+__device__ __forceinline__ int32_t quotient(int32_t x, uint32_t by) {
+  return by == 0 ? x : static_cast<int32_t>(__umulhi(static_cast<uint32_t>(x), by));
+}
 
 // Positions that a sequence can hold.
 __device__ __forceinline__ int32_t append_limit(const RotateArgs& a) {
   return a.scores != nullptr && a.scores_ld < a.cache.capacity ? static_cast<int32_t>(a.scores_ld) : a.cache.capacity;
 }
 
+// A token's place in the cache, found once for all its pieces: offset of its head 0, or -1: it is not appended; whether it
+// counts at all.
+struct Place {
+  int64_t at;
+  int32_t taken;
+};
+
 // One piece under way: where it goes, and its two vectors.
 template <int kE>
 struct Piece {
-  uint16_t* dst;             // nullptr: none
+  int32_t tok;               // token of the CTA's, or -1: none
+  int32_t to;                // 0: the rotated rows' output, 1: the cache's keys, 2: its values
+  int64_t dst;               // its offset (in the cache: from the token's)
   Vec<kE> a, b;
   int32_t apart;             // elements from the first vector to the second
   int32_t angle;             // index of its first pair's cos and sin, or -1: a copy
 };
 
 template <int kE, bool kAppend>
-__device__ __forceinline__ void load_piece(const RotateArgs& a, const Split& sp, uint32_t first, int32_t n, int32_t at,
-                                           int32_t width, Piece<kE>* pc) {
-  pc->dst = nullptr;
+__device__ __forceinline__ void load_piece(const RotateArgs& a, const Split& sp, int64_t b0, int32_t t0, int32_t n, int32_t at,
+                                           int32_t p0, int32_t width, const Place* places, Piece<kE>* pc) {
+  pc->tok = -1;
   if (at >= n * width) return;
-  const int32_t tok = at / width;
-  const int32_t x = blockIdx.x % sp.chunks * sp.per_chunk + at - tok * width;
-  const uint32_t token = first + tok, b = token / static_cast<uint32_t>(a.T);
-  const int32_t t = static_cast<int32_t>(token - b * a.T);
+  const int32_t tok = quotient(at, sp.by_width), x = p0 + at - tok * width;
+  if (x >= sp.pieces) return;
+  if (kAppend && places != nullptr && !places[tok].taken) return;
+  int64_t b = b0;
+  int32_t t = t0 + tok;
+  while (t >= a.T) t -= a.T, ++b;      // at most kMaxTokens - 1 times
   const int32_t per_head = a.dim / (2 * kE);
-  const int32_t head = x / per_head, v = x - head * per_head;
-  const bool rotated = v < a.rope.rd / (2 * kE);
+  const int32_t head = quotient(x, sp.by_head), v = x - head * per_head;
+  const bool value = kAppend && head >= a.heads + a.cache.heads;
   int32_t e0 = 2 * kE * v;
+  pc->tok = tok;
   pc->apart = kE;
   pc->angle = -1;
-  if (rotated) {
+  if (v < a.rope.rd / (2 * kE) && !value) {
     if (!a.rope.interleaved) {
       e0 = kE * v;
       pc->apart = a.rope.rd >> 1;
@@ -113,36 +131,31 @@ __device__ __forceinline__ void load_piece(const RotateArgs& a, const Split& sp,
   }
   const uint16_t* src;
   if (!kAppend || head < a.heads) {
-    if (kAppend && a.count != nullptr && t >= a.count[b]) return;
     src = a.x + b * a.x_b + t * a.x_t + head * a.x_h;
-    pc->dst = a.out + b * a.out_b + t * a.out_t + head * a.out_h + e0;
+    pc->to = 0;
+    pc->dst = b * a.out_b + t * a.out_t + head * a.out_h + e0;
   } else {
-    const int32_t limit = append_limit(a), len = kv_clamp(a.cache_len[b], limit, nullptr);
-    if ((a.count != nullptr && t >= a.count[b]) || t >= limit - len) return;
-    const bool value = head >= a.heads + a.cache.heads;
     const int32_t h = head - a.heads - (value ? a.cache.heads : 0);
-    bool ok;
-    const int64_t to = kv_offset(a.cache, b, len + t, h, a.err, &ok);
-    if (!value && v == 0 && a.scores != nullptr) a.scores[(static_cast<int64_t>(b) * a.cache.heads + h) * a.scores_ld + len + t] = 0.0f;
-    if (!ok) return;
-    if (value) {                       // plain vectors, side by side
-      e0 = 2 * kE * v;
-      pc->apart = kE;
-      pc->angle = -1;
-    }
     src = (value ? a.v_new : a.k_new) + b * a.new_b + t * a.new_t + h * a.new_h;
-    pc->dst = (value ? a.cache.v : a.cache.k) + to + e0;
+    pc->to = value ? 2 : 1;
+    pc->dst = h * a.cache.head_stride + e0;
   }
   pc->a = load_vec<kE>(src + e0);
   pc->b = load_vec<kE>(src + e0 + pc->apart);
 }
 
-template <int kE>
-__device__ __forceinline__ void store_piece(const RotateArgs& a, const Piece<kE>& pc, const float2* cs) {
-  if (pc.dst == nullptr) return;
+template <int kE, bool kAppend>
+__device__ __forceinline__ void store_piece(const RotateArgs& a, const Piece<kE>& pc, const float2* cs, const Place* places) {
+  if (pc.tok < 0) return;
+  uint16_t* dst = a.out + pc.dst;
+  if (kAppend) {
+    const Place place = places[pc.tok];
+    if (pc.to == 0 ? !place.taken : place.at < 0) return;
+    if (pc.to != 0) dst = (pc.to == 1 ? a.cache.k : a.cache.v) + place.at + pc.dst;
+  }
   if (pc.angle < 0) {
-    store_vec<kE>(pc.dst, pc.a);
-    store_vec<kE>(pc.dst + pc.apart, pc.b);
+    store_vec<kE>(dst, pc.a);
+    store_vec<kE>(dst + pc.apart, pc.b);
     return;
   }
   float x[2 * kE], y[2 * kE];
@@ -162,23 +175,48 @@ __device__ __forceinline__ void store_piece(const RotateArgs& a, const Piece<kE>
       y[kE + i] = y2;
     }
   }
-  store_vec<kE>(pc.dst, narrow<kE>(y));
-  store_vec<kE>(pc.dst + pc.apart, narrow<kE>(y + kE));
+  store_vec<kE>(dst, narrow<kE>(y));
+  store_vec<kE>(dst + pc.apart, narrow<kE>(y + kE));
 }
 
-template <int kE, bool kAppend>
+// kBulk: several tokens a CTA, for many tokens, and one piece a thread under way, which takes the fewest registers (65536
+// tokens of 72 heads of 128: 360 us, as fast as a copy; with two pieces 376, with four 496).  The append's CTAs
+// then know which tokens count before they load anything (8 prompts of 2048 to 4096 tokens, 80 heads: 169 us, 6.0 TB/s, 90% of
+// a copy's rate; with the first pieces loaded before 188).  Otherwise first pieces are loaded before anything else is
+// known, two a thread where there is one token a CTA (256 tokens of 80 heads: 4.4 us; with one 4.9).
+template <int kE, bool kAppend, bool kBulk>
 __global__ void __launch_bounds__(kThreads) rotate_kernel(const __grid_constant__ RotateArgs a, const Split sp) {
-  __shared__ float2 cs[kMaxTokens * (kMaxRotary / 2)];
-  constexpr int kBatch = 2;              // pieces of a thread under way at once
+  constexpr int kTokens = kBulk ? kMaxTokens : 1;
+  __shared__ float2 cs[kTokens * (kMaxRotary / 2)];
+  __shared__ Place places[kTokens];
+  constexpr int kBatch = kBulk ? 1 : 2;  // pieces of a thread under way at once
+  constexpr bool kEarly = !kBulk || !kAppend;
   const uint32_t first = blockIdx.x / sp.chunks * sp.tokens;           // B T < 2^31
   const int32_t n = static_cast<int32_t>(imin64(sp.tokens, a.B * a.T - first));
   const int32_t p0 = blockIdx.x % sp.chunks * sp.per_chunk;
-  const int32_t width = min(sp.per_chunk, sp.pieces - p0);   // pieces of a token that are this CTA's
+  const int32_t width = sp.per_chunk;    // pieces of a token that are this CTA's (the last chunk's may be fewer)
+  const int64_t b0 = a.T > 0 ? first / static_cast<uint32_t>(a.T) : 0;
+  const int32_t t0 = static_cast<int32_t>(first - b0 * a.T);
   pdl_wait();
   pdl_launch_dependents();
   Piece<kE> pc[kBatch];
+  if constexpr (kEarly)
 #pragma unroll
-  for (int i = 0; i < kBatch; ++i) load_piece<kE, kAppend>(a, sp, first, n, threadIdx.x + i * kThreads, width, &pc[i]);
+    for (int i = 0; i < kBatch; ++i)
+      load_piece<kE, kAppend>(a, sp, b0, t0, n, threadIdx.x + i * kThreads, p0, width, nullptr, &pc[i]);
+  if (kAppend && threadIdx.x < static_cast<unsigned>(n)) {
+    int64_t b = b0;
+    int32_t t = t0 + threadIdx.x;
+    while (t >= a.T) t -= a.T, ++b;
+    const int32_t limit = append_limit(a), len = kv_clamp(a.cache_len[b], limit, nullptr);
+    Place place = {-1, a.count == nullptr || t < a.count[b]};
+    if (place.taken && t < limit - len) {
+      bool ok;
+      const int64_t at = kv_offset(a.cache, b, len + t, 0, a.err, &ok);
+      if (ok) place.at = at;
+    }
+    places[threadIdx.x] = place;
+  }
   const int32_t half = a.rope.rd >> 1;
   for (int32_t x = threadIdx.x; x < n * half; x += kThreads) {
     const int32_t tok = x / half;
@@ -191,21 +229,34 @@ __global__ void __launch_bounds__(kThreads) rotate_kernel(const __grid_constant_
     sincospif(static_cast<float>(part) * 4.656612873077393e-10f, &s, &c);
     cs[x] = make_float2(c * a.rope.factor, (a.inverse ? -s : s) * a.rope.factor);
   }
-  if (kAppend)
+  if (kAppend) {
     for (int64_t b = static_cast<int64_t>(blockIdx.x) * kThreads + threadIdx.x; b < a.B; b += static_cast<int64_t>(gridDim.x) * kThreads) {
       const int32_t limit = append_limit(a), len = kv_clamp(a.cache_len[b], limit, a.err);
       const int32_t count = a.count == nullptr ? a.T : kv_clamp(a.count[b], a.T, a.err);
       if (count > limit - len) raise_error(a.err, DFLASH2_DEVERR_BAD_LENGTH);
       a.new_len[b] = len + min(count, limit - len);
     }
+    // the appended positions' scores, by the CTAs that have the tokens' first pieces
+    if (a.scores != nullptr && p0 == 0)
+      for (int32_t x = threadIdx.x; x < n * a.cache.heads; x += kThreads) {
+        const int32_t tok = x / a.cache.heads, h = x - tok * a.cache.heads;
+        int64_t b = b0;
+        int32_t t = t0 + tok;
+        while (t >= a.T) t -= a.T, ++b;
+        const int32_t limit = append_limit(a), len = kv_clamp(a.cache_len[b], limit, nullptr);
+        if ((a.count == nullptr || t < a.count[b]) && t < limit - len)
+          a.scores[(b * a.cache.heads + h) * a.scores_ld + len + t] = 0.0f;
+      }
+  }
   __syncthreads();
+  if constexpr (kEarly)
 #pragma unroll
-  for (int i = 0; i < kBatch; ++i) store_piece<kE>(a, pc[i], cs);
-  for (int32_t at = threadIdx.x + kBatch * kThreads; at < n * width; at += kBatch * kThreads) {
+    for (int i = 0; i < kBatch; ++i) store_piece<kE, kAppend>(a, pc[i], cs, places);
+  for (int32_t at = threadIdx.x + (kEarly ? kBatch * kThreads : 0); at < n * width; at += kBatch * kThreads) {
 #pragma unroll
-    for (int i = 0; i < kBatch; ++i) load_piece<kE, kAppend>(a, sp, first, n, at + i * kThreads, width, &pc[i]);
+    for (int i = 0; i < kBatch; ++i) load_piece<kE, kAppend>(a, sp, b0, t0, n, at + i * kThreads, p0, width, places, &pc[i]);
 #pragma unroll
-    for (int i = 0; i < kBatch; ++i) store_piece<kE>(a, pc[i], cs);
+    for (int i = 0; i < kBatch; ++i) store_piece<kE, kAppend>(a, pc[i], cs, places);
   }
 }
 
@@ -218,9 +269,14 @@ cudaError_t launch(const RotateArgs& a, int num_sms, cudaStream_t stream) {
   // several tokens a CTA where there are CTAs enough; else the pieces of a token are shared out
   sp.tokens = all >= static_cast<int64_t>(kMaxTokens) * 8 * num_sms ? kMaxTokens : 1;
   sp.chunks = 1;
-  if (sp.tokens == 1) sp.chunks = static_cast<int32_t>(imin64((sp.pieces + 2 * kThreads - 1) / (2 * kThreads), ((int64_t(1) << 31) - 1) / imax64(all, 1)));
+  // (few enough pieces a CTA that quotient() is exact, too)
+  const int64_t most = sp.tokens == 1 ? 2 * kThreads : 8192;
+  sp.chunks = static_cast<int32_t>(imin64((sp.pieces + most - 1) / most, ((int64_t(1) << 31) - 1) / imax64((all + sp.tokens - 1) / sp.tokens, 1)));
   sp.chunks = sp.chunks < 1 ? 1 : sp.chunks;
   sp.per_chunk = (sp.pieces + sp.chunks - 1) / sp.chunks;
+  const auto reciprocal = [](uint32_t d) { return d <= 1 ? 0u : static_cast<uint32_t>(((uint64_t(1) << 32) + d - 1) / d); };
+  sp.by_head = reciprocal(a.dim / (2 * kE));
+  sp.by_width = reciprocal(sp.per_chunk);
   cudaLaunchAttribute attr = pdl_attribute();
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(static_cast<unsigned>(imax64(1, (all + sp.tokens - 1) / sp.tokens * sp.chunks)), 1, 1);   // (T = 0: new_len)
@@ -228,7 +284,8 @@ cudaError_t launch(const RotateArgs& a, int num_sms, cudaStream_t stream) {
   cfg.stream = stream;
   cfg.attrs = &attr;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, rotate_kernel<kE, kAppend>, a, sp);
+  return sp.tokens > 1 ? cudaLaunchKernelEx(&cfg, rotate_kernel<kE, kAppend, true>, a, sp)
+                       : cudaLaunchKernelEx(&cfg, rotate_kernel<kE, kAppend, false>, a, sp);
 }
 
 // Elements of a vector: the widest of which whole pieces make up both the rotated part
