@@ -9,11 +9,14 @@
 // under way while each takes its own vector, if that is not listed, through all nodes: there only
 // the mask matters.  Such a vector is copied; where out is logits nothing of it is read, and
 // what is not allowed is written.
-// 128 blocks of 17 nodes over 151936 tokens in place, half of them bound by a grammar, 2000
-// tokens emitted and 2000 in the prompt: 174 us (every thread adjusting its own vector: 470; masks fetched
-// by each thread, partly masked vectors read: 220 to 195; the listed vectors' loads after the others: 189).
-// Memory takes about 95 of it: 330 MB of -inf, 120 MB of counts and masks, and of every listed vector a
-// 32-byte sector each way; the rest is instructions, and at most 4 CTAs on an SM (more of them spill: 184, 204).
+// What bounds it (128 blocks of 17 nodes over 151936 tokens, 2000 tokens emitted and 2000 in the prompt):
+//   out of place  memory: 190 us for a plain copy of 1.3 GB (6.9 TB/s), 231 with penalties and masks (94% of a copy's rate).
+//   in place, half of the requests bound by a grammar: 174 us, of which 82 are masks and -inf. The listed vectors are
+//   scattered: 35 of a CTA's 256, and of each a sector of 32 bytes goes each way, 366 MB, which memory fetches 64
+//   bytes at a time; alone they take 131 us.  (Every thread adjusting its own vector: 470; masks fetched by each thread, partly
+//   masked vectors read: 220 to 195; the listed vectors' loads after the others: 189; 4 of their rows at once: 177.)
+//   At most 4 CTAs on an SM: more of them spill (184, 204).
+// 128 blocks over 5000 tokens make 384 CTAs: their nodes are cut as well, 45 to 33 us.
 #include "launch.h"
 #include "serve.h"
 
@@ -99,8 +102,8 @@ __device__ __forceinline__ bool node_sees(const LogitsArgs& a, int64_t b, int32_
   return a.mask[(b * a.T + t) * ((a.T + 63) >> 6) + (s >> 6)] >> (s & 63) & 1ull;
 }
 
-__global__ void __launch_bounds__(kThreads, 4) logits_adjust_kernel(const __grid_constant__ LogitsArgs a, int32_t blocks_per_seq) {
-  extern __shared__ uint32_t masks[];     // [T][kBlockWords], the CTA's columns
+__global__ void __launch_bounds__(kThreads, 4) logits_adjust_kernel(const __grid_constant__ LogitsArgs a, int32_t blocks_per_seq, int32_t rows) {
+  extern __shared__ uint32_t masks[];     // [rows][kBlockWords], the CTA's nodes and columns
   __shared__ Draft drafts[kMaxNodes];
   __shared__ uint16_t listed[kThreads];   // vectors that hold a token to be adjusted; bit 15: a drafted one
   __shared__ int32_t num_drafts, num_listed;
@@ -108,17 +111,21 @@ __global__ void __launch_bounds__(kThreads, 4) logits_adjust_kernel(const __grid
   const int32_t block = blockIdx.x % blocks_per_seq, c0 = block * kBlockCols;
   const int32_t tid = threadIdx.x, lane = tid & 31;
   const bool inplace = a.out == a.logits, restricted = a.allowed != nullptr;
+  const int32_t t_begin = blockIdx.y * rows, t_end = min(a.T, t_begin + rows);   // the CTA's nodes
   if (tid == 0) num_drafts = num_listed = 0;
   pdl_wait();
   pdl_launch_dependents();
   if (restricted) {
     const int32_t words = min(kBlockWords, ((a.V + 31) >> 5) - c0 / 32);
-    const uint32_t* from = a.allowed + b * a.allowed_b + c0 / 32;
+    const uint32_t* from = a.allowed + b * a.allowed_b + t_begin * a.allowed_t + c0 / 32;
 #pragma unroll 4
-    for (int32_t x = tid; x < a.T * kBlockWords; x += kThreads)
+    for (int32_t x = tid; x < (t_end - t_begin) * kBlockWords; x += kThreads)
       masks[x] = x % kBlockWords < words ? from[x / kBlockWords * a.allowed_t + x % kBlockWords] : 0u;
   }
-  const uint8_t* may_of = reinterpret_cast<const uint8_t*>(masks);      // of node t, vector v: [t * kThreads + v]
+  // of node t, vector v: [(t - t_begin) * kThreads + v]
+  const auto may_of = [&](int32_t t, int32_t v) {
+    return static_cast<uint32_t>(reinterpret_cast<const uint8_t*>(masks)[(t - t_begin) * kThreads + v]);
+  };
   const int32_t col = c0 + tid * kCols, cols = min(kCols, a.V - col);
   bool some = false, drafted = false;   // whether the thread's own vector is adjusted at every node, or has a drafted token
   if (cols > 0) {
@@ -139,7 +146,7 @@ __global__ void __launch_bounds__(kThreads, 4) logits_adjust_kernel(const __grid
     if (tid < a.T) {
       const int32_t tok = a.tokens[b * a.T + tid];
       if (tok < 0 || tok >= a.V) {
-        if (block == 0) raise_error(a.err, DFLASH2_DEVERR_BAD_TOKEN);
+        if (block == 0 && t_begin == 0) raise_error(a.err, DFLASH2_DEVERR_BAD_TOKEN);
       } else if (tok >= c0 && tok < c0 + kBlockCols) {
         drafts[atomicAdd(&num_drafts, 1)] = {static_cast<int16_t>(tok - c0), static_cast<int16_t>(tid)};
       }
@@ -160,9 +167,9 @@ __global__ void __launch_bounds__(kThreads, 4) logits_adjust_kernel(const __grid
   uint16_t* dst = a.out + b * a.out_b;
   // The listed vector that the thread adjusts, at every `step`th node: its first rows are under way while the
   // thread's own vector is copied or masked.
-  const int32_t n = num_listed, step = n > 0 ? kThreads / n : 1, first = n > 0 ? tid / n : a.T;
-  const bool busy = first < step && first < a.T;
-  const uint32_t which = busy ? listed[tid - first * n] : 0u;
+  const int32_t n = num_listed, step = n > 0 ? kThreads / n : 1, first = t_begin + (n > 0 ? tid / n : a.T);
+  const bool busy = first - t_begin < step && first < t_end;
+  const uint32_t which = busy ? listed[tid - (first - t_begin) * n] : 0u;
   const int32_t vec = which & 0x7FFF, vec_col = c0 + vec * kCols, vec_cols = min(kCols, a.V - vec_col);
   const uint32_t vec_full = (1u << vec_cols) - 1;
   uint32_t may[kRows];
@@ -171,7 +178,7 @@ __global__ void __launch_bounds__(kThreads, 4) logits_adjust_kernel(const __grid
 #pragma unroll
     for (int y = 0; y < kRows; ++y) {
       const int32_t t = t0 + y * step;
-      may[y] = t >= a.T ? 0u : restricted ? may_of[t * kThreads + vec] & vec_full : vec_full;
+      may[y] = t >= t_end ? 0u : restricted ? may_of(t, vec) & vec_full : vec_full;
       w[y] = make_uint4(0, 0, 0, 0);
       if (may[y] != 0) w[y] = *reinterpret_cast<const uint4*>(src + t * a.x_t + vec_col);
     }
@@ -182,10 +189,10 @@ __global__ void __launch_bounds__(kThreads, 4) logits_adjust_kernel(const __grid
     const uint32_t full = (1u << cols) - 1;
     if (inplace) {
       // nothing is read but the masks: a vector of which some columns stay is written column by column
-      uint16_t* to = dst + col;
+      uint16_t* to = dst + t_begin * a.out_t + col;
 #pragma unroll 4
-      for (int32_t t = 0; restricted && t < a.T; ++t, to += a.out_t) {
-        const uint32_t may = may_of[t * kThreads + tid] & full;
+      for (int32_t t = t_begin; restricted && t < t_end; ++t, to += a.out_t) {
+        const uint32_t may = may_of(t, tid) & full;
         if (may == 0 && cols == kCols) {
           *reinterpret_cast<uint4*>(to) = make_uint4(kNone, kNone, kNone, kNone);
         } else if (may != full) {
@@ -195,19 +202,19 @@ __global__ void __launch_bounds__(kThreads, 4) logits_adjust_kernel(const __grid
         }
       }
     } else {
-      for (int32_t t0 = 0; t0 < a.T; t0 += kCopyRows) {
+      for (int32_t t0 = t_begin; t0 < t_end; t0 += kCopyRows) {
         uint32_t may[kCopyRows];
         uint4 w[kCopyRows];
 #pragma unroll
         for (int y = 0; y < kCopyRows; ++y) {
           const int32_t t = t0 + y;
-          may[y] = t >= a.T ? 0u : restricted ? may_of[t * kThreads + tid] & full : full;
+          may[y] = t >= t_end ? 0u : restricted ? may_of(t, tid) & full : full;
           w[y] = make_uint4(0, 0, 0, 0);
           if (may[y] != 0) w[y] = *reinterpret_cast<const uint4*>(src + t * a.x_t + col);
         }
 #pragma unroll
         for (int y = 0; y < kCopyRows; ++y)
-          if (t0 + y < a.T) store_cols(dst + (t0 + y) * a.out_t + col, masked(w[y], may[y], full), cols);
+          if (t0 + y < t_end) store_cols(dst + (t0 + y) * a.out_t + col, masked(w[y], may[y], full), cols);
       }
     }
   }
@@ -233,7 +240,7 @@ __global__ void __launch_bounds__(kThreads, 4) logits_adjust_kernel(const __grid
 #pragma unroll
     for (int y = 0; y < kRows; ++y) {
       const int32_t t = t0 + y * step;
-      if (t >= a.T) break;
+      if (t >= t_end) break;
       if (may[y] != 0) {
         float off[kCols];
         uint32_t knows = known;
@@ -261,7 +268,7 @@ __global__ void __launch_bounds__(kThreads, 4) logits_adjust_kernel(const __grid
       store_cols(dst + t * a.out_t + vec_col, masked(w[y], may[y], vec_full), vec_cols);
     }
     t0 += kRows * step;
-    if (t0 >= a.T) return;
+    if (t0 >= t_end) return;
     fetch(t0);
   }
 }
@@ -294,17 +301,20 @@ __global__ void __launch_bounds__(kThreads) token_counts_kernel(const CountArgs 
 
 }  // namespace
 
-cudaError_t launch_logits_adjust(const LogitsArgs& a, int, cudaStream_t stream) {
+cudaError_t launch_logits_adjust(const LogitsArgs& a, int num_sms, cudaStream_t stream) {
   const int64_t blocks = (static_cast<int64_t>(a.V) + kBlockCols - 1) / kBlockCols;
+  // where that makes too few CTAs, a sequence's nodes are cut as well (and what does not depend on them is read again)
+  const int64_t cuts = imin64(a.T, imax64(1, 8 * num_sms / (a.B * blocks)));
+  const int32_t rows = static_cast<int32_t>((a.T + cuts - 1) / cuts);
   cudaLaunchAttribute attr = pdl_attribute();
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(static_cast<unsigned>(a.B * blocks), 1, 1);
+  cfg.gridDim = dim3(static_cast<unsigned>(a.B * blocks), static_cast<unsigned>((a.T + rows - 1) / rows), 1);
   cfg.blockDim = dim3(kThreads, 1, 1);
   cfg.stream = stream;
-  cfg.dynamicSmemBytes = a.allowed != nullptr ? static_cast<size_t>(a.T) * kBlockWords * 4 : 0;   // at most 32 KB
+  cfg.dynamicSmemBytes = a.allowed != nullptr ? static_cast<size_t>(rows) * kBlockWords * 4 : 0;   // at most 32 KB
   cfg.attrs = &attr;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, logits_adjust_kernel, a, static_cast<int32_t>(blocks));
+  return cudaLaunchKernelEx(&cfg, logits_adjust_kernel, a, static_cast<int32_t>(blocks), rows);
 }
 
 cudaError_t launch_token_counts(const CountArgs& a, cudaStream_t stream) {
