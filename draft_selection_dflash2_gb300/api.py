@@ -541,7 +541,8 @@ class Rope:
 def rope(h: Handle, x, rope: Rope, base=None, depth=None, inverse: bool = False, out=None, stream=None):
     """x [B, T, heads, dim] rotated by its positions base[b] + depth[b, t] -> out, bf16 of the same shape.
 
-    base int32 [B] (None: 0), depth int32 [B, T] (None: t; a tree's nodes have their depths).  out may be x.
+    base int32 [B] (None: 0), depth int32 [B, T] (None: t; a tree's nodes have their depths).  out may be x (drafted keys
+    rotated in place keep the strides that they have to share with their values).
     inverse: by the negated angles, which is the gradient (and undoes the rotation, but for the scaling's factor)."""
     _need(rope.device == h.device, "rope: expected one on the handle's device")
     if out is None:

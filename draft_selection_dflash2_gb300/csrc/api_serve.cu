@@ -143,6 +143,14 @@ int dflash2_cache_append(dflash2_handle* h, const uint16_t* k_new, const uint16_
   if (!aligned(k_new, 16) || !aligned(v_new, 16) || !aligned(cache_len, 4) || !aligned(count, 4) || !aligned(position, 4) ||
       !aligned(scores, 4) || !aligned(new_len, 4) || !aligned(q, 16) || !aligned(q_out, 16))
     return DFLASH2_ERR_MISALIGNED;
+  // rows are read and written by different CTAs at once
+  const dflash2::KvView& c = a.cache;
+  const int64_t pool = 2 * ((c.num_pages - 1) * c.page_stride + (c.page_size - 1) * c.token_stride +
+                            (c.heads - 1) * c.head_stride + cache->head_dim);
+  const int64_t rows = span_bytes(ns, B, T, c.heads, cache->head_dim);
+  if (T > 0 && c.capacity > 0 && (ranges_meet(k_new, rows, c.k, pool) || ranges_meet(v_new, rows, c.v, pool) ||
+                                  ranges_meet(k_new, rows, c.v, pool) || ranges_meet(v_new, rows, c.k, pool)))
+    return DFLASH2_ERR_INVALID_ARG;
   if (q && T > 0) {
     RowStrides qs = {q_batch_stride, q_token_stride, q_head_stride};
     RowStrides os = {q_out_batch_stride, q_out_token_stride, q_out_head_stride};

@@ -654,7 +654,7 @@ int dflash2_rope(dflash2_handle* h, const dflash2_rope_table* rope, const uint16
 /*
  * Appends new tokens (a prompt, or the next token of each sequence) to the cache:
  * token i < count[b] becomes position cache_len[b] + i, its key rotated, its value as it is.
- *   k_new, v_new  device bf16 [B, T, cache->heads, head_dim] (strides as above)
+ *   k_new, v_new  device bf16 [B, T, cache->heads, head_dim] (strides as above); not in the cache's memory
  *   rope          NULL: nothing is rotated
  *   count         device int32 [B] or NULL: T; outside [0, T]: clamped and flagged
  *   position      device int32 [B], the angle's position of token 0, or NULL: cache_len (they
@@ -691,7 +691,7 @@ int dflash2_cache_append(dflash2_handle* h, const uint16_t* k_new, const uint16_
  *   tokens       device int32 [B, T], the nodes' tokens, not yet counted, or NULL: none.  An id
  *                outside [0, V) is flagged and counts nothing
  *   tree_mask    device uint64 [B, T, (T + 63) / 64] as in dflash2_tree_attention, or NULL: a chain
- *   repetition, frequency, presence  device fp32 [B] or NULL: 1, 0, 0
+ *   repetition, frequency, presence  device fp32 [B] or NULL: 1, 0, 0 (1 / repetition is rounded to fp32 first)
  *   bias         device fp32 [B, bias_ld] (bias_ld 0: one row for all) or NULL: 0
  *   allowed      device uint32 words, bit v % 32 of word v / 32, (V + 31) / 32 words for each node, with the given
  *                strides in words (0: shared), or NULL: everything

@@ -91,6 +91,7 @@ Q = dict(q=1 << 22, qb=1024, qt=256, qh=64, qo=1 << 23, ob=1024, ot=256, oh=64, 
     (dict(new_len=4100), INVALID), (dict(count=8192), INVALID), (dict(position=8188), INVALID), (dict(nt=60), INVALID), (dict(nt=124), MISALIGNED),
     (dict(k=1 << 20 | 8), MISALIGNED), (dict(len=4098), MISALIGNED), (dict(scores=16384, ld=-1), INVALID),
     (dict(q=1 << 22), INVALID), ({**Q, "heads": 0}, INVALID), ({**Q, "q": 8}, MISALIGNED), ({**Q, "qo": (1 << 22) + 256}, INVALID),
+    (dict(k=4096 + 256), INVALID), (dict(v=8192 + 512), INVALID), (dict(v=4096), INVALID),   # in the cache
     ({**Q, "heads": 65537}, UNSUPPORTED), ({**Q, "qt": 32}, INVALID)])
 def test_append_refuses(lib, h, change, status):
     assert lib.dflash2_cache_append(h, *append_args(**change).values()) == status
@@ -111,6 +112,33 @@ LOGITS = dict(x=4096, xb=4096, xt=1024, B=2, T=4, V=1000, counts=1 << 20, cld=10
     (dict(out=4096, ot=2048, ob=8192), INVALID)])
 def test_logits_refuses(lib, h, change, status):
     assert lib.dflash2_logits_adjust(h, *{**LOGITS, **change}.values()) == status
+
+
+PREFIX = dict(q=1 << 20, qb=1024, qt=256, qh=64, cache=cache(), len=4096, plen=4096, pstart=4096, groups=2, k=1 << 21, v=1 << 22,
+              nb=512, nt=128, nh=64, mask=None, B=2, T=4, heads=4, scale=0.125, out=1 << 23, lse=None, ws=1 << 24,
+              bytes=1 << 40, stream=None)
+
+
+@pytest.mark.parametrize("change,status", [
+    (dict(groups=-1), INVALID), (dict(groups=3), INVALID), (dict(pstart=None), INVALID), (dict(plen=None), INVALID),
+    (dict(q=None), INVALID), (dict(len=None), INVALID), (dict(out=None), INVALID), (dict(k=None), INVALID),
+    (dict(cache=None), INVALID), (dict(scale=0.0), INVALID), (dict(heads=3), INVALID), (dict(T=129), UNSUPPORTED),
+    (dict(B=65536), UNSUPPORTED), (dict(plen=4098), MISALIGNED), (dict(pstart=4098), MISALIGNED), (dict(ws=1 << 24 | 128), MISALIGNED),
+    (dict(qt=60), INVALID), (dict(qt=260), MISALIGNED), (dict(bytes=1 << 10), -7), (dict(ws=None), -7),
+    (dict(k=None, v=None, mask=4096), INVALID)])
+def test_prefix_refuses(lib, h, change, status):
+    assert lib.dflash2_prefix_attention(h, *{**PREFIX, **change}.values()) == status
+
+
+def test_prefix_accepts(lib, h):
+    for change in ({}, dict(groups=0, plen=None, pstart=None), dict(groups=1, pstart=None), dict(qb=2048)):
+        assert past_the_checks(lib.dflash2_prefix_attention(h, *{**PREFIX, **change}.values()))
+    assert lib.dflash2_prefix_attention(h, *{**PREFIX, "T": 0, "q": None}.values()) == 0
+    assert lib.dflash2_prefix_attention(None, *PREFIX.values()) == INVALID
+    size = lib.dflash2_prefix_attention_workspace
+    assert size(None, 1, 1, 1, 1, 64) == 0 and size(h, 0, 1, 1, 1, 64) == 0 and size(h, 1, 129, 1, 1, 64) == 0
+    assert size(h, 2, 4, 4, 2, 96) == 0 and size(h, 2, 4, 3, 2, 64) == 0
+    assert size(h, 2, 4, 4, 2, 64) >= lib.dflash2_tree_attention_workspace(h, 2, 4, 4, 2, 64) > 0
 
 
 COUNTS = dict(tokens=4096, count=None, path=None, B=2, N=10, V=100, prompt=0, counts=8192, ld=100, stream=None)
