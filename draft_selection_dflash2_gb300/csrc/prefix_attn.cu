@@ -19,7 +19,11 @@
 // softmax of two pipelines).  A CTA takes a run of the pairs, each pipeline one row tile of every
 // item, and two runs of the single tiles, one for each pipeline, whose units alternate in the
 // ring: a short item is a chain of latencies (keys, S, softmax, O, its sums' way out), and two
-// at once hide each other's.  The same inputs give the same bits on every call.
+// at once hide each other's.  Where a sequence has at most 32 rows a kv head, its own row tile holds four copies of them, one
+// for each warp of the softmax, and each takes a quarter of a chunk's keys: with one warp at
+// work a chunk took 0.65 us, and twice that beside the other pipeline's (64 sequences of one token behind 8192
+// positions: 84 to 75 us; 128 behind 8192 in two groups, 4000 of their own: 283 to 244).
+// The same inputs give the same bits on every call.
 #include "tree_attn.cuh"
 
 namespace dflash2 {
@@ -28,6 +32,7 @@ namespace {
 constexpr int kListThreads = 1024;
 constexpr int64_t kMostUnits = int64_t(1) << 26, kMostRows = int64_t(1) << 26;
 constexpr int kListed = 32;              // most stretches that producers list for themselves, a lane each
+constexpr int kFewGroups = 1024;         // groups whose starts and lengths are held in shared memory while the list is made
 constexpr int kSegs = 4;                 // segments that a pipeline's warps may lag behind the producer
 
 // A group's shared prefix, seen by all nodes of its sequences, or what one sequence has of its own.
@@ -46,13 +51,17 @@ struct PrefixPlan {
   int32_t groups;
   int32_t tpt;              // nodes per row tile
   int32_t num_stretches;    // groups, then sequences
+  // A sequence's rows are at most 32: its own row tile holds four copies of them, one in each quarter of the lanes, and each
+  // warp of the softmax takes a quarter of a chunk's keys for its copy, instead of one warp all of them.
+  bool spread;
+  int64_t rows;             // of the output
   float c;                  // scale * log2(e)
   int32_t box_rows;         // rows of a K or V box
-  uint32_t q_box_bytes;
+  uint32_t q_box_bytes, spread_bytes;   // of a row tile's queries, and of one copy of a sequence's
   int32_t* shared;          // [groups] shared positions; and the stretches, where CTAs do not list them
   Stretch* stretches;       // [num_stretches + 1]
-  // every row's first part, of its own keys and of its prefix, by row of the output: O [rows][D], and (m, l, where the other
-  // parts are, whether there is a prefix)
+  // every row's first part, of its own keys (with `spread` four, copy after copy) and of its prefix, by row of the output: O
+  // [rows][D], and (m, l, where the other parts are, whether there is a prefix)
   float* first_o[2];
   float4* first_ml[2];
   // the other parts, one place a run: 2 * runs places of pairs (one per tile), then 2 * runs of halves of runs of single tiles
@@ -68,11 +77,11 @@ __device__ __forceinline__ int32_t group_start(const PrefixPlan& p, int32_t g) {
 }
 
 // The group of sequence b (the starts ascend from 0 to B).
-__device__ __forceinline__ int32_t group_of(const PrefixPlan& p, int32_t b) {
-  int32_t lo = 0, hi = p.groups;
+__device__ __forceinline__ int32_t group_of(const int32_t* start, int32_t groups, int32_t b) {
+  int32_t lo = 0, hi = groups;
   while (hi - lo > 1) {
     const int32_t mid = (lo + hi) >> 1;
-    if (group_start(p, mid) <= b)
+    if (start[mid] <= b)
       lo = mid;
     else
       hi = mid;
@@ -97,16 +106,18 @@ __device__ __forceinline__ uint64_t warp_before(uint64_t x, uint64_t* total) {
 // apart, and a run of single tiles is cut in halves: a run has to be as long as two of their units and as one of the pairs'.
 enum List { kPairs = 0, kSingles = 1 };
 constexpr uint32_t kLeastRun = 22;
-__device__ __forceinline__ uint32_t unit_cost(List which) { return which == kPairs ? 17 : 11; }
-__device__ __forceinline__ uint32_t ahead_cost(List which) { return which == kPairs ? 24 : 20; }
-__device__ __forceinline__ uint32_t item_cost(List which, int32_t n) { return n * unit_cost(which) + ahead_cost(which); }
+__device__ __forceinline__ uint32_t unit_cost(const PrefixPlan& p, List which) { return which == kPairs ? 17 : p.spread ? 8 : 11; }
+__device__ __forceinline__ uint32_t ahead_cost(const PrefixPlan& p, List which) { return which == kPairs ? 24 : p.spread ? 16 : 20; }
+__device__ __forceinline__ uint32_t item_cost(const PrefixPlan& p, List which, int32_t n) {
+  return n * unit_cost(p, which) + ahead_cost(p, which);
+}
 
 // The costs of a stretch's pairs (upper half) and single row tiles.
 __device__ __forceinline__ uint64_t cost_of(const PrefixPlan& p, const Stretch& s) {
   if (s.n == 0) return 0;
   const uint32_t tiles = static_cast<uint32_t>((s.nodes + p.tpt - 1) / p.tpt), heads = p.a.cache.heads;
-  return static_cast<uint64_t>(item_cost(kPairs, s.n) * heads * (tiles >> 1)) << 32 |
-         item_cost(kSingles, s.n) * heads * (tiles & 1);
+  return static_cast<uint64_t>(item_cost(p, kPairs, s.n) * heads * (tiles >> 1)) << 32 |
+         item_cost(p, kSingles, s.n) * heads * (tiles & 1);
 }
 
 __device__ __forceinline__ Stretch prefix_stretch(const PrefixPlan& p, int32_t s0, int32_t s1, int32_t tiles) {
@@ -161,25 +172,33 @@ __device__ __forceinline__ void list_few(const PrefixPlan& p, Stretch* list, boo
   __syncwarp();
 }
 
-// Lists any number, with one block.
-__device__ __forceinline__ void list_many(const PrefixPlan& p, int32_t* shared, Stretch* list, uint64_t* warp_sum) {
+// Lists any number, with one block.  start, shared: places for the groups' starts (and the end) and common lengths.
+__device__ __forceinline__ void list_many(const PrefixPlan& p, int32_t* start, int32_t* shared, Stretch* list,
+                                          uint64_t* warp_sum) {
   const AttnArgs& a = p.a;
   const int32_t B = static_cast<int32_t>(a.B), tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int32_t capacity = a.cache.capacity;
+  const auto raw_len = [&](int32_t v) { return v >= p.groups && v < p.num_stretches ? a.cache_len[v - p.groups] : 0; };
+  const int32_t raw = raw_len(tid);          // (of the thread's first stretch; fetched along with the groups)
   bool bad = false;
   for (int32_t g = tid; g < p.groups; g += kListThreads) {
     const int32_t s0 = group_start(p, g), s1 = group_start(p, g + 1);
     bad |= s0 < 0 || s1 < s0 || s1 > B || (g == 0 && s0 != 0) || (g == p.groups - 1 && s1 != B);
     shared[g] = kv_clamp(p.shared_len[g], capacity, a.err);
+    start[g] = s0;
+    if (g == p.groups - 1) start[g + 1] = s1;
   }
   // starts that are none: nothing is shared
   const bool none = __syncthreads_or(bad) != 0 || p.groups == 0;
   if (none && p.groups > 0 && tid == 0) raise_error(a.err, DFLASH2_DEVERR_BAD_LENGTH);
-  for (int32_t b = tid; b < B; b += kListThreads) {
-    const int32_t len = kv_clamp(a.cache_len[b], capacity, a.err);
+  int32_t group = 0;                         // of the thread's first stretch
+  for (int32_t v = tid; v < p.num_stretches; v += kListThreads) {
+    if (v < p.groups) continue;
+    const int32_t len = kv_clamp(v == tid ? raw : raw_len(v), capacity, a.err);
     if (none) continue;
-    const int32_t g = group_of(p, b);
-    if (len < shared[g]) {          // (only ever lowered: whatever is read here, the least one stays)
+    const int32_t g = group_of(start, p.groups, v - p.groups);
+    if (v == tid) group = g;
+    if (len < *static_cast<volatile int32_t*>(&shared[g])) {   // (only ever lowered: whatever is read here, the least one stays)
       raise_error(a.err, DFLASH2_DEVERR_BAD_LENGTH);
       atomicMin(&shared[g], len);
     }
@@ -187,17 +206,18 @@ __device__ __forceinline__ void list_many(const PrefixPlan& p, int32_t* shared, 
   __syncthreads();
   // shared tiles of a group: a sequence by itself shares nothing
   const auto tiles_of = [&](int32_t g) {
-    return none || group_start(p, g + 1) - group_start(p, g) < 2 ? 0 : *static_cast<volatile int32_t*>(&shared[g]) / kTile;
+    return none || start[g + 1] - start[g] < 2 ? 0 : *static_cast<volatile int32_t*>(&shared[g]) / kTile;
   };
   uint64_t before = 0;
   for (int32_t v0 = 0; v0 <= p.num_stretches; v0 += kListThreads) {
     const int32_t v = v0 + tid;
     Stretch s = {};
-    if (v < p.groups && !none)
-      s = prefix_stretch(p, group_start(p, v), group_start(p, v + 1), tiles_of(v));
-    else if (v >= p.groups && v < p.num_stretches)
-      s = own_stretch(p, v - p.groups, none ? 0 : tiles_of(group_of(p, v - p.groups)),
-                      kv_clamp(a.cache_len[v - p.groups], capacity, nullptr));
+    if (v < p.groups && !none) {
+      s = prefix_stretch(p, start[v], start[v + 1], tiles_of(v));
+    } else if (v >= p.groups && v < p.num_stretches) {
+      const int32_t g = none ? 0 : v0 == 0 ? group : group_of(start, p.groups, v - p.groups);
+      s = own_stretch(p, v - p.groups, none ? 0 : tiles_of(g), kv_clamp(v0 == 0 ? raw : raw_len(v), capacity, nullptr));
+    }
     uint64_t total, sums;
     uint64_t at = before + warp_before(cost_of(p, s), &total);
     if (lane == 0) warp_sum[warp] = total;
@@ -208,20 +228,30 @@ __device__ __forceinline__ void list_many(const PrefixPlan& p, int32_t* shared, 
     s.before[0] = static_cast<uint32_t>(at >> 32);
     s.before[1] = static_cast<uint32_t>(at);
     if (v <= p.num_stretches) list[v] = s;
-    __syncthreads();
+    if (v0 + kListThreads <= p.num_stretches) __syncthreads();
   }
 }
 
 __global__ void __launch_bounds__(kListThreads) prefix_list_kernel(const __grid_constant__ PrefixPlan p) {
   __shared__ uint64_t warp_sum[kListThreads / 32];   // 32 warps
+  __shared__ int32_t groups[2 * kFewGroups + 1];
   pdl_wait();
   pdl_launch_dependents();
-  list_many(p, p.shared, p.stretches, warp_sum);
+  int32_t* start = p.groups <= kFewGroups ? groups : p.shared;
+  list_many(p, start, start + p.groups + 1, p.stretches, warp_sum);
 }
 
 // ---------------------------------------------------------------------------
 // walking a run
 // ---------------------------------------------------------------------------
+// 32 bytes at once: a warp's lanes write rows of their own, and every line costs its turn per instruction (16 bytes at once: a
+// pair's 256 rows took 7 us).
+__device__ __forceinline__ void store_sector(float* dst, const float* v) {
+  asm volatile("st.global.v8.f32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(dst), "f"(v[0]), "f"(v[1]), "f"(v[2]), "f"(v[3]),
+               "f"(v[4]), "f"(v[5]), "f"(v[6]), "f"(v[7])
+               : "memory");
+}
+
 // One item's part of a run.
 struct SharedSegment {
   int32_t b, h, pair;       // `pair`: the first of its row tiles is 2 * pair
@@ -230,7 +260,7 @@ struct SharedSegment {
   int32_t tile0, len, node0, nodes;
   uint32_t others;          // the item's runs, the first one and the last one (10 bits each); bit 28: single tiles
   int32_t place;            // of its own part, if that is not the item's first
-  bool own;
+  bool own, spread;
   uint32_t ring;            // the ring's unit that is unit s; single tiles' are every second one
   __device__ __forceinline__ uint32_t ring_unit(int u) const { return ring + (tiles == 1 ? 2 : 1) * (u - s); }
   __device__ __forceinline__ int position(int u) const { return (tile0 + u) * kTile; }
@@ -250,13 +280,19 @@ struct SharedPlace {
   static constexpr int kStep = 1;
   const SharedSegment& g;
   __device__ __forceinline__ SharedPlace(const PrefixPlan&, const SharedSegment& g, const uint8_t*) : g(g) {}
+  __device__ __forceinline__ int copies() const { return g.spread ? 4 : 1; }
+  // (r: with copies, the row of the copy + 32 times the copy)
+  __device__ __forceinline__ int64_t first_row(const PrefixPlan& p, int r, int64_t orow) const {
+    return g.spread ? (r >> 5) * p.rows + orow : orow;
+  }
   __device__ __forceinline__ float4* part(const PrefixPlan& p, int tile, int r, int64_t orow) const {
-    float* at = g.s == 0 ? p.first_o[g.own ? 0 : 1] + orow * D : p.part + (static_cast<int64_t>(g.place + tile) * kTile + r) * D;
+    float* at = g.s == 0 ? p.first_o[g.own ? 0 : 1] + first_row(p, r, orow) * D
+                         : p.part + (static_cast<int64_t>(g.place + tile) * kTile + r) * D;
     return reinterpret_cast<float4*>(at);
   }
   __device__ __forceinline__ void put_ml(const PrefixPlan& p, int tile, int r, int64_t orow, float m, float l) const {
     if (g.s == 0)
-      p.first_ml[g.own ? 0 : 1][orow] = make_float4(
+      p.first_ml[g.own ? 0 : 1][first_row(p, r, orow)] = make_float4(
           m, l, __uint_as_float(g.others | static_cast<uint32_t>(tile * kTile + r) << 20), g.tile0 > 0 ? 1.0f : 0.0f);
     else
       p.part_ml[static_cast<int64_t>(g.place + tile) * kTile + r] = make_float2(m, l);
@@ -282,12 +318,13 @@ struct RunOfList {
   int32_t v, item, s;       // the next one: stretch (-1: none), item of its items, unit
   int32_t place;
   List which;
-  __device__ __forceinline__ uint32_t unit_cost() const { return dflash2::unit_cost(which); }
-  __device__ __forceinline__ uint32_t ahead() const { return ahead_cost(which); }
+  uint32_t unit, ahead;     // costs
   // The units of the list that start at costs [from, to); parts that are no item's first go to place `where`.
   __device__ __forceinline__ void start(const PrefixPlan& p, const Stretch* l, List w, uint32_t from, uint32_t to, int32_t where) {
     list = l;
     which = w;
+    unit = unit_cost(p, w);
+    ahead = ahead_cost(p, w);
     place = where;
     end = to;
     v = -1;
@@ -302,11 +339,11 @@ struct RunOfList {
       hi = min(hi, lo + step);
     }
     v = lo;
-    const uint32_t rel = from - l[v].before[w], cost = item_cost(w, l[v].n);
+    const uint32_t rel = from - l[v].before[w], cost = item_cost(p, w, l[v].n);
     item = static_cast<int32_t>(rel / cost);
     const uint32_t in_item = rel - item * cost;
-    s = in_item <= ahead() ? 0 : static_cast<int32_t>((in_item - ahead() + unit_cost() - 1) / unit_cost());   // (n: all before)
-    at = from - in_item + ahead();
+    s = in_item <= ahead ? 0 : static_cast<int32_t>((in_item - ahead + unit - 1) / unit);   // (n: all before)
+    at = from - in_item + ahead;
     settle(p);
   }
   __device__ __forceinline__ int32_t tiles_of(const PrefixPlan& p, const Stretch& st) const {
@@ -315,7 +352,7 @@ struct RunOfList {
   // Moves on to an item that has units left, and to none where the next unit is not the run's.
   __device__ __forceinline__ void settle(const PrefixPlan& p) {
     if (s == list[v].n) {
-      at += s * unit_cost() + ahead();
+      at += s * unit + ahead;
       s = 0;
       ++item;
       for (;;) {
@@ -326,7 +363,7 @@ struct RunOfList {
         ++v;
       }
     }
-    if (at + s * unit_cost() >= end) v = -1;
+    if (at + s * unit >= end) v = -1;
   }
   __device__ __forceinline__ bool more() const { return v >= 0; }
   // The next segment (more() holds).
@@ -335,7 +372,7 @@ struct RunOfList {
     const int32_t tiles = tiles_of(p, st), per_head = which == kPairs ? tiles >> 1 : 1;
     g->s = s;
     g->n = st.n;
-    g->e = static_cast<int32_t>(min(static_cast<uint32_t>(st.n), (end - at + unit_cost() - 1) / unit_cost()));
+    g->e = static_cast<int32_t>(min(static_cast<uint32_t>(st.n), (end - at + unit - 1) / unit));
     g->b = st.b;
     g->h = item / per_head;
     g->pair = which == kPairs ? item - g->h * per_head : tiles >> 1;
@@ -345,7 +382,8 @@ struct RunOfList {
     g->node0 = st.b * p.a.T;
     g->nodes = st.nodes;
     g->own = v >= p.groups;
-    const uint32_t last = at + (st.n - 1) * unit_cost();
+    g->spread = g->own && p.spread;
+    const uint32_t last = at + (st.n - 1) * unit;
     if (which == kPairs)
       g->others = at / (2 * cuts.half) | last / (2 * cuts.half) << 10;
     else
@@ -379,11 +417,11 @@ struct PrefixSmem {
   uint64_t q_full[2], q_empty[2];     // of each pipeline
   uint64_t s_full[2][kBufs], p_ready[2][kBufs], pv_done[2][kBufs], drain;
   uint64_t seg_full[2][kSegs], seg_empty[2][kSegs];
-  uint64_t seen[3];                   // threads that have seen to a drafted tile: of each pipeline, or of both
+  uint64_t seen;                      // threads that have seen to a drafted tile that both pipelines take
   SharedSegment seg[2][kSegs];        // each pipeline's segments; tiles = 0: no more
   Stretch list[kListed + 1];
   uint32_t segs[2], q_issued[2];   // each pipeline's segments so far, and their queries' copies (the producer's)
-  uint32_t bad[3][4];       // drafted nodes that hold a non-finite value: of each pipeline's tile, or of both
+  uint32_t own_bad[2][kSegs][4], both_bad[4];   // drafted nodes that hold a non-finite value: of a pipeline's segment; of both's tile
   uint32_t tmem;
   int abort_flag;
   int odd;                  // whether some row's sums have to be taken again
@@ -407,7 +445,7 @@ template <int D>
 struct Producer {
   static constexpr int S = Cfg<D>::kSlots;
   const PrefixPlan& p;
-  const CUtensorMap *q, *k, *v, *kn, *vn;
+  const CUtensorMap *q, *qs, *k, *v, *kn, *vn;
   uint8_t *q_smem, *ring;
   PrefixSmem& s;
   int lane;
@@ -424,6 +462,8 @@ struct Producer {
     if (lane == 0 && live) {
       g.ring = tiles / 2;
       *to = g;
+#pragma unroll
+      for (int w = 0; w < 4; ++w) s.own_bad[i][x % kSegs][w] = 0;
       s.segs[i] = x + 1;
       mbar_arrive(&s.seg_full[i][x % kSegs]);
     }
@@ -433,10 +473,12 @@ struct Producer {
     live = __all_sync(0xFFFFFFFFu, live);
     if (lane == 0 && live) {
       s.q_issued[i] = x + 1;
-      mbar_arrive_expect_tx(&s.q_full[i], p.q_box_bytes);
-#pragma unroll
-      for (int c = 0; c < Cfg<D>::kHalves; ++c)
-        tma_load_5d(q_smem + i * Cfg<D>::kTileBytes + c * kTile * 128, q, c * 64, 0,
+      const int copies = g.spread ? 4 : 1;
+      mbar_arrive_expect_tx(&s.q_full[i], g.spread ? 4 * p.spread_bytes : p.q_box_bytes);
+#pragma unroll 1
+      for (int c = 0; c < copies * Cfg<D>::kHalves; ++c)
+        tma_load_5d(q_smem + i * Cfg<D>::kTileBytes + (c % Cfg<D>::kHalves) * kTile * 128 + c / Cfg<D>::kHalves * 32 * 128,
+                    g.spread ? qs : q, c % Cfg<D>::kHalves * 64, 0,
                     g.node0 + (2 * g.pair + (g.tiles == 2 ? i : 0)) * p.tpt, g.h, 0, &s.q_full[i]);
     }
     __syncwarp();
@@ -593,11 +635,12 @@ __device__ __noinline__ void take_again(const PrefixPlan& p, const Stretch* list
   }
 }
 
-template <int D>
+template <int D, bool kSpread>
 __global__ void __launch_bounds__(kThreads, 1)
-    prefix_attn_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmK,
-                       const __grid_constant__ CUtensorMap tmV, const __grid_constant__ CUtensorMap tmKn,
-                       const __grid_constant__ CUtensorMap tmVn, const __grid_constant__ PrefixPlan p) {
+    prefix_attn_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmQs,
+                       const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmV,
+                       const __grid_constant__ CUtensorMap tmKn, const __grid_constant__ CUtensorMap tmVn,
+                       const __grid_constant__ PrefixPlan p) {
   using C = Cfg<D>;
   constexpr int S = C::kSlots;
   extern __shared__ __align__(1024) uint8_t q_smem[];   // no static shared memory: the base is 1024-byte aligned
@@ -627,9 +670,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         mbar_init(&s.seg_full[i][x], 1);
         mbar_init(&s.seg_empty[i][x], 6);      // its two product warps and four softmax warps
       }
-    mbar_init(&s.seen[0], kTile);
-    mbar_init(&s.seen[1], kTile);
-    mbar_init(&s.seen[2], 2 * kTile);
+    mbar_init(&s.seen, 2 * kTile);
     mbar_init(&s.drain, 4);
     for (int i = 0; i < 2; ++i) s.segs[i] = s.q_issued[i] = 0;
     s.abort_flag = 0;
@@ -657,7 +698,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   if (warp == 0) {
     // ---- producer ----
     if (p.num_stretches <= kListed) list_few(p, s.list, blockIdx.x == 0);
-    Producer<D> out = {p, &tmQ, &tmK, &tmV, &tmKn, &tmVn, q_smem, ring, s, lane};
+    Producer<D> out = {p, &tmQ, &tmQs, &tmK, &tmV, &tmKn, &tmVn, q_smem, ring, s, lane};
     out.run(list);
     live = out.live;
     // after a wait that gave up: this CTA's copies have landed before it exits (else the products have used them)
@@ -760,15 +801,20 @@ __global__ void __launch_bounds__(kThreads, 1)
     const uint32_t lanes = static_cast<uint32_t>((warp & 3) * 32) << 16;
     const uint32_t tm_s = tmem + i * kBufs * kChunk + lanes, tm_o = tmem + kTmemO + i * D + lanes;
     BufPos at_s;       // the pipeline's next chunk
-    uint32_t met = 0;  // parities of the meetings over drafted tiles: the pipeline's own (bit 0), and both's (bit 1)
+      uint32_t met = 0;  // parity of the pipelines' meetings over a drafted tile
     // What is needed once a unit is read from shared memory there: the loop over the chunks has no registers to spare.
     const auto field = [](const int32_t& x) { return *const_cast<const volatile int32_t*>(&x); };
     for (uint32_t seg = 0;; ++seg) {
       const SharedSegment* at_g = next_segment(s, i, seg, &live, a.err);
       if (at_g == nullptr) break;
       const SharedSegment& g = *at_g;
-      const auto row_node = [&]() { return (2 * field(g.pair) + (field(g.tiles) == 2 ? i : 0)) * p.tpt + r / a.group; };
-      const bool row_ok = r < p.tpt * a.group && row_node() < field(g.nodes);
+      const bool spread = kSpread && g.spread;
+      // the thread's row of the row tile, and its node
+      const auto tile_row = [&]() { return spread ? r & 31 : r; };
+      const auto row_node = [&]() {
+        return (2 * field(g.pair) + (field(g.tiles) == 2 ? i : 0)) * p.tpt + tile_row() / a.group;
+      };
+      const bool row_ok = tile_row() < p.tpt * a.group && row_node() < field(g.nodes);
       // a warp none of whose rows is a query's has nothing to do but to keep step
       const bool busy = __any_sync(0xFFFFFFFFu, row_ok);
       float m = -INFINITY, l = 0.0f;
@@ -777,23 +823,30 @@ __global__ void __launch_bounds__(kThreads, 1)
       for (int u = field(g.s); u < field(g.e); ++u) {
         int valid = kTile;            // keys of the unit; negative: drafted ones
         wait_live(&s.s_full[i][at_s.buf], at_s.use & 1, &live, abort_flag, a.err);
-        if (u >= field(g.len) / kTile - field(g.tile0)) {
+        // (a prefix's units are whole)
+        if (kSpread ? spread && u >= field(g.len) / kTile - field(g.tile0) : u >= field(g.len) / kTile - field(g.tile0)) {
           const bool drafted = g.drafted(a, u);
           valid = g.keys(a, u);
           const int chunks = valid <= kChunk ? 1 : 2;
           if (drafted || valid < chunks * kChunk) {
             const RingPos<S> at_v = ring_pos<S>(2 * g.ring_unit(u) + 1);
+            uint8_t* v_tile = ring + at_v.slot * C::kTileBytes;
             wait_live(at_v.full(s.kv_full), at_v.parity(), &live, abort_flag, a.err);
-            // the pipelines that take the drafted tile look through it together
-            const bool both = g.tiles == 2;
-            bad_seen |= see_tile<D>(a, ring + at_v.slot * C::kTileBytes, drafted, valid, chunks, g.b, row_node(), row_ok,
-                                    both ? static_cast<int>(threadIdx.x) - kTile : r, both ? 2 * kTile : kTile, r,
-                                    s.bad[both ? 2 : i], [&]() {
-                                      uint64_t* bar = &s.seen[both ? 2 : i];
-                                      mbar_arrive(bar);
-                                      wait_live(bar, met >> (both ? 1 : 0) & 1, &live, abort_flag, a.err);
-                                      met ^= both ? 2 : 1;
-                                    });
+            if (drafted && (kSpread || g.tiles == 1)) {
+              // no meeting: the products with the tile start when all warps have handed in their P
+              const bool any = clear_nonfinite<D>(v_tile, a.T, r, kTile, s.own_bad[i][seg % kSegs]);
+              __syncwarp();
+              if (any) asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+            } else {
+              // the pipelines look through their drafted tile together
+              bad_seen |= see_tile<D>(a, v_tile, !kSpread && drafted, valid, chunks, static_cast<int>(threadIdx.x) - kTile,
+                                      2 * kTile, r, s.both_bad,
+                                      [&](int w) { return seen_keys(a, true, valid, g.b, row_node(), row_ok, w); }, [&]() {
+                                        mbar_arrive(&s.seen);
+                                        wait_live(&s.seen, met & 1, &live, abort_flag, a.err);
+                                        met ^= 1;
+                                      });
+            }
           }
           if (drafted) valid = -valid;
         }
@@ -804,13 +857,22 @@ __global__ void __launch_bounds__(kThreads, 1)
           if (c > 0) wait_live(&s.s_full[i][buf], at_s.use & 1, &live, abort_flag, a.err);
           __syncwarp();
           tc_fence_after();
-          if (busy)
-            softmax_chunk<D>(tm_s + buf * kChunk, tm_o, p.c, valid < chunks * kChunk,
+          const auto wait_products = [&]() {
+            const BufPos prev = at_s.before();
+            wait_live(&s.pv_done[i][prev.buf], prev.use & 1, &live, abort_flag, a.err);
+          };
+          const bool partial = valid < chunks * kChunk;
+          if (busy && spread)
+            softmax_quarter<D>(tm_s + buf * kChunk, tm_o, p.c, warp & 3, partial,
+                               [&]() {
+                                 return seen_keys(a, valid < 0, abs(valid), g.b, row_node(), row_ok, 2 * c + (warp >> 1 & 1)) >>
+                                        16 * (warp & 1);
+                               },
+                               first, row_ok, &m, &l, wait_products);
+          else if (busy)
+            softmax_chunk<D>(tm_s + buf * kChunk, tm_o, p.c, !kSpread && partial,
                              [&](int w) { return seen_keys(a, valid < 0, abs(valid), g.b, row_node(), row_ok, 2 * c + w); },
-                             first, row_ok, &m, &l, [&]() {
-                               const BufPos prev = at_s.before();
-                               wait_live(&s.pv_done[i][prev.buf], prev.use & 1, &live, abort_flag, a.err);
-                             });
+                             first, row_ok, &m, &l, wait_products);
           first = false;
           tmem_st_wait();
           tc_fence_before();
@@ -826,9 +888,10 @@ __global__ void __launch_bounds__(kThreads, 1)
       tc_fence_after();
       if (busy) {
         const int tile = g.tiles == 2 ? i : 0;
+        bad_seen |= sees_bad(s.own_bad[i][seg % kSegs], [&](int w) { return seen_keys(a, true, a.T, g.b, row_node(), row_ok, w); });
         const SharedPlace<D> place(p, g, ring);
         const bool empty = l == 0.0f;   // the row saw nothing: 0, whatever the values were
-        const int64_t orow = g.node(a, row_node()) * a.heads + g.h * a.group + r % a.group;
+        const int64_t orow = g.node(a, row_node()) * a.heads + g.h * a.group + tile_row() % a.group;
         if (row_ok) place.put_ml(p, tile, r, orow, m, l);
         uint64_t odd[4] = {};           // 0, or NaN once an element of O is not finite (four chains of pairs)
 #pragma unroll 1
@@ -846,9 +909,9 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
           for (int y = 0; y < 32; y += 2) odd[y / 2 & 3] = fma2(pack2(o[y], o[y + 1]), 0ull, odd[y / 2 & 3]);
           if (row_ok) {
-            float4* dst = place.part(p, tile, r, orow) + x / 4;
+            float* dst = reinterpret_cast<float*>(place.part(p, tile, r, orow)) + x;
 #pragma unroll
-            for (int y = 0; y < 32; y += 4) dst[y / 4] = make_float4(o[y], o[y + 1], o[y + 2], o[y + 3]);
+            for (int y = 0; y < 32; y += 8) store_sector(dst + y, o + y);
           }
         }
         const float2 odds = unpack2(add2(add2(odd[0], odd[1]), add2(odd[2], odd[3])));
@@ -877,7 +940,8 @@ constexpr int kJoinThreads = 256, kJoinWarps = kJoinThreads / 32, kJoinBatch = 4
 
 // A warp takes a row of the output, a lane D / 32 columns.  kSplit = kJoinWarps: a CTA's warps share out the parts of one row
 // and add their sums in order; for few rows, whose items were cut into many parts.
-template <int D, int kSplit>
+// kCopies: of a sequence's own rows.
+template <int D, int kSplit, int kCopies>
 __global__ void __launch_bounds__(kJoinThreads) prefix_join_kernel(const __grid_constant__ PrefixPlan p, int32_t runs) {
   constexpr int E = D / 32;              // columns of a lane
   struct alignas(4 * E) Cols {
@@ -890,16 +954,26 @@ __global__ void __launch_bounds__(kJoinThreads) prefix_join_kernel(const __grid_
   pdl_launch_dependents();
   if (row >= a.B * a.T * a.heads) return;
   PartSum<E> sum;
-  // (without a prefix the second one holds anything and is not used)
-  const float4 first[2] = {p.first_ml[0][row], p.first_ml[1][row]};
-  const Cols o[2] = {*reinterpret_cast<const Cols*>(p.first_o[0] + row * D + lane * E),
-                     *reinterpret_cast<const Cols*>(p.first_o[1] + row * D + lane * E)};
+  const auto cols_at = [&](const float* o, int64_t at) { return *reinterpret_cast<const Cols*>(o + at * D + lane * E); };
+  // a sequence's own first parts, and its prefix's (without a prefix that one holds anything and is not used)
+  float4 first[kCopies + 1];
+  Cols o[kCopies + 1];
 #pragma unroll
-  for (int w = 0; w < 2; ++w) {
-    if (w == 1 && first[0].w == 0.0f) break;
-    if (kSplit == 1 || warp == 0) sum.add(first[w].x, first[w].y, o[w].v);
-    const uint32_t others = __float_as_uint(first[w].z);
-    const int32_t c1 = others >> 10 & 1023, at = others >> 20 & 255;
+  for (int k = 0; k <= kCopies; ++k) {
+    const int64_t from = k < kCopies ? k * p.rows + row : row;
+    first[k] = p.first_ml[k < kCopies ? 0 : 1][from];
+    o[k] = cols_at(p.first_o[k < kCopies ? 0 : 1], from);
+  }
+  const bool shared = first[0].w != 0.0f;
+  if (kSplit == 1 || warp == 0) {
+#pragma unroll
+    for (int k = 0; k <= kCopies; ++k)
+      if (k < kCopies || shared) sum.add(first[k].x, first[k].y, o[k].v);
+  }
+#pragma unroll 1
+  for (int w = 0; w < (shared ? kCopies + 1 : kCopies); ++w) {
+    const uint32_t others = __float_as_uint(w == kCopies ? first[kCopies].z : first[0].z);
+    const int32_t c1 = others >> 10 & 1023, at = (others >> 20 & 255) + (w == kCopies ? 0 : 32 * w);
     const bool single = others >> 28 & 1;
 #pragma unroll 1
     for (int32_t c = (others & 1023) + 1 + (kSplit > 1 ? warp : 0); c <= c1; c += kJoinBatch * kSplit) {
@@ -910,7 +984,7 @@ __global__ void __launch_bounds__(kJoinThreads) prefix_join_kernel(const __grid_
         const int32_t run = min(c + y * kSplit, c1);
         const int64_t from = static_cast<int64_t>(single ? 2 * runs + run : 2 * run) * kTile + at;
         ml[y] = p.part_ml[from];
-        part[y] = *reinterpret_cast<const Cols*>(p.part + from * D + lane * E);
+        part[y] = cols_at(p.part, from);
       }
 #pragma unroll
       for (int y = 0; y < kJoinBatch; ++y)
@@ -940,7 +1014,10 @@ struct Layout {
   size_t stretches, shared, first_o[2], first_ml[2], part, part_ml, bytes;
 };
 
-Layout layout(int64_t B, int64_t T, int64_t heads, int64_t head_dim, int num_sms) {
+// Whether a sequence's rows of a kv head fit a quarter of a row tile.
+bool spreads(int64_t T, int64_t group) { return T * group <= kTile / 4; }
+
+Layout layout(int64_t B, int64_t T, int64_t heads, int64_t kv_heads, int64_t head_dim, int num_sms) {
   Layout l;
   size_t at = 0;
   const auto take = [&](size_t bytes) {
@@ -950,10 +1027,11 @@ Layout layout(int64_t B, int64_t T, int64_t heads, int64_t head_dim, int num_sms
   };
   const size_t rows = static_cast<size_t>(B) * T * heads, runs = static_cast<size_t>(imin64(num_sms, kMaxRuns));
   l.stretches = take((2 * static_cast<size_t>(B) + 1) * sizeof(Stretch));
-  l.shared = take(static_cast<size_t>(B) * 4);
+  l.shared = take((2 * static_cast<size_t>(B) + 1) * 4);
   for (int i = 0; i < 2; ++i) {
-    l.first_o[i] = take(rows * head_dim * 4);
-    l.first_ml[i] = take(rows * sizeof(float4));
+    const size_t copies = i == 0 && spreads(T, heads / kv_heads) ? 4 : 1;
+    l.first_o[i] = take(copies * rows * head_dim * 4);
+    l.first_ml[i] = take(copies * rows * sizeof(float4));
   }
   l.part = take(runs * 4 * kTile * head_dim * 4);
   l.part_ml = take(runs * 4 * kTile * sizeof(float2));
@@ -961,12 +1039,12 @@ Layout layout(int64_t B, int64_t T, int64_t heads, int64_t head_dim, int num_sms
   return l;
 }
 
-template <int D>
+template <int D, bool kSpread>
 cudaError_t launch(const PrefixArgs& x, void* workspace, int num_sms, cudaStream_t stream) {
   AttnArgs a = x.attn;
   if (a.T == 1) a.q_t = a.q_b;       // from one node to the next, through all sequences
   a.q_b = a.q_t;
-  const Layout l = layout(a.B, a.T, a.heads, D, num_sms);
+  const Layout l = layout(a.B, a.T, a.heads, a.cache.heads, D, num_sms);
   uint8_t* ws = static_cast<uint8_t*>(workspace);
   const Tiling t = tile_rows(a.T, a.group);
   const int runs = static_cast<int>(imin64(num_sms, kMaxRuns));
@@ -980,6 +1058,9 @@ cudaError_t launch(const PrefixArgs& x, void* workspace, int num_sms, cudaStream
   p.c = a.scale * 1.4426950408889634f;
   p.box_rows = box_rows(a.cache);
   p.q_box_bytes = static_cast<uint32_t>(t.tpt * a.group) * D * 2;
+  p.spread = kSpread;
+  p.rows = a.B * a.T * a.heads;
+  p.spread_bytes = static_cast<uint32_t>(a.T * a.group) * D * 2;
   p.shared = reinterpret_cast<int32_t*>(ws + l.shared);
   p.stretches = reinterpret_cast<Stretch*>(ws + l.stretches);
   for (int i = 0; i < 2; ++i) {
@@ -988,10 +1069,12 @@ cudaError_t launch(const PrefixArgs& x, void* workspace, int num_sms, cudaStream
   }
   p.part = reinterpret_cast<float*>(ws + l.part);
   p.part_ml = reinterpret_cast<float2*>(ws + l.part_ml);
-  Maps m;
-  if (!make_maps<D>(a, t.tpt, p.box_rows, a.B * a.T, 1, &m)) return cudaErrorInvalidValue;
+  Maps m, copy;                      // (of `copy` the queries: boxes of one sequence's nodes)
+  if (!make_maps<D>(a, t.tpt, p.box_rows, a.B * a.T, 1, &m) ||
+      !make_maps<D>(a, p.spread ? a.T : t.tpt, p.box_rows, a.B * a.T, 1, &copy))
+    return cudaErrorInvalidValue;
   const size_t smem = Cfg<D>::kRing + sizeof(PrefixSmem);
-  cudaError_t e = set_smem_limit<prefix_attn_kernel<D>>(smem);
+  cudaError_t e = set_smem_limit<prefix_attn_kernel<D, kSpread>>(smem);
   if (e != cudaSuccess) return e;
   cudaLaunchAttribute attr = pdl_attribute();
   cudaLaunchConfig_t cfg = {};
@@ -1007,15 +1090,15 @@ cudaError_t launch(const PrefixArgs& x, void* workspace, int num_sms, cudaStream
   cfg.gridDim = dim3(runs, 1, 1);
   cfg.blockDim = dim3(kThreads, 1, 1);
   cfg.dynamicSmemBytes = smem;
-  e = cudaLaunchKernelEx(&cfg, prefix_attn_kernel<D>, m.q, m.k, m.v, m.kn, m.vn, p);
+  e = cudaLaunchKernelEx(&cfg, prefix_attn_kernel<D, kSpread>, m.q, copy.q, m.k, m.v, m.kn, m.vn, p);
   if (e != cudaSuccess) return e;
-  const int64_t rows = a.B * a.T * a.heads;
+  const int64_t rows = p.rows;
   const bool split = rows <= 8 * num_sms;
   cfg.gridDim = dim3(static_cast<unsigned>(split ? rows : (rows + kJoinWarps - 1) / kJoinWarps), 1, 1);
   cfg.blockDim = dim3(kJoinThreads, 1, 1);
   cfg.dynamicSmemBytes = 0;
-  return split ? cudaLaunchKernelEx(&cfg, prefix_join_kernel<D, kJoinWarps>, p, static_cast<int32_t>(runs))
-               : cudaLaunchKernelEx(&cfg, prefix_join_kernel<D, 1>, p, static_cast<int32_t>(runs));
+  return split ? cudaLaunchKernelEx(&cfg, prefix_join_kernel<D, kJoinWarps, kSpread ? 4 : 1>, p, static_cast<int32_t>(runs))
+               : cudaLaunchKernelEx(&cfg, prefix_join_kernel<D, 1, kSpread ? 4 : 1>, p, static_cast<int32_t>(runs));
 }
 
 
@@ -1044,13 +1127,16 @@ size_t prefix_attn_workspace_bytes(int64_t B, int64_t T, int64_t heads, int64_t 
   if (heads / kv_heads > kTile) return 0;
   const size_t tree = tree_attn_workspace_bytes(B, T, heads, kv_heads, head_dim, num_sms);
   if (B * T * heads >= kMostRows) return tree;
-  const size_t shared = layout(B, T, heads, head_dim, num_sms).bytes;
+  const size_t shared = layout(B, T, heads, kv_heads, head_dim, num_sms).bytes;
   return shared > tree ? shared : tree;
 }
 
 cudaError_t launch_prefix_attn(const PrefixArgs& a, int64_t head_dim, void* workspace, int num_sms, cudaStream_t stream) {
   if (as_tree_attn(a, num_sms)) return launch_tree_attn(a.attn, head_dim, workspace, num_sms, stream);
-  return head_dim == 64 ? launch<64>(a, workspace, num_sms, stream) : launch<128>(a, workspace, num_sms, stream);
+  const bool spread = spreads(a.attn.T, a.attn.group);
+  if (head_dim == 64)
+    return spread ? launch<64, true>(a, workspace, num_sms, stream) : launch<64, false>(a, workspace, num_sms, stream);
+  return spread ? launch<128, true>(a, workspace, num_sms, stream) : launch<128, false>(a, workspace, num_sms, stream);
 }
 
 }  // namespace dflash2

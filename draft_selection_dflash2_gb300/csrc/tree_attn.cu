@@ -173,6 +173,7 @@ struct PartPlace {
         mls(kTeam ? reinterpret_cast<float2*>(ring + 2 * kTile * D * 4) : p.part_ml) {}
   // Row r's O in the tile, four columns every kStep float4, and its m and l.
   static constexpr int kStep = kTile;
+  static constexpr int copies() { return 1; }
   __device__ __forceinline__ float4* part(const AttnPlan& p, int tile, int r, int64_t) const {
     return parts + (static_cast<int64_t>(slot) * p.areas + tile) * (D / 4) * kTile + r;
   }
@@ -562,13 +563,18 @@ __global__ void __launch_bounds__(kThreads, 1)
           RingPos<S> at_v = seg_v;
           at_v.advance_far(2 * (j * step + off));
           wait_live(at_v.full(s.kv_full), at_v.parity(), &live, abort_flag, a.err);
+          const bool masked = drafted && a.mask != nullptr;
+          const int upto = drafted && !masked ? min(valid, node + 1) : valid;
+          const uint64_t m0 = masked ? mask_word(a, g.b, node, row_ok, 0) : ~0ull;
+          const uint64_t m1 = masked ? mask_word(a, g.b, node, row_ok, 1) : ~0ull;
 #pragma unroll
-          for (int w = 0; w < 4; ++w) vis[w] = seen_keys(a, drafted, valid, g.b, node, row_ok, w);
+          for (int w = 0; w < 4; ++w) vis[w] = keys_before(upto, w) & static_cast<uint32_t>((w < 2 ? m0 : m1) >> (w & 1) * 32);
           // the pipelines that take the drafted tile look through it together
           const bool both = g.tiles == 2;
-          bad_seen |= see_tile<D>(a, ring + at_v.slot * C::kTileBytes, drafted, valid, chunks, g.b, node, row_ok,
-                      both ? static_cast<int>(threadIdx.x) - kTile : r, both ? 2 * kTile : kTile, r, s.bad,
-                      [&]() { named_bar_sync(both ? 1 : 2 + i, both ? 2 * kTile : kTile); });
+          bad_seen |= see_tile<D>(a, ring + at_v.slot * C::kTileBytes, drafted, valid, chunks,
+                                  both ? static_cast<int>(threadIdx.x) - kTile : r, both ? 2 * kTile : kTile, r, s.bad,
+                                  [&](int w) { return vis[w]; },
+                                  [&]() { named_bar_sync(both ? 1 : 2 + i, both ? 2 * kTile : kTile); });
         }
 #pragma unroll 1
         for (int c = 0; c < chunks; ++c, at_s.advance()) {

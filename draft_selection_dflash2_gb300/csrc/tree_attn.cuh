@@ -82,36 +82,30 @@ __device__ __noinline__ void rescale_rows(uint32_t tm, int cols, float f) {
 // (the weights of the definition do not).
 __device__ __forceinline__ float weighted(float v, float f) { return fabsf(v) < INFINITY ? v * f : v; }
 
-// The keys 32 w .. 32 w + 31 of a tile that is not whole which the row sees, a bit each: of `valid` cached keys, or of
-// the drafted nodes.
+// The nodes 64 y .. 64 y + 63 that the mask lets the row see.
+__device__ __forceinline__ uint64_t mask_word(const AttnArgs& a, int64_t b, int node, bool row_ok, int y) {
+  const int words = (a.T + 63) >> 6;
+  return row_ok && y < words ? a.mask[(b * a.T + node) * words + y] : 0ull;
+}
+// Which of the keys 32 w .. 32 w + 31 come before `upto`, a bit each.
+__device__ __forceinline__ uint32_t keys_before(int upto, int w) {
+  const int k = upto - 32 * w;
+  return k >= 32 ? 0xFFFFFFFFu : k <= 0 ? 0u : (1u << k) - 1u;
+}
+// The keys 32 w .. 32 w + 31 of a tile that is not whole which the row sees: of `valid` cached keys, or of the drafted nodes.
 __device__ __forceinline__ uint32_t seen_keys(const AttnArgs& a, bool drafted, int valid, int64_t b, int node, bool row_ok,
                                               int w) {
-  const int k = (drafted && a.mask == nullptr ? min(valid, node + 1) : valid) - 32 * w;
-  uint32_t see = k >= 32 ? 0xFFFFFFFFu : k <= 0 ? 0u : (1u << k) - 1u;
-  if (drafted && a.mask != nullptr) {
-    const int words = (a.T + 63) >> 6;
-    const uint64_t m = row_ok && w / 2 < words ? a.mask[(b * a.T + node) * words + w / 2] : 0ull;
-    see &= static_cast<uint32_t>(w & 1 ? m >> 32 : m);
-  }
-  return see;
+  const uint32_t see = keys_before(drafted && a.mask == nullptr ? min(valid, node + 1) : valid, w);
+  return drafted && a.mask != nullptr ? see & static_cast<uint32_t>(mask_word(a, b, node, row_ok, w / 2) >> (w & 1) * 32) : see;
 }
 
-// The V tile of a tile that is not whole, without what nobody may see.  A drafted tile is looked through by
-// `threads` threads (tid), which meet() waits for; returns whether the row sees a node that was zeroed.
-template <int D, class Meet>
-__device__ __forceinline__ bool see_tile(const AttnArgs& a, uint8_t* v_tile, bool drafted, int valid, int chunks, int64_t b,
-                                         int node, bool row_ok, int tid, int threads, int r, uint32_t* bad, const Meet& meet) {
-  if (!drafted) {
-    zero_rows<D>(v_tile, valid, chunks * kChunk, r, kTile);
-    asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
-    return false;
-  }
-  if (tid < 4) bad[tid] = 0;
-  __syncwarp();
-  meet();
+// Zeroes what is not finite of T drafted nodes' values (this thread's share of `threads`), and notes the nodes in bad.
+template <int D>
+__device__ __forceinline__ bool clear_nonfinite(uint8_t* v_tile, int T, int tid, int threads, uint32_t* bad) {
+  bool any = false;
 #pragma unroll
   for (int half = 0; half < Cfg<D>::kHalves; ++half)
-    for (int x = tid; x < a.T * 8; x += threads) {
+    for (int x = tid; x < T * 8; x += threads) {
       uint4* at = reinterpret_cast<uint4*>(v_tile + half * kTile * 128 + x * 16);
       uint4 q = *at;
       uint32_t* e = &q.x;
@@ -124,16 +118,40 @@ __device__ __forceinline__ bool see_tile(const AttnArgs& a, uint8_t* v_tile, boo
       if (hit) {
         *at = q;
         atomicOr(&bad[x >> 8], 1u << ((x >> 3) & 31));
+        any = true;
       }
     }
+  return any;
+}
+
+// Whether the row sees one of the bad nodes: seen(w) are the nodes 32 w .. 32 w + 31 that it sees.
+template <class Seen>
+__device__ __forceinline__ bool sees_bad(const uint32_t* bad, const Seen& seen) {
+  uint32_t some = 0;
+#pragma unroll
+  for (int w = 0; w < 4; ++w)
+    if (bad[w] != 0) some |= seen(w) & bad[w];
+  return some != 0;
+}
+
+// The V tile of a tile that is not whole, without what nobody may see.  A drafted tile is looked through by
+// `threads` threads (tid), which meet() waits for; returns whether the row sees a node that was zeroed.
+template <int D, class Seen, class Meet>
+__device__ __forceinline__ bool see_tile(const AttnArgs& a, uint8_t* v_tile, bool drafted, int valid, int chunks, int tid,
+                                         int threads, int r, uint32_t* bad, const Seen& seen, const Meet& meet) {
+  if (!drafted) {
+    zero_rows<D>(v_tile, valid, chunks * kChunk, r, kTile);
+    asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+    return false;
+  }
+  if (tid < 4) bad[tid] = 0;
+  __syncwarp();
+  meet();
+  clear_nonfinite<D>(v_tile, a.T, tid, threads, bad);
   __syncwarp();
   asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
   meet();
-  uint32_t seen = 0;
-#pragma unroll
-  for (int w = 0; w < 4; ++w)
-    if (bad[w] != 0) seen |= seen_keys(a, true, valid, b, node, row_ok, w) & bad[w];
-  return seen != 0;
+  return sees_bad(bad, seen);
 }
 
 // The softmax of a chunk, of the thread's row: S (64 columns at tm_s) becomes P in two terms, and the row's maximum m and
@@ -202,6 +220,79 @@ __device__ __forceinline__ void softmax_chunk(uint32_t tm_sb, uint32_t tm_o, flo
   *l += sum.x + sum.y;
 }
 
+__device__ __forceinline__ void tmem_ld_x16(uint32_t taddr, float (&v)[16]) {
+  uint32_t r[16];
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, [%16];"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
+        "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+      : "r"(taddr)
+      : "memory");
+#pragma unroll
+  for (int i = 0; i < 16; ++i) v[i] = __uint_as_float(r[i]);
+}
+__device__ __forceinline__ void tmem_st_x8(uint32_t taddr, const uint32_t (&r)[8]) {
+  asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"r"(taddr), "r"(r[0]), "r"(r[1]),
+               "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7])
+               : "memory");
+}
+
+// The softmax of a quarter of a chunk: the 16 keys from 16 w on; P is 0 for the others.  sees(): which of the 16 the row sees.
+template <int D, class Sees, class Wait>
+__device__ __forceinline__ void softmax_quarter(uint32_t tm_sb, uint32_t tm_o, float scale, int w, bool partial,
+                                                const Sees& sees, bool first, bool row_ok, float* m, float* l,
+                                                const Wait& wait_products) {
+  float z[16];
+  tmem_ld_x16(tm_sb + 16 * w, z);
+  tmem_ld_wait();
+  asm volatile("" : "+f"(z[0]), "+f"(z[1]), "+f"(z[2]), "+f"(z[3]), "+f"(z[4]), "+f"(z[5]), "+f"(z[6]), "+f"(z[7]));
+  asm volatile("" : "+f"(z[8]), "+f"(z[9]), "+f"(z[10]), "+f"(z[11]), "+f"(z[12]), "+f"(z[13]), "+f"(z[14]), "+f"(z[15]));
+  if (partial) {
+    const uint32_t v = sees();
+#pragma unroll
+    for (int y = 0; y < 16; ++y)
+      if (!(v >> y & 1u)) z[y] = -INFINITY;
+  }
+  float tops[2] = {-INFINITY, -INFINITY};
+#pragma unroll
+  for (int y = 0; y < 16; y += 2) tops[y / 2 & 1] = fmaxf(tops[y / 2 & 1], fmaxf(z[y], z[y + 1]));
+  const float top = fmaxf(tops[0], tops[1]) * scale;
+  if (first) {
+    *m = top;
+  } else if (__any_sync(0xFFFFFFFFu, row_ok && top > *m + kRescale)) {   // (see softmax_chunk)
+    const float m1 = fmaxf(*m, top);
+    const float f = *m == -INFINITY ? 1.0f : exp2_approx(*m - m1);
+    *m = m1;
+    *l *= f;
+    wait_products();
+    __syncwarp();
+    tc_fence_after();
+    rescale_rows(tm_o, D, f);
+  }
+  const float mm = *m == -INFINITY ? 0.0f : *m;
+  float sum = 0.0f;
+  uint32_t hi[8], lo[8], zero[8] = {};
+#pragma unroll
+  for (int y = 0; y < 16; y += 2) {
+    const float p0 = exp2_approx(fmaf(z[y], scale, -mm)), p1 = exp2_approx(fmaf(z[y + 1], scale, -mm));
+    sum += p0 + p1;
+    const uint32_t b = pack_bf16(p0, p1);
+    hi[y / 2] = b;
+    lo[y / 2] = pack_bf16(p0 - __uint_as_float(b << 16), p1 - __uint_as_float(b & 0xFFFF0000u));
+  }
+  *l += sum;
+#pragma unroll
+  for (int x = 0; x < 4; ++x) {
+    if (x == w) {
+      tmem_st_x8(tm_sb + 8 * x, hi);
+      tmem_st_x8(tm_sb + kChunk / 2 + 8 * x, lo);
+    } else {
+      tmem_st_x8(tm_sb + 8 * x, zero);
+      tmem_st_x8(tm_sb + kChunk / 2 + 8 * x, zero);
+    }
+  }
+}
+
 // <q, k> over D bf16 each.
 template <int D>
 __device__ __forceinline__ float dot_bf16(const uint16_t* q, const uint16_t* k) {
@@ -241,6 +332,11 @@ __device__ __noinline__ void sum_again(const Plan& p, Walk walk, uint8_t* ring) 
         bool finite = true;
 #pragma unroll
         for (int e = 0; e < E; ++e) finite &= place.whole ? finite_bf16(out[e]) : fabsf(part[e]) < INFINITY;
+        for (int k = 1; k < place.copies(); ++k) {
+          const float* more = reinterpret_cast<const float*>(place.part(p, tile, r + k * 32, orow)) + lane * E;
+#pragma unroll
+          for (int e = 0; e < E; ++e) finite &= fabsf(more[e]) < INFINITY;
+        }
         if (__all_sync(0xFFFFFFFFu, finite)) continue;
         const uint16_t* q = a.q + g.q_row(a, node) + hq * a.q_h;
         float m = -INFINITY, l = 0.0f, o[E] = {};   // l: of the lane's keys
@@ -294,6 +390,8 @@ __device__ __noinline__ void sum_again(const Plan& p, Walk walk, uint8_t* ring) 
 #pragma unroll
           for (int e = 0; e < E; ++e) part[e] = o[e];
           if (lane == 0) place.put_ml(p, tile, r, orow, m, -l);        // (see PartSum::add)
+          for (int k = 1; k < place.copies(); ++k)
+            if (lane == 0) place.put_ml(p, tile, r + k * 32, orow, -INFINITY, 0.0f);
         }
       }
     }

@@ -17,7 +17,13 @@ of 64): attention (2 sequences of 131072 positions, one token each),
 attention_block (64 blocks of 17 over lengths of 1500 to 12000), attention_tree (8
 trees of 64 nodes over 16384 positions), commit (256 paths of 1 to 64 nodes),
 scores (16 blocks of 17, 1 to 17 accepted, over lengths of 4096 to 32768) and
-evict (16 sequences of 4096 to 32768 positions to 8001).
+evict (16 sequences of 4096 to 32768 positions to 8001).  So have the operators around
+them: prefix (64 sequences of one token behind 8192 shared positions and 125 to 1000 of their
+own), prefix_block (32 blocks of 17 in four groups behind 16384 shared and 250 to 2000 own
+ones), rope (72 heads of 16 x 4096 tokens, 64 of 128 elements rotated in neighbouring pairs),
+append (8 prompts of 2048 to 4096 tokens, queries rotated along), logits (128 blocks of 17 over
+V = 151936 with penalties, a bias and, for every second sequence, about 200 allowed tokens a
+node) and counts (32 prompts of 16384 to 32768 tokens).
 """
 import argparse
 import os
@@ -81,6 +87,61 @@ def cache_stage(torch, h, rng, stage):
     return lambda: api.tree_attention(h, q, cache, lens, k, v, tree_mask=mask, workspace=ws)
 
 
+def serve_stage(torch, h, rng, stage):
+    """One call of an operator around the cache (see the module's text for its shape)."""
+    heads, H, dim, page = 64, 8, 128, 64
+    g = torch.Generator(device="cuda")
+    g.manual_seed(9)
+
+    def randn(*shape):
+        return torch.empty(shape, dtype=torch.bfloat16, device="cuda").normal_(generator=g)
+
+    def i32(a):
+        return torch.from_numpy(np.ascontiguousarray(a, dtype=np.int32)).cuda()
+
+    def pool(table):
+        shape = (int(table.max()) + 1, page, H, dim)
+        return api.KVCache(randn(*shape), randn(*shape), i32(table))
+
+    if stage in ("prefix", "prefix_block"):
+        B, T, groups, shared, own = {"prefix": (64, 1, 1, 8192, 1000), "prefix_block": (32, 17, 4, 16384, 2000)}[stage]
+        first, mine = shared // page, -(-(own + T) // page)
+        group = np.arange(B) * groups // B
+        table = np.concatenate([group[:, None] * first + np.arange(first),
+                                groups * first + np.arange(B * mine).reshape(B, mine)], axis=1)
+        cache, starts = pool(table), i32(np.arange(groups + 1) * B // groups)
+        lens, prefix = i32(shared + rng.integers(own // 8, own + 1, B)), i32(np.full(groups, shared))
+        q, k, v = randn(B, T, heads, dim), randn(B, T, H, dim), randn(B, T, H, dim)
+        ws = torch.empty(api.prefix_attention_workspace(h, B, T, heads, H, dim), dtype=torch.uint8, device="cuda")
+        return lambda: api.prefix_attention(h, q, cache, lens, prefix, starts, k, v, workspace=ws)
+    if stage == "rope":
+        x = randn(16, 4096, heads + 16, dim)[:, :, :heads + 8]
+        out, r = torch.empty(x.shape, dtype=x.dtype, device="cuda"), api.Rope(64, theta=500000.0, interleaved=True)
+        return lambda: api.rope(h, x, r, out=out)
+    if stage == "append":
+        B, T = 8, 4096
+        cache, count = pool(np.arange(B * T // page).reshape(B, -1)), i32(rng.integers(T // 2, T + 1, B))
+        q, k, v = randn(B, T, heads + 2 * H, dim).split([heads, H, H], 2)
+        out, lens, r = torch.zeros((B, T, heads, dim), dtype=q.dtype, device="cuda"), i32(np.zeros(B)), api.Rope(dim)
+        return lambda: api.cache_append(h, k, v, cache, lens, r, count=count, q=q, q_out=out)
+    B, N = (128, 17) if stage == "logits" else (32, 32768)
+    tokens, counts = i32(rng.integers(0, V, (B, N))), torch.zeros((B, V), dtype=torch.int32, device="cuda")
+    if stage == "counts":
+        count = i32(rng.integers(N // 2, N + 1, B))
+        return lambda: api.token_counts(h, tokens, counts, count, prompt=True)
+    api.token_counts(h, i32(rng.integers(0, V, (B, 2000))), counts)
+    api.token_counts(h, i32(rng.integers(0, V, (B, 2000))), counts, prompt=True)
+    logits, bias = randn(B, N, V), torch.randn((1, V), generator=g, device="cuda")
+    allowed = np.full((B, N, -(-V // 32)), -1, np.int32)
+    for b in range(0, B, 2):
+        bits = np.zeros((N, allowed.shape[2] * 32), np.uint8)
+        bits[np.arange(N)[:, None], rng.integers(0, V, (N, 200))] = 1
+        allowed[b] = np.packbits(bits, axis=-1, bitorder="little").view(np.int32)
+    allowed = i32(allowed)
+    factor = [torch.full((B,), x, device="cuda") for x in (1.1, 0.2, 0.2)]
+    return lambda: api.logits_adjust(h, logits, counts, tokens, None, *factor, bias, allowed, out=logits)
+
+
 def main():
     import torch
 
@@ -88,7 +149,8 @@ def main():
     ap.add_argument("--stage", required=True,
                     choices=["topk", "pairs", "walk0", "walk1", "conv", "verify0", "verify1", "lmhead",
                              "lmhead_gate", "viterbi", "eval", "proj", "gemm_conv", "attention", "attention_block",
-                             "attention_tree", "commit", "scores", "evict"])
+                             "attention_tree", "commit", "scores", "evict", "prefix", "prefix_block", "rope", "append",
+                             "logits", "counts"])
     ap.add_argument("--B", type=int, default=128)
     ap.add_argument("--reps", type=int, default=3)
     args = ap.parse_args()
@@ -98,6 +160,8 @@ def main():
     rng = np.random.default_rng(0)
     if args.stage in ("attention", "attention_block", "attention_tree", "commit", "scores", "evict"):
         run = cache_stage(torch, h, rng, args.stage)
+    elif args.stage in ("prefix", "prefix_block", "rope", "append", "logits", "counts"):
+        run = serve_stage(torch, h, rng, args.stage)
     elif args.stage == "topk":
         U = bf(torch, synth.logits_planted(rng, B * L, V))
         run = lambda: api.topk(h, U)  # noqa: E731
