@@ -31,7 +31,10 @@ namespace {
 
 constexpr int kListThreads = 1024;
 constexpr int64_t kMostUnits = int64_t(1) << 26, kMostRows = int64_t(1) << 26;
-constexpr int kListed = 32;              // most stretches that producers list for themselves, a lane each
+// Most stretches that every CTA's producer lists for itself, in shared memory; more of them are listed by a kernel before.  (36
+// stretches, 32 x 17 over 16384: 346 us against 352 with the kernel; 57, 50 x 9: 50.7 and 52.5; 65, 64 x 1 over 8192: 75.9 and
+// 75.6, over 16384: 83.6 and 77.)
+constexpr int kListed = 64;
 constexpr int kFewGroups = 1024;         // groups whose starts and lengths are held in shared memory while the list is made
 constexpr int kSegs = 4;                 // segments that a pipeline's warps may lag behind the producer
 
@@ -127,47 +130,62 @@ __device__ __forceinline__ Stretch own_stretch(const PrefixPlan& p, int32_t b, i
   return {{0, 0}, max(1, (len + kTile - 1) / kTile - tile0 + (p.a.k_new != nullptr ? 1 : 0)), b, p.a.T, tile0, len};
 }
 
-// Lists up to 32 stretches with one warp, a lane each.  Small calls run this with an empty instruction cache, so it
+// Lists up to kListed stretches with one warp, a lane every 32nd.  Small calls run this with an empty instruction cache, so it
 // is short, and its loads do not wait for one another.
 __device__ __forceinline__ void list_few(const PrefixPlan& p, Stretch* list, bool flag) {
   const AttnArgs& a = p.a;
   uint32_t* err = flag ? a.err : nullptr;
-  const int32_t B = static_cast<int32_t>(a.B), lane = threadIdx.x & 31, b = lane - p.groups;
-  const bool is_group = lane < p.groups, is_own = !is_group && b < B;
-  int32_t s0 = 0, s1 = 0, len = 0x7FFFFFFF, most = 0;
-  if (is_group) {
-    s0 = group_start(p, lane);
-    s1 = group_start(p, lane + 1);
-    most = kv_clamp(p.shared_len[lane], a.cache.capacity, err);
-  }
-  if (is_own) len = kv_clamp(a.cache_len[b], a.cache.capacity, err);
-  bool bad = is_group && (s0 < 0 || s1 < s0 || s1 > B || (lane == 0 && s0 != 0) || (lane == p.groups - 1 && s1 != B));
-  bad = __any_sync(0xFFFFFFFFu, bad);                  // starts that are none: nothing is shared
-  Stretch s = {};
-  int32_t tile0 = 0;
+  const int32_t B = static_cast<int32_t>(a.B), lane = threadIdx.x & 31;
+  bool bad = false;
 #pragma unroll 1
-  for (int32_t g = 0; g < (bad ? 0 : p.groups); ++g) {
-    const int32_t g0 = __shfl_sync(0xFFFFFFFFu, s0, g), g1 = __shfl_sync(0xFFFFFFFFu, s1, g);
-    const int32_t limit = __shfl_sync(0xFFFFFFFFu, most, g);
-    const bool member = is_own && b >= g0 && b < g1;
-    const int32_t least = min(limit, __reduce_min_sync(0xFFFFFFFFu, member ? len : 0x7FFFFFFF));
-    bad |= least < limit;
-    const int32_t tiles = g1 - g0 < 2 ? 0 : least / kTile;   // a sequence by itself shares nothing
-    if (lane == g) s = prefix_stretch(p, s0, s1, tiles);
-    if (member) tile0 = tiles;
+  for (int32_t v = lane; v <= p.num_stretches; v += 32) {
+    Stretch s = {};
+    int32_t len = 0;
+    if (v < p.groups) {
+      const int32_t s0 = group_start(p, v), s1 = group_start(p, v + 1);
+      len = p.shared_len[v];
+      bad |= s0 < 0 || s1 < s0 || s1 > B || (v == 0 && s0 != 0) || (v == p.groups - 1 && s1 != B);
+      s.b = s0;
+      s.nodes = s1 - s0;                               // (its sequences, for now)
+    } else if (v < p.num_stretches) {
+      len = a.cache_len[v - p.groups];
+      s.b = v - p.groups;
+    }
+    s.len = kv_clamp(len, a.cache.capacity, err);
+    list[v] = s;
+  }
+  bad = __any_sync(0xFFFFFFFFu, bad);                  // starts that are none: nothing is shared
+  const bool none = bad;
+  __syncwarp();
+#pragma unroll 1
+  for (int32_t g = 0; g < p.groups; ++g) {
+    const Stretch s = list[g];
+    int32_t least = s.len;
+    for (int32_t b = s.b + lane; !none && b < s.b + s.nodes; b += 32) least = min(least, list[p.groups + b].len);
+    least = __reduce_min_sync(0xFFFFFFFFu, least);
+    bad |= least < s.len;
+    const int32_t tiles = none || s.nodes < 2 ? 0 : least / kTile;   // a sequence by itself shares nothing
+    for (int32_t b = s.b + lane; tiles > 0 && b < s.b + s.nodes; b += 32) list[p.groups + b].tile0 = tiles;
+    __syncwarp();
+    if (lane == 0) list[g] = none ? Stretch{} : prefix_stretch(p, s.b, s.b + s.nodes, tiles);
   }
   if (bad && lane == 0) raise_error(err, DFLASH2_DEVERR_BAD_LENGTH);
-  if (is_own) s = own_stretch(p, b, tile0, len);
-  uint64_t total;
-  const uint64_t before = warp_before(cost_of(p, s), &total);
-  s.before[0] = static_cast<uint32_t>(before >> 32);
-  s.before[1] = static_cast<uint32_t>(before);
-  list[lane] = s;                                      // (lanes past the last stretch hold the totals)
-  if (lane == 0) {
-    s = {};
-    s.before[0] = static_cast<uint32_t>(total >> 32);
-    s.before[1] = static_cast<uint32_t>(total);
-    list[p.num_stretches] = s;
+  __syncwarp();
+  // a lane's stretches lie beside one another here
+  const int32_t each = (p.num_stretches + 32) / 32, v0 = lane * each, v1 = min(v0 + each, p.num_stretches);
+  uint64_t own = 0, total;
+#pragma unroll 1
+  for (int32_t v = v0; v < v1; ++v) {
+    Stretch s = list[v];
+    if (v >= p.groups) list[v] = s = own_stretch(p, s.b, s.tile0, s.len);
+    own += cost_of(p, s);
+  }
+  uint64_t at = warp_before(own, &total);
+#pragma unroll 1
+  for (int32_t v = v0; v < min(v0 + each, p.num_stretches + 1); ++v) {
+    list[v].before[0] = static_cast<uint32_t>(at >> 32);
+    list[v].before[1] = static_cast<uint32_t>(at);
+    at += cost_of(p, list[v]);
   }
   __syncwarp();
 }
