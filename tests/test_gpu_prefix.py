@@ -253,6 +253,57 @@ def test_infinite_and_nan_values(handle, groups, T, heads, H, D, page):
         assert torch.isfinite(out[1:, ..., D - 1]).all() and handle.device_error() == 0
 
 
+@pytest.mark.parametrize("T,heads,H,D", [(3, 8, 2, 128), (9, 12, 2, 64), (17, 16, 2, 128), (5, 4, 2, 64)])
+@pytest.mark.parametrize("tree", [True, False])
+def test_infinite_and_nan_drafted_values(handle, T, heads, H, D, tree):
+    """They reach the rows that see their nodes, of their sequences alone; many short items follow one another on a CTA."""
+    gen = torch.Generator(device="cuda").manual_seed(T)
+    rng = np.random.default_rng(T)
+    groups = [(256, [int(n) for n in rng.integers(0, 50, 100)]), (130, [int(n) for n in rng.integers(0, 200, 60)])]
+    cache, rows, cl, pl, ps = shared_cache(gen, groups, H, D, 16, 340, room=4000)
+    B = len(rows)
+    q, kn, vn = (randn(gen, B, T, n, D) for n in (heads, H, H))
+    sees = mask = None
+    if tree:
+        s = random_tree(rng, B, T)
+        sees, mask = torch.from_numpy(s).cuda(), words(s)
+    for b in range(0, B, 3):
+        vn[b, b % T, b % H, b % D] = (INF, -INF, NAN)[b // 3 % 3]
+    kn[7, T - 1, 0] = NAN
+    out, _ = api.prefix_attention(handle, q, cache, cl, pl, ps, kn, vn, tree_mask=mask)
+    want = definition(q, rows, kn, vn, sees, D ** -0.5)
+    want[0][7, T - 1, :heads // H] = NAN       # a NaN score makes its row's softmax NaN (the definition's helper takes that for an empty row)
+    check(out, want)
+    again, _ = api.prefix_attention(handle, q, cache, cl, pl, ps, kn, vn, tree_mask=mask)
+    assert torch.equal(out.view(torch.int16), again.view(torch.int16)) and handle.device_error() == 0
+
+
+@pytest.mark.parametrize("first,second", [(30, 0), (31, 0), (29, 3), (61, 1), (62, 0), (63, 0), (64, 0), (40, 24), (1, 64)])
+def test_any_number_of_stretches(handle, first, second):
+    """Around the numbers of groups and sequences at which the list of stretches is made in another way."""
+    gen = torch.Generator(device="cuda").manual_seed(first)
+    rng = np.random.default_rng(first)
+    groups = [(384, [int(n) for n in rng.integers(0, 90, first)])]
+    groups += [(130, [int(n) for n in rng.integers(0, 90, second)])] if second else []
+    cache, rows, cl, pl, ps = shared_cache(gen, groups, 1, 64, 16, 480, room=40000)
+    B = len(rows)
+    q, kn, vn = (randn(gen, B, 2, n, 64) for n in (4, 1, 1))
+    out, lse = api.prefix_attention(handle, q, cache, cl, pl, ps, kn, vn)
+    check(out, definition(q, rows, kn, vn, None, 64 ** -0.5))
+    check_lse(lse, *logsumexp(q, rows, kn, None, 64 ** -0.5))
+    assert handle.device_error() == 0
+    # one sequence shorter than its group's prefix, and starts that are none
+    short = cl.clone()
+    short[B - 1] = 120
+    out, _ = api.prefix_attention(handle, q, cache, short, pl, ps, kn, vn)
+    assert handle.device_error() == 0x10
+    cut = rows[:-1] + [tuple(x[:120] for x in rows[-1])]
+    check(out, definition(q, cut, kn, vn, None, 64 ** -0.5))
+    out, _ = api.prefix_attention(handle, q, cache, cl, pl, ps + 1, kn, vn)
+    assert handle.device_error() == 0x10
+    check(out, definition(q, rows, kn, vn, None, 64 ** -0.5))
+
+
 def test_a_graph_replays_on_new_lengths_and_groups(handle):
     gen = torch.Generator(device="cuda").manual_seed(7)
     B, T, heads, H, D = 6, 3, 8, 2, 128
