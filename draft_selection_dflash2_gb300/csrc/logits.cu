@@ -16,6 +16,8 @@
 //   bytes at a time; alone they take 131 us.  (Every thread adjusting its own vector: 470; masks fetched by each thread, partly
 //   masked vectors read: 220 to 195; the listed vectors' loads after the others: 189; 4 of their rows at once: 177.)
 //   At most 4 CTAs on an SM: more of them spill (184, 204).
+//   a bias of every token: all vectors are listed, 262 us, 198 at a copy's rate; two rows of a thread are under way and the
+//   next two on their way to L2 (290 without; 4 or 8 rows ahead: 265, 273).
 // 128 blocks over 5000 tokens make 384 CTAs: their nodes are cut as well, 45 to 33 us.
 #include "launch.h"
 #include "serve.h"
@@ -181,6 +183,8 @@ __global__ void __launch_bounds__(kThreads, 4) logits_adjust_kernel(const __grid
       may[y] = t >= t_end ? 0u : restricted ? may_of(t, vec) & vec_full : vec_full;
       w[y] = make_uint4(0, 0, 0, 0);
       if (may[y] != 0) w[y] = *reinterpret_cast<const uint4*>(src + t * a.x_t + vec_col);
+      // the next rows' way to L2
+      if (t + kRows * step < t_end) asm volatile("prefetch.global.L2 [%0];" ::"l"(src + (t + kRows * step) * a.x_t + vec_col));
     }
   };
   if (busy) fetch(first);
