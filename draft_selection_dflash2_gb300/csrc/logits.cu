@@ -183,7 +183,7 @@ __global__ void __launch_bounds__(kThreads, 4) logits_adjust_kernel(const __grid
       may[y] = t >= t_end ? 0u : restricted ? may_of(t, vec) & vec_full : vec_full;
       w[y] = make_uint4(0, 0, 0, 0);
       if (may[y] != 0) w[y] = *reinterpret_cast<const uint4*>(src + t * a.x_t + vec_col);
-      // the next rows' way to L2
+      // the next rows' way to L2, whether they are needed or not (only the needed ones: 303 us where 262 are said above)
       if (t + kRows * step < t_end) asm volatile("prefetch.global.L2 [%0];" ::"l"(src + (t + kRows * step) * a.x_t + vec_col));
     }
   };
@@ -280,7 +280,8 @@ __global__ void __launch_bounds__(kThreads, 4) logits_adjust_kernel(const __grid
 // ---------------------------------------------------------------------------
 // counts: a thread takes a token.  Additions and ORs of whole numbers give the same result in any order.  A
 // prompt's common tokens come thousands of times: once a flag is set, later ones
-// only read it.
+// only read it.  Bound by the launch (128 paths of up to 17: 3.1 us), and by scattered sectors of the counts (32 prompts of
+// 16384 to 32768 tokens: 5.7 us, 9.4 MB in 32-byte sectors from L2).
 // ---------------------------------------------------------------------------
 __global__ void __launch_bounds__(kThreads) token_counts_kernel(const CountArgs a) {
   pdl_wait();

@@ -22,7 +22,7 @@ them: prefix (64 sequences of one token behind 8192 shared positions and 125 to 
 own), prefix_block (32 blocks of 17 in four groups behind 16384 shared and 250 to 2000 own
 ones), rope (72 heads of 16 x 4096 tokens, 64 of 128 elements rotated in neighbouring pairs),
 append (8 prompts of 2048 to 4096 tokens, queries rotated along), logits (128 blocks of 17 over
-V = 151936 with penalties, a bias and, for every second sequence, about 200 allowed tokens a
+V = 151936 with penalties, 300 biases and, for every second sequence, about 200 allowed tokens a
 node) and counts (32 prompts of 16384 to 32768 tokens).
 """
 import argparse
@@ -131,7 +131,8 @@ def serve_stage(torch, h, rng, stage):
         return lambda: api.token_counts(h, tokens, counts, count, prompt=True)
     api.token_counts(h, i32(rng.integers(0, V, (B, 2000))), counts)
     api.token_counts(h, i32(rng.integers(0, V, (B, 2000))), counts, prompt=True)
-    logits, bias = randn(B, N, V), torch.randn((1, V), generator=g, device="cuda")
+    logits, bias = randn(B, N, V), torch.zeros((1, V), device="cuda")
+    bias[0, torch.from_numpy(rng.permutation(V)[:300]).cuda()] = 1.5
     allowed = np.full((B, N, -(-V // 32)), -1, np.int32)
     for b in range(0, B, 2):
         bits = np.zeros((N, allowed.shape[2] * 32), np.uint8)
