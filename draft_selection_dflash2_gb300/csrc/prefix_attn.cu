@@ -1122,21 +1122,26 @@ cudaError_t launch(const PrefixArgs& x, void* workspace, int num_sms, cudaStream
 
 // Whether a call is taken as tree attention, which reads every sequence's keys for itself: where the nodes of a
 // group's sequences are no rows of one operand, where the costs would not fit 32 bits, and where sharing cannot
-// save what it costs.  A unit of one sequence's tiles takes 1.1 us (one row tile) or 2.1 (a pair), and its share of
-// a prefix's full pairs 2.1 us * rows / 256; at most all tiles of all sequences but one of each group are saved.  The lengths
-// are on the device, so the capacity stands for them.  Measured on 60 calls (saved at most, tree attention against this, us): 1.7: 12.1
-// and 16.5; 3.4: 19.0 and 17.0; 4.0: 28.7 and 38.6; 5.5: 23.1 and 19.5; 10.8: 24.4 and 19.7; 21: 48.6 and 31.9; 52: 94 and 32.5;
-// the worst above 5 was 17 groups of few or no shared tiles, 28: 52.6 and 57.8.
-bool as_tree_attn(const PrefixArgs& x, int num_sms) {
+// save what it costs.  Saved (us): a unit of one sequence's tiles takes 1.1 (one row tile) or 2.1 (a pair) on an SM, its share of
+// a prefix's full pairs 2.1 rows / 256, and at most all tiles of all sequences but one of each group are saved; the
+// lengths are on the device, so the capacity stands for them.  Spent: 6 for the list and the join, 8 for each SM's
+// items of prefixes (queries, first S, 256 rows of O on their way out), and every row's sums of two parts in fp32, written and
+// read, at 4 TB/s.  Measured on 70 calls (saved, spent: tree attention against this, us): 4.4, 6.5: 15.9 and 19.3; 5.4, 12:
+// 29 and 37; 10, 35: 54 and 68; 19, 62: 78 and 118; 26, 27: 64 and 88; above: 10.6, 6.5: 27 and 24; 12.2, 8.1: 36 and 33; 16, 7: 43
+// and 35; 33, 10: 53 and 49; 302, 7: 267 and 102.  The worst that is taken here: 9.9, 6.2: 20 and 27, with 222 shared positions
+// where the capacity is 1200.
+bool as_tree_attn(const PrefixArgs& x, int64_t head_dim, int num_sms) {
   const AttnArgs& a = x.attn;
   if (a.B > 1 && a.T > 1 && a.q_b != a.T * a.q_t) return true;
   const Tiling t = tile_rows(a.T, a.group);
-  const int64_t tiles = a.cache.capacity / kTile + 2, heads = a.cache.heads;
+  const int64_t tiles = a.cache.capacity / kTile + 2, heads = a.cache.heads, rows = a.B * a.T * a.heads;
+  const int64_t prefix_pairs = (a.B * a.T + t.tpt - 1) / t.tpt / 2 + 1;
   // a stretch's items and units, the prefixes' row tiles being those of all nodes and one more a group
-  if (heads * tiles * (a.B * t.pairs + (a.B * a.T + t.tpt - 1) / t.tpt / 2 + a.B + 1) >= kMostUnits || a.B * a.T * a.heads >= kMostRows)
-    return true;
+  if (heads * tiles * (a.B * t.pairs + prefix_pairs + a.B) >= kMostUnits || rows >= kMostRows) return true;
   const double unit = 2.1 * (t.row_tiles / 2) + 1.1 * (t.row_tiles % 2) - 2.1 / (2 * kTile) * static_cast<double>(a.T) * a.group;
-  return static_cast<double>((a.B - x.groups) * heads * tiles) * unit < 5.0 * num_sms;
+  const double saved = static_cast<double>((a.B - x.groups) * heads * tiles) * unit / num_sms;
+  const double spent = 6.0 + 8.0 * static_cast<double>(heads * prefix_pairs) / num_sms + static_cast<double>(rows * head_dim) * 16 / 4e6;
+  return saved < spent;
 }
 
 }  // namespace
@@ -1150,7 +1155,7 @@ size_t prefix_attn_workspace_bytes(int64_t B, int64_t T, int64_t heads, int64_t 
 }
 
 cudaError_t launch_prefix_attn(const PrefixArgs& a, int64_t head_dim, void* workspace, int num_sms, cudaStream_t stream) {
-  if (as_tree_attn(a, num_sms)) return launch_tree_attn(a.attn, head_dim, workspace, num_sms, stream);
+  if (as_tree_attn(a, head_dim, num_sms)) return launch_tree_attn(a.attn, head_dim, workspace, num_sms, stream);
   const bool spread = spreads(a.attn.T, a.attn.group);
   if (head_dim == 64)
     return spread ? launch<64, true>(a, workspace, num_sms, stream) : launch<64, false>(a, workspace, num_sms, stream);

@@ -24,7 +24,7 @@ def i32(a):
 def roomy(groups, H, capacity):
     """A capacity for which sharing is expected to pay, whatever the lengths."""
     B = sum(len(own) for _, own in groups)
-    return max(capacity, 128 * (1600 // max(1, (B - len(groups)) * H) + 1))
+    return max(capacity, 128 * (6000 // max(1, (B - len(groups)) * H) + 1))
 
 
 def shared_cache(gen, groups, H, D, page, capacity, layout="nhd", spoil=None, room=None):
