@@ -109,8 +109,8 @@ __device__ __forceinline__ uint64_t warp_before(uint64_t x, uint64_t* total) {
 // apart, and a run of single tiles is cut in halves: a run has to be as long as two of their units and as one of the pairs'.
 enum List { kPairs = 0, kSingles = 1 };
 constexpr uint32_t kLeastRun = 22;
-__device__ __forceinline__ uint32_t unit_cost(const PrefixPlan& p, List which) { return which == kPairs ? 17 : p.spread ? 8 : 11; }
-__device__ __forceinline__ uint32_t ahead_cost(const PrefixPlan& p, List which) { return which == kPairs ? 24 : p.spread ? 16 : 20; }
+__device__ __forceinline__ uint32_t unit_cost(const PrefixPlan& p, List which) { return which == kPairs ? 17 : p.spread ? 10 : 11; }
+__device__ __forceinline__ uint32_t ahead_cost(const PrefixPlan& p, List which) { return which == kPairs ? 40 : p.spread ? 20 : 26; }
 __device__ __forceinline__ uint32_t item_cost(const PrefixPlan& p, List which, int32_t n) {
   return n * unit_cost(p, which) + ahead_cost(p, which);
 }
