@@ -2,8 +2,8 @@
 
 Every function has the name of the C entry point it calls (without the
 ``dflash2_`` prefix) and runs entirely in the CUDA library: torch tensors only
-supply device memory and the current stream.  The cache operators' arguments are
-checked and passed on by the compiled module _dflash2_bind.  bf16 tensors may be given as
+supply device memory and the current stream.  The arguments of the cache operators, and of
+rope, logits_adjust and token_counts, are checked and passed on by the compiled module _dflash2_bind.  bf16 tensors may be given as
 torch.bfloat16 or as int16/uint16 bit patterns.  Outputs that are not passed in
 are allocated with torch before the call (the library itself never allocates).
 """

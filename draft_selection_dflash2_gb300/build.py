@@ -44,7 +44,7 @@ def _stale(target, deps):
 
 
 def build_bind(force: bool = False) -> str:
-    """The extension module that checks the cache operators' tensors and calls the C ABI (needs g++ and the headers of
+    """The extension module that checks the cache and serving operators' tensors and calls the C ABI (needs g++ and the headers of
     torch and Python)."""
     import sysconfig
 
@@ -81,7 +81,7 @@ def _try_bind(force: bool = False):
 
 
 def build(force: bool = False, verbose: bool = False, extra_flags=()) -> str:
-    """Builds the library, which has to succeed, and the binding, without which only the cache operators are missing."""
+    """Builds the library, which has to succeed, and the binding, without which only the cache and serving operators are missing."""
     srcs, hdrs = _sources(), _headers()
     os.makedirs(BUILD, exist_ok=True)
     if not force and not _stale(LIB, srcs + hdrs + [__file__]):
