@@ -439,7 +439,9 @@ struct PrefixSmem {
   SharedSegment seg[2][kSegs];        // each pipeline's segments; tiles = 0: no more
   Stretch list[kListed + 1];
   uint32_t segs[2], q_issued[2];   // each pipeline's segments so far, and their queries' copies (the producer's)
-  uint32_t own_bad[2][kSegs][4], both_bad[4];   // drafted nodes that hold a non-finite value: of a pipeline's segment; of both's tile
+  // drafted nodes that hold a non-finite value: of a pipeline's segment; of both's tile (every second one's: a warp may still read
+  // one's nodes when the other pipeline has come to the next; to the one after that it comes by a meeting)
+  uint32_t own_bad[2][kSegs][4], both_bad[2][4];
   uint32_t tmem;
   int abort_flag;
   int odd;                  // whether some row's sums have to be taken again
@@ -819,7 +821,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     const uint32_t lanes = static_cast<uint32_t>((warp & 3) * 32) << 16;
     const uint32_t tm_s = tmem + i * kBufs * kChunk + lanes, tm_o = tmem + kTmemO + i * D + lanes;
     BufPos at_s;       // the pipeline's next chunk
-      uint32_t met = 0;  // parity of the pipelines' meetings over a drafted tile
+      uint32_t met = 0;  // the pipelines' meetings over drafted tiles, two for each
     // What is needed once a unit is read from shared memory there: the loop over the chunks has no registers to spare.
     const auto field = [](const int32_t& x) { return *const_cast<const volatile int32_t*>(&x); };
     for (uint32_t seg = 0;; ++seg) {
@@ -858,11 +860,11 @@ __global__ void __launch_bounds__(kThreads, 1)
             } else {
               // the pipelines look through their drafted tile together
               bad_seen |= see_tile<D>(a, v_tile, !kSpread && drafted, valid, chunks, static_cast<int>(threadIdx.x) - kTile,
-                                      2 * kTile, r, s.both_bad,
+                                      2 * kTile, r, s.both_bad[met >> 1 & 1],
                                       [&](int w) { return seen_keys(a, true, valid, g.b, row_node(), row_ok, w); }, [&]() {
                                         mbar_arrive(&s.seen);
                                         wait_live(&s.seen, met & 1, &live, abort_flag, a.err);
-                                        met ^= 1;
+                                        ++met;
                                       });
             }
           }
