@@ -1119,6 +1119,9 @@ cudaError_t launch(const PrefixArgs& x, void* workspace, int num_sms, cudaStream
   cfg.dynamicSmemBytes = smem;
   e = cudaLaunchKernelEx(&cfg, prefix_attn_kernel<D, kSpread>, m.q, copy.q, m.k, m.v, m.kn, m.vn, p);
   if (e != cudaSuccess) return e;
+  // A CTA a row pays where rows are few and their prefixes cut into many parts (rows an SM, us with a warp a row and a CTA: 3,
+  // behind 32768: 48 and 42; 7, behind 16384: 36.4 and 34.4, behind 4000: 29.7 and 32.3; 13, behind 2000: 41.6 and 50.3, behind
+  // 16384: 52 and 51; 27: 68 and 79).
   const int64_t rows = p.rows;
   const bool split = rows <= 8 * num_sms;
   cfg.gridDim = dim3(static_cast<unsigned>(split ? rows : (rows + kJoinWarps - 1) / kJoinWarps), 1, 1);
